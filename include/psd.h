@@ -14,6 +14,10 @@
  *   cascade_decode        device: level 0 with KV-head-major stacked queries,
  *                         level 1, and the exact merge (Decomposition section)
  *
+ *   append_tokens, multi_token_decode, verify_drafts
+ *                         a step of several new tokens a request (drafts, prompt chunks):
+ *                         rotation + append, attention over the cache, verification
+ *
  * Conventions shared by every entry point
  *   - Every function returns psd_status; nothing throws or aborts across the ABI.
  *     On failure psd_last_error() returns a thread-local message.
@@ -536,6 +540,182 @@ typedef struct {
 } psd_rope_append_args;
 
 psd_status rope_append_kv(psd_ctx *ctx, const psd_rope_append_args *args, psd_stream_t stream);
+
+/* ------------------------------------------------- steps of several new tokens
+ * The source pages decline multi-token steps (mlxcel PR #1004, Task item 4: they fall
+ * back) and name speculative acceptance as a neighbouring item (Left out / unsure).
+ * The three operators below make that step: a request brings n_b >= 0 new tokens (its
+ * last accepted token and some drafts, or a chunk of its prompt), which are rotated and
+ * appended, attended over the cache, and, for drafts, verified.
+ *
+ * Request b owns the token rows [q_indptr[b], q_indptr[b+1]); its page table covers
+ * L_b tokens INCLUDING the new ones, so its new token i sits at index
+ * P_b + i, P_b = L_b - n_b.  Rows from q_indptr[B] on belong to no request: they are
+ * neither read nor written. */
+
+/* Rotary frequencies, scaled for long contexts (host, 64 bits).  With r = rot_dim,
+ * f_i = base^(-2 i / r), i < r/2:
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor
+ *   NTK     base' = base * factor^(r / (r - 2)) in place of base        (r > 2)
+ *   YARN    f_i k_i + (f_i / factor) (1 - k_i) with k_i = 1 - clamp((i - lo) / (hi - lo)),
+ *           lo = max(floor(dim(high)), 0), hi = min(ceil(dim(low)), r - 1) (hi - lo >= 0.001),
+ *           dim(t) = r log(original / (2 pi t)) / (2 log base): frequencies that turn more than
+ *           `high` times within the original context are kept, those below `low` divided;
+ *           magnitude = 0.1 log(factor) + 1 (1 for factor <= 1)
+ *   BANDS   the same mix with k_i = clamp((turns_i - low) / (high - low)),
+ *           turns_i = original f_i / (2 pi)
+ * inv_freq [rot_dim / 2] and magnitude (the factor on cos and sin; 1 except YARN) are
+ * host outputs. */
+typedef enum {
+  PSD_ROPE_PLAIN = 0,
+  PSD_ROPE_LINEAR = 1,
+  PSD_ROPE_NTK = 2,
+  PSD_ROPE_YARN = 3,
+  PSD_ROPE_BANDS = 4
+} psd_rope_kind;
+typedef struct {
+  int32_t kind;                  /* psd_rope_kind */
+  int32_t rot_dim;               /* even, in [2, 512] */
+  double base;                   /* > 1 */
+  double factor;                 /* > 0 (all but PLAIN) */
+  int32_t original_max_position; /* > 0 (YARN, BANDS) */
+  double low, high;              /* turns, 0 < low < high (YARN, BANDS); e.g. 1, 32 and 1, 4 */
+} psd_rope_scaling;
+psd_status psd_rope_frequencies(const psd_rope_scaling *scaling, double *inv_freq, double *magnitude);
+
+/* Rotates the new tokens' queries and keys and appends their K and V rows to the pools,
+ * finding each row's page in the device page table (no slot list, no cos/sin table).
+ * Token row t of request b, new token i: pos = positions[t], or P_b + i when positions
+ * is NULL; angle a_j = pos * inv_freq[j], taken exactly modulo one turn in 64-bit fixed
+ * point; c_j = magnitude cos a_j, s_j = magnitude sin a_j in f32;
+ *   x' = x c - y s, y' = y c + x s in f32
+ * on the pairs (j, j + r/2) (neox) or (2j, 2j + 1) of columns [rot_col, rot_col + r) of
+ * every query and key head; the other columns are copied.  q_out[t] gets the query row
+ * in bf16; the pool rows at index P_b + i get K and V in bf16, or as the saturating
+ * round-to-nearest-even E4M3 code of value / scale.  NaN stays NaN.
+ * q, k and v are [T, heads, D] with their own token strides (heads of a token are
+ * contiguous), e.g. views of one fused projection.  q_out may be q itself when q is
+ * contiguous (the strides agree); otherwise inputs and outputs must not overlap.
+ * A token whose index falls outside [0, its page list) or whose page id is out of range
+ * keeps its pool rows unwritten (q_out is written) and sets PSD_FAULT_PAGE_ID; a negative
+ * position (its own or given) leaves the token untouched and sets PSD_FAULT_RANGE, both
+ * OR-ed into *fault_dev.  Two tokens that share a pool row (a page listed twice) leave
+ * one of the two rows there.
+ * num_tokens == 0 or batch == 0 is a no-op (the pointers are not checked). */
+typedef struct {
+  const void *q;                 /* device [T, Hq, D] bf16 (NULL iff Hq == 0) */
+  const void *k;                 /* device [T, Hkv, D] bf16 */
+  const void *v;                 /* device [T, Hkv, Dv] bf16 (NULL iff Dv == 0: V is in the K row) */
+  int64_t q_stride, k_stride, v_stride; /* elements between tokens, >= heads * dim */
+  void *q_out;                   /* device [T, Hq, D] bf16, contiguous (NULL iff Hq == 0) */
+  int32_t num_tokens, batch;     /* T rows; requests */
+  int32_t Hq, Hkv, D, Dv;
+  int32_t rot_col, rot_dim, neox;/* rot_dim even, in [2, 512], rot_col + rot_dim <= D */
+  const double *inv_freq;        /* host [rot_dim / 2], finite, >= 0 */
+  double magnitude;              /* finite */
+  const int32_t *q_indptr;       /* device [batch + 1] */
+  const int32_t *kv_len;         /* device [batch]: L_b, the new tokens included */
+  const int32_t *positions;      /* device [T] or NULL */
+  const int32_t *page_indptr;    /* device [batch + 1] */
+  const int32_t *page_indices;   /* device [num_page_indices] */
+  int64_t num_page_indices;
+  void *k_pool;                  /* device [num_pages, page_size, Hkv, D] */
+  void *v_pool;                  /* device [num_pages, page_size, Hkv, Dv] (NULL iff Dv == 0) */
+  int64_t num_pages;
+  int32_t page_size, kv_dtype;   /* PSD_BF16 or PSD_FP8_E4M3 (both pools) */
+  float k_scale, v_scale;        /* fp8 only: finite and > 0 */
+  int32_t *fault_dev;            /* device int32 fault word */
+} psd_append_args;
+psd_status append_tokens(psd_ctx *ctx, const psd_append_args *args, psd_stream_t stream);
+
+/* Plan of a multi-token step (host).  requests has capacity >= batch. */
+typedef struct {
+  int32_t token0;   /* the request's first token row */
+  int32_t num_new;  /* n_b */
+  int32_t page_off; /* position of its first page in page_indices */
+  int32_t kv_len;   /* L_b */
+} psd_token_request;
+typedef struct {
+  int32_t batch_capacity;      /* in */
+  psd_token_request *requests; /* in: [batch_capacity], written by the planner */
+  int32_t batch, page_size, num_tokens; /* out; num_tokens = q_indptr[batch] */
+  int32_t max_new;             /* out: the largest n_b */
+} psd_multi_token_plan;
+/* host: the page table after the append (every request >= 1 page, as for the decode
+ * entry points); q_indptr: host [batch + 1], from 0, non-decreasing, n_b <= L_b. */
+psd_status psd_plan_multi_token(const psd_page_table *host, const int32_t *q_indptr,
+                                psd_multi_token_plan *plan);
+
+/* Attention of every new token over the paged cache.  Row (t, h), new token i of
+ * request b, sees the keys j < L_b with
+ *   tree_mask == NULL: j <= P_b + i (causal), or
+ *   tree_mask != NULL: j < P_b, or bit (j - P_b) of tree_mask[t] (bits >= n_b are
+ *                      ignored; every n_b <= 64), e.g. a draft tree's ancestors:
+ *   t_j = sm_scale <q, k_j> log2(e), m = max t_j, l = sum 2^(t_j - m),
+ *   o = sum 2^(t_j - m) v_j / l, lse = m + log2(l) (log2 units, as merge_states takes).
+ * A row that sees no key gets o = 0 and lse = -inf.  Values the request's own tokens
+ * hold in hidden places must be finite; pool rows outside the L_b tokens may hold
+ * anything.
+ * P (the softmax weights before normalisation) meets V as one bf16 term for bf16
+ * outputs and as two (about 16 bits) for f32 outputs; sums, maxima and O are f32.
+ * Two kernels: head dims 64 and 128 with page sizes that are multiples of 8, at most 128
+ * query heads per KV head and sm_scale > 0 run on the tcgen05 tensor cores; every other
+ * shape (D a multiple of 8 up to 256) on CUDA cores.
+ * workspace: >= psd_multi_token_workspace_bytes(ctx, D) bytes, 16-byte aligned, reusable
+ * by calls on one stream; calls that may overlap (other streams, captured graphs that
+ * may run at the same time) need their own.  psd_check_device_error reports its faults.
+ * Captured into a graph, a call replays with the plan it was captured with.  The lists
+ * travel in the launches' parameters, so no staging memory is read at replay. */
+typedef struct {
+  const void *q;                   /* device [num_tokens.., Hq, D] bf16 */
+  int64_t q_stride;                /* elements between tokens: >= Hq * D, a multiple of 8 */
+  const void *k_pool, *v_pool;     /* device [num_pages, page_size, Hkv, D] */
+  const int32_t *page_indices_dev; /* device [num_page_indices] */
+  int64_t num_page_indices, num_pages;
+  int32_t num_tokens;              /* rows of q and of the outputs, >= the plan's */
+  int32_t Hq, Hkv, D, page_size;
+  int32_t kv_dtype;                /* PSD_BF16 or PSD_FP8_E4M3 */
+  float k_scale, v_scale;          /* fp8 only: finite */
+  float sm_scale;                  /* finite */
+  const uint64_t *tree_mask;       /* device [num_tokens] or NULL */
+  int32_t out_f32;                 /* o is f32 (1) or bf16 (0) */
+} psd_multi_token_args;
+size_t psd_multi_token_workspace_bytes(const psd_ctx *ctx, int32_t D);
+psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *args,
+                              const psd_multi_token_plan *plan, void *o, float *lse,
+                              void *workspace, size_t workspace_bytes, psd_stream_t stream);
+
+/* Verification of drafted tokens.  Request b has K_b = draft_indptr[b+1] - draft_indptr[b]
+ * drafts and K_b + 1 target rows, from row R_b = draft_indptr[b] + b (its rows of a
+ * multi-token step): target row R_b + j is p after draft j's predecessors.
+ * Draft j (token d, proposal q_j) is accepted while u_{R_b + j} * q_j(d) < p_{R_b+j}(d); let
+ * a be the number accepted before the first refusal.  The next token is drawn with the
+ * number u = uniforms[R_b + K_b]: over the weights max(p - q, 0) of place a where a draft
+ * was refused (p itself where those sum to zero), over p of place K_b where none was:
+ * the least v whose running sum exceeds u times the total.
+ * draft_probs == NULL: the drafts have no probabilities of their own (looked up):
+ * q is 1 at the draft token and 0 elsewhere.
+ * out_tokens[R_b ..]: the a accepted drafts, the new token, then -1.  num_accepted[b] = a.
+ * Products and comparisons of the acceptance are exact; the running sums are exact sums
+ * of the probabilities cut at 2^-58, so the outcome does not depend on the order of
+ * summation.  Probabilities are f32 in [0, 1] and each row sums to at most 16; values that
+ * are not (NaN, negative) count as 0, larger than 1 as 1.  A draft token outside [0, vocab)
+ * is refused, its q is 0 everywhere, and PSD_FAULT_RANGE is set; so is a row whose
+ * weights are all 0 (its new token is -1).  Rows with no request are not touched. */
+typedef struct {
+  const float *target_probs;   /* device [num_drafts + batch, vocab] */
+  const float *draft_probs;    /* device [num_drafts, vocab] or NULL */
+  int64_t target_stride, draft_stride; /* elements between rows, >= vocab */
+  const int32_t *draft_tokens; /* device [num_drafts] */
+  const int32_t *draft_indptr; /* device [batch + 1], from 0, non-decreasing, its end num_drafts */
+  const float *uniforms;       /* device [num_drafts + batch], in [0, 1) */
+  int32_t batch, num_drafts, vocab;
+  int32_t *num_accepted;       /* device [batch] */
+  int32_t *out_tokens;         /* device [num_drafts + batch] */
+  int32_t *fault_dev;          /* device int32 fault word, OR-ed */
+} psd_verify_args;
+psd_status verify_drafts(psd_ctx *ctx, const psd_verify_args *args, psd_stream_t stream);
 
 /* Synchronises `stream` and reads the workspace's fault word: PSD_OK, or
  * PSD_ERR_DEVICE_FAULT with the PSD_FAULT_* bits in *fault_bits (nullable).

@@ -9,5 +9,7 @@ from .api import (CachedPlan, Context, HostTable, NestedPlan, Plan, PlanCache,  
                   cascade_decode_no_alloc,
                   cascade_env_enabled, check_device_error, decode_args, detect_shared_prefix,
                   merge_states, paged_decode_partial, plan_decode, rope_append_kv, split_plan,
-                  workspace_bytes, workspace_for)
+                  workspace_bytes, workspace_for,
+                  RopeFrequencies, rope_frequencies, append_tokens, MultiTokenPlan, plan_multi_token,
+                  multi_token_workspace, multi_token_args, multi_token_decode, verify_drafts)
 from ._lib import PsdError, load  # noqa: F401

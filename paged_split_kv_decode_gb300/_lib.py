@@ -26,7 +26,10 @@ EXPORTS = [
     "psd_plan_cache_create", "psd_plan_cache_destroy", "psd_plan_cache_lookup", "psd_plan_cache_lookup_gen",
     "psd_plan_cache_stats", "rope_append_kv", "psd_plan_nested_capacity", "psd_plan_nested",
     "psd_nested_workspace_bytes", "cascade_decode_nested", "psd_autotune_tile", "psd_tuned_tile",
+    "psd_rope_frequencies", "append_tokens", "psd_plan_multi_token", "psd_multi_token_workspace_bytes",
+    "multi_token_decode", "verify_drafts",
 ]
+PSD_ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
 
 class PageTable(C.Structure):
@@ -91,6 +94,45 @@ class Counters(C.Structure):
                 ("lists_inline", i64), ("lists_uploaded", i64)]
 
 
+class RopeScaling(C.Structure):
+    _fields_ = [("kind", i32), ("rot_dim", i32), ("base", C.c_double), ("factor", C.c_double),
+                ("original_max_position", i32), ("low", C.c_double), ("high", C.c_double)]
+
+
+class AppendArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("k", C.c_void_p), ("v", C.c_void_p), ("q_stride", i64), ("k_stride", i64),
+                ("v_stride", i64), ("q_out", C.c_void_p), ("num_tokens", i32), ("batch", i32), ("Hq", i32),
+                ("Hkv", i32), ("D", i32), ("Dv", i32), ("rot_col", i32), ("rot_dim", i32), ("neox", i32),
+                ("inv_freq", C.POINTER(C.c_double)), ("magnitude", C.c_double), ("q_indptr", C.c_void_p),
+                ("kv_len", C.c_void_p), ("positions", C.c_void_p), ("page_indptr", C.c_void_p),
+                ("page_indices", C.c_void_p), ("num_page_indices", i64), ("k_pool", C.c_void_p),
+                ("v_pool", C.c_void_p), ("num_pages", i64), ("page_size", i32), ("kv_dtype", i32),
+                ("k_scale", C.c_float), ("v_scale", C.c_float), ("fault_dev", C.c_void_p)]
+
+
+class TokenRequest(C.Structure):
+    _fields_ = [("token0", i32), ("num_new", i32), ("page_off", i32), ("kv_len", i32)]
+
+
+class MultiTokenPlan(C.Structure):
+    _fields_ = [("batch_capacity", i32), ("requests", C.POINTER(TokenRequest)), ("batch", i32), ("page_size", i32),
+                ("num_tokens", i32), ("max_new", i32)]
+
+
+class MultiTokenArgs(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_stride", i64), ("k_pool", C.c_void_p), ("v_pool", C.c_void_p),
+                ("page_indices_dev", C.c_void_p), ("num_page_indices", i64), ("num_pages", i64), ("num_tokens", i32),
+                ("Hq", i32), ("Hkv", i32), ("D", i32), ("page_size", i32), ("kv_dtype", i32), ("k_scale", C.c_float),
+                ("v_scale", C.c_float), ("sm_scale", C.c_float), ("tree_mask", C.c_void_p), ("out_f32", i32)]
+
+
+class VerifyArgs(C.Structure):
+    _fields_ = [("target_probs", C.c_void_p), ("draft_probs", C.c_void_p), ("target_stride", i64),
+                ("draft_stride", i64), ("draft_tokens", C.c_void_p), ("draft_indptr", C.c_void_p),
+                ("uniforms", C.c_void_p), ("batch", i32), ("num_drafts", i32), ("vocab", i32),
+                ("num_accepted", C.c_void_p), ("out_tokens", C.c_void_p), ("fault_dev", C.c_void_p)]
+
+
 _LIB = None
 
 
@@ -150,11 +192,18 @@ def _sig(lib):
     lib.psd_check_device_error.argtypes = [V, V, V, P_i32]
     lib.cascade_decode_no_alloc.argtypes = [V, C.POINTER(DecodeArgs), C.POINTER(CascadePlan), V, V, V,
                                             C.POINTER(CascadeStats), V]
+    lib.psd_rope_frequencies.argtypes = [C.POINTER(RopeScaling), C.POINTER(C.c_double), C.POINTER(C.c_double)]
+    lib.append_tokens.argtypes = [V, C.POINTER(AppendArgs), V]
+    lib.psd_plan_multi_token.argtypes = [C.POINTER(PageTable), P_i32, C.POINTER(MultiTokenPlan)]
+    lib.psd_multi_token_workspace_bytes.argtypes = [V, i32]
+    lib.psd_multi_token_workspace_bytes.restype = C.c_size_t
+    lib.multi_token_decode.argtypes = [V, C.POINTER(MultiTokenArgs), C.POINTER(MultiTokenPlan), V, V, V, C.c_size_t, V]
+    lib.verify_drafts.argtypes = [V, C.POINTER(VerifyArgs), V]
     for name in EXPORTS:
         f = getattr(lib, name)
         if f.restype is C.c_int or f.restype is None:
             if name not in ("psd_last_error", "psd_cascade_env_enabled", "psd_workspace_bytes",
-                            "psd_nested_workspace_bytes", "psd_tuned_tile"):
+                            "psd_nested_workspace_bytes", "psd_tuned_tile", "psd_multi_token_workspace_bytes"):
                 f.restype = C.c_int
 
 

@@ -375,6 +375,249 @@ def rope_append_kv(ctx: Context, q, k_nope, k_rope, v, cos_sin, positions, slot_
     return fault
 
 
+class RopeFrequencies:
+    """Rotary frequencies for append_tokens: inv_freq [rot_dim / 2] float64 and the factor on
+    cos and sin.  `rope_frequencies` makes them; a caller's own go in as they are."""
+
+    def __init__(self, inv_freq, magnitude: float = 1.0):
+        self.inv_freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
+        self.magnitude = float(magnitude)
+        self._ptr = self.inv_freq.ctypes.data_as(C.POINTER(C.c_double))
+
+    @property
+    def rot_dim(self) -> int:
+        return 2 * int(self.inv_freq.shape[0])
+
+
+def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                     original_max_position: int = 0, low: float = None, high: float = None) -> RopeFrequencies:
+    """psd_rope_frequencies: scaling is 'plain', 'linear', 'ntk', 'yarn' or 'bands'.  low and
+    high (turns within the original context) default to 1 and 32 for yarn, 1 and 4 for bands."""
+    if scaling not in L.PSD_ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {sorted(L.PSD_ROPE_KINDS)}")
+    a = L.RopeScaling(L.PSD_ROPE_KINDS[scaling], int(rot_dim), float(base), float(factor), int(original_max_position),
+                      1.0 if low is None else float(low),
+                      (4.0 if scaling == "bands" else 32.0) if high is None else float(high))
+    f = np.zeros(max(int(rot_dim) // 2, 1), dtype=np.float64)
+    m = C.c_double()
+    L.check(L.load().psd_rope_frequencies(C.byref(a), f.ctypes.data_as(C.POINTER(C.c_double)), C.byref(m)))
+    return RopeFrequencies(f, m.value)
+
+
+def _rows_ptr(t: torch.Tensor, name: str, dtype, ndim: int):
+    """(pointer, elements between rows) of a CUDA tensor whose rows are contiguous but may
+    lie apart (a view of a wider tensor)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+    width = 1
+    for d in range(ndim - 1, 0, -1):
+        if t.shape[d] != 1 and t.stride(d) != width:
+            raise ValueError(f"{name}: the values of a row must be contiguous")
+        width *= int(t.shape[d])
+    return t.data_ptr(), (int(t.stride(0)) if t.shape[0] > 1 else width)
+
+
+def _int32_ptr(t: torch.Tensor, name: str, numel: int = None) -> int:
+    p = _dev_ptr(t, name)
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must hold {numel} values")
+    return p
+
+
+def _ctx_stream(ctx: Context, stream) -> C.c_void_p:
+    """The stream given, or the current one of the context's device (which need not be the
+    current device)."""
+    if stream is None and _raw_stream is not None:
+        return C.c_void_p(_raw_stream(ctx.device))
+    return _stream(torch.cuda.current_stream(ctx.device) if stream is None else stream)
+
+
+def _on_device(ctx: Context, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.is_cuda and t.device.index != ctx.device:
+            raise ValueError(f"{name} is on cuda:{t.device.index}, the context on cuda:{ctx.device}")
+
+
+def append_tokens(ctx: Context, q, k, v, q_out, *, q_indptr, kv_len, page_indptr, page_indices, k_pool, v_pool,
+                  rope: RopeFrequencies, neox: bool, rope_col: int = 0, positions=None, k_scale: float = 1.0,
+                  v_scale: float = 1.0, fault=None, stream=None):
+    """append_tokens: rotate the new tokens' queries into q_out and append their rotated K and
+    their V to the pools, at the places the device page table gives.
+
+    q [T, Hq, D], k [T, Hkv, D], v [T, Hkv, Dv] bf16, possibly views with a token stride; q_out
+    [T, Hq, D] bf16 (q and q_out None for a K/V-only append, v and v_pool None for a shared
+    latent); q_indptr and page_indptr [B + 1], kv_len [B] (new tokens included), page_indices
+    and positions ([T], optional) int32 on the device; pools bf16 or uint8 fp8-e4m3 codes
+    [pages, page_size, Hkv, D].  Returns the int32 fault word tensor (the one given, or a new
+    zero one)."""
+    a = L.AppendArgs()
+    a.k, a.k_stride = _rows_ptr(k, "k", torch.bfloat16, 3)
+    T, Hkv, D = (int(x) for x in k.shape)
+    if (q is None) != (q_out is None) or (v is None) != (v_pool is None):
+        raise ValueError("q goes with q_out, v with v_pool")
+    if q is not None:
+        a.q, a.q_stride = _rows_ptr(q, "q", torch.bfloat16, 3)
+        if int(q.shape[0]) != T or int(q.shape[2]) != D or q_out.shape != q.shape or q_out.dtype != torch.bfloat16:
+            raise ValueError("q and q_out must be bf16 [T, Hq, D] with k's T and D")
+        a.q_out, a.Hq = _dev_ptr(q_out, "q_out"), int(q.shape[1])
+    if v is not None:
+        a.v, a.v_stride = _rows_ptr(v, "v", torch.bfloat16, 3)
+        a.Dv = int(v.shape[2])
+        if int(v.shape[0]) != T or int(v.shape[1]) != Hkv:
+            raise ValueError("v must be [T, Hkv, Dv] with k's T and Hkv")
+        if v_pool.dtype != k_pool.dtype or tuple(v_pool.shape) != tuple(k_pool.shape[:3]) + (a.Dv,):
+            raise ValueError("v_pool must be [num_pages, page_size, Hkv, Dv] of k_pool's type")
+        a.v_pool = _dev_ptr(v_pool, "v_pool")
+    if k_pool.dim() != 4 or int(k_pool.shape[2]) != Hkv or int(k_pool.shape[3]) != D:
+        raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
+    if fault is None:
+        fault = torch.zeros(1, dtype=torch.int32, device=k_pool.device)
+    _on_device(ctx, q=q, k=k, v=v, q_out=q_out, q_indptr=q_indptr, kv_len=kv_len, page_indptr=page_indptr,
+               page_indices=page_indices, positions=positions, k_pool=k_pool, v_pool=v_pool, fault=fault)
+    B = int(kv_len.numel())
+    a.num_tokens, a.batch, a.Hkv, a.D = T, B, Hkv, D
+    a.rot_col, a.rot_dim, a.neox = int(rope_col), rope.rot_dim, int(bool(neox))
+    a.inv_freq, a.magnitude = rope._ptr, rope.magnitude
+    a.q_indptr = _int32_ptr(q_indptr, "q_indptr", B + 1)
+    a.kv_len = _int32_ptr(kv_len, "kv_len")
+    a.positions = None if positions is None else _int32_ptr(positions, "positions", T)
+    a.page_indptr = _int32_ptr(page_indptr, "page_indptr", B + 1)
+    a.page_indices, a.num_page_indices = _int32_ptr(page_indices, "page_indices"), int(page_indices.numel())
+    a.k_pool = _dev_ptr(k_pool, "k_pool")
+    a.num_pages, a.page_size = int(k_pool.shape[0]), int(k_pool.shape[1])
+    a.kv_dtype = kv_dtype_code(k_pool)
+    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
+    a.fault_dev = _int32_ptr(fault, "fault")
+    L.check(L.load().append_tokens(ctx.handle, C.byref(a), _ctx_stream(ctx, stream)))
+    return fault
+
+
+class MultiTokenPlan:
+    """A psd_multi_token_plan with caller-owned arrays."""
+
+    def __init__(self, capacity: int):
+        self.requests_a = (L.TokenRequest * max(int(capacity), 1))()
+        self.c = L.MultiTokenPlan()
+        self.c.batch_capacity = int(capacity)
+        self.c.requests = self.requests_a
+
+    @property
+    def requests(self):
+        return [(r.token0, r.num_new, r.page_off, r.kv_len) for r in self.requests_a[: self.c.batch]]
+
+    def __getattr__(self, name):
+        if name in ("batch", "page_size", "num_tokens", "max_new"):
+            return getattr(self.c, name)
+        raise AttributeError(name)
+
+
+def plan_multi_token(table: HostTable, q_indptr, Hq: int = None, Hkv: int = None) -> MultiTokenPlan:
+    """psd_plan_multi_token: the table after the append, and the new tokens' CSR (host).  Hq
+    and Hkv, when given, are checked (Hq % Hkv == 0); the plan does not depend on them."""
+    qi = _i32(q_indptr)
+    if qi.shape != (table.batch + 1,):
+        raise ValueError("q_indptr must hold batch + 1 values")
+    if Hq is not None and Hkv is not None and (Hkv < 1 or Hq < 1 or Hq % Hkv):
+        raise ValueError("need Hq % Hkv == 0")
+    plan = MultiTokenPlan(table.batch)
+    L.check(L.load().psd_plan_multi_token(C.byref(table.c), _ptr_i32(qi), C.byref(plan.c)))
+    return plan
+
+
+def multi_token_workspace(ctx: Context, plan: MultiTokenPlan, D: int, device) -> torch.Tensor:
+    """A workspace for multi_token_decode: its size depends on the head dim alone, so one
+    serves every plan."""
+    n = int(L.load().psd_multi_token_workspace_bytes(ctx.handle, int(D)))
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def multi_token_args(q, k_pool, v_pool, page_indices_dev, *, sm_scale: float, k_scale: float = 1.0,
+                     v_scale: float = 1.0, tree_mask=None) -> L.MultiTokenArgs:
+    """psd_multi_token_args from device tensors: q [T, Hq, D] bf16 (possibly a view with a
+    token stride), pools [pages, page_size, Hkv, D] bf16 or uint8 fp8-e4m3 codes, page_indices
+    int32, tree_mask [T] int64 (64 bits a token) or None."""
+    a = L.MultiTokenArgs()
+    a.q, a.q_stride = _rows_ptr(q, "q", torch.bfloat16, 3)
+    a.num_tokens, a.Hq, a.D = (int(x) for x in q.shape)
+    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype or int(k_pool.shape[3]) != a.D:
+        raise ValueError("k_pool and v_pool must be alike, [num_pages, page_size, Hkv, D]")
+    a.k_pool, a.v_pool = _dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool")
+    a.page_indices_dev = _int32_ptr(page_indices_dev, "page_indices")
+    a.num_page_indices = int(page_indices_dev.numel())
+    a.num_pages, a.page_size, a.Hkv = (int(x) for x in k_pool.shape[:3])
+    a.kv_dtype = kv_dtype_code(k_pool)
+    a.k_scale, a.v_scale, a.sm_scale = float(k_scale), float(v_scale), float(sm_scale)
+    if tree_mask is not None:
+        if tree_mask.dtype != torch.int64 or tree_mask.numel() != a.num_tokens:
+            raise ValueError("tree_mask must be int64 [T]")
+        a.tree_mask = _dev_ptr(tree_mask, "tree_mask")
+    tensors = (q, k_pool, v_pool, page_indices_dev, tree_mask)
+    a.device = q.device.index
+    if any(t is not None and t.device.index != a.device for t in tensors):
+        raise ValueError("the tensors are on different devices")
+    a.tensors = tensors  # the structure holds their addresses
+    return a
+
+
+def multi_token_decode(ctx: Context, args: L.MultiTokenArgs, plan: MultiTokenPlan, o: torch.Tensor,
+                       lse: torch.Tensor = None, workspace: torch.Tensor = None, stream=None):
+    """multi_token_decode: o [T, Hq, D] bf16 or f32, lse [T, Hq] f32 (log2 units) or None."""
+    if o.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("o must be bf16 or f32")
+    if tuple(o.shape) != (args.num_tokens, args.Hq, args.D):
+        raise ValueError("o must be [T, Hq, D]")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (args.num_tokens, args.Hq)):
+        raise ValueError("lse must be f32 [T, Hq]")
+    _on_device(ctx, o=o, lse=lse, workspace=workspace)
+    if args.device != ctx.device:
+        raise ValueError(f"the arguments are on cuda:{args.device}, the context on cuda:{ctx.device}")
+    args.out_f32 = int(o.dtype == torch.float32)
+    L.check(L.load().multi_token_decode(
+        ctx.handle, C.byref(args), C.byref(plan.c), _dev_ptr(o, "o"), None if lse is None else _dev_ptr(lse, "lse"),
+        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), _ctx_stream(ctx, stream)))
+
+
+def verify_drafts(ctx: Context, target_probs, draft_probs, draft_tokens, draft_indptr, uniforms, num_accepted,
+                  out_tokens, *, fault=None, stream=None):
+    """verify_drafts: target_probs [D + B, vocab], draft_probs [D, vocab] or None (f32, rows
+    possibly apart), draft_tokens [D], draft_indptr [B + 1] int32, uniforms [D + B] f32;
+    num_accepted [B] and out_tokens [D + B] int32 outputs, all on the device.  Returns the
+    int32 fault word tensor (the one given, or a new zero one)."""
+    a = L.VerifyArgs()
+    a.target_probs, a.target_stride = _rows_ptr(target_probs, "target_probs", torch.float32, 2)
+    D, B, V = int(draft_tokens.numel()), int(num_accepted.numel()), int(target_probs.shape[1])
+    if int(target_probs.shape[0]) != D + B:
+        raise ValueError("target_probs must have num_drafts + batch rows")
+    if draft_probs is not None:
+        a.draft_probs, a.draft_stride = _rows_ptr(draft_probs, "draft_probs", torch.float32, 2)
+        if tuple(draft_probs.shape) != (D, V):
+            raise ValueError("draft_probs must be [num_drafts, vocab]")
+        if D == 0:
+            a.draft_probs = None
+    if uniforms.dtype != torch.float32 or uniforms.numel() != D + B:
+        raise ValueError("uniforms must be f32 [num_drafts + batch]")
+    if fault is None:
+        fault = torch.zeros(1, dtype=torch.int32, device=target_probs.device)
+    _on_device(ctx, target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
+               draft_indptr=draft_indptr, uniforms=uniforms, num_accepted=num_accepted, out_tokens=out_tokens,
+               fault=fault)
+    a.draft_tokens = _int32_ptr(draft_tokens, "draft_tokens")
+    a.draft_indptr = _int32_ptr(draft_indptr, "draft_indptr", B + 1)
+    a.uniforms = _dev_ptr(uniforms, "uniforms")
+    a.batch, a.num_drafts, a.vocab = B, D, V
+    a.num_accepted = _int32_ptr(num_accepted, "num_accepted")
+    a.out_tokens = _int32_ptr(out_tokens, "out_tokens", D + B)
+    a.fault_dev = _int32_ptr(fault, "fault")
+    L.check(L.load().verify_drafts(ctx.handle, C.byref(a), _ctx_stream(ctx, stream)))
+    return fault
+
+
 def build_cascade_plan(table: HostTable, members, shared_pages: int, tile_tokens: int) -> Plan:
     plan = Plan(table)
     m = _i32(list(members) if len(members) else [0])

@@ -1,0 +1,35 @@
+// A step's attention over several new tokens a request: what the entry point hands to the
+// kernels.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "kernels.h"
+
+namespace psd {
+
+// Requests of one launch, carried in its parameters (a batch with more takes several
+// launches): no list in memory that a captured call would read again.
+constexpr int kStepRequests = 768;
+struct StepRequests {
+  psd_token_request r[kStepRequests];
+};
+
+struct StepParams {
+  const __nv_bfloat16 *q;
+  const void *k_pool, *v_pool;
+  const int32_t *page_indices;
+  const uint64_t *tree;
+  void *o;
+  float *lse;
+  FaultRef fault;
+  int64_t q_stride, num_pages;
+  int B;  // requests of this launch
+  int Hq, Hkv, G, D, page_size, fp8, out_f32;
+  float q_scale;  // sm_scale * log2(e) * k_scale
+  float v_scale;
+};
+
+psd_status launch_step_general(const StepParams &p, const StepRequests &req, const DeviceInfo &dev, cudaStream_t s);
+
+}  // namespace psd
