@@ -162,9 +162,9 @@ psd_status launch_step_general(const StepParams &p, const StepRequests &req, con
 using namespace psd;
 
 extern "C" size_t psd_multi_token_workspace_bytes(const psd_ctx *ctx, int32_t D) {
-  (void)ctx;
-  (void)D;
-  return 256;  // the fault word
+  if (!ctx || D < 1) return 0;
+  // the fault word, then the partial rows of the tensor-core kernel's CTAs, one per SM
+  return 256 + (D == 64 || D == 128 ? 4 * step_tc_part_floats(ctx->dev.num_sms, D) : 0);
 }
 
 extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *a, const psd_multi_token_plan *plan,
@@ -228,6 +228,7 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   p.fault = next_fault(ctx, workspace);
   p.q_stride = a->q_stride;
   p.num_pages = a->num_pages;
+  p.num_tokens = a->num_tokens;
   p.Hq = a->Hq;
   p.Hkv = a->Hkv;
   p.G = a->Hq / a->Hkv;
@@ -237,14 +238,20 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   p.out_f32 = a->out_f32 != 0;
   p.q_scale = a->sm_scale * 1.4426950408889634f * (fp8 ? a->k_scale : 1.f);
   p.v_scale = fp8 ? a->v_scale : 1.f;
+  StepPlace place;
+  place.ctas = ctx->dev.num_sms > 0 ? ctx->dev.num_sms : 1;
+  place.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256);
+  place.part_lse = place.part_o + size_t(place.ctas) * 512 * size_t(a->D);
   StepRequests req;
+  const bool tensor = step_tc_supports(p);
   for (int32_t b0 = 0; b0 < plan->batch;) {
     // up to kStepRequests requests that have new tokens
     p.B = 0;
     for (; b0 < plan->batch && p.B < kStepRequests; ++b0)  // (the others' rows are none)
       if (plan->requests[b0].num_new > 0) req.r[p.B++] = plan->requests[b0];
     if (p.B == 0) break;
-    const psd_status st = launch_step_general(p, req, ctx->dev, s);
+    const psd_status st =
+        tensor ? launch_step_tc(p, req, place, ctx->dev, s) : launch_step_general(p, req, ctx->dev, s);
     if (st != PSD_OK) return st;
   }
   return PSD_OK;

@@ -24,12 +24,22 @@ struct StepParams {
   float *lse;
   FaultRef fault;
   int64_t q_stride, num_pages;
-  int B;  // requests of this launch
+  int B;           // requests of this launch
+  int num_tokens;  // rows of q
   int Hq, Hkv, G, D, page_size, fp8, out_f32;
   float q_scale;  // sm_scale * log2(e) * k_scale
   float v_scale;
 };
 
+// The tensor-core kernel's CTAs and where they keep the partial rows of units they share.
+struct StepPlace {
+  int ctas;
+  float *part_o, *part_lse;
+};
+size_t step_tc_part_floats(int ctas, int D);
+bool step_tc_supports(const StepParams &p);
+psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
+                          cudaStream_t s);
 psd_status launch_step_general(const StepParams &p, const StepRequests &req, const DeviceInfo &dev, cudaStream_t s);
 
 }  // namespace psd

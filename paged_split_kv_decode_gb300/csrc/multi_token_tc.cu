@@ -1,0 +1,850 @@
+// Attention of several new tokens a request on the 5th-generation tensor cores
+// (tcgen05.mma kind::f16: bf16 operands, f32 accumulators in TMEM).
+//
+// Rows.  The G query heads of one KV head and the request's new tokens are stacked
+// token-major into row tiles of TH = floor(128 / G) tokens (TH * G <= 128 TMEM lanes), so
+// every K/V element crosses into shared memory once for up to 256 rows.  A unit is one
+// (request, KV head, one or two row tiles); its work is its key tiles of NK tokens.
+//
+// Split.  The key tiles of all units lie on one line, kv head by kv head, and CTA c of
+// the launch takes the stretch [c N / C, (c + 1) N / C): every SM gets the same number of
+// tiles whatever the lengths, with one CTA per SM and no second wave.  A stretch that
+// holds a whole unit writes its output; a piece of a unit writes a normalised partial
+// and its LSE to the workspace (at most two pieces a CTA, so the workspace does not
+// grow with the batch), and a second kernel joins the pieces of each split unit in key
+// order.  Nothing is added atomically: results repeat bit for bit.
+//
+// Pipeline.  Two softmax slots alternate on the tensor cores: op t is S = Q K^T and, after
+// the slot's warpgroup has turned S into P, O += P V; while one slot's rows take their
+// softmax the other slot's MMAs run.  A unit of two row tiles gives each slot one of them
+// (op 2j and 2j + 1 share key tile j); a unit of one row tile gives the slots its even and
+// odd key tiles, with an O, maximum and sum each, joined when the unit ends.  The MMA warp
+// issues S(t + 2) right after P V(t): they use the same TMEM columns (P lies over S), and
+// MMAs of one CTA execute in issue order.
+//   TMEM (512 columns): per slot S [128 x NK] f32 with P over it, and O [128 x D] f32.
+//   Shared memory: two row tiles of Q, a ring of K and V half-tiles (K, V, K, V, ...).
+//   Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row = TMEM lane), 8 MMA,
+//   9 loads Q and K, 10 loads V.
+//
+// Tiles are read by TMA through a 5-D view of the pool, [groups of 8 token slots][KV head]
+// [64-column halves][8 slots][64 columns], whose box of a page's part lands as complete
+// 128-byte-swizzle atoms: one copy carries a whole head row (both halves at D = 128) of up
+// to 128 slots of a page.  Page positions past the request's pages load as zeros.
+//
+// Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
+// by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
+// terms of NK keys need 3 NK / 2 columns, which is why f32 outputs take tiles of 64 keys.
+// The row maximum follows lazily: O and l are rescaled only when it grows by more than
+// 2^8, so P <= 2^8.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstring>
+#include <vector>
+
+#include "device.cuh"
+#include "multi_token.h"
+
+namespace psd {
+
+namespace {
+
+constexpr int kRows = 128;       // TMEM lanes of a row tile
+constexpr float kLazy = 8.f;     // log2 units
+constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
+constexpr int kThreads = 11 * 32;
+constexpr uint32_t kRingBytes = 160 * 1024;
+constexpr int kMaxStages = 20;
+
+template <int D, int TERMS>
+struct Lay {
+  static constexpr int NK = TERMS == 1 ? 128 : 64;             // keys per tile
+  static constexpr int kHalves = D / 64;                       // 64-column halves of a row
+  static constexpr uint32_t kGroupBytes = kHalves * 1024;      // 8 slots of one head
+  static constexpr uint32_t kTileBytes = NK / 8 * kGroupBytes; // K or V of a tile
+  static constexpr int kStages = int(kRingBytes / kTileBytes); // half-tiles in the ring
+  static constexpr uint32_t kQHalfBytes = kRows * 128;
+  static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;   // one row tile
+  static constexpr uint32_t kOffQ = kStages * kTileBytes;
+  static constexpr uint32_t kOffLM = kOffQ + 2 * kQBytes;      // slot 1's (m, l) of a unit of one row tile
+  static constexpr uint32_t kOffBar = kOffLM + kRows * 8;
+  static constexpr uint32_t kSmem = kOffBar + 512 + 1024;      // barriers, alignment slack
+  static constexpr uint32_t kPCols = NK / 2;                   // 32-bit columns of one P term
+  static constexpr uint32_t kSCols = TERMS == 1 ? NK : 96;     // a slot's S, or its P terms if they are wider
+  static constexpr uint32_t kColS = 2 * D;                     // after the two O
+  static_assert(TERMS * kPCols <= kSCols && NK <= int(kSCols), "S region");
+  static_assert(kColS + 2 * kSCols <= 512, "TMEM columns");
+  static_assert(kStages >= 5 && kStages <= kMaxStages, "S runs two tiles ahead of PV");
+  static_assert(kSmem <= 227u * 1024u, "shared memory");
+  static_assert(kTileBytes % 1024 == 0, "128-byte-swizzle atoms");
+};
+
+enum {
+  T_FULL = 0, T_EMPTY = kMaxStages,  // per half-tile: landed / its MMAs have read it
+  T_QFULL = 2 * kMaxStages, T_QFREE, // the unit's Q landed / every S of the unit is done
+  T_SFULL,                           // [2] S of the slot's next op is complete
+  T_PFULL = T_SFULL + 2,             // [2] its P is written (4 warps)
+  T_OFULL = T_PFULL + 2,             // every PV of the unit is complete
+  T_OFREE,                           // the unit's O are read out (8 warps)
+  T_XREADY, T_XFREE,                 // slot 1's (m, l) written / read (4 warps)
+  T_DRAIN, T_SLOT, T_TAIL
+};
+static_assert(T_TAIL * 8 + 12 <= 512, "barrier area");
+
+struct TCParams {
+  const int32_t *page_indices;
+  const uint64_t *tree;
+  void *o;
+  float *lse;
+  float *part_o;    // [CTAs][2][2 * 128 rows][D]
+  float *part_lse;  // [CTAs][2][2 * 128 rows]
+  FaultRef fault;
+  int64_t num_pages;
+  int64_t total;    // key tiles of the launch
+  int B, Hq, Hkv, G, TH, page_size, sub, out_f32;
+  float q_scale, v_scale;
+  long long wait_limit;
+  int withhold_from;  // testing aid: no loads for a unit's key tiles from this index on
+};
+// Requests with new tokens, and the number of key tiles before each (per-launch prefix).
+struct TCRequests {
+  psd_token_request r[kStepRequests];
+  int32_t base[kStepRequests + 1];
+};
+
+// ------------------------------------------------------------------ walking the units
+struct Unit {
+  psd_token_request r;
+  int kv, tok0;      // KV head, first new token of the unit
+  int two;           // 1: two row tiles
+  int j0, j1, n;     // this CTA's key tiles of the unit's n
+};
+
+// Key tiles of the unit whose first token is tok0.
+__host__ __device__ __forceinline__ int unit_tiles(const psd_token_request &r, int tok0, int TH, int NK, bool tree) {
+  const int start = r.kv_len - r.num_new;
+  const int end = tok0 + 2 * TH < r.num_new ? tok0 + 2 * TH : r.num_new;  // tokens up to here
+  const int keys = tree ? r.kv_len : start + end;
+  return (keys + NK - 1) / NK;
+}
+
+// Walks the units of the stretch [lo, hi) of the line of key tiles.
+template <int NK>
+struct Walk {
+  const TCParams &p;
+  const TCRequests &req;
+  int64_t at, hi;
+  int b, kv, tok0, j;
+  __device__ Walk(const TCParams &p_, const TCRequests &req_, int64_t lo, int64_t hi_) : p(p_), req(req_), at(lo), hi(hi_) {
+    b = 0;
+    if (at >= hi) return;
+    for (int n = p.B; n > 1;) {  // the last request with base <= lo
+      const int mid = n / 2;
+      if (req.base[b + mid] <= at) b += mid, n -= mid;
+      else n = mid;
+    }
+    int rem = int(at - req.base[b]);
+    const int per_head = (req.base[b + 1] - req.base[b]) / p.Hkv;
+    kv = rem / per_head;
+    rem -= kv * per_head;
+    tok0 = 0;
+    for (;;) {
+      const int n = unit_tiles(req.r[b], tok0, p.TH, NK, p.tree != nullptr);
+      if (rem < n) break;
+      rem -= n;
+      tok0 += 2 * p.TH;
+    }
+    j = rem;
+  }
+  __device__ bool next(Unit &u) {
+    if (at >= hi) return false;
+    u.r = req.r[b];
+    u.kv = kv;
+    u.tok0 = tok0;
+    u.two = u.r.num_new - tok0 > p.TH ? 1 : 0;
+    u.n = unit_tiles(u.r, tok0, p.TH, NK, p.tree != nullptr);
+    u.j0 = j;
+    u.j1 = int64_t(u.n - j) < hi - at ? u.n : j + int(hi - at);
+    at += u.j1 - u.j0;
+    j = 0;
+    tok0 += 2 * p.TH;
+    if (tok0 >= u.r.num_new) {
+      tok0 = 0;
+      if (++kv == p.Hkv) kv = 0, ++b;
+    }
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------------ PTX wrappers
+// Shared-memory matrix descriptor, 128-byte swizzle (layout code 2), version 1.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
+         (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// kind::f16: f32 accumulate, bf16 A and B, A K-major, B K-major or (b_mn) MN-major.
+__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]),
+      "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]),
+      "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, int c4,
+                                            uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ uint64_t l2_normal_policy() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+// The visible keys of one row among the NK from `base` on, one bit each.
+template <int NK>
+__device__ __forceinline__ void visible(int base, int seen, int start, uint64_t tree, bool has_tree,
+                                        uint32_t (&w)[NK / 32]) {
+#pragma unroll
+  for (int k = 0; k < NK / 32; ++k) {
+    const int n = (has_tree ? start : seen) - base - 32 * k;  // keys before this one are visible
+    uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+    if (has_tree) {
+      const int sh = start - base - 32 * k;  // the tree's bit 0 is key `start`
+      if (sh >= 0 && sh < 32) bits |= uint32_t(tree << sh);
+      else if (sh < 0 && sh > -64) bits |= uint32_t(tree >> -sh);
+    }
+    w[k] = bits;
+  }
+}
+
+template <int D, int TERMS>
+__global__ void __launch_bounds__(kThreads, 1)
+    step_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                   const __grid_constant__ CUtensorMap tmV, const TCParams p, const __grid_constant__ TCRequests req) {
+  using L = Lay<D, TERMS>;
+  constexpr int NK = L::NK, NS = L::kStages;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  dependents_may_launch();  // the joining kernel waits for this grid on its own
+  uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kOffBar);
+  uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + T_SLOT);
+  int *tail = reinterpret_cast<int *>(bars + T_TAIL);  // what the load warps issued
+  float2 *lm = reinterpret_cast<float2 *>(sm + L::kOffLM);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t lo = int64_t(blockIdx.x) * p.total / gridDim.x, hi = int64_t(blockIdx.x + 1) * p.total / gridDim.x;
+  const bool has_tree = p.tree != nullptr;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(bar(T_FULL + i), 1);
+      mbar_init(bar(T_EMPTY + i), 1);
+    }
+    mbar_init(bar(T_QFULL), 1);
+    mbar_init(bar(T_QFREE), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(T_SFULL + i), 1);
+      mbar_init(bar(T_PFULL + i), 4);
+    }
+    mbar_init(bar(T_OFULL), 1);
+    mbar_init(bar(T_OFREE), 8);
+    mbar_init(bar(T_XREADY), 4);
+    mbar_init(bar(T_XFREE), 4);
+    mbar_init(bar(T_DRAIN), 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tslot;
+  auto wait_all = [&](int b, uint32_t parity) {  // a warp's bounded wait
+    return __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u, p.fault, p.wait_limit)) != 0;
+  };
+  Walk<NK> walk(p, req, lo, hi);
+  Unit u;
+
+  if (warp == kKWarp || warp == kVWarp) {
+    // ----------------------------------------------------------------- loads
+    // Half-tile i of the ring: K of key tile i / 2 (even) or V of it (odd).
+    const bool is_v = warp == kVWarp;
+    const CUtensorMap *map = is_v ? &tmV : &tmK;
+    const uint64_t pol = l2_normal_policy();
+    const int n_copies = NK / p.sub;          // a lane each; p.sub tokens of one page
+    const uint32_t copy_bytes = uint32_t(p.sub / 8) * L::kGroupBytes;
+    const int P = p.page_size;
+    int g = 0, units = 0;                     // key tiles and units so far
+    bool ok = true, withheld = false;
+    while (ok && !withheld && walk.next(u)) {
+      if (!is_v) {
+        if (units > 0) ok = wait_all(T_QFREE, uint32_t(units - 1));  // every S of the last unit is done
+        if (!ok) break;
+        const int tiles = 1 + u.two;
+        if (lane == 0) mbar_arrive_expect_tx(bar(T_QFULL), uint32_t(tiles * L::kHalves * p.TH * p.G) * 128u);
+        __syncwarp();
+        if (lane < tiles * L::kHalves) {
+          const int tile = lane / L::kHalves, half = lane % L::kHalves;
+          tma_load_4d(smem_u32(sm + L::kOffQ + tile * L::kQBytes + half * L::kQHalfBytes), &tmQ, 0, u.kv * p.G,
+                      u.r.token0 + u.tok0 + tile * p.TH, half, bar(T_QFULL), pol);
+        }
+        __syncwarp();
+        ++units;
+      }
+      const int n_pages = (u.r.kv_len + P - 1) / P;
+      // This lane's copy: the page id of its tokens, fetched a tile ahead of its use.
+      auto page_id = [&](int j) {
+        const int pos = (j * NK + lane * p.sub) / P;
+        return lane < n_copies && j < u.j1 && pos < n_pages ? __ldg(p.page_indices + u.r.page_off + pos) : -1;
+      };
+      int id = page_id(u.j0);
+      for (int j = u.j0; j < u.j1; ++j, ++g) {
+        if (j >= p.withhold_from) {
+          withheld = true;
+          break;
+        }
+        const int id_next = page_id(j + 1);
+        const int i = 2 * g + (is_v ? 1 : 0), st = i % NS;
+        if (i >= NS && !wait_all(T_EMPTY + st, uint32_t(i / NS - 1))) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(bar(T_FULL + st), L::kTileBytes);
+        __syncwarp();
+        if (lane < n_copies) {
+          const int tok = j * NK + lane * p.sub, pos = tok / P;
+          int group = -64;  // wholly outside the view: zeros
+          if (pos < n_pages) {
+            if (id < 0 || int64_t(id) >= p.num_pages) raise_fault(p.fault, PSD_FAULT_PAGE_ID);
+            else group = int((int64_t(id) * P + (tok - pos * P)) >> 3);
+          }
+          tma_load_5d(smem_u32(sm + st * L::kTileBytes + lane * copy_bytes), map, 0, 0, 0, u.kv, group, bar(T_FULL + st),
+                      pol);
+        }
+        __syncwarp();
+        id = id_next;
+      }
+    }
+    if (lane == 0) {
+      tail[is_v] = g;
+      if (!is_v) tail[2] = units;
+    }
+  } else if (warp == kMmaWarp) {
+    // ------------------------------------------------------------------- MMAs
+    const uint32_t id_s = idesc_bf16(kRows, NK, false);
+    const uint32_t id_pv = idesc_bf16(kRows, D, true);
+    // Q: 8-row groups 1024 B apart.  K (K-major): 8-token groups kGroupBytes apart, a half 1024 B
+    // further.  V (MN-major): 64-column atoms 1024 B apart, 8-token groups kGroupBytes apart.
+    const uint64_t qd = desc_sw128(smem_u32(sm + L::kOffQ), 16, 1024);
+    const uint64_t kd = desc_sw128(smem_u32(sm), 16, L::kGroupBytes);
+    const uint64_t vd = desc_sw128(smem_u32(sm), 1024, L::kGroupBytes);
+    int g = 0, units = 0;
+    uint32_t ops[2] = {0, 0};  // ops of each slot whose P was awaited
+    bool ok = true;
+    while (ok && walk.next(u)) {
+      const int nt = u.j1 - u.j0, T = u.two ? 2 * nt : nt;
+      ok = wait_all(T_QFULL, uint32_t(units));
+      if (!ok) break;
+      fence_after();
+      auto issue_s = [&](int t) -> bool {
+        const int slot = t & 1, i = 2 * (g + (u.two ? t >> 1 : t)), st = i % NS;
+        if (!(u.two && slot) && !wait_all(T_FULL + st, uint32_t(i / NS))) return false;
+        fence_after();
+        if (elect()) {
+          const uint64_t a = qd + ((u.two && slot ? L::kQBytes : 0u) >> 4);
+          const uint64_t b = kd + ((st * L::kTileBytes) >> 4);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_ss(tmem + L::kColS + slot * L::kSCols, a + (((k >> 2) * L::kQHalfBytes + (k & 3) * 32) >> 4),
+                   b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_s, k > 0);
+          commit(bar(T_SFULL + slot));
+          if (!u.two || slot) commit(bar(T_EMPTY + st));
+          if (t == T - 1) commit(bar(T_QFREE));
+        }
+        __syncwarp();
+        return true;
+      };
+      auto issue_pv = [&](int t) -> bool {
+        const int slot = t & 1, i = 2 * (g + (u.two ? t >> 1 : t)) + 1, st = i % NS;
+        if (!(u.two && slot) && !wait_all(T_FULL + st, uint32_t(i / NS))) return false;
+        if (t == 0 && units > 0 && !wait_all(T_OFREE, uint32_t(units - 1))) return false;
+        if (!wait_all(T_PFULL + slot, ops[slot])) return false;
+        ++ops[slot];
+        fence_after();
+        if (elect()) {
+          const uint32_t d = tmem + D * slot, a = tmem + L::kColS + slot * L::kSCols;
+          const uint64_t b = vd + ((st * L::kTileBytes) >> 4);
+#pragma unroll
+          for (int k = 0; k < NK / 16; ++k)
+#pragma unroll
+            for (int x = 0; x < TERMS; ++x)
+              mma_ts(d, a + x * L::kPCols + 8 * k, b + ((k * 2 * L::kGroupBytes) >> 4), id_pv, t >= 2 || k > 0 || x > 0);
+          if (!u.two || slot) commit(bar(T_EMPTY + st));
+          if (t == T - 1) commit(bar(T_OFULL));
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = issue_s(0) && (T < 2 || issue_s(1));
+      for (int t = 0; t < T && ok; ++t) ok = issue_pv(t) && (t + 2 >= T || issue_s(t + 2));
+      g += nt;
+      ++units;
+    }
+    // every MMA issued has completed before TMEM is released
+    if (elect()) commit(bar(T_DRAIN));
+    __syncwarp();
+    mbar_wait(bar(T_DRAIN), 0u, p.fault, p.wait_limit);
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int slot = warp >> 2, r = tid & 127;       // row of the tile = TMEM lane
+    const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
+    const uint32_t s_col = lane_base + L::kColS + slot * L::kSCols;
+    const float qs = p.q_scale;
+    const int rt = r / p.G, rg = r - rt * p.G;        // token of the tile, head of the group
+    int g = 0, units = 0, singles = 0;                // key tiles, units, units of one row tile so far
+    uint32_t ops = 0;
+    bool ok = true;
+    while (ok && walk.next(u)) {
+      const int nt = u.j1 - u.j0, T = u.two ? 2 * nt : nt;
+      const int tile_tok = u.tok0 + (u.two && slot ? p.TH : 0);
+      const int tok = tile_tok + rt;                  // new token of the request
+      const bool live = rt < p.TH && tok < u.r.num_new;
+      const bool warp_live = __any_sync(0xffffffffu, live);
+      const int start = u.r.kv_len - u.r.num_new;
+      uint64_t tree = 0;
+      if (has_tree && live) {
+        tree = __ldg(reinterpret_cast<const unsigned long long *>(p.tree) + u.r.token0 + tok);
+        if (u.r.num_new < 64) tree &= (uint64_t(1) << u.r.num_new) - 1;
+      }
+      const int seen = start + tok + 1;               // causal: keys before this one
+      const int clear = has_tree ? start : seen;      // every key before this one is visible
+      float m = neg_inf(), l = 0.f;
+      for (int t = slot; t < T; t += 2, ++ops) {
+        const int j = u.j0 + (u.two ? t >> 1 : t), base = j * NK;
+        ok = wait_all(T_SFULL + slot, ops);
+        if (!ok) break;
+        fence_after();
+        if (warp_live) {
+          uint32_t w[NK];
+#pragma unroll
+          for (int c = 0; c < NK; c += 32) tmem_ld32(s_col + c, w + c);
+          ld_wait();
+          float top = neg_inf();
+          if (__any_sync(0xffffffffu, live && clear < base + NK)) {
+            uint32_t bits[NK / 32];
+            visible<NK>(base, seen, start, tree, has_tree, bits);
+#pragma unroll
+            for (int c = 0; c < NK; ++c) {
+              const float s = (bits[c >> 5] >> (c & 31)) & 1u ? __uint_as_float(w[c]) : neg_inf();
+              w[c] = __float_as_uint(s);
+              top = fmaxf(top, s);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < NK; ++c) top = fmaxf(top, __uint_as_float(w[c]));
+          }
+          if (!live) top = neg_inf();                  // (a dead row's scores are whatever Q held)
+          top *= qs;                                   // qs > 0
+          const bool grow = top > m + kLazy;
+          if (__any_sync(0xffffffffu, grow)) {
+            // S(t) is complete, so PV(t - 2), issued before it, is too: O may be changed
+            const float m_new = grow ? top : m;
+            if (t >= 2) {
+              const float alpha = grow ? ex2(m - m_new) : 1.f;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(lane_base + D * slot + c, o);
+                ld_wait();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                tmem_st32(lane_base + D * slot + c, o);
+              }
+              l *= alpha;
+            }
+            m = m_new;
+          }
+          const float nm = m == neg_inf() ? 0.f : -m;
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int c0 = 0; c0 < NK; c0 += 64) {
+            uint32_t hi_w[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float a = ex2(fmaf(__uint_as_float(w[c0 + 2 * c]), qs, nm));
+              const float b = ex2(fmaf(__uint_as_float(w[c0 + 2 * c + 1]), qs, nm));
+              sum = __fadd2_rn(sum, make_float2(a, b));
+              hi_w[c] = bf16x2_bits(a, b);
+              if constexpr (TERMS > 1) {  // what the first term leaves, for the next ones
+                w[c0 + 2 * c] = __float_as_uint(a - bf16_lo(hi_w[c]));
+                w[c0 + 2 * c + 1] = __float_as_uint(b - bf16_hi(hi_w[c]));
+              }
+            }
+            tmem_st32(s_col + c0 / 2, hi_w);
+            if constexpr (TERMS > 1) {
+#pragma unroll
+              for (int x = 1; x < TERMS; ++x) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                  const float a = __uint_as_float(w[c0 + 2 * c]), b = __uint_as_float(w[c0 + 2 * c + 1]);
+                  hi_w[c] = bf16x2_bits(a, b);
+                  w[c0 + 2 * c] = __float_as_uint(a - bf16_lo(hi_w[c]));
+                  w[c0 + 2 * c + 1] = __float_as_uint(b - bf16_hi(hi_w[c]));
+                }
+                tmem_st32(s_col + x * L::kPCols + c0 / 2, hi_w);
+              }
+            }
+          }
+          l += sum.x + sum.y;
+        }
+        // V rows past the request's last token may hold anything, NaN included: the slot whose PV
+        // comes first zeroes them, so that P = 0 never meets a NaN.
+        const int left = u.r.kv_len - base;
+        if (left < NK && !(u.two && slot)) {
+          const int i = 2 * (g + (u.two ? t >> 1 : t)) + 1, st = i % NS;
+          ok = wait_all(T_FULL + st, uint32_t(i / NS));
+          if (!ok) break;
+          uint8_t *vt = sm + st * L::kTileBytes;
+          // 16-byte chunks of the tokens [left, NK): token tk's row of half h
+          for (int c = r; c < (NK - left) * L::kHalves * 8; c += 128) {
+            const int tk = left + c / (L::kHalves * 8), h = (c >> 3) % L::kHalves;
+            *reinterpret_cast<uint4 *>(vt + (tk >> 3) * L::kGroupBytes + h * 1024 + (tk & 7) * 128 + (c & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async();
+        }
+        st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(T_PFULL + slot));
+      }
+      if (!ok) break;
+
+      // ------------------------------------------------------------- epilogue
+      ok = wait_all(T_OFULL, uint32_t(units));
+      if (!ok) break;
+      fence_after();
+      const bool whole = u.j0 == 0 && u.j1 == u.n;
+      const int row = tile_tok * p.G + r - u.tok0 * p.G;   // row of the unit (p.TH * p.G a tile)
+      const int piece = 2 * blockIdx.x + (lo == walk.at - nt ? 0 : 1);  // the CTA's first piece, or its last
+      float *part = p.part_o + (int64_t(piece) * 2 * kRows + row) * D;
+      const int64_t out = (int64_t(u.r.token0) + tok) * p.Hq + u.kv * p.G + rg;
+      // One row of O, scaled, to the output or the workspace.
+      auto put32 = [&](const float *x, int c) {
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4 *>(part + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        } else if (TERMS > 1) {
+          float *dst = static_cast<float *>(p.o) + out * D + c;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<float4 *>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+        } else {
+          __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.o) + out * D + c;
+#pragma unroll
+          for (int k = 0; k < 32; k += 8)
+            *reinterpret_cast<uint4 *>(dst + k) =
+                make_uint4(bf16x2_bits(x[k], x[k + 1]), bf16x2_bits(x[k + 2], x[k + 3]), bf16x2_bits(x[k + 4], x[k + 5]),
+                           bf16x2_bits(x[k + 6], x[k + 7]));
+        }
+      };
+      auto put_lse = [&](float v) {
+        if (!whole) p.part_lse[int64_t(piece) * 2 * kRows + row] = v;
+        else if (p.lse) p.lse[out] = v;
+      };
+      if (u.two || T == 1) {
+        if (warp_live && (u.two || slot == 0)) {
+          const float inv = l == 0.f ? 0.f : p.v_scale / l;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            float x[32];
+            tmem_ld32(lane_base + D * slot + c, o);
+            ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
+            if (live) put32(x, c);
+          }
+          if (live) put_lse(l == 0.f ? neg_inf() : m + log2f(l));
+        }
+      } else if (slot == 1) {
+        // the unit's other keys: (m, l) for slot 0, which joins the two O
+        if (singles > 0) ok = wait_all(T_XFREE, uint32_t(singles - 1));
+        if (!ok) break;
+        lm[r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(T_XREADY));
+        ++singles;
+      } else {
+        ok = wait_all(T_XREADY, uint32_t(singles));
+        if (!ok) break;
+        const float2 other = lm[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(T_XFREE));
+        ++singles;
+        if (warp_live) {
+          const float m1 = other.x, l1 = other.y;
+          const float top = fmaxf(m, m1), from = top == neg_inf() ? 0.f : top;
+          const float w0 = ex2(m - from), w1 = ex2(m1 - from);  // 0 where the half saw no key
+          const float all = l * w0 + l1 * w1, inv = all == 0.f ? 0.f : p.v_scale / all;
+          const float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o0[32], o1[32];
+            float x[32];
+            tmem_ld32(lane_base + c, o0);
+            tmem_ld32(lane_base + D + c, o1);
+            ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              x[k] = (l == 0.f ? 0.f : __uint_as_float(o0[k]) * f0) + (l1 == 0.f ? 0.f : __uint_as_float(o1[k]) * f1);
+            if (live) put32(x, c);
+          }
+          if (live) put_lse(all == 0.f ? neg_inf() : top + log2f(all));
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(T_OFREE));
+      g += nt;
+      ++units;
+    }
+  }
+  st_wait();
+  fence_before();
+  __syncthreads();
+  if (warp == kKWarp) {
+    // No copy may be in flight when the CTA exits, after a wait that ran out either: the last
+    // half-tile issued into each stage, by either load warp, and the last Q.
+    if (lane < NS) {
+      int last = -1;
+      for (int v = 0; v < 2; ++v) {
+        const int top = 2 * (tail[v] - 1) + v;
+        for (int i = top; i > last && i > top - 2 * NS; i -= 2)
+          if (i % NS == lane) last = i;
+      }
+      if (last >= 0) mbar_wait(bar(T_FULL + lane), uint32_t(last / NS) & 1u, p.fault, p.wait_limit);
+    }
+    if (lane == 0 && tail[2] > 0) mbar_wait(bar(T_QFULL), uint32_t(tail[2] - 1) & 1u, p.fault, p.wait_limit);
+  }
+  if (warp == kMmaWarp) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+// Joins the pieces of the units that the CTAs' bounds cut.  blockIdx.x + 1 is a bound; it
+// works if it is the first bound inside its unit.  A warp per row; pieces in key order.
+template <int D, int NK>
+__global__ void __launch_bounds__(256)
+    step_join_kernel(const TCParams p, const __grid_constant__ TCRequests req, int ctas) {
+  const int64_t cut = int64_t(blockIdx.x + 1) * p.total / ctas;
+  Walk<NK> walk(p, req, cut, p.total);
+  Unit u;
+  if (!walk.next(u) || u.j0 == 0) return;         // the bound lies between two units
+  const int64_t first = cut - u.j0, end = first + u.n;
+  if (int64_t(blockIdx.x) * p.total / ctas > first) return;  // an earlier bound of this unit
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.y * 8 + warp;
+  const int per_tile = p.TH * p.G, tok = u.tok0 + row / p.G;
+  if (row >= (1 + u.two) * per_tile || tok >= u.r.num_new) return;
+  wait_for_prior_grid();
+  const int c0 = blockIdx.x;                      // the CTA of the unit's first piece
+  auto slot_of = [&](int c) { return 2 * c + (first <= int64_t(c) * p.total / ctas ? 0 : 1); };
+  float m = neg_inf();
+  for (int c = c0; c < ctas && int64_t(c) * p.total / ctas < end; ++c)
+    m = fmaxf(m, p.part_lse[int64_t(slot_of(c)) * 2 * kRows + row]);
+  const float from = m == neg_inf() ? 0.f : m;
+  float x[D / 32] = {}, sum = 0.f;
+  for (int c = c0; c < ctas && int64_t(c) * p.total / ctas < end; ++c) {
+    const int64_t at = int64_t(slot_of(c)) * 2 * kRows + row;
+    const float s = p.part_lse[at], w = ex2(s - from);
+    if (s == neg_inf()) continue;                 // no key of this piece is visible
+    sum += w;
+#pragma unroll
+    for (int k = 0; k < D / 32; ++k) x[k] = fmaf(w, p.part_o[at * D + 32 * k + lane], x[k]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t out = (int64_t(u.r.token0) + tok) * p.Hq + u.kv * p.G + row % p.G;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    if (p.out_f32) static_cast<float *>(p.o)[out * D + 32 * k + lane] = x[k] * inv;
+    else static_cast<__nv_bfloat16 *>(p.o)[out * D + 32 * k + lane] = __float2bfloat16_rn(x[k] * inv);
+  }
+  if (lane == 0 && p.lse) p.lse[out] = sum == 0.f ? neg_inf() : m + log2f(sum);
+}
+
+// ------------------------------------------------------------------------- launch
+bool encode(CUtensorMap *map, const DeviceInfo &dev, int rank, const void *base, const cuuint64_t *dims,
+            const cuuint64_t *strides, const cuuint32_t *box) {
+  auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(dev.encode_tiled);
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(base), dims, strides, box,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int TERMS>
+psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &place, const DeviceInfo &dev,
+               cudaStream_t s) {
+  using L = Lay<D, TERMS>;
+  TCParams p;
+  p.page_indices = S.page_indices;
+  p.tree = S.tree;
+  p.o = S.o;
+  p.lse = S.lse;
+  p.fault = S.fault;
+  p.num_pages = S.num_pages;
+  p.B = S.B;
+  p.Hq = S.Hq;
+  p.Hkv = S.Hkv;
+  p.G = S.G;
+  p.TH = kRows / S.G;
+  p.page_size = S.page_size;
+  p.sub = 8;
+  while (p.sub < L::NK && S.page_size % (2 * p.sub) == 0) p.sub *= 2;
+  p.out_f32 = S.out_f32;
+  p.q_scale = S.q_scale;
+  p.v_scale = S.v_scale;
+  p.wait_limit = dev.test_wait_limit > 0 ? dev.test_wait_limit : kWaitLimitCycles;
+  p.withhold_from = dev.test_withhold_from >= 0 ? dev.test_withhold_from : 0x7fffffff;
+  TCRequests req;
+  std::memcpy(req.r, sreq.r, sizeof(psd_token_request) * size_t(S.B));
+  int64_t total = 0;
+  int most = 0;  // rows of a unit at most
+  for (int b = 0; b < S.B; ++b) {
+    req.base[b] = int32_t(total);
+    const psd_token_request &r = req.r[b];
+    int64_t head = 0;
+    for (int t = 0; t < r.num_new; t += 2 * p.TH) head += unit_tiles(r, t, p.TH, L::NK, S.tree != nullptr);
+    total += head * S.Hkv;
+    if (total > 0x7fffffffLL)
+      return fail(PSD_ERR_UNSUPPORTED, "multi_token_decode: more than 2^31 key tiles in one launch");
+    most = std::max(most, std::min(r.num_new, 2 * p.TH) * S.G);
+  }
+  req.base[S.B] = int32_t(total);
+  p.total = total;
+  const int ctas = int(std::min<int64_t>(total, place.ctas));
+  p.part_o = place.part_o;
+  p.part_lse = place.part_lse;
+
+  CUtensorMap tmQ, tmK, tmV;
+  {
+    const cuuint64_t dims[4] = {64, cuuint64_t(S.Hq), cuuint64_t(S.num_tokens), cuuint64_t(L::kHalves)};
+    const cuuint64_t strides[3] = {cuuint64_t(D) * 2, cuuint64_t(S.q_stride) * 2, 128};
+    const cuuint32_t box[4] = {64, cuuint32_t(S.G), cuuint32_t(p.TH), 1};
+    if (!encode(&tmQ, dev, 4, S.q, dims, strides, box))
+      return fail(PSD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the queries");
+  }
+  const cuuint64_t row = cuuint64_t(S.Hkv) * D * 2;  // bytes of a token slot
+  const cuuint64_t dims[5] = {64, 8, cuuint64_t(L::kHalves), cuuint64_t(S.Hkv),
+                              cuuint64_t(S.num_pages) * cuuint64_t(S.page_size) / 8};
+  const cuuint64_t strides[4] = {row, 128, cuuint64_t(D) * 2, 8 * row};
+  const cuuint32_t box[5] = {64, 8, cuuint32_t(L::kHalves), 1, cuuint32_t(p.sub / 8)};
+  if (!encode(&tmK, dev, 5, S.k_pool, dims, strides, box) || !encode(&tmV, dev, 5, S.v_pool, dims, strides, box))
+    return fail(PSD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
+
+  auto kern = step_tc_kernel<D, TERMS>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::kSmem));
+  if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  kern<<<ctas, kThreads, L::kSmem, s>>>(tmQ, tmK, tmV, p, req);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode launch: %s", cudaGetErrorString(e));
+  // Is a unit cut?  Bounds fall on c total / ctas.
+  bool cut = false;
+  for (int c = 1, b = 0; c < ctas && !cut; ++c) {
+    const int64_t at = int64_t(c) * total / ctas;
+    while (req.base[b + 1] <= at) ++b;
+    int64_t rem = (at - req.base[b]) % ((req.base[b + 1] - req.base[b]) / S.Hkv);
+    for (int t = 0; rem > 0; t += 2 * p.TH) rem -= unit_tiles(req.r[b], t, p.TH, L::NK, S.tree != nullptr);
+    cut = rem < 0;
+  }
+  if (!cut) return PSD_OK;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas - 1), unsigned((most + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, step_join_kernel<D, L::NK>, p, req, ctas);
+  if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode join launch: %s", cudaGetErrorString(e));
+  return PSD_OK;
+}
+
+}  // namespace
+
+bool step_tc_supports(const StepParams &p) {
+  // q_scale > 0: the kernel takes the row maximum of the raw scores before scaling
+  return !p.fp8 && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.G <= kRows && p.q_scale > 0.f &&
+         p.num_pages * p.page_size / 8 < 0x7fffffffLL;
+}
+
+size_t step_tc_part_floats(int ctas, int D) { return size_t(ctas) * 2 * 2 * kRows * size_t(D + 1); }
+
+psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
+                          cudaStream_t s) {
+  if (p.D == 64) return p.out_f32 ? run<64, 3>(p, req, place, dev, s) : run<64, 1>(p, req, place, dev, s);
+  return p.out_f32 ? run<128, 3>(p, req, place, dev, s) : run<128, 1>(p, req, place, dev, s);
+}
+
+}  // namespace psd

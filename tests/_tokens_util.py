@@ -83,7 +83,7 @@ def bounds(oracle, D, n_keys, out_f32, terms):
     empty, lse = np.isneginf(lse), np.where(np.isneginf(lse), 0.0, lse)
     score = (D + 8) * 2.0 ** -23 * top + (np.abs(lse) + 40) * 2.0 ** -22 + 2.0 ** -20
     sums = (n_keys + 64) * 2.0 ** -23
-    p_round = {0: 0.0, 1: 2.0 ** -8, 2: 2.0 ** -16}[terms]
+    p_round = {0: 0.0, 1: 2.0 ** -8, 3: 2.0 ** -24}[terms]
     out = 2.0 ** -24 if out_f32 else 2.0 ** -8
     e_o = (2 * score[..., None] + sums * 2 + p_round) * pv * (1 + out) + out * np.abs(o) + 1e-30
     e_l = (score + sums) * LOG2E + 2.0 ** -22 * np.abs(lse) + 1e-30

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 
 def _tensor_cores(s, sm_scale):
-    return s.D in (64, 128) and s.page % 8 == 0 and s.Hq // s.Hkv <= 128 and sm_scale > 0
+    return s.kv == "bf16" and s.D in (64, 128) and s.page % 8 == 0 and s.Hq // s.Hkv <= 128 and sm_scale > 0
 
 
 def _run(s, *, out_f32=False, sm_scale=None, q=None, workspace=None, plan=None, o=None, lse=None, indices=None):
@@ -40,7 +40,7 @@ def _check(s, *, out_f32=False, sm_scale=None, got=None):
     n = int(s.q_indptr[-1])
     assert torch.all(o[n:] == 5.0) and torch.all(lse[n:] == 5.0)   # rows behind the last request stay
     want = s.oracle(sm_scale)
-    terms = (2 if out_f32 else 1) if _tensor_cores(s, s.sm_scale if sm_scale is None else sm_scale) else 0
+    terms = (3 if out_f32 else 1) if _tensor_cores(s, s.sm_scale if sm_scale is None else sm_scale) else 0
     e_o, e_l = bounds(want, s.D, int(s.total.max()), out_f32, terms)
     o, lse = o[:n].double().cpu().numpy(), lse[:n].double().cpu().numpy()
     empty = np.isneginf(want[1])

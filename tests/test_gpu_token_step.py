@@ -61,7 +61,7 @@ def test_three_steps(D, page, kv):
         values = [A.e4m3_to_f64(p.cpu().numpy()).reshape(shape) * c if kv == "fp8" else p.double().cpu().numpy()
                   for p, c in zip(pools, scales)]
         want = TK.attend(q_rot.double().cpu().numpy(), *values, q_indptr, length, page_indptr, indices, page, D ** -0.5)
-        e_o, e_l = bounds(want, D, max(length), True, 2)
+        e_o, e_l = bounds(want, D, max(length), True, 3)
         assert bool(np.all(np.abs(o.double().cpu().numpy() - want[0]) <= e_o))
         assert bool(np.all(np.abs(lse.double().cpu().numpy() - want[1]) <= e_l))
         # the outputs stand for the target's logits; every new token but the first is a draft
