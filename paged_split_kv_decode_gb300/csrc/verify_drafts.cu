@@ -54,91 +54,176 @@ __device__ __forceinline__ uint64_t share_of(float u, uint64_t total) {
   return sh < 128 ? hi >> (sh - 64) : 0;
 }
 
-// Inclusive sum over the block's threads in thread order; `tmp` holds a sum per warp.
-__device__ __forceinline__ uint64_t block_scan(uint64_t x, uint64_t *tmp, uint64_t &total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kMaxSums = 512;  // sums a CTA keeps of its part of a row
+
+__device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  return x;
+}
+__device__ __forceinline__ uint64_t warp_scan(uint64_t x) {  // inclusive, in lane order
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const uint64_t y = __shfl_up_sync(0xffffffffu, x, d);
     if (lane >= d) x += y;
   }
-  if (lane == 31) tmp[warp] = x;
-  __syncthreads();
-  uint64_t before = 0;
-  total = 0;
-  for (int w = 0; w < int(blockDim.x >> 5); ++w) {
-    if (w < warp) before += tmp[w];
-    total += tmp[w];
-  }
-  __syncthreads();
-  return x + before;
+  return x;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint64_t peer_load(const uint64_t *mine, int rank) {
+  uint32_t at;
+  uint64_t x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(mine)), "r"(rank));
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
+  return x;
 }
 
-// One CTA per request: the accepted drafts, then two passes over the chosen row.
-__global__ void __launch_bounds__(1024) verify_drafts_kernel(const VerifyParams p) {
-  __shared__ uint64_t tmp[32];
-  __shared__ int first_refused, found;
-  const int b = blockIdx.x, tid = threadIdx.x;
-  const int d0 = p.indptr[b], d1 = p.indptr[b + 1];
-  if (d0 < 0 || d1 < d0 || d1 > p.num_drafts) {
-    if (tid == 0) atomicOr(p.fault, PSD_FAULT_RANGE);
+// The row that the next token is drawn from: weights max(p - q, 0).
+struct Row {
+  const float *p, *q;  // q NULL: p alone
+  int hot;             // a token of weight 0, or -1
+  __device__ __forceinline__ uint64_t at(int v) const {
+    return v == hot ? 0 : (q ? weight(__ldg(p + v), __ldg(q + v)) : fix58(__ldg(p + v)));
+  }
+};
+
+// One cluster per request.  Every CTA finds the accepted drafts for itself (a gather of
+// K values of p and q); then the CTAs share out the chosen row, a stretch each: a warp sums
+// blocks of `step` entries, keeping each block's sum, so that the row is read once, and
+// the CTA that holds the crossing looks only at the block where it lies again.
+// The work is the row's bytes: 8 V with a refusal, 4 V without; 8 CTAs a request put
+// enough loads in flight from one request on.
+__global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const VerifyParams p, int ctas) {
+  __shared__ uint64_t sums[kMaxSums], warps[kVerifyWarps], mine;
+  __shared__ int first_refused;
+  const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int d0 = __ldg(p.indptr + b), d1 = __ldg(p.indptr + b + 1);
+  if (d0 < 0 || d1 < d0 || d1 > p.num_drafts) {  // the whole cluster leaves
+    if (rank == 0 && tid == 0) atomicOr(p.fault, PSD_FAULT_RANGE);
     return;
   }
   const int K = d1 - d0, R = d0 + b;
-  if (tid == 0) first_refused = K, found = p.V;
+  if (tid == 0) first_refused = K;
   __syncthreads();
-  for (int j = tid; j < K; j += blockDim.x) {
-    const int d = p.tokens[d0 + j];
-    const bool inside = d >= 0 && d < p.V;
+  for (int j = tid; j < K; j += kVerifyThreads) {
+    const int d = __ldg(p.tokens + d0 + j);
     bool ok = false;
-    if (inside) {
-      const double q = p.draft ? double(p.draft[(d0 + j) * p.draft_stride + d]) : 1.0;
-      ok = double(p.uniforms[R + j]) * q < double(p.target[(R + j) * p.target_stride + d]);
+    if (d >= 0 && d < p.V) {
+      const double q = p.draft ? double(__ldg(p.draft + (d0 + j) * p.draft_stride + d)) : 1.0;
+      ok = double(__ldg(p.uniforms + R + j)) * q < double(__ldg(p.target + (R + j) * p.target_stride + d));
     }
     if (!ok) atomicMin(&first_refused, j);
   }
+  const float u = __ldg(p.uniforms + R + K);
   __syncthreads();
   const int a = first_refused;
-  const float *prow = p.target + (R + a) * p.target_stride;
-  const float *qrow = nullptr;
-  int hot = -1;  // the refused token of a draft without probabilities
+  Row row{p.target + (R + a) * p.target_stride, nullptr, -1};
+  bool outside = false;
   if (a < K) {
-    const int d = p.tokens[d0 + a];
-    if (d < 0 || d >= p.V) {
-      if (tid == 0) atomicOr(p.fault, PSD_FAULT_RANGE);
-    } else if (p.draft) {
-      qrow = p.draft + (d0 + a) * p.draft_stride;
-    } else {
-      hot = d;
+    const int d = __ldg(p.tokens + d0 + a);
+    outside = d < 0 || d >= p.V;
+    if (!outside && p.draft) row.q = p.draft + (d0 + a) * p.draft_stride;
+    if (!outside && !p.draft) row.hot = d;
+  }
+  // This CTA's entries [v0, v1), in blocks of `step` (a multiple of 256).
+  const int part = (p.V + ctas - 1) / ctas;
+  const int v0 = min(rank * part, p.V), v1 = min(v0 + part, p.V);
+  const int step = 256 * ((part + 256 * kMaxSums - 1) / (256 * kMaxSums));
+  const int blocks = (v1 - v0 + step - 1) / step;
+  uint64_t total = 0, before = 0;
+  for (int pass = 0; pass < 2 && total == 0; ++pass) {
+    if (pass == 1) {  // p <= q everywhere: draw from p
+      row.q = nullptr, row.hot = -1;
+      cluster_sync();  // the peers have read `mine`
+    }
+    uint64_t own = 0;
+    for (int k = warp; k < blocks; k += kVerifyWarps) {
+      const int lo = v0 + k * step, hi = min(lo + step, v1);
+      uint64_t x = 0;
+      for (int c = lo; c < hi; c += 256) {
+        if (c + 256 <= hi) {
+          float pv[8], qv[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) pv[i] = __ldg(row.p + c + 32 * i + lane);
+          if (row.q) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) qv[i] = __ldg(row.q + c + 32 * i + lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x += weight(pv[i], qv[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x += c + 32 * i + lane == row.hot ? 0 : fix58(pv[i]);
+          }
+        } else {
+          for (int v = c + lane; v < hi; v += 32) x += row.at(v);
+        }
+      }
+      x = warp_sum(x);
+      if (lane == 0) sums[k] = x;
+      own += x;
+    }
+    if (lane == 0) warps[warp] = own;
+    __syncthreads();
+    if (tid == 0) {
+      uint64_t x = 0;
+      for (int w = 0; w < kVerifyWarps; ++w) x += warps[w];
+      mine = x;
+    }
+    cluster_sync();
+    total = before = 0;
+    for (int c = 0; c < ctas; ++c) {
+      const uint64_t x = peer_load(&mine, c);
+      if (c < rank) before += x;
+      total += x;
     }
   }
-  uint64_t total = 0;
-  for (int pass = 0; pass < 2 && total == 0; ++pass) {
-    if (pass == 1) qrow = nullptr, hot = -1;  // p <= q everywhere: draw from p
-    uint64_t sum = 0;
-    for (int v = tid; v < p.V; v += blockDim.x)
-      if (v != hot) sum += weight(prow[v], qrow ? qrow[v] : 0.f);
-    block_scan(sum, tmp, total);
+  const uint64_t own = mine;
+  uint64_t want = share_of(u, total);
+  if (want >= total && total) want = total - 1;  // u >= 1 (outside the contract): the last entry with a weight
+  if (warp == 0 && total && before <= want && want < before + own) {
+    // the block, then the entry, at which the running sum passes `want`
+    want -= before;
+    int k0 = 0;
+    uint64_t run = 0;
+    for (;; k0 += 32) {
+      const uint64_t x = warp_scan(k0 + lane < blocks ? sums[k0 + lane] : 0);
+      const uint32_t past = __ballot_sync(0xffffffffu, run + x > want);
+      const int f = past ? __ffs(past) - 1 : 32;
+      if (f > 0) {
+        const uint64_t y = __shfl_sync(0xffffffffu, x, f - 1);
+        run += y;
+      }
+      if (past || k0 + 32 >= blocks) {
+        k0 += f;
+        break;
+      }
+    }
+    const int lo = v0 + k0 * step, hi = min(lo + step, v1);
+    for (int c = lo; c < hi; c += 32) {
+      const int v = c + lane;
+      const uint64_t x = warp_scan(v < hi ? row.at(v) : 0);
+      const uint32_t past = __ballot_sync(0xffffffffu, run + x > want);
+      if (past) {
+        if (lane == 0) p.out[R + a] = c + __ffs(past) - 1;
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, x, 31);
+    }
   }
-  const uint64_t want = share_of(p.uniforms[R + K], total);
-  uint64_t before = 0;
-  for (int v0 = 0; v0 < p.V && total; v0 += blockDim.x) {
-    const int v = v0 + tid;
-    const uint64_t w = v < p.V && v != hot ? weight(prow[v], qrow ? qrow[v] : 0.f) : 0;
-    uint64_t here;
-    const uint64_t c = before + block_scan(w, tmp, here);
-    // u >= 1 (outside the contract): the last entry with a weight
-    if (w && (c > want || (want >= total && c == total))) atomicMin(&found, v);
-    before += here;
-    if (before > want || before == total) break;
+  if (rank == 0) {
+    for (int j = tid; j <= K; j += kVerifyThreads)
+      if (j != a || !total) p.out[R + j] = j < a ? __ldg(p.tokens + d0 + j) : -1;
+    if (tid == 0) {
+      p.accepted[b] = a;
+      if (outside || !total) atomicOr(p.fault, PSD_FAULT_RANGE);
+    }
   }
-  __syncthreads();
-  for (int j = tid; j <= K; j += blockDim.x)
-    p.out[R + j] = j < a ? p.tokens[d0 + j] : (j == a && total ? found : -1);
-  if (tid == 0) {
-    p.accepted[b] = a;
-    if (!total) atomicOr(p.fault, PSD_FAULT_RANGE);
-  }
+  cluster_sync();  // a peer may still read `mine`
 }
 
 }  // namespace
@@ -149,11 +234,12 @@ using namespace psd;
 extern "C" psd_status verify_drafts(psd_ctx *ctx, const psd_verify_args *a, psd_stream_t stream) {
   clear_error();
   if (!ctx || !a) return fail(PSD_ERR_INVALID_ARG, "verify_drafts: NULL");
-  if (a->batch < 0 || a->num_drafts < 0 || a->vocab < 1 || (a->batch == 0 && a->num_drafts > 0))
+  if (a->batch < 0 || a->num_drafts < 0 || a->vocab < 1 || a->vocab > (1 << 30) || (a->batch == 0 && a->num_drafts > 0))
     return fail(PSD_ERR_INVALID_ARG, "verify_drafts: batch %d, num_drafts %d, vocab %d", a->batch, a->num_drafts,
                 a->vocab);
   if (int64_t(a->batch) + a->num_drafts > 0x7fffffffLL) return fail(PSD_ERR_INVALID_ARG, "verify_drafts: too many rows");
   if (a->batch == 0) return PSD_OK;
+  if (a->batch > 0x7fffffff / 8) return fail(PSD_ERR_UNSUPPORTED, "verify_drafts: batch %d", a->batch);
   if (!a->target_probs || !a->draft_indptr || !a->uniforms || !a->num_accepted || !a->out_tokens || !a->fault_dev ||
       (a->num_drafts > 0 && !a->draft_tokens))
     return fail(PSD_ERR_INVALID_ARG, "verify_drafts: NULL pointer");
@@ -162,8 +248,20 @@ extern "C" psd_status verify_drafts(psd_ctx *ctx, const psd_verify_args *a, psd_
   DeviceGuard g(ctx->dev.device);
   VerifyParams p{a->target_probs, a->draft_probs, a->target_stride, a->draft_stride, a->draft_tokens, a->draft_indptr,
                  a->uniforms, a->num_accepted, a->out_tokens, a->fault_dev, a->batch, a->num_drafts, a->vocab};
-  verify_drafts_kernel<<<a->batch, 1024, 0, reinterpret_cast<cudaStream_t>(stream)>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  // 2048 entries or more a CTA, 8 CTAs (the portable cluster) at most
+  int ctas = 1;
+  while (ctas < 8 && a->vocab > 2048 * ctas) ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(a->batch) * unsigned(ctas));
+  cfg.blockDim = dim3(kVerifyThreads);
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_drafts_kernel, p, ctas);
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "verify_drafts launch: %s", cudaGetErrorString(e));
   return PSD_OK;
 }
