@@ -162,6 +162,186 @@ __global__ void __launch_bounds__(256)
     put(p.v_pool, x.slot * nv + j, __bfloat162float(p.v[t * p.v_stride + j]), p.fp8 != 0, p.v_scale);
 }
 
+// ------------------------------------------------------------------ 16-byte form
+// NT consecutive tokens per CTA, 8 pairs or 8 columns a thread and access.  A thread takes
+// the same columns of all NT tokens, so that index arithmetic is paid once and NT loads
+// are in flight; the first queries are on their way while the places and angles are found.
+struct F8 {
+  float v[8];
+};
+__device__ __forceinline__ F8 unpack8(uint4 w) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  F8 f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f.v[2 * k] = bf16_lo(u[k]);
+    f.v[2 * k + 1] = bf16_hi(u[k]);
+  }
+  return f;
+}
+__device__ __forceinline__ uint4 pack8(const F8 &f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    __nv_bfloat162 x = __floats2bfloat162_rn(f.v[2 * k], f.v[2 * k + 1]);
+    u[k] = *reinterpret_cast<uint32_t *>(&x);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
+}
+// Eight values at element `at` of a pool.
+__device__ __forceinline__ void put8(void *pool, int64_t at, const F8 &f, bool fp8, float scale) {
+  if (!fp8) {
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(pool) + at) = pack8(f);
+    return;
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fdiv_rn(f.v[4 * k + 1], scale)), "f"(__fdiv_rn(f.v[4 * k], scale)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fdiv_rn(f.v[4 * k + 3], scale)), "f"(__fdiv_rn(f.v[4 * k + 2], scale)));
+    w[k] = uint32_t(lo) | (uint32_t(hi) << 16);
+  }
+  *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(pool) + at) = make_uint2(w[0], w[1]);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(256)
+    append_tokens_vec_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
+  __shared__ __align__(16) float cosine[NT][kMaxPairs], sine[NT][kMaxPairs];
+  __shared__ Place places[NT];
+  const int t0 = blockIdx.x * NT, tid = threadIdx.x;
+  const int half = p.rot / 2, groups = half / 8;          // 8-pair groups of a head
+  const int rest = (p.D - p.rot) / 8;                     // 8-column chunks outside the rotation
+  const bool neox = p.neox != 0, fp8 = p.fp8 != 0;
+  // Group g of a head: its two runs of 8 columns start at a and a + far.
+  const int far = neox ? half : 8;
+  auto column = [&](int g) { return p.rot_col + (neox ? 8 * g : 16 * g); };
+  auto load = [&](uint4 (&x)[NT][2], const __nv_bfloat16 *src, int64_t stride, int col) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const uint4 *at = reinterpret_cast<const uint4 *>(src + (t0 + n) * stride + col);
+      if (t0 + n < p.T) {
+        x[n][0] = *at;
+        x[n][1] = *reinterpret_cast<const uint4 *>(src + (t0 + n) * stride + col + far);
+      }
+    }
+  };
+  // Rotates token n's group g in place: f0 and f1 are its two runs.
+  auto rotate = [&](int n, int g, F8 &f0, F8 &f1) {
+    float c[8], s[8];
+#pragma unroll
+    for (int k = 0; k < 8; k += 4) {
+      *reinterpret_cast<float4 *>(c + k) = *reinterpret_cast<const float4 *>(&cosine[n][8 * g + k]);
+      *reinterpret_cast<float4 *>(s + k) = *reinterpret_cast<const float4 *>(&sine[n][8 * g + k]);
+    }
+    if (neox) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float x = f0.v[k], y = f1.v[k];
+        f0.v[k] = x * c[k] - y * s[k];
+        f1.v[k] = y * c[k] + x * s[k];
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = f0.v[2 * k], y = f0.v[2 * k + 1], z = f1.v[2 * k], w = f1.v[2 * k + 1];
+        f0.v[2 * k] = x * c[k] - y * s[k];
+        f0.v[2 * k + 1] = y * c[k] + x * s[k];
+        f1.v[2 * k] = z * c[k + 4] - w * s[k + 4];
+        f1.v[2 * k + 1] = w * c[k + 4] + z * s[k + 4];
+      }
+    }
+  };
+
+  const int nq = p.Hq * groups;
+  uint4 x[NT][2];
+  int j = tid, h = j / groups, col = column(j - h * groups);
+  if (j < nq) load(x, p.q + int64_t(h) * p.D, p.q_stride, col);
+  for (int n = tid >> 5; n < NT; n += 8) {                 // a warp per token
+    uint32_t faults = 0;
+    Place at{-1, -1};
+    if (t0 + n < p.T) at = place_of(p, t0 + n, faults);
+    if ((tid & 31) == 0) {
+      places[n] = at;
+      if (faults) atomicOr(p.fault, int32_t(faults));
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < NT * half; i += 256) {
+    const int n = i / half, k = i - n * half;
+    const float2 cs = places[n].pos >= 0 ? turn(turns.f[k], places[n].pos, p.magnitude) : make_float2(0.f, 0.f);
+    cosine[n][k] = cs.x;
+    sine[n][k] = cs.y;
+  }
+  __syncthreads();
+  // ---- queries
+  while (j < nq) {
+    const int g = j - h * groups;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      if (places[n].pos < 0) continue;
+      F8 f0 = unpack8(x[n][0]), f1 = unpack8(x[n][1]);
+      rotate(n, g, f0, f1);
+      __nv_bfloat16 *dst = p.q_out + (int64_t(t0 + n) * p.Hq + h) * p.D + col;
+      *reinterpret_cast<uint4 *>(dst) = pack8(f0);
+      *reinterpret_cast<uint4 *>(dst + far) = pack8(f1);
+    }
+    j += 256;
+    if (j >= nq) break;
+    h = j / groups;
+    col = column(j - h * groups);
+    load(x, p.q + int64_t(h) * p.D, p.q_stride, col);
+  }
+  // ---- keys
+  for (j = tid; j < p.Hkv * groups; j += 256) {
+    h = j / groups;
+    const int g = j - h * groups;
+    col = column(g);
+    load(x, p.k + int64_t(h) * p.D, p.k_stride, col);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const Place at = places[n];
+      if (at.pos < 0 || at.slot < 0) continue;
+      F8 f0 = unpack8(x[n][0]), f1 = unpack8(x[n][1]);
+      rotate(n, g, f0, f1);
+      const int64_t dst = (at.slot * p.Hkv + h) * p.D + col;
+      put8(p.k_pool, dst, f0, fp8, p.k_scale);
+      put8(p.k_pool, dst + far, f1, fp8, p.k_scale);
+    }
+  }
+  // ---- columns outside the rotation, and V
+  const int cq = p.Hq * rest, ck = p.Hkv * rest, cv = p.Hkv * p.Dv / 8;
+  for (j = tid; j < cq + ck + cv; j += 256) {
+    const bool is_q = j < cq, is_k = !is_q && j < cq + ck;
+    const int i = is_q ? j : is_k ? j - cq : j - cq - ck;
+    int64_t off;  // in the token's heads
+    if (is_q || is_k) {
+      h = i / rest;
+      col = 8 * (i - h * rest);
+      if (col >= p.rot_col) col += p.rot;
+      off = int64_t(h) * p.D + col;
+    } else {
+      off = 8 * int64_t(i);
+    }
+    const __nv_bfloat16 *src = (is_q ? p.q : is_k ? p.k : p.v) + off;
+    const int64_t stride = is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride;
+    uint4 y[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (t0 + n < p.T) y[n] = *reinterpret_cast<const uint4 *>(src + (t0 + n) * stride);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const Place at = places[n];
+      if (at.pos < 0) continue;
+      if (is_q) *reinterpret_cast<uint4 *>(p.q_out + int64_t(t0 + n) * p.Hq * p.D + off) = y[n];
+      else if (at.slot < 0) continue;
+      else if (is_k) put8(p.k_pool, at.slot * p.Hkv * p.D + off, unpack8(y[n]), fp8, p.k_scale);
+      else put8(p.v_pool, at.slot * p.Hkv * p.Dv + off, unpack8(y[n]), fp8, p.v_scale);
+    }
+  }
+}
+
 }  // namespace
 
 static psd_status launch_append_tokens(const psd_append_args *a, cudaStream_t s) {
@@ -204,7 +384,14 @@ static psd_status launch_append_tokens(const psd_append_args *a, cudaStream_t s)
     const double f = a->inv_freq[i] * (0.5 / 3.14159265358979323846);
     turns.f[i] = uint64_t(std::ldexp(f - std::floor(f), 64));
   }
-  append_tokens_kernel<<<a->num_tokens, 256, 0, s>>>(p, turns);
+  auto fits = [](const void *ptr, int64_t stride) { return aligned16(ptr) && stride % 8 == 0; };
+  const bool vec = a->rot_dim % 16 == 0 && a->rot_col % 8 == 0 && a->D % 8 == 0 && a->Dv % 8 == 0 &&
+                   fits(a->q, a->Hq ? a->q_stride : 0) && fits(a->k, a->k_stride) && fits(a->v, a->Dv ? a->v_stride : 0) &&
+                   aligned16(a->q_out) && aligned16(a->k_pool) && aligned16(a->v_pool);
+  constexpr int kMany = 4;
+  if (!vec) append_tokens_kernel<<<a->num_tokens, 256, 0, s>>>(p, turns);
+  else if (a->num_tokens < 2048) append_tokens_vec_kernel<1><<<a->num_tokens, 256, 0, s>>>(p, turns);
+  else append_tokens_vec_kernel<kMany><<<(a->num_tokens - 1) / kMany + 1, 256, 0, s>>>(p, turns);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "append_tokens launch: %s", cudaGetErrorString(e));
   return PSD_OK;
