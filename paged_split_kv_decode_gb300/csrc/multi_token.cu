@@ -164,7 +164,7 @@ using namespace psd;
 extern "C" size_t psd_multi_token_workspace_bytes(const psd_ctx *ctx, int32_t D) {
   if (!ctx || D < 1) return 0;
   // the fault word, then the partial rows of the tensor-core kernel's CTAs, one per SM
-  return 256 + (D == 64 || D == 128 ? 4 * step_tc_part_floats(ctx->dev.num_sms, D) : 0);
+  return 256 + (D == 64 || D == 128 ? 4 * step_tc_place(ctx->dev.num_sms, D, nullptr).floats : 0);
 }
 
 extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *a, const psd_multi_token_plan *plan,
@@ -238,10 +238,8 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   p.out_f32 = a->out_f32 != 0;
   p.q_scale = a->sm_scale * 1.4426950408889634f * (fp8 ? a->k_scale : 1.f);
   p.v_scale = fp8 ? a->v_scale : 1.f;
-  StepPlace place;
-  place.ctas = ctx->dev.num_sms > 0 ? ctx->dev.num_sms : 1;
-  place.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256);
-  place.part_lse = place.part_o + size_t(place.ctas) * 512 * size_t(a->D);
+  const StepPlace place =
+      step_tc_place(ctx->dev.num_sms, a->D, reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256));
   StepRequests req;
   const bool tensor = step_tc_supports(p);
   for (int32_t b0 = 0; b0 < plan->batch;) {

@@ -31,12 +31,14 @@ struct StepParams {
   float v_scale;
 };
 
-// The tensor-core kernel's CTAs and where they keep the partial rows of units they share.
+// The tensor-core kernel's CTAs, and where they keep the partial rows of units they share and
+// the sums of f32 outputs: `floats` from a 16-byte aligned base on.
 struct StepPlace {
   int ctas;
-  float *part_o, *part_lse;
+  float *part_o, *sum_o, *part_lse;
+  size_t floats;
 };
-size_t step_tc_part_floats(int ctas, int D);
+StepPlace step_tc_place(int ctas, int D, float *base);
 bool step_tc_supports(const StepParams &p);
 psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
                           cudaStream_t s);

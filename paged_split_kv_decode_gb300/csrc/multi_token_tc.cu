@@ -34,6 +34,10 @@
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
 // terms of NK keys need 3 NK / 2 columns, which is why f32 outputs take tiles of 64 keys.
+// The tensor cores' f32 accumulation cuts low bits at every step of 16 keys and term, always
+// towards zero: over 8000 keys it cost 1.3e-5 of the result's norm.  bf16 outputs do not
+// see that; for f32 outputs O starts anew every kFlush ops of a slot, and the rows add what
+// they read out to a sum in the workspace, rounded to nearest.
 // The row maximum follows lazily: O and l are rescaled only when it grows by more than
 // 2^8, so P <= 2^8.
 #include <cuda.h>
@@ -57,6 +61,7 @@ constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
 constexpr int kThreads = 11 * 32;
 constexpr uint32_t kRingBytes = 160 * 1024;
 constexpr int kMaxStages = 20;
+constexpr int kFlush = 16;       // f32 outputs: ops of a slot (64 keys each) O holds at most
 
 template <int D, int TERMS>
 struct Lay {
@@ -100,6 +105,7 @@ struct TCParams {
   float *lse;
   float *part_o;    // [CTAs][2][2 * 128 rows][D]
   float *part_lse;  // [CTAs][2][2 * 128 rows]
+  float *sum_o;     // [CTAs][2 slots][128 rows][D], f32 outputs only
   FaultRef fault;
   int64_t num_pages;
   int64_t total;    // key tiles of the launch
@@ -430,11 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect()) {
           const uint32_t d = tmem + D * slot, a = tmem + L::kColS + slot * L::kSCols;
           const uint64_t b = vd + ((st * L::kTileBytes) >> 4);
+          const bool fresh = TERMS > 1 ? (t >> 1) % kFlush == 0 : t < 2;  // O starts at zero
 #pragma unroll
           for (int k = 0; k < NK / 16; ++k)
 #pragma unroll
             for (int x = 0; x < TERMS; ++x)
-              mma_ts(d, a + x * L::kPCols + 8 * k, b + ((k * 2 * L::kGroupBytes) >> 4), id_pv, t >= 2 || k > 0 || x > 0);
+              mma_ts(d, a + x * L::kPCols + 8 * k, b + ((k * 2 * L::kGroupBytes) >> 4), id_pv, !fresh || k > 0 || x > 0);
           if (!u.two || slot) commit(bar(T_EMPTY + st));
           if (t == T - 1) commit(bar(T_OFULL));
         }
@@ -475,6 +482,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = start + tok + 1;               // causal: keys before this one
       const int clear = has_tree ? start : seen;      // every key before this one is visible
       float m = neg_inf(), l = 0.f;
+      // f32 outputs: the row's O of the ops before the last flush, relative to 2^m_sum
+      float *sum_row = p.sum_o + ((int64_t(blockIdx.x) * 2 + slot) * kRows + r) * D;
+      float m_sum = neg_inf();
+      bool flushed = false;
       for (int t = slot; t < T; t += 2, ++ops) {
         const int j = u.j0 + (u.two ? t >> 1 : t), base = j * NK;
         ok = wait_all(T_SFULL + slot, ops);
@@ -485,6 +496,33 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NK; c += 32) tmem_ld32(s_col + c, w + c);
           ld_wait();
+          bool empty = t < 2;                           // O holds nothing
+          if constexpr (TERMS > 1) {
+            if (t >= 2 && (t >> 1) % kFlush == 0) {
+              // S(t) is complete, so PV(t - 2), issued before it, is too
+              const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                uint32_t o[32];
+                tmem_ld32(lane_base + D * slot + c, o);
+                ld_wait();
+                if (live) {
+#pragma unroll
+                  for (int k = 0; k < 32; k += 4) {
+                    float4 *at = reinterpret_cast<float4 *>(sum_row + c + k);
+                    float4 x = flushed ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x.x = fmaf(x.x, keep, __uint_as_float(o[k]));
+                    x.y = fmaf(x.y, keep, __uint_as_float(o[k + 1]));
+                    x.z = fmaf(x.z, keep, __uint_as_float(o[k + 2]));
+                    x.w = fmaf(x.w, keep, __uint_as_float(o[k + 3]));
+                    *at = x;
+                  }
+                }
+              }
+              m_sum = m;
+              flushed = empty = true;
+            }
+          }
           float top = neg_inf();
           if (__any_sync(0xffffffffu, live && clear < base + NK)) {
             uint32_t bits[NK / 32];
@@ -505,8 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (__any_sync(0xffffffffu, grow)) {
             // S(t) is complete, so PV(t - 2), issued before it, is too: O may be changed
             const float m_new = grow ? top : m;
-            if (t >= 2) {
-              const float alpha = grow ? ex2(m - m_new) : 1.f;
+            const float alpha = grow ? ex2(m - m_new) : 1.f;
+            l *= alpha;
+            if (!empty) {
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -516,7 +555,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
                 tmem_st32(lane_base + D * slot + c, o);
               }
-              l *= alpha;
             }
             m = m_new;
           }
@@ -585,6 +623,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int piece = 2 * blockIdx.x + (lo == walk.at - nt ? 0 : 1);  // the CTA's first piece, or its last
       float *part = p.part_o + (int64_t(piece) * 2 * kRows + row) * D;
       const int64_t out = (int64_t(u.r.token0) + tok) * p.Hq + u.kv * p.G + rg;
+      // What the flushed ops of slot `of` add to column c + k of the row, scaled to 2^m_of.
+      const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);
+      auto add_flushed = [&](float *x, int c, const float *row_of, float scale) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 y = *reinterpret_cast<const float4 *>(row_of + c + k);
+          x[k] = fmaf(y.x, scale, x[k]);
+          x[k + 1] = fmaf(y.y, scale, x[k + 1]);
+          x[k + 2] = fmaf(y.z, scale, x[k + 2]);
+          x[k + 3] = fmaf(y.w, scale, x[k + 3]);
+        }
+      };
       // One row of O, scaled, to the output or the workspace.
       auto put32 = [&](const float *x, int c) {
         if (!whole) {
@@ -620,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ld_wait();
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
+            if (TERMS > 1 && live && flushed && l != 0.f) add_flushed(x, c, sum_row, keep * inv);
             if (live) put32(x, c);
           }
           if (live) put_lse(l == 0.f ? neg_inf() : m + log2f(l));
@@ -628,6 +679,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the unit's other keys: (m, l) for slot 0, which joins the two O
         if (singles > 0) ok = wait_all(T_XFREE, uint32_t(singles - 1));
         if (!ok) break;
+        if constexpr (TERMS > 1) {
+          // fold the flushed sum into 2^m units, so that slot 0 needs no more than (m, l)
+          if (live && flushed && l != 0.f && keep != 1.f) {
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+              float4 *at = reinterpret_cast<float4 *>(sum_row + c);
+              float4 x = *at;
+              *at = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
+            }
+          }
+          __threadfence_block();
+        }
         lm[r] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(T_XREADY));
@@ -655,6 +718,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 32; ++k)
               x[k] = (l == 0.f ? 0.f : __uint_as_float(o0[k]) * f0) + (l1 == 0.f ? 0.f : __uint_as_float(o1[k]) * f1);
+            if constexpr (TERMS > 1) {
+              // (slot 1 flushed if it had more than kFlush ops: every row, its T / 2 ops)
+              if (live && flushed && l != 0.f) add_flushed(x, c, sum_row, keep * f0);
+              if (live && (T >> 1) > kFlush && l1 != 0.f) add_flushed(x, c, sum_row + kRows * D, f1);
+            }
             if (live) put32(x, c);
           }
           if (live) put_lse(all == 0.f ? neg_inf() : top + log2f(all));
@@ -784,6 +852,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   const int ctas = int(std::min<int64_t>(total, place.ctas));
   p.part_o = place.part_o;
   p.part_lse = place.part_lse;
+  p.sum_o = place.sum_o;
 
   CUtensorMap tmQ, tmK, tmV;
   {
@@ -839,7 +908,15 @@ bool step_tc_supports(const StepParams &p) {
          p.num_pages * p.page_size / 8 < 0x7fffffffLL;
 }
 
-size_t step_tc_part_floats(int ctas, int D) { return size_t(ctas) * 2 * 2 * kRows * size_t(D + 1); }
+StepPlace step_tc_place(int ctas, int D, float *base) {
+  StepPlace x;
+  x.ctas = ctas;
+  x.part_o = base;
+  x.sum_o = x.part_o + size_t(ctas) * 4 * kRows * size_t(D);
+  x.part_lse = x.sum_o + size_t(ctas) * 2 * kRows * size_t(D);
+  x.floats = size_t(ctas) * kRows * (6 * size_t(D) + 4);
+  return x;
+}
 
 psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
                           cudaStream_t s) {
