@@ -698,9 +698,9 @@ psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *args,
  * q is 1 at the draft token and 0 elsewhere.
  * out_tokens[R_b ..]: the a accepted drafts, the new token, then -1.  num_accepted[b] = a.
  * Products and comparisons of the acceptance are exact; the running sums are exact sums
- * of the probabilities cut at 2^-58, so the outcome does not depend on the order of
- * summation.  Probabilities are f32 in [0, 1] and each row sums to at most 16; values that
- * are not (NaN, negative) count as 0, larger than 1 as 1.  A draft token outside [0, vocab)
+ * of the weights rounded to multiples of 2^-46, so the outcome does not depend on the order
+ * of summation.  Probabilities are f32 in [0, 1]; in the weights, values that are not (NaN,
+ * negative) count as 0, larger than 1 as 1.  A draft token outside [0, vocab)
  * is refused, its q is 0 everywhere, and PSD_FAULT_RANGE is set; so is a row whose
  * weights are all 0 (its new token is -1).  Rows with no request are not touched. */
 typedef struct {

@@ -758,43 +758,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of the units that the CTAs' bounds cut.  blockIdx.x + 1 is a bound; it
-// works if it is the first bound inside its unit.  A warp per row; pieces in key order.
-template <int D, int NK>
-__global__ void __launch_bounds__(256)
-    step_join_kernel(const TCParams p, const __grid_constant__ TCRequests req, int ctas) {
-  const int64_t cut = int64_t(blockIdx.x + 1) * p.total / ctas;
-  Walk<NK> walk(p, req, cut, p.total);
-  Unit u;
-  if (!walk.next(u) || u.j0 == 0) return;         // the bound lies between two units
-  const int64_t first = cut - u.j0, end = first + u.n;
-  if (int64_t(blockIdx.x) * p.total / ctas > first) return;  // an earlier bound of this unit
+// A unit that the CTAs' bounds cut.
+struct Cut {
+  int64_t out;   // output row of the unit's first token and head
+  int rows;      // live rows
+  int first, n;  // the CTA of its first piece, and its pieces: one a CTA from there on
+  int late;      // the first piece is the second of its CTA
+};
+constexpr int kMaxCuts = 192;  // bounds of a launch, one less than its CTAs
+struct Cuts {
+  Cut c[kMaxCuts];
+};
+
+// Joins the pieces of the cut units (blockIdx.x), in key order: a warp per row.  The host
+// names them: found by a walk on the device, as the main kernel's stretches are, they cost
+// 47 us behind a 4096-token prompt against 17.
+template <int D>
+__global__ void __launch_bounds__(256) step_join_kernel(const TCParams p, const __grid_constant__ Cuts cuts) {
+  const Cut &u = cuts.c[blockIdx.x];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.y * 8 + warp;
-  const int per_tile = p.TH * p.G, tok = u.tok0 + row / p.G;
-  if (row >= (1 + u.two) * per_tile || tok >= u.r.num_new) return;
+  if (row >= u.rows) return;
   wait_for_prior_grid();
-  const int c0 = blockIdx.x;                      // the CTA of the unit's first piece
-  auto slot_of = [&](int c) { return 2 * c + (first <= int64_t(c) * p.total / ctas ? 0 : 1); };
+  auto at = [&](int i) { return int64_t(2 * (u.first + i) + (i == 0 ? u.late : 0)) * 2 * kRows + row; };
   float m = neg_inf();
-  for (int c = c0; c < ctas && int64_t(c) * p.total / ctas < end; ++c)
-    m = fmaxf(m, p.part_lse[int64_t(slot_of(c)) * 2 * kRows + row]);
+  for (int i = lane; i < u.n; i += 32) m = fmaxf(m, p.part_lse[at(i)]);
+#pragma unroll
+  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float from = m == neg_inf() ? 0.f : m;
   float x[D / 32] = {}, sum = 0.f;
-  for (int c = c0; c < ctas && int64_t(c) * p.total / ctas < end; ++c) {
-    const int64_t at = int64_t(slot_of(c)) * 2 * kRows + row;
-    const float s = p.part_lse[at], w = ex2(s - from);
-    if (s == neg_inf()) continue;                 // no key of this piece is visible
+#pragma unroll 4
+  for (int i = 0; i < u.n; ++i) {
+    const float s = p.part_lse[at(i)], w = ex2(s - from);
+    const float *src = p.part_o + at(i) * D + lane * (D / 32);
     sum += w;
+    float y[D / 32];
+    if constexpr (D == 128) *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(src);
+    else *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(src);
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) x[k] = fmaf(w, p.part_o[at * D + 32 * k + lane], x[k]);
+    for (int k = 0; k < D / 32; ++k) x[k] = s == neg_inf() ? x[k] : fmaf(w, y[k], x[k]);
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const int64_t out = (int64_t(u.r.token0) + tok) * p.Hq + u.kv * p.G + row % p.G;
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) {
-    if (p.out_f32) static_cast<float *>(p.o)[out * D + 32 * k + lane] = x[k] * inv;
-    else static_cast<__nv_bfloat16 *>(p.o)[out * D + 32 * k + lane] = __float2bfloat16_rn(x[k] * inv);
+  for (int k = 0; k < D / 32; ++k) x[k] *= inv;
+  const int64_t out = u.out + int64_t(row / p.G) * p.Hq + row % p.G;
+  const int64_t o = out * D + lane * (D / 32);
+  if (p.out_f32) {
+    float *dst = static_cast<float *>(p.o) + o;
+    if constexpr (D == 128) *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+    else *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
+  } else {
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + o);
+#pragma unroll
+    for (int k = 0; k < D / 64; ++k) dst[k] = bf16x2_bits(x[2 * k], x[2 * k + 1]);
   }
   if (lane == 0 && p.lse) p.lse[out] = sum == 0.f ? neg_inf() : m + log2f(sum);
 }
@@ -836,7 +852,6 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   TCRequests req;
   std::memcpy(req.r, sreq.r, sizeof(psd_token_request) * size_t(S.B));
   int64_t total = 0;
-  int most = 0;  // rows of a unit at most
   for (int b = 0; b < S.B; ++b) {
     req.base[b] = int32_t(total);
     const psd_token_request &r = req.r[b];
@@ -845,11 +860,10 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
     total += head * S.Hkv;
     if (total > 0x7fffffffLL)
       return fail(PSD_ERR_UNSUPPORTED, "multi_token_decode: more than 2^31 key tiles in one launch");
-    most = std::max(most, std::min(r.num_new, 2 * p.TH) * S.G);
   }
   req.base[S.B] = int32_t(total);
   p.total = total;
-  const int ctas = int(std::min<int64_t>(total, place.ctas));
+  const int ctas = int(std::min<int64_t>(total, std::min(place.ctas, kMaxCuts + 1)));
   p.part_o = place.part_o;
   p.part_lse = place.part_lse;
   p.sum_o = place.sum_o;
@@ -876,18 +890,38 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   kern<<<ctas, kThreads, L::kSmem, s>>>(tmQ, tmK, tmV, p, req);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode launch: %s", cudaGetErrorString(e));
-  // Is a unit cut?  Bounds fall on c total / ctas.
-  bool cut = false;
-  for (int c = 1, b = 0; c < ctas && !cut; ++c) {
-    const int64_t at = int64_t(c) * total / ctas;
+  // The units that a bound c total / ctas cuts, each named at its first.
+  Cuts cuts;
+  int n_cuts = 0, most = 0;
+  int64_t done = 0;  // end of the last unit named
+  auto bound = [&](int64_t c) { return c * total / ctas; };
+  for (int c = 1, b = 0; c < ctas; ++c) {
+    const int64_t at = bound(c);
+    if (at < done) continue;
     while (req.base[b + 1] <= at) ++b;
-    int64_t rem = (at - req.base[b]) % ((req.base[b + 1] - req.base[b]) / S.Hkv);
-    for (int t = 0; rem > 0; t += 2 * p.TH) rem -= unit_tiles(req.r[b], t, p.TH, L::NK, S.tree != nullptr);
-    cut = rem < 0;
+    const psd_token_request &r = req.r[b];
+    const int64_t head = (req.base[b + 1] - req.base[b]) / S.Hkv;
+    const int kv = int((at - req.base[b]) / head);
+    int64_t first = req.base[b] + kv * head;
+    int tok0 = 0, n = 0;
+    for (;; tok0 += 2 * p.TH, first += n) {
+      n = unit_tiles(r, tok0, p.TH, L::NK, S.tree != nullptr);
+      if (at < first + n) break;
+    }
+    if (at == first) continue;  // between two units
+    done = first + n;
+    Cut &u = cuts.c[n_cuts++];
+    u.out = (int64_t(r.token0) + tok0) * S.Hq + int64_t(kv) * S.G;
+    u.rows = std::min(r.num_new - tok0, 2 * p.TH) * S.G;
+    u.first = c - 1;
+    u.late = bound(c - 1) < first;
+    u.n = 1;
+    while (c - 1 + u.n < ctas && bound(c - 1 + u.n) < done) ++u.n;
+    most = std::max(most, u.rows);
   }
-  if (!cut) return PSD_OK;
+  if (n_cuts == 0) return PSD_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(ctas - 1), unsigned((most + 7) / 8));
+  cfg.gridDim = dim3(unsigned(n_cuts), unsigned((most + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -895,7 +929,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, step_join_kernel<D, L::NK>, p, req, ctas);
+  e = cudaLaunchKernelEx(&cfg, step_join_kernel<D>, p, cuts);
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode join launch: %s", cudaGetErrorString(e));
   return PSD_OK;
 }

@@ -4,10 +4,17 @@
 // and drawing from max(p - q, 0) after a refusal leaves the outcome distributed as p.
 // Acceptance compares u q(d) < p(d): the product of two f32 numbers is exact in 64 bits.
 // The draw wants the least v with C_v > u C: a border decided by sums of up to 2^17
-// numbers, so the sums are taken exactly, in 64-bit fixed point with 58 fraction bits
-// (a probability below 2^-34 loses bits under 2^-58, at most 2^-41 in all over 2^17
-// entries; the sums stay below 2^63 up to a row total of 16).  Integer sums
-// do not depend on their order, so the split over threads cannot change a token.
+// numbers, so the weights are summed as integers, multiples of 2^-46 (the totals stay below
+// 2^63 far past any row's).  Integer sums do not depend on their order, so the split over
+// threads cannot change a token.  A weight is rounded to that unit once: weights from
+// 2^-23 on (1.2e-7) are exact, the error of a row's sum is about 1e-12.
+//
+// The weight of an entry with p > q, in f32 operations: d = p - q rounded, and its error e =
+// (p - d) - q, exact since p >= q >= 0; d's multiples of 2^-23 are the low bits of d + 1
+// (whose unit in the last place is 2^-23), what that leaves, r, is exact too, and the
+// multiples of 2^-46 in r and e are the low bits of their sums with 1.5 * 2^-23.  18
+// instructions an entry; shifting the two significands into place as 64-bit integers took
+// 41 and bounded the kernel (128 requests: 36 us against 29).
 #include <cuda_runtime.h>
 
 #include "context.h"
@@ -28,19 +35,38 @@ struct VerifyParams {
   int B, num_drafts, V;
 };
 
-// A probability in 58-bit fixed point, cut: 0 for NaN and what is not positive, 2^58 from 1 on.
-__device__ __forceinline__ uint64_t fix58(float x) {
-  if (!(x > 0.f)) return 0;
-  const uint32_t bits = __float_as_uint(fminf(x, 1.f));
-  const int e = int(bits >> 23);                                   // 2^(e - 127)
-  const uint64_t m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u);    // 24 bits
-  const int sh = (e ? e : 1) - 127 - 23 + 58;                      // <= 35
-  return sh >= 0 ? m << sh : (sh > -24 ? m >> -sh : 0);
-}
-__device__ __forceinline__ uint64_t weight(float p, float q) {
-  const uint64_t a = fix58(p), b = fix58(q);
-  return a > b ? a - b : 0;
-}
+// Low words of sums of weights: the weight is high * 2^-23 + low * 2^-46.
+struct Acc {
+  uint32_t high = 0, low = 0;  // modulo 2^32, the added constants' bits included
+  __device__ __forceinline__ void level(float d, float e) {
+    constexpr float kOne = 1.f, kSmall = 1.5f * 0x1p-23f;
+    const float t = d + kOne;
+    const float r = d - (t - kOne);
+    high += __float_as_uint(t);
+    low += __float_as_uint(r + kSmall) + __float_as_uint(e + kSmall);
+  }
+  __device__ __forceinline__ void level(float d) {  // e = 0
+    constexpr float kOne = 1.f, kSmall = 1.5f * 0x1p-23f;
+    const float t = d + kOne;
+    high += __float_as_uint(t);
+    low += __float_as_uint(d - (t - kOne) + kSmall);
+  }
+  // max(p - q, 0); p and q are taken as 0 where NaN or negative, as 1 from 1 on
+  __device__ __forceinline__ void add(float p, float q) {
+    p = __saturatef(p);
+    q = __saturatef(q);
+    const float d = p - q, e = (p - d) - q;
+    const bool some = p > q;
+    level(some ? d : 0.f, some ? e : 0.f);
+  }
+  __device__ __forceinline__ void add(float p) { level(__saturatef(p)); }
+  // The sum of n weights added with a q each (two low words) or without: n <= 128.
+  __device__ __forceinline__ uint64_t value(int n, bool with_q) const {
+    const uint32_t h = high - uint32_t(n) * 0x3f800000u;
+    const int32_t l = int32_t(low - uint32_t(with_q ? 2 * n : n) * 0x34400000u);
+    return (uint64_t(h) << 23) + uint64_t(int64_t(l));
+  }
+};
 // floor(u * total): the least v with C_v > u * total is the least with C_v > this.
 __device__ __forceinline__ uint64_t share_of(float u, uint64_t total) {
   if (!(u > 0.f)) return 0;
@@ -87,7 +113,10 @@ struct Row {
   const float *p, *q;  // q NULL: p alone
   int hot;             // a token of weight 0, or -1
   __device__ __forceinline__ uint64_t at(int v) const {
-    return v == hot ? 0 : (q ? weight(__ldg(p + v), __ldg(q + v)) : fix58(__ldg(p + v)));
+    Acc x;
+    if (q) x.add(__ldg(p + v), __ldg(q + v));
+    else x.add(v == hot ? 0.f : __ldg(p + v));
+    return x.value(1, q != nullptr);
   }
 };
 
@@ -97,7 +126,7 @@ struct Row {
 // the CTA that holds the crossing looks only at the block where it lies again.
 // The work is the row's bytes: 8 V with a refusal, 4 V without; 8 CTAs a request put
 // enough loads in flight from one request on.
-__global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const VerifyParams p, int ctas) {
+__global__ void __launch_bounds__(kVerifyThreads, 7) verify_drafts_kernel(const VerifyParams p, int ctas) {
   __shared__ uint64_t sums[kMaxSums], warps[kVerifyWarps], mine;
   __shared__ int first_refused;
   const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
@@ -148,17 +177,19 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
       for (int c = lo; c < hi; c += 256) {
         if (c + 256 <= hi) {
           float pv[8], qv[8];
+          Acc s;
 #pragma unroll
           for (int i = 0; i < 8; ++i) pv[i] = __ldg(row.p + c + 32 * i + lane);
           if (row.q) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) qv[i] = __ldg(row.q + c + 32 * i + lane);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x += weight(pv[i], qv[i]);
+            for (int i = 0; i < 8; ++i) s.add(pv[i], qv[i]);
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x += c + 32 * i + lane == row.hot ? 0 : fix58(pv[i]);
+            for (int i = 0; i < 8; ++i) s.add(row.hot - c - lane == 32 * i ? 0.f : pv[i]);
           }
+          x += s.value(8, row.q != nullptr);
         } else {
           for (int v = c + lane; v < hi; v += 32) x += row.at(v);
         }
@@ -204,15 +235,24 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_drafts_kernel(const Ver
       }
     }
     const int lo = v0 + k0 * step, hi = min(lo + step, v1);
-    for (int c = lo; c < hi; c += 32) {
-      const int v = c + lane;
-      const uint64_t x = warp_scan(v < hi ? row.at(v) : 0);
-      const uint32_t past = __ballot_sync(0xffffffffu, run + x > want);
-      if (past) {
-        if (lane == 0) p.out[R + a] = c + __ffs(past) - 1;
-        break;
+    bool done = false;
+    for (int c = lo; c < hi && !done; c += 256) {
+      uint64_t w[8];  // all on their way before the first is needed
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int v = c + 32 * i + lane;
+        w[i] = v < hi ? row.at(v) : 0;
       }
-      run += __shfl_sync(0xffffffffu, x, 31);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t x = warp_scan(w[i]);
+        const uint32_t past = __ballot_sync(0xffffffffu, run + x > want);
+        if (past && !done) {
+          if (lane == 0) p.out[R + a] = c + 32 * i + __ffs(past) - 1;
+          done = true;
+        }
+        run += __shfl_sync(0xffffffffu, x, 31);
+      }
     }
   }
   if (rank == 0) {
