@@ -24,7 +24,7 @@
 //   TMEM (512 columns): per slot S [128 x NK] f32 with P over it, and O [128 x D] f32.
 //   Shared memory: two row tiles of Q, a ring of K and V half-tiles (K, V, K, V, ...).
 //   Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row = TMEM lane), 8 MMA,
-//   9 loads Q and K, 10 loads V.
+//   9 loads Q and K, 10 loads V, 11 none.
 //
 // Tiles are read by TMA through a 5-D view of the pool, [groups of 8 token slots][KV head]
 // [64-column halves][8 slots][64 columns], whose box of a page's part lands as complete
@@ -58,8 +58,13 @@ namespace {
 constexpr int kRows = 128;       // TMEM lanes of a row tile
 constexpr float kLazy = 8.f;     // log2 units
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
-constexpr int kThreads = 11 * 32;
-constexpr uint32_t kRingBytes = 160 * 1024;
+constexpr int kThreads = 12 * 32;
+// Registers a thread: 168 at launch (64512 of 384 threads); the softmax warps hold a tile's
+// scores and weights and take what the other four (warp 11 only gives) do without:
+// 256 * 208 + 128 * 88 = 64512.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
+constexpr uint32_t kRingBytes = 128 * 1024;
 constexpr int kMaxStages = 20;
 constexpr int kFlush = 16;       // f32 outputs: ops of a slot (64 keys each) O holds at most
 
@@ -73,7 +78,8 @@ struct Lay {
   static constexpr uint32_t kQHalfBytes = kRows * 128;
   static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;   // one row tile
   static constexpr uint32_t kOffQ = kStages * kTileBytes;
-  static constexpr uint32_t kOffLM = kOffQ + 2 * kQBytes;      // slot 1's (m, l) of a unit of one row tile
+  static constexpr uint32_t kOffOut = kOffQ + 2 * kQBytes;     // 32 rows of 128 bytes for each softmax warp
+  static constexpr uint32_t kOffLM = kOffOut + 8 * 32 * 128;       // slot 1's (m, l) of a unit of one row tile
   static constexpr uint32_t kOffBar = kOffLM + kRows * 8;
   static constexpr uint32_t kSmem = kOffBar + 512 + 1024;      // barriers, alignment slack
   static constexpr uint32_t kPCols = NK / 2;                   // 32-bit columns of one P term
@@ -81,7 +87,7 @@ struct Lay {
   static constexpr uint32_t kColS = 2 * D;                     // after the two O
   static_assert(TERMS * kPCols <= kSCols && NK <= int(kSCols), "S region");
   static_assert(kColS + 2 * kSCols <= 512, "TMEM columns");
-  static_assert(kStages >= 5 && kStages <= kMaxStages, "S runs two tiles ahead of PV");
+  static_assert(kStages >= 4 && kStages <= kMaxStages, "S runs two tiles ahead of PV");
   static_assert(kSmem <= 227u * 1024u, "shared memory");
   static_assert(kTileBytes % 1024 == 0, "128-byte-swizzle atoms");
 };
@@ -260,21 +266,16 @@ __device__ __forceinline__ uint64_t l2_normal_policy() {
   return pol;
 }
 
-// The visible keys of one row among the NK from `base` on, one bit each.
-template <int NK>
-__device__ __forceinline__ void visible(int base, int seen, int start, uint64_t tree, bool has_tree,
-                                        uint32_t (&w)[NK / 32]) {
-#pragma unroll
-  for (int k = 0; k < NK / 32; ++k) {
-    const int n = (has_tree ? start : seen) - base - 32 * k;  // keys before this one are visible
-    uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
-    if (has_tree) {
-      const int sh = start - base - 32 * k;  // the tree's bit 0 is key `start`
-      if (sh >= 0 && sh < 32) bits |= uint32_t(tree << sh);
-      else if (sh < 0 && sh > -64) bits |= uint32_t(tree >> -sh);
-    }
-    w[k] = bits;
+// The visible keys of one row among the 32 from `base` on, one bit each.
+__device__ __forceinline__ uint32_t visible(int base, int seen, int start, uint64_t tree, bool has_tree) {
+  const int n = (has_tree ? start : seen) - base;  // keys before this one are visible
+  uint32_t bits = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u;
+  if (has_tree) {
+    const int sh = start - base;                   // the tree's bit 0 is key `start`
+    if (sh >= 0 && sh < 32) bits |= uint32_t(tree << sh);
+    else if (sh < 0 && sh > -64) bits |= uint32_t(tree >> -sh);
   }
+  return bits;
 }
 
 template <int D, int TERMS>
@@ -324,9 +325,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait_all = [&](int b, uint32_t parity) {  // a warp's bounded wait
     return __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u, p.fault, p.wait_limit)) != 0;
   };
+  // (Each role sets its register share inside its own branch: where the branches met again
+  // the compiler would hold every role to the smallest.)
+  if (warp >= kMmaWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   Walk<NK> walk(p, req, lo, hi);
   Unit u;
-
   if (warp == kKWarp || warp == kVWarp) {
     // ----------------------------------------------------------------- loads
     // Half-tile i of the ring: K of key tile i / 2 (even) or V of it (odd).
@@ -457,8 +461,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect()) commit(bar(T_DRAIN));
     __syncwarp();
     mbar_wait(bar(T_DRAIN), 0u, p.fault, p.wait_limit);
+  }
   } else {
     // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    Walk<NK> walk(p, req, lo, hi);
+    Unit u;
     const int slot = warp >> 2, r = tid & 127;       // row of the tile = TMEM lane
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_col = lane_base + L::kColS + slot * L::kSCols;
@@ -492,10 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         fence_after();
         if (warp_live) {
-          uint32_t w[NK];
-#pragma unroll
-          for (int c = 0; c < NK; c += 32) tmem_ld32(s_col + c, w + c);
-          ld_wait();
           bool empty = t < 2;                           // O holds nothing
           if constexpr (TERMS > 1) {
             if (t >= 2 && (t >> 1) % kFlush == 0) {
@@ -523,24 +527,53 @@ __global__ void __launch_bounds__(kThreads, 1)
               flushed = empty = true;
             }
           }
-          float top = neg_inf();
-          if (__any_sync(0xffffffffu, live && clear < base + NK)) {
-            uint32_t bits[NK / 32];
-            visible<NK>(base, seen, start, tree, has_tree, bits);
+          const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
+          // P with the row's running maximum as it stands, and the tile's own maximum beside it: on
+          // most tiles no row grows by more than 2^8 and the maximum is off the critical path.
+          // Otherwise (a unit's first tile among them) O and l are rescaled and P is taken again.
+          uint32_t pk[NK / 2];                          // TERMS == 1: two bf16 each
+          float pf[TERMS > 1 ? NK : 1];
+          float2 sum[2];
+          for (;;) {
+            const float nm = m == neg_inf() ? 0.f : -m;
+            const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
+            float t4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+            sum[0] = sum[1] = make_float2(0.f, 0.f);
+            uint32_t w[2][32];
+            tmem_ld32(s_col, w[0]);
 #pragma unroll
-            for (int c = 0; c < NK; ++c) {
-              const float s = (bits[c >> 5] >> (c & 31)) & 1u ? __uint_as_float(w[c]) : neg_inf();
-              w[c] = __float_as_uint(s);
-              top = fmaxf(top, s);
+            for (int c0 = 0; c0 < NK; c0 += 32) {
+              ld_wait();
+              uint32_t *x = w[(c0 >> 5) & 1];
+              if (c0 + 32 < NK) tmem_ld32(s_col + c0 + 32, w[((c0 >> 5) + 1) & 1]);
+              if (masked) {
+                const uint32_t bits = visible(base + c0, seen, start, tree, has_tree);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1u ? x[c] : 0xff800000u;
+              }
+#pragma unroll
+              for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  t4[y] = fmaxf(t4[y], fmaxf(__uint_as_float(x[c + 2 * y]), __uint_as_float(x[c + 2 * y + 1])));
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) {
+                const float2 z =
+                    __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), qs2, nm2);
+                const float a = ex2(z.x), b = ex2(z.y);
+                sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
+                if constexpr (TERMS == 1) {
+                  pk[(c0 + c) / 2] = bf16x2_bits(a, b);
+                } else {
+                  pf[c0 + c] = a;
+                  pf[c0 + c + 1] = b;
+                }
+              }
             }
-          } else {
-#pragma unroll
-            for (int c = 0; c < NK; ++c) top = fmaxf(top, __uint_as_float(w[c]));
-          }
-          if (!live) top = neg_inf();                  // (a dead row's scores are whatever Q held)
-          top *= qs;                                   // qs > 0
-          const bool grow = top > m + kLazy;
-          if (__any_sync(0xffffffffu, grow)) {
+            float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+            top = live ? top * qs : neg_inf();          // qs > 0; (a dead row's scores are whatever Q held)
+            const bool grow = top > m + kLazy;
+            if (!__any_sync(0xffffffffu, grow)) break;
             // S(t) is complete, so PV(t - 2), issued before it, is too: O may be changed
             const float m_new = grow ? top : m;
             const float alpha = grow ? ex2(m - m_new) : 1.f;
@@ -552,44 +585,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld32(lane_base + D * slot + c, o);
                 ld_wait();
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
                 tmem_st32(lane_base + D * slot + c, o);
               }
             }
             m = m_new;
           }
-          const float nm = m == neg_inf() ? 0.f : -m;
-          float2 sum = make_float2(0.f, 0.f);
+          if constexpr (TERMS == 1) {
 #pragma unroll
-          for (int c0 = 0; c0 < NK; c0 += 64) {
-            uint32_t hi_w[32];
+            for (int c = 0; c < NK / 2; c += 32) tmem_st32(s_col + c, pk + c);
+          } else {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              const float a = ex2(fmaf(__uint_as_float(w[c0 + 2 * c]), qs, nm));
-              const float b = ex2(fmaf(__uint_as_float(w[c0 + 2 * c + 1]), qs, nm));
-              sum = __fadd2_rn(sum, make_float2(a, b));
-              hi_w[c] = bf16x2_bits(a, b);
-              if constexpr (TERMS > 1) {  // what the first term leaves, for the next ones
-                w[c0 + 2 * c] = __float_as_uint(a - bf16_lo(hi_w[c]));
-                w[c0 + 2 * c + 1] = __float_as_uint(b - bf16_hi(hi_w[c]));
+            for (int x = 0; x < TERMS; ++x) {           // each term takes what the ones before left
+#pragma unroll
+              for (int c = 0; c < NK; c += 2) {
+                pk[c / 2] = bf16x2_bits(pf[c], pf[c + 1]);
+                pf[c] -= bf16_lo(pk[c / 2]);
+                pf[c + 1] -= bf16_hi(pk[c / 2]);
               }
-            }
-            tmem_st32(s_col + c0 / 2, hi_w);
-            if constexpr (TERMS > 1) {
-#pragma unroll
-              for (int x = 1; x < TERMS; ++x) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                  const float a = __uint_as_float(w[c0 + 2 * c]), b = __uint_as_float(w[c0 + 2 * c + 1]);
-                  hi_w[c] = bf16x2_bits(a, b);
-                  w[c0 + 2 * c] = __float_as_uint(a - bf16_lo(hi_w[c]));
-                  w[c0 + 2 * c + 1] = __float_as_uint(b - bf16_hi(hi_w[c]));
-                }
-                tmem_st32(s_col + x * L::kPCols + c0 / 2, hi_w);
-              }
+              tmem_st32(s_col + x * L::kPCols, pk);
             }
           }
-          l += sum.x + sum.y;
+          sum[0] = __fadd2_rn(sum[0], sum[1]);
+          l += sum[0].x + sum[0].y;
         }
         // V rows past the request's last token may hold anything, NaN included: the slot whose PV
         // comes first zeroes them, so that P = 0 never meets a NaN.
@@ -621,13 +639,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = u.j0 == 0 && u.j1 == u.n;
       const int row = tile_tok * p.G + r - u.tok0 * p.G;   // row of the unit (p.TH * p.G a tile)
       const int piece = 2 * blockIdx.x + (lo == walk.at - nt ? 0 : 1);  // the CTA's first piece, or its last
-      float *part = p.part_o + (int64_t(piece) * 2 * kRows + row) * D;
       const int64_t out = (int64_t(u.r.token0) + tok) * p.Hq + u.kv * p.G + rg;
+      // Where this row goes, in elements: the output, or a piece's rows in the workspace.
+      const int64_t dst = live ? (whole ? out : int64_t(piece) * 2 * kRows + row) * D : -1;
+      uint8_t *stage = sm + L::kOffOut + warp * (32 * 128);
+      // 128 bytes of each of the warp's rows, from the row's lane to coalesced stores: chunk k of
+      // row lane at (k ^ lane % 8), then 8 lanes a row, 4 rows a store.  (A lane storing its own
+      // row writes 32 lines at once: 10000 cycles a unit, against 2800.)
+      auto put128 = [&](const uint4 (&v)[8], uint8_t *base, int64_t byte, int elem) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = v[k];
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int rr = 4 * k + (lane >> 3);
+          const int64_t to = __shfl_sync(0xffffffffu, dst, rr);
+          const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
+          if (to >= 0) *reinterpret_cast<uint4 *>(base + to * elem + byte + (lane & 7) * 16) = x;
+        }
+        __syncwarp();
+      };
       // What the flushed ops of slot `of` add to column c + k of the row, scaled to 2^m_of.
       const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);
       auto add_flushed = [&](float *x, int c, const float *row_of, float scale) {
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
+        for (int k = 0; k < 64; k += 4) {
           const float4 y = *reinterpret_cast<const float4 *>(row_of + c + k);
           x[k] = fmaf(y.x, scale, x[k]);
           x[k + 1] = fmaf(y.y, scale, x[k + 1]);
@@ -635,24 +671,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           x[k + 3] = fmaf(y.w, scale, x[k + 3]);
         }
       };
-      // One row of O, scaled, to the output or the workspace.
-      auto put32 = [&](const float *x, int c) {
-        if (!whole) {
+      // Columns [c, c + 64) of the rows, scaled.
+      auto put64 = [&](const float (&x)[64], int c) {
+        uint4 v[8];
+        if (whole && TERMS == 1) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4 *>(part + c + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
-        } else if (TERMS > 1) {
-          float *dst = static_cast<float *>(p.o) + out * D + c;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<float4 *>(dst + k) = make_float4(x[k], x[k + 1], x[k + 2], x[k + 3]);
+          for (int k = 0; k < 8; ++k)
+            v[k] = make_uint4(bf16x2_bits(x[8 * k], x[8 * k + 1]), bf16x2_bits(x[8 * k + 2], x[8 * k + 3]),
+                              bf16x2_bits(x[8 * k + 4], x[8 * k + 5]), bf16x2_bits(x[8 * k + 6], x[8 * k + 7]));
+          put128(v, static_cast<uint8_t *>(p.o), int64_t(c) * 2, 2);
         } else {
-          __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(p.o) + out * D + c;
+          uint8_t *base = whole ? static_cast<uint8_t *>(p.o) : reinterpret_cast<uint8_t *>(p.part_o);
 #pragma unroll
-          for (int k = 0; k < 32; k += 8)
-            *reinterpret_cast<uint4 *>(dst + k) =
-                make_uint4(bf16x2_bits(x[k], x[k + 1]), bf16x2_bits(x[k + 2], x[k + 3]), bf16x2_bits(x[k + 4], x[k + 5]),
-                           bf16x2_bits(x[k + 6], x[k + 7]));
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              v[k] = make_uint4(__float_as_uint(x[32 * h + 4 * k]), __float_as_uint(x[32 * h + 4 * k + 1]),
+                                __float_as_uint(x[32 * h + 4 * k + 2]), __float_as_uint(x[32 * h + 4 * k + 3]));
+            put128(v, base, int64_t(c + 32 * h) * 4, 4);
+          }
         }
       };
       auto put_lse = [&](float v) {
@@ -663,15 +700,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp_live && (u.two || slot == 0)) {
           const float inv = l == 0.f ? 0.f : p.v_scale / l;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            float x[32];
-            tmem_ld32(lane_base + D * slot + c, o);
+          for (int c = 0; c < D; c += 64) {
+            float x[64];
+            tmem_ld32(lane_base + D * slot + c, reinterpret_cast<uint32_t *>(x));
+            tmem_ld32(lane_base + D * slot + c + 32, reinterpret_cast<uint32_t *>(x) + 32);
             ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * inv;
+            for (int k = 0; k < 64; ++k) x[k] = l == 0.f ? 0.f : x[k] * inv;
             if (TERMS > 1 && live && flushed && l != 0.f) add_flushed(x, c, sum_row, keep * inv);
-            if (live) put32(x, c);
+            put64(x, c);
           }
           if (live) put_lse(l == 0.f ? neg_inf() : m + log2f(l));
         }
@@ -709,21 +746,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float all = l * w0 + l1 * w1, inv = all == 0.f ? 0.f : p.v_scale / all;
           const float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o0[32], o1[32];
-            float x[32];
-            tmem_ld32(lane_base + c, o0);
-            tmem_ld32(lane_base + D + c, o1);
-            ld_wait();
+          for (int c = 0; c < D; c += 64) {
+            float x[64];
+            tmem_ld32(lane_base + c, reinterpret_cast<uint32_t *>(x));
+            tmem_ld32(lane_base + c + 32, reinterpret_cast<uint32_t *>(x) + 32);
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-              x[k] = (l == 0.f ? 0.f : __uint_as_float(o0[k]) * f0) + (l1 == 0.f ? 0.f : __uint_as_float(o1[k]) * f1);
+            for (int h = 0; h < 64; h += 32) {
+              uint32_t y[32];
+              tmem_ld32(lane_base + D + c + h, y);
+              ld_wait();
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                x[h + k] = (l == 0.f ? 0.f : x[h + k] * f0) + (l1 == 0.f ? 0.f : __uint_as_float(y[k]) * f1);
+            }
             if constexpr (TERMS > 1) {
               // (slot 1 flushed if it had more than kFlush ops: every row, its T / 2 ops)
               if (live && flushed && l != 0.f) add_flushed(x, c, sum_row, keep * f0);
               if (live && (T >> 1) > kFlush && l1 != 0.f) add_flushed(x, c, sum_row + kRows * D, f1);
             }
-            if (live) put32(x, c);
+            put64(x, c);
           }
           if (live) put_lse(all == 0.f ? neg_inf() : top + log2f(all));
         }
