@@ -21,10 +21,11 @@
 // odd key tiles, with an O, maximum and sum each, joined when the unit ends.  The MMA warp
 // issues S(t + 2) right after P V(t): they use the same TMEM columns (P lies over S), and
 // MMAs of one CTA execute in issue order.
+// A tile's P goes in parts of 64 keys, so that PV of the first runs while the second is made.
 //   TMEM (512 columns): per slot S [128 x NK] f32 with P over it, and O [128 x D] f32.
 //   Shared memory: two row tiles of Q, a ring of K and V half-tiles (K, V, K, V, ...).
-//   Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row = TMEM lane), 8 MMA,
-//   9 loads Q and K, 10 loads V, 11 none.
+//   Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row = TMEM lane), 8 MMA (one
+//   thread), 9 loads Q and K, 10 loads V, 11 none.
 //
 // Tiles are read by TMA through a 5-D view of the pool, [groups of 8 token slots][KV head]
 // [64-column halves][8 slots][64 columns], whose box of a page's part lands as complete
@@ -71,6 +72,7 @@ constexpr int kFlush = 16;       // f32 outputs: ops of a slot (64 keys each) O 
 template <int D, int TERMS>
 struct Lay {
   static constexpr int NK = TERMS == 1 ? 128 : 64;             // keys per tile
+  static constexpr int kParts = NK / 64;                       // parts of a tile whose P go separately
   static constexpr int kHalves = D / 64;                       // 64-column halves of a row
   static constexpr uint32_t kGroupBytes = kHalves * 1024;      // 8 slots of one head
   static constexpr uint32_t kTileBytes = NK / 8 * kGroupBytes; // K or V of a tile
@@ -96,8 +98,9 @@ enum {
   T_FULL = 0, T_EMPTY = kMaxStages,  // per half-tile: landed / its MMAs have read it
   T_QFULL = 2 * kMaxStages, T_QFREE, // the unit's Q landed / every S of the unit is done
   T_SFULL,                           // [2] S of the slot's next op is complete
-  T_PFULL = T_SFULL + 2,             // [2] its P is written (4 warps)
-  T_OFULL = T_PFULL + 2,             // every PV of the unit is complete
+  T_PFULL = T_SFULL + 2,             // [part][2] the part's P is written (4 warps)
+  T_HALF = T_PFULL + 4,              // [2] the first part's PV of the slot's op is complete
+  T_OFULL = T_HALF + 2,              // every PV of the unit is complete
   T_OFREE,                           // the unit's O are read out (8 warps)
   T_XREADY, T_XFREE,                 // slot 1's (m, l) written / read (4 warps)
   T_DRAIN, T_SLOT, T_TAIL
@@ -266,6 +269,12 @@ __device__ __forceinline__ uint64_t l2_normal_policy() {
   return pol;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN operands lose, as in fmaxf
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The visible keys of one row among the 32 from `base` on, one bit each.
 __device__ __forceinline__ uint32_t visible(int base, int seen, int start, uint64_t tree, bool has_tree) {
   const int n = (has_tree ? start : seen) - base;  // keys before this one are visible
@@ -306,6 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(T_SFULL + i), 1);
       mbar_init(bar(T_PFULL + i), 4);
+      mbar_init(bar(T_PFULL + 2 + i), 4);
+      mbar_init(bar(T_HALF + i), 1);
     }
     mbar_init(bar(T_OFULL), 1);
     mbar_init(bar(T_OFREE), 8);
@@ -395,8 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tail[is_v] = g;
       if (!is_v) tail[2] = units;
     }
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp && elect()) {
     // ------------------------------------------------------------------- MMAs
+    // One thread.  What stands between a P and its MMAs is on the critical path of both slots
+    // (a warp that voted on each wait and waited for K between P V and S spent 600 cycles an
+    // op there): the tiles of an op are waited for before its P, and S(t + 2) follows
+    // P V(t) without a wait.
     const uint32_t id_s = idesc_bf16(kRows, NK, false);
     const uint32_t id_pv = idesc_bf16(kRows, D, true);
     // Q: 8-row groups 1024 B apart.  K (K-major): 8-token groups kGroupBytes apart, a half 1024 B
@@ -404,62 +419,70 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t qd = desc_sw128(smem_u32(sm + L::kOffQ), 16, 1024);
     const uint64_t kd = desc_sw128(smem_u32(sm), 16, L::kGroupBytes);
     const uint64_t vd = desc_sw128(smem_u32(sm), 1024, L::kGroupBytes);
+    auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, p.fault, p.wait_limit); };
     int g = 0, units = 0;
     uint32_t ops[2] = {0, 0};  // ops of each slot whose P was awaited
     bool ok = true;
     while (ok && walk.next(u)) {
       const int nt = u.j1 - u.j0, T = u.two ? 2 * nt : nt;
-      ok = wait_all(T_QFULL, uint32_t(units));
+      auto half_tile = [&](int t) { return 2 * (g + (u.two ? t >> 1 : t)); };  // K of op t; V is the next
+      auto k_ready = [&](int t) {
+        const int i = half_tile(t);
+        return (u.two && (t & 1)) || wait(T_FULL + i % NS, uint32_t(i / NS));
+      };
+      auto issue_s = [&](int t) {
+        const int slot = t & 1, st = half_tile(t) % NS;
+        const uint64_t a = qd + ((u.two && slot ? L::kQBytes : 0u) >> 4);
+        const uint64_t b = kd + ((st * L::kTileBytes) >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss(tmem + L::kColS + slot * L::kSCols, a + (((k >> 2) * L::kQHalfBytes + (k & 3) * 32) >> 4),
+                 b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_s, k > 0);
+        commit(bar(T_SFULL + slot));
+        if (!u.two || slot) commit(bar(T_EMPTY + st));
+        if (t == T - 1) commit(bar(T_QFREE));
+      };
+      ok = wait(T_QFULL, uint32_t(units)) && k_ready(0);
       if (!ok) break;
       fence_after();
-      auto issue_s = [&](int t) -> bool {
-        const int slot = t & 1, i = 2 * (g + (u.two ? t >> 1 : t)), st = i % NS;
-        if (!(u.two && slot) && !wait_all(T_FULL + st, uint32_t(i / NS))) return false;
+      issue_s(0);
+      if (T > 1) {
+        if (!(ok = k_ready(1))) break;
         fence_after();
-        if (elect()) {
-          const uint64_t a = qd + ((u.two && slot ? L::kQBytes : 0u) >> 4);
-          const uint64_t b = kd + ((st * L::kTileBytes) >> 4);
+        issue_s(1);
+      }
+      for (int t = 0; t < T; ++t) {
+        const int slot = t & 1, i = half_tile(t) + 1, st = i % NS;
+        // K of op t + 2 has a stage that op t or an earlier one freed: no P stands before it
+        ok = ((u.two && slot) || wait(T_FULL + st, uint32_t(i / NS))) && (t + 2 >= T || k_ready(t + 2)) &&
+             (t > 0 || units == 0 || wait(T_OFREE, uint32_t(units - 1)));
+        if (!ok) break;
+        const uint32_t d = tmem + D * slot, a = tmem + L::kColS + slot * L::kSCols;
+        const uint64_t b = vd + ((st * L::kTileBytes) >> 4);
+        const bool fresh = TERMS > 1 ? (t >> 1) % kFlush == 0 : t < 2;  // O starts at zero
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + L::kColS + slot * L::kSCols, a + (((k >> 2) * L::kQHalfBytes + (k & 3) * 32) >> 4),
-                   b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_s, k > 0);
-          commit(bar(T_SFULL + slot));
-          if (!u.two || slot) commit(bar(T_EMPTY + st));
-          if (t == T - 1) commit(bar(T_QFREE));
-        }
-        __syncwarp();
-        return true;
-      };
-      auto issue_pv = [&](int t) -> bool {
-        const int slot = t & 1, i = 2 * (g + (u.two ? t >> 1 : t)) + 1, st = i % NS;
-        if (!(u.two && slot) && !wait_all(T_FULL + st, uint32_t(i / NS))) return false;
-        if (t == 0 && units > 0 && !wait_all(T_OFREE, uint32_t(units - 1))) return false;
-        if (!wait_all(T_PFULL + slot, ops[slot])) return false;
-        ++ops[slot];
-        fence_after();
-        if (elect()) {
-          const uint32_t d = tmem + D * slot, a = tmem + L::kColS + slot * L::kSCols;
-          const uint64_t b = vd + ((st * L::kTileBytes) >> 4);
-          const bool fresh = TERMS > 1 ? (t >> 1) % kFlush == 0 : t < 2;  // O starts at zero
+        for (int part = 0; part < L::kParts; ++part) {
+          ok = wait(T_PFULL + 2 * part + slot, ops[slot]);
+          if (!ok) break;
+          fence_after();
 #pragma unroll
-          for (int k = 0; k < NK / 16; ++k)
+          for (int k = 4 * part; k < 4 * part + 4; ++k)
 #pragma unroll
             for (int x = 0; x < TERMS; ++x)
               mma_ts(d, a + x * L::kPCols + 8 * k, b + ((k * 2 * L::kGroupBytes) >> 4), id_pv, !fresh || k > 0 || x > 0);
-          if (!u.two || slot) commit(bar(T_EMPTY + st));
-          if (t == T - 1) commit(bar(T_OFULL));
+          if (part == 0 && L::kParts > 1) commit(bar(T_HALF + slot));
         }
-        __syncwarp();
-        return true;
-      };
-      ok = issue_s(0) && (T < 2 || issue_s(1));
-      for (int t = 0; t < T && ok; ++t) ok = issue_pv(t) && (t + 2 >= T || issue_s(t + 2));
+        if (!ok) break;
+        ++ops[slot];
+        if (!u.two || slot) commit(bar(T_EMPTY + st));
+        if (t == T - 1) commit(bar(T_OFULL));
+        if (t + 2 < T) issue_s(t + 2);
+      }
       g += nt;
       ++units;
     }
     // every MMA issued has completed before TMEM is released
-    if (elect()) commit(bar(T_DRAIN));
-    __syncwarp();
+    commit(bar(T_DRAIN));
     mbar_wait(bar(T_DRAIN), 0u, p.fault, p.wait_limit);
   }
   } else {
@@ -499,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_all(T_SFULL + slot, ops);
         if (!ok) break;
         fence_after();
+        bool empty = t < 2;                             // O holds nothing
         if (warp_live) {
-          bool empty = t < 2;                           // O holds nothing
           if constexpr (TERMS > 1) {
             if (t >= 2 && (t >> 1) % kFlush == 0) {
               // S(t) is complete, so PV(t - 2), issued before it, is too
@@ -527,90 +550,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               flushed = empty = true;
             }
           }
-          const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
-          // P with the row's running maximum as it stands, and the tile's own maximum beside it: on
-          // most tiles no row grows by more than 2^8 and the maximum is off the critical path.
-          // Otherwise (a unit's first tile among them) O and l are rescaled and P is taken again.
-          uint32_t pk[NK / 2];                          // TERMS == 1: two bf16 each
-          float pf[TERMS > 1 ? NK : 1];
-          float2 sum[2];
-          for (;;) {
-            const float nm = m == neg_inf() ? 0.f : -m;
-            const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
-            float t4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-            sum[0] = sum[1] = make_float2(0.f, 0.f);
-            uint32_t w[2][32];
-            tmem_ld32(s_col, w[0]);
-#pragma unroll
-            for (int c0 = 0; c0 < NK; c0 += 32) {
-              ld_wait();
-              uint32_t *x = w[(c0 >> 5) & 1];
-              if (c0 + 32 < NK) tmem_ld32(s_col + c0 + 32, w[((c0 >> 5) + 1) & 1]);
-              if (masked) {
-                const uint32_t bits = visible(base + c0, seen, start, tree, has_tree);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1u ? x[c] : 0xff800000u;
-              }
-#pragma unroll
-              for (int c = 0; c < 32; c += 8)
-#pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  t4[y] = fmaxf(t4[y], fmaxf(__uint_as_float(x[c + 2 * y]), __uint_as_float(x[c + 2 * y + 1])));
-#pragma unroll
-              for (int c = 0; c < 32; c += 2) {
-                const float2 z =
-                    __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), qs2, nm2);
-                const float a = ex2(z.x), b = ex2(z.y);
-                sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
-                if constexpr (TERMS == 1) {
-                  pk[(c0 + c) / 2] = bf16x2_bits(a, b);
-                } else {
-                  pf[c0 + c] = a;
-                  pf[c0 + c + 1] = b;
-                }
-              }
-            }
-            float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-            top = live ? top * qs : neg_inf();          // qs > 0; (a dead row's scores are whatever Q held)
-            const bool grow = top > m + kLazy;
-            if (!__any_sync(0xffffffffu, grow)) break;
-            // S(t) is complete, so PV(t - 2), issued before it, is too: O may be changed
-            const float m_new = grow ? top : m;
-            const float alpha = grow ? ex2(m - m_new) : 1.f;
-            l *= alpha;
-            if (!empty) {
-#pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                uint32_t o[32];
-                tmem_ld32(lane_base + D * slot + c, o);
-                ld_wait();
-#pragma unroll
-                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
-                tmem_st32(lane_base + D * slot + c, o);
-              }
-            }
-            m = m_new;
-          }
-          if constexpr (TERMS == 1) {
-#pragma unroll
-            for (int c = 0; c < NK / 2; c += 32) tmem_st32(s_col + c, pk + c);
-          } else {
-#pragma unroll
-            for (int x = 0; x < TERMS; ++x) {           // each term takes what the ones before left
-#pragma unroll
-              for (int c = 0; c < NK; c += 2) {
-                pk[c / 2] = bf16x2_bits(pf[c], pf[c + 1]);
-                pf[c] -= bf16_lo(pk[c / 2]);
-                pf[c + 1] -= bf16_hi(pk[c / 2]);
-              }
-              tmem_st32(s_col + x * L::kPCols, pk);
-            }
-          }
-          sum[0] = __fadd2_rn(sum[0], sum[1]);
-          l += sum[0].x + sum[0].y;
         }
         // V rows past the request's last token may hold anything, NaN included: the slot whose PV
-        // comes first zeroes them, so that P = 0 never meets a NaN.
+        // comes first zeroes them before it gives its P, so that P = 0 never meets a NaN.
         const int left = u.r.kv_len - base;
         if (left < NK && !(u.two && slot)) {
           const int i = 2 * (g + (u.two ? t >> 1 : t)) + 1, st = i % NS;
@@ -625,10 +567,103 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async();
         }
-        st_wait();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(T_PFULL + slot));
+        const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
+        auto give_part = [&](auto which) -> bool {
+          constexpr int part = decltype(which)::value;
+          if (warp_live) {
+            uint32_t x[64];
+            tmem_ld32(s_col + 64 * part, x);
+            tmem_ld32(s_col + 64 * part + 32, x + 32);
+            ld_wait();
+            if (masked) {
+#pragma unroll
+              for (int h = 0; h < 64; h += 32) {
+                const uint32_t bits = visible(base + 64 * part + h, seen, start, tree, has_tree);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) x[h + c] = (bits >> c) & 1u ? x[h + c] : 0xff800000u;
+              }
+            }
+            // P with the row's running maximum as it stands, and the part's own maximum beside it: on
+            // most tiles no row grows by more than 2^8 and the maximum is off the critical path.
+            // Otherwise (a unit's first tile among them) O and l are rescaled and P is taken again.
+            uint32_t pk[32];                            // two bf16 each
+            [[maybe_unused]] float pf[TERMS > 1 ? 64 : 1];
+            float2 sum[2];
+            for (;;) {
+              const float nm = m == neg_inf() ? 0.f : -m;
+              const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
+              float t4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+              sum[0] = sum[1] = make_float2(0.f, 0.f);
+#pragma unroll
+              for (int c = 0; c < 64; c += 8)
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  t4[y] = max3(t4[y], __uint_as_float(x[c + 2 * y]), __uint_as_float(x[c + 2 * y + 1]));
+#pragma unroll
+              for (int c = 0; c < 64; c += 2) {
+                const float2 z =
+                    __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), qs2, nm2);
+                const float a = ex2(z.x), b = ex2(z.y);
+                sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
+                if constexpr (TERMS == 1) {
+                  pk[c / 2] = bf16x2_bits(a, b);
+                } else {
+                  pf[c] = a;
+                  pf[c + 1] = b;
+                }
+              }
+              float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+              top = live ? top * qs : neg_inf();        // qs > 0; (a dead row's scores are whatever Q held)
+              const bool grow = top > m + kLazy;
+              if (!__any_sync(0xffffffffu, grow)) break;
+              // O may be changed: S(t) is complete, so PV(t - 2), issued before it, is too; the first
+              // part's PV of this op is waited for
+              if (part > 0) {
+                if (!wait_all(T_HALF + slot, ops)) return false;
+                fence_after();
+              }
+              const float m_new = grow ? top : m;
+              const float alpha = grow ? ex2(m - m_new) : 1.f;
+              l *= alpha;
+              if (part > 0 || !empty) {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(lane_base + D * slot + c, o);
+                  ld_wait();
+#pragma unroll
+                  for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
+                  tmem_st32(lane_base + D * slot + c, o);
+                }
+              }
+              m = m_new;
+            }
+            if constexpr (TERMS == 1) {
+              tmem_st32(s_col + 32 * part, pk);
+            } else {
+#pragma unroll
+              for (int y = 0; y < TERMS; ++y) {         // each term takes what the ones before left
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) {
+                  pk[c / 2] = bf16x2_bits(pf[c], pf[c + 1]);
+                  pf[c] -= bf16_lo(pk[c / 2]);
+                  pf[c + 1] -= bf16_hi(pk[c / 2]);
+                }
+                tmem_st32(s_col + y * L::kPCols, pk);
+              }
+            }
+            sum[0] = __fadd2_rn(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
+          }
+          st_wait();
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(T_PFULL + 2 * part + slot));
+          return true;
+        };
+        ok = give_part(std::integral_constant<int, 0>{});
+        if constexpr (L::kParts > 1) ok = ok && give_part(std::integral_constant<int, 1>{});
+        if (!ok) break;
       }
       if (!ok) break;
 
@@ -776,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++units;
     }
   }
+  __syncwarp();
   st_wait();
   fence_before();
   __syncthreads();
