@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t vd = desc_sw128(smem_u32(sm), 1024, L::kGroupBytes);
     auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, p.fault, p.wait_limit); };
     int g = 0, units = 0;
-    uint32_t ops[2] = {0, 0};  // ops of each slot whose P was awaited
+    uint32_t ops = 0;  // bit `slot`: parity of the slot's ops so far
     bool ok = true;
     while (ok && walk.next(u)) {
       const int nt = u.j1 - u.j0, T = u.two ? 2 * nt : nt;
@@ -462,18 +462,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool fresh = TERMS > 1 ? (t >> 1) % kFlush == 0 : t < 2;  // O starts at zero
 #pragma unroll
         for (int part = 0; part < L::kParts; ++part) {
-          ok = wait(T_PFULL + 2 * part + slot, ops[slot]);
+          ok = wait(T_PFULL + 2 * part + slot, ops >> slot);
           if (!ok) break;
           fence_after();
+          const uint32_t ap = a + 32 * part;
+          const uint64_t bp = b + ((part * 8 * L::kGroupBytes) >> 4);
 #pragma unroll
-          for (int k = 4 * part; k < 4 * part + 4; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int x = 0; x < TERMS; ++x)
-              mma_ts(d, a + x * L::kPCols + 8 * k, b + ((k * 2 * L::kGroupBytes) >> 4), id_pv, !fresh || k > 0 || x > 0);
+              mma_ts(d, ap + x * L::kPCols + 8 * k, bp + ((k * 2 * L::kGroupBytes) >> 4), id_pv,
+                     !fresh || part > 0 || k > 0 || x > 0);
           if (part == 0 && L::kParts > 1) commit(bar(T_HALF + slot));
         }
         if (!ok) break;
-        ++ops[slot];
+        ops ^= 1u << slot;
         if (!u.two || slot) commit(bar(T_EMPTY + st));
         if (t == T - 1) commit(bar(T_OFULL));
         if (t + 2 < T) issue_s(t + 2);
@@ -568,6 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async();
         }
         const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
+        // (one copy of the code for both parts: unrolled, the loop outgrew the instruction caches)
         auto give_part = [&](auto which) -> bool {
           constexpr int part = decltype(which)::value;
           if (warp_live) {
