@@ -120,7 +120,7 @@ struct TCParams {
   int64_t total;    // key tiles of the launch
   int B, Hq, Hkv, G, TH, page_size, sub, out_f32;
   float q_scale, v_scale;
-  long long wait_limit;
+  uint32_t wait_limit;
   int withhold_from;  // testing aid: no loads for a unit's key tiles from this index on
 };
 // Requests with new tokens, and the number of key tiles before each (per-launch prefix).
@@ -275,6 +275,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN opera
   return d;
 }
 
+// Waits for phase `parity` of the barrier, at most `limit` cycles.  The kernel's waits are many
+// and inlined, so that they leave the fault word to the end of their role.
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint32_t limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint32_t t0 = uint32_t(clock());
+  while (!mbar_try_wait(bar, parity))
+    if (uint32_t(clock()) - t0 > limit) return false;
+  return true;
+}
+
 // The visible keys of one row among the 32 from `base` on, one bit each.
 __device__ __forceinline__ uint32_t visible(int base, int seen, int start, uint64_t tree, bool has_tree) {
   const int n = (has_tree ? start : seen) - base;  // keys before this one are visible
@@ -334,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_after();
   const uint32_t tmem = *tslot;
   auto wait_all = [&](int b, uint32_t parity) {  // a warp's bounded wait
-    return __all_sync(0xffffffffu, mbar_wait(bar(b), parity & 1u, p.fault, p.wait_limit)) != 0;
+    return __all_sync(0xffffffffu, wait_bounded(bar(b), parity & 1u, p.wait_limit)) != 0;
   };
   // (Each role sets its register share inside its own branch: where the branches met again
   // the compiler would hold every role to the smallest.)
@@ -402,6 +412,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         id = id_next;
       }
     }
+    if (!ok && lane == 0) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
     if (lane == 0) {
       tail[is_v] = g;
       if (!is_v) tail[2] = units;
@@ -419,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t qd = desc_sw128(smem_u32(sm + L::kOffQ), 16, 1024);
     const uint64_t kd = desc_sw128(smem_u32(sm), 16, L::kGroupBytes);
     const uint64_t vd = desc_sw128(smem_u32(sm), 1024, L::kGroupBytes);
-    auto wait = [&](int b, uint32_t parity) { return mbar_wait(bar(b), parity & 1u, p.fault, p.wait_limit); };
+    auto wait = [&](int b, uint32_t parity) { return wait_bounded(bar(b), parity & 1u, p.wait_limit); };
     int g = 0, units = 0;
     uint32_t ops = 0;  // bit `slot`: parity of the slot's ops so far
     bool ok = true;
@@ -486,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // every MMA issued has completed before TMEM is released
     commit(bar(T_DRAIN));
-    mbar_wait(bar(T_DRAIN), 0u, p.fault, p.wait_limit);
+    if (!wait(T_DRAIN, 0u) || !ok) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
   }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -814,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       g += nt;
       ++units;
     }
+    if (!ok && lane == 0) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
   }
   __syncwarp();
   st_wait();
@@ -928,7 +940,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   p.out_f32 = S.out_f32;
   p.q_scale = S.q_scale;
   p.v_scale = S.v_scale;
-  p.wait_limit = dev.test_wait_limit > 0 ? dev.test_wait_limit : kWaitLimitCycles;
+  p.wait_limit = uint32_t(dev.test_wait_limit > 0 ? dev.test_wait_limit : kWaitLimitCycles);
   p.withhold_from = dev.test_withhold_from >= 0 ? dev.test_withhold_from : 0x7fffffff;
   TCRequests req;
   std::memcpy(req.r, sreq.r, sizeof(psd_token_request) * size_t(S.B));
