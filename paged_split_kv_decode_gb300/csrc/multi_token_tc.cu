@@ -32,6 +32,9 @@
 // 128-byte-swizzle atoms: one copy carries a whole head row (both halves at D = 128) of up
 // to 128 slots of a page.  Page positions past the request's pages load as zeros.
 //
+// fp8 pools: the copies bring codes (plain rows) into a ring of their own, and four more warps
+// (12-15) turn them into bf16 tiles of 64 keys in the layout above, half-tile by half-tile.
+//
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
 // terms of NK keys need 3 NK / 2 columns, which is why f32 outputs take tiles of 64 keys.
@@ -59,44 +62,50 @@ namespace {
 constexpr int kRows = 128;       // TMEM lanes of a row tile
 constexpr float kLazy = 8.f;     // log2 units
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
-constexpr int kThreads = 12 * 32;
-// Registers a thread: 168 at launch (64512 of 384 threads); the softmax warps hold a tile's
-// scores and weights and take what the other four (warp 11 only gives) do without:
-// 256 * 208 + 128 * 88 = 64512.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * 168, "registers of the launch");
+constexpr int kConvertWarp = 12, kConvertWarps = 4;  // fp8 pools only
 constexpr uint32_t kRingBytes = 128 * 1024;
-constexpr int kMaxStages = 20;
+constexpr int kMaxStages = 16;
 constexpr int kFlush = 16;       // f32 outputs: ops of a slot (64 keys each) O holds at most
 
-template <int D, int TERMS>
+template <int D, int TERMS, bool FP8>
 struct Lay {
-  static constexpr int NK = TERMS == 1 ? 128 : 64;             // keys per tile
+  static constexpr int NK = TERMS == 1 && !FP8 ? 128 : 64;     // keys per tile
   static constexpr int kParts = NK / 64;                       // parts of a tile whose P go separately
   static constexpr int kHalves = D / 64;                       // 64-column halves of a row
   static constexpr uint32_t kGroupBytes = kHalves * 1024;      // 8 slots of one head
   static constexpr uint32_t kTileBytes = NK / 8 * kGroupBytes; // K or V of a tile
-  static constexpr int kStages = int(kRingBytes / kTileBytes); // half-tiles in the ring
+  static constexpr uint32_t kRawBytes = NK * D;                // its fp8 codes
+  // half-tiles in the ring; with fp8 pools it shares its space with a ring of codes
+  static constexpr int kStages = int((FP8 ? kRingBytes / 2 : kRingBytes) / kTileBytes);
+  static constexpr int kRaw = FP8 ? int(kRingBytes / 2 / kRawBytes) : 0;
+  static constexpr uint32_t kOffRaw = kStages * kTileBytes;
   static constexpr uint32_t kQHalfBytes = kRows * 128;
   static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;   // one row tile
-  static constexpr uint32_t kOffQ = kStages * kTileBytes;
+  static constexpr uint32_t kOffQ = kRingBytes;
   static constexpr uint32_t kOffOut = kOffQ + 2 * kQBytes;     // 32 rows of 128 bytes for each softmax warp
-  static constexpr uint32_t kOffLM = kOffOut + 8 * 32 * 128;       // slot 1's (m, l) of a unit of one row tile
+  static constexpr uint32_t kOffLM = kOffOut + 8 * 32 * 128;   // slot 1's (m, l) of a unit of one row tile
   static constexpr uint32_t kOffBar = kOffLM + kRows * 8;
-  static constexpr uint32_t kSmem = kOffBar + 512 + 1024;      // barriers, alignment slack
+  static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;     // barriers, alignment slack
   static constexpr uint32_t kPCols = NK / 2;                   // 32-bit columns of one P term
   static constexpr uint32_t kSCols = TERMS == 1 ? NK : 96;     // a slot's S, or its P terms if they are wider
   static constexpr uint32_t kColS = 2 * D;                     // after the two O
+  static constexpr int kThreads = FP8 ? 16 * 32 : 12 * 32;
+  // Registers a thread: 168 at launch of 384 threads, 128 of 512; the softmax warps hold a
+  // part's scores and weights and take what the others (warp 11 only gives) do without.
+  static constexpr int kLaunchRegs = FP8 ? 128 : 168;
+  static constexpr int kSoftmaxRegs = FP8 ? 176 : 208, kOtherRegs = FP8 ? 80 : 88;
+  static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "registers of the launch");
   static_assert(TERMS * kPCols <= kSCols && NK <= int(kSCols), "S region");
   static_assert(kColS + 2 * kSCols <= 512, "TMEM columns");
-  static_assert(kStages >= 4 && kStages <= kMaxStages, "S runs two tiles ahead of PV");
+  static_assert(kStages >= 4 && kStages <= kMaxStages && kRaw <= kMaxStages, "S runs two tiles ahead of PV");
   static_assert(kSmem <= 227u * 1024u, "shared memory");
   static_assert(kTileBytes % 1024 == 0, "128-byte-swizzle atoms");
 };
 
 enum {
-  T_FULL = 0, T_EMPTY = kMaxStages,  // per half-tile: landed / its MMAs have read it
-  T_QFULL = 2 * kMaxStages, T_QFREE, // the unit's Q landed / every S of the unit is done
+  T_FULL = 0, T_EMPTY = kMaxStages,  // per half-tile: landed (or converted) / its MMAs have read it
+  T_RFULL = 2 * kMaxStages, T_REMPTY = 3 * kMaxStages,  // per half-tile of codes: landed / converted
+  T_QFULL = 4 * kMaxStages, T_QFREE, // the unit's Q landed / every S of the unit is done
   T_SFULL,                           // [2] S of the slot's next op is complete
   T_PFULL = T_SFULL + 2,             // [part][2] the part's P is written (4 warps)
   T_HALF = T_PFULL + 4,              // [2] the first part's PV of the slot's op is complete
@@ -105,7 +114,7 @@ enum {
   T_XREADY, T_XFREE,                 // slot 1's (m, l) written / read (4 warps)
   T_DRAIN, T_SLOT, T_TAIL
 };
-static_assert(T_TAIL * 8 + 12 <= 512, "barrier area");
+static_assert(T_TAIL * 8 + 12 <= 1024, "barrier area");
 
 struct TCParams {
   const int32_t *page_indices;
@@ -263,6 +272,14 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(bar), "l"(policy)
       : "memory");
 }
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar,
+                                            uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
+      : "memory");
+}
 __device__ __forceinline__ uint64_t l2_normal_policy() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
@@ -297,12 +314,15 @@ __device__ __forceinline__ uint32_t visible(int base, int seen, int start, uint6
   return bits;
 }
 
-template <int D, int TERMS>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, int TERMS, bool FP8>
+__global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     step_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TCParams p, const __grid_constant__ TCRequests req) {
-  using L = Lay<D, TERMS>;
+  using L = Lay<D, TERMS, FP8>;
   constexpr int NK = L::NK, NS = L::kStages;
+  // the ring that the copies fill
+  constexpr int NC = FP8 ? L::kRaw : NS, kLanded = FP8 ? T_RFULL : T_FULL, kFreed = FP8 ? T_REMPTY : T_EMPTY;
+  constexpr uint32_t kCopied = FP8 ? L::kRawBytes : L::kTileBytes;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   dependents_may_launch();  // the joining kernel waits for this grid on its own
   uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -317,8 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(bar(T_FULL + i), 1);
+      mbar_init(bar(T_FULL + i), FP8 ? kConvertWarps : 1);
       mbar_init(bar(T_EMPTY + i), 1);
+    }
+    for (int i = 0; i < L::kRaw; ++i) {
+      mbar_init(bar(T_RFULL + i), 1);
+      mbar_init(bar(T_REMPTY + i), kConvertWarps);
     }
     mbar_init(bar(T_QFULL), 1);
     mbar_init(bar(T_QFREE), 1);
@@ -349,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (Each role sets its register share inside its own branch: where the branches met again
   // the compiler would hold every role to the smallest.)
   if (warp >= kMmaWarp) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
   Walk<NK> walk(p, req, lo, hi);
   Unit u;
   if (warp == kKWarp || warp == kVWarp) {
@@ -359,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap *map = is_v ? &tmV : &tmK;
     const uint64_t pol = l2_normal_policy();
     const int n_copies = NK / p.sub;          // a lane each; p.sub tokens of one page
-    const uint32_t copy_bytes = uint32_t(p.sub / 8) * L::kGroupBytes;
+    const uint32_t copy_bytes = FP8 ? uint32_t(p.sub * D) : uint32_t(p.sub / 8) * L::kGroupBytes;
     const int P = p.page_size;
     int g = 0, units = 0;                     // key tiles and units so far
     bool ok = true, withheld = false;
@@ -391,22 +415,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         const int id_next = page_id(j + 1);
-        const int i = 2 * g + (is_v ? 1 : 0), st = i % NS;
-        if (i >= NS && !wait_all(T_EMPTY + st, uint32_t(i / NS - 1))) {
+        const int i = 2 * g + (is_v ? 1 : 0), st = i % NC;
+        if (i >= NC && !wait_all(kFreed + st, uint32_t(i / NC - 1))) {
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar(T_FULL + st), L::kTileBytes);
+        if (lane == 0) mbar_arrive_expect_tx(bar(kLanded + st), kCopied);
         __syncwarp();
         if (lane < n_copies) {
           const int tok = j * NK + lane * p.sub, pos = tok / P;
-          int group = -64;  // wholly outside the view: zeros
-          if (pos < n_pages) {
-            if (id < 0 || int64_t(id) >= p.num_pages) raise_fault(p.fault, PSD_FAULT_PAGE_ID);
-            else group = int((int64_t(id) * P + (tok - pos * P)) >> 3);
-          }
-          tma_load_5d(smem_u32(sm + st * L::kTileBytes + lane * copy_bytes), map, 0, 0, 0, u.kv, group, bar(T_FULL + st),
-                      pol);
+          const bool there = pos < n_pages && id >= 0 && int64_t(id) < p.num_pages;
+          if (pos < n_pages && !there) raise_fault(p.fault, PSD_FAULT_PAGE_ID);
+          // the first token slot; not there: wholly outside the view, which reads as zeros
+          const int64_t first = there ? int64_t(id) * P + (tok - pos * P) : -1024;
+          if constexpr (FP8)
+            tma_load_3d(smem_u32(sm + L::kOffRaw + st * kCopied + lane * copy_bytes), map, 0, u.kv, int(first),
+                        bar(kLanded + st), pol);
+          else
+            tma_load_5d(smem_u32(sm + st * kCopied + lane * copy_bytes), map, 0, 0, 0, u.kv, int(first / 8),
+                        bar(kLanded + st), pol);
         }
         __syncwarp();
         id = id_next;
@@ -417,6 +444,47 @@ __global__ void __launch_bounds__(kThreads, 1)
       tail[is_v] = g;
       if (!is_v) tail[2] = units;
     }
+  } else if (FP8 && warp >= kConvertWarp) {
+    // ------------------------------------------------------ fp8 codes to bf16
+    // Half-tile by half-tile in the order of the ring: 16 codes a thread and step, exact
+    // (e4m3 to f16 to f32 to bf16; the scales are in the scores' and the output's factors), into
+    // the swizzled layout the MMAs read.  V rows past the request's last token become zeros.
+    const int th = tid - 32 * kConvertWarp;
+    int g = 0;
+    bool ok = true;
+    while (ok && walk.next(u)) {
+      for (int j = u.j0; j < u.j1 && ok; ++j, ++g)
+        for (int v = 0; v < 2; ++v) {
+          const int i = 2 * g + v, st = i % NS, rs = i % NC;
+          ok = wait_all(T_RFULL + rs, uint32_t(i / NC)) && (i < NS || wait_all(T_EMPTY + st, uint32_t(i / NS - 1)));
+          if (!ok) break;
+          const uint8_t *src = sm + L::kOffRaw + rs * L::kRawBytes;
+          uint8_t *dst = sm + st * L::kTileBytes;
+          const int left = v ? u.r.kv_len - j * NK : NK;
+#pragma unroll
+          for (int c = th; c < NK * D / 16; c += 32 * kConvertWarps) {
+            const int tk = c / (D / 16), col8 = 2 * (c % (D / 16)), h = col8 >> 3, k = col8 & 7;
+            const uint4 w = *reinterpret_cast<const uint4 *>(src + c * 16);
+            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+            uint32_t out[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const float2 f = e4m3x2_to_float2(in[y >> 1] >> (16 * (y & 1)));
+              out[y] = tk < left ? bf16x2_bits(f.x, f.y) : 0u;
+            }
+            uint8_t *row = dst + (tk >> 3) * L::kGroupBytes + h * 1024 + (tk & 7) * 128;
+            *reinterpret_cast<uint4 *>(row + ((k ^ (tk & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+            *reinterpret_cast<uint4 *>(row + (((k + 1) ^ (tk & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(bar(T_FULL + st));
+            mbar_arrive(bar(T_REMPTY + rs));
+          }
+        }
+    }
+    if (!ok && lane == 0) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
   } else if (warp == kMmaWarp && elect()) {
     // ------------------------------------------------------------------- MMAs
     // One thread.  What stands between a P and its MMAs is on the critical path of both slots
@@ -501,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     // ---------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
     Walk<NK> walk(p, req, lo, hi);
     Unit u;
     const int slot = warp >> 2, r = tid & 127;       // row of the tile = TMEM lane
@@ -568,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // V rows past the request's last token may hold anything, NaN included: the slot whose PV
         // comes first zeroes them before it gives its P, so that P = 0 never meets a NaN.
         const int left = u.r.kv_len - base;
-        if (left < NK && !(u.two && slot)) {
+        if (!FP8 && left < NK && !(u.two && slot)) {
           const int i = 2 * (g + (u.two ? t >> 1 : t)) + 1, st = i % NS;
           ok = wait_all(T_FULL + st, uint32_t(i / NS));
           if (!ok) break;
@@ -834,14 +902,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kKWarp) {
     // No copy may be in flight when the CTA exits, after a wait that ran out either: the last
     // half-tile issued into each stage, by either load warp, and the last Q.
-    if (lane < NS) {
+    if (lane < NC) {
       int last = -1;
       for (int v = 0; v < 2; ++v) {
         const int top = 2 * (tail[v] - 1) + v;
-        for (int i = top; i > last && i > top - 2 * NS; i -= 2)
-          if (i % NS == lane) last = i;
+        for (int i = top; i > last && i > top - 2 * NC; i -= 2)
+          if (i % NC == lane) last = i;
       }
-      if (last >= 0) mbar_wait(bar(T_FULL + lane), uint32_t(last / NS) & 1u, p.fault, p.wait_limit);
+      if (last >= 0) mbar_wait(bar(kLanded + lane), uint32_t(last / NC) & 1u, p.fault, p.wait_limit);
     }
     if (lane == 0 && tail[2] > 0) mbar_wait(bar(T_QFULL), uint32_t(tail[2] - 1) & 1u, p.fault, p.wait_limit);
   }
@@ -910,18 +978,19 @@ __global__ void __launch_bounds__(256) step_join_kernel(const TCParams p, const 
 
 // ------------------------------------------------------------------------- launch
 bool encode(CUtensorMap *map, const DeviceInfo &dev, int rank, const void *base, const cuuint64_t *dims,
-            const cuuint64_t *strides, const cuuint32_t *box) {
+            const cuuint64_t *strides, const cuuint32_t *box, bool codes = false) {
   auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(dev.encode_tiled);
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-  return fn && fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank), const_cast<void *>(base), dims, strides, box,
-                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  return fn && fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank),
+                  const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int TERMS>
+template <int D, int TERMS, bool FP8>
 psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &place, const DeviceInfo &dev,
                cudaStream_t s) {
-  using L = Lay<D, TERMS>;
+  using L = Lay<D, TERMS, FP8>;
   TCParams p;
   p.page_indices = S.page_indices;
   p.tree = S.tree;
@@ -969,18 +1038,26 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
     if (!encode(&tmQ, dev, 4, S.q, dims, strides, box))
       return fail(PSD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the queries");
   }
-  const cuuint64_t row = cuuint64_t(S.Hkv) * D * 2;  // bytes of a token slot
-  const cuuint64_t dims[5] = {64, 8, cuuint64_t(L::kHalves), cuuint64_t(S.Hkv),
-                              cuuint64_t(S.num_pages) * cuuint64_t(S.page_size) / 8};
-  const cuuint64_t strides[4] = {row, 128, cuuint64_t(D) * 2, 8 * row};
-  const cuuint32_t box[5] = {64, 8, cuuint32_t(L::kHalves), 1, cuuint32_t(p.sub / 8)};
-  if (!encode(&tmK, dev, 5, S.k_pool, dims, strides, box) || !encode(&tmV, dev, 5, S.v_pool, dims, strides, box))
-    return fail(PSD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
+  const cuuint64_t slots = cuuint64_t(S.num_pages) * cuuint64_t(S.page_size);
+  bool mapped;
+  if constexpr (FP8) {  // token slots of D codes a head, as they lie
+    const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(S.Hkv), slots};
+    const cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(S.Hkv) * D};
+    const cuuint32_t box[3] = {cuuint32_t(D), 1, cuuint32_t(p.sub)};
+    mapped = encode(&tmK, dev, 3, S.k_pool, dims, strides, box, true) && encode(&tmV, dev, 3, S.v_pool, dims, strides, box, true);
+  } else {
+    const cuuint64_t row = cuuint64_t(S.Hkv) * D * 2;  // bytes of a token slot
+    const cuuint64_t dims[5] = {64, 8, cuuint64_t(L::kHalves), cuuint64_t(S.Hkv), slots / 8};
+    const cuuint64_t strides[4] = {row, 128, cuuint64_t(D) * 2, 8 * row};
+    const cuuint32_t box[5] = {64, 8, cuuint32_t(L::kHalves), 1, cuuint32_t(p.sub / 8)};
+    mapped = encode(&tmK, dev, 5, S.k_pool, dims, strides, box) && encode(&tmV, dev, 5, S.v_pool, dims, strides, box);
+  }
+  if (!mapped) return fail(PSD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
 
-  auto kern = step_tc_kernel<D, TERMS>;
+  auto kern = step_tc_kernel<D, TERMS, FP8>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::kSmem));
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-  kern<<<ctas, kThreads, L::kSmem, s>>>(tmQ, tmK, tmV, p, req);
+  kern<<<ctas, L::kThreads, L::kSmem, s>>>(tmQ, tmK, tmV, p, req);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode launch: %s", cudaGetErrorString(e));
   // The units that a bound c total / ctas cuts, each named at its first.
@@ -1031,8 +1108,8 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
 
 bool step_tc_supports(const StepParams &p) {
   // q_scale > 0: the kernel takes the row maximum of the raw scores before scaling
-  return !p.fp8 && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.G <= kRows && p.q_scale > 0.f &&
-         p.num_pages * p.page_size / 8 < 0x7fffffffLL;
+  return (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.G <= kRows && p.q_scale > 0.f &&
+         p.num_pages * p.page_size <= 0x7fffffffLL;
 }
 
 StepPlace step_tc_place(int ctas, int D, float *base) {
@@ -1047,8 +1124,12 @@ StepPlace step_tc_place(int ctas, int D, float *base) {
 
 psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
                           cudaStream_t s) {
-  if (p.D == 64) return p.out_f32 ? run<64, 3>(p, req, place, dev, s) : run<64, 1>(p, req, place, dev, s);
-  return p.out_f32 ? run<128, 3>(p, req, place, dev, s) : run<128, 1>(p, req, place, dev, s);
+  auto go = [&](auto d) {
+    constexpr int D = decltype(d)::value;
+    if (p.fp8) return p.out_f32 ? run<D, 3, true>(p, req, place, dev, s) : run<D, 1, true>(p, req, place, dev, s);
+    return p.out_f32 ? run<D, 3, false>(p, req, place, dev, s) : run<D, 1, false>(p, req, place, dev, s);
+  };
+  return p.D == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
 }
 
 }  // namespace psd

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 
 
 def _tensor_cores(s, sm_scale):
-    return s.kv == "bf16" and s.D in (64, 128) and s.page % 8 == 0 and s.Hq // s.Hkv <= 128 and sm_scale > 0
+    return s.D in (64, 128) and s.page % 8 == 0 and s.Hq // s.Hkv <= 128 and sm_scale > 0
 
 
 def _run(s, *, out_f32=False, sm_scale=None, q=None, workspace=None, plan=None, o=None, lse=None, indices=None):
