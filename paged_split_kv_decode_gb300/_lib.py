@@ -193,12 +193,12 @@ def _sig(lib):
     lib.cascade_decode_no_alloc.argtypes = [V, C.POINTER(DecodeArgs), C.POINTER(CascadePlan), V, V, V,
                                             C.POINTER(CascadeStats), V]
     lib.psd_rope_frequencies.argtypes = [C.POINTER(RopeScaling), C.POINTER(C.c_double), C.POINTER(C.c_double)]
-    lib.append_tokens.argtypes = [V, C.POINTER(AppendArgs), V]
+    lib.append_tokens.argtypes = [V, V, V]       # (the structure's bytes, packed by the caller)
     lib.psd_plan_multi_token.argtypes = [C.POINTER(PageTable), P_i32, C.POINTER(MultiTokenPlan)]
     lib.psd_multi_token_workspace_bytes.argtypes = [V, i32]
     lib.psd_multi_token_workspace_bytes.restype = C.c_size_t
     lib.multi_token_decode.argtypes = [V, C.POINTER(MultiTokenArgs), C.POINTER(MultiTokenPlan), V, V, V, C.c_size_t, V]
-    lib.verify_drafts.argtypes = [V, C.POINTER(VerifyArgs), V]
+    lib.verify_drafts.argtypes = [V, V, V]
     for name in EXPORTS:
         f = getattr(lib, name)
         if f.restype is C.c_int or f.restype is None:

@@ -8,6 +8,7 @@ becomes the CUDA stream.  Every step of the decode path (planning included) runs
 from __future__ import annotations
 
 import ctypes as C
+import struct
 from dataclasses import dataclass
 
 import numpy as np
@@ -382,11 +383,8 @@ class RopeFrequencies:
     def __init__(self, inv_freq, magnitude: float = 1.0):
         self.inv_freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
         self.magnitude = float(magnitude)
-        self._ptr = self.inv_freq.ctypes.data_as(C.POINTER(C.c_double))
-
-    @property
-    def rot_dim(self) -> int:
-        return 2 * int(self.inv_freq.shape[0])
+        self.rot_dim = 2 * int(self.inv_freq.shape[0])
+        self.address = self.inv_freq.ctypes.data
 
 
 def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -404,44 +402,59 @@ def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "pla
     return RopeFrequencies(f, m.value)
 
 
-def _rows_ptr(t: torch.Tensor, name: str, dtype, ndim: int):
-    """(pointer, elements between rows) of a CUDA tensor whose rows are contiguous but may
-    lie apart (a view of a wider tensor)."""
+def _ctx_stream(ctx: Context, stream):
+    """The stream given, or the current one of the context's device (which need not be the
+    current device)."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(ctx.device)
+    return _stream(torch.cuda.current_stream(ctx.device) if stream is None else stream)
+
+
+# The operators of a multi-token step run between other launches of a serving loop, so their
+# host time counts: each fills its argument structure with one struct.pack (about 1 us on a
+# Grace host; 35 ctypes field stores take 6) and asks a tensor for its device by get_device().
+_APPEND = struct.Struct("@PPPqqqP9iPd5PqPPqiiffP")
+_VERIFY = struct.Struct("@PPqqPPPiiiPPP")
+assert _APPEND.size == C.sizeof(L.AppendArgs) and _VERIFY.size == C.sizeof(L.VerifyArgs)
+
+
+def _refuse(t, name: str, dtype, dev: int):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.dim() != ndim:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, expected cuda:{dev}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _flat(t: torch.Tensor, name: str, dtype, dev: int) -> int:
+    """The address of a contiguous tensor on device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, dtype, dev)
+    return t.data_ptr()
+
+
+def _shape(t: torch.Tensor, ndim: int, name: str):
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape = t.shape
+    if len(shape) != ndim:
         raise ValueError(f"{name} must have {ndim} dimensions")
-    width = 1
-    for d in range(ndim - 1, 0, -1):
-        if t.shape[d] != 1 and t.stride(d) != width:
+    return shape
+
+
+def _row_stride(t: torch.Tensor, shape, name: str, dtype, dev: int) -> int:
+    """Elements between the rows of a tensor on device `dev` whose rows are contiguous but may
+    lie apart (a view of a wider tensor)."""
+    if t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, dtype, dev)
+    stride, width = t.stride(), 1
+    for d in range(len(shape) - 1, 0, -1):
+        if stride[d] != width and shape[d] != 1:
             raise ValueError(f"{name}: the values of a row must be contiguous")
-        width *= int(t.shape[d])
-    return t.data_ptr(), (int(t.stride(0)) if t.shape[0] > 1 else width)
-
-
-def _int32_ptr(t: torch.Tensor, name: str, numel: int = None) -> int:
-    p = _dev_ptr(t, name)
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32")
-    if numel is not None and t.numel() != numel:
-        raise ValueError(f"{name} must hold {numel} values")
-    return p
-
-
-def _ctx_stream(ctx: Context, stream) -> C.c_void_p:
-    """The stream given, or the current one of the context's device (which need not be the
-    current device)."""
-    if stream is None and _raw_stream is not None:
-        return C.c_void_p(_raw_stream(ctx.device))
-    return _stream(torch.cuda.current_stream(ctx.device) if stream is None else stream)
-
-
-def _on_device(ctx: Context, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.is_cuda and t.device.index != ctx.device:
-            raise ValueError(f"{name} is on cuda:{t.device.index}, the context on cuda:{ctx.device}")
+        width *= shape[d]
+    return stride[0] if shape[0] > 1 else width
 
 
 def append_tokens(ctx: Context, q, k, v, q_out, *, q_indptr, kv_len, page_indptr, page_indices, k_pool, v_pool,
@@ -456,45 +469,52 @@ def append_tokens(ctx: Context, q, k, v, q_out, *, q_indptr, kv_len, page_indptr
     and positions ([T], optional) int32 on the device; pools bf16 or uint8 fp8-e4m3 codes
     [pages, page_size, Hkv, D].  Returns the int32 fault word tensor (the one given, or a new
     zero one)."""
-    a = L.AppendArgs()
-    a.k, a.k_stride = _rows_ptr(k, "k", torch.bfloat16, 3)
-    T, Hkv, D = (int(x) for x in k.shape)
+    dev, bf16, i32 = ctx.device, torch.bfloat16, torch.int32
+    ks = _shape(k, 3, "k")
+    T, Hkv, D = ks
+    k_stride = _row_stride(k, ks, "k", bf16, dev)
     if (q is None) != (q_out is None) or (v is None) != (v_pool is None):
         raise ValueError("q goes with q_out, v with v_pool")
+    q_ptr = out_ptr = q_stride = Hq = v_ptr = v_pool_ptr = v_stride = Dv = 0
     if q is not None:
-        a.q, a.q_stride = _rows_ptr(q, "q", torch.bfloat16, 3)
-        if int(q.shape[0]) != T or int(q.shape[2]) != D or q_out.shape != q.shape or q_out.dtype != torch.bfloat16:
+        qs = _shape(q, 3, "q")
+        Hq = qs[1]
+        if qs[0] != T or qs[2] != D or _shape(q_out, 3, "q_out") != qs:
             raise ValueError("q and q_out must be bf16 [T, Hq, D] with k's T and D")
-        a.q_out, a.Hq = _dev_ptr(q_out, "q_out"), int(q.shape[1])
-    if v is not None:
-        a.v, a.v_stride = _rows_ptr(v, "v", torch.bfloat16, 3)
-        a.Dv = int(v.shape[2])
-        if int(v.shape[0]) != T or int(v.shape[1]) != Hkv:
-            raise ValueError("v must be [T, Hkv, Dv] with k's T and Hkv")
-        if v_pool.dtype != k_pool.dtype or tuple(v_pool.shape) != tuple(k_pool.shape[:3]) + (a.Dv,):
-            raise ValueError("v_pool must be [num_pages, page_size, Hkv, Dv] of k_pool's type")
-        a.v_pool = _dev_ptr(v_pool, "v_pool")
-    if k_pool.dim() != 4 or int(k_pool.shape[2]) != Hkv or int(k_pool.shape[3]) != D:
+        q_ptr, q_stride = q.data_ptr(), _row_stride(q, qs, "q", bf16, dev)
+        out_ptr = _flat(q_out, "q_out", bf16, dev)
+    pool_shape = _shape(k_pool, 4, "k_pool")
+    num_pages, page_size, pool_heads, pool_dim = pool_shape
+    if pool_heads != Hkv or pool_dim != D:
         raise ValueError("k_pool must be [num_pages, page_size, Hkv, D]")
+    pool_type = k_pool.dtype
+    if v is not None:
+        vs = _shape(v, 3, "v")
+        Dv = vs[2]
+        if vs[0] != T or vs[1] != Hkv:
+            raise ValueError("v must be [T, Hkv, Dv] with k's T and Hkv")
+        if _shape(v_pool, 4, "v_pool") != pool_shape[:3] + (Dv,) or v_pool.dtype is not pool_type:
+            raise ValueError("v_pool must be [num_pages, page_size, Hkv, Dv] of k_pool's type")
+        v_ptr, v_stride = v.data_ptr(), _row_stride(v, vs, "v", bf16, dev)
+        v_pool_ptr = _flat(v_pool, "v_pool", pool_type, dev)
     if fault is None:
-        fault = torch.zeros(1, dtype=torch.int32, device=k_pool.device)
-    _on_device(ctx, q=q, k=k, v=v, q_out=q_out, q_indptr=q_indptr, kv_len=kv_len, page_indptr=page_indptr,
-               page_indices=page_indices, positions=positions, k_pool=k_pool, v_pool=v_pool, fault=fault)
-    B = int(kv_len.numel())
-    a.num_tokens, a.batch, a.Hkv, a.D = T, B, Hkv, D
-    a.rot_col, a.rot_dim, a.neox = int(rope_col), rope.rot_dim, int(bool(neox))
-    a.inv_freq, a.magnitude = rope._ptr, rope.magnitude
-    a.q_indptr = _int32_ptr(q_indptr, "q_indptr", B + 1)
-    a.kv_len = _int32_ptr(kv_len, "kv_len")
-    a.positions = None if positions is None else _int32_ptr(positions, "positions", T)
-    a.page_indptr = _int32_ptr(page_indptr, "page_indptr", B + 1)
-    a.page_indices, a.num_page_indices = _int32_ptr(page_indices, "page_indices"), int(page_indices.numel())
-    a.k_pool = _dev_ptr(k_pool, "k_pool")
-    a.num_pages, a.page_size = int(k_pool.shape[0]), int(k_pool.shape[1])
-    a.kv_dtype = kv_dtype_code(k_pool)
-    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
-    a.fault_dev = _int32_ptr(fault, "fault")
-    L.check(L.load().append_tokens(ctx.handle, C.byref(a), _ctx_stream(ctx, stream)))
+        fault = torch.zeros(1, dtype=i32, device=k_pool.device)
+    tables = (_flat(q_indptr, "q_indptr", i32, dev), _flat(kv_len, "kv_len", i32, dev),
+              0 if positions is None else _flat(positions, "positions", i32, dev),
+              _flat(page_indptr, "page_indptr", i32, dev), _flat(page_indices, "page_indices", i32, dev))
+    B = kv_len.numel()
+    if q_indptr.numel() != B + 1 or page_indptr.numel() != B + 1:
+        raise ValueError(f"q_indptr and page_indptr must hold {B + 1} values")
+    if positions is not None and positions.numel() != T:
+        raise ValueError(f"positions must hold {T} values")
+    args = _APPEND.pack(
+        q_ptr, k.data_ptr(), v_ptr, q_stride, k_stride, v_stride, out_ptr, T, B, Hq, Hkv, D, Dv, rope_col,
+        rope.rot_dim, 1 if neox else 0, rope.address, rope.magnitude, *tables, page_indices.numel(),
+        _flat(k_pool, "k_pool", pool_type, dev), v_pool_ptr, num_pages, page_size, kv_dtype_code(k_pool), k_scale,
+        v_scale, _flat(fault, "fault", i32, dev))
+    status = L.load().append_tokens(ctx._h, args, _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
     return fault
 
 
@@ -541,46 +561,44 @@ def multi_token_args(q, k_pool, v_pool, page_indices_dev, *, sm_scale: float, k_
                      v_scale: float = 1.0, tree_mask=None) -> L.MultiTokenArgs:
     """psd_multi_token_args from device tensors: q [T, Hq, D] bf16 (possibly a view with a
     token stride), pools [pages, page_size, Hkv, D] bf16 or uint8 fp8-e4m3 codes, page_indices
-    int32, tree_mask [T] int64 (64 bits a token) or None."""
-    a = L.MultiTokenArgs()
-    a.q, a.q_stride = _rows_ptr(q, "q", torch.bfloat16, 3)
-    a.num_tokens, a.Hq, a.D = (int(x) for x in q.shape)
-    if k_pool.dim() != 4 or v_pool.shape != k_pool.shape or v_pool.dtype != k_pool.dtype or int(k_pool.shape[3]) != a.D:
+    int32, tree_mask [T] int64 (64 bits a token) or None.  The structure keeps the tensors."""
+    shape = _shape(q, 3, "q")
+    T, Hq, D = shape
+    dev = q.get_device()
+    stride = _row_stride(q, shape, "q", torch.bfloat16, dev)
+    pool_shape, pool_type = _shape(k_pool, 4, "k_pool"), k_pool.dtype
+    if _shape(v_pool, 4, "v_pool") != pool_shape or v_pool.dtype is not pool_type or pool_shape[3] != D:
         raise ValueError("k_pool and v_pool must be alike, [num_pages, page_size, Hkv, D]")
-    a.k_pool, a.v_pool = _dev_ptr(k_pool, "k_pool"), _dev_ptr(v_pool, "v_pool")
-    a.page_indices_dev = _int32_ptr(page_indices_dev, "page_indices")
-    a.num_page_indices = int(page_indices_dev.numel())
-    a.num_pages, a.page_size, a.Hkv = (int(x) for x in k_pool.shape[:3])
-    a.kv_dtype = kv_dtype_code(k_pool)
-    a.k_scale, a.v_scale, a.sm_scale = float(k_scale), float(v_scale), float(sm_scale)
-    if tree_mask is not None:
-        if tree_mask.dtype != torch.int64 or tree_mask.numel() != a.num_tokens:
-            raise ValueError("tree_mask must be int64 [T]")
-        a.tree_mask = _dev_ptr(tree_mask, "tree_mask")
-    tensors = (q, k_pool, v_pool, page_indices_dev, tree_mask)
-    a.device = q.device.index
-    if any(t is not None and t.device.index != a.device for t in tensors):
-        raise ValueError("the tensors are on different devices")
-    a.tensors = tensors  # the structure holds their addresses
+    if tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.numel() != T):
+        raise ValueError("tree_mask must be int64 [T]")
+    a = L.MultiTokenArgs(
+        q.data_ptr(), stride, _flat(k_pool, "k_pool", pool_type, dev), _flat(v_pool, "v_pool", pool_type, dev),
+        _flat(page_indices_dev, "page_indices", torch.int32, dev), page_indices_dev.numel(), pool_shape[0], T, Hq,
+        pool_shape[2], D, pool_shape[1], kv_dtype_code(k_pool), k_scale, v_scale, sm_scale,
+        None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, dev), 0)
+    a.tensors, a.device = (q, k_pool, v_pool, page_indices_dev, tree_mask), dev
     return a
 
 
 def multi_token_decode(ctx: Context, args: L.MultiTokenArgs, plan: MultiTokenPlan, o: torch.Tensor,
                        lse: torch.Tensor = None, workspace: torch.Tensor = None, stream=None):
     """multi_token_decode: o [T, Hq, D] bf16 or f32, lse [T, Hq] f32 (log2 units) or None."""
-    if o.dtype not in (torch.bfloat16, torch.float32):
+    dev, out_type, shape = ctx.device, o.dtype, (args.num_tokens, args.Hq, args.D)
+    if args.device != dev:
+        raise ValueError(f"the arguments are on cuda:{args.device}, the context on cuda:{dev}")
+    args.out_f32 = out_type is torch.float32
+    if not args.out_f32 and out_type is not torch.bfloat16:
         raise TypeError("o must be bf16 or f32")
-    if tuple(o.shape) != (args.num_tokens, args.Hq, args.D):
+    if o.shape != shape:
         raise ValueError("o must be [T, Hq, D]")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (args.num_tokens, args.Hq)):
+    if lse is not None and lse.shape != shape[:2]:
         raise ValueError("lse must be f32 [T, Hq]")
-    _on_device(ctx, o=o, lse=lse, workspace=workspace)
-    if args.device != ctx.device:
-        raise ValueError(f"the arguments are on cuda:{args.device}, the context on cuda:{ctx.device}")
-    args.out_f32 = int(o.dtype == torch.float32)
-    L.check(L.load().multi_token_decode(
-        ctx.handle, C.byref(args), C.byref(plan.c), _dev_ptr(o, "o"), None if lse is None else _dev_ptr(lse, "lse"),
-        _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(), _ctx_stream(ctx, stream)))
+    status = L.load().multi_token_decode(
+        ctx._h, args, plan.c, _flat(o, "o", out_type, dev),
+        None if lse is None else _flat(lse, "lse", torch.float32, dev),
+        _flat(workspace, "workspace", torch.uint8, dev), workspace.numel(), _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
 
 
 def verify_drafts(ctx: Context, target_probs, draft_probs, draft_tokens, draft_indptr, uniforms, num_accepted,
@@ -589,32 +607,30 @@ def verify_drafts(ctx: Context, target_probs, draft_probs, draft_tokens, draft_i
     possibly apart), draft_tokens [D], draft_indptr [B + 1] int32, uniforms [D + B] f32;
     num_accepted [B] and out_tokens [D + B] int32 outputs, all on the device.  Returns the
     int32 fault word tensor (the one given, or a new zero one)."""
-    a = L.VerifyArgs()
-    a.target_probs, a.target_stride = _rows_ptr(target_probs, "target_probs", torch.float32, 2)
-    D, B, V = int(draft_tokens.numel()), int(num_accepted.numel()), int(target_probs.shape[1])
-    if int(target_probs.shape[0]) != D + B:
-        raise ValueError("target_probs must have num_drafts + batch rows")
-    if draft_probs is not None:
-        a.draft_probs, a.draft_stride = _rows_ptr(draft_probs, "draft_probs", torch.float32, 2)
-        if tuple(draft_probs.shape) != (D, V):
-            raise ValueError("draft_probs must be [num_drafts, vocab]")
-        if D == 0:
-            a.draft_probs = None
-    if uniforms.dtype != torch.float32 or uniforms.numel() != D + B:
-        raise ValueError("uniforms must be f32 [num_drafts + batch]")
+    dev, i32, f32 = ctx.device, torch.int32, torch.float32
+    shape = _shape(target_probs, 2, "target_probs")
+    rows, V = shape
+    t_stride = _row_stride(target_probs, shape, "target_probs", f32, dev)
     if fault is None:
-        fault = torch.zeros(1, dtype=torch.int32, device=target_probs.device)
-    _on_device(ctx, target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
-               draft_indptr=draft_indptr, uniforms=uniforms, num_accepted=num_accepted, out_tokens=out_tokens,
-               fault=fault)
-    a.draft_tokens = _int32_ptr(draft_tokens, "draft_tokens")
-    a.draft_indptr = _int32_ptr(draft_indptr, "draft_indptr", B + 1)
-    a.uniforms = _dev_ptr(uniforms, "uniforms")
-    a.batch, a.num_drafts, a.vocab = B, D, V
-    a.num_accepted = _int32_ptr(num_accepted, "num_accepted")
-    a.out_tokens = _int32_ptr(out_tokens, "out_tokens", D + B)
-    a.fault_dev = _int32_ptr(fault, "fault")
-    L.check(L.load().verify_drafts(ctx.handle, C.byref(a), _ctx_stream(ctx, stream)))
+        fault = torch.zeros(1, dtype=i32, device=target_probs.device)
+    ptrs = (_flat(draft_tokens, "draft_tokens", i32, dev), _flat(draft_indptr, "draft_indptr", i32, dev),
+            _flat(uniforms, "uniforms", f32, dev))
+    outs = (_flat(num_accepted, "num_accepted", i32, dev), _flat(out_tokens, "out_tokens", i32, dev),
+            _flat(fault, "fault", i32, dev))
+    D, B = draft_tokens.numel(), num_accepted.numel()
+    if rows != D + B or uniforms.numel() != rows or out_tokens.numel() != rows or draft_indptr.numel() != B + 1:
+        raise ValueError("target_probs, uniforms and out_tokens have num_drafts + batch rows, draft_indptr batch + 1")
+    d_ptr = d_stride = 0
+    if draft_probs is not None:
+        d_shape = _shape(draft_probs, 2, "draft_probs")
+        if d_shape[0] != D or d_shape[1] != V:
+            raise ValueError("draft_probs must be [num_drafts, vocab]")
+        d_stride = _row_stride(draft_probs, d_shape, "draft_probs", f32, dev)
+        d_ptr = draft_probs.data_ptr()
+    args = _VERIFY.pack(target_probs.data_ptr(), d_ptr, t_stride, d_stride, *ptrs, B, D, V, *outs)
+    status = L.load().verify_drafts(ctx._h, args, _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
     return fault
 
 

@@ -8,9 +8,10 @@
 
 namespace psd {
 
-// Requests of one launch, carried in its parameters (a batch with more takes several
-// launches): no list in memory that a captured call would read again.
-constexpr int kStepRequests = 768;
+// Requests of one launch, carried in its parameters: no list in memory that a captured call
+// would read again.  A batch with more takes several launches; parameters cost about 0.1 us a
+// KB, here 20 bytes a request, in every launch.
+constexpr int kStepRequests = 256;
 struct StepRequests {
   psd_token_request r[kStepRequests];
 };

@@ -49,6 +49,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <vector>
 
@@ -922,9 +923,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
 // A unit that the CTAs' bounds cut.
 struct Cut {
   int64_t out;   // output row of the unit's first token and head
-  int rows;      // live rows
-  int first, n;  // the CTA of its first piece, and its pieces: one a CTA from there on
-  int late;      // the first piece is the second of its CTA
+  int16_t rows;  // live rows
+  int16_t n;     // its pieces, one a CTA
+  int16_t first; // the CTA of the first
+  int16_t late;  // the first piece is the second of its CTA
 };
 constexpr int kMaxCuts = 192;  // bounds of a launch, one less than its CTAs
 struct Cuts {
@@ -1055,8 +1057,15 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   if (!mapped) return fail(PSD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
 
   auto kern = step_tc_kernel<D, TERMS, FP8>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::kSmem));
-  if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+  // once a device: the attribute stays, and setting it is a microsecond of every call
+  static std::atomic<uint64_t> ready{0};
+  const uint64_t bit = dev.device < 64 ? uint64_t(1) << dev.device : 0;
+  cudaError_t e = cudaSuccess;
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(L::kSmem));
+    if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    ready.fetch_or(bit, std::memory_order_release);
+  }
   kern<<<ctas, L::kThreads, L::kSmem, s>>>(tmQ, tmK, tmV, p, req);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode launch: %s", cudaGetErrorString(e));
@@ -1082,12 +1091,12 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
     done = first + n;
     Cut &u = cuts.c[n_cuts++];
     u.out = (int64_t(r.token0) + tok0) * S.Hq + int64_t(kv) * S.G;
-    u.rows = std::min(r.num_new - tok0, 2 * p.TH) * S.G;
-    u.first = c - 1;
+    u.rows = int16_t(std::min(r.num_new - tok0, 2 * p.TH) * S.G);
+    u.first = int16_t(c - 1);
     u.late = bound(c - 1) < first;
     u.n = 1;
     while (c - 1 + u.n < ctas && bound(c - 1 + u.n) < done) ++u.n;
-    most = std::max(most, u.rows);
+    most = std::max(most, int(u.rows));
   }
   if (n_cuts == 0) return PSD_OK;
   cudaLaunchConfig_t cfg = {};
