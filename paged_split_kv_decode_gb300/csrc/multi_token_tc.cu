@@ -32,8 +32,8 @@
 // 128-byte-swizzle atoms: one copy carries a whole head row (both halves at D = 128) of up
 // to 128 slots of a page.  Page positions past the request's pages load as zeros.
 //
-// fp8 pools: the copies bring codes (plain rows) into a ring of their own, and four more warps
-// (12-15) turn them into bf16 tiles of 64 keys in the layout above, half-tile by half-tile.
+// fp8 pools: the copies bring codes (plain rows) into a ring of their own, and eight more warps
+// (12-19) turn them into bf16 tiles of 64 keys in the layout above, half-tile by half-tile.
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
@@ -63,7 +63,7 @@ namespace {
 constexpr int kRows = 128;       // TMEM lanes of a row tile
 constexpr float kLazy = 8.f;     // log2 units
 constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
-constexpr int kConvertWarp = 12, kConvertWarps = 4;  // fp8 pools only
+constexpr int kConvertWarp = 12, kConvertWarps = 4;  // fp8 pools only: 4 warps for K, then 4 for V
 constexpr uint32_t kRingBytes = 128 * 1024;
 constexpr int kMaxStages = 16;
 constexpr int kFlush = 16;       // f32 outputs: ops of a slot (64 keys each) O holds at most
@@ -90,11 +90,11 @@ struct Lay {
   static constexpr uint32_t kPCols = NK / 2;                   // 32-bit columns of one P term
   static constexpr uint32_t kSCols = TERMS == 1 ? NK : 96;     // a slot's S, or its P terms if they are wider
   static constexpr uint32_t kColS = 2 * D;                     // after the two O
-  static constexpr int kThreads = FP8 ? 16 * 32 : 12 * 32;
-  // Registers a thread: 168 at launch of 384 threads, 128 of 512; the softmax warps hold a
+  static constexpr int kThreads = FP8 ? 20 * 32 : 12 * 32;
+  // Registers a thread: 168 at launch of 384 threads, 96 of 640; the softmax warps hold a
   // part's scores and weights and take what the others (warp 11 only gives) do without.
-  static constexpr int kLaunchRegs = FP8 ? 128 : 168;
-  static constexpr int kSoftmaxRegs = FP8 ? 176 : 208, kOtherRegs = FP8 ? 80 : 88;
+  static constexpr int kLaunchRegs = FP8 ? 96 : 168;
+  static constexpr int kSoftmaxRegs = FP8 ? 144 : 208, kOtherRegs = FP8 ? 64 : 88;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "registers of the launch");
   static_assert(TERMS * kPCols <= kSCols && NK <= int(kSCols), "S region");
   static_assert(kColS + 2 * kSCols <= 512, "TMEM columns");
@@ -293,6 +293,34 @@ __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN opera
   return d;
 }
 
+// 16 e4m3 codes to bf16, exactly: the code's exponent and mantissa bits, set at the low end of
+// bf16's, are the value times 2^-120 (denormals too), and one product puts it right.  NaN codes
+// (0x7f, 0xff) would come out as 480: a word that holds one takes the hardware conversion, which
+// is slow (a chain of three conversions a pair).
+__device__ __forceinline__ void codes_to_bf16(const uint4 &codes, uint32_t (&out)[8]) {
+  const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+  const uint32_t scale = 0x7b807b80u;  // 2^120, twice
+  uint32_t nan = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t x = __byte_perm(w[i], 0u, h ? 0x3424 : 0x1404);  // a code in the top byte of each half
+      const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
+      const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), *reinterpret_cast<const __nv_bfloat162 *>(&scale));
+      out[2 * i + h] = *reinterpret_cast<const uint32_t *>(&z);
+    }
+  }
+  if (nan & 0x80808080u) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = e4m3x2_to_float2(w[i >> 1] >> (16 * (i & 1)));
+      out[i] = bf16x2_bits(f.x, f.y);
+    }
+  }
+}
+
 // Waits for phase `parity` of the barrier, at most `limit` cycles.  The kernel's waits are many
 // and inlined, so that they leave the fault word to the end of their role.
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint32_t limit) {
@@ -447,43 +475,47 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     }
   } else if (FP8 && warp >= kConvertWarp) {
     // ------------------------------------------------------ fp8 codes to bf16
-    // Half-tile by half-tile in the order of the ring: 16 codes a thread and step, exact
-    // (e4m3 to f16 to f32 to bf16; the scales are in the scores' and the output's factors), into
-    // the swizzled layout the MMAs read.  V rows past the request's last token become zeros.
-    const int th = tid - 32 * kConvertWarp;
+    // Four warps take the K half-tiles and four the V, in the order of the ring: 16 codes a thread
+    // and step, exact (the scales are in the scores' and the output's factors), into the
+    // swizzled layout the MMAs read.  V rows past the request's last token become zeros.
+    const int th = (tid - 32 * kConvertWarp) & 127, v = warp >= kConvertWarp + kConvertWarps ? 1 : 0;
     int g = 0;
     bool ok = true;
     while (ok && walk.next(u)) {
-      for (int j = u.j0; j < u.j1 && ok; ++j, ++g)
-        for (int v = 0; v < 2; ++v) {
-          const int i = 2 * g + v, st = i % NS, rs = i % NC;
-          ok = wait_all(T_RFULL + rs, uint32_t(i / NC)) && (i < NS || wait_all(T_EMPTY + st, uint32_t(i / NS - 1)));
+      for (int j = u.j0; j < u.j1; ++j, ++g) {
+        const int i = 2 * g + v, st = i % NS, rs = i % NC;
+        {  // the codes have landed (lane 0 asks) and the stage is free (lane 1)
+          const int b = lane == 0 ? T_RFULL + rs : lane == 1 && i >= NS ? T_EMPTY + st : -1;
+          ok = b < 0 || wait_bounded(bar(b), uint32_t(lane == 0 ? i / NC : i / NS - 1) & 1u, p.wait_limit);
+          ok = __all_sync(0xffffffffu, ok) != 0;
           if (!ok) break;
-          const uint8_t *src = sm + L::kOffRaw + rs * L::kRawBytes;
-          uint8_t *dst = sm + st * L::kTileBytes;
-          const int left = v ? u.r.kv_len - j * NK : NK;
-#pragma unroll
-          for (int c = th; c < NK * D / 16; c += 32 * kConvertWarps) {
-            const int tk = c / (D / 16), col8 = 2 * (c % (D / 16)), h = col8 >> 3, k = col8 & 7;
-            const uint4 w = *reinterpret_cast<const uint4 *>(src + c * 16);
-            const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-            uint32_t out[8];
-#pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              const float2 f = e4m3x2_to_float2(in[y >> 1] >> (16 * (y & 1)));
-              out[y] = tk < left ? bf16x2_bits(f.x, f.y) : 0u;
-            }
-            uint8_t *row = dst + (tk >> 3) * L::kGroupBytes + h * 1024 + (tk & 7) * 128;
-            *reinterpret_cast<uint4 *>(row + ((k ^ (tk & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-            *reinterpret_cast<uint4 *>(row + (((k + 1) ^ (tk & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(bar(T_FULL + st));
-            mbar_arrive(bar(T_REMPTY + rs));
-          }
         }
+        const uint8_t *src = sm + L::kOffRaw + rs * L::kRawBytes;
+        uint8_t *dst = sm + st * L::kTileBytes;
+        const int left = v ? u.r.kv_len - j * NK : NK;
+        uint4 w[NK * D / 16 / 128];
+#pragma unroll
+        for (int c = 0; c < NK * D / 16 / 128; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + (128 * c + th) * 16);
+#pragma unroll
+        for (int c = 0; c < NK * D / 16 / 128; ++c) {
+          const int at = 128 * c + th, tk = at / (D / 16), col8 = 2 * (at % (D / 16)), h = col8 >> 3, k = col8 & 7;
+          uint32_t out[8];
+          codes_to_bf16(w[c], out);
+          if (tk >= left) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) out[y] = 0u;
+          }
+          uint8_t *row = dst + (tk >> 3) * L::kGroupBytes + h * 1024 + (tk & 7) * 128;
+          *reinterpret_cast<uint4 *>(row + ((k ^ (tk & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+          *reinterpret_cast<uint4 *>(row + (((k + 1) ^ (tk & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(T_FULL + st));
+          mbar_arrive(bar(T_REMPTY + rs));
+        }
+      }
     }
     if (!ok && lane == 0) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
   } else if (warp == kMmaWarp && elect()) {
@@ -655,18 +687,6 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         auto give_part = [&](auto which) -> bool {
           constexpr int part = decltype(which)::value;
           if (warp_live) {
-            uint32_t x[64];
-            tmem_ld32(s_col + 64 * part, x);
-            tmem_ld32(s_col + 64 * part + 32, x + 32);
-            ld_wait();
-            if (masked) {
-#pragma unroll
-              for (int h = 0; h < 64; h += 32) {
-                const uint32_t bits = visible(base + 64 * part + h, seen, start, tree, has_tree);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) x[h + c] = (bits >> c) & 1u ? x[h + c] : 0xff800000u;
-              }
-            }
             // P with the row's running maximum as it stands, and the part's own maximum beside it: on
             // most tiles no row grows by more than 2^8 and the maximum is off the critical path.
             // Otherwise (a unit's first tile among them) O and l are rescaled and P is taken again.
@@ -679,21 +699,32 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
               float t4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
               sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
-              for (int c = 0; c < 64; c += 8)
+              for (int c0 = 0; c0 < 64; c0 += 32) {
+                uint32_t x[32];
+                tmem_ld32(s_col + 64 * part + c0, x);
+                ld_wait();
+                if (masked) {
+                  const uint32_t bits = visible(base + 64 * part + c0, seen, start, tree, has_tree);
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                  t4[y] = max3(t4[y], __uint_as_float(x[c + 2 * y]), __uint_as_float(x[c + 2 * y + 1]));
+                  for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1u ? x[c] : 0xff800000u;
+                }
 #pragma unroll
-              for (int c = 0; c < 64; c += 2) {
-                const float2 z =
-                    __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), qs2, nm2);
-                const float a = ex2(z.x), b = ex2(z.y);
-                sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
-                if constexpr (TERMS == 1) {
-                  pk[c / 2] = bf16x2_bits(a, b);
-                } else {
-                  pf[c] = a;
-                  pf[c + 1] = b;
+                for (int c = 0; c < 32; c += 8)
+#pragma unroll
+                  for (int y = 0; y < 4; ++y)
+                    t4[y] = max3(t4[y], __uint_as_float(x[c + 2 * y]), __uint_as_float(x[c + 2 * y + 1]));
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                  const float2 z =
+                      __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), qs2, nm2);
+                  const float a = ex2(z.x), b = ex2(z.y);
+                  sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
+                  if constexpr (TERMS == 1) {
+                    pk[(c0 + c) / 2] = bf16x2_bits(a, b);
+                  } else {
+                    pf[c0 + c] = a;
+                    pf[c0 + c + 1] = b;
+                  }
                 }
               }
               float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
