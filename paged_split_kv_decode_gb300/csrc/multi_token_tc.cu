@@ -32,7 +32,7 @@
 // 128-byte-swizzle atoms: one copy carries a whole head row (both halves at D = 128) of up
 // to 128 slots of a page.  Page positions past the request's pages load as zeros.
 //
-// fp8 pools: the copies bring codes (plain rows) into a ring of their own, and eight more warps
+// fp8 pools: the copies bring codes (swizzled rows of a head) into a ring of their own, and eight more warps
 // (12-19) turn them into bf16 tiles of 64 keys in the layout above, half-tile by half-tile.
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
@@ -293,31 +293,14 @@ __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN opera
   return d;
 }
 
-// 16 e4m3 codes to bf16, exactly: the code's exponent and mantissa bits, set at the low end of
-// bf16's, are the value times 2^-120 (denormals too), and one product puts it right.  NaN codes
-// (0x7f, 0xff) would come out as 480: a word that holds one takes the hardware conversion, which
-// is slow (a chain of three conversions a pair).
+// 16 e4m3 codes to bf16, exactly, through f16 and f32.  (Setting the code's bits into bf16 and
+// multiplying by 2^120 is twice as slow: 40 half-rate integer steps against 8 conversions.)
 __device__ __forceinline__ void codes_to_bf16(const uint4 &codes, uint32_t (&out)[8]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-  const uint32_t scale = 0x7b807b80u;  // 2^120, twice
-  uint32_t nan = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    nan |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint32_t x = __byte_perm(w[i], 0u, h ? 0x3424 : 0x1404);  // a code in the top byte of each half
-      const uint32_t y = ((x >> 4) & 0x07f007f0u) | (x & 0x80008000u);
-      const __nv_bfloat162 z = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), *reinterpret_cast<const __nv_bfloat162 *>(&scale));
-      out[2 * i + h] = *reinterpret_cast<const uint32_t *>(&z);
-    }
-  }
-  if (nan & 0x80808080u) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = e4m3x2_to_float2(w[i >> 1] >> (16 * (i & 1)));
-      out[i] = bf16x2_bits(f.x, f.y);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = e4m3x2_to_float2(w[i >> 1] >> (16 * (i & 1)));
+    out[i] = bf16x2_bits(f.x, f.y);
   }
 }
 
@@ -493,19 +476,34 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         const uint8_t *src = sm + L::kOffRaw + rs * L::kRawBytes;
         uint8_t *dst = sm + st * L::kTileBytes;
         const int left = v ? u.r.kv_len - j * NK : NK;
-        uint4 w[NK * D / 16 / 128];
+        // A warp's step: 8 tokens, 4 chunks of 16 codes each; 8 lanes that move together have the 8
+        // tokens of a swizzle atom, codes and bf16, and so 8 different banks.
+        constexpr int kSteps = NK * D / 16 / 128;
+        const int step0 = (th >> 5) * kSteps;
+        auto place = [&](int c, int &tk, int &chunk) {
+          const int s = step0 + c;
+          tk = (D == 128 ? s >> 1 : s) * 8 + (lane & 7);
+          chunk = (D == 128 ? (s & 1) * 4 : 0) + (lane >> 3);
+        };
+        uint4 w[kSteps];
 #pragma unroll
-        for (int c = 0; c < NK * D / 16 / 128; ++c) w[c] = *reinterpret_cast<const uint4 *>(src + (128 * c + th) * 16);
+        for (int c = 0; c < kSteps; ++c) {
+          int tk, chunk;
+          place(c, tk, chunk);
+          w[c] = *reinterpret_cast<const uint4 *>(src + tk * D + ((chunk ^ (D == 128 ? tk & 7 : (tk >> 1) & 3)) << 4));
+        }
 #pragma unroll
-        for (int c = 0; c < NK * D / 16 / 128; ++c) {
-          const int at = 128 * c + th, tk = at / (D / 16), col8 = 2 * (at % (D / 16)), h = col8 >> 3, k = col8 & 7;
+        for (int c = 0; c < kSteps; ++c) {
+          int tk, chunk;
+          place(c, tk, chunk);
           uint32_t out[8];
           codes_to_bf16(w[c], out);
           if (tk >= left) {
 #pragma unroll
             for (int y = 0; y < 8; ++y) out[y] = 0u;
           }
-          uint8_t *row = dst + (tk >> 3) * L::kGroupBytes + h * 1024 + (tk & 7) * 128;
+          const int k = (2 * chunk) & 7;
+          uint8_t *row = dst + (tk >> 3) * L::kGroupBytes + (chunk >> 2) * 1024 + (tk & 7) * 128;
           *reinterpret_cast<uint4 *>(row + ((k ^ (tk & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
           *reinterpret_cast<uint4 *>(row + (((k + 1) ^ (tk & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
         }
@@ -1011,12 +1009,12 @@ __global__ void __launch_bounds__(256) step_join_kernel(const TCParams p, const 
 
 // ------------------------------------------------------------------------- launch
 bool encode(CUtensorMap *map, const DeviceInfo &dev, int rank, const void *base, const cuuint64_t *dims,
-            const cuuint64_t *strides, const cuuint32_t *box, bool codes = false) {
+            const cuuint64_t *strides, const cuuint32_t *box, int codes = 0) {  // bytes of a row of codes
   auto fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(dev.encode_tiled);
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   return fn && fn(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, cuuint32_t(rank),
                   const_cast<void *>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  codes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1077,7 +1075,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
     const cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(S.Hkv), slots};
     const cuuint64_t strides[2] = {cuuint64_t(D), cuuint64_t(S.Hkv) * D};
     const cuuint32_t box[3] = {cuuint32_t(D), 1, cuuint32_t(p.sub)};
-    mapped = encode(&tmK, dev, 3, S.k_pool, dims, strides, box, true) && encode(&tmV, dev, 3, S.v_pool, dims, strides, box, true);
+    mapped = encode(&tmK, dev, 3, S.k_pool, dims, strides, box, D) && encode(&tmV, dev, 3, S.v_pool, dims, strides, box, D);
   } else {
     const cuuint64_t row = cuuint64_t(S.Hkv) * D * 2;  // bytes of a token slot
     const cuuint64_t dims[5] = {64, 8, cuuint64_t(L::kHalves), cuuint64_t(S.Hkv), slots / 8};
