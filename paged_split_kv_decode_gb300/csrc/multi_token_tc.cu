@@ -127,16 +127,21 @@ struct TCParams {
   float *sum_o;     // [CTAs][2 slots][128 rows][D], f32 outputs only
   FaultRef fault;
   int64_t num_pages;
-  int64_t total;    // key tiles of the launch
-  int B, Hq, Hkv, G, TH, page_size, sub, out_f32;
+  int total;        // key tiles of the launch
+  int Hq, Hkv, G, TH, page_size, sub, out_f32;
   float q_scale, v_scale;
   uint32_t wait_limit;
   int withhold_from;  // testing aid: no loads for a unit's key tiles from this index on
 };
-// Requests with new tokens, and the number of key tiles before each (per-launch prefix).
+// Requests with new tokens, and where each CTA's stretch of the line of key tiles begins.
+constexpr int kMaxCtas = 192;
+struct Start {
+  uint16_t b, kv;  // request, KV head
+  int32_t tok0, j; // first token and key tile of the unit
+};
 struct TCRequests {
   psd_token_request r[kStepRequests];
-  int32_t base[kStepRequests + 1];
+  Start start[kMaxCtas];
 };
 
 // ------------------------------------------------------------------ walking the units
@@ -145,6 +150,7 @@ struct Unit {
   int kv, tok0;      // KV head, first new token of the unit
   int two;           // 1: two row tiles
   int j0, j1, n;     // this CTA's key tiles of the unit's n
+  bool first;        // the CTA's first unit
 };
 
 // Key tiles of the unit whose first token is tok0.
@@ -155,44 +161,35 @@ __host__ __device__ __forceinline__ int unit_tiles(const psd_token_request &r, i
   return (keys + NK - 1) / NK;
 }
 
-// Walks the units of the stretch [lo, hi) of the line of key tiles.
+__host__ __device__ __forceinline__ int bound(int c, int total, int ctas) { return int(int64_t(c) * total / ctas); }
+
+// Walks the units of this CTA's stretch.
 template <int NK>
 struct Walk {
   const TCParams &p;
   const TCRequests &req;
-  int64_t at, hi;
-  int b, kv, tok0, j;
-  __device__ Walk(const TCParams &p_, const TCRequests &req_, int64_t lo, int64_t hi_) : p(p_), req(req_), at(lo), hi(hi_) {
-    b = 0;
-    if (at >= hi) return;
-    for (int n = p.B; n > 1;) {  // the last request with base <= lo
-      const int mid = n / 2;
-      if (req.base[b + mid] <= at) b += mid, n -= mid;
-      else n = mid;
-    }
-    int rem = int(at - req.base[b]);
-    const int per_head = (req.base[b + 1] - req.base[b]) / p.Hkv;
-    kv = rem / per_head;
-    rem -= kv * per_head;
-    tok0 = 0;
-    for (;;) {
-      const int n = unit_tiles(req.r[b], tok0, p.TH, NK, p.tree != nullptr);
-      if (rem < n) break;
-      rem -= n;
-      tok0 += 2 * p.TH;
-    }
-    j = rem;
+  int left, b, kv, tok0, j;  // key tiles left; the next unit and tile
+  bool first = true;
+  __device__ Walk(const TCParams &p_, const TCRequests &req_) : p(p_), req(req_) {
+    const int c = blockIdx.x;
+    left = bound(c + 1, p.total, gridDim.x) - bound(c, p.total, gridDim.x);
+    b = req.start[c].b;
+    kv = req.start[c].kv;
+    tok0 = req.start[c].tok0;
+    j = req.start[c].j;
   }
   __device__ bool next(Unit &u) {
-    if (at >= hi) return false;
+    if (left == 0) return false;
     u.r = req.r[b];
     u.kv = kv;
     u.tok0 = tok0;
     u.two = u.r.num_new - tok0 > p.TH ? 1 : 0;
     u.n = unit_tiles(u.r, tok0, p.TH, NK, p.tree != nullptr);
     u.j0 = j;
-    u.j1 = int64_t(u.n - j) < hi - at ? u.n : j + int(hi - at);
-    at += u.j1 - u.j0;
+    u.j1 = min(u.n, j + left);
+    u.first = first;
+    left -= u.j1 - u.j0;
+    first = false;
     j = 0;
     tok0 += 2 * p.TH;
     if (tok0 >= u.r.num_new) {
@@ -344,7 +341,6 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
   float2 *lm = reinterpret_cast<float2 *>(sm + L::kOffLM);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t lo = int64_t(blockIdx.x) * p.total / gridDim.x, hi = int64_t(blockIdx.x + 1) * p.total / gridDim.x;
   const bool has_tree = p.tree != nullptr;
 
   if (tid == 0) {
@@ -379,6 +375,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
   __syncthreads();
   fence_after();
   const uint32_t tmem = *tslot;
+  uint32_t bad = 0;  // what this thread has to report when its role ends
   auto wait_all = [&](int b, uint32_t parity) {  // a warp's bounded wait
     return __all_sync(0xffffffffu, wait_bounded(bar(b), parity & 1u, p.wait_limit)) != 0;
   };
@@ -386,7 +383,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
   // the compiler would hold every role to the smallest.)
   if (warp >= kMmaWarp) {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kOtherRegs));
-  Walk<NK> walk(p, req, lo, hi);
+  Walk<NK> walk(p, req);
   Unit u;
   if (warp == kKWarp || warp == kVWarp) {
     // ----------------------------------------------------------------- loads
@@ -437,7 +434,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         if (lane < n_copies) {
           const int tok = j * NK + lane * p.sub, pos = tok / P;
           const bool there = pos < n_pages && id >= 0 && int64_t(id) < p.num_pages;
-          if (pos < n_pages && !there) raise_fault(p.fault, PSD_FAULT_PAGE_ID);
+          if (pos < n_pages && !there) bad |= PSD_FAULT_PAGE_ID;
           // the first token slot; not there: wholly outside the view, which reads as zeros
           const int64_t first = there ? int64_t(id) * P + (tok - pos * P) : -1024;
           if constexpr (FP8)
@@ -451,7 +448,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         id = id_next;
       }
     }
-    if (!ok && lane == 0) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
+    if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
     if (lane == 0) {
       tail[is_v] = g;
       if (!is_v) tail[2] = units;
@@ -515,7 +512,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         }
       }
     }
-    if (!ok && lane == 0) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
+    if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
   } else if (warp == kMmaWarp && elect()) {
     // ------------------------------------------------------------------- MMAs
     // One thread.  What stands between a P and its MMAs is on the critical path of both slots
@@ -596,12 +593,12 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     }
     // every MMA issued has completed before TMEM is released
     commit(bar(T_DRAIN));
-    if (!wait(T_DRAIN, 0u) || !ok) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
+    if (!wait(T_DRAIN, 0u) || !ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
   }
   } else {
     // ---------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoftmaxRegs));
-    Walk<NK> walk(p, req, lo, hi);
+    Walk<NK> walk(p, req);
     Unit u;
     const int slot = warp >> 2, r = tid & 127;       // row of the tile = TMEM lane
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
@@ -786,88 +783,59 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       fence_after();
       const bool whole = u.j0 == 0 && u.j1 == u.n;
       const int row = tile_tok * p.G + r - u.tok0 * p.G;   // row of the unit (p.TH * p.G a tile)
-      const int piece = 2 * blockIdx.x + (lo == walk.at - nt ? 0 : 1);  // the CTA's first piece, or its last
+      const int piece = 2 * blockIdx.x + (u.first ? 0 : 1);  // the CTA's first piece, or its last
       const int64_t out = (int64_t(u.r.token0) + tok) * p.Hq + u.kv * p.G + rg;
       // Where this row goes, in elements: the output, or a piece's rows in the workspace.
       const int64_t dst = live ? (whole ? out : int64_t(piece) * 2 * kRows + row) * D : -1;
+      // 32 columns of the warp's rows, as f32, from the rows' lanes to coalesced stores through
+      // shared memory: chunk k of row `lane` lies at k ^ lane % 8; then 4 lanes a row, 8 columns each,
+      // 8 rows a step.  (Lanes that store their own rows touch 32 lines at once: 10000 cycles a unit
+      // of 256 rows.  One rolled copy of the code: it runs once or a few times a CTA, and what it
+      // costs then is fetching it.)
       uint8_t *stage = sm + L::kOffOut + warp * (32 * 128);
-      // 128 bytes of each of the warp's rows, from the row's lane to coalesced stores: chunk k of
-      // row lane at (k ^ lane % 8), then 8 lanes a row, 4 rows a store.  (A lane storing its own
-      // row writes 32 lines at once: 10000 cycles a unit, against 2800.)
-      auto put128 = [&](const uint4 (&v)[8], uint8_t *base, int64_t byte, int elem) {
+      auto put32 = [&](const float (&x)[32], int c) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = v[k];
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<float4 *>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+              make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
         __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int rr = 4 * k + (lane >> 3);
+        const int k = 2 * (lane & 3), at = c + 4 * k;
+#pragma unroll 1
+        for (int rr = lane >> 2; rr < 32; rr += 8) {
           const int64_t to = __shfl_sync(0xffffffffu, dst, rr);
-          const uint4 x = *reinterpret_cast<const uint4 *>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) << 4));
-          if (to >= 0) *reinterpret_cast<uint4 *>(base + to * elem + byte + (lane & 7) * 16) = x;
+          const float4 y = *reinterpret_cast<const float4 *>(stage + rr * 128 + ((k ^ (rr & 7)) << 4));
+          const float4 z = *reinterpret_cast<const float4 *>(stage + rr * 128 + (((k + 1) ^ (rr & 7)) << 4));
+          if (to < 0) continue;
+          if (whole && TERMS == 1) {
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.o) + to + at) =
+                make_uint4(bf16x2_bits(y.x, y.y), bf16x2_bits(y.z, y.w), bf16x2_bits(z.x, z.y), bf16x2_bits(z.z, z.w));
+          } else {
+            float4 *out4 = reinterpret_cast<float4 *>((whole ? static_cast<float *>(p.o) : p.part_o) + to + at);
+            out4[0] = y;
+            out4[1] = z;
+          }
         }
         __syncwarp();
       };
-      // What the flushed ops of slot `of` add to column c + k of the row, scaled to 2^m_of.
-      const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);
-      auto add_flushed = [&](float *x, int c, const float *row_of, float scale) {
+      const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);  // flushed sums to 2^m
+      auto add_flushed = [&](float (&x)[32], const float *from, float scale) {
 #pragma unroll
-        for (int k = 0; k < 64; k += 4) {
-          const float4 y = *reinterpret_cast<const float4 *>(row_of + c + k);
+        for (int k = 0; k < 32; k += 4) {
+          const float4 y = *reinterpret_cast<const float4 *>(from + k);
           x[k] = fmaf(y.x, scale, x[k]);
           x[k + 1] = fmaf(y.y, scale, x[k + 1]);
           x[k + 2] = fmaf(y.z, scale, x[k + 2]);
           x[k + 3] = fmaf(y.w, scale, x[k + 3]);
         }
       };
-      // Columns [c, c + 64) of the rows, scaled.
-      auto put64 = [&](const float (&x)[64], int c) {
-        uint4 v[8];
-        if (whole && TERMS == 1) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            v[k] = make_uint4(bf16x2_bits(x[8 * k], x[8 * k + 1]), bf16x2_bits(x[8 * k + 2], x[8 * k + 3]),
-                              bf16x2_bits(x[8 * k + 4], x[8 * k + 5]), bf16x2_bits(x[8 * k + 6], x[8 * k + 7]));
-          put128(v, static_cast<uint8_t *>(p.o), int64_t(c) * 2, 2);
-        } else {
-          uint8_t *base = whole ? static_cast<uint8_t *>(p.o) : reinterpret_cast<uint8_t *>(p.part_o);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              v[k] = make_uint4(__float_as_uint(x[32 * h + 4 * k]), __float_as_uint(x[32 * h + 4 * k + 1]),
-                                __float_as_uint(x[32 * h + 4 * k + 2]), __float_as_uint(x[32 * h + 4 * k + 3]));
-            put128(v, base, int64_t(c + 32 * h) * 4, 4);
-          }
-        }
-      };
-      auto put_lse = [&](float v) {
-        if (!whole) p.part_lse[int64_t(piece) * 2 * kRows + row] = v;
-        else if (p.lse) p.lse[out] = v;
-      };
-      if (u.two || T == 1) {
-        if (warp_live && (u.two || slot == 0)) {
-          const float inv = l == 0.f ? 0.f : p.v_scale / l;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            float x[64];
-            tmem_ld32(lane_base + D * slot + c, reinterpret_cast<uint32_t *>(x));
-            tmem_ld32(lane_base + D * slot + c + 32, reinterpret_cast<uint32_t *>(x) + 32);
-            ld_wait();
-#pragma unroll
-            for (int k = 0; k < 64; ++k) x[k] = l == 0.f ? 0.f : x[k] * inv;
-            if (TERMS > 1 && live && flushed && l != 0.f) add_flushed(x, c, sum_row, keep * inv);
-            put64(x, c);
-          }
-          if (live) put_lse(l == 0.f ? neg_inf() : m + log2f(l));
-        }
-      } else if (slot == 1) {
-        // the unit's other keys: (m, l) for slot 0, which joins the two O
-        if (singles > 0) ok = wait_all(T_XFREE, uint32_t(singles - 1));
-        if (!ok) break;
+      const bool joint = !u.two && T > 1;  // the slots have the unit's even and odd tiles: slot 0 joins them
+      float m1 = neg_inf(), l1 = 0.f;
+      if (joint && slot == 1) {
+        if (singles > 0 && !(ok = wait_all(T_XFREE, uint32_t(singles - 1)))) break;
         if constexpr (TERMS > 1) {
           // fold the flushed sum into 2^m units, so that slot 0 needs no more than (m, l)
           if (live && flushed && l != 0.f && keep != 1.f) {
-#pragma unroll 4
+#pragma unroll 1
             for (int c = 0; c < D; c += 4) {
               float4 *at = reinterpret_cast<float4 *>(sum_row + c);
               float4 x = *at;
@@ -880,41 +848,44 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(T_XREADY));
         ++singles;
-      } else {
-        ok = wait_all(T_XREADY, uint32_t(singles));
-        if (!ok) break;
+      } else if (joint) {
+        if (!(ok = wait_all(T_XREADY, uint32_t(singles)))) break;
         const float2 other = lm[r];
+        m1 = other.x, l1 = other.y;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(T_XFREE));
         ++singles;
-        if (warp_live) {
-          const float m1 = other.x, l1 = other.y;
-          const float top = fmaxf(m, m1), from = top == neg_inf() ? 0.f : top;
-          const float w0 = ex2(m - from), w1 = ex2(m1 - from);  // 0 where the half saw no key
-          const float all = l * w0 + l1 * w1, inv = all == 0.f ? 0.f : p.v_scale / all;
-          const float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
+      }
+      if (warp_live && (u.two || slot == 0)) {
+        const float top = fmaxf(m, m1), from = top == neg_inf() ? 0.f : top;
+        const float w0 = ex2(m - from), w1 = ex2(m1 - from);  // 0 where a slot saw no key
+        const float all = l * w0 + l1 * w1, inv = all == 0.f ? 0.f : p.v_scale / all;
+        const float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
 #pragma unroll 1
-          for (int c = 0; c < D; c += 64) {
-            float x[64];
-            tmem_ld32(lane_base + c, reinterpret_cast<uint32_t *>(x));
-            tmem_ld32(lane_base + c + 32, reinterpret_cast<uint32_t *>(x) + 32);
+        for (int c = 0; c < D; c += 32) {
+          float x[32];
+          tmem_ld32(lane_base + D * slot + c, reinterpret_cast<uint32_t *>(x));
+          ld_wait();
 #pragma unroll
-            for (int h = 0; h < 64; h += 32) {
-              uint32_t y[32];
-              tmem_ld32(lane_base + D + c + h, y);
-              ld_wait();
+          for (int k = 0; k < 32; ++k) x[k] = l == 0.f ? 0.f : x[k] * f0;
+          if (joint) {
+            uint32_t y[32];
+            tmem_ld32(lane_base + D + c, y);
+            ld_wait();
 #pragma unroll
-              for (int k = 0; k < 32; ++k)
-                x[h + k] = (l == 0.f ? 0.f : x[h + k] * f0) + (l1 == 0.f ? 0.f : __uint_as_float(y[k]) * f1);
-            }
-            if constexpr (TERMS > 1) {
-              // (slot 1 flushed if it had more than kFlush ops: every row, its T / 2 ops)
-              if (live && flushed && l != 0.f) add_flushed(x, c, sum_row, keep * f0);
-              if (live && (T >> 1) > kFlush && l1 != 0.f) add_flushed(x, c, sum_row + kRows * D, f1);
-            }
-            put64(x, c);
+            for (int k = 0; k < 32; ++k) x[k] = l1 == 0.f ? x[k] : fmaf(__uint_as_float(y[k]), f1, x[k]);
           }
-          if (live) put_lse(all == 0.f ? neg_inf() : top + log2f(all));
+          if constexpr (TERMS > 1) {
+            if (live && flushed && l != 0.f) add_flushed(x, sum_row + c, keep * f0);
+            // (slot 1 flushed if it had more than kFlush ops: every row, its T / 2 ops)
+            if (joint && live && (T >> 1) > kFlush && l1 != 0.f) add_flushed(x, sum_row + kRows * D + c, f1);
+          }
+          put32(x, c);
+        }
+        if (live) {
+          const float v = all == 0.f ? neg_inf() : top + log2f(all);
+          if (!whole) p.part_lse[int64_t(piece) * 2 * kRows + row] = v;
+          else if (p.lse) p.lse[out] = v;
         }
       }
       fence_before();
@@ -923,7 +894,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       g += nt;
       ++units;
     }
-    if (!ok && lane == 0) raise_fault(p.fault, PSD_FAULT_WAIT_TIMEOUT);
+    if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
   }
   __syncwarp();
   st_wait();
@@ -939,10 +910,13 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         for (int i = top; i > last && i > top - 2 * NC; i -= 2)
           if (i % NC == lane) last = i;
       }
-      if (last >= 0) mbar_wait(bar(kLanded + lane), uint32_t(last / NC) & 1u, p.fault, p.wait_limit);
+      if (last >= 0 && !wait_bounded(bar(kLanded + lane), uint32_t(last / NC) & 1u, p.wait_limit))
+        bad |= PSD_FAULT_WAIT_TIMEOUT;
     }
-    if (lane == 0 && tail[2] > 0) mbar_wait(bar(T_QFULL), uint32_t(tail[2] - 1) & 1u, p.fault, p.wait_limit);
+    if (lane == 0 && tail[2] > 0 && !wait_bounded(bar(T_QFULL), uint32_t(tail[2] - 1) & 1u, p.wait_limit))
+      bad |= PSD_FAULT_WAIT_TIMEOUT;
   }
+  if (bad) raise_fault(p.fault, bad);
   if (warp == kMmaWarp) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
@@ -957,9 +931,8 @@ struct Cut {
   int16_t first; // the CTA of the first
   int16_t late;  // the first piece is the second of its CTA
 };
-constexpr int kMaxCuts = 192;  // bounds of a launch, one less than its CTAs
 struct Cuts {
-  Cut c[kMaxCuts];
+  Cut c[kMaxCtas - 1];
 };
 
 // Joins the pieces of the cut units (blockIdx.x), in key order: a warp per row.  The host
@@ -1029,7 +1002,6 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   p.lse = S.lse;
   p.fault = S.fault;
   p.num_pages = S.num_pages;
-  p.B = S.B;
   p.Hq = S.Hq;
   p.Hkv = S.Hkv;
   p.G = S.G;
@@ -1044,19 +1016,52 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   p.withhold_from = dev.test_withhold_from >= 0 ? dev.test_withhold_from : 0x7fffffff;
   TCRequests req;
   std::memcpy(req.r, sreq.r, sizeof(psd_token_request) * size_t(S.B));
+  const bool tree = S.tree != nullptr;
   int64_t total = 0;
+  int head[kStepRequests];  // key tiles of one KV head of a request
   for (int b = 0; b < S.B; ++b) {
-    req.base[b] = int32_t(total);
     const psd_token_request &r = req.r[b];
-    int64_t head = 0;
-    for (int t = 0; t < r.num_new; t += 2 * p.TH) head += unit_tiles(r, t, p.TH, L::NK, S.tree != nullptr);
-    total += head * S.Hkv;
+    int64_t n = 0;
+    for (int t = 0; t < r.num_new; t += 2 * p.TH) n += unit_tiles(r, t, p.TH, L::NK, tree);
+    total += n * S.Hkv;
     if (total > 0x7fffffffLL)
       return fail(PSD_ERR_UNSUPPORTED, "multi_token_decode: more than 2^31 key tiles in one launch");
+    head[b] = int(n);
   }
-  req.base[S.B] = int32_t(total);
-  p.total = total;
-  const int ctas = int(std::min<int64_t>(total, std::min(place.ctas, kMaxCuts + 1)));
+  p.total = int(total);
+  const int ctas = int(std::min<int64_t>(total, std::min(place.ctas, kMaxCtas)));
+  // Where the CTAs' stretches begin, and the units that a bound cuts, each named at its first.
+  Cuts cuts;
+  int n_cuts = 0, most = 0;
+  {
+    int b = 0, kv = 0, tok0 = 0, n = unit_tiles(req.r[0], 0, p.TH, L::NK, tree);
+    int64_t base = 0, first = 0;  // tiles before request b and before the unit
+    for (int c = 0; c < ctas; ++c) {
+      const int64_t at = bound(c, p.total, ctas);
+      while (at >= base + int64_t(head[b]) * S.Hkv) base += int64_t(head[b++]) * S.Hkv, first = -1;
+      const int h = int((at - base) / head[b]);
+      if (first < 0 || h != kv) {
+        kv = h, tok0 = 0, first = base + int64_t(h) * head[b];
+        n = unit_tiles(req.r[b], 0, p.TH, L::NK, tree);
+      }
+      while (at >= first + n) {
+        first += n, tok0 += 2 * p.TH;
+        n = unit_tiles(req.r[b], tok0, p.TH, L::NK, tree);
+      }
+      req.start[c] = Start{uint16_t(b), uint16_t(kv), tok0, int32_t(at - first)};
+      // cut here, and not at a bound before?
+      if (at == first || (c > 0 && bound(c - 1, p.total, ctas) > first)) continue;
+      const psd_token_request &r = req.r[b];
+      Cut &u = cuts.c[n_cuts++];
+      u.out = (int64_t(r.token0) + tok0) * S.Hq + int64_t(kv) * S.G;
+      u.rows = int16_t(std::min(r.num_new - tok0, 2 * p.TH) * S.G);
+      u.first = int16_t(c - 1);
+      u.late = bound(c - 1, p.total, ctas) < first;
+      u.n = 1;
+      while (c - 1 + u.n < ctas && bound(c - 1 + u.n, p.total, ctas) < first + n) ++u.n;
+      most = std::max(most, int(u.rows));
+    }
+  }
   p.part_o = place.part_o;
   p.part_lse = place.part_lse;
   p.sum_o = place.sum_o;
@@ -1098,35 +1103,6 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   kern<<<ctas, L::kThreads, L::kSmem, s>>>(tmQ, tmK, tmV, p, req);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode launch: %s", cudaGetErrorString(e));
-  // The units that a bound c total / ctas cuts, each named at its first.
-  Cuts cuts;
-  int n_cuts = 0, most = 0;
-  int64_t done = 0;  // end of the last unit named
-  auto bound = [&](int64_t c) { return c * total / ctas; };
-  for (int c = 1, b = 0; c < ctas; ++c) {
-    const int64_t at = bound(c);
-    if (at < done) continue;
-    while (req.base[b + 1] <= at) ++b;
-    const psd_token_request &r = req.r[b];
-    const int64_t head = (req.base[b + 1] - req.base[b]) / S.Hkv;
-    const int kv = int((at - req.base[b]) / head);
-    int64_t first = req.base[b] + kv * head;
-    int tok0 = 0, n = 0;
-    for (;; tok0 += 2 * p.TH, first += n) {
-      n = unit_tiles(r, tok0, p.TH, L::NK, S.tree != nullptr);
-      if (at < first + n) break;
-    }
-    if (at == first) continue;  // between two units
-    done = first + n;
-    Cut &u = cuts.c[n_cuts++];
-    u.out = (int64_t(r.token0) + tok0) * S.Hq + int64_t(kv) * S.G;
-    u.rows = int16_t(std::min(r.num_new - tok0, 2 * p.TH) * S.G);
-    u.first = int16_t(c - 1);
-    u.late = bound(c - 1) < first;
-    u.n = 1;
-    while (c - 1 + u.n < ctas && bound(c - 1 + u.n) < done) ++u.n;
-    most = std::max(most, int(u.rows));
-  }
   if (n_cuts == 0) return PSD_OK;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(n_cuts), unsigned((most + 7) / 8));
