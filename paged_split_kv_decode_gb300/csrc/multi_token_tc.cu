@@ -24,8 +24,8 @@
 // A tile's P goes in parts of 64 keys, so that PV of the first runs while the second is made.
 //   TMEM (512 columns): per slot S [128 x NK] f32 with P over it, and O [128 x D] f32.
 //   Shared memory: two row tiles of Q, a ring of K and V half-tiles (K, V, K, V, ...).
-//   Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row = TMEM lane), 8 MMA (one
-//   thread), 9 loads Q and K, 10 loads V, 11 none.
+//   Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row = TMEM lane), 8 and 11 (one
+//   thread each) the MMAs of the slots, 9 loads Q and K, 10 loads V.
 //
 // Tiles are read by TMA through a 5-D view of the pool, [groups of 8 token slots][KV head]
 // [64-column halves][8 slots][64 columns], whose box of a page's part lands as complete
@@ -62,7 +62,7 @@ namespace {
 
 constexpr int kRows = 128;       // TMEM lanes of a row tile
 constexpr float kLazy = 8.f;     // log2 units
-constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10;
+constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kMmaWarp1 = 11;
 constexpr int kConvertWarp = 12, kConvertWarps = 4;  // fp8 pools only: 4 warps for K, then 4 for V
 constexpr uint32_t kRingBytes = 128 * 1024;
 constexpr int kMaxStages = 16;
@@ -92,7 +92,7 @@ struct Lay {
   static constexpr uint32_t kColS = 2 * D;                     // after the two O
   static constexpr int kThreads = FP8 ? 20 * 32 : 12 * 32;
   // Registers a thread: 168 at launch of 384 threads, 96 of 640; the softmax warps hold a
-  // part's scores and weights and take what the others (warp 11 only gives) do without.
+  // part's scores and weights and take what the others do without.
   static constexpr int kLaunchRegs = FP8 ? 96 : 168;
   static constexpr int kSoftmaxRegs = FP8 ? 144 : 208, kOtherRegs = FP8 ? 64 : 88;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "registers of the launch");
@@ -110,7 +110,8 @@ enum {
   T_SFULL,                           // [2] S of the slot's next op is complete
   T_PFULL = T_SFULL + 2,             // [part][2] the part's P is written (4 warps)
   T_HALF = T_PFULL + 4,              // [2] the first part's PV of the slot's op is complete
-  T_OFULL = T_HALF + 2,              // every PV of the unit is complete
+  T_TURN = T_HALF + 2,               // [2] the MMAs of the other slot's op before are issued
+  T_OFULL = T_TURN + 2,              // every PV of the unit is complete
   T_OFREE,                           // the unit's O are read out (8 warps)
   T_XREADY, T_XFREE,                 // slot 1's (m, l) written / read (4 warps)
   T_DRAIN, T_SLOT, T_TAIL
@@ -346,25 +347,26 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(bar(T_FULL + i), FP8 ? kConvertWarps : 1);
-      mbar_init(bar(T_EMPTY + i), 1);
+      mbar_init(bar(T_EMPTY + i), 2);
     }
     for (int i = 0; i < L::kRaw; ++i) {
       mbar_init(bar(T_RFULL + i), 1);
       mbar_init(bar(T_REMPTY + i), kConvertWarps);
     }
     mbar_init(bar(T_QFULL), 1);
-    mbar_init(bar(T_QFREE), 1);
+    mbar_init(bar(T_QFREE), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(T_SFULL + i), 1);
       mbar_init(bar(T_PFULL + i), 4);
       mbar_init(bar(T_PFULL + 2 + i), 4);
       mbar_init(bar(T_HALF + i), 1);
+      mbar_init(bar(T_TURN + i), 1);
     }
-    mbar_init(bar(T_OFULL), 1);
+    mbar_init(bar(T_OFULL), 2);
     mbar_init(bar(T_OFREE), 8);
     mbar_init(bar(T_XREADY), 4);
     mbar_init(bar(T_XFREE), 4);
-    mbar_init(bar(T_DRAIN), 1);
+    mbar_init(bar(T_DRAIN), 2);
     fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -513,12 +515,16 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       }
     }
     if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
-  } else if (warp == kMmaWarp && elect()) {
-    // ------------------------------------------------------------------- MMAs
-    // One thread.  What stands between a P and its MMAs is on the critical path of both slots
-    // (a warp that voted on each wait and waited for K between P V and S spent 600 cycles an
-    // op there): the tiles of an op are waited for before its P, and S(t + 2) follows
-    // P V(t) without a wait.
+  } else if (elect()) {
+    // ------------------------------------------------------- the MMAs of a slot
+    // One thread a slot: an op costs its thread about 1300 cycles (16 issues, six waits of over
+    // 100 cycles on barriers that are ready), more than the 1024 its MMAs take.  The ops go in
+    // turn, so that the slots stay half a period apart: left alone they fall into step, and the
+    // tensor cores idle while both take their softmax (368 us for the 4096-token prompt).
+    // The tiles of an op are waited for before its P, and S(t + 2) follows P V(t) without a wait.
+    // A half-tile is released by two commits: one from each slot where both read it, two
+    // from the slot that has it alone.
+    const int slot = warp == kMmaWarp1 ? 1 : 0;
     const uint32_t id_s = idesc_bf16(kRows, NK, false);
     const uint32_t id_pv = idesc_bf16(kRows, D, true);
     // Q: 8-row groups 1024 B apart.  K (K-major): 8-token groups kGroupBytes apart, a half 1024 B
@@ -526,67 +532,68 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     const uint64_t qd = desc_sw128(smem_u32(sm + L::kOffQ), 16, 1024);
     const uint64_t kd = desc_sw128(smem_u32(sm), 16, L::kGroupBytes);
     const uint64_t vd = desc_sw128(smem_u32(sm), 1024, L::kGroupBytes);
+    const uint32_t d = tmem + D * slot, sp = tmem + L::kColS + slot * L::kSCols;  // O; S and P
     auto wait = [&](int b, uint32_t parity) { return wait_bounded(bar(b), parity & 1u, p.wait_limit); };
     int g = 0, units = 0;
-    uint32_t ops = 0;  // bit `slot`: parity of the slot's ops so far
+    uint32_t ops = 0, turns = 0;  // this slot's ops, and turns waited for
     bool ok = true;
     while (ok && walk.next(u)) {
       const int nt = u.j1 - u.j0, T = u.two ? 2 * nt : nt;
       auto half_tile = [&](int t) { return 2 * (g + (u.two ? t >> 1 : t)); };  // K of op t; V is the next
       auto k_ready = [&](int t) {
         const int i = half_tile(t);
-        return (u.two && (t & 1)) || wait(T_FULL + i % NS, uint32_t(i / NS));
+        return wait(T_FULL + i % NS, uint32_t(i / NS));
       };
+      const uint64_t q = qd + ((u.two && slot ? L::kQBytes : 0u) >> 4);
       auto issue_s = [&](int t) {
-        const int slot = t & 1, st = half_tile(t) % NS;
-        const uint64_t a = qd + ((u.two && slot ? L::kQBytes : 0u) >> 4);
+        const int st = half_tile(t) % NS;
         const uint64_t b = kd + ((st * L::kTileBytes) >> 4);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)
-          mma_ss(tmem + L::kColS + slot * L::kSCols, a + (((k >> 2) * L::kQHalfBytes + (k & 3) * 32) >> 4),
-                 b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), id_s, k > 0);
+          mma_ss(sp, q + (((k >> 2) * L::kQHalfBytes + (k & 3) * 32) >> 4), b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
+                 id_s, k > 0);
         commit(bar(T_SFULL + slot));
-        if (!u.two || slot) commit(bar(T_EMPTY + st));
-        if (t == T - 1) commit(bar(T_QFREE));
+        commit(bar(T_EMPTY + st));
+        if (!u.two) commit(bar(T_EMPTY + st));
+        if (t + 2 >= T) commit(bar(T_QFREE));
       };
-      ok = wait(T_QFULL, uint32_t(units)) && k_ready(0);
+      ok = wait(T_QFULL, uint32_t(units)) && (slot >= T || k_ready(slot));
       if (!ok) break;
       fence_after();
-      issue_s(0);
-      if (T > 1) {
-        if (!(ok = k_ready(1))) break;
-        fence_after();
-        issue_s(1);
+      if (slot < T) {
+        issue_s(slot);
+      } else {  // one key tile: slot 0's
+        commit(bar(T_QFREE));
+        commit(bar(T_OFULL));
       }
-      for (int t = 0; t < T; ++t) {
-        const int slot = t & 1, i = half_tile(t) + 1, st = i % NS;
+      for (int t = slot; t < T; t += 2) {
+        const int i = half_tile(t) + 1, st = i % NS;
         // K of op t + 2 has a stage that op t or an earlier one freed: no P stands before it
-        ok = ((u.two && slot) || wait(T_FULL + st, uint32_t(i / NS))) && (t + 2 >= T || k_ready(t + 2)) &&
-             (t > 0 || units == 0 || wait(T_OFREE, uint32_t(units - 1)));
+        ok = wait(T_FULL + st, uint32_t(i / NS)) && (t + 2 >= T || k_ready(t + 2)) &&
+             (t > 1 || units == 0 || wait(T_OFREE, uint32_t(units - 1))) && (t == 0 || wait(T_TURN + slot, turns));
         if (!ok) break;
-        const uint32_t d = tmem + D * slot, a = tmem + L::kColS + slot * L::kSCols;
+        if (t > 0) ++turns;
         const uint64_t b = vd + ((st * L::kTileBytes) >> 4);
         const bool fresh = TERMS > 1 ? (t >> 1) % kFlush == 0 : t < 2;  // O starts at zero
 #pragma unroll
         for (int part = 0; part < L::kParts; ++part) {
-          ok = wait(T_PFULL + 2 * part + slot, ops >> slot);
+          ok = wait(T_PFULL + 2 * part + slot, ops);
           if (!ok) break;
           fence_after();
-          const uint32_t ap = a + 32 * part;
-          const uint64_t bp = b + ((part * 8 * L::kGroupBytes) >> 4);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 4 * part; k < 4 * part + 4; ++k)
 #pragma unroll
             for (int x = 0; x < TERMS; ++x)
-              mma_ts(d, ap + x * L::kPCols + 8 * k, bp + ((k * 2 * L::kGroupBytes) >> 4), id_pv,
-                     !fresh || part > 0 || k > 0 || x > 0);
+              mma_ts(d, sp + x * L::kPCols + 8 * k, b + ((k * 2 * L::kGroupBytes) >> 4), id_pv, !fresh || k > 0 || x > 0);
           if (part == 0 && L::kParts > 1) commit(bar(T_HALF + slot));
         }
         if (!ok) break;
-        ops ^= 1u << slot;
-        if (!u.two || slot) commit(bar(T_EMPTY + st));
-        if (t == T - 1) commit(bar(T_OFULL));
+        ++ops;
+        commit(bar(T_EMPTY + st));
+        if (!u.two) commit(bar(T_EMPTY + st));
+        if (t + 2 >= T) commit(bar(T_OFULL));
         if (t + 2 < T) issue_s(t + 2);
+        if (t + 1 < T) mbar_arrive(bar(T_TURN + (slot ^ 1)));
       }
       g += nt;
       ++units;
