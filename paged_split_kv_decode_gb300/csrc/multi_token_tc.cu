@@ -84,8 +84,7 @@ struct Lay {
   static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;   // one row tile
   static constexpr uint32_t kOffQ = kRingBytes;
   static constexpr uint32_t kOffOut = kOffQ + 2 * kQBytes;     // 32 rows of 128 bytes for each softmax warp
-  static constexpr uint32_t kOffLM = kOffOut + 8 * 32 * 128;   // slot 1's (m, l) of a unit of one row tile
-  static constexpr uint32_t kOffBar = kOffLM + kRows * 8;
+  static constexpr uint32_t kOffBar = kOffOut + 8 * 32 * 128;
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;     // barriers, alignment slack
   static constexpr uint32_t kPCols = NK / 2;                   // 32-bit columns of one P term
   static constexpr uint32_t kSCols = TERMS == 1 ? NK : 96;     // a slot's S, or its P terms if they are wider
@@ -106,17 +105,18 @@ struct Lay {
 enum {
   T_FULL = 0, T_EMPTY = kMaxStages,  // per half-tile: landed (or converted) / its MMAs have read it
   T_RFULL = 2 * kMaxStages, T_REMPTY = 3 * kMaxStages,  // per half-tile of codes: landed / converted
-  T_QFULL = 4 * kMaxStages, T_QFREE, // the unit's Q landed / every S of the unit is done
-  T_SFULL,                           // [2] S of the slot's next op is complete
+  T_QFULL = 4 * kMaxStages,          // [2] the row tile of Q landed
+  T_QFREE = T_QFULL + 2,             // [2] every S that reads it is done
+  T_SFULL = T_QFREE + 2,             // [2] S of the slot's next op is complete
   T_PFULL = T_SFULL + 2,             // [part][2] the part's P is written (4 warps)
   T_HALF = T_PFULL + 4,              // [2] the first part's PV of the slot's op is complete
   T_TURN = T_HALF + 2,               // [2] the MMAs of the other slot's op before are issued
   T_OFULL = T_TURN + 2,              // every PV of the unit is complete
   T_OFREE,                           // the unit's O are read out (8 warps)
-  T_XREADY, T_XFREE,                 // slot 1's (m, l) written / read (4 warps)
-  T_DRAIN, T_SLOT, T_TAIL
+  T_XREADY,                          // [2] the other slot's (m, l) of the rows are there (4 warps)
+  T_DRAIN = T_XREADY + 2, T_SLOT, T_TAIL
 };
-static_assert(T_TAIL * 8 + 12 <= 1024, "barrier area");
+static_assert(T_TAIL * 8 + 16 <= 1024, "barrier area");
 
 struct TCParams {
   const int32_t *page_indices;
@@ -279,6 +279,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap *map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *at) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(at) : "memory");
+}
 __device__ __forceinline__ uint64_t l2_normal_policy() {
   uint64_t pol;
   asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
@@ -339,7 +345,6 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + L::kOffBar);
   uint32_t *tslot = reinterpret_cast<uint32_t *>(bars + T_SLOT);
   int *tail = reinterpret_cast<int *>(bars + T_TAIL);  // what the load warps issued
-  float2 *lm = reinterpret_cast<float2 *>(sm + L::kOffLM);
   auto bar = [&](int i) { return smem_u32(bars + i); };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool has_tree = p.tree != nullptr;
@@ -353,21 +358,31 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       mbar_init(bar(T_RFULL + i), 1);
       mbar_init(bar(T_REMPTY + i), kConvertWarps);
     }
-    mbar_init(bar(T_QFULL), 1);
-    mbar_init(bar(T_QFREE), 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(T_SFULL + i), 1);
       mbar_init(bar(T_PFULL + i), 4);
       mbar_init(bar(T_PFULL + 2 + i), 4);
       mbar_init(bar(T_HALF + i), 1);
       mbar_init(bar(T_TURN + i), 1);
+      mbar_init(bar(T_QFULL + i), 1);
+      mbar_init(bar(T_QFREE + i), 2);
+      mbar_init(bar(T_XREADY + i), 4);
     }
     mbar_init(bar(T_OFULL), 2);
     mbar_init(bar(T_OFREE), 8);
-    mbar_init(bar(T_XREADY), 4);
-    mbar_init(bar(T_XFREE), 4);
     mbar_init(bar(T_DRAIN), 2);
     fence_mbar_init();
+  }
+  if (warp == kKWarp || warp == kVWarp) {
+    // what the first copies need, on its way while the CTA sets up: the tensor maps and page ids
+    const Start &a = req.start[blockIdx.x];
+    const psd_token_request &r = req.r[a.b];
+    const int pos = (a.j * NK + lane * p.sub) / p.page_size;
+    if (lane * p.sub < NK && int64_t(pos) * p.page_size < r.kv_len) prefetch_l2(p.page_indices + r.page_off + pos);
+    if (lane == 0) {
+      prefetch_map(warp == kKWarp ? &tmK : &tmV);
+      if (warp == kKWarp) prefetch_map(&tmQ);
+    }
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tslot)), "r"(512u));
@@ -396,22 +411,28 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     const int n_copies = NK / p.sub;          // a lane each; p.sub tokens of one page
     const uint32_t copy_bytes = FP8 ? uint32_t(p.sub * D) : uint32_t(p.sub / 8) * L::kGroupBytes;
     const int P = p.page_size;
-    int g = 0, units = 0;                     // key tiles and units so far
+    int g = 0, q_next = 0, q_uses0 = 0, q_uses1 = 0;  // key tiles so far; the Q buffers' uses
     bool ok = true, withheld = false;
     while (ok && !withheld && walk.next(u)) {
       if (!is_v) {
-        if (units > 0) ok = wait_all(T_QFREE, uint32_t(units - 1));  // every S of the last unit is done
-        if (!ok) break;
-        const int tiles = 1 + u.two;
-        if (lane == 0) mbar_arrive_expect_tx(bar(T_QFULL), uint32_t(tiles * L::kHalves * p.TH * p.G) * 128u);
-        __syncwarp();
-        if (lane < tiles * L::kHalves) {
-          const int tile = lane / L::kHalves, half = lane % L::kHalves;
-          tma_load_4d(smem_u32(sm + L::kOffQ + tile * L::kQBytes + half * L::kQHalfBytes), &tmQ, 0, u.kv * p.G,
-                      u.r.token0 + u.tok0 + tile * p.TH, half, bar(T_QFULL), pol);
+        // A unit of one row tile uses the Q buffers in turn, so that its Q comes while the unit
+        // before is worked on; a unit of two uses both.
+        const int h0 = u.two ? 0 : q_next;
+        for (int h = h0; h <= h0 + u.two && ok; ++h) {
+          const int uses = h ? q_uses1 : q_uses0;
+          if (uses > 0) ok = wait_all(T_QFREE + h, uint32_t(uses - 1));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(bar(T_QFULL + h), uint32_t(L::kHalves * p.TH * p.G) * 128u);
+          __syncwarp();
+          if (lane < L::kHalves)
+            tma_load_4d(smem_u32(sm + L::kOffQ + h * L::kQBytes + lane * L::kQHalfBytes), &tmQ, 0, u.kv * p.G,
+                        u.r.token0 + u.tok0 + (u.two ? h * p.TH : 0), lane, bar(T_QFULL + h), pol);
+          __syncwarp();
+          if (h) ++q_uses1;
+          else ++q_uses0;
         }
-        __syncwarp();
-        ++units;
+        if (!ok) break;
+        if (!u.two) q_next ^= 1;
       }
       const int n_pages = (u.r.kv_len + P - 1) / P;
       // This lane's copy: the page id of its tokens, fetched a tile ahead of its use.
@@ -453,7 +474,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
     if (lane == 0) {
       tail[is_v] = g;
-      if (!is_v) tail[2] = units;
+      if (!is_v) tail[2] = q_uses0, tail[3] = q_uses1;
     }
   } else if (FP8 && warp >= kConvertWarp) {
     // ------------------------------------------------------ fp8 codes to bf16
@@ -524,6 +545,11 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     // The tiles of an op are waited for before its P, and S(t + 2) follows P V(t) without a wait.
     // A half-tile is released by two commits: one from each slot where both read it, two
     // from the slot that has it alone.
+    // A wait tells a phase of its barrier from the one before, not from the one before that.  So a
+    // thread may wait for a half-tile only when the stage's last half-tile has landed for certain,
+    // also where that was the other slot's: within a unit a stage keeps its slot (or both see
+    // every tile), and between units a thread waits first until every S of the unit before is
+    // done (its K landed), and before its first P V until that unit is read out (its V landed).
     const int slot = warp == kMmaWarp1 ? 1 : 0;
     const uint32_t id_s = idesc_bf16(kRows, NK, false);
     const uint32_t id_pv = idesc_bf16(kRows, D, true);
@@ -536,6 +562,9 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     auto wait = [&](int b, uint32_t parity) { return wait_bounded(bar(b), parity & 1u, p.wait_limit); };
     int g = 0, units = 0;
     uint32_t ops = 0, turns = 0;  // this slot's ops, and turns waited for
+    int q_next = 0;
+    uint32_t q_parity = 0;        // bit h: parity of Q buffer h's uses
+    int h_before = 0;             // the Q buffer of the other slot's S in the unit before
     bool ok = true;
     while (ok && walk.next(u)) {
       const int nt = u.j1 - u.j0, T = u.two ? 2 * nt : nt;
@@ -544,7 +573,12 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         const int i = half_tile(t);
         return wait(T_FULL + i % NS, uint32_t(i / NS));
       };
-      const uint64_t q = qd + ((u.two && slot ? L::kQBytes : 0u) >> 4);
+      const int h = u.two ? slot : q_next;  // the Q buffer
+      const uint64_t q = qd + ((h ? L::kQBytes : 0u) >> 4);
+      auto q_free = [&]() {  // (two commits a use: one from each slot, or both from its only one)
+        commit(bar(T_QFREE + h));
+        if (u.two) commit(bar(T_QFREE + h));
+      };
       auto issue_s = [&](int t) {
         const int st = half_tile(t) % NS;
         const uint64_t b = kd + ((st * L::kTileBytes) >> 4);
@@ -555,22 +589,29 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         commit(bar(T_SFULL + slot));
         commit(bar(T_EMPTY + st));
         if (!u.two) commit(bar(T_EMPTY + st));
-        if (t + 2 >= T) commit(bar(T_QFREE));
+        if (t + 2 >= T) q_free();
       };
-      ok = wait(T_QFULL, uint32_t(units)) && (slot >= T || k_ready(slot));
+      ok = (units == 0 || wait(T_QFREE + h_before, (q_parity >> h_before) ^ 1u)) && wait(T_QFULL + h, q_parity >> h) &&
+           (slot >= T || k_ready(slot));
+      h_before = u.two ? slot ^ 1 : q_next;
       if (!ok) break;
       fence_after();
       if (slot < T) {
         issue_s(slot);
-      } else {  // one key tile: slot 0's
-        commit(bar(T_QFREE));
+      } else {
+        // One key tile, slot 0's.  The unit before is read out first: its phase of T_OFULL must
+        // not take this slot's arrival for slot 0's.
+        if (units > 0 && !(ok = wait(T_OFREE, uint32_t(units - 1)))) break;
+        q_free();
         commit(bar(T_OFULL));
       }
+      q_parity ^= u.two ? 3u : 1u << q_next;
+      if (!u.two) q_next ^= 1;
       for (int t = slot; t < T; t += 2) {
         const int i = half_tile(t) + 1, st = i % NS;
         // K of op t + 2 has a stage that op t or an earlier one freed: no P stands before it
-        ok = wait(T_FULL + st, uint32_t(i / NS)) && (t + 2 >= T || k_ready(t + 2)) &&
-             (t > 1 || units == 0 || wait(T_OFREE, uint32_t(units - 1))) && (t == 0 || wait(T_TURN + slot, turns));
+        ok = (t > 1 || units == 0 || wait(T_OFREE, uint32_t(units - 1))) && wait(T_FULL + st, uint32_t(i / NS)) &&
+             (t + 2 >= T || k_ready(t + 2)) && (t == 0 || wait(T_TURN + slot, turns));
         if (!ok) break;
         if (t > 0) ++turns;
         const uint64_t b = vd + ((st * L::kTileBytes) >> 4);
@@ -835,41 +876,32 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           x[k + 3] = fmaf(y.w, scale, x[k + 3]);
         }
       };
-      const bool joint = !u.two && T > 1;  // the slots have the unit's even and odd tiles: slot 0 joins them
-      float m1 = neg_inf(), l1 = 0.f;
-      if (joint && slot == 1) {
-        if (singles > 0 && !(ok = wait_all(T_XFREE, uint32_t(singles - 1)))) break;
-        if constexpr (TERMS > 1) {
-          // fold the flushed sum into 2^m units, so that slot 0 needs no more than (m, l)
-          if (live && flushed && l != 0.f && keep != 1.f) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 4) {
-              float4 *at = reinterpret_cast<float4 *>(sum_row + c);
-              float4 x = *at;
-              *at = make_float4(x.x * keep, x.y * keep, x.z * keep, x.w * keep);
-            }
-          }
-          __threadfence_block();
-        }
-        lm[r] = make_float2(m, l);
+      // The slots have the even and odd tiles of a unit of one row tile: they tell each other m and
+      // l (and the factor of their flushed sums) through the other's staging rows, and join the two O
+      // of half the columns each.  (Those rows are free: their warp is past its last unit's stores,
+      // which this unit's O waited for, and waits here before its next.)
+      const bool joint = !u.two && T > 1;
+      float m1 = neg_inf(), l1 = 0.f, keep1 = 0.f;
+      if (joint) {
+        if constexpr (TERMS > 1) __threadfence_block();  // sum_row is read by the other slot
+        reinterpret_cast<float4 *>(sm + L::kOffOut + (warp ^ 4) * (32 * 128))[lane] =
+            make_float4(m, l, flushed ? keep : 0.f, 0.f);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(T_XREADY));
-        ++singles;
-      } else if (joint) {
-        if (!(ok = wait_all(T_XREADY, uint32_t(singles)))) break;
-        const float2 other = lm[r];
-        m1 = other.x, l1 = other.y;
+        if (lane == 0) mbar_arrive(bar(T_XREADY + (slot ^ 1)));
+        if (!(ok = wait_all(T_XREADY + slot, uint32_t(singles)))) break;
+        const float4 other = reinterpret_cast<const float4 *>(stage)[lane];
+        m1 = other.x, l1 = other.y, keep1 = other.z;
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(T_XFREE));
         ++singles;
       }
-      if (warp_live && (u.two || slot == 0)) {
+      if (warp_live && (u.two || joint || slot == 0)) {
         const float top = fmaxf(m, m1), from = top == neg_inf() ? 0.f : top;
         const float w0 = ex2(m - from), w1 = ex2(m1 - from);  // 0 where a slot saw no key
         const float all = l * w0 + l1 * w1, inv = all == 0.f ? 0.f : p.v_scale / all;
         const float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
+        const int c_end = joint ? D / 2 * (slot + 1) : D;
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
+        for (int c = joint ? D / 2 * slot : 0; c < c_end; c += 32) {
           float x[32];
           tmem_ld32(lane_base + D * slot + c, reinterpret_cast<uint32_t *>(x));
           ld_wait();
@@ -877,19 +909,19 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           for (int k = 0; k < 32; ++k) x[k] = l == 0.f ? 0.f : x[k] * f0;
           if (joint) {
             uint32_t y[32];
-            tmem_ld32(lane_base + D + c, y);
+            tmem_ld32(lane_base + D * (slot ^ 1) + c, y);
             ld_wait();
 #pragma unroll
             for (int k = 0; k < 32; ++k) x[k] = l1 == 0.f ? x[k] : fmaf(__uint_as_float(y[k]), f1, x[k]);
           }
           if constexpr (TERMS > 1) {
             if (live && flushed && l != 0.f) add_flushed(x, sum_row + c, keep * f0);
-            // (slot 1 flushed if it had more than kFlush ops: every row, its T / 2 ops)
-            if (joint && live && (T >> 1) > kFlush && l1 != 0.f) add_flushed(x, sum_row + kRows * D + c, f1);
+            if (live && keep1 != 0.f && l1 != 0.f)
+              add_flushed(x, sum_row + (slot ? -kRows * D : kRows * D) + c, keep1 * f1);
           }
           put32(x, c);
         }
-        if (live) {
+        if (live && (u.two || slot == 0)) {
           const float v = all == 0.f ? neg_inf() : top + log2f(all);
           if (!whole) p.part_lse[int64_t(piece) * 2 * kRows + row] = v;
           else if (p.lse) p.lse[out] = v;
@@ -920,7 +952,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       if (last >= 0 && !wait_bounded(bar(kLanded + lane), uint32_t(last / NC) & 1u, p.wait_limit))
         bad |= PSD_FAULT_WAIT_TIMEOUT;
     }
-    if (lane == 0 && tail[2] > 0 && !wait_bounded(bar(T_QFULL), uint32_t(tail[2] - 1) & 1u, p.wait_limit))
+    if (lane < 2 && tail[2 + lane] > 0 &&
+        !wait_bounded(bar(T_QFULL + lane), uint32_t(tail[2 + lane] - 1) & 1u, p.wait_limit))
       bad |= PSD_FAULT_WAIT_TIMEOUT;
   }
   if (bad) raise_fault(p.fault, bad);

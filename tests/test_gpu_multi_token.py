@@ -156,6 +156,21 @@ def test_batches_of_several_launches(B):
     _check(Step(rng.integers(0, 3, B), rng.integers(1, 40, B), Hq=2, Hkv=1, seed=B))
 
 
+@pytest.mark.parametrize("kv,D,out_f32", [("bf16", 128, False), ("bf16", 128, True), ("fp8", 128, False), ("bf16", 64, False),
+                                          ("fp8", 64, True)])
+def test_many_long_units_a_cta(kv, D, out_f32):
+    """Several units share a CTA, with odd and even numbers of tiles, and one-tile pieces and units
+    of two row tiles between them: every ring and buffer passes from one to the next."""
+    new = [2, 1, 3, 5, 1, 2, 70, 1, 4, 2, 3, 1, 1, 2]
+    before = [3000, 130, 900, 1500, 2500, 60, 2000, 5, 800, 3900, 257, 1100, 640, 2049]
+    s = Step(new, before, Hq=16, Hkv=8, D=D, page=16, kv=kv, seed=31)
+    first = _run(s, out_f32=out_f32)
+    _check(s, out_f32=out_f32, got=first)
+    for _ in range(5):
+        again = _run(s, out_f32=out_f32)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
 def test_more_keys_pages_repeat():
     """A page listed twice holds its tokens twice."""
     s = Step([2], [78], Hq=2, Hkv=1, seed=15)
