@@ -90,6 +90,12 @@ struct Lay {
   static constexpr uint32_t kSCols = TERMS == 1 ? NK : 96;     // a slot's S, or its P terms if they are wider
   static constexpr uint32_t kColS = 2 * D;                     // after the two O
   static constexpr int kThreads = FP8 ? 20 * 32 : 12 * 32;
+  // What a CTA's time is made of, in quarters of a key tile that waits for memory: the tiles of a
+  // unit of one row tile and of two (at D = 64 the second is bound by its softmax), and what a
+  // unit costs beside its tiles (two of 128 keys, four of 64).
+  // Stretches equal in tiles alone left the CTAs with most units 15 % behind the mean: 63 us for
+  // 32 drafted requests against 55, 71 for fp8 trees against 60.
+  static constexpr int kOneCost = D == 64 && NK == 128 ? 3 : 4, kTwoCost = 4, kUnitCost = NK == 128 ? 8 : 16;
   // Registers a thread: 168 at launch of 384 threads, 96 of 640; the softmax warps hold a
   // part's scores and weights and take what the others do without.
   static constexpr int kLaunchRegs = FP8 ? 96 : 168;
@@ -128,7 +134,6 @@ struct TCParams {
   float *sum_o;     // [CTAs][2 slots][128 rows][D], f32 outputs only
   FaultRef fault;
   int64_t num_pages;
-  int total;        // key tiles of the launch
   int Hq, Hkv, G, TH, page_size, sub, out_f32;
   float q_scale, v_scale;
   uint32_t wait_limit;
@@ -139,6 +144,7 @@ constexpr int kMaxCtas = 192;
 struct Start {
   uint16_t b, kv;  // request, KV head
   int32_t tok0, j; // first token and key tile of the unit
+  int32_t tiles;   // key tiles of the stretch
 };
 struct TCRequests {
   psd_token_request r[kStepRequests];
@@ -162,8 +168,6 @@ __host__ __device__ __forceinline__ int unit_tiles(const psd_token_request &r, i
   return (keys + NK - 1) / NK;
 }
 
-__host__ __device__ __forceinline__ int bound(int c, int total, int ctas) { return int(int64_t(c) * total / ctas); }
-
 // Walks the units of this CTA's stretch.
 template <int NK>
 struct Walk {
@@ -173,7 +177,7 @@ struct Walk {
   bool first = true;
   __device__ Walk(const TCParams &p_, const TCRequests &req_) : p(p_), req(req_) {
     const int c = blockIdx.x;
-    left = bound(c + 1, p.total, gridDim.x) - bound(c, p.total, gridDim.x);
+    left = req.start[c].tiles;
     b = req.start[c].b;
     kv = req.start[c].kv;
     tok0 = req.start[c].tok0;
@@ -1057,49 +1061,83 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   TCRequests req;
   std::memcpy(req.r, sreq.r, sizeof(psd_token_request) * size_t(S.B));
   const bool tree = S.tree != nullptr;
-  int64_t total = 0;
-  int head[kStepRequests];  // key tiles of one KV head of a request
+  // The units on their line, each with its tiles and its cost.
+  auto unit_cost = [&](const psd_token_request &r, int tok0, int n) {
+    return L::kUnitCost + n * (r.num_new - tok0 > p.TH ? L::kTwoCost : L::kOneCost);
+  };
+  int64_t tiles = 0, cost = 0;
+  struct {
+    int64_t tiles, cost;
+  } head[kStepRequests];  // of one KV head of a request
   for (int b = 0; b < S.B; ++b) {
     const psd_token_request &r = req.r[b];
-    int64_t n = 0;
-    for (int t = 0; t < r.num_new; t += 2 * p.TH) n += unit_tiles(r, t, p.TH, L::NK, tree);
-    total += n * S.Hkv;
-    if (total > 0x7fffffffLL)
-      return fail(PSD_ERR_UNSUPPORTED, "multi_token_decode: more than 2^31 key tiles in one launch");
-    head[b] = int(n);
+    head[b] = {0, 0};
+    for (int t = 0; t < r.num_new; t += 2 * p.TH) {
+      const int n = unit_tiles(r, t, p.TH, L::NK, tree);
+      head[b].tiles += n;
+      head[b].cost += unit_cost(r, t, n);
+    }
+    tiles += head[b].tiles * S.Hkv;
+    cost += head[b].cost * S.Hkv;
   }
-  p.total = int(total);
-  const int ctas = int(std::min<int64_t>(total, std::min(place.ctas, kMaxCtas)));
-  // Where the CTAs' stretches begin, and the units that a bound cuts, each named at its first.
+  if (tiles > 0x7fffffffLL) return fail(PSD_ERR_UNSUPPORTED, "multi_token_decode: more than 2^31 key tiles in one launch");
+  // One CTA per SM; a stretch costs at least a tile, so that two bounds inside a unit differ.
+  constexpr int kTile = L::kOneCost > L::kTwoCost ? L::kOneCost : L::kTwoCost;
+  const int ctas = int(std::min<int64_t>({tiles, cost / kTile, place.ctas, kMaxCtas}));
+  // Where the CTAs' stretches begin, and the units that a bound cuts.
   Cuts cuts;
   int n_cuts = 0, most = 0;
   {
-    int b = 0, kv = 0, tok0 = 0, n = unit_tiles(req.r[0], 0, p.TH, L::NK, tree);
-    int64_t base = 0, first = 0;  // tiles before request b and before the unit
-    for (int c = 0; c < ctas; ++c) {
-      const int64_t at = bound(c, p.total, ctas);
-      while (at >= base + int64_t(head[b]) * S.Hkv) base += int64_t(head[b++]) * S.Hkv, first = -1;
-      const int h = int((at - base) / head[b]);
-      if (first < 0 || h != kv) {
-        kv = h, tok0 = 0, first = base + int64_t(h) * head[b];
-        n = unit_tiles(req.r[b], 0, p.TH, L::NK, tree);
+    int b = 0, kv = 0, tok0 = 0, n = 0;          // the unit
+    int64_t at_tile = 0, at_cost = 0;            // tiles and cost before it
+    int64_t req_tile = 0, req_cost = 0;          // before its request
+    int64_t before = 0;                          // the tile at which the CTA before begins
+    bool cut = false;                            // the unit is in `cuts` already
+    auto enter = [&](int kv_, int tok0_) {
+      kv = kv_, tok0 = tok0_, n = unit_tiles(req.r[b], tok0, p.TH, L::NK, tree);
+      cut = false;
+    };
+    enter(0, 0);
+    for (int c = 0; c <= ctas; ++c) {
+      const int64_t at = c * cost / ctas;
+      int64_t tile = tiles;
+      if (c < ctas) {
+        bool moved = false;
+        while (at >= req_cost + head[b].cost * S.Hkv) {
+          req_tile += head[b].tiles * S.Hkv;
+          req_cost += head[b].cost * S.Hkv;
+          ++b, moved = true;
+        }
+        const int h = int((at - req_cost) / head[b].cost);
+        if (moved || h != kv) {
+          at_tile = req_tile + h * head[b].tiles;
+          at_cost = req_cost + h * head[b].cost;
+          enter(h, 0);
+        }
+        while (at >= at_cost + unit_cost(req.r[b], tok0, n)) {
+          at_tile += n;
+          at_cost += unit_cost(req.r[b], tok0, n);
+          enter(kv, tok0 + 2 * p.TH);
+        }
+        const psd_token_request &r = req.r[b];
+        const int per = r.num_new - tok0 > p.TH ? L::kTwoCost : L::kOneCost;
+        const int j = int(std::max<int64_t>(0, (at - at_cost - L::kUnitCost) / per));
+        tile = at_tile + j;
+        req.start[c] = Start{uint16_t(b), uint16_t(kv), tok0, j, 0};
+        if (j > 0 && !cut) {  // CTA c - 1 has the first piece
+          cut = true;
+          Cut &u = cuts.c[n_cuts++];
+          u.out = (int64_t(r.token0) + tok0) * S.Hq + int64_t(kv) * S.G;
+          u.rows = int16_t(std::min(r.num_new - tok0, 2 * p.TH) * S.G);
+          u.first = int16_t(c - 1);
+          u.late = before < at_tile;
+          u.n = 1;
+          most = std::max(most, int(u.rows));
+        }
+        if (j > 0) ++cuts.c[n_cuts - 1].n;
       }
-      while (at >= first + n) {
-        first += n, tok0 += 2 * p.TH;
-        n = unit_tiles(req.r[b], tok0, p.TH, L::NK, tree);
-      }
-      req.start[c] = Start{uint16_t(b), uint16_t(kv), tok0, int32_t(at - first)};
-      // cut here, and not at a bound before?
-      if (at == first || (c > 0 && bound(c - 1, p.total, ctas) > first)) continue;
-      const psd_token_request &r = req.r[b];
-      Cut &u = cuts.c[n_cuts++];
-      u.out = (int64_t(r.token0) + tok0) * S.Hq + int64_t(kv) * S.G;
-      u.rows = int16_t(std::min(r.num_new - tok0, 2 * p.TH) * S.G);
-      u.first = int16_t(c - 1);
-      u.late = bound(c - 1, p.total, ctas) < first;
-      u.n = 1;
-      while (c - 1 + u.n < ctas && bound(c - 1 + u.n, p.total, ctas) < first + n) ++u.n;
-      most = std::max(most, int(u.rows));
+      if (c > 0) req.start[c - 1].tiles = int32_t(tile - before);
+      before = tile;
     }
   }
   p.part_o = place.part_o;
