@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     uint32_t ops = 0, turns = 0;  // this slot's ops, and turns waited for
     int q_next = 0;
     uint32_t q_parity = 0;        // bit h: parity of Q buffer h's uses
-    int h_before = 0;             // the Q buffer of the other slot's S in the unit before
+    int h_before = 0;             // a Q buffer of the unit before
     bool ok = true;
     while (ok && walk.next(u)) {
       const int nt = u.j1 - u.j0, T = u.two ? 2 * nt : nt;
@@ -579,9 +579,11 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       };
       const int h = u.two ? slot : q_next;  // the Q buffer
       const uint64_t q = qd + ((h ? L::kQBytes : 0u) >> 4);
-      auto q_free = [&]() {  // (two commits a use: one from each slot, or both from its only one)
+      // Each slot's commit, to every buffer of the unit: a buffer's phase then needs both slots, and
+      // neither can run two phases ahead of the other's wait below.
+      auto q_free = [&]() {
         commit(bar(T_QFREE + h));
-        if (u.two) commit(bar(T_QFREE + h));
+        if (u.two) commit(bar(T_QFREE + (h ^ 1)));
       };
       auto issue_s = [&](int t) {
         const int st = half_tile(t) % NS;
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       };
       ok = (units == 0 || wait(T_QFREE + h_before, (q_parity >> h_before) ^ 1u)) && wait(T_QFULL + h, q_parity >> h) &&
            (slot >= T || k_ready(slot));
-      h_before = u.two ? slot ^ 1 : q_next;
+      h_before = h;
       if (!ok) break;
       fence_after();
       if (slot < T) {

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import paged_split_kv_decode_gb300 as psd
+from oracle import tokens as TK
 from _gpu_util import ctx
 from _tokens_util import Step, bounds
 
@@ -169,6 +170,29 @@ def test_many_long_units_a_cta(kv, D, out_f32):
     for _ in range(5):
         again = _run(s, out_f32=out_f32)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("D,kv,out_f32", [(64, "bf16", False), (128, "bf16", False), (64, "fp8", False), (128, "bf16", True)])
+def test_many_short_prompts(D, kv, out_f32):
+    """Units of two row tiles and one key tile, many to a CTA, with others between them."""
+    rng = np.random.default_rng(D)
+    new = [int(x) for x in rng.integers(33, 65, 60)]
+    before = [int(x) for x in rng.integers(0, 40, 60)]
+    new[10], before[10], new[40], before[40] = 2, 70, 1, 300
+    s = Step(new, before, Hq=32, Hkv=8, D=D, page=8, kv=kv, seed=33)
+    first = _run(s, out_f32=out_f32)
+    for _ in range(30):
+        again = _run(s, out_f32=out_f32)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    keep = [0, 9, 10, 11, 39, 40, 41, 59]                 # the oracle looks at some of the requests
+    o, lse = (x.double().cpu().numpy() for x in first)
+    for b in keep:
+        lo, hi = int(s.q_indptr[b]), int(s.q_indptr[b + 1])
+        pages = s.page_indices[s.page_indptr[b]: s.page_indptr[b + 1]]
+        want = TK.attend(s.q[lo:hi].double().numpy(), s.values(s.k, s.scales[0]), s.values(s.v, s.scales[1]), [0, hi - lo],
+                         [s.total[b]], [0, len(pages)], pages, s.page, s.sm_scale)
+        e_o, e_l = bounds(want, D, int(s.total[b]), out_f32, 3 if out_f32 else 1)
+        assert bool((np.abs(o[lo:hi] - want[0]) <= e_o).all()) and bool((np.abs(lse[lo:hi] - want[1]) <= e_l).all())
 
 
 def test_more_keys_pages_repeat():
