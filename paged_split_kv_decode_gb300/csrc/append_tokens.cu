@@ -388,7 +388,7 @@ static psd_status launch_append_tokens(const psd_append_args *a, cudaStream_t s)
   const bool vec = a->rot_dim % 16 == 0 && a->rot_col % 8 == 0 && a->D % 8 == 0 && a->Dv % 8 == 0 &&
                    fits(a->q, a->Hq ? a->q_stride : 0) && fits(a->k, a->k_stride) && fits(a->v, a->Dv ? a->v_stride : 0) &&
                    aligned16(a->q_out) && aligned16(a->k_pool) && aligned16(a->v_pool);
-  constexpr int kMany = 4;
+  constexpr int kMany = 2;
   if (!vec) append_tokens_kernel<<<a->num_tokens, 256, 0, s>>>(p, turns);
   else if (a->num_tokens < 2048) append_tokens_vec_kernel<1><<<a->num_tokens, 256, 0, s>>>(p, turns);
   else append_tokens_vec_kernel<kMany><<<(a->num_tokens - 1) / kMany + 1, 256, 0, s>>>(p, turns);

@@ -981,47 +981,48 @@ struct Cuts {
   Cut c[kMaxCtas - 1];
 };
 
-// Joins the pieces of the cut units (blockIdx.x), in key order: a warp per row.  The host
+// Joins the pieces of the cut units (blockIdx.x), in key order: LANES lanes a row.  The host
 // names them: found by a walk on the device, as the main kernel's stretches are, they cost
-// 47 us behind a 4096-token prompt against 17.
-template <int D>
+// 30 us more behind a 4096-token prompt.
+template <int D, int LANES>
 __global__ void __launch_bounds__(256) step_join_kernel(const TCParams p, const __grid_constant__ Cuts cuts) {
+  constexpr int kCols = D / LANES;  // of a row, a lane: chunks of 4, LANES chunks apart
   const Cut &u = cuts.c[blockIdx.x];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + warp;
-  if (row >= u.rows) return;
+  const int lane = threadIdx.x % LANES, row = blockIdx.y * (256 / LANES) + threadIdx.x / LANES;
   wait_for_prior_grid();
-  auto at = [&](int i) { return int64_t(2 * (u.first + i) + (i == 0 ? u.late : 0)) * 2 * kRows + row; };
+  const bool live = row < u.rows;
+  auto at = [&](int i) {
+    return int64_t(2 * (u.first + i) + (i == 0 ? u.late : 0)) * 2 * kRows + (live ? row : 0);
+  };
   float m = neg_inf();
-  for (int i = lane; i < u.n; i += 32) m = fmaxf(m, p.part_lse[at(i)]);
+  for (int i = lane; i < u.n; i += LANES) m = fmaxf(m, p.part_lse[at(i)]);
 #pragma unroll
-  for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  for (int x = LANES / 2; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float from = m == neg_inf() ? 0.f : m;
-  float x[D / 32] = {}, sum = 0.f;
-#pragma unroll 4
+  float x[kCols] = {}, sum = 0.f;
+#pragma unroll 2
   for (int i = 0; i < u.n; ++i) {
     const float s = p.part_lse[at(i)], w = ex2(s - from);
-    const float *src = p.part_o + at(i) * D + lane * (D / 32);
+    const float *src = p.part_o + at(i) * D + 4 * lane;
     sum += w;
-    float y[D / 32];
-    if constexpr (D == 128) *reinterpret_cast<float4 *>(y) = *reinterpret_cast<const float4 *>(src);
-    else *reinterpret_cast<float2 *>(y) = *reinterpret_cast<const float2 *>(src);
+    float y[kCols];
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) x[k] = s == neg_inf() ? x[k] : fmaf(w, y[k], x[k]);
+    for (int k = 0; k < kCols; k += 4)
+      *reinterpret_cast<float4 *>(y + k) = *reinterpret_cast<const float4 *>(src + LANES * k);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) x[k] = s == neg_inf() ? x[k] : fmaf(w, y[k], x[k]);
   }
+  if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-  for (int k = 0; k < D / 32; ++k) x[k] *= inv;
   const int64_t out = u.out + int64_t(row / p.G) * p.Hq + row % p.G;
-  const int64_t o = out * D + lane * (D / 32);
-  if (p.out_f32) {
-    float *dst = static_cast<float *>(p.o) + o;
-    if constexpr (D == 128) *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-    else *reinterpret_cast<float2 *>(dst) = make_float2(x[0], x[1]);
-  } else {
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.o) + o);
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k) dst[k] = bf16x2_bits(x[2 * k], x[2 * k + 1]);
+  for (int k = 0; k < kCols; k += 4) {
+    const int64_t o = out * D + 4 * lane + LANES * k;
+    const float4 y = make_float4(x[k] * inv, x[k + 1] * inv, x[k + 2] * inv, x[k + 3] * inv);
+    if (p.out_f32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(p.o) + o) = y;
+    else
+      *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.o) + o) = make_uint2(bf16x2_bits(y.x, y.y), bf16x2_bits(y.z, y.w));
   }
   if (lane == 0 && p.lse) p.lse[out] = sum == 0.f ? neg_inf() : m + log2f(sum);
 }
@@ -1185,7 +1186,13 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode launch: %s", cudaGetErrorString(e));
   if (n_cuts == 0) return PSD_OK;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(n_cuts), unsigned((most + 7) / 8));
+  // Few rows have many pieces and want lanes, many rows have two and want loads in flight: 32 lanes a
+  // row against 8 took 6.3 us against 8.6 for 4 rows of 24 units in six pieces each, 4.4 against 4.9
+  // for 20 rows of 132 units, the same for 96 of 103, and 12.5 against 10 for 256 of 128.
+  const bool few = most <= 32;
+  constexpr int kWide = D / 4, kNarrow = 8;  // lanes a row
+  const int rows = 256 / (few ? kWide : kNarrow);
+  cfg.gridDim = dim3(unsigned(n_cuts), unsigned((most + rows - 1) / rows));
   cfg.blockDim = dim3(256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1193,7 +1200,8 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, step_join_kernel<D>, p, cuts);
+  e = few ? cudaLaunchKernelEx(&cfg, step_join_kernel<D, kWide>, p, cuts)
+          : cudaLaunchKernelEx(&cfg, step_join_kernel<D, kNarrow>, p, cuts);
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode join launch: %s", cudaGetErrorString(e));
   return PSD_OK;
 }
