@@ -1,14 +1,15 @@
 // Attention of several new tokens a request on the 5th-generation tensor cores
-// (tcgen05.mma kind::f16: bf16 operands, f32 accumulators in TMEM).
+// (tcgen05.mma kind::f16: bf16 operands, f16 with fp8 pools; f32 accumulators in TMEM).
 //
 // Rows.  The G query heads of one KV head and the request's new tokens are stacked
 // token-major into row tiles of TH = floor(128 / G) tokens (TH * G <= 128 TMEM lanes), so
 // every K/V element crosses into shared memory once for up to 256 rows.  A unit is one
 // (request, KV head, one or two row tiles); its work is its key tiles of NK tokens.
 //
-// Split.  The key tiles of all units lie on one line, kv head by kv head, and CTA c of
-// the launch takes the stretch [c N / C, (c + 1) N / C): every SM gets the same number of
-// tiles whatever the lengths, with one CTA per SM and no second wave.  A stretch that
+// Split.  The key tiles of all units lie on one line, request by request and KV head by KV
+// head, and each CTA takes a stretch of it that costs the same (a unit costs some tiles beside
+// its own: Lay): every SM gets its share whatever the lengths, with one CTA per SM and no
+// second wave.  The host finds where the stretches begin.  A stretch that
 // holds a whole unit writes its output; a piece of a unit writes a normalised partial
 // and its LSE to the workspace (at most two pieces a CTA, so the workspace does not
 // grow with the batch), and a second kernel joins the pieces of each split unit in key
@@ -18,12 +19,12 @@
 // the slot's warpgroup has turned S into P, O += P V; while one slot's rows take their
 // softmax the other slot's MMAs run.  A unit of two row tiles gives each slot one of them
 // (op 2j and 2j + 1 share key tile j); a unit of one row tile gives the slots its even and
-// odd key tiles, with an O, maximum and sum each, joined when the unit ends.  The MMA warp
-// issues S(t + 2) right after P V(t): they use the same TMEM columns (P lies over S), and
-// MMAs of one CTA execute in issue order.
+// odd key tiles, with an O, maximum and sum each, joined when the unit ends.  Each slot has an
+// MMA thread, which issues S(t + 2) right after P V(t): they use the same TMEM columns (P lies
+// over S), and a thread's MMAs execute in issue order.
 // A tile's P goes in parts of 64 keys, so that PV of the first runs while the second is made.
 //   TMEM (512 columns): per slot S [128 x NK] f32 with P over it, and O [128 x D] f32.
-//   Shared memory: two row tiles of Q, a ring of K and V half-tiles (K, V, K, V, ...).
+//   Shared memory: two row tiles of Q (fp8 pools: none), a ring of K and V half-tiles (K, V, ...).
 //   Warps: 0-3 softmax of slot 0, 4-7 of slot 1 (thread = row = TMEM lane), 8 and 11 (one
 //   thread each) the MMAs of the slots, 9 loads Q and K, 10 loads V.
 //
@@ -32,18 +33,26 @@
 // 128-byte-swizzle atoms: one copy carries a whole head row (both halves at D = 128) of up
 // to 128 slots of a page.  Page positions past the request's pages load as zeros.
 //
-// fp8 pools: the copies bring codes (swizzled rows of a head) into a ring of their own, and eight more warps
-// (12-19) turn them into bf16 tiles of 64 keys in the layout above, half-tile by half-tile.
+// fp8 pools: the copies bring codes (swizzled rows of a head) into a ring of their own, and eight more
+// warps (12-19) turn them into f16 tiles of 64 keys in the layout above, half-tile by half-tile: one
+// conversion for two codes, where bf16 takes four.  Q lies in TMEM, D / 2 columns a slot, written by
+// the softmax warps as f16 scaled row by row: S of 64 keys reads K alone from shared memory, which
+// copies, conversion and MMAs otherwise fill.  With bf16 operands and Q in shared memory 16 requests'
+// trees of 9 to 24 tokens over 512 to 8192 keys took 61 us against 54.  (K's codes taken as they are by
+// kind::f8f6f4, against Q in two e4m3 terms, were no faster.)
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
 // terms of NK keys need 3 NK / 2 columns, which is why f32 outputs take tiles of 64 keys.
+// With fp8 pools the terms are f16: one (2^-11) or two (2^-22; with O, S and Q there is no room
+// for a third), and P's scale is 2^7 higher, so that what f16 loses at its low end is 2^-32 of
+// the row's largest P.
 // The tensor cores' f32 accumulation cuts low bits at every step of 16 keys and term, always
 // towards zero: over 8000 keys it cost 1.3e-5 of the result's norm.  bf16 outputs do not
 // see that; for f32 outputs O starts anew every kFlush ops of a slot, and the rows add what
 // they read out to a sum in the workspace, rounded to nearest.
 // The row maximum follows lazily: O and l are rescaled only when it grows by more than
-// 2^8, so P <= 2^8.
+// 2^8, so P <= 2^8 (2^15 as f16).
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
@@ -76,33 +85,36 @@ struct Lay {
   static constexpr uint32_t kGroupBytes = kHalves * 1024;      // 8 slots of one head
   static constexpr uint32_t kTileBytes = NK / 8 * kGroupBytes; // K or V of a tile
   static constexpr uint32_t kRawBytes = NK * D;                // its fp8 codes
-  // half-tiles in the ring; with fp8 pools it shares its space with a ring of codes
-  static constexpr int kStages = int((FP8 ? kRingBytes / 2 : kRingBytes) / kTileBytes);
-  static constexpr int kRaw = FP8 ? int(kRingBytes / 2 / kRawBytes) : 0;
+  // half-tiles in the ring; fp8 pools have a ring of codes beside it
+  static constexpr int kStages = FP8 ? 8 : int(kRingBytes / kTileBytes);
+  static constexpr int kRaw = FP8 ? (D == 64 ? 16 : 8) : 0;
   static constexpr uint32_t kOffRaw = kStages * kTileBytes;
   static constexpr uint32_t kQHalfBytes = kRows * 128;
   static constexpr uint32_t kQBytes = kHalves * kQHalfBytes;   // one row tile
-  static constexpr uint32_t kOffQ = kRingBytes;
-  static constexpr uint32_t kOffOut = kOffQ + 2 * kQBytes;     // 32 rows of 128 bytes for each softmax warp
+  static constexpr uint32_t kOffQ = kOffRaw + kRaw * kRawBytes;
+  static constexpr uint32_t kOffOut = kOffQ + (FP8 ? 0 : 2 * kQBytes);  // 32 rows of 128 bytes for each softmax warp
   static constexpr uint32_t kOffBar = kOffOut + 8 * 32 * 128;
   static constexpr uint32_t kSmem = kOffBar + 1024 + 1024;     // barriers, alignment slack
   static constexpr uint32_t kPCols = NK / 2;                   // 32-bit columns of one P term
-  static constexpr uint32_t kSCols = TERMS == 1 ? NK : 96;     // a slot's S, or its P terms if they are wider
+  static constexpr uint32_t kSCols = TERMS == 3 ? 96 : NK;     // a slot's S, or its P terms if they are wider
   static constexpr uint32_t kColS = 2 * D;                     // after the two O
+  static constexpr uint32_t kColQ = kColS + 2 * kSCols;        // fp8 pools: a slot's Q, D / 2 columns
+  // P = 2^(s - m) with the row's top at 2^kBias: f16 holds P down to 2^-31 of it.
+  static constexpr float kBias = FP8 ? 7.f : 0.f;
   static constexpr int kThreads = FP8 ? 20 * 32 : 12 * 32;
   // What a CTA's time is made of, in quarters of a key tile that waits for memory: the tiles of a
   // unit of one row tile and of two (at D = 64 the second is bound by its softmax), and what a
-  // unit costs beside its tiles (two of 128 keys, four of 64).
+  // unit costs beside its tiles (two of 128 keys, four of 64; twelve where Q comes through registers).
   // Stretches equal in tiles alone left the CTAs with most units 15 % behind the mean: 63 us for
-  // 32 drafted requests against 55, 71 for fp8 trees against 60.
-  static constexpr int kOneCost = D == 64 && NK == 128 ? 3 : 4, kTwoCost = 4, kUnitCost = NK == 128 ? 8 : 16;
+  // 32 drafted requests against 54; fp8 trees take 65 with 16 quarters a unit, 54 with 48.
+  static constexpr int kOneCost = D == 64 && NK == 128 ? 3 : 4, kTwoCost = 4, kUnitCost = NK == 128 ? 8 : FP8 ? 48 : 16;
   // Registers a thread: 168 at launch of 384 threads, 96 of 640; the softmax warps hold a
   // part's scores and weights and take what the others do without.
   static constexpr int kLaunchRegs = FP8 ? 96 : 168;
   static constexpr int kSoftmaxRegs = FP8 ? 144 : 208, kOtherRegs = FP8 ? 64 : 88;
   static_assert(256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs <= kThreads * kLaunchRegs, "registers of the launch");
   static_assert(TERMS * kPCols <= kSCols && NK <= int(kSCols), "S region");
-  static_assert(kColS + 2 * kSCols <= 512, "TMEM columns");
+  static_assert(kColQ + (FP8 ? D : 0) <= 512, "TMEM columns");
   static_assert(kStages >= 4 && kStages <= kMaxStages && kRaw <= kMaxStages, "S runs two tiles ahead of PV");
   static_assert(kSmem <= 227u * 1024u, "shared memory");
   static_assert(kTileBytes % 1024 == 0, "128-byte-swizzle atoms");
@@ -111,7 +123,7 @@ struct Lay {
 enum {
   T_FULL = 0, T_EMPTY = kMaxStages,  // per half-tile: landed (or converted) / its MMAs have read it
   T_RFULL = 2 * kMaxStages, T_REMPTY = 3 * kMaxStages,  // per half-tile of codes: landed / converted
-  T_QFULL = 4 * kMaxStages,          // [2] the row tile of Q landed
+  T_QFULL = 4 * kMaxStages,          // [2] the row tile of Q landed; fp8 pools: the slot's is written (4 warps)
   T_QFREE = T_QFULL + 2,             // [2] every S that reads it is done
   T_SFULL = T_QFREE + 2,             // [2] S of the slot's next op is complete
   T_PFULL = T_SFULL + 2,             // [part][2] the part's P is written (4 warps)
@@ -127,6 +139,8 @@ static_assert(T_TAIL * 8 + 16 <= 1024, "barrier area");
 struct TCParams {
   const int32_t *page_indices;
   const uint64_t *tree;
+  const __nv_bfloat16 *q;
+  int64_t q_stride;  // elements between tokens
   void *o;
   float *lse;
   float *part_o;    // [CTAs][2][2 * 128 rows][D]
@@ -211,9 +225,9 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
   return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t((lbo >> 4) & 0x3FFFu) << 16) |
          (uint64_t((sbo >> 4) & 0x3FFFu) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
-// kind::f16: f32 accumulate, bf16 A and B, A K-major, B K-major or (b_mn) MN-major.
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool b_mn) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
+// kind::f16: f32 accumulate, A and B both bf16 or both f16, A K-major, B K-major or (b_mn) MN-major.
+__host__ __device__ constexpr uint32_t idesc_16bit(bool bf16, int M, int N, bool b_mn) {
+  return (1u << 4) | (uint32_t(bf16) << 7) | (uint32_t(bf16) << 10) | (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) |
          (uint32_t(M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
@@ -301,15 +315,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {  // NaN opera
   return d;
 }
 
-// 16 e4m3 codes to bf16, exactly, through f16 and f32.  (Setting the code's bits into bf16 and
-// multiplying by 2^120 is twice as slow: 40 half-rate integer steps against 8 conversions.)
-__device__ __forceinline__ void codes_to_bf16(const uint4 &codes, uint32_t (&out)[8]) {
+// 16 e4m3 codes to f16, exactly.
+__device__ __forceinline__ void codes_to_f16(const uint4 &codes, uint32_t (&out)[8]) {
   const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 f = e4m3x2_to_float2(w[i >> 1] >> (16 * (i & 1)));
-    out[i] = bf16x2_bits(f.x, f.y);
-  }
+  for (int i = 0; i < 4; ++i)
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(out[2 * i]), "=r"(out[2 * i + 1])
+        : "r"(w[i]));
+}
+__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Two values of P as the MMAs take them, and back.
+template <bool F16>
+__device__ __forceinline__ uint32_t p_bits(float lo, float hi) {
+  return F16 ? f16x2_bits(lo, hi) : bf16x2_bits(lo, hi);
+}
+template <bool F16>
+__device__ __forceinline__ float2 p_values(uint32_t w) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+  else return make_float2(bf16_lo(w), bf16_hi(w));
 }
 
 // Waits for phase `parity` of the barrier, at most `limit` cycles.  The kernel's waits are many
@@ -368,7 +396,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       mbar_init(bar(T_PFULL + 2 + i), 4);
       mbar_init(bar(T_HALF + i), 1);
       mbar_init(bar(T_TURN + i), 1);
-      mbar_init(bar(T_QFULL + i), 1);
+      mbar_init(bar(T_QFULL + i), FP8 ? 4 : 1);
       mbar_init(bar(T_QFREE + i), 2);
       mbar_init(bar(T_XREADY + i), 4);
     }
@@ -385,7 +413,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     if (lane * p.sub < NK && int64_t(pos) * p.page_size < r.kv_len) prefetch_l2(p.page_indices + r.page_off + pos);
     if (lane == 0) {
       prefetch_map(warp == kKWarp ? &tmK : &tmV);
-      if (warp == kKWarp) prefetch_map(&tmQ);
+      if (!FP8 && warp == kKWarp) prefetch_map(&tmQ);
     }
   }
   if (warp == kMmaWarp) {
@@ -414,11 +442,11 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     const uint64_t pol = l2_normal_policy();
     const int n_copies = NK / p.sub;          // a lane each; p.sub tokens of one page
     const uint32_t copy_bytes = FP8 ? uint32_t(p.sub * D) : uint32_t(p.sub / 8) * L::kGroupBytes;
-    const int P = p.page_size;
+    const int P = p.page_size, pages_a_tile = NK / P, rest_a_tile = NK % P;
     int g = 0, q_next = 0, q_uses0 = 0, q_uses1 = 0;  // key tiles so far; the Q buffers' uses
     bool ok = true, withheld = false;
     while (ok && !withheld && walk.next(u)) {
-      if (!is_v) {
+      if (!FP8 && !is_v) {
         // A unit of one row tile uses the Q buffers in turn, so that its Q comes while the unit
         // before is worked on; a unit of two uses both.
         const int h0 = u.two ? 0 : q_next;
@@ -439,18 +467,27 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         if (!u.two) q_next ^= 1;
       }
       const int n_pages = (u.r.kv_len + P - 1) / P;
-      // This lane's copy: the page id of its tokens, fetched a tile ahead of its use.
-      auto page_id = [&](int j) {
-        const int pos = (j * NK + lane * p.sub) / P;
-        return lane < n_copies && j < u.j1 && pos < n_pages ? __ldg(p.page_indices + u.r.page_off + pos) : -1;
+      // This lane's copy: its page of the tile and the token in it, a tile at a time without a division,
+      // and page ids fetched two tiles ahead.
+      int pos = (u.j0 * NK + lane * p.sub) / P, off = u.j0 * NK + lane * p.sub - pos * P;
+      int ahead = pos, ahead_off = off;
+      auto step = [&](int &page, int &at) {
+        page += pages_a_tile;
+        at += rest_a_tile;
+        if (at >= P) at -= P, ++page;
       };
-      int id = page_id(u.j0);
+      auto next_id = [&]() {
+        const int id = lane < n_copies && ahead < n_pages ? __ldg(p.page_indices + u.r.page_off + ahead) : -1;
+        step(ahead, ahead_off);
+        return id;
+      };
+      int id = next_id(), id_next = next_id();
       for (int j = u.j0; j < u.j1; ++j, ++g) {
         if (j >= p.withhold_from) {
           withheld = true;
           break;
         }
-        const int id_next = page_id(j + 1);
+        const int id_after = next_id();
         const int i = 2 * g + (is_v ? 1 : 0), st = i % NC;
         if (i >= NC && !wait_all(kFreed + st, uint32_t(i / NC - 1))) {
           ok = false;
@@ -459,11 +496,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(bar(kLanded + st), kCopied);
         __syncwarp();
         if (lane < n_copies) {
-          const int tok = j * NK + lane * p.sub, pos = tok / P;
           const bool there = pos < n_pages && id >= 0 && int64_t(id) < p.num_pages;
           if (pos < n_pages && !there) bad |= PSD_FAULT_PAGE_ID;
           // the first token slot; not there: wholly outside the view, which reads as zeros
-          const int64_t first = there ? int64_t(id) * P + (tok - pos * P) : -1024;
+          const int64_t first = there ? int64_t(id) * P + off : -1024;
           if constexpr (FP8)
             tma_load_3d(smem_u32(sm + L::kOffRaw + st * kCopied + lane * copy_bytes), map, 0, u.kv, int(first),
                         bar(kLanded + st), pol);
@@ -472,7 +508,9 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                         bar(kLanded + st), pol);
         }
         __syncwarp();
+        step(pos, off);
         id = id_next;
+        id_next = id_after;
       }
     }
     if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
@@ -481,7 +519,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       if (!is_v) tail[2] = q_uses0, tail[3] = q_uses1;
     }
   } else if (FP8 && warp >= kConvertWarp) {
-    // ------------------------------------------------------ fp8 codes to bf16
+    // ------------------------------------------------------- fp8 codes to f16
     // Four warps take the K half-tiles and four the V, in the order of the ring: 16 codes a thread
     // and step, exact (the scales are in the scores' and the output's factors), into the
     // swizzled layout the MMAs read.  V rows past the request's last token become zeros.
@@ -501,7 +539,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         uint8_t *dst = sm + st * L::kTileBytes;
         const int left = v ? u.r.kv_len - j * NK : NK;
         // A warp's step: 8 tokens, 4 chunks of 16 codes each; 8 lanes that move together have the 8
-        // tokens of a swizzle atom, codes and bf16, and so 8 different banks.
+        // tokens of a swizzle atom, codes and f16, and so 8 different banks.
         constexpr int kSteps = NK * D / 16 / 128;
         const int step0 = (th >> 5) * kSteps;
         auto place = [&](int c, int &tk, int &chunk) {
@@ -521,7 +559,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           int tk, chunk;
           place(c, tk, chunk);
           uint32_t out[8];
-          codes_to_bf16(w[c], out);
+          codes_to_f16(w[c], out);
           if (tk >= left) {
 #pragma unroll
             for (int y = 0; y < 8; ++y) out[y] = 0u;
@@ -555,14 +593,15 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     // every tile), and between units a thread waits first until every S of the unit before is
     // done (its K landed), and before its first P V until that unit is read out (its V landed).
     const int slot = warp == kMmaWarp1 ? 1 : 0;
-    const uint32_t id_s = idesc_bf16(kRows, NK, false);
-    const uint32_t id_pv = idesc_bf16(kRows, D, true);
+    const uint32_t id_s = idesc_16bit(!FP8, kRows, NK, false);
+    const uint32_t id_pv = idesc_16bit(!FP8, kRows, D, true);
     // Q: 8-row groups 1024 B apart.  K (K-major): 8-token groups kGroupBytes apart, a half 1024 B
     // further.  V (MN-major): 64-column atoms 1024 B apart, 8-token groups kGroupBytes apart.
     const uint64_t qd = desc_sw128(smem_u32(sm + L::kOffQ), 16, 1024);
     const uint64_t kd = desc_sw128(smem_u32(sm), 16, L::kGroupBytes);
     const uint64_t vd = desc_sw128(smem_u32(sm), 1024, L::kGroupBytes);
     const uint32_t d = tmem + D * slot, sp = tmem + L::kColS + slot * L::kSCols;  // O; S and P
+    const uint32_t qt = tmem + L::kColQ + slot * (D / 2);  // fp8 pools: Q
     auto wait = [&](int b, uint32_t parity) { return wait_bounded(bar(b), parity & 1u, p.wait_limit); };
     int g = 0, units = 0;
     uint32_t ops = 0, turns = 0;  // this slot's ops, and turns waited for
@@ -589,15 +628,18 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         const int st = half_tile(t) % NS;
         const uint64_t b = kd + ((st * L::kTileBytes) >> 4);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss(sp, q + (((k >> 2) * L::kQHalfBytes + (k & 3) * 32) >> 4), b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4),
-                 id_s, k > 0);
+        for (int k = 0; k < D / 16; ++k) {
+          const uint64_t bk = b + (((k >> 2) * 1024 + (k & 3) * 32) >> 4);
+          if constexpr (FP8) mma_ts(sp, qt + 8 * k, bk, id_s, k > 0);
+          else mma_ss(sp, q + (((k >> 2) * L::kQHalfBytes + (k & 3) * 32) >> 4), bk, id_s, k > 0);
+        }
         commit(bar(T_SFULL + slot));
         commit(bar(T_EMPTY + st));
         if (!u.two) commit(bar(T_EMPTY + st));
         if (t + 2 >= T) q_free();
       };
-      ok = (units == 0 || wait(T_QFREE + h_before, (q_parity >> h_before) ^ 1u)) && wait(T_QFULL + h, q_parity >> h) &&
+      ok = (units == 0 || wait(T_QFREE + h_before, (q_parity >> h_before) ^ 1u)) && 
+           (FP8 ? wait(T_QFULL + slot, uint32_t(units)) : wait(T_QFULL + h, q_parity >> h)) &&
            (slot >= T || k_ready(slot));
       h_before = h;
       if (!ok) break;
@@ -657,8 +699,62 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     const int slot = warp >> 2, r = tid & 127;       // row of the tile = TMEM lane
     const uint32_t lane_base = tmem + (uint32_t(32 * (warp & 3)) << 16);
     const uint32_t s_col = lane_base + L::kColS + slot * L::kSCols;
-    const float qs = p.q_scale;
+    [[maybe_unused]] float qs = p.q_scale;
     const int rt = r / p.G, rg = r - rt * p.G;        // token of the tile, head of the group
+    // fp8 pools: the row's Q of a unit as f16, times the power of two that puts its top in [2^14, 2^15):
+    // exact but for elements 2^-31 below the top.  Returns the row's score factor.
+    auto q_row = [&](const Unit &v, bool &there) {
+      const int t = v.tok0 + (v.two && slot ? p.TH : 0) + rt;
+      there = rt < p.TH && t < v.r.num_new;
+      return reinterpret_cast<const uint4 *>(p.q + (int64_t(v.r.token0) + t) * p.q_stride + (int64_t(v.kv) * p.G + rg) * D);
+    };
+    auto give_q = [&](const Unit &v) {
+      bool there;
+      const uint4 *src = q_row(v, there);
+      float f_inv = 1.f;
+      if (__any_sync(0xffffffffu, there)) {
+        const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+        float top = 0.f;
+        {
+          uint4 w[D / 8];
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) w[c] = there ? __ldg(src + c) : none;
+#pragma unroll
+          for (int c = 0; c < D / 8; ++c) {
+            const uint32_t y[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max3(top, fabsf(bf16_lo(y[k])), fabsf(bf16_hi(y[k])));
+          }
+        }
+        const int e = min(100, max(-114, 14 - (int(__float_as_uint(top) >> 23) - 127)));
+        const float f = __uint_as_float(uint32_t(127 + e) << 23);
+        f_inv = __uint_as_float(uint32_t(127 - e) << 23);
+        const uint32_t q_col = lane_base + L::kColQ + slot * (D / 2);
+        // 64 elements at a time, from the first-level cache (held since the pass above they would spill)
+#pragma unroll 1
+        for (int c0 = 0; c0 < D / 8; c0 += 8) {
+          uint32_t x[32];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 w = there ? __ldg(src + c0 + c) : none;
+            const uint32_t y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[4 * c + k] = f16x2_bits(bf16_lo(y[k]) * f, bf16_hi(y[k]) * f);
+          }
+          tmem_st32(q_col + 4 * c0, x);
+        }
+      }
+      st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(T_QFULL + slot));
+      return p.q_scale * f_inv;
+    };
+    [[maybe_unused]] float qs_next = p.q_scale;
+    if constexpr (FP8) {
+      Walk<NK> ahead = walk;
+      if (ahead.next(u)) qs_next = give_q(u);
+    }
     int g = 0, units = 0, singles = 0;                // key tiles, units, units of one row tile so far
     uint32_t ops = 0;
     bool ok = true;
@@ -673,6 +769,19 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       if (has_tree && live) {
         tree = __ldg(reinterpret_cast<const unsigned long long *>(p.tree) + u.r.token0 + tok);
         if (u.r.num_new < 64) tree &= (uint64_t(1) << u.r.num_new) - 1;
+      }
+      if constexpr (FP8) {
+        qs = qs_next;
+        Walk<NK> ahead = walk;
+        Unit v;
+        bool there;
+        if (ahead.next(v)) {  // its Q on the way to the second-level cache
+          const uint4 *src = q_row(v, there);
+          if (there) {
+            prefetch_l2(src);
+            if constexpr (D == 128) prefetch_l2(src + 8);
+          }
+        }
       }
       const int seen = start + tok + 1;               // causal: keys before this one
       const int clear = has_tree ? start : seen;      // every key before this one is visible
@@ -732,7 +841,6 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           fence_proxy_async();
         }
         const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
-        // (one copy of the code for both parts: unrolled, the loop outgrew the instruction caches)
         auto give_part = [&](auto which) -> bool {
           constexpr int part = decltype(which)::value;
           if (warp_live) {
@@ -769,7 +877,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                   const float a = ex2(z.x), b = ex2(z.y);
                   sum[(c >> 1) & 1] = __fadd2_rn(sum[(c >> 1) & 1], make_float2(a, b));
                   if constexpr (TERMS == 1) {
-                    pk[(c0 + c) / 2] = bf16x2_bits(a, b);
+                    pk[(c0 + c) / 2] = p_bits<FP8>(a, b);
                   } else {
                     pf[c0 + c] = a;
                     pf[c0 + c + 1] = b;
@@ -778,7 +886,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
               }
               float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
               top = live ? top * qs : neg_inf();        // qs > 0; (a dead row's scores are whatever Q held)
-              const bool grow = top > m + kLazy;
+              const bool grow = top > m + (L::kBias + kLazy);
               if (!__any_sync(0xffffffffu, grow)) break;
               // O may be changed: S(t) is complete, so PV(t - 2), issued before it, is too; the first
               // part's PV of this op is waited for
@@ -786,7 +894,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                 if (!wait_all(T_HALF + slot, ops)) return false;
                 fence_after();
               }
-              const float m_new = grow ? top : m;
+              const float m_new = grow ? top - L::kBias : m;
               const float alpha = grow ? ex2(m - m_new) : 1.f;
               l *= alpha;
               if (part > 0 || !empty) {
@@ -809,9 +917,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
               for (int y = 0; y < TERMS; ++y) {         // each term takes what the ones before left
 #pragma unroll
                 for (int c = 0; c < 64; c += 2) {
-                  pk[c / 2] = bf16x2_bits(pf[c], pf[c + 1]);
-                  pf[c] -= bf16_lo(pk[c / 2]);
-                  pf[c + 1] -= bf16_hi(pk[c / 2]);
+                  pk[c / 2] = p_bits<FP8>(pf[c], pf[c + 1]);
+                  const float2 got = p_values<FP8>(pk[c / 2]);
+                  pf[c] -= got.x;
+                  pf[c + 1] -= got.y;
                 }
                 tmem_st32(s_col + y * L::kPCols, pk);
               }
@@ -835,6 +944,13 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       ok = wait_all(T_OFULL, uint32_t(units));
       if (!ok) break;
       fence_after();
+      if constexpr (FP8) {
+        // Q of the next unit, so that its S need not wait for what follows.  (Not before the wait: both
+        // MMA threads must have seen this unit's Q.)
+        Walk<NK> ahead = walk;
+        Unit v;
+        if (ahead.next(v)) qs_next = give_q(v);
+      }
       const bool whole = u.j0 == 0 && u.j1 == u.n;
       const int row = tile_tok * p.G + r - u.tok0 * p.G;   // row of the unit (p.TH * p.G a tile)
       const int piece = 2 * blockIdx.x + (u.first ? 0 : 1);  // the CTA's first piece, or its last
@@ -958,7 +1074,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       if (last >= 0 && !wait_bounded(bar(kLanded + lane), uint32_t(last / NC) & 1u, p.wait_limit))
         bad |= PSD_FAULT_WAIT_TIMEOUT;
     }
-    if (lane < 2 && tail[2 + lane] > 0 &&
+    if (!FP8 && lane < 2 && tail[2 + lane] > 0 &&
         !wait_bounded(bar(T_QFULL + lane), uint32_t(tail[2 + lane] - 1) & 1u, p.wait_limit))
       bad |= PSD_FAULT_WAIT_TIMEOUT;
   }
@@ -1045,6 +1161,8 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   TCParams p;
   p.page_indices = S.page_indices;
   p.tree = S.tree;
+  p.q = static_cast<const __nv_bfloat16 *>(S.q);
+  p.q_stride = S.q_stride;
   p.o = S.o;
   p.lse = S.lse;
   p.fault = S.fault;
@@ -1147,8 +1265,8 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   p.part_lse = place.part_lse;
   p.sum_o = place.sum_o;
 
-  CUtensorMap tmQ, tmK, tmV;
-  {
+  CUtensorMap tmQ = {}, tmK, tmV;
+  if (!FP8) {
     const cuuint64_t dims[4] = {64, cuuint64_t(S.Hq), cuuint64_t(S.num_tokens), cuuint64_t(L::kHalves)};
     const cuuint64_t strides[3] = {cuuint64_t(D) * 2, cuuint64_t(S.q_stride) * 2, 128};
     const cuuint32_t box[4] = {64, cuuint32_t(S.G), cuuint32_t(p.TH), 1};
@@ -1228,7 +1346,7 @@ psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const St
                           cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
-    if (p.fp8) return p.out_f32 ? run<D, 3, true>(p, req, place, dev, s) : run<D, 1, true>(p, req, place, dev, s);
+    if (p.fp8) return p.out_f32 ? run<D, 2, true>(p, req, place, dev, s) : run<D, 1, true>(p, req, place, dev, s);
     return p.out_f32 ? run<D, 3, false>(p, req, place, dev, s) : run<D, 1, false>(p, req, place, dev, s);
   };
   return p.D == 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});

@@ -75,7 +75,7 @@ def bounds(oracle, D, n_keys, out_f32, terms):
     Scores: an f32 sum of D exact products (each add off by at most 2^-23 of the running
     absolute sum, truncation included), then a scale, an fma and a subtraction in log2
     units.  exp2: 2 ulp.  P meets V as `terms` bf16 terms (0: as f32): off by 2^-8 of it, or
-    2^-16 with two.  O and l: f32 sums of n_keys terms, in any grouping; a lazy maximum can
+    2^-24 with three; two stands for two f16 terms, 2^-22.  O and l: f32 sums of n_keys terms, in any grouping; a lazy maximum can
     rescale them a few times (each a rounding, counted in the same term).  The output
     is rounded to bf16 (2^-8) or f32.  An error e of every score moves o by at most
     2 e sum p |v|."""
@@ -83,7 +83,7 @@ def bounds(oracle, D, n_keys, out_f32, terms):
     empty, lse = np.isneginf(lse), np.where(np.isneginf(lse), 0.0, lse)
     score = (D + 8) * 2.0 ** -23 * top + (np.abs(lse) + 40) * 2.0 ** -22 + 2.0 ** -20
     sums = (n_keys + 64) * 2.0 ** -23
-    p_round = {0: 0.0, 1: 2.0 ** -8, 3: 2.0 ** -24}[terms]
+    p_round = {0: 0.0, 1: 2.0 ** -8, 2: 2.0 ** -22, 3: 2.0 ** -24}[terms]
     out = 2.0 ** -24 if out_f32 else 2.0 ** -8
     e_o = (2 * score[..., None] + sums * 2 + p_round) * pv * (1 + out) + out * np.abs(o) + 1e-30
     e_l = (score + sums) * LOG2E + 2.0 ** -22 * np.abs(lse) + 1e-30

@@ -41,7 +41,7 @@ def _check(s, *, out_f32=False, sm_scale=None, got=None):
     n = int(s.q_indptr[-1])
     assert torch.all(o[n:] == 5.0) and torch.all(lse[n:] == 5.0)   # rows behind the last request stay
     want = s.oracle(sm_scale)
-    terms = (3 if out_f32 else 1) if _tensor_cores(s, s.sm_scale if sm_scale is None else sm_scale) else 0
+    terms = (1 if not out_f32 else 2 if s.kv == "fp8" else 3) if _tensor_cores(s, s.sm_scale if sm_scale is None else sm_scale) else 0
     e_o, e_l = bounds(want, s.D, int(s.total.max()), out_f32, terms)
     o, lse = o[:n].double().cpu().numpy(), lse[:n].double().cpu().numpy()
     empty = np.isneginf(want[1])
