@@ -219,6 +219,8 @@ psd_status psd_set_timing(psd_ctx *ctx, int32_t enable);
  * their waits for those tiles run out after wait_limit_cycles (1e5 to 2e9 SM
  * cycles); each timed-out warp stops consuming tiles, the kernel completes, and the
  * call's fault word carries PSD_FAULT_WAIT_TIMEOUT for psd_check_device_error.
+ * multi_token_decode's tensor-core kernel does the same with each unit's key tiles (of
+ * 128 keys; of 64 for fp8 pools and f32 outputs).
  * Every copy a kernel did issue is waited for before it exits, and the tcgen05
  * kernels free their tensor memory only after their issued MMAs have completed.
  * The streaming form of psd_merge_states copies no input row from index from_tile
@@ -657,11 +659,13 @@ psd_status psd_plan_multi_token(const psd_page_table *host, const int32_t *q_ind
  * A row that sees no key gets o = 0 and lse = -inf.  Values the request's own tokens
  * hold in hidden places must be finite; pool rows outside the L_b tokens may hold
  * anything.
- * P (the softmax weights before normalisation) meets V as one bf16 term for bf16
- * outputs and as two (about 16 bits) for f32 outputs; sums, maxima and O are f32.
- * Two kernels: head dims 64 and 128 with page sizes that are multiples of 8, at most 128
- * query heads per KV head and sm_scale > 0 run on the tcgen05 tensor cores; every other
- * shape (D a multiple of 8 up to 256) on CUDA cores.
+ * Sums, maxima and O are f32.  Two kernels: head dims 64 and 128 with page sizes that are
+ * multiples of 8, at most 128 query heads per KV head, sm_scale * k_scale > 0 and at most
+ * 2^31 - 1 token slots in the pool run on the tcgen05 tensor cores; every other shape (D a
+ * multiple of 8 up to 256) on CUDA cores, with P (the weights before normalisation) in f32.
+ * On the tensor cores P meets V as one bf16 term (2^-8) for bf16 outputs and three (2^-24)
+ * for f32 outputs; with fp8 pools as one f16 term (2^-11) and two (2^-22).
+ * o must not overlap q or the pools.
  * workspace: >= psd_multi_token_workspace_bytes(ctx, D) bytes, 16-byte aligned, reusable
  * by calls on one stream; calls that may overlap (other streams, captured graphs that
  * may run at the same time) need their own.  psd_check_device_error reports its faults.

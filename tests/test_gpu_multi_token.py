@@ -277,6 +277,73 @@ def test_two_streams_with_their_own_workspaces():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_two_graphs_with_their_own_workspaces():
+    """Replayed on two streams at a time, over split units in both."""
+    steps = [Step([4, 1], [3000, 2500 + i], seed=40 + i) for i in range(2)]
+    graphs, outs = [], []
+    for s in steps:
+        args = psd.multi_token_args(s.q.cuda(), s.k.cuda(), s.v.cuda(), torch.from_numpy(s.page_indices).cuda(),
+                                    sm_scale=s.sm_scale)
+        plan = psd.plan_multi_token(psd.HostTable(s.page_indptr, s.page_indices, s.last, s.page), s.q_indptr)
+        ws = psd.multi_token_workspace(ctx(), plan, s.D, "cuda")
+        o = torch.full((s.T, s.Hq, s.D), 5.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((s.T, s.Hq), 5.0, device="cuda")
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            psd.multi_token_decode(ctx(), args, plan, o, lse, ws)
+        graphs.append((g, args, ws))
+        outs.append((o, lse))
+    streams = [torch.cuda.Stream() for _ in steps]
+    for _ in range(20):
+        for (g, _, _), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for s, got in zip(steps, outs):
+        _check(s, got=got)
+
+
+@pytest.mark.parametrize("kv,out_f32", [("bf16", False), ("fp8", False), ("fp8", True)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_powers_of_two_in_the_queries(kv, out_f32, D):
+    """Queries times 2^e and a scale of 2^-e change nothing; a row with one element 2^9 above the
+    rest stays within the bounds."""
+    s = Step([5, 40], [100, 300], D=D, kv=kv, seed=50)
+    want = _run(s, out_f32=out_f32)
+    q = s.q.clone()
+    for e in (-60, 40):
+        s.q = (q.float() * 2.0 ** e).to(torch.bfloat16)
+        got = _run(s, out_f32=out_f32, sm_scale=s.sm_scale * 2.0 ** -e)
+        assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    s.q = q
+    s.q[:, :, 3] *= 512
+    _check(s, out_f32=out_f32, sm_scale=s.sm_scale / 64)
+
+
+def test_nothing_to_attend():
+    """No request, and requests without new tokens: the outputs stay as they were."""
+    s = Step([0, 0], [20, 33], seed=51)
+    o, lse = _run(s)
+    assert bool((o == 5.0).all()) and bool((lse == 5.0).all())
+
+
+@pytest.mark.parametrize("kv,D,out_f32", [("bf16", 64, False), ("bf16", 128, True), ("fp8", 64, True), ("fp8", 128, False)])
+def test_bounded_wait_runs_out_and_is_reported(kv, D, out_f32):
+    """The loads of each unit's key tiles from index 1 on are withheld: the waits for them run out
+    (about 1 ms), every role stops, the call completes and reports it, and the next call is
+    clean."""
+    s = Step([4, 70, 1], [1500, 300, 900], D=D, kv=kv, seed=52)
+    ctx().test_withhold_loads(1, 2_000_000)
+    try:
+        with pytest.raises(psd.PsdError) as e:
+            _run(s, out_f32=out_f32)
+    finally:
+        ctx().test_withhold_loads(-1)
+    assert e.value.status == 4 and e.value.fault_bits == 2
+    _check(s, out_f32=out_f32)
+
+
 @pytest.mark.parametrize("D", [64, 40])
 def test_bad_page_id_is_flagged(D):
     s = Step([2, 3], [100, 40], D=D, seed=21)

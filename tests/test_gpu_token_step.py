@@ -79,3 +79,65 @@ def test_three_steps(D, page, kv):
         assert accepted.tolist() == a and out.tolist() == said
         length = [n - int(d) + x for n, d, x in zip(length, drafts, a)]  # refused drafts leave the cache
     assert int(fault) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_a_captured_step(kv):
+    """Append, attention and verification in one graph, replayed over other queries: as the calls
+    one by one."""
+    B, new, before, Hq, Hkv, D, page, V = 3, [5, 1, 4], [300, 900, 40], 8, 2, 64, 16, 50
+    length = [n + x for n, x in zip(new, before)]
+    pages = [-(-n // page) for n in length]
+    rng = np.random.default_rng(7)
+    indptr = np.concatenate([[0], np.cumsum(pages)])
+    indices = rng.permutation(int(indptr[-1])).astype(np.int32)
+    q_indptr = np.concatenate([[0], np.cumsum(new)])
+    d_indptr = q_indptr - np.arange(B + 1)
+    T = int(q_indptr[-1])
+    i32 = lambda a: torch.from_numpy(np.asarray(a).astype(np.int32)).cuda()  # noqa: E731
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *n: torch.randn(*n, device="cuda", generator=gen).to(torch.bfloat16)  # noqa: E731
+    shape = (len(indices), page, Hkv, D)
+    start = [torch.randint(0, 96, shape, dtype=torch.uint8, device="cuda", generator=gen) if kv == "fp8" else rand(*shape)
+             for _ in range(2)]
+    pools = [p.clone() for p in start]
+    q, k, v = rand(T, Hq, D), rand(T, Hkv, D), rand(T, Hkv, D)
+    q_rot, o, lse = torch.empty_like(q), torch.empty_like(q), torch.empty((T, Hq), device="cuda")
+    rope = psd.rope_frequencies(D)
+    idx, q_ind, kv_len, p_ind = i32(indices), i32(q_indptr), i32(length), i32(indptr)
+    plan = psd.plan_multi_token(psd.HostTable(indptr, indices, [n - (c - 1) * page for n, c in zip(length, pages)], page),
+                                q_indptr, Hq, Hkv)
+    ws = psd.multi_token_workspace(ctx(), plan, D, "cuda")
+    args = psd.multi_token_args(q_rot, *pools, idx, sm_scale=D ** -0.5, k_scale=0.02, v_scale=0.015)
+    probs = torch.softmax(torch.randn(T, V, device="cuda", generator=gen), -1)
+    tokens, u = i32(rng.integers(0, V, T - B)), torch.rand(T, device="cuda", generator=gen)
+    accepted, out, fault = i32(np.zeros(B)), i32(np.zeros(T)), i32(np.zeros(1))
+    d_ind = i32(d_indptr)
+
+    def step():
+        psd.append_tokens(ctx(), q, k, v, q_rot, q_indptr=q_ind, kv_len=kv_len, page_indptr=p_ind, page_indices=idx,
+                          k_pool=pools[0], v_pool=pools[1], rope=rope, neox=True, k_scale=0.02, v_scale=0.015, fault=fault)
+        psd.multi_token_decode(ctx(), args, plan, o, lse, ws)
+        psd.verify_drafts(ctx(), probs, None, tokens, d_ind, u, accepted, out, fault=fault)
+
+    def outputs():
+        torch.cuda.synchronize()
+        assert int(fault) == 0 and psd.check_device_error(ctx(), ws) == 0
+        return [x.clone() for x in (q_rot, o, lse, accepted, out, *pools)]
+
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(2):
+        q.copy_(rand(T, Hq, D))
+        u.copy_(torch.rand(T, device="cuda", generator=gen))
+        results = []
+        for run in (step, g.replay):
+            for p, at in zip(pools, start):
+                p.copy_(at)
+            for x in (q_rot, o, lse, accepted, out):
+                x.zero_()
+            run()
+            results.append(outputs())
+        assert all(torch.equal(a, b) for a, b in zip(*results))
