@@ -102,12 +102,13 @@ struct Lay {
   // P = 2^(s - m) with the row's top at 2^kBias: f16 holds P down to 2^-31 of it.
   static constexpr float kBias = FP8 ? 7.f : 0.f;
   static constexpr int kThreads = FP8 ? 20 * 32 : 12 * 32;
-  // What a CTA's time is made of, in quarters of a key tile that waits for memory: the tiles of a
-  // unit of one row tile and of two (at D = 64 the second is bound by its softmax), and what a
-  // unit costs beside its tiles (two of 128 keys, four of 64; twelve where Q comes through registers).
-  // Stretches equal in tiles alone left the CTAs with most units 15 % behind the mean: 63 us for
-  // 32 drafted requests against 54; fp8 trees take 65 with 16 quarters a unit, 54 with 48.
-  static constexpr int kOneCost = D == 64 && NK == 128 ? 3 : 4, kTwoCost = 4, kUnitCost = NK == 128 ? 8 : FP8 ? 48 : 16;
+  // What a CTA's time is made of, in halves of a key tile of one row tile: such a tile, a tile of
+  // two row tiles, and what a unit costs beside its tiles (three tiles of 128 keys, five of 64, and
+  // fourteen where Q comes through registers).  Stretches equal in tiles alone left the CTAs with
+  // most units 15 % behind the mean.  Tiles of two row tiles counted as one: 34 us for 24 requests of
+  // 1 to 4 tokens and one of 200 over 100 to 3000 keys against 27 (f32 outputs: 36 against 25); fp8
+  // units counted as four tiles: 65 us for 16 requests' trees against 54.
+  static constexpr int kOneCost = 2, kTwoCost = 4, kUnitCost = NK == 128 ? 6 : FP8 ? 28 : 10;
   // Registers a thread: 168 at launch of 384 threads, 96 of 640; the softmax warps hold a
   // part's scores and weights and take what the others do without.
   static constexpr int kLaunchRegs = FP8 ? 96 : 168;
