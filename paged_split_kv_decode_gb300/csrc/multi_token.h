@@ -43,6 +43,6 @@ StepPlace step_tc_place(int ctas, int D, float *base);
 bool step_tc_supports(const StepParams &p);
 psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
                           cudaStream_t s);
-psd_status launch_step_general(const StepParams &p, const StepRequests &req, const DeviceInfo &dev, cudaStream_t s);
+psd_status launch_step_general(const StepParams &p, const StepRequests &req, float *base, const DeviceInfo &dev, cudaStream_t s);
 
 }  // namespace psd

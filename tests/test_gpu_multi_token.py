@@ -90,6 +90,22 @@ def test_long_cache_is_split(out_f32):
     _check(Step([1, 1, 3], [5000, 3, 2500], Hq=4, Hkv=2, page=64, seed=2), out_f32=out_f32)
 
 
+@pytest.mark.parametrize("D,page,G,kv,out_f32", [(256, 16, 4, "bf16", False), (96, 7, 1, "fp8", True), (64, 1, 2, "bf16", True),
+                                                 (8, 3, 9, "fp8", False), (128, 12, 130, "bf16", False)])
+def test_long_cache_of_the_general_kernel(D, page, G, kv, out_f32):
+    """Few rows over many keys: the keys are split over CTAs and joined; some rows see far fewer."""
+    s = Step([1, 3, 2], [5000, 900, 0], Hq=2 * G, Hkv=2, D=D, page=page, kv=kv, seed=60)
+    _check(s, out_f32=out_f32)
+    first, again = _run(s, out_f32=out_f32), _run(s, out_f32=out_f32)
+    assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("D,page", [(80, 4), (200, 16)])
+def test_trees_of_the_general_kernel(D, page):
+    s = Step([1, 40, 64, 0, 7], [3000, 70, 1, 20, 129], D=D, page=page, seed=61, tree="random")
+    _check(s)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8"])
 def test_prompt_and_single_tokens(kv):
     _check(Step([1, 500, 1, 2], [700, 150, 33, 0], Hq=4, Hkv=1, kv=kv, D=128, seed=7))
