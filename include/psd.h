@@ -602,8 +602,8 @@ psd_status psd_rope_frequencies(const psd_rope_scaling *scaling, double *inv_fre
  * A token whose index falls outside [0, its page list) or whose page id is out of range
  * keeps its pool rows unwritten (q_out is written) and sets PSD_FAULT_PAGE_ID; a negative
  * position (its own or given) leaves the token untouched and sets PSD_FAULT_RANGE, both
- * OR-ed into *fault_dev.  Two tokens that share a pool row (a page listed twice) leave
- * one of the two rows there.
+ * OR-ed into *fault_dev.  Where two tokens share a pool row (a page listed twice), each
+ * element of it holds the value of one of them.
  * num_tokens == 0 or batch == 0 is a no-op (the pointers are not checked). */
 typedef struct {
   const void *q;                 /* device [T, Hq, D] bf16 (NULL iff Hq == 0) */
