@@ -23,6 +23,7 @@ namespace psd {
 namespace {
 
 constexpr int kMaxPairs = 256;  // rot_dim / 2
+constexpr int kCtasPerSm = 5;   // of the 16-byte form: 48 registers a thread
 
 struct AppendParams {
   const __nv_bfloat16 *q, *k, *v;
@@ -167,9 +168,12 @@ __global__ void __launch_bounds__(256)
 // NT consecutive tokens per CTA, 8 pairs or 8 columns a thread and access.  A thread takes
 // the same columns of all NT tokens, so that index arithmetic is paid once and NT loads
 // are in flight; the first queries are on their way while the places and angles are found.
+// Keys start at the threads that the queries' last round left idle, copies after those: the
+// phases of a CTA overlap (9800 tokens 42.9 us against 47.5 with each phase from thread 0 on, and
+// with 64 of 128 columns rotated and fp8 pools 49.5 against 68.5).
 // 32 query and 8 KV heads of 128, cold caches: one token 6.7 us (a chain of dependent loads:
-// lengths, page id, frequencies, rows), 160 tokens into fp8 pools 9 us, 10784 tokens 51 us (265 MB at
-// 5.2 TB/s, writes and reads mixed; 40 % of the issue slots go into rotation and addresses).
+// lengths, page id, frequencies, rows), 160 tokens into fp8 pools 8 us, 10784 tokens 47 us (265 MB at
+// 5.6 TB/s, writes and reads mixed).
 struct F8 {
   float v[8];
 };
@@ -210,7 +214,7 @@ __device__ __forceinline__ void put8(void *pool, int64_t at, const F8 &f, bool f
 }
 
 template <int NT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, kCtasPerSm)
     append_tokens_vec_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   __shared__ __align__(16) float cosine[NT][kMaxPairs], sine[NT][kMaxPairs];
   __shared__ Place places[NT];
@@ -298,7 +302,8 @@ __global__ void __launch_bounds__(256)
     load(x, p.q + int64_t(h) * p.D, p.q_stride, col);
   }
   // ---- keys
-  for (j = tid; j < p.Hkv * groups; j += 256) {
+  const int nk = p.Hkv * groups;
+  for (j = (tid - nq) & 255; j < nk; j += 256) {  // the threads the queries left idle first
     h = j / groups;
     const int g = j - h * groups;
     col = column(g);
@@ -316,7 +321,7 @@ __global__ void __launch_bounds__(256)
   }
   // ---- columns outside the rotation, and V
   const int cq = p.Hq * rest, ck = p.Hkv * rest, cv = p.Hkv * p.Dv / 8;
-  for (j = tid; j < cq + ck + cv; j += 256) {
+  for (j = (tid - nq - nk) & 255; j < cq + ck + cv; j += 256) {
     const bool is_q = j < cq, is_k = !is_q && j < cq + ck;
     const int i = is_q ? j : is_k ? j - cq : j - cq - ck;
     int64_t off;  // in the token's heads
@@ -348,7 +353,7 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-static psd_status launch_append_tokens(const psd_append_args *a, cudaStream_t s) {
+static psd_status launch_append_tokens(const psd_append_args *a, int sms, cudaStream_t s) {
   AppendParams p;
   p.q = static_cast<const __nv_bfloat16 *>(a->q);
   p.k = static_cast<const __nv_bfloat16 *>(a->k);
@@ -392,11 +397,11 @@ static psd_status launch_append_tokens(const psd_append_args *a, cudaStream_t s)
   const bool vec = a->rot_dim % 16 == 0 && a->rot_col % 8 == 0 && a->D % 8 == 0 && a->Dv % 8 == 0 &&
                    fits(a->q, a->Hq ? a->q_stride : 0) && fits(a->k, a->k_stride) && fits(a->v, a->Dv ? a->v_stride : 0) &&
                    aligned16(a->q_out) && aligned16(a->k_pool) && aligned16(a->v_pool);
-  // Two tokens a CTA for long calls: 17 us against 18.3 for 2436 tokens and 47 against 53 for 9800, but
-  // 12.4 against 11.6 for 1218 (too few CTAs); four: 50 us for 9800, 18.5 for 2436 (registers).
+  // One token a CTA while all of them fit on the SMs at once, two beyond: 608 tokens 7.6 us against 8.2,
+  // 1218 tokens 10.7 against 9.3, 9800 tokens 47.8 against 42.9 (four: 46.8; registers).
   constexpr int kMany = 2;
   if (!vec) append_tokens_kernel<<<a->num_tokens, 256, 0, s>>>(p, turns);
-  else if (a->num_tokens < 2048) append_tokens_vec_kernel<1><<<a->num_tokens, 256, 0, s>>>(p, turns);
+  else if (a->num_tokens <= kCtasPerSm * sms) append_tokens_vec_kernel<1><<<a->num_tokens, 256, 0, s>>>(p, turns);
   else append_tokens_vec_kernel<kMany><<<(a->num_tokens - 1) / kMany + 1, 256, 0, s>>>(p, turns);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "append_tokens launch: %s", cudaGetErrorString(e));
@@ -443,5 +448,5 @@ extern "C" psd_status append_tokens(psd_ctx *ctx, const psd_append_args *a, psd_
     if (!(a->inv_freq[i] >= 0.0) || !std::isfinite(a->inv_freq[i]))
       return fail(PSD_ERR_INVALID_ARG, "append_tokens: inv_freq[%d] must be finite and >= 0", i);
   DeviceGuard g(ctx->dev.device);
-  return launch_append_tokens(a, reinterpret_cast<cudaStream_t>(stream));
+  return launch_append_tokens(a, ctx->dev.num_sms, reinterpret_cast<cudaStream_t>(stream));
 }
