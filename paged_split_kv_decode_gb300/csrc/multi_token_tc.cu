@@ -49,14 +49,16 @@
 // the row's largest P.
 // The tensor cores' f32 accumulation cuts low bits at every step of 16 keys and term, always
 // towards zero: over 8000 keys it cost 1.3e-5 of the result's norm.  bf16 outputs do not
-// see that; for f32 outputs O starts anew every kFlush ops of a slot, and the rows add what
-// they read out to a sum in the workspace, rounded to nearest.
+// see that; for f32 outputs O starts anew every kFlush ops of a slot (36 steps), and the rows add
+// what they read out to a sum in the workspace, rounded to nearest.  3 single tokens over 20000 to
+// 65536 keys: 8e-7 of the norm and 127 us, against 3.5e-6 and 113 us with 16 ops and 5e-7 and
+// some 180 us with one.
 // The row maximum follows lazily: O and l are rescaled only when it grows by more than
 // 2^8, so P <= 2^8 (2^15 as f16).
 //
 // Measured, 32 query and 8 KV heads of 128, cold caches, the join beside it: 32 requests of 5 tokens
 // over 512 to 4096 keys 54 + 4 us (286 MB, 0.79 of a plain copy's rate: copies bound it); their f32
-// outputs 70 us; 3 single tokens over 20000 to 65536 keys, f32 outputs, 116 + 6 us (0.81); a
+// outputs 84 us; 3 single tokens over 20000 to 65536 keys, f32 outputs, 127 + 6 us (0.74); a
 // 4096-token chunk over 4096 286 + 10 us (1440 TFLOP/s: tensor cores 64 % active, the rest is what one
 // slot's chain of S, softmax and P V leaves uncovered by the other's); fp8 trees as above, bound by that
 // chain over tiles of 64 keys and by the conversion.
@@ -81,11 +83,11 @@ constexpr int kMmaWarp = 8, kKWarp = 9, kVWarp = 10, kMmaWarp1 = 11;
 constexpr int kConvertWarp = 12, kConvertWarps = 4;  // fp8 pools only: 4 warps for K, then 4 for V
 constexpr uint32_t kRingBytes = 128 * 1024;
 constexpr int kMaxStages = 16;
-constexpr int kFlush = 16;       // f32 outputs: ops of a slot (64 keys each) O holds at most
 
 template <int D, int TERMS, bool FP8>
 struct Lay {
   static constexpr int NK = TERMS == 1 && !FP8 ? 128 : 64;     // keys per tile
+  static constexpr int kFlush = 9 / TERMS;                     // f32 outputs: ops of a slot that O holds at most
   static constexpr int kParts = NK / 64;                       // parts of a tile whose P go separately
   static constexpr int kHalves = D / 64;                       // 64-column halves of a row
   static constexpr uint32_t kGroupBytes = kHalves * 1024;      // 8 slots of one head
@@ -670,7 +672,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         if (!ok) break;
         if (t > 0) ++turns;
         const uint64_t b = vd + ((st * L::kTileBytes) >> 4);
-        const bool fresh = TERMS > 1 ? (t >> 1) % kFlush == 0 : t < 2;  // O starts at zero
+        const bool fresh = TERMS > 1 ? (t >> 1) % L::kFlush == 0 : t < 2;  // O starts at zero
 #pragma unroll
         for (int part = 0; part < L::kParts; ++part) {
           ok = wait(T_PFULL + 2 * part + slot, ops);
@@ -793,8 +795,9 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       const int seen = start + tok + 1;               // causal: keys before this one
       const int clear = has_tree ? start : seen;      // every key before this one is visible
       float m = neg_inf(), l = 0.f;
-      // f32 outputs: the row's O of the ops before the last flush, relative to 2^m_sum
-      float *sum_row = p.sum_o + ((int64_t(blockIdx.x) * 2 + slot) * kRows + r) * D;
+      // f32 outputs: the row's O of the ops before the last flush, relative to 2^m_sum; columns
+      // c .. c + 3 at sum_row + c kRows, so that a warp's rows lie side by side
+      float *sum_row = p.sum_o + (int64_t(blockIdx.x) * 2 + slot) * kRows * D + 4 * r;
       float m_sum = neg_inf();
       bool flushed = false;
       for (int t = slot; t < T; t += 2, ++ops) {
@@ -805,7 +808,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         bool empty = t < 2;                             // O holds nothing
         if (warp_live) {
           if constexpr (TERMS > 1) {
-            if (t >= 2 && (t >> 1) % kFlush == 0) {
+            if (t >= 2 && (t >> 1) % L::kFlush == 0) {
               // S(t) is complete, so PV(t - 2), issued before it, is too
               const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);
 #pragma unroll 1
@@ -816,7 +819,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                 if (live) {
 #pragma unroll
                   for (int k = 0; k < 32; k += 4) {
-                    float4 *at = reinterpret_cast<float4 *>(sum_row + c + k);
+                    float4 *at = reinterpret_cast<float4 *>(sum_row + (c + k) * kRows);
                     float4 x = flushed ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
                     x.x = fmaf(x.x, keep, __uint_as_float(o[k]));
                     x.y = fmaf(x.y, keep, __uint_as_float(o[k + 1]));
@@ -998,7 +1001,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       auto add_flushed = [&](float (&x)[32], const float *from, float scale) {
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
-          const float4 y = *reinterpret_cast<const float4 *>(from + k);
+          const float4 y = *reinterpret_cast<const float4 *>(from + k * kRows);
           x[k] = fmaf(y.x, scale, x[k]);
           x[k + 1] = fmaf(y.y, scale, x[k + 1]);
           x[k + 2] = fmaf(y.z, scale, x[k + 2]);
@@ -1044,9 +1047,9 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             for (int k = 0; k < 32; ++k) x[k] = l1 == 0.f ? x[k] : fmaf(__uint_as_float(y[k]), f1, x[k]);
           }
           if constexpr (TERMS > 1) {
-            if (live && flushed && l != 0.f) add_flushed(x, sum_row + c, keep * f0);
+            if (live && flushed && l != 0.f) add_flushed(x, sum_row + c * kRows, keep * f0);
             if (live && keep1 != 0.f && l1 != 0.f)
-              add_flushed(x, sum_row + (slot ? -kRows * D : kRows * D) + c, keep1 * f1);
+              add_flushed(x, sum_row + (slot ? -kRows * D : kRows * D) + c * kRows, keep1 * f1);
           }
           put32(x, c);
         }
