@@ -1120,23 +1120,35 @@ __global__ void __launch_bounds__(256) step_join_kernel(const TCParams p, const 
   auto at = [&](int i) {
     return int64_t(2 * (u.first + i) + (i == 0 ? u.late : 0)) * 2 * kRows + (live ? row : 0);
   };
+  // The first two pieces (there are two at least) are on their way beside the LSEs.
+  float y[2][kCols];
+  auto fetch = [&](int i, float (&to)[kCols]) {
+    const float *src = p.part_o + at(i) * D + 4 * lane;
+#pragma unroll
+    for (int k = 0; k < kCols; k += 4)
+      *reinterpret_cast<float4 *>(to + k) = *reinterpret_cast<const float4 *>(src + LANES * k);
+  };
+  fetch(0, y[0]);
+  fetch(1, y[1]);
   float m = neg_inf();
   for (int i = lane; i < u.n; i += LANES) m = fmaxf(m, p.part_lse[at(i)]);
 #pragma unroll
   for (int x = LANES / 2; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   const float from = m == neg_inf() ? 0.f : m;
   float x[kCols] = {}, sum = 0.f;
-#pragma unroll 2
-  for (int i = 0; i < u.n; ++i) {
-    const float s = p.part_lse[at(i)], w = ex2(s - from);
-    const float *src = p.part_o + at(i) * D + 4 * lane;
-    sum += w;
-    float y[kCols];
+  for (int i = 0; i < u.n; i += 2) {
+    if (i > 0) {
+      fetch(i, y[0]);
+      if (i + 1 < u.n) fetch(i + 1, y[1]);
+    }
 #pragma unroll
-    for (int k = 0; k < kCols; k += 4)
-      *reinterpret_cast<float4 *>(y + k) = *reinterpret_cast<const float4 *>(src + LANES * k);
+    for (int k2 = 0; k2 < 2; ++k2) {
+      if (i + k2 >= u.n) break;
+      const float s = p.part_lse[at(i + k2)], w = ex2(s - from);
+      sum += w;
 #pragma unroll
-    for (int k = 0; k < kCols; ++k) x[k] = s == neg_inf() ? x[k] : fmaf(w, y[k], x[k]);
+      for (int k = 0; k < kCols; ++k) x[k] = s == neg_inf() ? x[k] : fmaf(w, y[k2][k], x[k]);
+    }
   }
   if (!live) return;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
