@@ -81,6 +81,7 @@ __device__ __forceinline__ uint64_t share_of(float u, uint64_t total) {
 }
 
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
+constexpr int kDeepCtas = 4;   // CTAs an SM of the form for few CTAs
 constexpr int kMaxSums = 512;  // sums a CTA keeps of its part of a row
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
@@ -125,10 +126,14 @@ struct Row {
 // blocks of `step` entries, keeping each block's sum, so that the row is read once, and
 // the CTA that holds the crossing looks only at the block where it lies again.
 // The work is the row's bytes: 8 V with a refusal, 4 V without; 8 CTAs a request put
-// enough loads in flight from one request on.  4 requests of 32000 words take 13.5 us, nearly all of
+// enough loads in flight from one request on.  4 requests of 32000 words take 12.6 us, nearly all of
 // it the chain (offsets, drafts, their p and q, the row, two cluster barriers, the block again);
 // 128 requests of 98305 words with sampled drafts 30 us (101 MB: the chain, then 5 TB/s).
-__global__ void __launch_bounds__(kVerifyThreads, 7) verify_drafts_kernel(const VerifyParams p, int ctas) {
+// U blocks of a warp are on their way at once: two where all CTAs fit at four an SM, one at seven
+// an SM else.  48 requests of 131072 words 15.1 us against 16.7 with one (17 against 19 sampled),
+// 128 requests of 98305 words in 1024 CTAs 38 us with two against 29.7: a second wave.
+template <int U>
+__global__ void __launch_bounds__(kVerifyThreads, U == 1 ? 7 : kDeepCtas) verify_drafts_kernel(const VerifyParams p, int ctas) {
   __shared__ uint64_t sums[kMaxSums], warps[kVerifyWarps], mine;
   __shared__ int first_refused;
   const int b = blockIdx.x / ctas, rank = blockIdx.x - b * ctas;
@@ -174,6 +179,35 @@ __global__ void __launch_bounds__(kVerifyThreads, 7) verify_drafts_kernel(const 
     }
     uint64_t own = 0;
     for (int k = warp; k < blocks; k += kVerifyWarps) {
+      if constexpr (U > 1) {
+        const int at = v0 + k * 256 + lane;
+        if (step == 256 && v0 + (k + (U - 1) * kVerifyWarps + 1) * 256 <= v1) {  // U whole blocks of the warp
+          float pv[U][8], qv[U][8];
+#pragma unroll
+          for (int n = 0; n < U; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) pv[n][i] = __ldg(row.p + at + n * kVerifyWarps * 256 + 32 * i);
+          if (row.q)
+#pragma unroll
+            for (int n = 0; n < U; ++n)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) qv[n][i] = __ldg(row.q + at + n * kVerifyWarps * 256 + 32 * i);
+#pragma unroll
+          for (int n = 0; n < U; ++n) {
+            Acc s;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (row.q) s.add(pv[n][i], qv[n][i]);
+              else s.add(row.hot - at == n * kVerifyWarps * 256 + 32 * i ? 0.f : pv[n][i]);
+            }
+            const uint64_t x = warp_sum(s.value(8, row.q != nullptr));
+            if (lane == 0) sums[k + n * kVerifyWarps] = x;
+            own += x;
+          }
+          k += (U - 1) * kVerifyWarps;
+          continue;
+        }
+      }
       const int lo = v0 + k * step, hi = min(lo + step, v1);
       uint64_t x = 0;
       for (int c = lo; c < hi; c += 256) {
@@ -303,7 +337,9 @@ extern "C" psd_status verify_drafts(psd_ctx *ctx, const psd_verify_args *a, psd_
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, verify_drafts_kernel, p, ctas);
+  const bool few = int64_t(a->batch) * ctas <= int64_t(kDeepCtas) * ctx->dev.num_sms;  // all on the SMs at once
+  const cudaError_t e = few ? cudaLaunchKernelEx(&cfg, verify_drafts_kernel<2>, p, ctas)
+                            : cudaLaunchKernelEx(&cfg, verify_drafts_kernel<1>, p, ctas);
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "verify_drafts launch: %s", cudaGetErrorString(e));
   return PSD_OK;
 }
