@@ -337,6 +337,21 @@ def test_powers_of_two_in_the_queries(kv, out_f32, D):
     _check(s, out_f32=out_f32, sm_scale=s.sm_scale / 64)
 
 
+@pytest.mark.parametrize("kv,D,out_f32", [("bf16", 128, False), ("fp8", 128, False), ("fp8", 64, True), ("bf16", 64, True), ("bf16", 40, False)])
+def test_rows_that_are_not_finite_stay_alone(kv, D, out_f32):
+    """NaN or infinite query rows give NaN in their own rows; the others are what they were."""
+    s = Step([5, 40], [100, 300], D=D, kv=kv, seed=70)
+    o, lse = _run(s, out_f32=out_f32)
+    s.q[2, 1] = float("nan")
+    s.q[30, 0] = float("inf")
+    s.q[31, 5, 7] = -float("inf")
+    got_o, got_lse = _run(s, out_f32=out_f32)
+    at = torch.zeros((s.T, s.Hq), dtype=torch.bool, device="cuda")
+    at[2, 1] = at[30, 0] = at[31, 5] = True
+    assert bool(torch.isnan(got_o[at]).all()) and bool(torch.isnan(got_lse[at]).all())
+    assert torch.equal(got_o[~at], o[~at]) and torch.equal(got_lse[~at], lse[~at])
+
+
 def test_nothing_to_attend():
     """No request, and requests without new tokens: the outputs stay as they were."""
     s = Step([0, 0], [20, 33], seed=51)

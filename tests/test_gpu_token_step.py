@@ -141,3 +141,46 @@ def test_a_captured_step(kv):
             run()
             results.append(outputs())
         assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("kv,page", [("bf16", 16), ("fp8", 16), ("bf16", 12)])
+def test_pools_past_32_bits(kv, page):
+    """The same step in a small pool and at the end of one with more than 2^31 elements (bf16: more
+    than 2^32 bytes) agrees bit for bit."""
+    new, before, Hq, Hkv, D = [5, 40], [300, 20], 16, 8, 128
+    length = [n + x for n, x in zip(new, before)]
+    pages = [-(-n // page) for n in length]
+    indptr = np.concatenate([[0], np.cumsum(pages)])
+    used = int(indptr[-1])
+    many = (1 << 31) // (page * Hkv * D) + 100
+    order = np.random.default_rng(11).permutation(used).astype(np.int32)
+    q_indptr = np.concatenate([[0], np.cumsum(new)])
+    T = int(q_indptr[-1])
+    i32 = lambda a: torch.from_numpy(np.asarray(a).astype(np.int32)).cuda()  # noqa: E731
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    rand = lambda *n: torch.randn(*n, device="cuda", generator=gen).to(torch.bfloat16)  # noqa: E731
+    shape = (used, page, Hkv, D)
+    start = [torch.randint(0, 96, shape, dtype=torch.uint8, device="cuda", generator=gen) if kv == "fp8" else rand(*shape)
+             for _ in range(2)]
+    q, k, v = rand(T, Hq, D), rand(T, Hkv, D), rand(T, Hkv, D)
+    rope, results = psd.rope_frequencies(D), []
+    for pool_pages in (used, many):
+        pools = [torch.empty((pool_pages, page, Hkv, D), dtype=x.dtype, device="cuda") for x in start]
+        for pool, x in zip(pools, start):
+            pool[pool_pages - used:] = x
+        indices = order + (pool_pages - used)
+        idx, q_rot = i32(indices), torch.empty_like(q)
+        fault = psd.append_tokens(ctx(), q, k, v, q_rot, q_indptr=i32(q_indptr), kv_len=i32(length), page_indptr=i32(indptr),
+                                  page_indices=idx, k_pool=pools[0], v_pool=pools[1], rope=rope, neox=True,
+                                  k_scale=0.02, v_scale=0.015)
+        plan = psd.plan_multi_token(psd.HostTable(indptr, indices, [n - (c - 1) * page for n, c in zip(length, pages)], page),
+                                    q_indptr, Hq, Hkv)
+        ws = psd.multi_token_workspace(ctx(), plan, D, "cuda")
+        o, lse = torch.empty_like(q), torch.empty((T, Hq), device="cuda")
+        psd.multi_token_decode(ctx(), psd.multi_token_args(q_rot, *pools, idx, sm_scale=D ** -0.5, k_scale=0.02,
+                                                           v_scale=0.015), plan, o, lse, ws)
+        assert int(fault) == 0 and psd.check_device_error(ctx(), ws) == 0
+        results.append([q_rot, o, lse] + [pool[pool_pages - used:].clone() for pool in pools])
+        del pools
+    assert all(torch.equal(a, b) for a, b in zip(*results))
+    assert not torch.equal(results[0][3], start[0])
