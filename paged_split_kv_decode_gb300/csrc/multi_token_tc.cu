@@ -687,10 +687,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         }
         if (!ok) break;
         ++ops;
+        if (t + 2 < T) issue_s(t + 2);  // before the commits below: a softmax waits for it
         commit(bar(T_EMPTY + st));
         if (!u.two) commit(bar(T_EMPTY + st));
         if (t + 2 >= T) commit(bar(T_OFULL));
-        if (t + 2 < T) issue_s(t + 2);
         if (t + 1 < T) mbar_arrive(bar(T_TURN + (slot ^ 1)));
       }
       g += nt;
