@@ -705,8 +705,9 @@ psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *args,
  * of the weights rounded to multiples of 2^-46, so the outcome does not depend on the order
  * of summation.  Probabilities are f32 in [0, 1]; in the weights, values that are not (NaN,
  * negative) count as 0, larger than 1 as 1.  A draft token outside [0, vocab)
- * is refused, its q is 0 everywhere, and PSD_FAULT_RANGE is set; so is a row whose
- * weights are all 0 (its new token is -1).  Rows with no request are not touched. */
+ * is refused, its q is 0 everywhere, and PSD_FAULT_RANGE is set.  It is also set for a row
+ * whose weights are all 0 or sum to 2^18 or more (64 bits of sums hold less): its new token
+ * is -1.  Rows with no request are not touched. */
 typedef struct {
   const float *target_probs;   /* device [num_drafts + batch, vocab] */
   const float *draft_probs;    /* device [num_drafts, vocab] or NULL */

@@ -3,10 +3,11 @@
 // Mathematics.  With draft d drawn from q, accepting with probability min(1, p(d)/q(d))
 // and drawing from max(p - q, 0) after a refusal leaves the outcome distributed as p.
 // Acceptance compares u q(d) < p(d): the product of two f32 numbers is exact in 64 bits.
-// The draw wants the least v with C_v > u C: a border decided by sums of up to 2^17
-// numbers, so the weights are summed as integers, multiples of 2^-46 (the totals stay below
-// 2^63 far past any row's).  Integer sums do not depend on their order, so the split over
-// threads cannot change a token.  A weight is rounded to that unit once: weights from
+// The draw wants the least v with C_v > u C: a border decided by sums of many thousand
+// numbers, so the weights are summed as integers, multiples of 2^-46.  Integer sums do not depend
+// on their order, so the split over threads cannot change a token.  64 bits hold sums below
+// 2^18; larger ones (rows that are no probabilities) stay at the largest number, in any order
+// too, and are reported as a row without weights is.  A weight is rounded to that unit once: weights from
 // 2^-23 on (1.2e-7) are exact, the error of a row's sum is about 1e-12.
 //
 // The weight of an entry with p > q, in f32 operations: d = p - q rounded, and its error e =
@@ -82,7 +83,10 @@ __device__ __forceinline__ uint64_t share_of(float u, uint64_t total) {
 
 constexpr int kVerifyThreads = 256, kVerifyWarps = kVerifyThreads / 32;
 constexpr int kDeepCtas = 4;   // CTAs an SM of the form for few CTAs
-constexpr int kMaxSums = 512;  // sums a CTA keeps of its part of a row
+constexpr int kMaxSums = 1023; // sums a CTA keeps of its part of a row; 256 kMaxSums < 2^18
+constexpr uint64_t kFull = ~uint64_t(0);  // 2^18 or more
+
+__device__ __forceinline__ uint64_t add_sums(uint64_t x, uint64_t y) { return x + y < x ? kFull : x + y; }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -166,7 +170,8 @@ __global__ void __launch_bounds__(kVerifyThreads, U == 1 ? 7 : kDeepCtas) verify
     if (!outside && p.draft) row.q = p.draft + (d0 + a) * p.draft_stride;
     if (!outside && !p.draft) row.hot = d;
   }
-  // This CTA's entries [v0, v1), in blocks of `step` (a multiple of 256).
+  // This CTA's entries [v0, v1), in blocks of `step` (a multiple of 256).  The sum of a block, of up
+  // to 131328 entries, fits 64 bits, and with blocks of 256 that of all of them does.
   const int part = (p.V + ctas - 1) / ctas;
   const int v0 = min(rank * part, p.V), v1 = min(v0 + part, p.V);
   const int step = 256 * ((part + 256 * kMaxSums - 1) / (256 * kMaxSums));
@@ -236,19 +241,28 @@ __global__ void __launch_bounds__(kVerifyThreads, U == 1 ? 7 : kDeepCtas) verify
     }
     if (lane == 0) warps[warp] = own;
     __syncthreads();
-    if (tid == 0) {
+    if (step == 256) {
+      if (tid == 0) {
+        uint64_t x = 0;
+        for (int w = 0; w < kVerifyWarps; ++w) x += warps[w];
+        mine = x;
+      }
+    } else if (warp == 0) {
       uint64_t x = 0;
-      for (int w = 0; w < kVerifyWarps; ++w) x += warps[w];
-      mine = x;
+      for (int k = lane; k < blocks; k += 32) x = add_sums(x, sums[k]);
+#pragma unroll
+      for (int d = 16; d; d >>= 1) x = add_sums(x, __shfl_xor_sync(0xffffffffu, x, d));
+      if (lane == 0) mine = x;
     }
     cluster_sync();
     total = before = 0;
     for (int c = 0; c < ctas; ++c) {
       const uint64_t x = peer_load(&mine, c);
-      if (c < rank) before += x;
-      total += x;
+      if (c < rank) before = add_sums(before, x);
+      total = add_sums(total, x);
     }
   }
+  if (total == kFull) total = 0;  // no token's
   const uint64_t own = mine;
   uint64_t want = share_of(u, total);
   if (want >= total && total) want = total - 1;  // u >= 1 (outside the contract): the last entry with a weight

@@ -1,5 +1,7 @@
 """verify_drafts on the GPU against exact rational arithmetic: accepted counts and tokens
 are equal, whatever the sizes."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -162,3 +164,26 @@ def test_repeats_agree_and_replay():
     s["uniforms"][:] = 0
     want = TK.verify(s["target"], s["draft"], s["tokens"], s["indptr"], s["uniforms"])
     assert args[5].tolist() == want[0] and args[6].tolist() == want[1]
+
+
+@pytest.mark.parametrize("V", [131072, 200001, 262143])
+def test_rows_that_sum_far_past_one(V):
+    """Weights of 1 everywhere: sums of V, in units of 2^-46 up to 64 bits."""
+    s = dict(target=np.ones((1, V), dtype=np.float32), draft=None, tokens=np.zeros(0), indptr=[0, 0])
+    for u in (0.0, 0.37, 1 - 2.0 ** -24):
+        s["uniforms"] = np.array([u], dtype=np.float32)
+        # the least v with v + 1 > u V
+        want = int(Fraction(float(s["uniforms"][0])) * V)
+        assert _run(s) == ([0], [want], 0)
+
+
+@pytest.mark.parametrize("V,ones", [(262144, 262144), (300000, 300000), (1100003, 1100003), (1100003, 262144), (1100003, 262145),
+                                    (2200003, 300000), (2200003, 2200003)])
+def test_sums_that_64_bits_do_not_hold(V, ones):
+    """A sum of 2^18 or more is no token's: -1 and a fault, in a batch whose other rows are drawn."""
+    target = np.zeros((3, V), dtype=np.float32)
+    target[0, 17], target[2, V - 1] = 0.5, 0.25
+    target[1, V - ones:] = 1.0
+    s = dict(target=target, draft=None, tokens=np.zeros(0), indptr=[0, 0, 0, 0],
+             uniforms=np.array([0.3, 0.3, 0.9], dtype=np.float32))
+    assert _run(s) == ([0, 0, 0], [17, -1, V - 1], 4)
