@@ -85,7 +85,8 @@ typedef enum {
 } psd_decline_reason;
 
 /* Device-fault flag bits written by kernels into the workspace's fault word (its
- * first 8 bytes, tagged with the call that wrote them; psd_check_device_error). */
+ * first 8 bytes, tagged with the call that wrote them, or the next 8 for replays of a
+ * captured call; psd_check_device_error). */
 enum {
   PSD_FAULT_PAGE_ID = 1,      /* a page id outside [0, num_pages) was skipped */
   PSD_FAULT_WAIT_TIMEOUT = 2, /* a bounded barrier wait gave up */
@@ -668,7 +669,8 @@ psd_status psd_plan_multi_token(const psd_page_table *host, const int32_t *q_ind
  * o must not overlap q or the pools.
  * workspace: >= psd_multi_token_workspace_bytes(ctx, D) bytes, 16-byte aligned, reusable
  * by calls on one stream; calls that may overlap (other streams, captured graphs that
- * may run at the same time) need their own.  psd_check_device_error reports its faults.
+ * may run at the same time) need their own.  psd_check_device_error reports its faults, and
+ * those of a replay whatever calls came after its capture.
  * Captured into a graph, a call replays with the plan it was captured with.  The lists
  * travel in the launches' parameters, so no staging memory is read at replay. */
 typedef struct {
@@ -728,7 +730,10 @@ psd_status verify_drafts(psd_ctx *ctx, const psd_verify_args *args, psd_stream_t
  * only faults of this context's latest decode call on `workspace` are reported, so
  * nothing has to clear it between calls and a fresh workspace needs no
  * initialisation.  The context remembers its 64 most recently used workspaces;
- * an older one reads as clean.  A reported fault is cleared. */
+ * an older one reads as clean.  Replays of captured multi_token_decode calls have a word of
+ * their own (the next 8 bytes), tagged with this context, which gathers their faults until
+ * they are reported (or another entry point is given the workspace).  A reported fault is
+ * cleared. */
 psd_status psd_check_device_error(psd_ctx *ctx, void *workspace, psd_stream_t stream,
                                   int32_t *fault_bits);
 

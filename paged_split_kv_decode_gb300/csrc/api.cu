@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <algorithm>
+#include <atomic>
 #include <cstring>
 #include <string>
 #include <vector>
@@ -291,6 +292,8 @@ extern "C" psd_status psd_create(psd_ctx **out, int device) {
     return fail(PSD_ERR_CUDA, "driver entry point cuTensorMapEncodeTiled unavailable");
   }
   c->dev.encode_tiled = fn;
+  static std::atomic<uint32_t> contexts{0};
+  c->replay_tag = 0x72706c79u + contexts.fetch_add(1, std::memory_order_relaxed);  // not 0 nor all ones, what memory often holds
   for (int i = 0; i < 2; ++i) {
     e = cudaEventCreateWithFlags(&c->staging_done[i], cudaEventDisableTiming);
     if (e != cudaSuccess) {
@@ -862,14 +865,15 @@ extern "C" psd_status psd_check_device_error(psd_ctx *ctx, void *workspace, psd_
   if (!ctx || !workspace) return fail(PSD_ERR_INVALID_ARG, "NULL");
   DeviceGuard g(ctx->dev.device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  unsigned long long word = 0;
-  cudaError_t e = cudaMemcpyAsync(&word, workspace, sizeof(word), cudaMemcpyDeviceToHost, s);
+  unsigned long long word[2] = {0, 0};  // of calls, of replays
+  cudaError_t e = cudaMemcpyAsync(word, workspace, sizeof(word), cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "psd_check_device_error: %s", cudaGetErrorString(e));
-  // only the bits of this context's latest call on the workspace count
+  // only the bits of this context's latest call on the workspace count, and of its replays
   const int slot = ctx->epoch_slot(workspace);
-  const bool latest = slot >= 0 && ctx->ws_epoch[slot] == uint32_t(word >> 32);
-  const int32_t flag = latest ? int32_t(uint32_t(word)) : 0;
+  const bool latest = slot >= 0 && ctx->ws_epoch[slot] == uint32_t(word[0] >> 32);
+  const bool replayed = ctx->replay_tag == uint32_t(word[1] >> 32);
+  const int32_t flag = (latest ? int32_t(uint32_t(word[0])) : 0) | (replayed ? int32_t(uint32_t(word[1])) : 0);
   if (fault_bits) *fault_bits = flag;
   if (flag) {
     e = cudaMemsetAsync(workspace, 0, sizeof(word), s);

@@ -41,6 +41,9 @@ struct psd_ctx {
   const void *ws_ptr[kEpochSlots] = {};
   uint32_t ws_epoch[kEpochSlots] = {};
   int ws_next = 0;
+  // What calls captured into graphs carry instead: a replay's launches keep the tag of their
+  // capture, which is no longer the latest call's, so it is one tag for all of them.
+  uint32_t replay_tag = 0;
   // the slot of workspace `ws`, or -1
   int epoch_slot(const void *ws) const {
     for (int i = 0; i < kEpochSlots; ++i)
@@ -62,6 +65,17 @@ inline FaultRef next_fault(psd_ctx *c, void *ws) {
   }
   c->ws_epoch[i] = c->epoch;
   return FaultRef{static_cast<unsigned long long *>(ws), c->epoch};
+}
+// The same for a call on stream `s` that may be captured: replays write the workspace's second
+// word, where neither the tag of a later call nor its faults meet theirs.
+inline FaultRef next_fault(psd_ctx *c, void *ws, cudaStream_t s) {
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+    cudaGetLastError();  // the legacy stream beside another's capture: this call's launch reports it
+    capture = cudaStreamCaptureStatusNone;
+  }
+  if (capture == cudaStreamCaptureStatusNone) return next_fault(c, ws);
+  return FaultRef{static_cast<unsigned long long *>(ws) + 1, c->replay_tag};
 }
 // Records timing event `i` (0..5) of the context on stream `s` when timing is on.
 inline void time_mark(psd_ctx *c, int i, cudaStream_t s) {

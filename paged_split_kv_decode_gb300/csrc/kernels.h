@@ -25,7 +25,8 @@ struct DeviceInfo {
   int64_t test_wait_limit = 0;
 };
 
-// The workspace's fault word: 64 bits at its start, (epoch << 32) | fault bits.  The
+// The workspace's fault word: 64 bits at its start (replays of a captured call: the next 64, with
+// the context's tag in place of the epoch), (epoch << 32) | fault bits.  The
 // kernels of one call carry that call's epoch; a kernel that flags a fault ORs its
 // bits in when the word holds its epoch and replaces the word otherwise, so the word
 // needs no clearing before a call, and bits left by an earlier call (or whatever a

@@ -382,7 +382,7 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   p.tree = a->tree_mask;
   p.o = o;
   p.lse = lse;
-  p.fault = next_fault(ctx, workspace);
+  p.fault = next_fault(ctx, workspace, s);
   p.q_stride = a->q_stride;
   p.num_pages = a->num_pages;
   p.num_tokens = a->num_tokens;

@@ -430,3 +430,49 @@ def test_refusals():
     refused(1, fresh(), plan=broken)
     empty = psd.plan_multi_token(psd.HostTable([0], [], [], 16), [0])
     psd.multi_token_decode(ctx(), fresh(), empty, o, lse, ws)   # nothing to do
+
+
+@pytest.mark.parametrize("D", [64, 40])
+def test_faults_of_replays_and_of_calls_on_one_workspace(D):
+    """A bad page id (skipped by the kernel's own check) of a replay is reported whatever calls came
+    after the capture, and a replay leaves an unread fault of a call."""
+    s = Step([2, 3], [100, 40], D=D, seed=80)
+    q, k, v, idx = s.q.cuda(), s.k.cuda(), s.v.cuda(), torch.from_numpy(s.page_indices).cuda()
+    good, bad = idx.clone(), idx.clone()
+    bad[1] = s.num_pages + 9
+    args = psd.multi_token_args(q, k, v, idx, sm_scale=s.sm_scale)
+    plan = psd.plan_multi_token(psd.HostTable(s.page_indptr, s.page_indices, s.last, s.page), s.q_indptr)
+    ws = psd.multi_token_workspace(ctx(), plan, s.D, "cuda")
+    ws.fill_(255)
+    o, lse = torch.empty((s.T, s.Hq, D), device="cuda"), torch.empty((s.T, s.Hq), device="cuda")
+    call = lambda: psd.multi_token_decode(ctx(), args, plan, o, lse, ws)  # noqa: E731
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g.replay)
+
+    def check(*runs):
+        for ids, run in runs:
+            idx.copy_(ids)
+            run()
+        return psd.check_device_error(ctx(), ws)
+
+    def flagged(*runs):
+        with pytest.raises(psd.PsdError) as e:
+            check(*runs)
+        assert e.value.status == 4 and e.value.fault_bits == 1
+        assert psd.check_device_error(ctx(), ws) == 0     # a reported fault is cleared
+
+    first, second = graphs
+    assert check((good, first)) == 0
+    flagged((bad, first))
+    flagged((good, call), (bad, first))                   # the context's latest call is another
+    flagged((bad, first), (good, call))                   # the call does not take the replay's fault
+    flagged((bad, first), (good, second))
+    flagged((bad, call), (good, first))                   # nor the replay the call's
+    flagged((bad, call), (bad, second))
+    assert check((bad, call), (good, call)) == 0          # a call's faults are the latest call's
+    assert check((good, first), (good, call), (good, second)) == 0
