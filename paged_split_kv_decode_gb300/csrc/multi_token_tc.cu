@@ -735,7 +735,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             for (int k = 0; k < 4; ++k) top = max3(top, fabsf(bf16_lo(y[k])), fabsf(bf16_hi(y[k])));
           }
         }
-        const int e = min(100, max(-114, 14 - (int(__float_as_uint(top) >> 23) - 127)));
+        // the factor stays a normal number: times a score of -inf, 0 would be NaN (a row so small beside
+        // the scale scores 0 anyway)
+        const int most = min(100, int(__float_as_uint(p.q_scale) >> 23) - 1);
+        const int e = min(most, max(-114, 14 - (int(__float_as_uint(top) >> 23) - 127)));
         const float f = __uint_as_float(uint32_t(127 + e) << 23);
         f_inv = __uint_as_float(uint32_t(127 - e) << 23);
         const uint32_t q_col = lane_base + L::kColQ + slot * (D / 2);

@@ -476,3 +476,13 @@ def test_faults_of_replays_and_of_calls_on_one_workspace(D):
     flagged((bad, call), (bad, second))
     assert check((bad, call), (good, call)) == 0          # a call's faults are the latest call's
     assert check((good, first), (good, call), (good, second)) == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("sm_scale", [2.0 ** -60, 2.0 ** -120])
+def test_small_scales_beside_rows_of_zeros(kv, sm_scale):
+    """Scores of almost 0: every visible key weighs the same, hidden ones nothing."""
+    s = Step([5, 40], [100, 300], kv=kv, seed=81)
+    s.q[[0, 2, 30]] = 0.0
+    s.q[3] = 2.0 ** -100
+    _check(s, sm_scale=sm_scale, out_f32=True)
