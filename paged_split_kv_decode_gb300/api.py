@@ -38,6 +38,17 @@ def _stream(stream) -> C.c_void_p:
     return C.c_void_p(int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _new_fault(device, stream) -> torch.Tensor:
+    """An int32 fault word that is 0 before what comes next on the call's stream."""
+    if stream is None or torch.device(device).type != "cuda":
+        return torch.zeros(1, dtype=torch.int32, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if int(stream) \
+            else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(1, dtype=torch.int32, device=device)
+
+
 def _dev_ptr(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -344,7 +355,7 @@ def rope_append_kv(ctx: Context, q, k_nope, k_rope, v, cos_sin, positions, slot_
     Hkv, D].  Returns the int32 fault word tensor (the one given, or a new zero one)."""
     T = int(positions.numel())
     if fault is None:
-        fault = torch.zeros(1, dtype=torch.int32, device=k_pool.device)
+        fault = _new_fault(k_pool.device, stream)
     for name, t in (("positions", positions), ("slot_mapping", slot_mapping)):
         if t.dtype != torch.int32:
             raise TypeError(f"{name} must be int32")
@@ -498,7 +509,7 @@ def append_tokens(ctx: Context, q, k, v, q_out, *, q_indptr, kv_len, page_indptr
         v_ptr, v_stride = v.data_ptr(), _row_stride(v, vs, "v", bf16, dev)
         v_pool_ptr = _flat(v_pool, "v_pool", pool_type, dev)
     if fault is None:
-        fault = torch.zeros(1, dtype=i32, device=k_pool.device)
+        fault = _new_fault(k_pool.device, stream)
     tables = (_flat(q_indptr, "q_indptr", i32, dev), _flat(kv_len, "kv_len", i32, dev),
               0 if positions is None else _flat(positions, "positions", i32, dev),
               _flat(page_indptr, "page_indptr", i32, dev), _flat(page_indices, "page_indices", i32, dev))
@@ -612,7 +623,7 @@ def verify_drafts(ctx: Context, target_probs, draft_probs, draft_tokens, draft_i
     rows, V = shape
     t_stride = _row_stride(target_probs, shape, "target_probs", f32, dev)
     if fault is None:
-        fault = torch.zeros(1, dtype=i32, device=target_probs.device)
+        fault = _new_fault(target_probs.device, stream)
     ptrs = (_flat(draft_tokens, "draft_tokens", i32, dev), _flat(draft_indptr, "draft_indptr", i32, dev),
             _flat(uniforms, "uniforms", f32, dev))
     outs = (_flat(num_accepted, "num_accepted", i32, dev), _flat(out_tokens, "out_tokens", i32, dev),

@@ -230,3 +230,20 @@ def test_graph_replay_on_another_stream():
     call(want)
     assert torch.equal(q_out[:4], want[:4])
     assert torch.equal(pools[0], s["k_pool"]) and torch.equal(pools[1], s["v_pool"]) and int(fault) == 0
+
+
+def test_a_new_fault_word_on_the_stream_of_the_call():
+    """The word that a call makes for itself starts at 0 in the call's stream, whatever the current
+    stream is busy with."""
+    s = _make([2, 2], [3, 16], fused=False, pad_rows=0)
+    s["page_indices"][0] = 10 ** 6                       # skipped by the kernel's own check
+    rope, q_out = psd.rope_frequencies(64), torch.empty_like(s["q"])
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)                   # the current stream, some 50 ms
+        f = psd.append_tokens(ctx(), s["q"], s["k"], s["v"], q_out, q_indptr=s["q_indptr"], kv_len=s["kv_len"],
+                              page_indptr=s["page_indptr"], page_indices=s["page_indices"], k_pool=s["k_pool"],
+                              v_pool=s["v_pool"], rope=rope, neox=True, stream=stream)
+        torch.cuda.synchronize()
+        assert int(f) == 1

@@ -136,3 +136,20 @@ def test_scalar_form_for_narrow_rotary(neox):
     st.rot_dim = 8
     st.cos_sin = synth.rope_cos_sin_table(st.cos_sin.shape[0], 8)
     _compare(st)
+
+
+def test_a_new_fault_word_on_the_stream_of_the_call():
+    """The word that a call makes for itself starts at 0 in the call's stream, whatever the current
+    stream is busy with."""
+    st = synth.append_step(seed=12, kind="gqa", T=4, num_pages=128)
+    dev = lambda t: None if t is None else t.cuda().contiguous()  # noqa: E731
+    args = [dev(st.q), dev(st.k_nope), dev(st.k_rope), dev(st.v), torch.from_numpy(st.cos_sin).cuda(),
+            torch.full((4,), st.cos_sin.shape[0], dtype=torch.int32, device="cuda"),     # past the table: skipped
+            torch.from_numpy(st.slot_mapping).cuda(), dev(st.k_pool), dev(st.v_pool)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                       # the current stream, some 50 ms
+    f = psd.rope_append_kv(ctx(), *args, rot_dim=st.rot_dim, neox=st.neox, q_rope_col=st.q_rope_col,
+                           page_size=st.page_size, k_scale=st.k_scale, v_scale=st.v_scale, stream=side)
+    torch.cuda.synchronize()
+    assert int(f) == 4

@@ -187,3 +187,15 @@ def test_sums_that_64_bits_do_not_hold(V, ones):
     s = dict(target=target, draft=None, tokens=np.zeros(0), indptr=[0, 0, 0, 0],
              uniforms=np.array([0.3, 0.3, 0.9], dtype=np.float32))
     assert _run(s) == ([0, 0, 0], [17, -1, V - 1], 4)
+
+
+def test_a_new_fault_word_on_the_stream_of_the_call():
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    p = torch.full((2, 16), 1 / 16, device="cuda")
+    args = [p, None, i32(99), i32(0, 1), torch.zeros(2, device="cuda"), i32(0), i32(0, 0)]   # a token outside
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)                       # the current stream, some 50 ms
+    f = psd.verify_drafts(ctx(), *args, stream=side)
+    torch.cuda.synchronize()
+    assert int(f) == 4
