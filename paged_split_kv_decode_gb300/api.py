@@ -389,13 +389,29 @@ def rope_append_kv(ctx: Context, q, k_nope, k_rope, v, cos_sin, positions, slot_
 
 class RopeFrequencies:
     """Rotary frequencies for append_tokens: inv_freq [rot_dim / 2] float64 and the factor on
-    cos and sin.  `rope_frequencies` makes them; a caller's own go in as they are."""
+    cos and sin.  `rope_frequencies` makes them; a caller's own go in as they are (copied)."""
 
     def __init__(self, inv_freq, magnitude: float = 1.0):
-        self.inv_freq = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64).reshape(-1))
+        self.inv_freq = inv_freq
         self.magnitude = float(magnitude)
-        self.rot_dim = 2 * int(self.inv_freq.shape[0])
-        self.address = self.inv_freq.ctypes.data
+
+    @property
+    def inv_freq(self) -> np.ndarray:
+        return self._f
+
+    @inv_freq.setter
+    def inv_freq(self, f):
+        # the address is kept (numpy takes a microsecond for it) and changes with the array
+        self._f = np.array(f, dtype=np.float64).reshape(-1)
+        self._address = self._f.ctypes.data
+
+    @property
+    def rot_dim(self) -> int:
+        return 2 * self._f.shape[0]
+
+    @property
+    def address(self) -> int:
+        return self._address
 
 
 def rope_frequencies(rot_dim: int, *, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,

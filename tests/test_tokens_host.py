@@ -104,3 +104,25 @@ def test_oracle_verification_keeps_the_target_distribution():
                 _, out = TK.verify(np.stack([p, p]).astype(np.float32), q[None].astype(np.float32), [d], [0, 1], u)
                 mass[out[0]] += q[d] / N / N
     assert np.allclose(mass, p, atol=1 / N)
+
+
+def test_replaced_frequencies_are_the_ones_in_use(psd):
+    """The address and width a call passes on are those of the array that is there."""
+    import ctypes
+
+    def in_use(r):
+        return list((ctypes.c_double * (r.rot_dim // 2)).from_address(r.address))
+
+    r = psd.rope_frequencies(64)
+    assert in_use(r) == list(r.inv_freq) and r.rot_dim == 64
+    r.inv_freq = [1.0, 0.5, 0.25]
+    assert r.rot_dim == 6 and in_use(r) == [1.0, 0.5, 0.25]
+    own = np.array([0.5, 0.125])
+    r.inv_freq = own
+    own[0] = 7.0                                     # the caller's array stays the caller's
+    assert in_use(r) == [0.5, 0.125] == list(r.inv_freq)
+    r.inv_freq[1] = 2.0
+    assert in_use(r) == [0.5, 2.0]
+    for name in ("rot_dim", "address"):
+        with pytest.raises(AttributeError):
+            setattr(r, name, 2)
