@@ -637,7 +637,7 @@ typedef struct {
   int32_t token0;   /* the request's first token row */
   int32_t num_new;  /* n_b */
   int32_t page_off; /* position of its first page in page_indices */
-  int32_t kv_len;   /* L_b */
+  int32_t kv_len;   /* L_b, at most 2^31 - 256 */
 } psd_token_request;
 typedef struct {
   int32_t batch_capacity;      /* in */

@@ -364,8 +364,8 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   int64_t row = 0;
   for (int32_t b = 0; b < plan->batch; ++b) {
     const psd_token_request &r = plan->requests[b];
-    if (r.token0 != row || r.num_new < 0 || r.kv_len < 1 || r.num_new > r.kv_len || r.page_off < 0 ||
-        (a->tree_mask && r.num_new > 64) ||
+    if (r.token0 != row || r.num_new < 0 || r.kv_len < 1 || r.kv_len > kMaxKvLen || r.num_new > r.kv_len ||
+        r.page_off < 0 || (a->tree_mask && r.num_new > 64) ||
         int64_t(r.page_off) + (int64_t(r.kv_len) + a->page_size - 1) / a->page_size > a->num_page_indices)
       return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: request %d of the plan", b);
     row += r.num_new;

@@ -19,6 +19,10 @@ psd_status fail(psd_status st, const char *fmt, ...);
 
 psd_status validate_table(const psd_page_table *t, int64_t num_pages);
 
+// Tokens of a request in a multi-token step: its last tile of up to 128 keys, and the tokens of
+// two row tiles past its last, are counted in 32 bits.
+constexpr int32_t kMaxKvLen = 0x7fffff00;
+
 // Workspace layout (all offsets 256-byte aligned):
 //   [0, 256)        header: int32 fault flag at offset 0
 //   lists           work items, CTA order, members, member_row_base, o_indptr

@@ -70,7 +70,7 @@ extern "C" psd_status psd_plan_multi_token(const psd_page_table *host, const int
     if (n < 0 || n > len)
       return fail(PSD_ERR_INVALID_ARG, "psd_plan_multi_token: request %d has %lld new tokens of %lld", b, (long long)n,
                   (long long)len);
-    if (len > 0x7fffff00LL) return fail(PSD_ERR_INVALID_ARG, "psd_plan_multi_token: request %d too long", b);
+    if (len > kMaxKvLen) return fail(PSD_ERR_INVALID_ARG, "psd_plan_multi_token: request %d too long", b);
     plan->requests[b] = psd_token_request{q_indptr[b], int32_t(n), host->page_indptr[b], int32_t(len)};
     most = std::max(most, int32_t(n));
   }

@@ -486,3 +486,19 @@ def test_small_scales_beside_rows_of_zeros(kv, sm_scale):
     s.q[[0, 2, 30]] = 0.0
     s.q[3] = 2.0 ** -100
     _check(s, sm_scale=sm_scale, out_f32=True)
+
+
+@pytest.mark.parametrize("D", [64, 40])
+def test_a_plan_of_ones_own_past_the_planners_lengths(D):
+    """psd_plan_multi_token takes up to 2^31 - 256 tokens a request, and so does the call."""
+    s = Step([1], [3], D=D, seed=82)
+    plan = psd.plan_multi_token(psd.HostTable(s.page_indptr, s.page_indices, s.last, s.page), s.q_indptr)
+    args = psd.multi_token_args(s.q.cuda(), s.k.cuda(), s.v.cuda(), torch.from_numpy(s.page_indices).cuda(),
+                                sm_scale=s.sm_scale)
+    args.page_size, args.num_pages, args.num_page_indices, plan.c.page_size = 1 << 30, 1, 2, 1 << 30
+    o, ws = torch.empty((s.T, s.Hq, D), device="cuda"), psd.multi_token_workspace(ctx(), plan, D, "cuda")
+    for length in (2 ** 31 - 1, 2 ** 31 - 255):      # nothing is launched
+        plan.requests_a[0].kv_len = length
+        with pytest.raises(psd.PsdError) as e:
+            psd.multi_token_decode(ctx(), args, plan, o, None, ws)
+        assert e.value.status == 1
