@@ -616,7 +616,7 @@ typedef struct {
   int32_t Hq, Hkv, D, Dv;
   int32_t rot_col, rot_dim, neox;/* rot_dim even, in [2, 512], rot_col + rot_dim <= D */
   const double *inv_freq;        /* host [rot_dim / 2], finite, >= 0 */
-  double magnitude;              /* finite */
+  double magnitude;              /* finite in f32 */
   const int32_t *q_indptr;       /* device [batch + 1] */
   const int32_t *kv_len;         /* device [batch]: L_b, the new tokens included */
   const int32_t *positions;      /* device [T] or NULL */

@@ -443,7 +443,8 @@ extern "C" psd_status append_tokens(psd_ctx *ctx, const psd_append_args *a, psd_
   if (a->kv_dtype == PSD_FP8_E4M3 &&
       !(std::isfinite(a->k_scale) && a->k_scale > 0.f && std::isfinite(a->v_scale) && a->v_scale > 0.f))
     return fail(PSD_ERR_INVALID_ARG, "append_tokens: fp8 scales must be finite and > 0");
-  if (!std::isfinite(a->magnitude)) return fail(PSD_ERR_INVALID_ARG, "append_tokens: magnitude must be finite");
+  if (!std::isfinite(float(a->magnitude)))
+    return fail(PSD_ERR_INVALID_ARG, "append_tokens: magnitude must be finite in f32");
   for (int i = 0; i < a->rot_dim / 2; ++i)
     if (!(a->inv_freq[i] >= 0.0) || !std::isfinite(a->inv_freq[i]))
       return fail(PSD_ERR_INVALID_ARG, "append_tokens: inv_freq[%d] must be finite and >= 0", i);

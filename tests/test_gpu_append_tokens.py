@@ -247,3 +247,14 @@ def test_a_new_fault_word_on_the_stream_of_the_call():
                               v_pool=s["v_pool"], rope=rope, neox=True, stream=stream)
         torch.cuda.synchronize()
         assert int(f) == 1
+
+
+def test_a_magnitude_that_f32_does_not_hold():
+    s = _make([2], [3], pad_rows=0)
+    before = s["k_pool"].clone()
+    for magnitude in (1e39, -1e39):
+        with pytest.raises(psd.PsdError) as e:
+            _call(s, psd.RopeFrequencies([0.5, 0.25], magnitude), neox=True)
+        assert e.value.status == 1
+    assert torch.equal(s["k_pool"], before)
+    _check(s, psd.RopeFrequencies([0.5, 0.25], -3.0))
