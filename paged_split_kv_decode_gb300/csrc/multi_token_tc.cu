@@ -543,6 +543,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           ok = b < 0 || wait_bounded(bar(b), uint32_t(lane == 0 ? i / NC : i / NS - 1) & 1u, p.wait_limit);
           ok = __all_sync(0xffffffffu, ok) != 0;
           if (!ok) break;
+          __syncwarp();  // (a vote orders no memory: what two lanes have seen holds for all from here on)
         }
         const uint8_t *src = sm + L::kOffRaw + rs * L::kRawBytes;
         uint8_t *dst = sm + st * L::kTileBytes;
