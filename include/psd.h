@@ -683,7 +683,7 @@ typedef struct {
   int32_t Hq, Hkv, D, page_size;
   int32_t kv_dtype;                /* PSD_BF16 or PSD_FP8_E4M3 */
   float k_scale, v_scale;          /* fp8 only: finite */
-  float sm_scale;                  /* finite */
+  float sm_scale;                  /* finite, and so sm_scale * log2(e) * k_scale */
   const uint64_t *tree_mask;       /* device [num_tokens] or NULL */
   int32_t out_f32;                 /* o is f32 (1) or bf16 (0) */
 } psd_multi_token_args;

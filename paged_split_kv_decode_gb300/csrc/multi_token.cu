@@ -344,8 +344,10 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   if (a->kv_dtype != PSD_BF16 && a->kv_dtype != PSD_FP8_E4M3)
     return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: kv_dtype %d", a->kv_dtype);
   const bool fp8 = a->kv_dtype == PSD_FP8_E4M3;
-  if (!std::isfinite(a->sm_scale) || (fp8 && (!std::isfinite(a->k_scale) || !std::isfinite(a->v_scale))))
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: scales must be finite");
+  const float q_scale = a->sm_scale * 1.4426950408889634f * (fp8 ? a->k_scale : 1.f);
+  if (!std::isfinite(a->sm_scale) || (fp8 && (!std::isfinite(a->k_scale) || !std::isfinite(a->v_scale))) ||
+      !std::isfinite(q_scale))
+    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: scales and sm_scale * log2(e) * k_scale must be finite");
   if (a->q_stride < int64_t(a->Hq) * a->D || a->q_stride % 8)
     return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: q_stride must be a multiple of 8 and >= Hq * D");
   if (a->tree_mask && plan->max_new > 64)
@@ -393,7 +395,7 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   p.page_size = a->page_size;
   p.fp8 = fp8;
   p.out_f32 = a->out_f32 != 0;
-  p.q_scale = a->sm_scale * 1.4426950408889634f * (fp8 ? a->k_scale : 1.f);
+  p.q_scale = q_scale;
   p.v_scale = fp8 ? a->v_scale : 1.f;
   float *const base = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256);
   const StepPlace place = step_tc_place(ctx->dev.num_sms, a->D, base);

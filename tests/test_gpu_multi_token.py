@@ -502,3 +502,12 @@ def test_a_plan_of_ones_own_past_the_planners_lengths(D):
         with pytest.raises(psd.PsdError) as e:
             psd.multi_token_decode(ctx(), args, plan, o, None, ws)
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("kv,sm_scale,k_scale", [("bf16", 3e38, 1.0), ("fp8", 1e20, 1e20), ("fp8", -1e20, 1e20)])
+def test_scales_whose_product_f32_does_not_hold(kv, sm_scale, k_scale):
+    s = Step([2], [30], kv=kv, seed=83)
+    s.scales, s.sm_scale = (k_scale, 1.0), sm_scale
+    with pytest.raises(psd.PsdError) as e:
+        _run(s)
+    assert e.value.status == 1
