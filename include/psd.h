@@ -553,8 +553,8 @@ psd_status rope_append_kv(psd_ctx *ctx, const psd_rope_append_args *args, psd_st
  *
  * Request b owns the token rows [q_indptr[b], q_indptr[b+1]); its page table covers
  * L_b tokens INCLUDING the new ones, so its new token i sits at index
- * P_b + i, P_b = L_b - n_b.  Rows from q_indptr[B] on belong to no request: they are
- * neither read nor written. */
+ * P_b + i, P_b = L_b - n_b.  Rows from q_indptr[B] on (up to num_tokens) belong to no request:
+ * inputs' may be read, whatever they hold, and decide nothing; outputs' are not written. */
 
 /* Rotary frequencies, scaled for long contexts (host, 64 bits).  With r = rot_dim,
  * f_i = base^(-2 i / r), i < r/2:
