@@ -709,7 +709,9 @@ psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *args,
  * negative) count as 0, larger than 1 as 1.  A draft token outside [0, vocab)
  * is refused, its q is 0 everywhere, and PSD_FAULT_RANGE is set.  It is also set for a row
  * whose weights are all 0 or sum to 2^18 or more (64 bits of sums hold less): its new token
- * is -1.  Rows with no request are not touched. */
+ * is -1.  A request whose offsets are out of range (draft_indptr decreases, or leaves
+ * [0, num_drafts]) sets PSD_FAULT_RANGE and its outputs stay as they were, as do rows with no
+ * request. */
 typedef struct {
   const float *target_probs;   /* device [num_drafts + batch, vocab] */
   const float *draft_probs;    /* device [num_drafts, vocab] or NULL */
