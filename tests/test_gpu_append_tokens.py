@@ -258,3 +258,76 @@ def test_a_magnitude_that_f32_does_not_hold():
         assert e.value.status == 1
     assert torch.equal(s["k_pool"], before)
     _check(s, psd.RopeFrequencies([0.5, 0.25], -3.0))
+
+
+MANY = dict(new=[300, 1, 0, 450, 76, 2, 113], before=[3, 500, 20, 0, 61, 16, 15])   # two tokens a CTA, the last alone
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("neox", [True, False])
+@pytest.mark.parametrize("D,rot,col", [(64, 64, 0), (128, 64, 64), (128, 32, 16), (256, 128, 0)])
+def test_many_tokens_of_every_layout(kv, neox, D, rot, col):
+    s = _make(**MANY, Hq=4, Hkv=2, D=D, kv=kv, seed=D + rot, pad_rows=3)
+    rng = np.random.default_rng(D)
+    scales = dict(k_scale=0.03, v_scale=0.017) if kv == "fp8" else {}
+    _check(s, psd.rope_frequencies(rot), neox=neox, rope_col=col, **scales)
+    far = [int(x) for x in rng.integers(0, 2 ** 31, s["q"].shape[0])]
+    _check(s, psd.rope_frequencies(rot, scaling="yarn", factor=8.0, original_max_position=4096), neox=neox,
+           rope_col=col, positions=far, **scales)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("Dv", [128, 40, 20])
+def test_values_of_another_width(Dv, many, kv):
+    shape = MANY if many else dict(new=[3, 1, 0, 17], before=[0, 40, 9, 15])
+    scales = dict(k_scale=0.03, v_scale=0.017) if kv == "fp8" else {}
+    _check(_make(**shape, Hq=4, Hkv=2, D=64, Dv=Dv, kv=kv, seed=Dv), psd.rope_frequencies(32), **scales)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("D,rot,col", [(192, 64, 128), (40, 10, 7)])
+def test_keys_alone(D, rot, col, many, kv):
+    """No values (they lie in the key rows): queries and keys as with values, bit for bit."""
+    shape = MANY if many else dict(new=[3, 1, 0, 17], before=[0, 40, 9, 15])
+    s = _make(**shape, Hq=8, Hkv=1, D=D, kv=kv, seed=D)
+    rope, start = psd.rope_frequencies(rot), s["k_pool"].clone()
+    kw = dict(neox=False, rope_col=col, k_scale=0.03)
+    want, fault = _call(s, rope, **kw)
+    keys = s["k_pool"].clone()
+    s["k_pool"].copy_(start)
+    s["v"] = s["v_pool"] = None
+    got, fault2 = _call(s, rope, **kw)
+    assert fault == fault2 == 0
+    assert torch.equal(want, got) and torch.equal(keys, s["k_pool"]) and not torch.equal(keys, start)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_faults_among_many_tokens(kv):
+    """Two tokens a CTA, one of them or both at fault: theirs is left out, the others are what they were."""
+    rope = psd.rope_frequencies(32)
+    make = lambda: _make(**MANY, Hq=4, Hkv=2, D=64, kv=kv, seed=6, pad_rows=0)  # noqa: E731
+    s = make()
+    start = s["k_pool"].clone(), s["v_pool"].clone()
+    T, h = s["q"].shape[0], s["host"]
+    where = TK.positions_of(h["q_indptr"], h["total"])
+    pos = [p for _, p in where]
+    want, fault = _call(s, rope, neox=True)
+    assert fault == 0
+    rows = [int(h["page_indices"][h["page_indptr"][b] + p // h["page"]]) * h["page"] + p % h["page"] for b, p in where]
+    untouched, unwritten = [0, 7, 100, 101, T - 1], [t for t in range(T) if where[t] in {(3, p) for p in range(16, 32)}]
+    for t in untouched:
+        pos[t] = -1 - t
+    bad = make()
+    bad["page_indices"][int(h["page_indptr"][3]) + 1] = 2 ** 31 - 1     # a page of request 3
+    out, fault = _call(bad, rope, neox=True, positions=torch.tensor(pos, dtype=torch.int32, device="cuda"))
+    assert fault == 5 and len(unwritten) == 16
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[untouched] = False
+    assert torch.equal(out[keep], want[keep]) and bool((out[~keep] == 7.0).all())
+    left = [rows[t] for t in untouched + unwritten]
+    for got, good, before in ((bad["k_pool"], s["k_pool"], start[0]), (bad["v_pool"], s["v_pool"], start[1])):
+        expect = good.clone().flatten(0, 1)
+        expect[left] = before.flatten(0, 1)[left]
+        assert torch.equal(got.flatten(0, 1), expect)

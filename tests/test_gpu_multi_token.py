@@ -511,3 +511,70 @@ def test_scales_whose_product_f32_does_not_hold(kv, sm_scale, k_scale):
     with pytest.raises(psd.PsdError) as e:
         _run(s)
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("B,D,page,kv,out_f32", [(600, 40, 16, "bf16", False), (300, 64, 5, "fp8", True), (258, 256, 16, "bf16", True)])
+def test_batches_of_several_launches_of_the_general_kernel(B, D, page, kv, out_f32):
+    """More than 256 requests that have new tokens: the launches share the workspace."""
+    rng = np.random.default_rng(B)
+    new, before = rng.integers(0 if B == 600 else 1, 3, B), rng.integers(1, 40, B)
+    before[[1, B - 1]], new[[1, B - 1]] = 700, 2            # keys split where a launch has few rows
+    assert int((new > 0).sum()) > 256
+    _check(Step(new, before, Hq=2, Hkv=1, D=D, page=page, kv=kv, seed=B), out_f32=out_f32)
+
+
+@pytest.mark.parametrize("D,kv", [(64, "bf16"), (128, "fp8"), (40, "bf16")])
+def test_calls_that_overlap_on_two_streams(D, kv):
+    """Many calls a stream in flight at once, each stream with a workspace of its own."""
+    steps = [Step([3, 60], [800 + 100 * i, 40], D=D, kv=kv, seed=90 + i) for i in range(2)]
+    want, calls = [_run(s) for s in steps], []
+    for s in steps:
+        args = psd.multi_token_args(s.q.cuda(), s.k.cuda(), s.v.cuda(), torch.from_numpy(s.page_indices).cuda(),
+                                    sm_scale=s.sm_scale, k_scale=s.scales[0], v_scale=s.scales[1])
+        plan = psd.plan_multi_token(psd.HostTable(s.page_indptr, s.page_indices, s.last, s.page), s.q_indptr)
+        outs = [(torch.full_like(want[0][0], 5.0), torch.full_like(want[0][1], 5.0)) for _ in range(20)]
+        calls.append((args, plan, psd.multi_token_workspace(ctx(), plan, D, "cuda"), outs, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    torch.cuda._sleep(2_000_000)
+    for *_, stream in calls:
+        stream.wait_stream(torch.cuda.current_stream())     # both begin together
+    for i in range(20):
+        for args, plan, ws, outs, stream in calls:
+            psd.multi_token_decode(ctx(), args, plan, *outs[i], ws, stream=stream)
+    torch.cuda.synchronize()
+    for (args, plan, ws, outs, stream), w in zip(calls, want):
+        assert psd.check_device_error(ctx(), ws) == 0
+        assert all(torch.equal(o, w[0]) and torch.equal(lse, w[1]) for o, lse in outs)
+
+
+def test_fewer_rows_than_the_plan_are_refused():
+    s = Step([2, 70], [3, 4], seed=22, pad_rows=0)
+    plan = psd.plan_multi_token(psd.HostTable(s.page_indptr, s.page_indices, s.last, s.page), s.q_indptr)
+    args = psd.multi_token_args(s.q.cuda()[:71], s.k.cuda(), s.v.cuda(), torch.from_numpy(s.page_indices).cuda(), sm_scale=0.1)
+    ws = psd.multi_token_workspace(ctx(), plan, s.D, "cuda")
+    with pytest.raises(psd.PsdError) as e:
+        psd.multi_token_decode(ctx(), args, plan, torch.empty((71, s.Hq, s.D), device="cuda"), None, ws)
+    assert e.value.status == 1
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_weights_over_fp8_pools_are_good_to_11_bits(D):
+    """Two keys with values 1 and -1: the output is the difference of two nearly equal weights, where a
+    weight's rounding shows beside the output's.  Weights of 8 bits would not pass, which is checked on
+    the host."""
+    s = Step([1] * 20, [1] * 20, Hq=64, Hkv=1, D=D, kv="fp8", spread=0.2, seed=91)
+    for b in range(20):
+        page = s.v[int(s.page_indices[s.page_indptr[b]])]
+        page[0], page[1] = 0x38, 0xB8
+    s.scales = (s.scales[0], 1.0)
+    o, lse = _run(s)
+    want = s.oracle()
+    # `bounds` without a rounding of the weights, and 2^-11 of them (2^-32 of the largest where f16 ends)
+    e_o, e_l = bounds(want, D, 2, False, 0)
+    e_o = e_o + (2.0 ** -11 + 2 * 2.0 ** -32) * want[2] * (1 + 2.0 ** -8)
+    n = int(s.q_indptr[-1])
+    assert bool((np.abs(o[:n].double().cpu().numpy() - want[0]) <= e_o).all())
+    assert bool((np.abs(lse[:n].double().cpu().numpy() - want[1]) <= e_l).all())
+    ratio = (1 - np.abs(want[0])) / (1 + np.abs(want[0]))       # of the smaller weight to the larger
+    coarse = torch.from_numpy(ratio).to(torch.bfloat16).double().numpy()
+    assert bool((np.abs((1 - coarse) / (1 + ratio) - np.abs(want[0])) > e_o).any())

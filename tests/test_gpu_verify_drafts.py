@@ -199,3 +199,53 @@ def test_a_new_fault_word_on_the_stream_of_the_call():
     f = psd.verify_drafts(ctx(), *args, stream=side)
     torch.cuda.synchronize()
     assert int(f) == 4
+
+
+def _check_in_64_bits(s):
+    """Against 64-bit arithmetic, for rows too many or too long for fractions.  The acceptance is exact in
+    it.  A weight in units of 2^-46 may differ by one from the kernel's, so a running sum, and the share
+    of the total it is compared with, by V each: where the borders that leave are further apart than that
+    the token is known, and that has to be nearly always."""
+    accepted, out, fault = _run(s)
+    assert fault == 0
+    V, B, sure = s["target"].shape[1], len(s["indptr"]) - 1, 0
+    f64 = lambda a: a.astype(np.float64)  # noqa: E731
+    for b in range(B):
+        d0, K = int(s["indptr"][b]), int(s["indptr"][b + 1] - s["indptr"][b])
+        R, a = d0 + b, 0
+        while a < K:
+            d = int(s["tokens"][d0 + a])
+            q = 1.0 if s["draft"] is None else float(s["draft"][d0 + a, d])
+            if not float(s["uniforms"][R + a]) * q < float(s["target"][R + a, d]):
+                break
+            a += 1
+        w = f64(s["target"][R + a])
+        if a < K and s["draft"] is not None:
+            w = np.maximum(w - f64(s["draft"][d0 + a]), 0)
+        elif a < K:
+            w[int(s["tokens"][d0 + a])] = 0
+        w = w if w.any() else f64(s["target"][R + a])
+        sums = np.cumsum(np.rint(w * 2.0 ** 46).astype(np.int64))
+        want = int(Fraction(float(s["uniforms"][R + K])) * int(sums[-1]))
+        lo, hi = (min(int(np.searchsorted(sums, x, side="right")), V - 1) for x in (want - 2 * V - 2, want + 2 * V + 2))
+        assert accepted[b] == a and lo <= out[R + a] <= hi
+        assert out[R: R + a] == s["tokens"][d0: d0 + a].tolist() and out[R + a + 1: R + K + 1] == [-1] * (K - a)
+        sure += lo == hi
+    assert sure >= B - B // 8
+
+
+@pytest.mark.parametrize("sampled", [True, False])
+@pytest.mark.parametrize("B,K,V", [(100, 4, 8200), (90, 1, 98305), (200, 2, 4097), (700, 1, 300)])
+def test_batches_of_more_ctas_than_the_sms_hold(B, K, V, sampled):
+    """More than four CTAs an SM: one block of a warp on its way at a time."""
+    rng = np.random.default_rng(B)
+    _check_in_64_bits(_make(rng.integers(0, K + 1, B), V, seed=B, sampled=sampled))
+
+
+@pytest.mark.parametrize("sampled", [True, False])
+@pytest.mark.parametrize("K,V", [([3, 0, 2], 98305), ([1, 2], 131072), ([5] * 20, 30011), ([1], 1100003), ([1], 2200003)])
+def test_long_rows(K, V, sampled):
+    """Blocks for every warp of a CTA, two at a time, and from 2.1 million words on blocks of more than
+    256 entries."""
+    for near in (0.2, 2.0):
+        _check_in_64_bits(_make(K, V, seed=V, sampled=sampled, near=near))
