@@ -763,7 +763,7 @@ def cascade_decode_no_alloc(ctx: Context, args: L.DecodeArgs, plan: Plan, o: tor
 def check_device_error(ctx: Context, workspace: torch.Tensor, stream=None) -> int:
     """psd_check_device_error: raises PsdError on a flagged device fault."""
     bits = C.c_int32()
-    st = L.load().psd_check_device_error(ctx.handle, _dev_ptr(workspace, "workspace"), _stream(stream),
+    st = L.load().psd_check_device_error(ctx.handle, _dev_ptr(workspace, "workspace"), _ctx_stream(ctx, stream),
                                          C.byref(bits))
     if st != L.PSD_OK:
         err = L.PsdError(st, L.load().psd_last_error().decode(errors="replace"))

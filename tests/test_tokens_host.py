@@ -126,3 +126,27 @@ def test_replaced_frequencies_are_the_ones_in_use(psd):
     for name in ("rot_dim", "address"):
         with pytest.raises(AttributeError):
             setattr(r, name, 2)
+
+
+def test_faults_are_read_on_the_stream_of_the_contexts_device(psd, monkeypatch):
+    """multi_token_decode runs on the current stream of its context's device, which need not be the
+    current device; its faults are read behind it on the same stream."""
+    from paged_split_kv_decode_gb300 import api
+    seen = []
+
+    class Library:
+        def psd_check_device_error(self, handle, workspace, stream, bits):
+            seen.append(getattr(stream, "value", stream))
+            return 0
+
+    class Fake:
+        device, handle, _h = 1, None, None
+
+    monkeypatch.setattr(api, "_raw_stream", lambda device: 1000 + device)
+    monkeypatch.setattr(api.torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(api, "_dev_ptr", lambda t, name: 0)
+    monkeypatch.setattr(api.L, "load", lambda: Library())
+    assert api._ctx_stream(Fake, None) == 1001
+    assert api.check_device_error(Fake, None) == 0 and seen == [1001]
+    api.check_device_error(Fake, None, stream=77)
+    assert seen[1] == 77
