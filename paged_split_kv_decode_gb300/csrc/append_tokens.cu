@@ -111,7 +111,7 @@ __device__ __forceinline__ float2 turn(uint64_t F, int pos, float magnitude) {
 }
 
 // One CTA per token, element by element: any width, stride and alignment.
-// (8502 tokens, 32 query and 8 KV heads of 128, 20 columns rotated: 153 us, 1.4 TB/s; issue bounds it.)
+// (8502 tokens, 32 query and 8 KV heads of 128, 20 columns rotated: 157 us, 1.3 TB/s; issue bounds it.)
 __global__ void __launch_bounds__(256)
     append_tokens_kernel(const AppendParams p, const __grid_constant__ Turns turns) {
   __shared__ float2 cs[kMaxPairs];
@@ -171,9 +171,9 @@ __global__ void __launch_bounds__(256)
 // Keys start at the threads that the queries' last round left idle, copies after those: the
 // phases of a CTA overlap (9800 tokens 42.9 us against 47.5 with each phase from thread 0 on, and
 // with 64 of 128 columns rotated and fp8 pools 49.5 against 68.5).
-// 32 query and 8 KV heads of 128, cold caches: one token 6.7 us (a chain of dependent loads:
-// lengths, page id, frequencies, rows), 160 tokens into fp8 pools 8 us, 10784 tokens 47 us (265 MB at
-// 5.6 TB/s, writes and reads mixed).
+// 32 query and 8 KV heads of 128, cold caches: one token 7 us (a chain of dependent loads:
+// lengths, page id, frequencies, rows), 160 tokens into fp8 pools 9 us, 10784 tokens 48 us (265 MB at
+// 5.5 TB/s, writes and reads mixed).
 struct F8 {
   float v[8];
 };

@@ -57,9 +57,9 @@
 // 2^8, so P <= 2^8 (2^15 as f16).
 //
 // Measured, 32 query and 8 KV heads of 128, cold caches, the join beside it: 32 requests of 5 tokens
-// over 512 to 4096 keys 54 + 4 us (286 MB, 0.79 of a plain copy's rate: copies bound it); their f32
-// outputs 84 us; 3 single tokens over 20000 to 65536 keys, f32 outputs, 127 + 6 us (0.74); a
-// 4096-token chunk over 4096 286 + 10 us (1440 TFLOP/s: tensor cores 64 % active, the rest is what one
+// over 512 to 4096 keys 55 + 5 us (286 MB, 0.77 of a plain copy's rate: copies bound it); with f32
+// outputs 85 + 6 us (322 MB); 3 single tokens over 20000 to 65536 keys, f32 outputs, 126 + 8 us (0.75); a
+// 4096-token chunk over 4096 283 + 12 us (1460 TFLOP/s: tensor cores 64 % active, the rest is what one
 // slot's chain of S, softmax and P V leaves uncovered by the other's); fp8 trees as above, bound by that
 // chain over tiles of 64 keys and by the conversion.
 #include <cuda.h>

@@ -130,9 +130,9 @@ struct Row {
 // blocks of `step` entries, keeping each block's sum, so that the row is read once, and
 // the CTA that holds the crossing looks only at the block where it lies again.
 // The work is the row's bytes: 8 V with a refusal, 4 V without; 8 CTAs a request put
-// enough loads in flight from one request on.  4 requests of 32000 words take 12.6 us, nearly all of
+// enough loads in flight from one request on.  4 requests of 32000 words take 13-14 us, nearly all of
 // it the chain (offsets, drafts, their p and q, the row, two cluster barriers, the block again);
-// 128 requests of 98305 words with sampled drafts 30 us (101 MB: the chain, then 5 TB/s).
+// 128 requests of 98305 words with sampled drafts 31 us (101 MB: the chain, then 5 TB/s).
 // U blocks of a warp are on their way at once: two where all CTAs fit at four an SM, one at seven
 // an SM else.  48 requests of 131072 words 15.1 us against 16.7 with one (17 against 19 sampled),
 // 128 requests of 98305 words in 1024 CTAs 38 us with two against 29.7: a second wave.
