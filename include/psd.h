@@ -692,8 +692,8 @@ psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *args,
                               const psd_multi_token_plan *plan, void *o, float *lse,
                               void *workspace, size_t workspace_bytes, psd_stream_t stream);
 
-/* Verification of drafted tokens that form a chain (not a tree).  Request b has K_b = draft_indptr[b+1] - draft_indptr[b]
- * drafts and K_b + 1 target rows, from row R_b = draft_indptr[b] + b (its rows of a
+/* Verification of drafted tokens that form a chain (not a tree).  Request b has
+ * K_b = draft_indptr[b+1] - draft_indptr[b] drafts and K_b + 1 target rows, from row R_b = draft_indptr[b] + b (its rows of a
  * multi-token step): target row R_b + j is p after draft j's predecessors.
  * Draft j (token d, proposal q_j) is accepted while u_{R_b + j} * q_j(d) < p_{R_b+j}(d); let
  * a be the number accepted before the first refusal.  The next token is drawn with the

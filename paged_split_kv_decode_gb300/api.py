@@ -609,7 +609,8 @@ def multi_token_args(q, k_pool, v_pool, page_indices_dev, *, sm_scale: float, k_
 
 def multi_token_decode(ctx: Context, args: L.MultiTokenArgs, plan: MultiTokenPlan, o: torch.Tensor,
                        lse: torch.Tensor = None, workspace: torch.Tensor = None, stream=None):
-    """multi_token_decode: o [T, Hq, D] bf16 or f32, lse [T, Hq] f32 (log2 units) or None."""
+    """multi_token_decode: o [T, Hq, D] bf16 or f32, lse [T, Hq] f32 (log2 units) or None;
+    workspace from multi_token_workspace (a call without one is refused)."""
     dev, out_type, shape = ctx.device, o.dtype, (args.num_tokens, args.Hq, args.D)
     if args.device != dev:
         raise ValueError(f"the arguments are on cuda:{args.device}, the context on cuda:{dev}")

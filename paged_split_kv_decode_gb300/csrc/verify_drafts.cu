@@ -7,8 +7,8 @@
 // numbers, so the weights are summed as integers, multiples of 2^-46.  Integer sums do not depend
 // on their order, so the split over threads cannot change a token.  64 bits hold sums below
 // 2^18; larger ones (rows that are no probabilities) stay at the largest number, in any order
-// too, and are reported as a row without weights is.  A weight is rounded to that unit once: weights from
-// 2^-23 on (1.2e-7) are exact, the error of a row's sum is about 1e-12.
+// too, and are reported as a row without weights is.  A weight is rounded to that unit once:
+// weights from 2^-23 on (1.2e-7) are exact, the error of a row's sum is about 1e-12.
 //
 // The weight of an entry with p > q, in f32 operations: d = p - q rounded, and its error e =
 // (p - d) - q, exact since p >= q >= 0; d's multiples of 2^-23 are the low bits of d + 1
