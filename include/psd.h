@@ -17,6 +17,9 @@
  *   append_tokens, multi_token_decode, verify_drafts
  *                         a step of several new tokens a request (drafts, prompt chunks):
  *                         rotation + append, attention over the cache, verification
+ *   append_tokens_scaled, multi_token_decode_scaled, beam_select, fork_pages
+ *                         a step of beam search over a cache of 8-bit blocks with a scale
+ *                         each; compact_pages, copy_pages, free_pages beside them
  *
  * Conventions shared by every entry point
  *   - Every function returns psd_status; nothing throws or aborts across the ABI.
@@ -90,8 +93,9 @@ typedef enum {
 enum {
   PSD_FAULT_PAGE_ID = 1,      /* a page id outside [0, num_pages) was skipped */
   PSD_FAULT_WAIT_TIMEOUT = 2, /* a bounded barrier wait gave up */
-  PSD_FAULT_RANGE = 4         /* an index outside the range an operation accepts
+  PSD_FAULT_RANGE = 4,        /* an index outside the range an operation accepts
                                  (a RoPE position past the cos/sin table) */
+  PSD_FAULT_NO_PAGES = 8      /* fork_pages: fewer free pages than the new requests need */
 };
 
 /* CSR page table (Detection section: PagedCsrView).  Host or device arrays. */
@@ -725,6 +729,168 @@ typedef struct {
   int32_t *fault_dev;          /* device int32 fault word, OR-ed */
 } psd_verify_args;
 psd_status verify_drafts(psd_ctx *ctx, const psd_verify_args *args, psd_stream_t stream);
+
+/* -------------------------------------------- a cache of 8-bit blocks with a scale each
+ * An e4m3 pool with one factor follows its data badly: a factor for the largest value of
+ * all tokens leaves the small ones few codes.  Here a block (`block` consecutive tokens of
+ * a page, one KV head) has its own, a power of two: byte e stands for 2^(e - 127), 255 for
+ * NaN.  (A power of two costs a floating-point code nothing but range, scaling a block
+ * anew is exact down to codes below 2^-6, and so is every product with it.)
+ * The pools are PSD_FP8_E4M3 with k_scale = v_scale = 1. */
+typedef struct {
+  uint8_t *k, *v; /* device [num_pages, page_size / block, Hkv] */
+  int32_t block;  /* 16, 32 or 64, dividing page_size */
+} psd_block_scales;
+
+/* append_tokens into such a cache.  Beside what append_tokens does, with A the largest
+ * magnitude among a block's new finite values (K after its rotation, in f32): e' is the
+ * least e >= 95 with A <= 448 * 2^(e - 127).  The block's e becomes e' where none of its
+ * tokens is older than this call's (index < P_b, the request's tokens before), else the
+ * larger of e' and the e it has; then the older tokens' codes c become the codes nearest
+ * to c * 2^(e_old - e), ties to even.  New codes are nearest to x * 2^(127 - e), ties to
+ * even; NaN stays NaN, infinities become 448.  Slots of the block behind the request's
+ * tokens keep what they hold.
+ * Head dims D and Dv are multiples of 8 up to 256 and Dv > 0, rot_dim is a multiple of 16
+ * and rot_col of 8, strides are multiples of 8, tensors 16-byte aligned; other shapes are
+ * refused as PSD_ERR_UNSUPPORTED.  Where two requests' new tokens meet in one block (a
+ * page listed twice), what the block holds is undefined. */
+psd_status append_tokens_scaled(psd_ctx *ctx, const psd_append_args *args, const psd_block_scales *scales,
+                                psd_stream_t stream);
+
+/* multi_token_decode over such a cache: k_j = 2^(e_K - 127) code, v_j = 2^(e_V - 127) code.
+ * Everything else is as there, the workspace too. */
+psd_status multi_token_decode_scaled(psd_ctx *ctx, const psd_multi_token_args *args, const psd_block_scales *scales,
+                                     const psd_multi_token_plan *plan, void *o, float *lse, void *workspace,
+                                     size_t workspace_bytes, psd_stream_t stream);
+
+/* ------------------------------------------------------------------------- beam search
+ * The best continuations of each request's beams.  Request b owns the rows
+ * [b * beams, (b + 1) * beams).  Token t after row r has the value
+ *   v(r, t) = scores[r] + x(r, t) - log sum_s exp(x(r, s))          (natural logarithm),
+ * x the logits; the k largest over the request's rows and tokens go out in descending
+ * order: out_scores f32, out_rows the row r (of all rows: what fork_pages takes as
+ * parents), out_tokens t.  Within a row values are ordered by their logits, between rows
+ * in 64 bits; equal ones by lower row, then lower token.  The sums of the exponentials
+ * are f32 with compensation, good to some 1e-8 of the sum.  Equal rows (the same logits
+ * and scores) have equal values.
+ * A row with finished[r] != 0 has one continuation, pad_token with the value scores[r];
+ * its logits are not read.  Logits of -inf and NaN are no continuations (and add nothing
+ * to the sum), and neither are rows whose score is -inf.  A row with a logit of +inf, a
+ * score that is NaN or +inf, or whose sum overflows has none either and sets
+ * PSD_FAULT_RANGE.  Where a request has fewer than k continuations the rest are -inf, -1,
+ * -1.  rows == 0 is a no-op.
+ * workspace: >= psd_beam_workspace_bytes(ctx, rows, beams, k) bytes, 16-byte aligned; calls
+ * that may overlap need their own. */
+typedef enum { PSD_LOGITS_F32 = 0, PSD_LOGITS_BF16 = 1, PSD_LOGITS_F16 = 2 } psd_logits_type;
+typedef struct {
+  const void *logits;       /* device [rows, vocab] */
+  int64_t logits_stride;    /* elements between rows, >= vocab */
+  int32_t logits_type;      /* psd_logits_type */
+  const float *scores;      /* device [rows] */
+  const uint8_t *finished;  /* device [rows] or NULL */
+  int32_t rows, beams;      /* rows a multiple of beams; beams in [1, 64], beams * k <= 4096 */
+  int32_t vocab, k;         /* k in [1, 64] */
+  int32_t pad_token;
+  float *out_scores;        /* device [rows / beams, k] */
+  int32_t *out_rows, *out_tokens; /* device [rows / beams, k] */
+  int32_t *fault_dev;       /* device int32 fault word, OR-ed */
+} psd_beam_args;
+size_t psd_beam_workspace_bytes(const psd_ctx *ctx, int32_t rows, int32_t beams, int32_t k);
+psd_status beam_select(psd_ctx *ctx, const psd_beam_args *args, void *workspace, size_t workspace_bytes,
+                       psd_stream_t stream);
+
+/* ------------------------------------------------------------------- pages of a cache
+ * Several requests may hold the same page (beams of one prompt; what cascade_decode reads
+ * once).  ref_count[g] counts the table entries that name page g; a page with 0 is free.
+ * A cache is any number of arrays whose first axis is the page (K and V of each layer,
+ * their scales): what is copied is copied in all of them. */
+typedef struct {
+  void *base;         /* device [num_pages] pages */
+  int64_t page_bytes; /* any; pages of 16-byte aligned multiples of 16 are copied fastest */
+} psd_page_pool;
+
+/* Makes a new table whose request i continues request parents[i] of the old one (several
+ * may continue one, -1: an empty request) and has space for `room` more tokens: the
+ * reordering of beams, or (keep_old) further requests beside the old ones.
+ * With L = kv_len[parents[i]] and P = page_size, request i has ceil((L + room) / P) pages
+ * and new_len[i] = L + room (0 for an empty one):
+ *   - the floor(L / P) full pages of its parent, shared;
+ *   - the part-full page, if L % P: shared where room == 0 (nothing will be written);
+ *     otherwise the lowest child of all that have the page takes it, if no table entry but
+ *     those that are let go refers to it, and every other gets a copy in a fresh page;
+ *   - fresh pages for the rest.  (Pages of the parent behind its L tokens are not handed
+ *     down.)
+ * Fresh pages are the lowest free ids once the old table has let go of its pages
+ * (keep_old == 0), in order of new request and position.  new_ref_count gets the counts:
+ * less those of all entries page_indices[page_indptr[0] .. page_indptr[batch]) unless
+ * keep_old, plus those of the new table.
+ * On a fault nothing is written but the bits in *fault_dev: PSD_FAULT_RANGE for a parent
+ * outside [-1, batch), a length that its row does not hold, offsets out of range, a count
+ * below 0 or below the entries let go, a new table longer than new_capacity;
+ * PSD_FAULT_PAGE_ID for a page id out of range; PSD_FAULT_NO_PAGES.
+ * The new table must not overlap the old one; new_ref_count may be ref_count.
+ * workspace: >= psd_pages_workspace_bytes(num_pages, num_new) bytes, 16-byte aligned;
+ * calls that may overlap need their own. */
+typedef struct {
+  const int32_t *parents;      /* device [num_new] */
+  int32_t num_new;             /* up to 2^24 */
+  int32_t room;                /* >= 0 */
+  const int32_t *page_indptr;  /* device [batch + 1] */
+  const int32_t *page_indices; /* device [num_page_indices] */
+  int64_t num_page_indices;
+  const int32_t *kv_len;       /* device [batch]: tokens of each request */
+  int32_t batch, page_size;
+  int32_t keep_old;            /* 1: the old requests live on */
+  const int32_t *ref_count;    /* device [num_pages] */
+  int32_t *new_ref_count;      /* device [num_pages], may be ref_count */
+  int64_t num_pages;
+  int32_t *new_indptr;         /* device [num_new + 1] */
+  int32_t *new_indices;        /* device [new_capacity]; entries behind the table keep what they hold */
+  int64_t new_capacity;
+  int32_t *new_len;            /* device [num_new] */
+  const psd_page_pool *pools;  /* host [num_pools] */
+  int32_t num_pools;
+  int32_t *fault_dev;          /* device int32 fault word, OR-ed */
+} psd_fork_args;
+size_t psd_pages_workspace_bytes(int64_t num_pages, int32_t num_new);
+psd_status fork_pages(psd_ctx *ctx, const psd_fork_args *args, void *workspace, size_t workspace_bytes,
+                      psd_stream_t stream);
+
+/* Lets go of every page that the table's entries page_indices[page_indptr[0] ..
+ * page_indptr[batch]) name.  Faults as fork_pages (nothing is written). */
+psd_status free_pages(psd_ctx *ctx, const int32_t *page_indptr, const int32_t *page_indices, int64_t num_page_indices,
+                      int32_t batch, int32_t *ref_count, int64_t num_pages, int32_t *fault_dev, void *workspace,
+                      size_t workspace_bytes, psd_stream_t stream);
+
+/* Moves the live pages (ref_count > 0) to the front: of n live pages, those with ids >= n
+ * go, in order, to the free ids below n, in order; their data in all pools, their counts
+ * and the entries of page_indices (any number of tables, one behind the other) with them.
+ * *num_live = n.  page_map (may be NULL): the new id of each old page, -1 for a free one.
+ * A table entry that is out of range or names a free page sets PSD_FAULT_PAGE_ID, a
+ * negative count PSD_FAULT_RANGE; then nothing else is written.  new_indices may be
+ * page_indices, new_ref_count ref_count.
+ * workspace: >= psd_pages_workspace_bytes(num_pages, 0) bytes. */
+typedef struct {
+  const int32_t *page_indices; /* device [num_page_indices] */
+  int64_t num_page_indices;
+  const int32_t *ref_count;    /* device [num_pages] */
+  int64_t num_pages;
+  int32_t *new_indices;        /* device [num_page_indices] */
+  int32_t *new_ref_count;      /* device [num_pages] */
+  int32_t *num_live;           /* device int32 */
+  int32_t *page_map;           /* device [num_pages] or NULL */
+  const psd_page_pool *pools;  /* host [num_pools] */
+  int32_t num_pools;
+  int32_t *fault_dev;          /* device int32 fault word, OR-ed */
+} psd_compact_args;
+psd_status compact_pages(psd_ctx *ctx, const psd_compact_args *args, void *workspace, size_t workspace_bytes,
+                         psd_stream_t stream);
+
+/* Copies page src[i] to page dst[i] in all pools, i < n (src and dst device).  The dst must
+ * differ from each other and from every src but their own (a page copied to itself stays).
+ * A pair with an id out of range is left out and sets PSD_FAULT_PAGE_ID. */
+psd_status copy_pages(psd_ctx *ctx, const psd_page_pool *pools, int32_t num_pools, int64_t num_pages, const int32_t *src,
+                      const int32_t *dst, int32_t n, int32_t *fault_dev, psd_stream_t stream);
 
 /* Synchronises `stream` and reads the workspace's fault word: PSD_OK, or
  * PSD_ERR_DEVICE_FAULT with the PSD_FAULT_* bits in *fault_bits (nullable).

@@ -11,5 +11,7 @@ from .api import (CachedPlan, Context, HostTable, NestedPlan, Plan, PlanCache,  
                   merge_states, paged_decode_partial, plan_decode, rope_append_kv, split_plan,
                   workspace_bytes, workspace_for,
                   RopeFrequencies, rope_frequencies, append_tokens, MultiTokenPlan, plan_multi_token,
-                  multi_token_workspace, multi_token_args, multi_token_decode, verify_drafts)
+                  multi_token_workspace, multi_token_args, multi_token_decode, verify_drafts,
+                  BlockScales, beam_workspace, beam_select, PagePools, pages_workspace, fork_pages, free_pages,
+                  compact_pages, copy_pages)
 from ._lib import PsdError, load  # noqa: F401

@@ -28,6 +28,8 @@ EXPORTS = [
     "psd_nested_workspace_bytes", "cascade_decode_nested", "psd_autotune_tile", "psd_tuned_tile",
     "psd_rope_frequencies", "append_tokens", "psd_plan_multi_token", "psd_multi_token_workspace_bytes",
     "multi_token_decode", "verify_drafts",
+    "append_tokens_scaled", "multi_token_decode_scaled", "psd_beam_workspace_bytes", "beam_select",
+    "psd_pages_workspace_bytes", "fork_pages", "free_pages", "compact_pages", "copy_pages",
 ]
 PSD_ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
 
@@ -120,6 +122,7 @@ class MultiTokenPlan(C.Structure):
 
 
 class MultiTokenArgs(C.Structure):
+    scales = None  # the blocks' scales, where the pools have them
     _fields_ = [("q", C.c_void_p), ("q_stride", i64), ("k_pool", C.c_void_p), ("v_pool", C.c_void_p),
                 ("page_indices_dev", C.c_void_p), ("num_page_indices", i64), ("num_pages", i64), ("num_tokens", i32),
                 ("Hq", i32), ("Hkv", i32), ("D", i32), ("page_size", i32), ("kv_dtype", i32), ("k_scale", C.c_float),
@@ -131,6 +134,35 @@ class VerifyArgs(C.Structure):
                 ("draft_stride", i64), ("draft_tokens", C.c_void_p), ("draft_indptr", C.c_void_p),
                 ("uniforms", C.c_void_p), ("batch", i32), ("num_drafts", i32), ("vocab", i32),
                 ("num_accepted", C.c_void_p), ("out_tokens", C.c_void_p), ("fault_dev", C.c_void_p)]
+
+
+class BlockScales(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("block", i32)]
+
+
+class BeamArgs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("logits_stride", i64), ("logits_type", i32), ("scores", C.c_void_p),
+                ("finished", C.c_void_p), ("rows", i32), ("beams", i32), ("vocab", i32), ("k", i32), ("pad_token", i32),
+                ("out_scores", C.c_void_p), ("out_rows", C.c_void_p), ("out_tokens", C.c_void_p),
+                ("fault_dev", C.c_void_p)]
+
+
+class PagePool(C.Structure):
+    _fields_ = [("base", C.c_void_p), ("page_bytes", i64)]
+
+
+class ForkArgs(C.Structure):
+    _fields_ = [("parents", C.c_void_p), ("num_new", i32), ("room", i32), ("page_indptr", C.c_void_p),
+                ("page_indices", C.c_void_p), ("num_page_indices", i64), ("kv_len", C.c_void_p), ("batch", i32),
+                ("page_size", i32), ("keep_old", i32), ("ref_count", C.c_void_p), ("new_ref_count", C.c_void_p),
+                ("num_pages", i64), ("new_indptr", C.c_void_p), ("new_indices", C.c_void_p), ("new_capacity", i64),
+                ("new_len", C.c_void_p), ("pools", C.c_void_p), ("num_pools", i32), ("fault_dev", C.c_void_p)]
+
+
+class CompactArgs(C.Structure):
+    _fields_ = [("page_indices", C.c_void_p), ("num_page_indices", i64), ("ref_count", C.c_void_p), ("num_pages", i64),
+                ("new_indices", C.c_void_p), ("new_ref_count", C.c_void_p), ("num_live", C.c_void_p),
+                ("page_map", C.c_void_p), ("pools", C.c_void_p), ("num_pools", i32), ("fault_dev", C.c_void_p)]
 
 
 _LIB = None
@@ -199,11 +231,24 @@ def _sig(lib):
     lib.psd_multi_token_workspace_bytes.restype = C.c_size_t
     lib.multi_token_decode.argtypes = [V, C.POINTER(MultiTokenArgs), C.POINTER(MultiTokenPlan), V, V, V, C.c_size_t, V]
     lib.verify_drafts.argtypes = [V, V, V]
+    lib.append_tokens_scaled.argtypes = [V, V, C.POINTER(BlockScales), V]
+    lib.multi_token_decode_scaled.argtypes = [V, C.POINTER(MultiTokenArgs), C.POINTER(BlockScales),
+                                              C.POINTER(MultiTokenPlan), V, V, V, C.c_size_t, V]
+    lib.psd_beam_workspace_bytes.argtypes = [V, i32, i32, i32]
+    lib.psd_beam_workspace_bytes.restype = C.c_size_t
+    lib.beam_select.argtypes = [V, V, V, C.c_size_t, V]
+    lib.psd_pages_workspace_bytes.argtypes = [i64, i32]
+    lib.psd_pages_workspace_bytes.restype = C.c_size_t
+    lib.fork_pages.argtypes = [V, V, V, C.c_size_t, V]
+    lib.free_pages.argtypes = [V, V, V, i64, i32, V, i64, V, V, C.c_size_t, V]
+    lib.compact_pages.argtypes = [V, V, V, C.c_size_t, V]
+    lib.copy_pages.argtypes = [V, V, i32, i64, V, V, i32, V, V]
     for name in EXPORTS:
         f = getattr(lib, name)
         if f.restype is C.c_int or f.restype is None:
             if name not in ("psd_last_error", "psd_cascade_env_enabled", "psd_workspace_bytes",
-                            "psd_nested_workspace_bytes", "psd_tuned_tile", "psd_multi_token_workspace_bytes"):
+                            "psd_nested_workspace_bytes", "psd_tuned_tile", "psd_multi_token_workspace_bytes",
+                            "psd_beam_workspace_bytes", "psd_pages_workspace_bytes"):
                 f.restype = C.c_int
 
 

@@ -484,9 +484,33 @@ def _row_stride(t: torch.Tensor, shape, name: str, dtype, dev: int) -> int:
     return stride[0] if shape[0] > 1 else width
 
 
+class BlockScales:
+    """psd_block_scales: the scales of a cache of 8-bit blocks, uint8 k and v [num_pages,
+    page_size // block, Hkv] on the device (byte e stands for 2^(e - 127), 255 for NaN); block is
+    16, 32 or 64 tokens of a page.  The object keeps the tensors."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block: int):
+        self.shape = tuple(_shape(k, 3, "k scales"))
+        if tuple(_shape(v, 3, "v scales")) != self.shape:
+            raise ValueError("the scales of K and V must be alike, [num_pages, page_size // block, Hkv]")
+        self.device = k.get_device()
+        self.c = L.BlockScales(_flat(k, "k scales", torch.uint8, self.device),
+                               _flat(v, "v scales", torch.uint8, self.device), int(block))
+        self.k, self.v, self.block = k, v, int(block)
+
+    def fit(self, pool_shape, dev: int):
+        """Refuses pools [num_pages, page_size, Hkv, D] that these are not the scales of."""
+        num_pages, page_size, Hkv = pool_shape[:3]
+        if self.block < 1 or self.shape != (num_pages, page_size // self.block, Hkv):
+            raise ValueError(f"scales must be [num_pages, page_size // block, Hkv] = "
+                             f"{(num_pages, page_size // max(self.block, 1), Hkv)}, not {self.shape}")
+        if self.device != dev:
+            raise ValueError(f"the scales are on cuda:{self.device}, expected cuda:{dev}")
+
+
 def append_tokens(ctx: Context, q, k, v, q_out, *, q_indptr, kv_len, page_indptr, page_indices, k_pool, v_pool,
                   rope: RopeFrequencies, neox: bool, rope_col: int = 0, positions=None, k_scale: float = 1.0,
-                  v_scale: float = 1.0, fault=None, stream=None):
+                  v_scale: float = 1.0, scales: "BlockScales" = None, fault=None, stream=None):
     """append_tokens: rotate the new tokens' queries into q_out and append their rotated K and
     their V to the pools, at the places the device page table gives.
 
@@ -494,7 +518,8 @@ def append_tokens(ctx: Context, q, k, v, q_out, *, q_indptr, kv_len, page_indptr
     [T, Hq, D] bf16 (q and q_out None for a K/V-only append, v and v_pool None for a shared
     latent); q_indptr and page_indptr [B + 1], kv_len [B] (new tokens included), page_indices
     and positions ([T], optional) int32 on the device; pools bf16 or uint8 fp8-e4m3 codes
-    [pages, page_size, Hkv, D].  Returns the int32 fault word tensor (the one given, or a new
+    [pages, page_size, Hkv, D].  scales: the pools are blocks with a scale each, which this call
+    sets (append_tokens_scaled).  Returns the int32 fault word tensor (the one given, or a new
     zero one)."""
     dev, bf16, i32 = ctx.device, torch.bfloat16, torch.int32
     ks = _shape(k, 3, "k")
@@ -539,7 +564,11 @@ def append_tokens(ctx: Context, q, k, v, q_out, *, q_indptr, kv_len, page_indptr
         rope.rot_dim, 1 if neox else 0, rope.address, rope.magnitude, *tables, page_indices.numel(),
         _flat(k_pool, "k_pool", pool_type, dev), v_pool_ptr, num_pages, page_size, kv_dtype_code(k_pool), k_scale,
         v_scale, _flat(fault, "fault", i32, dev))
-    status = L.load().append_tokens(ctx._h, args, _ctx_stream(ctx, stream))
+    if scales is None:
+        status = L.load().append_tokens(ctx._h, args, _ctx_stream(ctx, stream))
+    else:
+        scales.fit(pool_shape, dev)
+        status = L.load().append_tokens_scaled(ctx._h, args, scales.c, _ctx_stream(ctx, stream))
     if status:
         L.check(status)
     return fault
@@ -585,10 +614,12 @@ def multi_token_workspace(ctx: Context, plan: MultiTokenPlan, D: int, device) ->
 
 
 def multi_token_args(q, k_pool, v_pool, page_indices_dev, *, sm_scale: float, k_scale: float = 1.0,
-                     v_scale: float = 1.0, tree_mask=None) -> L.MultiTokenArgs:
+                     v_scale: float = 1.0, tree_mask=None, scales: BlockScales = None) -> L.MultiTokenArgs:
     """psd_multi_token_args from device tensors: q [T, Hq, D] bf16 (possibly a view with a
     token stride), pools [pages, page_size, Hkv, D] bf16 or uint8 fp8-e4m3 codes, page_indices
-    int32, tree_mask [T] int64 (64 bits a token) or None.  The structure keeps the tensors."""
+    int32, tree_mask [T] int64 (64 bits a token) or None.  scales: the pools are blocks with a
+    scale each (multi_token_decode then calls multi_token_decode_scaled).  The structure keeps
+    the tensors."""
     shape = _shape(q, 3, "q")
     T, Hq, D = shape
     dev = q.get_device()
@@ -603,7 +634,9 @@ def multi_token_args(q, k_pool, v_pool, page_indices_dev, *, sm_scale: float, k_
         _flat(page_indices_dev, "page_indices", torch.int32, dev), page_indices_dev.numel(), pool_shape[0], T, Hq,
         pool_shape[2], D, pool_shape[1], kv_dtype_code(k_pool), k_scale, v_scale, sm_scale,
         None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, dev), 0)
-    a.tensors, a.device = (q, k_pool, v_pool, page_indices_dev, tree_mask), dev
+    if scales is not None:
+        scales.fit(pool_shape, dev)
+    a.tensors, a.device, a.scales = (q, k_pool, v_pool, page_indices_dev, tree_mask), dev, scales
     return a
 
 
@@ -621,10 +654,12 @@ def multi_token_decode(ctx: Context, args: L.MultiTokenArgs, plan: MultiTokenPla
         raise ValueError("o must be [T, Hq, D]")
     if lse is not None and lse.shape != shape[:2]:
         raise ValueError("lse must be f32 [T, Hq]")
-    status = L.load().multi_token_decode(
-        ctx._h, args, plan.c, _flat(o, "o", out_type, dev),
-        None if lse is None else _flat(lse, "lse", torch.float32, dev),
-        _flat(workspace, "workspace", torch.uint8, dev), workspace.numel(), _ctx_stream(ctx, stream))
+    rest = (plan.c, _flat(o, "o", out_type, dev), None if lse is None else _flat(lse, "lse", torch.float32, dev),
+            _flat(workspace, "workspace", torch.uint8, dev), workspace.numel(), _ctx_stream(ctx, stream))
+    if args.scales is None:
+        status = L.load().multi_token_decode(ctx._h, args, *rest)
+    else:
+        status = L.load().multi_token_decode_scaled(ctx._h, args, args.scales.c, *rest)
     if status:
         L.check(status)
 
@@ -657,6 +692,192 @@ def verify_drafts(ctx: Context, target_probs, draft_probs, draft_tokens, draft_i
         d_ptr = draft_probs.data_ptr()
     args = _VERIFY.pack(target_probs.data_ptr(), d_ptr, t_stride, d_stride, *ptrs, B, D, V, *outs)
     status = L.load().verify_drafts(ctx._h, args, _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
+    return fault
+
+
+# ------------------------------------------------------------------------------ beam search
+_BEAM = struct.Struct("@PqiPP5iPPPP")
+assert _BEAM.size == C.sizeof(L.BeamArgs)
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def beam_workspace(ctx: Context, rows: int, beams: int, k: int, device) -> torch.Tensor:
+    """A workspace for beam_select calls of at most `rows` rows with these beams and k."""
+    n = int(L.load().psd_beam_workspace_bytes(ctx.handle, int(rows), int(beams), int(k)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def beam_select(ctx: Context, logits, scores, out_scores, out_rows, out_tokens, workspace, *, beams: int, finished=None,
+                pad_token: int = 0, fault=None, stream=None):
+    """beam_select: the k best continuations over each request's beams and the vocabulary.
+    logits [rows, vocab] f32, bf16 or f16 (rows possibly apart), scores [rows] f32, finished
+    [rows] uint8 or bool or None, request b's beams the rows [b * beams, (b + 1) * beams);
+    out_scores f32, out_rows and out_tokens int32, all [rows / beams, k].  out_rows are numbers of
+    rows, as fork_pages takes for its parents (-1: no continuation).  Returns the int32 fault word
+    tensor (the one given, or a new zero one)."""
+    dev, i32, f32 = ctx.device, torch.int32, torch.float32
+    shape = _shape(logits, 2, "logits")
+    rows, V = shape
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
+        raise TypeError("logits must be f32, bf16 or f16")
+    stride = _row_stride(logits, shape, "logits", logits.dtype, dev)
+    if beams < 1 or rows % beams:
+        raise ValueError("logits must have a multiple of `beams` rows")
+    out = _shape(out_tokens, 2, "out_tokens")
+    if out[0] != rows // beams or _shape(out_scores, 2, "out_scores") != out or _shape(out_rows, 2, "out_rows") != out:
+        raise ValueError("out_scores, out_rows and out_tokens must be [rows / beams, k]")
+    if scores.numel() != rows or (finished is not None and finished.numel() != rows):
+        raise ValueError("scores and finished must hold a value a row")
+    if fault is None:
+        fault = _new_fault(logits.device, stream)
+    done = 0
+    if finished is not None:
+        done = _flat(finished, "finished", torch.bool if finished.dtype is torch.bool else torch.uint8, dev)
+    args = _BEAM.pack(logits.data_ptr(), max(stride, V), kind, _flat(scores, "scores", f32, dev), done, rows, beams, V,
+                      out[1], pad_token, _flat(out_scores, "out_scores", f32, dev), _flat(out_rows, "out_rows", i32, dev),
+                      _flat(out_tokens, "out_tokens", i32, dev), _flat(fault, "fault", i32, dev))
+    status = L.load().beam_select(ctx._h, args, _flat(workspace, "workspace", torch.uint8, dev), workspace.numel(),
+                                  _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
+    return fault
+
+
+# ------------------------------------------------------------------------- pages of a cache
+_FORK = struct.Struct("@PiiPPqPiiiPPqPPqPPiP")
+_COMPACT = struct.Struct("@PqPqPPPPPiP")
+assert _FORK.size == C.sizeof(L.ForkArgs) and _COMPACT.size == C.sizeof(L.CompactArgs)
+
+
+class PagePools:
+    """The arrays of a cache whose first axis is the page (K and V of each layer, their scales):
+    contiguous tensors on one device, with equally many pages.  The object keeps them."""
+
+    def __init__(self, tensors):
+        tensors = list(tensors)
+        if not tensors:
+            raise ValueError("a cache has at least one array of pages")
+        for t in tensors:
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or not t.is_contiguous() or t.dim() < 1:
+                raise ValueError("pools must be contiguous CUDA tensors")
+            if t.shape[0] != tensors[0].shape[0] or t.get_device() != tensors[0].get_device():
+                raise ValueError("pools must have equally many pages, on one device")
+        self.num_pages, self.device = int(tensors[0].shape[0]), tensors[0].get_device()
+        self.c = (L.PagePool * len(tensors))(
+            *[L.PagePool(t.data_ptr(), t.numel() // max(self.num_pages, 1) * t.element_size()) for t in tensors])
+        self.tensors, self.count, self.address = tensors, len(tensors), C.addressof(self.c)
+
+    def fit(self, ref_count: torch.Tensor, dev: int):
+        if self.device != dev:
+            raise ValueError(f"the pools are on cuda:{self.device}, expected cuda:{dev}")
+        if ref_count.numel() != self.num_pages:
+            raise ValueError(f"ref_count must hold {self.num_pages} values")
+
+
+def pages_workspace(pages: PagePools, num_new: int, device) -> torch.Tensor:
+    """A workspace for fork_pages calls of at most num_new new requests (0: free_pages and
+    compact_pages)."""
+    n = int(L.load().psd_pages_workspace_bytes(pages.num_pages, int(num_new)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def fork_pages(ctx: Context, pages: PagePools, parents, *, page_indptr, page_indices, kv_len, page_size: int, room: int,
+               ref_count, new_indptr, new_indices, new_len, workspace, new_ref_count=None, keep_old: bool = False,
+               fault=None, stream=None):
+    """fork_pages: a new page table whose request i continues request parents[i] of the old one
+    (-1: none) with space for `room` more tokens; pages are shared, and those that two would write
+    to copied in all pools.  parents [N], page_indptr [B + 1], page_indices, kv_len [B], ref_count
+    [num_pages] and the outputs new_indptr [N + 1], new_indices (capacity), new_len [N] are int32
+    on the device; new_ref_count defaults to ref_count.  keep_old: the old requests live on.
+    Returns the int32 fault word tensor (the one given, or a new zero one)."""
+    dev, i32 = ctx.device, torch.int32
+    pages.fit(ref_count, dev)
+    if new_ref_count is None:
+        new_ref_count = ref_count
+    N, B = parents.numel(), kv_len.numel()
+    if page_indptr.numel() != B + 1 or new_indptr.numel() != N + 1 or new_len.numel() != N or \
+            new_ref_count.numel() != pages.num_pages:
+        raise ValueError("page_indptr must hold batch + 1 values, new_indptr num_new + 1, new_len num_new, "
+                         "new_ref_count num_pages")
+    if fault is None:
+        fault = _new_fault(ref_count.device, stream)
+    args = _FORK.pack(
+        _flat(parents, "parents", i32, dev), N, room, _flat(page_indptr, "page_indptr", i32, dev),
+        _flat(page_indices, "page_indices", i32, dev), page_indices.numel(), _flat(kv_len, "kv_len", i32, dev), B,
+        page_size, 1 if keep_old else 0, _flat(ref_count, "ref_count", i32, dev),
+        _flat(new_ref_count, "new_ref_count", i32, dev), pages.num_pages, _flat(new_indptr, "new_indptr", i32, dev),
+        _flat(new_indices, "new_indices", i32, dev), new_indices.numel(), _flat(new_len, "new_len", i32, dev),
+        pages.address, pages.count, _flat(fault, "fault", i32, dev))
+    status = L.load().fork_pages(ctx._h, args, _flat(workspace, "workspace", torch.uint8, dev), workspace.numel(),
+                                 _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
+    return fault
+
+
+def free_pages(ctx: Context, page_indptr, page_indices, ref_count, workspace, *, fault=None, stream=None):
+    """free_pages: lets go of every page of a table (page_indptr [B + 1], page_indices int32 on the
+    device), counting ref_count down in place.  workspace: of pages_workspace.  Returns the fault
+    word tensor."""
+    dev, i32 = ctx.device, torch.int32
+    if page_indptr.numel() < 1:
+        raise ValueError("page_indptr must hold batch + 1 values")
+    if fault is None:
+        fault = _new_fault(ref_count.device, stream)
+    status = L.load().free_pages(
+        ctx._h, _flat(page_indptr, "page_indptr", i32, dev), _flat(page_indices, "page_indices", i32, dev),
+        page_indices.numel(), page_indptr.numel() - 1, _flat(ref_count, "ref_count", i32, dev), ref_count.numel(),
+        _flat(fault, "fault", i32, dev), _flat(workspace, "workspace", torch.uint8, dev), workspace.numel(),
+        _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
+    return fault
+
+
+def compact_pages(ctx: Context, pages: PagePools, page_indices, ref_count, *, num_live, workspace, new_indices=None,
+                  new_ref_count=None, page_map=None, fault=None, stream=None):
+    """compact_pages: moves the live pages to the front of all pools, and the entries of
+    page_indices (any number of tables, one behind the other) and ref_count with them, in place
+    unless new_indices and new_ref_count are given.  num_live [1] int32 gets their number, page_map
+    [num_pages] (optional) each old page's new id.  Returns the fault word tensor."""
+    dev, i32 = ctx.device, torch.int32
+    pages.fit(ref_count, dev)
+    new_indices = page_indices if new_indices is None else new_indices
+    new_ref_count = ref_count if new_ref_count is None else new_ref_count
+    if new_indices.numel() != page_indices.numel() or new_ref_count.numel() != pages.num_pages or \
+            (page_map is not None and page_map.numel() != pages.num_pages) or num_live.numel() != 1:
+        raise ValueError("new_indices is as long as page_indices, new_ref_count and page_map hold num_pages values, "
+                         "num_live one")
+    if fault is None:
+        fault = _new_fault(ref_count.device, stream)
+    args = _COMPACT.pack(
+        _flat(page_indices, "page_indices", i32, dev), page_indices.numel(), _flat(ref_count, "ref_count", i32, dev),
+        pages.num_pages, _flat(new_indices, "new_indices", i32, dev), _flat(new_ref_count, "new_ref_count", i32, dev),
+        _flat(num_live, "num_live", i32, dev), 0 if page_map is None else _flat(page_map, "page_map", i32, dev),
+        pages.address, pages.count, _flat(fault, "fault", i32, dev))
+    status = L.load().compact_pages(ctx._h, args, _flat(workspace, "workspace", torch.uint8, dev), workspace.numel(),
+                                    _ctx_stream(ctx, stream))
+    if status:
+        L.check(status)
+    return fault
+
+
+def copy_pages(ctx: Context, pages: PagePools, src, dst, *, fault=None, stream=None):
+    """copy_pages: page src[i] to page dst[i] in all pools (int32 on the device).  Returns the fault
+    word tensor."""
+    dev, i32 = ctx.device, torch.int32
+    if pages.device != dev:
+        raise ValueError(f"the pools are on cuda:{pages.device}, expected cuda:{dev}")
+    if src.numel() != dst.numel():
+        raise ValueError("src and dst must be equally long")
+    if fault is None:
+        fault = _new_fault(src.device, stream)
+    status = L.load().copy_pages(ctx._h, pages.address, pages.count, pages.num_pages, _flat(src, "src", i32, dev),
+                                 _flat(dst, "dst", i32, dev), src.numel(), _flat(fault, "fault", i32, dev),
+                                 _ctx_stream(ctx, stream))
     if status:
         L.check(status)
     return fault

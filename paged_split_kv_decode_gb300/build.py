@@ -21,9 +21,10 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpsd.so")
 
 CU_SOURCES = ["api.cu", "merge.cu", "partial_cc.cu", "partial_tcs.cu", "partial_tc.cu", "partial_mla.cu", "partial_l0.cu",
-              "no_alloc.cu", "rope_append.cu", "autotune.cu", "append_tokens.cu", "multi_token.cu", "multi_token_tc.cu", "verify_drafts.cu"]
+              "no_alloc.cu", "rope_append.cu", "autotune.cu", "append_tokens.cu", "multi_token.cu", "multi_token_tc.cu", "verify_drafts.cu",
+              "append_scaled.cu", "multi_token_rows.cu", "beam_select.cu", "pages.cu"]
 CPP_SOURCES = ["plan.cpp", "plan_cache.cpp", "tokens_host.cpp"]
-HEADERS = ["psd_internal.h", "kernels.h", "device.cuh", "context.h", "multi_token.h"]
+HEADERS = ["psd_internal.h", "kernels.h", "device.cuh", "context.h", "multi_token.h", "append.cuh", "block_scales.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

@@ -124,6 +124,10 @@ psd_status launch_partial_tc(const PartialLaunch &p, const DeviceInfo &dev, cuda
 bool partial_l0_supports(const PartialLaunch &p);
 psd_status launch_partial_l0(const PartialLaunch &p, const DeviceInfo &dev, cudaStream_t s);
 
+// The scales of a cache of 8-bit blocks fit its pools (`what`: the entry point).
+psd_status check_scales(const char *what, const psd_block_scales *scales, int32_t page_size, int32_t kv_dtype, float k_scale,
+                        float v_scale);
+
 psd_status launch_rope_append(const psd_rope_append_args *a, cudaStream_t s);
 
 // after_partial: the launch directly follows a partial kernel on stream s (no event

@@ -73,7 +73,7 @@ __device__ __forceinline__ int request_of(const GeneralRequests &g, int B, int x
 // 20000 to 65536 keys, 510 us at 2.5 TB/s.  What bounds it is the latency of each lane's own key row
 // and the row's queries from shared memory.  (A CTA a token and query head, K read anew for each,
 // took 1450 and 7360 us.)
-template <bool FP8, int KG>
+template <bool FP8, int KG, bool SCALED>
 __global__ void __launch_bounds__(kWarps * 32, 4)
     step_general_kernel(const StepParams p, const __grid_constant__ GeneralRequests g) {
   constexpr int R = kGroupRows, kLanes = 32 / KG;  // lanes that share out a row of V
@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     const int j = 32 * t + lane;
     bool there = j < n_keys;
     int64_t row = 0;
+    [[maybe_unused]] float k_scale = 1.f, v_scale = 1.f;  // of the key's block
     if (there) {
       const int id = __ldg(p.page_indices + r.page_off + j / p.page_size);
       if (id < 0 || int64_t(id) >= p.num_pages) {
@@ -123,6 +124,11 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
         there = false;
       } else {
         row = (int64_t(id) * p.page_size + j % p.page_size) * p.Hkv + kv;
+        if constexpr (SCALED) {
+          const int64_t at = ((int64_t(id) * p.page_size + j % p.page_size) >> p.scales.shift) * p.Hkv + kv;
+          k_scale = scale_value(__ldg(p.scales.k + at));
+          v_scale = scale_value(__ldg(p.scales.v + at));
+        }
       }
     }
     float2 acc[R];
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
     for (int rr = 0; rr < R; ++rr) {
       const bool sees = there && (j < seen[rr] || (j >= start && j - start < 64 && (tree[rr] >> ((j - start) & 63) & 1)));
       any |= sees;
-      const float s = sees ? acc[rr].x + acc[rr].y : neg_inf();
+      const float s = sees ? (SCALED ? (acc[rr].x + acc[rr].y) * k_scale : acc[rr].x + acc[rr].y) : neg_inf();
       float top = s;
 #pragma unroll
       for (int x = 16; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
@@ -164,6 +170,10 @@ __global__ void __launch_bounds__(kWarps * 32, 4)
       l[rr] += w[rr];
     }
     const uint32_t weighed = __ballot_sync(0xffffffffu, any);
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int rr = 0; rr < R; ++rr) w[rr] = w[rr] == 0.f ? 0.f : w[rr] * v_scale;  // (0 beside a scale of NaN: hidden)
+    }
 #pragma unroll
     for (int rr = 0; rr < R; rr += 4)
       *reinterpret_cast<float4 *>(&weights[warp][lane][rr]) = make_float4(w[rr], w[rr + 1], w[rr + 2], w[rr + 3]);
@@ -293,16 +303,17 @@ psd_status launch_step_general(const StepParams &p, const StepRequests &req, flo
   g.part_o = base;
   g.part_lse = base + general_pieces(dev.num_sms) * kGroupRows * p.D;
   const dim3 grid(unsigned(groups), unsigned(p.Hkv), unsigned(splits));
-  auto go = [&](auto fp8, auto kg) {
-    step_general_kernel<decltype(fp8)::value, decltype(kg)::value><<<grid, kWarps * 32, 0, s>>>(p, g);
+  auto go = [&](auto fp8, auto kg, auto scaled) {
+    step_general_kernel<decltype(fp8)::value, decltype(kg)::value, decltype(scaled)::value><<<grid, kWarps * 32, 0, s>>>(p, g);
   };
-  auto by_dim = [&](auto fp8) {
-    if (p.D <= 64) go(fp8, std::integral_constant<int, 4>{});
-    else if (p.D <= 128) go(fp8, std::integral_constant<int, 2>{});
-    else go(fp8, std::integral_constant<int, 1>{});
+  auto by_dim = [&](auto fp8, auto scaled) {
+    if (p.D <= 64) go(fp8, std::integral_constant<int, 4>{}, scaled);
+    else if (p.D <= 128) go(fp8, std::integral_constant<int, 2>{}, scaled);
+    else go(fp8, std::integral_constant<int, 1>{}, scaled);
   };
-  if (p.fp8) by_dim(std::true_type{});
-  else by_dim(std::false_type{});
+  if (p.scaled) by_dim(std::true_type{}, std::true_type{});
+  else if (p.fp8) by_dim(std::true_type{}, std::false_type{});
+  else by_dim(std::false_type{}, std::false_type{});
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess && splits > 1) {
     general_join_kernel<<<dim3(unsigned(groups), unsigned(p.Hkv)), 256, 0, s>>>(p, g, splits);
@@ -321,45 +332,50 @@ extern "C" size_t psd_multi_token_workspace_bytes(const psd_ctx *ctx, int32_t D)
   // the fault word, then the partial rows of the tensor-core kernel's CTAs, one per SM, or the
   // other kernel's pieces
   const size_t general = size_t(general_pieces(ctx->dev.num_sms)) * kGroupRows * (size_t(D) + 1);
-  return 256 + 4 * (D == 64 || D == 128 ? std::max(general, step_tc_place(ctx->dev.num_sms, D, nullptr).floats) : general);
+  if (D != 64 && D != 128) return 256 + 4 * general;
+  return 256 + 4 * std::max({general, step_tc_place(ctx->dev.num_sms, D, nullptr).floats, step_rows_floats(ctx->dev.num_sms, D)});
 }
 
-extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *a, const psd_multi_token_plan *plan,
-                                         void *o, float *lse, void *workspace, size_t workspace_bytes,
-                                         psd_stream_t stream) {
-  clear_error();
-  if (!ctx || !a || !plan || !workspace) return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: NULL");
+// scales: NULL, or those of a cache of 8-bit blocks.
+static psd_status decode(const char *what, psd_ctx *ctx, const psd_multi_token_args *a, const psd_block_scales *scales,
+                         const psd_multi_token_plan *plan, void *o, float *lse, void *workspace, size_t workspace_bytes,
+                         psd_stream_t stream) {
+  if (!ctx || !a || !plan || !workspace) return fail(PSD_ERR_INVALID_ARG, "%s: NULL", what);
   if (plan->batch < 0 || plan->num_tokens < 0 || a->num_tokens < plan->num_tokens)
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: %d token rows, the plan has %d", a->num_tokens,
+    return fail(PSD_ERR_INVALID_ARG, "%s: %d token rows, the plan has %d", what, a->num_tokens,
                 plan->num_tokens);
   if (a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv)
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: need Hq %% Hkv == 0 (Hq %d, Hkv %d)", a->Hq, a->Hkv);
-  if (a->D < 8 || a->D % 8) return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: D %d must be a positive multiple of 8", a->D);
-  if (a->D > kMaxDim) return fail(PSD_ERR_UNSUPPORTED, "multi_token_decode: head dim %d > %d", a->D, kMaxDim);
-  if (a->Hq > 65535) return fail(PSD_ERR_UNSUPPORTED, "multi_token_decode: Hq %d", a->Hq);
+    return fail(PSD_ERR_INVALID_ARG, "%s: need Hq %% Hkv == 0 (Hq %d, Hkv %d)", what, a->Hq, a->Hkv);
+  if (a->D < 8 || a->D % 8) return fail(PSD_ERR_INVALID_ARG, "%s: D %d must be a positive multiple of 8", what, a->D);
+  if (a->D > kMaxDim) return fail(PSD_ERR_UNSUPPORTED, "%s: head dim %d > %d", what, a->D, kMaxDim);
+  if (a->Hq > 65535) return fail(PSD_ERR_UNSUPPORTED, "%s: Hq %d", what, a->Hq);
   if (a->page_size < 1 || a->page_size != plan->page_size || a->num_pages < 1 || a->num_pages > 0x7fffffffLL ||
       a->num_page_indices < 0)
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: page_size %d (plan %d) / num_pages / num_page_indices",
+    return fail(PSD_ERR_INVALID_ARG, "%s: page_size %d (plan %d) / num_pages / num_page_indices", what,
                 a->page_size, plan->page_size);
   if (a->kv_dtype != PSD_BF16 && a->kv_dtype != PSD_FP8_E4M3)
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: kv_dtype %d", a->kv_dtype);
+    return fail(PSD_ERR_INVALID_ARG, "%s: kv_dtype %d", what, a->kv_dtype);
   const bool fp8 = a->kv_dtype == PSD_FP8_E4M3;
   const float q_scale = a->sm_scale * 1.4426950408889634f * (fp8 ? a->k_scale : 1.f);
   if (!std::isfinite(a->sm_scale) || (fp8 && (!std::isfinite(a->k_scale) || !std::isfinite(a->v_scale))) ||
       !std::isfinite(q_scale))
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: scales and sm_scale * log2(e) * k_scale must be finite");
+    return fail(PSD_ERR_INVALID_ARG, "%s: scales and sm_scale * log2(e) * k_scale must be finite", what);
   if (a->q_stride < int64_t(a->Hq) * a->D || a->q_stride % 8)
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: q_stride must be a multiple of 8 and >= Hq * D");
+    return fail(PSD_ERR_INVALID_ARG, "%s: q_stride must be a multiple of 8 and >= Hq * D", what);
   if (a->tree_mask && plan->max_new > 64)
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: a tree mask holds 64 new tokens a request, the plan has %d",
+    return fail(PSD_ERR_INVALID_ARG, "%s: a tree mask holds 64 new tokens a request, the plan has %d", what,
                 plan->max_new);
+  if (scales) {
+    const psd_status st = check_scales(what, scales, a->page_size, a->kv_dtype, a->k_scale, a->v_scale);
+    if (st != PSD_OK) return st;
+  }
   if (plan->batch == 0 || plan->num_tokens == 0) return PSD_OK;
-  if (!plan->requests || !a->q || !a->k_pool || !a->v_pool || !a->page_indices_dev || !o)
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: NULL pointer");
+  if (!plan->requests || !a->q || !a->k_pool || !a->v_pool || !a->page_indices_dev || !o || (scales && (!scales->k || !scales->v)))
+    return fail(PSD_ERR_INVALID_ARG, "%s: NULL pointer", what);
   if (!aligned16(a->q) || !aligned16(a->k_pool) || !aligned16(a->v_pool) || !aligned16(o) || !aligned16(workspace))
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: q / pools / o / workspace must be 16-byte aligned");
+    return fail(PSD_ERR_INVALID_ARG, "%s: q / pools / o / workspace must be 16-byte aligned", what);
   if ((reinterpret_cast<uintptr_t>(a->tree_mask) & 7u) || (reinterpret_cast<uintptr_t>(lse) & 3u))
-    return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: tree_mask / lse alignment");
+    return fail(PSD_ERR_INVALID_ARG, "%s: tree_mask / lse alignment", what);
   const size_t need = psd_multi_token_workspace_bytes(ctx, a->D);
   if (workspace_bytes < need)
     return fail(PSD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
@@ -369,10 +385,10 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
     if (r.token0 != row || r.num_new < 0 || r.kv_len < 1 || r.kv_len > kMaxKvLen || r.num_new > r.kv_len ||
         r.page_off < 0 || (a->tree_mask && r.num_new > 64) ||
         int64_t(r.page_off) + (int64_t(r.kv_len) + a->page_size - 1) / a->page_size > a->num_page_indices)
-      return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: request %d of the plan", b);
+      return fail(PSD_ERR_INVALID_ARG, "%s: request %d of the plan", what, b);
     row += r.num_new;
   }
-  if (row != plan->num_tokens) return fail(PSD_ERR_INVALID_ARG, "multi_token_decode: the plan's token rows");
+  if (row != plan->num_tokens) return fail(PSD_ERR_INVALID_ARG, "%s: the plan's token rows", what);
 
   DeviceGuard g(ctx->dev.device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -397,19 +413,47 @@ extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_arg
   p.out_f32 = a->out_f32 != 0;
   p.q_scale = q_scale;
   p.v_scale = fp8 ? a->v_scale : 1.f;
+  p.scaled = scales != nullptr;
+  if (scales) {
+    p.scales.k = scales->k;
+    p.scales.v = scales->v;
+    while ((1 << p.scales.shift) < scales->block) ++p.scales.shift;
+  }
   float *const base = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + 256);
   const StepPlace place = step_tc_place(ctx->dev.num_sms, a->D, base);
-  StepRequests req;
-  const bool tensor = step_tc_supports(p);
-  for (int32_t b0 = 0; b0 < plan->batch;) {
-    // up to kStepRequests requests that have new tokens
-    p.B = 0;
-    for (; b0 < plan->batch && p.B < kStepRequests; ++b0)  // (the others' rows are none)
-      if (plan->requests[b0].num_new > 0) req.r[p.B++] = plan->requests[b0];
-    if (p.B == 0) break;
-    const psd_status st =
-        tensor ? launch_step_tc(p, req, place, ctx->dev, s) : launch_step_general(p, req, base, ctx->dev, s);
-    if (st != PSD_OK) return st;
+  // The kernel of a request, and launches of up to kStepRequests requests that have new tokens.  (The others' rows are
+  // none.)
+  const bool tensor = step_tc_supports(p), few = step_rows_supports(p);
+  const int kinds = few ? 2 : 1;
+  for (int kind = 0; kind < kinds; ++kind) {
+    StepRequests req;
+    for (int32_t b0 = 0; b0 < plan->batch;) {
+      p.B = 0;
+      for (; b0 < plan->batch && p.B < kStepRequests; ++b0) {
+        const psd_token_request &r = plan->requests[b0];
+        if (r.num_new > 0 && (!few || (int64_t(r.num_new) * p.G <= kFewRows) == (kind == 0))) req.r[p.B++] = r;
+      }
+      if (p.B == 0) break;
+      const psd_status st = few && kind == 0 ? launch_step_rows(p, req, base, ctx->dev, s)
+                            : tensor         ? launch_step_tc(p, req, place, ctx->dev, s)
+                                             : launch_step_general(p, req, base, ctx->dev, s);
+      if (st != PSD_OK) return st;
+    }
   }
   return PSD_OK;
+}
+
+extern "C" psd_status multi_token_decode(psd_ctx *ctx, const psd_multi_token_args *a, const psd_multi_token_plan *plan,
+                                         void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                         psd_stream_t stream) {
+  clear_error();
+  return decode("multi_token_decode", ctx, a, nullptr, plan, o, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" psd_status multi_token_decode_scaled(psd_ctx *ctx, const psd_multi_token_args *a, const psd_block_scales *scales,
+                                                const psd_multi_token_plan *plan, void *o, float *lse, void *workspace,
+                                                size_t workspace_bytes, psd_stream_t stream) {
+  clear_error();
+  if (!scales) return fail(PSD_ERR_INVALID_ARG, "multi_token_decode_scaled: NULL scales");
+  return decode("multi_token_decode_scaled", ctx, a, scales, plan, o, lse, workspace, workspace_bytes, stream);
 }

@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 
+#include "block_scales.cuh"
 #include "kernels.h"
 
 namespace psd {
@@ -30,6 +31,8 @@ struct StepParams {
   int Hq, Hkv, G, D, page_size, fp8, out_f32;
   float q_scale;  // sm_scale * log2(e) * k_scale
   float v_scale;
+  bool scaled;         // each block of the pools has its own scale
+  BlockScales scales;
 };
 
 // The tensor-core kernel's CTAs, and where they keep the partial rows of units they share and
@@ -43,6 +46,11 @@ StepPlace step_tc_place(int ctas, int D, float *base);
 bool step_tc_supports(const StepParams &p);
 psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
                           cudaStream_t s);
+// Few rows a KV head (new tokens times query heads) over a cache of 8-bit blocks.
+constexpr int kFewRows = 32;
+bool step_rows_supports(const StepParams &p);
+size_t step_rows_floats(int sms, int D);  // what it keeps from its base on
+psd_status launch_step_rows(const StepParams &p, const StepRequests &req, float *base, const DeviceInfo &dev, cudaStream_t s);
 psd_status launch_step_general(const StepParams &p, const StepRequests &req, float *base, const DeviceInfo &dev, cudaStream_t s);
 
 }  // namespace psd

@@ -1354,7 +1354,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
 
 bool step_tc_supports(const StepParams &p) {
   // q_scale > 0: the kernel takes the row maximum of the raw scores before scaling
-  return (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.G <= kRows && p.q_scale > 0.f &&
+  return !p.scaled && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.G <= kRows && p.q_scale > 0.f &&
          p.num_pages * p.page_size <= 0x7fffffffLL;
 }
 

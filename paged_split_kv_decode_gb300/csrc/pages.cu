@@ -1,0 +1,605 @@
+// Pages of a paged cache: forking, freeing, compacting and copying them (the contract is in include/psd.h).
+//
+// Which pages are free is what their reference counts say, so there is no free list to keep: a call that
+// needs n pages takes the n lowest free ids.  The tables and counts are worked on by one cluster of 8 CTAs
+// in phases that its barriers divide: 65536 pages' counts are 8 a thread, and a barrier of the cluster takes
+// a fraction of what a launch or a grid's barrier does.  All sums are of integers, so that the order of the
+// atomics shows nowhere.  Counts are worked on in the workspace and written when the call is known to go
+// through: a call that cannot writes nothing.  The pages' bytes are moved by a second kernel over all SMs.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "context.h"
+#include "device.cuh"
+#include "kernels.h"
+
+namespace psd {
+
+namespace {
+
+constexpr int kCtas = 8, kThreads = 1024, kAll = kCtas * kThreads, kWarps = kAll / 32;
+constexpr int kPoolsALaunch = 128;
+
+// The workspace: a header, then lists of 32-bit numbers.
+struct Header {
+  int32_t moves;                  // entries of the list of moves
+  int32_t pad[15];
+  long long totals[8][kCtas];     // one row for each exchange between the CTAs
+  uint32_t faults[8][kCtas];
+};
+constexpr size_t kHeaderBytes = 2048;
+static_assert(sizeof(Header) <= kHeaderBytes, "header");
+
+struct Lists {
+  Header *head;
+  int32_t *count;   // [num_pages] the reference counts as the call leaves them
+  int32_t *first;   // [num_pages] fork: the first child that may keep the page; compact: the new id
+  int32_t *fresh;   // [num_pages] fork: free pages in order; compact: the counts of the pages that move
+  int32_t *start;   // [num_new + 1] fork: where a child's pages begin in the new table
+  int32_t *blank;   // [num_new + 1] fork: and its fresh pages among all
+  int2 *moves;      // [max(num_new, num_pages / 2) + 1] source and destination; source < 0: none
+};
+size_t lists_of(Lists *l, void *base, int64_t num_pages, int64_t num_new) {
+  uint8_t *at = static_cast<uint8_t *>(base);
+  auto take = [&](size_t bytes) {
+    uint8_t *p = at;
+    at += (bytes + 255) / 256 * 256;
+    return p;
+  };
+  Lists x;
+  x.head = reinterpret_cast<Header *>(take(kHeaderBytes));
+  x.count = reinterpret_cast<int32_t *>(take(size_t(num_pages) * 4));
+  x.first = reinterpret_cast<int32_t *>(take(size_t(num_pages) * 4));
+  x.fresh = reinterpret_cast<int32_t *>(take(size_t(num_pages) * 4));
+  x.start = reinterpret_cast<int32_t *>(take(size_t(num_new + 1) * 4));
+  x.blank = reinterpret_cast<int32_t *>(take(size_t(num_new + 1) * 4));
+  x.moves = reinterpret_cast<int2 *>(take(size_t(std::max(num_new, num_pages / 2) + 1) * 8));
+  if (l) *l = x;
+  return size_t(at - static_cast<uint8_t *>(base));
+}
+
+struct ForkParams {
+  Lists w;
+  const int32_t *parents, *indptr, *indices, *kv_len, *ref;
+  int32_t *new_ref, *new_indptr, *new_indices, *new_len, *fault;
+  int64_t num_indices, num_pages, capacity;
+  int N, B, P, room, release;
+};
+
+// ------------------------------------------------------------------------------------- the cluster
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The cluster's threads, numbered through.
+struct Team {
+  Header *head;
+  int id, rank, turn = 0;
+  long long *sums;  // [33] shared
+  __device__ Team(Header *h, long long *s) : head(h), rank(int(cluster_rank())), sums(s) { id = rank * kThreads + threadIdx.x; }
+  // The sum of `v` over the threads before this one, and over all; `faults` of all are or-ed.  A barrier of
+  // the cluster: what its threads wrote before is there for all behind it.
+  __device__ long long scan(long long v, long long &total, uint32_t &faults) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long up = v;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, up, d);
+      if (lane >= d) up += x;
+    }
+    const uint32_t warp_faults = __reduce_or_sync(0xffffffffu, faults);
+    const bool any = __syncthreads_or(int(warp_faults)) != 0;  // (and `sums` is free)
+    if (lane == 31) sums[warp] = up;
+    uint32_t *bits = reinterpret_cast<uint32_t *>(sums + 32);
+    if (any && threadIdx.x == 0) *bits = 0;
+    __syncthreads();
+    if (any) {
+      if (lane == 0 && warp_faults) atomicOr(bits, warp_faults);
+      __syncthreads();
+    }
+    if (warp == 0) {
+      long long x = sums[lane];
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      sums[lane] = x;
+      if (lane == 31) {
+        head->totals[turn][rank] = x;
+        head->faults[turn][rank] = any ? *bits : 0u;
+      }
+    }
+    cluster_sync();
+    long long before = 0;
+    total = 0;
+    faults = 0;
+#pragma unroll
+    for (int c = 0; c < kCtas; ++c) {
+      const long long x = __ldcg(&head->totals[turn][c]);
+      faults |= __ldcg(&head->faults[turn][c]);
+      if (c < rank) before += x;
+      total += x;
+    }
+    ++turn;
+    return before + (warp ? sums[warp - 1] : 0) + up - v;
+  }
+};
+
+// ---------------------------------------------------------------------------------------------- fork
+// A child: its parent's pages that it takes over whole, whether it has a part-full one, and what it wants.
+struct Child {
+  int first, full, want, len;  // first: of the parent's row; want < 0: the child is refused
+  bool tail;
+};
+__device__ __forceinline__ Child child_of(const ForkParams &p, int i, uint32_t &faults) {
+  Child c{0, 0, 0, 0, false};
+  const int parent = p.parents[i];
+  if (parent == -1) return c;
+  if (parent < 0 || parent >= p.B) {
+    faults |= PSD_FAULT_RANGE;
+    return c;
+  }
+  c.first = p.indptr[parent];
+  c.len = p.kv_len[parent];
+  const int held = (c.len - 1) / p.P + (c.len > 0);  // pages
+  const int64_t want = (int64_t(c.len) + p.room + p.P - 1) / p.P;
+  if (c.len < 0 || c.first < 0 || int64_t(c.first) + held > p.indptr[parent + 1] || p.indptr[parent + 1] > p.num_indices ||
+      int64_t(c.len) + p.room > 0x7fffffff) {
+    faults |= PSD_FAULT_RANGE;
+    return Child{0, 0, 0, 0, false};
+  }
+  c.full = c.len / p.P;
+  c.tail = c.len % p.P != 0;
+  c.want = int(want);
+  return c;
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) fork_kernel(const ForkParams p) {
+  __shared__ long long sums[33];
+  dependents_may_launch();
+  Team team(p.w.head, sums);
+  const int id = team.id, lane = threadIdx.x & 31, warp = id >> 5;
+  // Children in runs, pages in runs: a run a thread, so that sums over the threads before give their places.
+  const int run = (p.N + kAll - 1) / kAll, i0 = min(p.N, id * run), i1 = min(p.N, i0 + run);
+  const int64_t stretch = (p.num_pages + kAll - 1) / kAll;
+  const int64_t g0 = min(p.num_pages, id * stretch), g1 = min(p.num_pages, g0 + stretch);
+  uint32_t faults = 0;
+  long long total;
+
+  // The children's wants; the counts to work on.
+  long long want = 0;
+  for (int i = i0; i < i1; ++i) want += child_of(p, i, faults).want;
+  const int64_t old_end = p.B > 0 ? p.indptr[p.B] : 0, old_begin = p.B > 0 ? p.indptr[0] : 0;
+  if (old_begin < 0 || old_end < old_begin || old_end > p.num_indices) faults |= PSD_FAULT_RANGE;
+  for (int64_t g = id; g < p.num_pages; g += kAll) {
+    const int r = p.ref[g];
+    if (r < 0) faults |= PSD_FAULT_RANGE;
+    p.w.count[g] = r;
+    p.w.first[g] = INT_MAX;
+  }
+  {
+    long long at = team.scan(want, total, faults);
+    for (int i = i0; i < i1; ++i) {
+      uint32_t none = 0;
+      p.w.start[i] = int(at);
+      at += child_of(p, i, none).want;
+    }
+  }
+  if (total > p.capacity) faults |= PSD_FAULT_RANGE;
+  const int pages_wanted = int(min(total, 0x7fffffffLL));
+
+  // The old requests let go of their pages.
+  if (!faults)
+    for (int64_t e = old_begin + id; e < old_end; e += kAll) {
+      const int g = p.indices[e];
+      if (g < 0 || g >= p.num_pages) faults |= PSD_FAULT_PAGE_ID;
+      else if (p.release) atomicSub(p.w.count + g, 1);
+    }
+  team.scan(0, total, faults);
+
+  // A part-full page that nobody else refers to goes to its first child.
+  if (!faults) {
+    for (int64_t g = id; g < p.num_pages; g += kAll)
+      if (__ldcg(p.w.count + g) < 0) faults |= PSD_FAULT_RANGE;  // referred to more often than counted
+    if (p.room)
+      for (int i = i0; i < i1; ++i) {
+        const Child c = child_of(p, i, faults);
+        if (!c.tail) continue;
+        const int g = p.indices[c.first + c.full];
+        if (g < 0 || g >= p.num_pages) faults |= PSD_FAULT_PAGE_ID;  // (behind the old table's end)
+        else if (__ldcg(p.w.count + g) == 0) atomicMin(p.w.first + g, i);
+      }
+  }
+  team.scan(0, total, faults);
+
+  // Pages handed down are counted, those to be found are numbered.
+  auto keeps = [&](const Child &c, int i) {
+    return c.tail && (!p.room || __ldcg(p.w.first + p.indices[c.first + c.full]) == i);
+  };
+  const int parts = max(1, kWarps / max(p.N, 1));  // warps a child
+  long long blanks = 0, all_blanks;
+  if (!faults) {
+    for (int i = i0; i < i1; ++i) {
+      const Child c = child_of(p, i, faults);
+      blanks += c.want - c.full - keeps(c, i);
+    }
+    for (int u = warp; u < p.N * parts; u += kWarps) {
+      const int i = u / parts;
+      const Child c = child_of(p, i, faults);
+      const int kept = c.full + keeps(c, i);
+      for (int j = (u % parts) * 32 + lane; j < kept; j += 32 * parts) {
+        const int g = p.indices[c.first + j];
+        if (g < 0 || g >= p.num_pages) faults |= PSD_FAULT_PAGE_ID;
+        else atomicAdd(p.w.count + g, 1);
+      }
+    }
+  }
+  {
+    long long at = team.scan(blanks, all_blanks, faults);
+    if (!faults)
+      for (int i = i0; i < i1; ++i) {
+        const Child c = child_of(p, i, faults);
+        p.w.blank[i] = int(at);
+        at += c.want - c.full - keeps(c, i);
+      }
+  }
+
+  // The free pages, lowest first.
+  long long free_pages = 0;
+  if (!faults)
+    for (int64_t g = g0; g < g1; ++g) free_pages += __ldcg(p.w.count + g) == 0;
+  {
+    long long at = team.scan(free_pages, total, faults);
+    if (total < all_blanks) faults |= PSD_FAULT_NO_PAGES;
+    if (!faults)
+      for (int64_t g = g0; g < g1; ++g) {
+        const int n = __ldcg(p.w.count + g);
+        const bool taken = n == 0 && at < all_blanks;
+        if (taken) p.w.fresh[at] = int(g);
+        at += n == 0;
+        p.new_ref[g] = taken ? 1 : n;
+      }
+  }
+  if (faults) {  // the same for all
+    if (id == 0) {
+      atomicOr(p.fault, int32_t(faults));
+      p.w.head->moves = 0;
+    }
+    return;
+  }
+  cluster_sync();
+
+  // The new table.
+  for (int u = warp; u < p.N * parts; u += kWarps) {
+    const int i = u / parts;
+    const Child c = child_of(p, i, faults);
+    const bool kept_tail = keeps(c, i);
+    const int kept = c.full + kept_tail;
+    const int start = __ldcg(p.w.start + i), blank = __ldcg(p.w.blank + i);
+    for (int j = (u % parts) * 32 + lane; j < c.want; j += 32 * parts)
+      p.new_indices[start + j] = j < kept ? p.indices[c.first + j] : __ldcg(p.w.fresh + blank + j - kept);
+    if (u % parts == 0 && lane == 0) {
+      p.new_indptr[i] = start;
+      p.new_len[i] = c.want ? c.len + p.room : 0;
+      p.w.moves[i] = c.tail && !kept_tail ? make_int2(p.indices[c.first + c.full], __ldcg(p.w.fresh + blank)) : make_int2(-1, -1);
+    }
+  }
+  if (id == 0) {
+    if (p.new_indptr) p.new_indptr[p.N] = pages_wanted;
+    p.w.head->moves = p.N;
+  }
+}
+
+// ------------------------------------------------------------------------------------------- compact
+struct CompactParams {
+  Lists w;
+  const int32_t *indices, *ref;
+  int32_t *new_indices, *new_ref, *num_live, *page_map, *fault;
+  int64_t num_indices, num_pages;
+};
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) compact_kernel(const CompactParams p) {
+  __shared__ long long sums[33];
+  dependents_may_launch();
+  Team team(p.w.head, sums);
+  const int id = team.id;
+  const int64_t stretch = (p.num_pages + kAll - 1) / kAll;
+  const int64_t g0 = min(p.num_pages, id * stretch), g1 = min(p.num_pages, g0 + stretch);
+  uint32_t faults = 0;
+  long long n_live, total, mine = 0;
+  for (int64_t g = g0; g < g1; ++g) {
+    const int r = p.ref[g];
+    if (r < 0) faults |= PSD_FAULT_RANGE;
+    mine += r > 0;
+  }
+  for (int64_t e = id; e < p.num_indices; e += kAll) {
+    const int g = p.indices[e];
+    if (g < 0 || g >= p.num_pages || p.ref[g] <= 0) faults |= PSD_FAULT_PAGE_ID;
+  }
+  team.scan(mine, n_live, faults);
+  if (faults) {
+    if (id == 0) {
+      atomicOr(p.fault, int32_t(faults));
+      p.w.head->moves = 0;
+    }
+    return;
+  }
+  // Free pages among the first n_live (high half), live pages behind them: there are as many of each.
+  long long both = 0;
+  for (int64_t g = g0; g < g1; ++g) {
+    const bool live = p.ref[g] > 0;
+    both += g < n_live ? (live ? 0LL : 1LL << 32) : live;
+  }
+  const long long at = team.scan(both, total, faults);
+  int hole = int(at >> 32), mover = int(at & 0xffffffff);
+  for (int64_t g = g0; g < g1; ++g) {
+    const int r = p.ref[g];
+    p.w.count[g] = r;
+    if (g < n_live && r == 0) p.w.moves[hole++].y = int(g);
+    if (g >= n_live && r > 0) {
+      p.w.fresh[mover] = r;
+      p.w.first[g] = mover;
+      p.w.moves[mover++].x = int(g);
+    }
+  }
+  cluster_sync();
+  hole = int(at >> 32);
+  for (int64_t g = g0; g < g1; ++g) {
+    const int r = p.w.count[g];
+    p.new_ref[g] = g >= n_live ? 0 : r > 0 ? r : __ldcg(p.w.fresh + hole++);
+    if (p.page_map) p.page_map[g] = r == 0 ? -1 : g < n_live ? int(g) : __ldcg(&p.w.moves[p.w.first[g]].y);
+  }
+  for (int64_t e = id; e < p.num_indices; e += kAll) {
+    const int g = p.indices[e];
+    p.new_indices[e] = g < n_live ? g : __ldcg(&p.w.moves[__ldcg(p.w.first + g)].y);
+  }
+  if (id == 0) {
+    *p.num_live = int(n_live);
+    p.w.head->moves = int(total & 0xffffffff);
+  }
+}
+
+// ---------------------------------------------------------------------------------------------- copy
+struct CopyPools {
+  psd_page_pool pool[kPoolsALaunch];
+};
+struct CopyParams {
+  const int32_t *count;       // entries, on the device, or
+  const int32_t *src, *dst;   // lists of a caller's, n long
+  const int2 *moves;
+  int32_t *fault;
+  int64_t num_pages;
+  int n, pools;
+};
+
+// A CTA takes one page of one pool at a time: 16 bytes a thread and access, four of them on their way.
+// 16 KB pages, 32 pools, 44 copies (46 MB moved): launch and ramp are most of it.
+__global__ void __launch_bounds__(256) copy_pages_kernel(const CopyParams p, const __grid_constant__ CopyPools pools) {
+  wait_for_prior_grid();
+  const int n = p.count ? __ldcg(p.count) : p.n;
+  for (int64_t u = blockIdx.x; u < int64_t(n) * p.pools; u += gridDim.x) {
+    const int i = int(u / p.pools);
+    const psd_page_pool pool = pools.pool[u - int64_t(i) * p.pools];
+    int64_t from, to;
+    if (p.moves) {
+      const int2 m = __ldcg(p.moves + i);
+      from = m.x, to = m.y;
+      if (from < 0) continue;
+    } else {
+      from = p.src[i], to = p.dst[i];
+      if (from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages) {
+        if (threadIdx.x == 0) atomicOr(p.fault, PSD_FAULT_PAGE_ID);
+        continue;
+      }
+    }
+    if (from == to) continue;
+    const uint8_t *a = static_cast<const uint8_t *>(pool.base) + from * pool.page_bytes;
+    uint8_t *b = static_cast<uint8_t *>(pool.base) + to * pool.page_bytes;
+    if (((reinterpret_cast<uintptr_t>(pool.base) | uint64_t(pool.page_bytes)) & 15) == 0) {
+      const int64_t words = pool.page_bytes / 16;
+      const uint4 *x = reinterpret_cast<const uint4 *>(a);
+      uint4 *y = reinterpret_cast<uint4 *>(b);
+      for (int64_t k = threadIdx.x; k < words; k += 4 * 256) {
+        uint4 w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (k + 256 * c < words) w[c] = __ldcs(x + k + 256 * c);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (k + 256 * c < words) y[k + 256 * c] = w[c];
+      }
+    } else {
+      for (int64_t k = threadIdx.x; k < pool.page_bytes; k += 256) b[k] = a[k];
+    }
+  }
+}
+
+// One or more launches over all pools, behind the kernel that makes the list (or not).
+psd_status launch_copy(CopyParams p, const psd_page_pool *pools, int num_pools, int64_t most, bool behind, const DeviceInfo &dev,
+                       cudaStream_t s) {
+  for (int k = 0; k < num_pools && most > 0; k += kPoolsALaunch) {
+    CopyPools c;
+    p.pools = std::min(kPoolsALaunch, num_pools - k);
+    std::copy(pools + k, pools + k + p.pools, c.pool);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(most * p.pools, int64_t(dev.num_sms) * 8)));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = behind && k == 0 ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, copy_pages_kernel, p, c);
+    if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "copy_pages launch: %s", cudaGetErrorString(e));
+  }
+  return PSD_OK;
+}
+
+psd_status check_pools(const char *what, const psd_page_pool *pools, int32_t num_pools, int64_t num_pages) {
+  if (num_pages < 1 || num_pages > 0x7fffffffLL) return fail(PSD_ERR_INVALID_ARG, "%s: num_pages %lld", what, (long long)num_pages);
+  if (num_pools < 0 || (num_pools > 0 && !pools)) return fail(PSD_ERR_INVALID_ARG, "%s: pools", what);
+  for (int32_t i = 0; i < num_pools; ++i)
+    if (!pools[i].base || pools[i].page_bytes < 1 || pools[i].page_bytes > (int64_t(1) << 40))
+      return fail(PSD_ERR_INVALID_ARG, "%s: pool %d", what, i);
+  return PSD_OK;
+}
+
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na > 0 && nb > 0 && x < y + uintptr_t(nb) * 4 && y < x + uintptr_t(na) * 4;
+}
+
+}  // namespace
+}  // namespace psd
+
+using namespace psd;
+
+extern "C" size_t psd_pages_workspace_bytes(int64_t num_pages, int32_t num_new) {
+  if (num_pages < 1 || num_new < 0) return 0;
+  return lists_of(nullptr, nullptr, num_pages, num_new);
+}
+
+extern "C" psd_status fork_pages(psd_ctx *ctx, const psd_fork_args *a, void *workspace, size_t workspace_bytes,
+                                 psd_stream_t stream) {
+  clear_error();
+  if (!ctx || !a) return fail(PSD_ERR_INVALID_ARG, "fork_pages: NULL");
+  const psd_status st = check_pools("fork_pages", a->pools, a->num_pools, a->num_pages);
+  if (st != PSD_OK) return st;
+  if (a->num_new < 0 || a->batch < 0 || a->num_page_indices < 0 || a->new_capacity < 0 || a->page_size < 1 || a->room < 0)
+    return fail(PSD_ERR_INVALID_ARG, "fork_pages: bad sizes");
+  if (a->num_new > (1 << 24) || a->num_page_indices > 0x7fffffffLL || a->new_capacity > 0x7fffffffLL)
+    return fail(PSD_ERR_UNSUPPORTED, "fork_pages: more than 2^24 new requests or 2^31 - 1 table entries");
+  if (!workspace || !aligned16(workspace)) return fail(PSD_ERR_INVALID_ARG, "fork_pages: workspace must be 16-byte aligned");
+  const size_t need = psd_pages_workspace_bytes(a->num_pages, a->num_new);
+  if (workspace_bytes < need) return fail(PSD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (!a->ref_count || !a->new_ref_count || !a->fault_dev ||
+      (a->batch > 0 && (!a->page_indptr || !a->kv_len || (a->num_page_indices > 0 && !a->page_indices))) ||
+      (a->num_new > 0 && (!a->parents || !a->new_indptr || !a->new_len || (a->new_capacity > 0 && !a->new_indices))))
+    return fail(PSD_ERR_INVALID_ARG, "fork_pages: NULL pointer");
+  if (overlap(a->page_indices, a->num_page_indices, a->new_indices, a->new_capacity) ||
+      overlap(a->page_indptr, int64_t(a->batch) + 1, a->new_indptr, int64_t(a->num_new) + 1) ||
+      overlap(a->kv_len, a->batch, a->new_len, a->num_new) || overlap(a->parents, a->num_new, a->new_len, a->num_new) ||
+      overlap(a->parents, a->num_new, a->new_indptr, int64_t(a->num_new) + 1) ||
+      overlap(a->parents, a->num_new, a->new_indices, a->new_capacity))
+    return fail(PSD_ERR_INVALID_ARG, "fork_pages: the new table overlaps the old one or the parents");
+  if (a->ref_count != a->new_ref_count && overlap(a->ref_count, a->num_pages, a->new_ref_count, a->num_pages))
+    return fail(PSD_ERR_INVALID_ARG, "fork_pages: new_ref_count is ref_count, or apart from it");
+  DeviceGuard g(ctx->dev.device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  ForkParams p = {};
+  lists_of(&p.w, workspace, a->num_pages, a->num_new);
+  p.parents = a->parents;
+  p.indptr = a->page_indptr;
+  p.indices = a->page_indices;
+  p.kv_len = a->kv_len;
+  p.ref = a->ref_count;
+  p.new_ref = a->new_ref_count;
+  p.new_indptr = a->new_indptr;
+  p.new_indices = a->new_indices;
+  p.new_len = a->new_len;
+  p.fault = a->fault_dev;
+  p.num_indices = a->num_page_indices;
+  p.num_pages = a->num_pages;
+  p.capacity = a->new_capacity;
+  p.N = a->num_new;
+  p.B = a->batch;
+  p.P = a->page_size;
+  p.room = a->room;
+  p.release = a->keep_old == 0;
+  fork_kernel<<<kCtas, kThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "fork_pages launch: %s", cudaGetErrorString(e));
+  CopyParams c = {};
+  c.count = &p.w.head->moves;
+  c.moves = p.w.moves;
+  c.fault = a->fault_dev;
+  c.num_pages = a->num_pages;
+  return launch_copy(c, a->pools, a->num_pools, a->room > 0 ? a->num_new : 0, true, ctx->dev, s);
+}
+
+extern "C" psd_status free_pages(psd_ctx *ctx, const int32_t *page_indptr, const int32_t *page_indices, int64_t num_page_indices,
+                                 int32_t batch, int32_t *ref_count, int64_t num_pages, int32_t *fault_dev, void *workspace,
+                                 size_t workspace_bytes, psd_stream_t stream) {
+  psd_fork_args a = {};
+  a.page_indptr = page_indptr;
+  a.page_indices = page_indices;
+  a.kv_len = page_indptr;  // (of no child: not read)
+  a.num_page_indices = num_page_indices;
+  a.batch = batch;
+  a.page_size = 1;
+  a.ref_count = ref_count;
+  a.new_ref_count = ref_count;
+  a.num_pages = num_pages;
+  a.fault_dev = fault_dev;
+  return fork_pages(ctx, &a, workspace, workspace_bytes, stream);
+}
+
+extern "C" psd_status compact_pages(psd_ctx *ctx, const psd_compact_args *a, void *workspace, size_t workspace_bytes,
+                                    psd_stream_t stream) {
+  clear_error();
+  if (!ctx || !a) return fail(PSD_ERR_INVALID_ARG, "compact_pages: NULL");
+  const psd_status st = check_pools("compact_pages", a->pools, a->num_pools, a->num_pages);
+  if (st != PSD_OK) return st;
+  if (a->num_page_indices < 0) return fail(PSD_ERR_INVALID_ARG, "compact_pages: num_page_indices");
+  if (!workspace || !aligned16(workspace)) return fail(PSD_ERR_INVALID_ARG, "compact_pages: workspace must be 16-byte aligned");
+  const size_t need = psd_pages_workspace_bytes(a->num_pages, 0);
+  if (workspace_bytes < need) return fail(PSD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (!a->ref_count || !a->new_ref_count || !a->num_live || !a->fault_dev ||
+      (a->num_page_indices > 0 && (!a->page_indices || !a->new_indices)))
+    return fail(PSD_ERR_INVALID_ARG, "compact_pages: NULL pointer");
+  if ((a->ref_count != a->new_ref_count && overlap(a->ref_count, a->num_pages, a->new_ref_count, a->num_pages)) ||
+      (a->page_indices != a->new_indices && overlap(a->page_indices, a->num_page_indices, a->new_indices, a->num_page_indices)) ||
+      overlap(a->page_map, a->num_pages, a->ref_count, a->num_pages) ||
+      overlap(a->page_map, a->num_pages, a->page_indices, a->num_page_indices))
+    return fail(PSD_ERR_INVALID_ARG, "compact_pages: an output is its input, or apart from all of them");
+  DeviceGuard g(ctx->dev.device);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  CompactParams p = {};
+  lists_of(&p.w, workspace, a->num_pages, 0);
+  p.indices = a->page_indices;
+  p.ref = a->ref_count;
+  p.new_indices = a->new_indices;
+  p.new_ref = a->new_ref_count;
+  p.num_live = a->num_live;
+  p.page_map = a->page_map;
+  p.fault = a->fault_dev;
+  p.num_indices = a->num_page_indices;
+  p.num_pages = a->num_pages;
+  compact_kernel<<<kCtas, kThreads, 0, s>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "compact_pages launch: %s", cudaGetErrorString(e));
+  CopyParams c = {};
+  c.count = &p.w.head->moves;
+  c.moves = p.w.moves;
+  c.fault = a->fault_dev;
+  c.num_pages = a->num_pages;
+  return launch_copy(c, a->pools, a->num_pools, a->num_pages / 2, true, ctx->dev, s);
+}
+
+extern "C" psd_status copy_pages(psd_ctx *ctx, const psd_page_pool *pools, int32_t num_pools, int64_t num_pages,
+                                 const int32_t *src, const int32_t *dst, int32_t n, int32_t *fault_dev, psd_stream_t stream) {
+  clear_error();
+  if (!ctx) return fail(PSD_ERR_INVALID_ARG, "copy_pages: NULL");
+  const psd_status st = check_pools("copy_pages", pools, num_pools, num_pages);
+  if (st != PSD_OK) return st;
+  if (n < 0) return fail(PSD_ERR_INVALID_ARG, "copy_pages: n %d", n);
+  if (n == 0 || num_pools == 0) return PSD_OK;
+  if (!src || !dst || !fault_dev) return fail(PSD_ERR_INVALID_ARG, "copy_pages: NULL pointer");
+  DeviceGuard g(ctx->dev.device);
+  CopyParams c = {};
+  c.src = src;
+  c.dst = dst;
+  c.n = n;
+  c.fault = fault_dev;
+  c.num_pages = num_pages;
+  return launch_copy(c, pools, num_pools, n, false, ctx->dev, reinterpret_cast<cudaStream_t>(stream));
+}

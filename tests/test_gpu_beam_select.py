@@ -1,0 +1,223 @@
+"""beam_select on the GPU against its definition in 64 bits: rows, tokens and scores; types, strides, ties, masks, beams at
+their end; its refusals and faults."""
+import numpy as np
+import pytest
+import torch
+
+import paged_split_kv_decode_gb300 as psd
+from oracle import beams as BM
+from _gpu_util import ctx
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def _run(logits, scores, beams, k, *, finished=None, pad=0, workspace=None):
+    rows = logits.shape[0]
+    out = [torch.full((rows // beams, k), -7, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    if workspace is None:
+        workspace = psd.beam_workspace(ctx(), rows, beams, k, "cuda")
+        workspace.fill_(255)
+    done = None if finished is None else torch.tensor(finished, dtype=torch.uint8, device="cuda")
+    fault = psd.beam_select(ctx(), logits, torch.as_tensor(np.asarray(scores, dtype=np.float32)).cuda(), *out, workspace,
+                            beams=beams, finished=done, pad_token=pad)
+    torch.cuda.synchronize()
+    return out, int(fault)
+
+
+def _check(logits, scores, beams, k, *, finished=None, pad=0, faults=0, twins=False):
+    """twins: rows hold the same logits in another order.  Their sums are equal, but for what rounding them in another
+    order moves (2^-21, see below): which of two equal values in different rows comes first is open."""
+    out, fault = _run(logits, scores, beams, k, finished=finished, pad=pad)
+    want = BM.select(logits.double().cpu().numpy(), np.asarray(scores, dtype=np.float32), beams, k, finished, pad)
+    assert fault == faults
+    if twins:
+        x = logits.double().cpu().numpy()
+        low = np.log(np.exp(x - x.max(-1, keepdims=True)).sum(-1)) + x.max(-1)
+        r, t = out[1].cpu().numpy(), out[2].cpu().numpy()
+        assert np.all(np.abs(np.asarray(scores)[r] + x[r, t] - low[r] - want[0]) <= 2 * 2.0 ** -21)
+        for b in range(len(r)):
+            assert len({*zip(r[b], t[b])}) == k and {*r[b]} <= set(range(b * beams, (b + 1) * beams))
+            for row in {*r[b]}:                                       # in a row: its largest, in order
+                assert list(t[b][r[b] == row]) == list(np.argsort(-x[row], kind="stable")[: int((r[b] == row).sum())])
+        return
+    assert np.array_equal(out[1].cpu().numpy(), want[1]), (out[1].cpu().numpy() - want[1])
+    assert np.array_equal(out[2].cpu().numpy(), want[2])
+    got, none = out[0].double().cpu().numpy(), np.isneginf(want[0])
+    assert np.array_equal(np.isneginf(got), none)
+    # rounded once to f32 (2^-24 of it); the sum of exponentials, whose terms are off by 2^-21 each at most
+    # (exp2 2 ulp, its argument rounded), moves the logarithm by no more than that
+    d = np.abs(np.where(none, 0, got) - np.where(none, 0, want[0]))
+    assert np.all(d <= 2.0 ** -24 * np.abs(np.where(none, 0, want[0])) + 2.0 ** -21)
+
+
+def _logits(rows, vocab, kind="f32", seed=0, spread=2.5):
+    rng = np.random.default_rng(seed)
+    return torch.from_numpy((spread * rng.standard_normal((rows, vocab))).astype(np.float32)).to(TYPES[kind]).cuda()
+
+
+def _scores(rows, seed=0):
+    return -5.0 - 3.0 * np.random.default_rng(seed + 99).random(rows)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("vocab", [1, 2, 7, 31, 256, 1000, 4095, 4096, 4097, 8193, 32000, 50257])
+def test_vocabularies(vocab, kind):
+    _check(_logits(6, vocab, kind, vocab), _scores(6, vocab), 3, 6)
+
+
+@pytest.mark.parametrize("beams,k", [(1, 1), (1, 64), (2, 3), (5, 10), (8, 8), (16, 32), (64, 64), (33, 7), (64, 1)])
+def test_beams_and_counts(beams, k):
+    _check(_logits(2 * beams, 5003, seed=k), _scores(2 * beams, k), beams, k)
+
+
+def test_more_rows_than_a_grid_is_high():
+    rows = 33000
+    logits, scores = _logits(rows, 40, seed=5), _scores(rows, 5)
+    _check(logits, scores, 10, 4)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_rows_apart_and_off_their_alignment(kind):
+    wide = _logits(8, 9001, kind, 3)
+    _check(wide[:, :9000], _scores(8), 4, 8)
+    _check(wide[:, 1:8200], _scores(8), 4, 8)                       # neither rows nor the first are aligned
+    _check(wide[::2, 3:], _scores(4), 2, 5)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_equal_logits_go_to_lower_tokens(kind):
+    x = torch.zeros((4, 20000), dtype=TYPES[kind], device="cuda")
+    x[:, 15000:15100] = 3.0
+    x[:, 15050] = 4.0
+    _check(x, [-1.0] * 4, 2, 64)
+    _check(torch.full((2, 9999), -2.5, dtype=TYPES[kind], device="cuda"), [-1.0, -1.0], 1, 20)   # all equal
+
+
+@pytest.mark.parametrize("vocab", [20000, 20001])
+def test_equal_rows_go_to_lower_rows(vocab):
+    """The same logits and scores in several rows, which lie differently in memory where the vocabulary is odd."""
+    x = _logits(1, vocab, seed=8).repeat(6, 1).contiguous()
+    _check(x, [-2.0] * 6, 3, 12)
+    _check(x, [-2.0, -2.0, -3.0, -2.0, -3.0, -2.0], 6, 30)
+
+
+def test_signed_zeros_are_equal():
+    x = torch.full((1, 300), -1.0, device="cuda")
+    x[0, 40], x[0, 20], x[0, 30] = 0.0, -0.0, 0.0
+    _check(x, [0.0], 1, 4)
+
+
+def test_masked_logits():
+    inf = float("inf")
+    x = _logits(6, 9000, seed=12)
+    x[0] = -inf                                                       # nothing left
+    x[1, 5:] = -inf                                                   # five tokens
+    x[2, :] = -inf
+    x[2, 8999] = 1.0                                                  # one
+    x[3, ::2] = float("nan")
+    x[4, :] = float("nan")
+    x[5, 100] = -3.4e38
+    _check(x, [-1.0] * 6, 3, 7)
+    _check(x, [-1.0] * 6, 1, 12)
+    _check(x[:2], [-1.0, -inf], 2, 8)                                 # a beam that was never filled
+    _check(x[:2], [-inf, -inf], 2, 8)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_finished_beams(kind):
+    x = _logits(8, 7000, kind, 4)
+    x[1] = float("nan")                                               # not read
+    s = _scores(8)
+    _check(x, s, 4, 8, finished=[0, 1, 0, 1, 0, 0, 0, 0], pad=2)
+    _check(x, s, 4, 8, finished=[1] * 8, pad=6999)
+    s[3] = -np.inf
+    _check(x, s, 4, 8, finished=[0, 1, 0, 1, 0, 0, 0, 0], pad=0)
+
+
+def test_what_has_no_value_is_reported():
+    inf = float("inf")
+    x = _logits(4, 5000, seed=6)
+    x[1, 77] = inf
+    _check(x, [-1.0] * 4, 2, 6, faults=4)
+    x = _logits(4, 5000, seed=6)
+    for bad in (float("nan"), inf):
+        _check(x, [-1.0, bad, -1.0, -1.0], 2, 6, faults=4)
+        _check(x, [-1.0, bad, -1.0, -1.0], 2, 6, finished=[0, 1, 0, 0], faults=4)
+
+
+@pytest.mark.parametrize("spread,shift", [(0.0, 0.0), (1e-4, 0.0), (40.0, 0.0), (3.0, 500.0), (3.0, -20000.0), (1e4, 0.0)])
+def test_ranges_of_the_logits(spread, shift):
+    """Flat, peaked and far from zero.  (Where logits are large their own spacing decides, not the sums.)"""
+    rng = np.random.default_rng(1)
+    x = (spread * rng.standard_normal((4, 30000)) + shift).astype(np.float32)
+    _check(torch.from_numpy(x).cuda(), [-1.0, -1.25, -1.5, -4.0], 2, 16)
+
+
+def test_rising_and_falling_logits():
+    """Each tile's largest above (below) all before: candidates are taken over and thinned out again."""
+    x = torch.linspace(-30, 30, 70001, device="cuda")
+    _check(torch.stack([x, x.flip(0), x * 0.001, x.flip(0) * 0.001]), [-1.0] * 4, 2, 64, twins=True)
+
+
+def test_near_values_across_rows():
+    """Two rows whose best values differ by some 1e-6 either way."""
+    x = _logits(2, 100003, seed=15, spread=2.0)
+    gap = BM.select(x.double().cpu().numpy(), np.float32([0, 0]), 1, 1)[0][:, 0]
+    for d in (-2e-6, 2e-6):
+        _check(x, np.float32([-3.0, -3.0 + gap[0] - gap[1] + d]), 2, 6)
+
+
+def test_workspace_is_used_again_and_results_repeat():
+    ws = psd.beam_workspace(ctx(), 64, 8, 16, "cuda")
+    x, s = _logits(64, 33001, seed=2), _scores(64)
+    first, _ = _run(x, s, 8, 16, workspace=ws)
+    _run(_logits(32, 700, "bf16"), _scores(32), 8, 16, workspace=ws)
+    again, _ = _run(x, s, 8, 16, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
+def test_captured_and_replayed_on_another_stream():
+    x, s = _logits(8, 20001, seed=30), torch.as_tensor(_scores(8).astype(np.float32)).cuda()
+    out = [torch.zeros((2, 8), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    ws, fault = psd.beam_workspace(ctx(), 8, 4, 8, "cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        psd.beam_select(ctx(), x, s, *out, ws, beams=4, fault=fault)
+    for seed in (31, 32):
+        x.copy_(_logits(8, 20001, seed=seed))
+        g.replay()
+        torch.cuda.synchronize()
+        want, _ = _run(x, s.cpu().numpy(), 4, 8)
+        assert all(torch.equal(a, b) for a, b in zip(out, want)) and int(fault) == 0
+
+
+def test_no_rows():
+    out = [torch.zeros((0, 4), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    psd.beam_select(ctx(), torch.zeros((0, 10), device="cuda"), torch.zeros(0, device="cuda"), *out,
+                    psd.beam_workspace(ctx(), 0, 2, 4, "cuda"), beams=2)
+    torch.cuda.synchronize()
+
+
+def test_argument_errors():
+    x, s = _logits(4, 100), torch.zeros(4, device="cuda")
+    out = lambda b=2, k=4: [torch.zeros((b, k), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]  # noqa: E731
+    ws = psd.beam_workspace(ctx(), 4, 2, 4, "cuda")
+    call = lambda *a, **kw: psd.beam_select(ctx(), *a, **{"beams": 2, **kw})  # noqa: E731
+    for a, kw in (((x, s, *out(3), ws), {}), ((x, s, *out(), ws), dict(beams=3)), ((x, s[:3], *out(), ws), {}),
+                  ((x, s, *out(), ws), dict(finished=torch.zeros(3, dtype=torch.uint8, device="cuda"))),
+                  ((x.t().contiguous().t(), s, *out(), ws), {}), ((x.cpu(), s, *out(), ws), {}), ((x, s.cpu(), *out(), ws), {})):
+        with pytest.raises((ValueError, TypeError)):
+            call(*a, **kw)
+    for a, kw in (((x.double(), s, *out(), ws), {}), ((x, s.double(), *out(), ws), {}),
+                  ((x, s, *out(), ws), dict(finished=torch.zeros(4, device="cuda")))):
+        with pytest.raises(TypeError):
+            call(*a, **kw)
+    for a, kw, status in (((x, s, *out(2, 65), ws), {}, 2), ((x, s, *out(), ws[:64]), {}, 5),
+                          ((_logits(65, 9), torch.zeros(65, device="cuda"), *out(1), ws), dict(beams=65), 2)):
+        with pytest.raises(psd.PsdError) as e:
+            call(*a, **kw)
+        assert e.value.status == status
