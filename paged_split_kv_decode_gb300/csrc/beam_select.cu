@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
   }
 }
 
-// One CTA a request: its rows' logarithms, then the k largest of their candidates.
+// One CTA a request: its rows' logarithms, then the k largest of their candidates.  As in the first kernel a bound
+// leaves few of them to be put in order: all ranks of 640 candidates took 80 us.
 __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParams p) {
   extern __shared__ unsigned long long shared[];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -268,23 +269,30 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   __shared__ unsigned long long bound[kWarps];
   __shared__ int n_shared;
   wait_for_prior_grid();
+  const int64_t from = int64_t(b) * most;
+  const unsigned long long early = tid < most ? p.keys[from + tid] : 0;  // on its way beside the sums
   if (tid == 0) n_shared = 0;
   for (int w = warp; w < p.beams; w += kWarps) {
     const int row = b * p.beams + w;
     const float score = p.scores[row];
     const bool done = p.finished && p.finished[row];
+    float ref = neg_inf(), refs[2];
+    double sums[2];  // at most 64 splits: two a lane
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int s = lane + 32 * i;
+      refs[i] = s < p.splits ? p.refs[int64_t(row) * p.splits + s] : neg_inf();
+      sums[i] = s < p.splits ? p.sums[int64_t(row) * p.splits + s] : 0.0;
+    }
     double add = double(score);
     int what = score == neg_inf() ? 0 : done ? 1 : 2;
     bool bad = isnan(score) || score == -neg_inf();
     if (what == 2 && !bad) {
-      float ref = neg_inf();
-      for (int s = lane; s < p.splits; s += 32) ref = fmaxf(ref, p.refs[int64_t(row) * p.splits + s]);
+      ref = fmaxf(refs[0], refs[1]);
 #pragma unroll
       for (int d = 16; d; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
       double sum = 0.0;
-      if (ref != neg_inf())
-        for (int s = lane; s < p.splits; s += 32)
-          sum += p.sums[int64_t(row) * p.splits + s] * double(ex2(p.refs[int64_t(row) * p.splits + s] - ref));
+      if (ref != neg_inf()) sum = sums[0] * double(ex2(refs[0] - ref)) + sums[1] * double(ex2(refs[1] - ref));
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       if (sum == 0.0) what = 0;  // nothing but -inf
@@ -299,47 +307,48 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
     }
   }
   __syncthreads();
-  // Candidates, side by side.
-  unsigned long long best = 0;
-  const int64_t from = int64_t(b) * most;
-  for (int i = tid; i < most; i += kThreads) {
+  auto candidate = [&](int i, unsigned long long &k) {  // v in order; 0: none
     const int w = i / per_row;
-    unsigned long long k = 0, v = 0;
     if (kind[w] == 2) {
-      k = p.keys[from + i];
-      if (k) v = ordered(double(from_ordered(uint32_t(k >> 32))) + base[w]);
-    } else if (kind[w] == 1 && i == w * per_row) {
-      k = key_of(0.f, uint32_t(p.pad));
-      v = ordered(base[w]);
+      k = i == tid ? early : p.keys[from + i];
+      return k ? ordered(double(from_ordered(uint32_t(k >> 32))) + base[w]) : 0ull;
     }
-    if (!k) continue;
-    const int at = atomicAdd(&n_shared, 1);
-    value[at] = v;
-    key[at] = k;
-    of[at] = uint8_t(w);
-    best = max(best, v);
-  }
+    k = key_of(0.f, uint32_t(p.pad));
+    return kind[w] == 1 && i == w * per_row ? ordered(base[w]) : 0ull;
+  };
+  unsigned long long best = 0, k;
+  for (int i = tid; i < most; i += kThreads) best = max(best, candidate(i, k));
   const unsigned long long mine = nth_largest(best, (p.k + kWarps - 1) / kWarps);
   if (lane == 0) bound[warp] = mine;
   __syncthreads();
   unsigned long long low = bound[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) low = min(low, bound[w]);
+  for (int i = tid; i < most; i += kThreads) {
+    const unsigned long long v = candidate(i, k);
+    if (v == 0 || v < low) continue;
+    const int at = atomicAdd(&n_shared, 1);
+    value[at] = v;
+    key[at] = k;
+    of[at] = uint8_t(i / per_row);
+  }
+  __syncthreads();
   const int n = n_shared;
   for (int i = tid; i < n; i += kThreads) {
-    const unsigned long long v = value[i], k = key[i];
-    if (v < low) continue;
+    const unsigned long long v = value[i], x = key[i];
     const uint8_t w = of[i];
     int larger = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const unsigned long long y = value[j];
-      larger += y > v || (y == v && (of[j] < w || (of[j] == w && key[j] > k)));
+      larger += y > v;
+      if (y == v) larger += of[j] < w || (of[j] == w && key[j] > x);
     }
     if (larger < p.k) {
       const int64_t to = int64_t(b) * p.k + larger;
       p.out_scores[to] = float(from_ordered(v));
       p.out_rows[to] = b * p.beams + w;
-      p.out_tokens[to] = int32_t(0xffffffffu - uint32_t(k));
+      p.out_tokens[to] = int32_t(0xffffffffu - uint32_t(x));
     }
   }
   for (int i = n + tid; i < p.k; i += kThreads) {
