@@ -40,6 +40,10 @@
 // copies, conversion and MMAs otherwise fill.  With bf16 operands and Q in shared memory 16 requests'
 // trees of 9 to 24 tokens over 512 to 8192 keys took 61 us against 54.  (K's codes taken as they are by
 // kind::f8f6f4, against Q in two e4m3 terms, were no faster.)
+// A cache of 8-bit blocks with a scale each (SCALED): the warp that loads K also brings, eight tiles ahead, each tile's four
+// scale bytes of K and of V into a ring in shared memory.  K's scale 2^a goes into the score factor of its 16 keys, V's 2^b
+// into the exponent of P: P' = 2^(s - m + b - r) with r the largest b of the row's keys so far (O is rescaled when r
+// grows), l = sum 2^(r - b) sum P', both exact.  Where b is more than 2^64 below r it counts as 2^64.
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
@@ -143,7 +147,11 @@ enum {
   T_XREADY,                          // [2] the other slot's (m, l) of the rows are there (4 warps)
   T_DRAIN = T_XREADY + 2, T_SLOT, T_TAIL
 };
-static_assert(T_TAIL * 8 + 16 <= 1024, "barrier area");
+// Behind the barriers: the scales of 32 key tiles, four pairs of K's byte and V's each.  The loads are at most 14 tiles
+// ahead of the softmax (eight of codes, four of f16, two that a slot may lag behind).
+constexpr uint32_t kScaleOff = 768;
+constexpr int kScaleTiles = 32;
+static_assert(T_TAIL * 8 + 16 <= kScaleOff && kScaleOff + kScaleTiles * 8 <= 1024, "barrier area");
 
 struct TCParams {
   const int32_t *page_indices;
@@ -161,6 +169,7 @@ struct TCParams {
   float q_scale, v_scale;
   uint32_t wait_limit;
   int withhold_from;  // testing aid: no loads for a unit's key tiles from this index on
+  BlockScales scales;
 };
 // Requests with new tokens, and where each CTA's stretch of the line of key tiles begins.
 constexpr int kMaxCtas = 192;
@@ -359,6 +368,9 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
   return true;
 }
 
+// Byte i of a tile's scales.
+__device__ __forceinline__ int scale_byte(const uint2 &w, int i) { return int((i < 4 ? w.x : w.y) >> (8 * (i & 3)) & 255u); }
+
 // The visible keys of one row among the 32 from `base` on, one bit each.
 __device__ __forceinline__ uint32_t visible(int base, int seen, int start, uint64_t tree, bool has_tree) {
   const int n = (has_tree ? start : seen) - base;  // keys before this one are visible
@@ -371,10 +383,11 @@ __device__ __forceinline__ uint32_t visible(int base, int seen, int start, uint6
   return bits;
 }
 
-template <int D, int TERMS, bool FP8>
+template <int D, int TERMS, bool FP8, bool SCALED>
 __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
     step_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const TCParams p, const __grid_constant__ TCRequests req) {
+  static_assert(FP8 || !SCALED, "blocks are of codes");
   using L = Lay<D, TERMS, FP8>;
   constexpr int NK = L::NK, NS = L::kStages;
   // the ring that the copies fill
@@ -490,23 +503,61 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         step(ahead, ahead_off);
         return id;
       };
-      int id = next_id(), id_next = next_id();
+      int id = -1, id_next = -1;
+      // Scaled blocks, K: page ids and scales of eight tiles, a lane for 16 keys; those of the next eight are on their way.
+      [[maybe_unused]] int ids = -1, ids_after = -1;
+      [[maybe_unused]] uint32_t scales = 0, scales_after = 0;
+      [[maybe_unused]] auto load_ids = [&](int tile) {
+        const int64_t token = int64_t(tile + lane / 4) * NK + 16 * (lane & 3);
+        if (tile + lane / 4 >= u.j1 || token >= u.r.kv_len) return -1;
+        const int x = __ldg(p.page_indices + u.r.page_off + int(token) / P);
+        if (x >= 0 && int64_t(x) < p.num_pages) return x;
+        bad |= PSD_FAULT_PAGE_ID;
+        return -1;
+      };
+      [[maybe_unused]] auto load_scales = [&](int tile, int x) {
+        if (x < 0) return 127u;  // K's and, as 0, V's: of keys that nobody sees
+        const int64_t slot = int64_t(x) * P + ((tile + lane / 4) * NK + 16 * (lane & 3)) % P;
+        const int64_t at = (slot >> p.scales.shift) * p.Hkv + u.kv;
+        return uint32_t(__ldg(p.scales.k + at)) | uint32_t(__ldg(p.scales.v + at)) << 8;
+      };
+      const bool by_window = SCALED && !is_v;
+      if (by_window) {
+        ids = load_ids(u.j0);
+        scales = load_scales(u.j0, ids);
+      } else {
+        id = next_id(), id_next = next_id();
+      }
       for (int j = u.j0; j < u.j1; ++j, ++g) {
         if (j >= p.withhold_from) {
           withheld = true;
           break;
         }
-        const int id_after = next_id();
+        int id_after = -1;
+        if (by_window) {
+          const int x = (j - u.j0) & 7;
+          if (x == 0 && j > u.j0) ids = ids_after, scales = scales_after;
+          if (x == 0) ids_after = load_ids(j + 8);
+          if (x == 4) scales_after = load_scales(j + 4, ids_after);
+          id = __shfl_sync(0xffffffffu, ids, 4 * x + (lane & 3));
+        } else {
+          id_after = next_id();
+        }
         const int i = 2 * g + (is_v ? 1 : 0), st = i % NC;
         if (i >= NC && !wait_all(kFreed + st, uint32_t(i / NC - 1))) {
           ok = false;
           break;
         }
+        if (by_window) {  // (before the arrival: who has seen that has seen these)
+          const uint32_t w = __shfl_sync(0xffffffffu, scales, 4 * ((j - u.j0) & 7) + (lane & 3));
+          if (lane < 4) *reinterpret_cast<uint16_t *>(sm + L::kOffBar + kScaleOff + (g & (kScaleTiles - 1)) * 8 + 2 * lane) = uint16_t(w);
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive_expect_tx(bar(kLanded + st), kCopied);
         __syncwarp();
         if (lane < n_copies) {
           const bool there = pos < n_pages && id >= 0 && int64_t(id) < p.num_pages;
-          if (pos < n_pages && !there) bad |= PSD_FAULT_PAGE_ID;
+          if (!by_window && pos < n_pages && !there) bad |= PSD_FAULT_PAGE_ID;
           // the first token slot; not there: wholly outside the view, which reads as zeros
           const int64_t first = there ? int64_t(id) * P + off : -1024;
           if constexpr (FP8)
@@ -518,8 +569,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         }
         __syncwarp();
         step(pos, off);
-        id = id_next;
-        id_next = id_after;
+        if (!by_window) id = id_next, id_next = id_after;
       }
     }
     if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
@@ -804,6 +854,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       float *sum_row = p.sum_o + (int64_t(blockIdx.x) * 2 + slot) * kRows * D + 4 * r;
       float m_sum = neg_inf();
       bool flushed = false;
+      // Scaled blocks: O is in units of 2^(vref - 127), vref V's largest scale byte so far; log2 of what O's sums are
+      // relative to.
+      [[maybe_unused]] int vref = 0;
+      auto o_log2 = [&]() { return SCALED ? m + float(vref) : m; };
       for (int t = slot; t < T; t += 2, ++ops) {
         const int j = u.j0 + (u.two ? t >> 1 : t), base = j * NK;
         ok = wait_all(T_SFULL + slot, ops);
@@ -814,7 +868,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           if constexpr (TERMS > 1) {
             if (t >= 2 && (t >> 1) % L::kFlush == 0) {
               // S(t) is complete, so PV(t - 2), issued before it, is too
-              const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);
+              const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - o_log2());
 #pragma unroll 1
               for (int c = 0; c < D; c += 32) {
                 uint32_t o[32];
@@ -833,7 +887,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                   }
                 }
               }
-              m_sum = m;
+              m_sum = o_log2();
               flushed = empty = true;
             }
           }
@@ -855,6 +909,41 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           fence_proxy_async();
         }
         const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
+        // Scaled blocks: the tile's scale bytes, 16 keys a half word, K's low.  (They were there before its K was, and so
+        // before the S that is complete now.)
+        [[maybe_unused]] uint2 scales = make_uint2(0u, 0u);
+        [[maybe_unused]] bool nan_scale = false;
+        if constexpr (SCALED) {
+          if (warp_live) {
+            const int i = (g + (u.two ? t >> 1 : t)) & (kScaleTiles - 1);
+            const volatile uint32_t *w = reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kScaleOff + i * 8);
+            scales = make_uint2(w[0], w[1]);
+            int most = 0;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int ke = scale_byte(scales, 2 * y), ve = scale_byte(scales, 2 * y + 1);
+              nan_scale |= ke == 255 || ve == 255;
+              if (ve != 255) most = max(most, ve);
+            }
+            if (most > vref) {
+              // S(t) is complete, so PV(t - 2), issued before it, is too
+              if (!empty) {
+                const float down = ex2(float(vref - most));
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                  uint32_t o[32];
+                  tmem_ld32(lane_base + D * slot + c, o);
+                  ld_wait();
+#pragma unroll
+                  for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * down);
+                  tmem_st32(lane_base + D * slot + c, o);
+                }
+              }
+              vref = most;
+            }
+            if (vref == 0) vref = 1;  // (all of them 2^-127, or NaN: what O is multiplied by must not be 0)
+          }
+        }
         auto give_part = [&](auto which) -> bool {
           constexpr int part = decltype(which)::value;
           if (warp_live) {
@@ -879,6 +968,47 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
 #pragma unroll
                   for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1u ? x[c] : 0xff800000u;
                 }
+                if constexpr (SCALED) {
+#pragma unroll
+                  for (int c1 = 0; c1 < 32; c1 += 16) {
+                    const int y = (c0 + c1) / 16, ke = scale_byte(scales, 2 * y), ve = scale_byte(scales, 2 * y + 1);
+                    // the scores' factor, and log2 of V's scale below vref
+                    const float factor = qs * (ke == 255 ? 1.f : scale_value(ke));
+                    const float down = ve == 255 ? 0.f : float(max(ve - vref, -64));
+                    if (nan_scale && ke == 255) {
+#pragma unroll
+                      for (int c = c1; c < c1 + 16; ++c) x[c] = x[c] == 0xff800000u ? x[c] : 0x7fffffffu;
+                    }
+                    float top4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+                    for (int c = c1; c < c1 + 16; c += 8)
+#pragma unroll
+                      for (int k = 0; k < 4; ++k)
+                        top4[k] = max3(top4[k], __uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1]));
+                    t4[y] = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * factor;
+                    const float2 f2 = make_float2(factor, factor), n2 = make_float2(nm + down, nm + down);
+                    float2 part_sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+                    for (int c = c1; c < c1 + 16; c += 2) {
+                      const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2, n2);
+                      float a = ex2(z.x), b = ex2(z.y);
+                      part_sum[(c >> 1) & 1] = __fadd2_rn(part_sum[(c >> 1) & 1], make_float2(a, b));
+                      if (nan_scale && ve == 255) {  // what is hidden stays so
+                        a = a == 0.f ? 0.f : __int_as_float(0x7fffffff);
+                        b = b == 0.f ? 0.f : __int_as_float(0x7fffffff);
+                      }
+                      if constexpr (TERMS == 1) {
+                        pk[(c0 + c) / 2] = p_bits<FP8>(a, b);
+                      } else {
+                        pf[c0 + c] = a;
+                        pf[c0 + c + 1] = b;
+                      }
+                    }
+                    part_sum[0] = __fadd2_rn(part_sum[0], part_sum[1]);
+                    const float up = ex2(-down);
+                    sum[0] = __ffma2_rn(part_sum[0], make_float2(up, up), sum[0]);
+                  }
+                } else {
 #pragma unroll
                 for (int c = 0; c < 32; c += 8)
 #pragma unroll
@@ -897,9 +1027,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                     pf[c0 + c + 1] = b;
                   }
                 }
+                }
               }
               float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-              top = live ? top * qs : neg_inf();        // qs > 0; (a dead row's scores are whatever Q held)
+              top = live ? (SCALED ? top : top * qs) : neg_inf();  // qs > 0; (a dead row's scores are whatever Q held)
               const bool grow = top > m + (L::kBias + kLazy);
               if (!__any_sync(0xffffffffu, grow)) break;
               // O may be changed: S(t) is complete, so PV(t - 2), issued before it, is too; the first
@@ -1001,7 +1132,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         }
         __syncwarp();
       };
-      const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - m);  // flushed sums to 2^m
+      const float keep = m_sum == neg_inf() ? 0.f : ex2(m_sum - o_log2());  // flushed sums to O's
       auto add_flushed = [&](float (&x)[32], const float *from, float scale) {
 #pragma unroll
         for (int k = 0; k < 32; k += 4) {
@@ -1018,15 +1149,17 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
       // which this unit's O waited for, and waits here before its next.)
       const bool joint = !u.two && T > 1;
       float m1 = neg_inf(), l1 = 0.f, keep1 = 0.f;
+      [[maybe_unused]] int vref1 = 0;
       if (joint) {
         if constexpr (TERMS > 1) __threadfence_block();  // sum_row is read by the other slot
         reinterpret_cast<float4 *>(sm + L::kOffOut + (warp ^ 4) * (32 * 128))[lane] =
-            make_float4(m, l, flushed ? keep : 0.f, 0.f);
+            make_float4(m, l, flushed ? keep : 0.f, __int_as_float(vref));
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(T_XREADY + (slot ^ 1)));
         if (!(ok = wait_all(T_XREADY + slot, uint32_t(singles)))) break;
         const float4 other = reinterpret_cast<const float4 *>(stage)[lane];
         m1 = other.x, l1 = other.y, keep1 = other.z;
+        vref1 = __float_as_int(other.w);
         __syncwarp();
         ++singles;
       }
@@ -1034,7 +1167,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         const float top = fmaxf(m, m1), from = top == neg_inf() ? 0.f : top;
         const float w0 = ex2(m - from), w1 = ex2(m1 - from);  // 0 where a slot saw no key
         const float all = l * w0 + l1 * w1, inv = all == 0.f ? 0.f : p.v_scale / all;
-        const float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
+        float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
+        if constexpr (SCALED) f0 *= scale_value(uint32_t(vref)), f1 *= scale_value(uint32_t(vref1));
         const int c_end = joint ? D / 2 * (slot + 1) : D;
 #pragma unroll 1
         for (int c = joint ? D / 2 * slot : 0; c < c_end; c += 32) {
@@ -1180,7 +1314,7 @@ bool encode(CUtensorMap *map, const DeviceInfo &dev, int rank, const void *base,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int TERMS, bool FP8>
+template <int D, int TERMS, bool FP8, bool SCALED = false>
 psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &place, const DeviceInfo &dev,
                cudaStream_t s) {
   using L = Lay<D, TERMS, FP8>;
@@ -1199,7 +1333,8 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   p.TH = kRows / S.G;
   p.page_size = S.page_size;
   p.sub = 8;
-  while (p.sub < L::NK && S.page_size % (2 * p.sub) == 0) p.sub *= 2;
+  while (p.sub < (SCALED ? 16 : L::NK) && S.page_size % (2 * p.sub) == 0) p.sub *= 2;
+  p.scales = S.scales;
   p.out_f32 = S.out_f32;
   p.q_scale = S.q_scale;
   p.v_scale = S.v_scale;
@@ -1315,7 +1450,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
   }
   if (!mapped) return fail(PSD_ERR_CUDA, "cuTensorMapEncodeTiled failed for the KV pool");
 
-  auto kern = step_tc_kernel<D, TERMS, FP8>;
+  auto kern = step_tc_kernel<D, TERMS, FP8, SCALED>;
   // once a device: the attribute stays, and setting it is a microsecond of every call
   static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev.device < 64 ? uint64_t(1) << dev.device : 0;
@@ -1354,7 +1489,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, const StepPlace &p
 
 bool step_tc_supports(const StepParams &p) {
   // q_scale > 0: the kernel takes the row maximum of the raw scores before scaling
-  return !p.scaled && (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.G <= kRows && p.q_scale > 0.f &&
+  return (p.D == 64 || p.D == 128) && p.page_size % 8 == 0 && p.G <= kRows && p.q_scale > 0.f &&
          p.num_pages * p.page_size <= 0x7fffffffLL;
 }
 
@@ -1372,6 +1507,7 @@ psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const St
                           cudaStream_t s) {
   auto go = [&](auto d) {
     constexpr int D = decltype(d)::value;
+    if (p.scaled) return p.out_f32 ? run<D, 2, true, true>(p, req, place, dev, s) : run<D, 1, true, true>(p, req, place, dev, s);
     if (p.fp8) return p.out_f32 ? run<D, 2, true>(p, req, place, dev, s) : run<D, 1, true>(p, req, place, dev, s);
     return p.out_f32 ? run<D, 3, false>(p, req, place, dev, s) : run<D, 1, false>(p, req, place, dev, s);
   };
