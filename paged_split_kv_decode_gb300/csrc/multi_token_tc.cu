@@ -40,10 +40,12 @@
 // copies, conversion and MMAs otherwise fill.  With bf16 operands and Q in shared memory 16 requests'
 // trees of 9 to 24 tokens over 512 to 8192 keys took 61 us against 54.  (K's codes taken as they are by
 // kind::f8f6f4, against Q in two e4m3 terms, were no faster.)
-// A cache of 8-bit blocks with a scale each (SCALED): the warp that loads K also brings, eight tiles ahead, each tile's four
-// scale bytes of K and of V into a ring in shared memory.  K's scale 2^a goes into the score factor of its 16 keys, V's 2^b
-// into the exponent of P: P' = 2^(s - m + b - r) with r the largest b of the row's keys so far (O is rescaled when r
-// grows), l = sum 2^(r - b) sum P', both exact.  Where b is more than 2^64 below r it counts as 2^64.
+// A cache of 8-bit blocks with a scale each (SCALED): the load warps also bring, eight tiles ahead, each tile's four scale
+// bytes into rings in shared memory, and the conversion gives f16 values in units of the tile's largest scale (a warp has one
+// block; blocks 2^15 below the tile's largest are exact, beyond that what f16 loses is 2^-33 of the largest).  What is left is
+// a factor a tile: K's on the scores, V's 2^b in the exponent of P, 2^(s - m + b - r) with r the largest b so far (O is
+// rescaled when r grows; b counts as r - 64 at least) and l += 2^(r - b) sum P.  Factors of every 16 keys in the softmax, whose
+// chain bounds the kernel, took 421 us for 2048 tokens over 4096 keys and 940 with f32 outputs.
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
@@ -147,11 +149,13 @@ enum {
   T_XREADY,                          // [2] the other slot's (m, l) of the rows are there (4 warps)
   T_DRAIN = T_XREADY + 2, T_SLOT, T_TAIL
 };
-// Behind the barriers: the scales of 32 key tiles, four pairs of K's byte and V's each.  The loads are at most 14 tiles
-// ahead of the softmax (eight of codes, four of f16, two that a slot may lag behind).
-constexpr uint32_t kScaleOff = 768;
-constexpr int kScaleTiles = 32;
-static_assert(T_TAIL * 8 + 16 <= kScaleOff && kScaleOff + kScaleTiles * 8 <= 1024, "barrier area");
+// Behind the barriers, scales of key tiles: V's four bytes of 16 tiles (from the V loads to its conversion, at most eight
+// tiles), and four pairs of K's and V's of 32 (from the K loads to its conversion and the softmax: at most eight tiles of
+// codes, four of f16 and two that a slot may lag behind).
+constexpr uint32_t kVScaleOff = 704, kScaleOff = 768;
+constexpr int kVScaleTiles = 16, kScaleTiles = 32;
+static_assert(T_TAIL * 8 + 16 <= kVScaleOff && kVScaleOff + kVScaleTiles * 4 <= kScaleOff && kScaleOff + kScaleTiles * 8 <= 1024,
+              "barrier area");
 
 struct TCParams {
   const int32_t *page_indices;
@@ -368,8 +372,16 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, uint
   return true;
 }
 
-// Byte i of a tile's scales.
-__device__ __forceinline__ int scale_byte(const uint2 &w, int i) { return int((i < 4 ? w.x : w.y) >> (8 * (i & 3)) & 255u); }
+// The largest of a tile's four scale bytes that are not NaN's.
+__device__ __forceinline__ int largest_scale(uint32_t e4) {
+  int most = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int e = int(e4 >> (8 * i) & 255u);
+    most = e == 255 ? most : max(most, e);
+  }
+  return most;
+}
 
 // The visible keys of one row among the 32 from `base` on, one bit each.
 __device__ __forceinline__ uint32_t visible(int base, int seen, int start, uint64_t tree, bool has_tree) {
@@ -504,7 +516,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         return id;
       };
       int id = -1, id_next = -1;
-      // Scaled blocks, K: page ids and scales of eight tiles, a lane for 16 keys; those of the next eight are on their way.
+      // Scaled blocks: page ids and scales of eight tiles, a lane for 16 keys; those of the next eight are on their way.
       [[maybe_unused]] int ids = -1, ids_after = -1;
       [[maybe_unused]] uint32_t scales = 0, scales_after = 0;
       [[maybe_unused]] auto load_ids = [&](int tile) {
@@ -516,13 +528,12 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         return -1;
       };
       [[maybe_unused]] auto load_scales = [&](int tile, int x) {
-        if (x < 0) return 127u;  // K's and, as 0, V's: of keys that nobody sees
+        if (x < 0) return 0u;  // of keys that nobody sees
         const int64_t slot = int64_t(x) * P + ((tile + lane / 4) * NK + 16 * (lane & 3)) % P;
         const int64_t at = (slot >> p.scales.shift) * p.Hkv + u.kv;
         return uint32_t(__ldg(p.scales.k + at)) | uint32_t(__ldg(p.scales.v + at)) << 8;
       };
-      const bool by_window = SCALED && !is_v;
-      if (by_window) {
+      if constexpr (SCALED) {
         ids = load_ids(u.j0);
         scales = load_scales(u.j0, ids);
       } else {
@@ -534,7 +545,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           break;
         }
         int id_after = -1;
-        if (by_window) {
+        if constexpr (SCALED) {
           const int x = (j - u.j0) & 7;
           if (x == 0 && j > u.j0) ids = ids_after, scales = scales_after;
           if (x == 0) ids_after = load_ids(j + 8);
@@ -548,16 +559,19 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           ok = false;
           break;
         }
-        if (by_window) {  // (before the arrival: who has seen that has seen these)
+        if constexpr (SCALED) {  // (before the arrival: who has seen that has seen these)
           const uint32_t w = __shfl_sync(0xffffffffu, scales, 4 * ((j - u.j0) & 7) + (lane & 3));
-          if (lane < 4) *reinterpret_cast<uint16_t *>(sm + L::kOffBar + kScaleOff + (g & (kScaleTiles - 1)) * 8 + 2 * lane) = uint16_t(w);
+          if (lane < 4) {
+            if (is_v) sm[L::kOffBar + kVScaleOff + (g & (kVScaleTiles - 1)) * 4 + lane] = uint8_t(w >> 8);
+            else *reinterpret_cast<uint16_t *>(sm + L::kOffBar + kScaleOff + (g & (kScaleTiles - 1)) * 8 + 2 * lane) = uint16_t(w);
+          }
           __syncwarp();
         }
         if (lane == 0) mbar_arrive_expect_tx(bar(kLanded + st), kCopied);
         __syncwarp();
         if (lane < n_copies) {
           const bool there = pos < n_pages && id >= 0 && int64_t(id) < p.num_pages;
-          if (!by_window && pos < n_pages && !there) bad |= PSD_FAULT_PAGE_ID;
+          if (!SCALED && pos < n_pages && !there) bad |= PSD_FAULT_PAGE_ID;
           // the first token slot; not there: wholly outside the view, which reads as zeros
           const int64_t first = there ? int64_t(id) * P + off : -1024;
           if constexpr (FP8)
@@ -569,7 +583,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         }
         __syncwarp();
         step(pos, off);
-        if (!by_window) id = id_next, id_next = id_after;
+        id = id_next;
+        id_next = id_after;
       }
     }
     if (!ok) bad |= PSD_FAULT_WAIT_TIMEOUT;
@@ -607,6 +622,22 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           tk = (D == 128 ? s >> 1 : s) * 8 + (lane & 7);
           chunk = (D == 128 ? (s & 1) * 4 : 0) + (lane >> 3);
         };
+        // Scaled blocks: a warp has the tile's tokens 16 w .. of one block; its scale, to the tile's largest.
+        static_assert(!SCALED || kSteps * 8 / (D == 128 ? 2 : 1) == 16, "a block a warp");
+        __half2 by = __floats2half2_rn(1.f, 1.f);
+        bool other = false;
+        if constexpr (SCALED) {
+          uint32_t e4;  // the four bytes
+          if (v) {
+            e4 = *reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kVScaleOff + (g & (kVScaleTiles - 1)) * 4);
+          } else {
+            const volatile uint32_t *at = reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kScaleOff + (g & (kScaleTiles - 1)) * 8);
+            e4 = __byte_perm(at[0], at[1], 0x6420);
+          }
+          const int mine = int(e4 >> (8 * (th >> 5)) & 255u), down = mine - largest_scale(e4);
+          other = down != 0;
+          by = mine == 255 ? __float2half2_rn(scale_value(255)) : __float2half2_rn(down < -24 ? 0.f : ex2(float(down)));
+        }
         uint4 w[kSteps];
 #pragma unroll
         for (int c = 0; c < kSteps; ++c) {
@@ -620,6 +651,13 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           place(c, tk, chunk);
           uint32_t out[8];
           codes_to_f16(w[c], out);
+          if (SCALED && other) {
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(out + y), by);
+              out[y] = *reinterpret_cast<const uint32_t *>(&x);
+            }
+          }
           if (tk >= left) {
 #pragma unroll
             for (int y = 0; y < 8; ++y) out[y] = 0u;
@@ -909,39 +947,37 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           fence_proxy_async();
         }
         const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
-        // Scaled blocks: the tile's scale bytes, 16 keys a half word, K's low.  (They were there before its K was, and so
-        // before the S that is complete now.)
-        [[maybe_unused]] uint2 scales = make_uint2(0u, 0u);
-        [[maybe_unused]] bool nan_scale = false;
+        // Scaled blocks: the tile's score factor, log2 of its V's scale below vref and the inverse.  (The scales were there
+        // before the tile's K was, and so before the S that is complete now.)
+        float tile_qs = qs;
+        [[maybe_unused]] float down = 0.f, up = 1.f;
         if constexpr (SCALED) {
           if (warp_live) {
             const int i = (g + (u.two ? t >> 1 : t)) & (kScaleTiles - 1);
             const volatile uint32_t *w = reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kScaleOff + i * 8);
-            scales = make_uint2(w[0], w[1]);
-            int most = 0;
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              const int ke = scale_byte(scales, 2 * y), ve = scale_byte(scales, 2 * y + 1);
-              nan_scale |= ke == 255 || ve == 255;
-              if (ve != 255) most = max(most, ve);
-            }
-            if (most > vref) {
+            const uint32_t w0 = w[0], w1 = w[1];
+            const int ve = largest_scale(__byte_perm(w0, w1, 0x7531));
+            if (ve > vref) {
               // S(t) is complete, so PV(t - 2), issued before it, is too
               if (!empty) {
-                const float down = ex2(float(vref - most));
+                const float alpha = ex2(float(vref - ve));
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                   uint32_t o[32];
                   tmem_ld32(lane_base + D * slot + c, o);
                   ld_wait();
 #pragma unroll
-                  for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * down);
+                  for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
                   tmem_st32(lane_base + D * slot + c, o);
                 }
               }
-              vref = most;
+              vref = ve;
             }
             if (vref == 0) vref = 1;  // (all of them 2^-127, or NaN: what O is multiplied by must not be 0)
+            // (a normal number: times a score of -inf, 0 would be NaN)
+            tile_qs = fmaxf(qs * scale_value(uint32_t(largest_scale(__byte_perm(w0, w1, 0x6420)))), 0x1p-126f);
+            down = float(max(ve - vref, -64));
+            up = ex2(-down);
           }
         }
         auto give_part = [&](auto which) -> bool {
@@ -955,7 +991,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             float2 sum[2];
             for (;;) {
               const float nm = m == neg_inf() ? 0.f : -m;
-              const float2 qs2 = make_float2(qs, qs), nm2 = make_float2(nm, nm);
+              const float2 qs2 = make_float2(tile_qs, tile_qs), nm2 = make_float2(nm + down, nm + down);
               float t4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
               sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -968,47 +1004,6 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
 #pragma unroll
                   for (int c = 0; c < 32; ++c) x[c] = (bits >> c) & 1u ? x[c] : 0xff800000u;
                 }
-                if constexpr (SCALED) {
-#pragma unroll
-                  for (int c1 = 0; c1 < 32; c1 += 16) {
-                    const int y = (c0 + c1) / 16, ke = scale_byte(scales, 2 * y), ve = scale_byte(scales, 2 * y + 1);
-                    // the scores' factor, and log2 of V's scale below vref
-                    const float factor = qs * (ke == 255 ? 1.f : scale_value(ke));
-                    const float down = ve == 255 ? 0.f : float(max(ve - vref, -64));
-                    if (nan_scale && ke == 255) {
-#pragma unroll
-                      for (int c = c1; c < c1 + 16; ++c) x[c] = x[c] == 0xff800000u ? x[c] : 0x7fffffffu;
-                    }
-                    float top4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-                    for (int c = c1; c < c1 + 16; c += 8)
-#pragma unroll
-                      for (int k = 0; k < 4; ++k)
-                        top4[k] = max3(top4[k], __uint_as_float(x[c + 2 * k]), __uint_as_float(x[c + 2 * k + 1]));
-                    t4[y] = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]) * factor;
-                    const float2 f2 = make_float2(factor, factor), n2 = make_float2(nm + down, nm + down);
-                    float2 part_sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-                    for (int c = c1; c < c1 + 16; c += 2) {
-                      const float2 z = __ffma2_rn(make_float2(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2, n2);
-                      float a = ex2(z.x), b = ex2(z.y);
-                      part_sum[(c >> 1) & 1] = __fadd2_rn(part_sum[(c >> 1) & 1], make_float2(a, b));
-                      if (nan_scale && ve == 255) {  // what is hidden stays so
-                        a = a == 0.f ? 0.f : __int_as_float(0x7fffffff);
-                        b = b == 0.f ? 0.f : __int_as_float(0x7fffffff);
-                      }
-                      if constexpr (TERMS == 1) {
-                        pk[(c0 + c) / 2] = p_bits<FP8>(a, b);
-                      } else {
-                        pf[c0 + c] = a;
-                        pf[c0 + c + 1] = b;
-                      }
-                    }
-                    part_sum[0] = __fadd2_rn(part_sum[0], part_sum[1]);
-                    const float up = ex2(-down);
-                    sum[0] = __ffma2_rn(part_sum[0], make_float2(up, up), sum[0]);
-                  }
-                } else {
 #pragma unroll
                 for (int c = 0; c < 32; c += 8)
 #pragma unroll
@@ -1027,10 +1022,9 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                     pf[c0 + c + 1] = b;
                   }
                 }
-                }
               }
               float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-              top = live ? (SCALED ? top : top * qs) : neg_inf();  // qs > 0; (a dead row's scores are whatever Q held)
+              top = live ? top * tile_qs : neg_inf();   // qs > 0; (a dead row's scores are whatever Q held)
               const bool grow = top > m + (L::kBias + kLazy);
               if (!__any_sync(0xffffffffu, grow)) break;
               // O may be changed: S(t) is complete, so PV(t - 2), issued before it, is too; the first
@@ -1071,7 +1065,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
               }
             }
             sum[0] = __fadd2_rn(sum[0], sum[1]);
-            l += sum[0].x + sum[0].y;
+            l = SCALED ? fmaf(sum[0].x + sum[0].y, up, l) : l + (sum[0].x + sum[0].y);
           }
           st_wait();
           fence_before();
