@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "context.h"
@@ -38,7 +39,7 @@ struct Lists {
   int32_t *first;   // [num_pages] fork: the first child that may keep the page; compact: the new id
   int32_t *fresh;   // [num_pages] fork: free pages in order; compact: the counts of the pages that move
   int32_t *start;   // [num_new + 1] fork: where a child's pages begin in the new table
-  int32_t *blank;   // [num_new + 1] fork: and its fresh pages among all
+  int4 *rows;       // [num_new + 1] fork: a child's parent's row, pages handed down, its own row, its fresh pages
   int2 *moves;      // [max(num_new, num_pages / 2) + 1] source and destination; source < 0: none
 };
 size_t lists_of(Lists *l, void *base, int64_t num_pages, int64_t num_new) {
@@ -54,7 +55,7 @@ size_t lists_of(Lists *l, void *base, int64_t num_pages, int64_t num_new) {
   x.first = reinterpret_cast<int32_t *>(take(size_t(num_pages) * 4));
   x.fresh = reinterpret_cast<int32_t *>(take(size_t(num_pages) * 4));
   x.start = reinterpret_cast<int32_t *>(take(size_t(num_new + 1) * 4));
-  x.blank = reinterpret_cast<int32_t *>(take(size_t(num_new + 1) * 4));
+  x.rows = reinterpret_cast<int4 *>(take(size_t(num_new + 1) * 16));
   x.moves = reinterpret_cast<int2 *>(take(size_t(std::max(num_new, num_pages / 2) + 1) * 8));
   if (l) *l = x;
   return size_t(at - static_cast<uint8_t *>(base));
@@ -247,8 +248,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
     if (!faults)
       for (int i = i0; i < i1; ++i) {
         const Child c = child_of(p, i, faults);
-        p.w.blank[i] = int(at);
-        at += c.want - c.full - keeps(c, i);
+        const int kept = c.full + keeps(c, i);
+        p.w.rows[i] = make_int4(c.first, kept, p.w.start[i], int(at));
+        at += c.want - kept;
       }
   }
 
@@ -277,23 +279,170 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
   }
   cluster_sync();
 
-  // The new table.
-  for (int u = warp; u < p.N * parts; u += kWarps) {
-    const int i = u / parts;
+  for (int i = i0; i < i1; ++i) {
     const Child c = child_of(p, i, faults);
-    const bool kept_tail = keeps(c, i);
-    const int kept = c.full + kept_tail;
-    const int start = __ldcg(p.w.start + i), blank = __ldcg(p.w.blank + i);
-    for (int j = (u % parts) * 32 + lane; j < c.want; j += 32 * parts)
-      p.new_indices[start + j] = j < kept ? p.indices[c.first + j] : __ldcg(p.w.fresh + blank + j - kept);
-    if (u % parts == 0 && lane == 0) {
-      p.new_indptr[i] = start;
-      p.new_len[i] = c.want ? c.len + p.room : 0;
-      p.w.moves[i] = c.tail && !kept_tail ? make_int2(p.indices[c.first + c.full], __ldcg(p.w.fresh + blank)) : make_int2(-1, -1);
-    }
+    const int4 r = p.w.rows[i];
+    p.new_indptr[i] = r.z;
+    p.new_len[i] = c.want ? c.len + p.room : 0;
+    p.w.moves[i] = c.tail && r.y == c.full ? make_int2(p.indices[c.first + c.full], __ldcg(p.w.fresh + r.w)) : make_int2(-1, -1);
   }
   if (id == 0) {
     if (p.new_indptr) p.new_indptr[p.N] = pages_wanted;
+    p.w.head->moves = p.N;
+  }
+}
+
+// The same by one CTA with the counts in shared memory, for up to kFewChildren children, kFewPages pages and
+// kFewEntries new entries: its barriers
+// and atomics take tens of cycles where the cluster's take hundreds.  4 children of 40 pages: 9 us against 21; 128 of
+// some 150 among 20000 pages: XX us against 25.
+constexpr int kFewChildren = 1024, kFewPages = 49152, kFewEntries = (1 << 21) - 2;
+
+__device__ __forceinline__ int block_scan(int v, int &total, int *sums) {  // the sum over the threads before
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int up = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, up, d);
+    if (lane >= d) up += x;
+  }
+  __syncthreads();  // (sums are free)
+  if (lane == 31) sums[warp] = up;
+  __syncthreads();
+  int x = sums[lane];
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  total = __shfl_sync(0xffffffffu, x, 31);
+  const int before = __shfl_sync(0xffffffffu, x, warp ? warp - 1 : 0);
+  return (warp ? before : 0) + up - v;
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams p) {
+  extern __shared__ int count[];  // [num_pages], then the rows
+  __shared__ int sums[32];
+  int4 *rows = reinterpret_cast<int4 *>(count + (p.num_pages + 3) / 4 * 4);
+  dependents_may_launch();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_pages = int(p.num_pages);
+  uint32_t faults = 0;
+  int total;
+  // The children, with their part-full pages; the counts.
+  Child c{0, 0, 0, 0, false};
+  int tail = 0;
+  if (tid < p.N) {
+    c = child_of(p, tid, faults);
+    if (c.tail) {
+      tail = p.indices[c.first + c.full];
+      if (tail < 0 || tail >= n_pages) faults |= PSD_FAULT_PAGE_ID, c.tail = false;
+    }
+  }
+  const int64_t old_end = p.B > 0 ? p.indptr[p.B] : 0, old_begin = p.B > 0 ? p.indptr[0] : 0;
+  if (old_begin < 0 || old_end < old_begin || old_end > p.num_indices) faults |= PSD_FAULT_RANGE;
+#pragma unroll 8
+  for (int g = tid; g < n_pages; g += kThreads) {
+    const int r = p.ref[g];
+    if (r < 0) faults |= PSD_FAULT_RANGE;
+    count[g] = r;
+  }
+  // (of wants that do not fit into the new table the sum only has to stay too large)
+  const int start = block_scan(int(min(int64_t(c.want), p.capacity + 1)), total, sums);
+  if (total > p.capacity) faults |= PSD_FAULT_RANGE;
+  // Everybody's faults: from here on all go the same way.
+  auto together = [&]() {
+    const uint32_t x = __reduce_or_sync(0xffffffffu, faults);
+    faults = uint32_t(__syncthreads_or(int(x & 1)) ? 1 : 0);
+    faults |= __syncthreads_or(int(x & 2)) ? 2u : 0u;
+    faults |= __syncthreads_or(int(x & 4)) ? 4u : 0u;
+    faults |= __syncthreads_or(int(x & 8)) ? 8u : 0u;
+    return faults != 0;
+  };
+  auto give_up = [&]() {
+    if (tid == 0) {
+      atomicOr(p.fault, int32_t(faults));
+      p.w.head->moves = 0;
+    }
+  };
+  if (__syncthreads_or(faults != 0)) {
+    together();
+    give_up();
+    return;
+  }
+  // The old requests let go of their pages.
+#pragma unroll 8
+  for (int64_t e = old_begin + tid; e < old_end; e += kThreads) {
+    const int g = p.indices[e];
+    if (g < 0 || g >= n_pages) faults |= PSD_FAULT_PAGE_ID;
+    else if (p.release) atomicSub(count + g, 1);
+  }
+  __syncthreads();
+  for (int g = tid; g < n_pages; g += kThreads)
+    if (count[g] < 0) faults |= PSD_FAULT_RANGE;  // referred to more often than counted
+  if (__syncthreads_or(faults != 0)) {
+    together();
+    give_up();
+    return;
+  }
+  // A part-full page that nobody else refers to goes to its first child: the least child, below 0, stands in its count.
+  const bool claims = c.tail && p.room && count[tail] == 0;
+  __syncthreads();
+  if (claims) atomicMin(count + tail, tid - kFewChildren);
+  __syncthreads();
+  const bool mine = claims && count[tail] == tid - kFewChildren;
+  const bool kept_tail = c.tail && (!p.room || mine);
+  __syncthreads();
+  if (mine) count[tail] = 0;
+  const int kept = c.full + kept_tail;
+  int all_blanks;
+  const int blank = block_scan(c.want - kept, all_blanks, sums);
+  if (tid < p.N) rows[tid] = p.w.rows[tid] = make_int4(c.first, kept, start, blank);
+  __syncthreads();
+  // Pages handed down are counted.
+  const int parts = max(1, kThreads / 32 / max(p.N, 1));  // warps a child
+  for (int u = warp; u < p.N * parts; u += kThreads / 32) {
+    const int4 r = rows[u / parts];
+#pragma unroll 8
+    for (int j = (u % parts) * 32 + lane; j < r.y; j += 32 * parts) {
+      const int g = p.indices[r.x + j];
+      if (g < 0 || g >= n_pages) faults |= PSD_FAULT_PAGE_ID;  // (behind the old table's end)
+      else atomicAdd(count + g, 1);
+    }
+  }
+  __syncthreads();
+  // The free pages, lowest first: a warp has a stretch of them, 32 at a time.
+  const int groups = (n_pages + 31) / 32, each = (groups + 31) / 32;
+  int free_pages = 0;
+  for (int k = warp * each; k < min(groups, (warp + 1) * each); ++k) {
+    const int g = 32 * k + lane;
+    free_pages += __popc(__ballot_sync(0xffffffffu, g < n_pages && count[g] == 0));
+  }
+  int at = block_scan(lane == 0 ? free_pages : 0, total, sums);
+  at = __shfl_sync(0xffffffffu, at, 0);
+  if (total < all_blanks) faults |= PSD_FAULT_NO_PAGES;
+  if (__syncthreads_or(faults != 0)) {
+    together();
+    give_up();
+    return;
+  }
+  for (int k = warp * each; k < min(groups, (warp + 1) * each); ++k) {
+    const int g = 32 * k + lane;
+    const bool free = g < n_pages && count[g] == 0;
+    const uint32_t who = __ballot_sync(0xffffffffu, free);
+    const int rank = at + __popc(who & ((1u << lane) - 1u));
+    if (free && rank < all_blanks) p.w.fresh[rank] = g;
+    if (g < n_pages) p.new_ref[g] = free && rank < all_blanks ? 1 : count[g];
+    at += __popc(who);
+  }
+  __syncthreads();
+  if (tid < p.N) {
+    p.new_indptr[tid] = start;
+    p.new_len[tid] = c.want ? c.len + p.room : 0;
+    p.w.moves[tid] = c.tail && !kept_tail ? make_int2(tail, p.w.fresh[blank]) : make_int2(-1, -1);
+    if (tid == p.N - 1) p.new_indptr[p.N] = start + c.want;
+  }
+  if (tid == 0) {
+    if (p.N == 0 && p.new_indptr) p.new_indptr[0] = 0;
     p.w.head->moves = p.N;
   }
 }
@@ -378,13 +527,26 @@ struct CopyParams {
   int32_t *fault;
   int64_t num_pages;
   int n, pools;
+  // a new table to be written first, if there are children
+  int children;
+  const int4 *rows;
+  const int32_t *new_indptr, *indices, *fresh;
+  int32_t *new_indices;
 };
 
-// A CTA takes one page of one pool at a time: 16 bytes a thread and access, four of them on their way.
-// 16 KB pages, 32 pools, 44 copies (46 MB moved): launch and ramp are most of it.
+// A CTA writes the rows of some children, then takes one page of one pool at a time: 16 bytes a thread and access, four of
+// them on their way.  (The rows here and not in the kernel before: 152 SMs write them beside the copies.)
 __global__ void __launch_bounds__(256) copy_pages_kernel(const CopyParams p, const __grid_constant__ CopyPools pools) {
   wait_for_prior_grid();
   const int n = p.count ? __ldcg(p.count) : p.n;
+  if (n > 0)  // (0: the call has been refused)
+    for (int i = blockIdx.x; i < p.children; i += gridDim.x) {
+      const int4 r = __ldcg(p.rows + i);
+      const int want = __ldcg(p.new_indptr + i + 1) - r.z;
+#pragma unroll 4
+      for (int j = threadIdx.x; j < want; j += 256)
+        p.new_indices[r.z + j] = j < r.y ? p.indices[r.x + j] : __ldcg(p.fresh + r.w + j - r.y);
+    }
   for (int64_t u = blockIdx.x; u < int64_t(n) * p.pools; u += gridDim.x) {
     const int i = int(u / p.pools);
     const psd_page_pool pool = pools.pool[u - int64_t(i) * p.pools];
@@ -425,12 +587,12 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const CopyParams p, con
 // One or more launches over all pools, behind the kernel that makes the list (or not).
 psd_status launch_copy(CopyParams p, const psd_page_pool *pools, int num_pools, int64_t most, bool behind, const DeviceInfo &dev,
                        cudaStream_t s) {
-  for (int k = 0; k < num_pools && most > 0; k += kPoolsALaunch) {
+  for (int k = 0; (k < num_pools && most > 0) || p.children > 0; k += kPoolsALaunch) {
     CopyPools c;
-    p.pools = std::min(kPoolsALaunch, num_pools - k);
+    p.pools = most > 0 ? std::min(kPoolsALaunch, num_pools - k) : 0;
     std::copy(pools + k, pools + k + p.pools, c.pool);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min<int64_t>(most * p.pools, int64_t(dev.num_sms) * 8)));
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(std::max<int64_t>(most * p.pools, p.children), int64_t(dev.num_sms) * 8)));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -440,6 +602,7 @@ psd_status launch_copy(CopyParams p, const psd_page_pool *pools, int num_pools, 
     cfg.numAttrs = behind && k == 0 ? 1 : 0;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, copy_pages_kernel, p, c);
     if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "copy_pages launch: %s", cudaGetErrorString(e));
+    p.children = 0;
   }
   return PSD_OK;
 }
@@ -515,14 +678,34 @@ extern "C" psd_status fork_pages(psd_ctx *ctx, const psd_fork_args *a, void *wor
   p.P = a->page_size;
   p.room = a->room;
   p.release = a->keep_old == 0;
-  fork_kernel<<<kCtas, kThreads, 0, s>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  const size_t shared = (size_t(a->num_pages) + 3) / 4 * 16 + size_t(a->num_new) * 16;
+  if (a->num_new <= kFewChildren && a->num_pages <= kFewPages && a->new_capacity <= kFewEntries) {
+    static std::atomic<uint64_t> ready{0};
+    const uint64_t bit = ctx->dev.device < 64 ? uint64_t(1) << ctx->dev.device : 0;
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(fork_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kFewPages * 4 + kFewChildren * 16);
+      if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+      ready.fetch_or(bit, std::memory_order_release);
+    }
+    fork_few_kernel<<<1, kThreads, shared, s>>>(p);
+  } else {
+    fork_kernel<<<kCtas, kThreads, 0, s>>>(p);
+  }
+  e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "fork_pages launch: %s", cudaGetErrorString(e));
   CopyParams c = {};
   c.count = &p.w.head->moves;
   c.moves = p.w.moves;
   c.fault = a->fault_dev;
   c.num_pages = a->num_pages;
+  c.children = a->num_new;
+  c.rows = p.w.rows;
+  c.new_indptr = a->new_indptr;
+  c.indices = a->page_indices;
+  c.fresh = p.w.fresh;
+  c.new_indices = a->new_indices;
   return launch_copy(c, a->pools, a->num_pools, a->room > 0 ? a->num_new : 0, true, ctx->dev, s);
 }
 

@@ -77,31 +77,38 @@ def check_fork(c, parents, room, **kw):
         assert torch.equal(old, pool)
 
 
+BOTH = pytest.mark.parametrize("extra", [60, 50000])   # one CTA, or a cluster for many pages
+
+
+@pytest.mark.parametrize("extra", [300, 50000])
 @pytest.mark.parametrize("room", [0, 1, 5, 40])
 @pytest.mark.parametrize("page", [1, 5, 16, 64])
-def test_lengths_and_rooms(page, room):
+def test_lengths_and_rooms(page, room, extra):
     lengths = [0, 1, page - 1, page, page + 1, 3 * page, 7 * page - 1]
-    c = Cache(lengths, page, extra=300, seed=page + room)
+    c = Cache(lengths, page, extra=extra, widths=((2,), (3,)), seed=page + room)
     check_fork(c, [0, 1, 1, 1, 2, 3, 3, 4, 4, 6, 6, -1, 5, 6], room)
 
 
 @pytest.mark.parametrize("keep_old", [False, True])
 @pytest.mark.parametrize("in_place", [False, True])
-def test_shared_prompts_and_references_from_outside(keep_old, in_place):
-    c = Cache([50, 50, 50, 33, 48], 16, shared=3, extra=40, seed=3, others=(3, 11))
+@BOTH
+def test_shared_prompts_and_references_from_outside(keep_old, in_place, extra):
+    c = Cache([50, 50, 50, 33, 48], 16, shared=3, extra=extra, seed=3, others=(3, 11))
     check_fork(c, [0, 0, 1, 2, 2, 2, 3, 4, 4], 1, keep_old=keep_old, in_place=in_place)
-    c = Cache([40, 40], 16, shared=3, extra=40, seed=4)                # both hold the same part-full page
+    c = Cache([40, 40], 16, shared=3, extra=extra, seed=4)                # both hold the same part-full page
     check_fork(c, [1, 0, 0], 1, keep_old=keep_old, in_place=in_place)
 
 
-def test_pages_behind_the_tokens_are_let_go():
-    c = Cache([20, 33], 16, spare_pages=2, extra=4, seed=5)
+@BOTH
+def test_pages_behind_the_tokens_are_let_go(extra):
+    c = Cache([20, 33], 16, spare_pages=2, extra=extra, seed=5)
     check_fork(c, [1, 0], 3)
 
 
 @pytest.mark.parametrize("parents", [[], [-1, -1], [0]])
-def test_few_and_none(parents):
-    c = Cache([70, 20, 0], 16, extra=3, seed=6)
+@BOTH
+def test_few_and_none(parents, extra):
+    c = Cache([70, 20, 0], 16, extra=extra, seed=6)
     if parents:
         check_fork(c, parents, 1)
     else:
@@ -111,8 +118,9 @@ def test_few_and_none(parents):
         assert int(fault) == 0 and not ref.any()
 
 
-def test_no_old_requests():
-    c = Cache([20], 16, extra=5, seed=7)
+@BOTH
+def test_no_old_requests(extra):
+    c = Cache([20], 16, extra=extra, seed=7)
     c.kv_len, c.indptr, c.indices, c.ref = [], np.array([0]), np.zeros(0, int), np.zeros_like(c.ref)
     check_fork(c, [-1, -1], 4)
 
@@ -129,6 +137,14 @@ def test_many_requests_and_pages():
 def test_one_request_with_a_long_cache():
     c = Cache([100003], 16, extra=20000, widths=((1,),), seed=9)
     check_fork(c, [0, 0, 0], 1)
+
+
+def test_a_large_pool_that_is_full():
+    """The cluster runs out of pages as the one CTA does."""
+    c = Cache([31, 31], 16, extra=50000, widths=((1,),), seed=10)
+    c.ref[c.ref == 0] = 1                                           # all of them somebody's
+    check_fork(c, [0, 0], 1)                                        # one copy, in a page that the other request left
+    check_fork(c, [0, 0, 0, 0, 1], 2)
 
 
 def test_every_free_page_is_used():
@@ -153,8 +169,9 @@ def test_many_pools():
     (dict(kv_len=[2 ** 31 - 1, 20]), 4), (dict(indptr=[0, 5, 9]), 4), (dict(indptr=[-1, 5, 7]), 4), (dict(indptr=[0, 5, 4]), 4),
     (dict(indices={2: -1}), 1), (dict(indices={6: 10 ** 9}), 1), (dict(ref={3: -1}), 4), (dict(ref="less"), 4),
     (dict(capacity=2), 4)])
-def test_faults_write_nothing(what, bits):
-    c = Cache([70, 20], 16, extra=9, seed=12)
+@BOTH
+def test_faults_write_nothing(what, bits, extra):
+    c = Cache([70, 20], 16, extra=extra, seed=12)
     before = [p.clone() for p in c.pools]
     parents, capacity = what.get("parents", [0, 0, 1]), what.get("capacity")
     c.kv_len = what.get("kv_len", c.kv_len)
