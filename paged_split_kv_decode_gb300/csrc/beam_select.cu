@@ -11,7 +11,10 @@
 //   Candidates: each warp keeps the r-th largest of its lanes' largest logits, r = ceil(k / 8); the least of the
 // 8 warps' is a lower bound of the k-th largest so far (8 r >= k logits are no smaller), found without a sort, and
 // rises tile by tile.  What is not below it is kept: some k ln(tiles) + k of a CTA's logits.  Order numbers
-// among those (a count of the larger ones) give the exact k.
+// among those that are not below the last bound (a count of the larger ones) give the exact k.  Warps wait for each
+// other only after the first tile, which makes the bound: with two barriers a tile 240 rows of 131072 took 38 us.
+// Where more is kept than there is room for (logits that rise, many equal ones) the CTA begins again and thins them
+// out tile by tile.
 //
 // A row is split over CTAs so that all SMs have work; a second kernel, one CTA a request, joins the
 // splits' sums and takes the k largest of the rows' candidates in 64 bits.
@@ -19,6 +22,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "context.h"
 #include "device.cuh"
@@ -28,9 +32,10 @@ namespace psd {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kPer = 16;
-constexpr int kTile = kThreads * kPer;       // logits a CTA takes at a time
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kChunk = 2048;                 // a split's logits are a multiple of this
 constexpr int kKeep = 1024;                  // candidates before they are thinned out
+constexpr int kFew = 256;                    // candidates at the end that are put in order among themselves
 constexpr int kMaxK = 64, kMaxBeams = 64;
 constexpr int kMost = 8192;                  // candidates of a request in the second kernel
 
@@ -65,6 +70,11 @@ __device__ __forceinline__ unsigned long long key_of(float x, uint32_t token) {
   return (unsigned long long)(ordered(x)) << 32 | (0xffffffffu - token);
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN operands lose, as in fmaxf
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // The r-th largest of the lanes' values (equal ones count singly).
 __device__ __forceinline__ uint32_t nth_largest(uint32_t v, int r) {
   uint32_t top = 0;
@@ -75,56 +85,33 @@ __device__ __forceinline__ uint32_t nth_largest(uint32_t v, int r) {
   }
   return top;
 }
-__device__ __forceinline__ unsigned long long nth_largest(unsigned long long v, int r) {
-  unsigned long long top = 0;
-  for (int i = 0; i < r; ++i) {
-    top = v;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const uint32_t who = __ballot_sync(0xffffffffu, v == top);
-    if ((threadIdx.x & 31) == __ffs(who) - 1) v = 0;
+template <typename T> __device__ __forceinline__ float logit(T x);
+template <> __device__ __forceinline__ float logit<float>(float x) { return x; }
+template <> __device__ __forceinline__ float logit<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <> __device__ __forceinline__ float logit<__half>(__half x) { return __half2float(x); }
+// A 32-bit word's logits.
+template <typename T> __device__ __forceinline__ void unpack(uint32_t w, float *x) {
+  if constexpr (sizeof(T) == 4) {
+    x[0] = __uint_as_float(w);
+  } else if constexpr (std::is_same_v<T, __half>) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    x[0] = f.x, x[1] = f.y;
+  } else {
+    x[0] = bf16_lo(w), x[1] = bf16_hi(w);
   }
-  return top;
 }
 
-template <typename T> struct Raw;  // 16 logits of a thread as they come
-template <> struct Raw<float> {
-  static constexpr int kVec = 4;
-  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
-    x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
-  }
-  static __device__ __forceinline__ float one(const float *p) { return __ldcs(p); }
-};
-template <> struct Raw<__nv_bfloat16> {
-  static constexpr int kVec = 8;
-  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[2 * i] = bf16_lo(u[i]), x[2 * i + 1] = bf16_hi(u[i]);
-  }
-  static __device__ __forceinline__ float one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-};
-template <> struct Raw<__half> {
-  static constexpr int kVec = 8;
-  static __device__ __forceinline__ void unpack(const uint4 &w, float *x) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(u + i));
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-  }
-  static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
-};
+// What a CTA takes at a time: 16 logits a thread, the next on their way while a tile is worked on.
+constexpr int kPer = 16, kTile = kThreads * kPer;
 
 // blockIdx.x: split, blockIdx.y (and z): row.  VEC: rows are 16-byte aligned; otherwise a warp's loads are
 // neighbours one by one.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectParams p) {
-  constexpr int N = Raw<T>::kVec, kLoads = kPer / N;
-  __shared__ unsigned long long kept[kKeep + kTile];
-  __shared__ float bound[kWarps];
-  __shared__ int n_kept;
+  constexpr int N = 16 / int(sizeof(T));  // logits of a 16-byte load
+  __shared__ unsigned long long kept[kKeep + kTile], few[kFew], chosen[kMaxK];
+  __shared__ volatile float bound[kWarps];
+  __shared__ int n_kept, n_few;
   __shared__ double warp_sum[kWarps];
   __shared__ float warp_ref[kWarps];
   dependents_may_launch();
@@ -134,104 +121,179 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
   // no continuations, or one: the second kernel sees to it (a NaN goes on, to be reported there)
   if (score == neg_inf() || (p.finished && p.finished[row])) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t begin = int64_t(split) * p.chunk, end = min(int64_t(p.vocab), begin + p.chunk);
-  const T *x_row = static_cast<const T *>(p.logits) + int64_t(row) * p.stride;
+  const int begin = split * p.chunk, size = min(p.vocab - begin, p.chunk);  // (below 2^31: the splits cover the row just)
+  const T *x_split = static_cast<const T *>(p.logits) + int64_t(row) * p.stride + begin;
   const int r = (p.k + kWarps - 1) / kWarps;
   if (tid == 0) n_kept = 0;
-
-  uint4 raw[kLoads];
-  float x[kPer];
-  // where element c of a thread's 16 lies in a tile
+  // Where a thread's c-th logit lies in a tile.
   auto place = [&](int c) { return VEC ? (c / N) * (kThreads * N) + tid * N + c % N : c * kThreads + tid; };
-  auto load = [&](int64_t tile) {
+  constexpr int kRaw = VEC ? kPer * int(sizeof(T)) / 4 : kPer;  // words on their way
+  uint32_t raw[kRaw];
+  const T *x_mine = x_split + place(0);
+  auto load = [&](int tile) {
+    const bool all = tile + kTile <= size;
     if constexpr (VEC) {
 #pragma unroll
-      for (int c = 0; c < kLoads; ++c)
-        if (tile + place(c * N) + N <= end) raw[c] = __ldcs(reinterpret_cast<const uint4 *>(x_row + tile + place(c * N)));
+      for (int c = 0; c < kPer; c += N)
+        if (all || tile + place(c) + N <= size) {
+          const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(x_mine + tile + (place(c) - place(0))));
+          raw[4 * (c / N)] = w.x, raw[4 * (c / N) + 1] = w.y, raw[4 * (c / N) + 2] = w.z, raw[4 * (c / N) + 3] = w.w;
+        }
+    } else {
+      using Word = std::conditional_t<sizeof(T) == 4, uint32_t, unsigned short>;
+      const Word *at = reinterpret_cast<const Word *>(x_mine + tile);
+      if (all) {
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) raw[c] = __ldcs(at + c * kThreads);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kPer; ++c)
+          if (tile + place(c) < size) raw[c] = __ldcs(at + c * kThreads);
+      }
     }
   };
-  auto values = [&](int64_t tile) {
+  float x[kPer];
+  auto values = [&](int tile) {
     if constexpr (VEC) {
 #pragma unroll
-      for (int c = 0; c < kLoads; ++c) {
-        if (tile + place(c * N) + N <= end) {
-          Raw<T>::unpack(raw[c], x + c * N);
-        } else {
+      for (int c = 0; c < kPer; c += N)
 #pragma unroll
-          for (int i = 0; i < N; ++i) x[c * N + i] = tile + place(c * N + i) < end ? Raw<T>::one(x_row + tile + place(c * N + i)) : neg_inf();
-        }
+        for (int w = 0; w < 4; ++w) unpack<T>(raw[4 * (c / N) + w], x + c + w * (N / 4));
+      if (tile + kTile > size) {
+#pragma unroll
+        for (int c = 0; c < kPer; c += N)
+          if (tile + place(c) + N > size)
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[c + i] = tile + place(c + i) < size ? logit<T>(x_split[tile + place(c + i)]) : neg_inf();
       }
     } else {
 #pragma unroll
-      for (int c = 0; c < kPer; ++c) x[c] = tile + place(c) < end ? Raw<T>::one(x_row + tile + place(c)) : neg_inf();
+      for (int c = 0; c < kPer; ++c) {
+        float two[2];
+        unpack<T>(raw[c], two);
+        x[c] = two[0];
+      }
+      if (tile + kTile > size) {
+#pragma unroll
+        for (int c = 0; c < kPer; ++c)
+          if (tile + place(c) >= size) x[c] = neg_inf();
+      }
     }
   };
   constexpr float kL = 1.44269502f, kL2 = 1.92596303e-8f;  // log2 e, f32 and the rest
   float ref = neg_inf(), sum = 0.f, rest = 0.f, best = neg_inf();
-  auto thin = [&]() {  // the k largest of those kept, in order, to the front; all threads
-    const int n = n_kept;
+  auto lowest = [&]() {
     float low = bound[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) low = fminf(low, bound[w]);
+    return low;
+  };
+  // The k largest of those kept, in order, to the front; all threads.
+  auto thin = [&]() {
+    const int n = n_kept;
+    const float low = lowest();
     const unsigned long long least = low == neg_inf() ? 1ull : (unsigned long long)(ordered(low)) << 32;
-    __shared__ unsigned long long chosen[kMaxK];
     if (tid < p.k) chosen[tid] = 0;
+    if (tid == 0) n_few = 0;
     __syncthreads();
-    for (int i = tid; i < n; i += kThreads) {
-      const unsigned long long mine = kept[i];
-      if (mine < least) continue;
+    for (int i = tid; i < n; i += kThreads)
+      if (kept[i] >= least) {
+        const int at = atomicAdd(&n_few, 1);
+        if (at < kFew) few[at] = kept[i];
+      }
+    __syncthreads();
+    const int m = n_few <= kFew ? n_few : n;
+    const unsigned long long *from = n_few <= kFew ? few : kept;
+    for (int i = tid; i < m; i += kThreads) {
+      const unsigned long long mine = from[i];
       int larger = 0;
-      for (int j = 0; j < n; ++j) larger += kept[j] > mine;
-      if (larger < p.k) chosen[larger] = mine;
+#pragma unroll 8
+      for (int j = 0; j < m; ++j) larger += from[j] > mine;
+      if (mine >= least && larger < p.k) chosen[larger] = mine;
     }
     __syncthreads();
     if (tid < p.k) kept[tid] = chosen[tid];
     if (tid == 0) n_kept = min(n, p.k);
     __syncthreads();
   };
-  load(begin);
-  for (int64_t tile = begin; tile < end; tile += kTile) {
-    values(tile);
-    if (tile + kTile < end) load(tile + kTile);
-    float top = neg_inf();
+  // One pass over the split's logits.  Careful: what is kept is thinned out wherever there could be too much of it.
+  // Otherwise false where there was.
+  auto pass = [&](bool careful) {
+    const int room = careful ? kKeep : kKeep + kTile;
+    bool full = false;  // this thread has found no room, or, careful, put one behind the kKeep-th
+    load(0);
+    for (int tile = 0; tile < size; tile += kTile) {
+      values(tile);
+      if (size - tile > kTile) load(tile + kTile);
+      float top = neg_inf();  // (NaN loses)
 #pragma unroll
-    for (int c = 0; c < kPer; ++c) {
-      x[c] = fmaxf(x[c], neg_inf());  // NaN counts as -inf
-      top = fmaxf(top, x[c]);
+      for (int c = 0; c < kPer; c += 2) top = max3(top, x[c], x[c + 1]);
+      if (top * kL > ref + 16.f) {  // (false while all are -inf)
+        const float to = fminf(ceilf(top * kL), 3e38f);
+        const float down = ref == neg_inf() ? 0.f : ex2(ref - to);
+        sum *= down, rest *= down;
+        ref = to;
+      }
+      const float from = ref == neg_inf() ? 0.f : -ref;
+      const float2 from2 = make_float2(from, from), l2 = make_float2(kL, kL), l22 = make_float2(kL2, kL2);
+      float e0;
+      for (;;) {
+        float2 e[kPer / 2];
+#pragma unroll
+        for (int c = 0; c < kPer / 2; ++c) {
+          const float2 y = make_float2(x[2 * c], x[2 * c + 1]);
+          const float2 z = __ffma2_rn(y, l22, __ffma2_rn(y, l2, from2));
+          e[c] = make_float2(ex2(z.x), ex2(z.y));
+        }
+#pragma unroll
+        for (int d = kPer / 4; d; d >>= 1)
+#pragma unroll
+          for (int c = 0; c < d; ++c) e[c] = __fadd2_rn(e[c], e[c + d]);
+        e0 = e[0].x + e[0].y;
+        if (e0 == e0) break;
+        bool nan = false;  // NaN counts as -inf (a sum that is NaN without one: +inf among the logits)
+#pragma unroll
+        for (int c = 0; c < kPer; ++c) {
+          nan |= x[c] != x[c];
+          x[c] = fmaxf(x[c], neg_inf());
+        }
+        if (!nan) break;
+      }
+      const float s = sum + e0, t = s - sum;
+      rest += (sum - (s - t)) + (e0 - t);
+      sum = s;
+      const bool first = tile == 0;
+      if (__any_sync(0xffffffffu, first || top > best)) {
+        best = fmaxf(best, top);
+        const uint32_t mine = nth_largest(ordered(best), r);
+        if (lane == 0) bound[warp] = from_ordered(mine);
+      }
+      if (careful) {
+        if (__syncthreads_or(full)) {
+          thin();
+          full = false;
+        }
+      } else if (first) {
+        __syncthreads();
+      }
+      const float low = lowest();  // (what others have put since only makes it sharper)
+      if (top >= low) {
+#pragma unroll
+        for (int c = 0; c < kPer; ++c)
+          if (x[c] >= low && x[c] != neg_inf()) {
+            const int at = atomicAdd(&n_kept, 1);
+            if (at < kKeep + kTile) kept[at] = key_of(x[c], uint32_t(begin + tile + place(c)));
+            full |= at >= room;
+          }
+      }
     }
-    if (top * kL > ref + 16.f) {  // (false while all are -inf)
-      const float to = fminf(ceilf(top * kL), 3e38f);
-      const float down = ref == neg_inf() ? 0.f : ex2(ref - to);
-      sum *= down, rest *= down;
-      ref = to;
-    }
-    const float from = ref == neg_inf() ? 0.f : -ref;
-    float e[kPer];
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) e[c] = ex2(fmaf(x[c], kL, from) + x[c] * kL2);
-#pragma unroll
-    for (int d = kPer / 2; d; d >>= 1)
-#pragma unroll
-      for (int c = 0; c < d; ++c) e[c] += e[c + d];
-    const float s = sum + e[0], t = s - sum;
-    rest += (sum - (s - t)) + (e[0] - t);
-    sum = s;
-    best = fmaxf(best, top);
-    const uint32_t mine = nth_largest(ordered(best), r);
-    if (lane == 0) reinterpret_cast<volatile float *>(bound)[warp] = from_ordered(mine);
-    __syncthreads();  // (the first tile's bounds are needed; later ones only become sharper)
-    float low = bound[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) low = fminf(low, bound[w]);
-    if (top >= low) {
-#pragma unroll
-      for (int c = 0; c < kPer; ++c)
-        if (x[c] >= low && x[c] != neg_inf()) kept[atomicAdd(&n_kept, 1)] = key_of(x[c], uint32_t(tile + place(c)));
-    }
+    return !__syncthreads_or(full);
+  };
+  for (bool careful = false; !pass(careful) && !careful; careful = true) {
+    if (tid == 0) n_kept = 0;
+    ref = best = neg_inf(), sum = rest = 0.f;
     __syncthreads();
-    if (n_kept > kKeep) thin();  // the same for all
   }
-  __syncthreads();
   thin();
   const int64_t at = int64_t(row) * p.splits + split;
   if (tid < p.k) p.keys[at * p.k + tid] = kept[tid];
@@ -256,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
   }
 }
 
-// One CTA a request: its rows' logarithms, then the k largest of their candidates.  As in the first kernel a bound
-// leaves few of them to be put in order: all ranks of 640 candidates took 80 us.
+// One CTA a request: its rows' logarithms, then the k largest of their candidates.  64 bits are slow here, so f32 sums
+// rounded down give a bound, those rounded up say who may reach it, and only these are added and put in order in 64 bits.
 __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParams p) {
   extern __shared__ unsigned long long shared[];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -265,85 +327,105 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   unsigned long long *value = shared, *key = shared + most;  // candidates: v in order, and the logit and token
   uint8_t *of = reinterpret_cast<uint8_t *>(key + most);     // and the row
   __shared__ double base[kMaxBeams];                         // what a row's logits are added to
+  __shared__ float row_ref[kMaxBeams], base_down[kMaxBeams], base_up[kMaxBeams];
   __shared__ uint8_t kind[kMaxBeams];                        // 0: no continuation, 1: pad_token, 2: candidates
-  __shared__ unsigned long long bound[kWarps];
+  __shared__ float bound[kWarps];
   __shared__ int n_shared;
+  // A warp takes every eighth candidate, so that all have some of every row: one without any leaves no bound.
   wait_for_prior_grid();
   const int64_t from = int64_t(b) * most;
-  const unsigned long long early = tid < most ? p.keys[from + tid] : 0;  // on its way beside the sums
+  const int first = lane * kWarps + warp;
+  const unsigned long long early = first < most ? p.keys[from + first] : 0;  // on its way beside the sums
+  float score = 0.f;
+  bool done = false;
+  if (tid < p.beams) {
+    score = p.scores[b * p.beams + tid];
+    done = p.finished && p.finished[b * p.beams + tid];
+  }
   if (tid == 0) n_shared = 0;
   for (int w = warp; w < p.beams; w += kWarps) {
-    const int row = b * p.beams + w;
-    const float score = p.scores[row];
-    const bool done = p.finished && p.finished[row];
-    float ref = neg_inf(), refs[2];
+    const int64_t at = int64_t(b * p.beams + w) * p.splits;
+    float refs[2];
     double sums[2];  // at most 64 splits: two a lane
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = lane + 32 * i;
-      refs[i] = s < p.splits ? p.refs[int64_t(row) * p.splits + s] : neg_inf();
-      sums[i] = s < p.splits ? p.sums[int64_t(row) * p.splits + s] : 0.0;
+      refs[i] = s < p.splits ? p.refs[at + s] : neg_inf();
+      sums[i] = s < p.splits ? p.sums[at + s] : 0.0;
     }
-    double add = double(score);
+    float ref = fmaxf(refs[0], refs[1]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
+    double sum = 0.0;
+    if (ref != neg_inf()) sum = sums[0] * double(ex2(refs[0] - ref)) + sums[1] * double(ex2(refs[1] - ref));
+#pragma unroll
+    for (int d = 16; d; d >>= 1)
+      if (d < p.splits) sum += __shfl_xor_sync(0xffffffffu, sum, d);  // (lanes behind the splits hold 0)
+    if (lane == 0) base[w] = sum, row_ref[w] = ref;
+  }
+  __syncthreads();
+  if (tid < p.beams) {  // a lane a row: the logarithms at once
     int what = score == neg_inf() ? 0 : done ? 1 : 2;
     bool bad = isnan(score) || score == -neg_inf();
-    if (what == 2 && !bad) {
-      ref = fmaxf(refs[0], refs[1]);
-#pragma unroll
-      for (int d = 16; d; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-      double sum = 0.0;
-      if (ref != neg_inf()) sum = sums[0] * double(ex2(refs[0] - ref)) + sums[1] * double(ex2(refs[1] - ref));
-#pragma unroll
-      for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    double add = double(score);
+    if (what == 2 && !bad) {  // (rows that are finished or were never filled have left no sums)
+      const double sum = base[tid];
+      const float ref = row_ref[tid];
       if (sum == 0.0) what = 0;  // nothing but -inf
       else if (!(sum < 1e300) || ref > 3e38f) bad = true;
       else add -= (double(ref) + log2(sum)) * 0.69314718055994530942;
     }
-    if (bad) what = 0;
-    if (lane == 0) {
-      base[w] = add;
-      kind[w] = uint8_t(what);
-      if (bad) atomicOr(p.fault, PSD_FAULT_RANGE);
+    if (bad) {
+      what = 0;
+      atomicOr(p.fault, PSD_FAULT_RANGE);
     }
+    base[tid] = add;
+    base_down[tid] = __double2float_rd(add);
+    base_up[tid] = __double2float_ru(add);
+    kind[tid] = uint8_t(what);
   }
   __syncthreads();
-  auto candidate = [&](int i, unsigned long long &k) {  // v in order; 0: none
-    const int w = i / per_row;
-    if (kind[w] == 2) {
-      k = i == tid ? early : p.keys[from + i];
-      return k ? ordered(double(from_ordered(uint32_t(k >> 32))) + base[w]) : 0ull;
-    }
-    k = key_of(0.f, uint32_t(p.pad));
-    return kind[w] == 1 && i == w * per_row ? ordered(base[w]) : 0ull;
+  // A candidate's logit and token; 0: none.
+  auto candidate = [&](int i, int w) {
+    if (kind[w] == 2) return i == first ? early : p.keys[from + i];
+    return kind[w] == 1 && i == w * per_row ? key_of(0.f, uint32_t(p.pad)) : 0ull;
   };
-  unsigned long long best = 0, k;
-  for (int i = tid; i < most; i += kThreads) best = max(best, candidate(i, k));
-  const unsigned long long mine = nth_largest(best, (p.k + kWarps - 1) / kWarps);
-  if (lane == 0) bound[warp] = mine;
+  float best = neg_inf();
+  for (int i = first; i < most; i += kThreads) {
+    const int w = i / per_row;
+    const unsigned long long k = candidate(i, w);
+    if (k) best = fmaxf(best, __fadd_rd(from_ordered(uint32_t(k >> 32)), base_down[w]));
+  }
+  const uint32_t mine = nth_largest(ordered(best), (p.k + kWarps - 1) / kWarps);
+  if (lane == 0) bound[warp] = from_ordered(mine);
   __syncthreads();
-  unsigned long long low = bound[0];
+  float low = bound[0];
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) low = min(low, bound[w]);
-  for (int i = tid; i < most; i += kThreads) {
-    const unsigned long long v = candidate(i, k);
-    if (v == 0 || v < low) continue;
+  for (int w = 1; w < kWarps; ++w) low = fminf(low, bound[w]);
+  for (int i = first; i < most; i += kThreads) {
+    const int w = i / per_row;
+    const unsigned long long k = candidate(i, w);
+    if (k == 0) continue;
+    const float x = from_ordered(uint32_t(k >> 32));
+    if (__fadd_ru(x, base_up[w]) < low) continue;
     const int at = atomicAdd(&n_shared, 1);
-    value[at] = v;
+    value[at] = ordered(double(x) + base[w]);
     key[at] = k;
-    of[at] = uint8_t(i / per_row);
+    of[at] = uint8_t(w);
   }
   __syncthreads();
   const int n = n_shared;
   for (int i = tid; i < n; i += kThreads) {
     const unsigned long long v = value[i], x = key[i];
     const uint8_t w = of[i];
-    int larger = 0;
-#pragma unroll 4
+    int larger = 0, equal = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) {
-      const unsigned long long y = value[j];
-      larger += y > v;
-      if (y == v) larger += of[j] < w || (of[j] == w && key[j] > x);
+      larger += value[j] > v;
+      equal += value[j] == v;
     }
+    if (equal > 1)
+      for (int j = 0; j < n; ++j) larger += value[j] == v && (of[j] < w || (of[j] == w && key[j] > x));
     if (larger < p.k) {
       const int64_t to = int64_t(b) * p.k + larger;
       p.out_scores[to] = float(from_ordered(v));
@@ -359,9 +441,10 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   }
 }
 
-// CTAs a row may be split over: two an SM in all, and what the second kernel's CTA can hold.
+// CTAs a row may be split over: those that run at once, four an SM, and what the second kernel's CTA can hold.  (A second
+// wave of few CTAs takes as long as the first.)
 int most_splits(int sms, int rows, int beams, int k) {
-  return int(std::max<int64_t>(1, std::min<int64_t>({(4 * int64_t(sms) + rows - 1) / rows, kMost / (beams * k), 64})));
+  return int(std::max<int64_t>(1, std::min<int64_t>({4 * int64_t(sms) / rows, kMost / (beams * k), 64})));
 }
 
 size_t join_bytes(const SelectParams &p) { return size_t(p.beams) * p.splits * p.k * 17; }
@@ -383,11 +466,11 @@ static psd_status launch_select(const psd_beam_args *a, void *workspace, const D
   p.out_rows = a->out_rows;
   p.out_tokens = a->out_tokens;
   p.fault = a->fault_dev;
-  const int tiles = int((int64_t(a->vocab) + kTile - 1) / kTile);
-  const int splits = std::min(tiles, most_splits(dev.num_sms, a->rows, a->beams, a->k));
-  const int each = (tiles + splits - 1) / splits;
-  p.splits = (tiles + each - 1) / each;
-  p.chunk = int(std::min<int64_t>(int64_t(each) * kTile, 0x7fffffff));
+  const int chunks = int((int64_t(a->vocab) + kChunk - 1) / kChunk);
+  const int splits = std::min(chunks, most_splits(dev.num_sms, a->rows, a->beams, a->k));
+  const int each = (chunks + splits - 1) / splits;
+  p.splits = (chunks + each - 1) / each;
+  p.chunk = int(std::min<int64_t>(int64_t(each) * kChunk, 0x7ffff800));
   uint8_t *at = static_cast<uint8_t *>(workspace);
   const size_t pieces = size_t(a->rows) * p.splits;
   p.sums = reinterpret_cast<double *>(at);
@@ -397,10 +480,14 @@ static psd_status launch_select(const psd_beam_args *a, void *workspace, const D
   const bool vec = aligned16(a->logits) && (a->logits_stride * int64_t(size)) % 16 == 0;
   const int high = std::min(a->rows, 32768);
   const dim3 grid(unsigned(p.splits), unsigned(high), unsigned((a->rows + high - 1) / high));
-  auto go = [&](auto kern) { kern<<<grid, kThreads, 0, s>>>(p); };
-  if (a->logits_type == PSD_LOGITS_F32) go(vec ? select_rows_kernel<float, true> : select_rows_kernel<float, false>);
-  else if (a->logits_type == PSD_LOGITS_BF16) go(vec ? select_rows_kernel<__nv_bfloat16, true> : select_rows_kernel<__nv_bfloat16, false>);
-  else go(vec ? select_rows_kernel<__half, true> : select_rows_kernel<__half, false>);
+  auto go = [&](auto type) {
+    using T = decltype(type);
+    auto kern = vec ? select_rows_kernel<T, true> : select_rows_kernel<T, false>;
+    kern<<<grid, kThreads, 0, s>>>(p);
+  };
+  if (a->logits_type == PSD_LOGITS_F32) go(float{});
+  else if (a->logits_type == PSD_LOGITS_BF16) go(__nv_bfloat16{});
+  else go(__half{});
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "beam_select launch: %s", cudaGetErrorString(e));
   const size_t shared = join_bytes(p);
@@ -429,7 +516,8 @@ using namespace psd;
 
 extern "C" size_t psd_beam_workspace_bytes(const psd_ctx *ctx, int32_t rows, int32_t beams, int32_t k) {
   if (!ctx || rows < 0 || beams < 1 || beams > kMaxBeams || k < 1 || k > kMaxK || beams * k > 4096) return 0;
-  return 256 + size_t(rows) * size_t(most_splits(ctx->dev.num_sms, std::max(rows, 1), beams, k)) * (12 + 8 * size_t(k));
+  // rows * splits is at most 4 an SM, or the rows: more rows never need less
+  return 256 + size_t(std::max(4 * ctx->dev.num_sms, rows)) * (12 + 8 * size_t(k));
 }
 
 extern "C" psd_status beam_select(psd_ctx *ctx, const psd_beam_args *a, void *workspace, size_t workspace_bytes,
