@@ -67,7 +67,7 @@ __device__ __forceinline__ Token locate(const ScaledParams &s, int t0, int own, 
   x.slot = int64_t(id) * p.page_size + at % p.page_size;
   x.older = at % s.block;
   // the first of the block: its request's first token, or the block's
-  if (t == begin || x.older == 0) x.count = min(s.block - x.older, end - t);
+  if (t == begin || x.older == 0) x.count = min(s.block - x.older, min(end, p.T) - t);  // (no row behind the last that is there)
   return x;
 }
 

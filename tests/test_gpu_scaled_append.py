@@ -259,6 +259,55 @@ def test_faults_leave_their_tokens_out(shape):
     _check(s, psd.rope_frequencies(64), positions=pos, left_out=gone, faults=4)
 
 
+@pytest.mark.parametrize("T", [3, 40])
+def test_offsets_that_go_past_the_rows_there_are(T):
+    """q_indptr counts more tokens than the call has rows: those that are there are appended, and nothing else moves the scale."""
+    s = _make([T + 9], [5], Hq=1, Hkv=2, D=64, seed=60, pad_rows=0, spread=1.0, fused=False)
+    s["v"][T:] = 1000.0
+    h, was, had = s["host"], s["v_pool"].cpu().clone(), s["ve"].cpu().clone()
+    cut = {**s, "q": None, "k": s["k"][:T], "v": s["v"][:T]}
+    _, fault = _call(cut, psd.rope_frequencies(32))
+    assert fault == 0
+    for j in range((5 + T + 9 + 15) // 16):                          # blocks of a page each
+        page, first = int(h["page_indices"][j]), 16 * j - 5           # the token of the block's first slot
+        rows = [t for t in range(max(first, 0), min(first + 16, T))]
+        got, e = _values(s["v_pool"][page].cpu().numpy()), s["ve"][page, 0].cpu().numpy()
+        if not rows:
+            assert torch.equal(s["v_pool"][page].cpu(), was[page]) and torch.equal(s["ve"][page].cpu(), had[page])
+            continue
+        x = s["v"][rows].double().cpu().numpy()
+        for head in range(2):
+            least = BM.scale_exponent(np.abs(x[:, head]).max())
+            assert e[head] == (max(least, int(had[page, 0, head])) if first < 0 else least)
+            slots = [t - first for t in rows]
+            y = x[:, head] * 2.0 ** (127 - int(e[head]))
+            assert np.all(np.abs(got[slots, head] - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10))
+        behind = [i for i in range(16) if first + i >= T]
+        assert torch.equal(s["v_pool"][page].cpu()[behind], was[page][behind])
+
+
+def test_pools_past_32_bits():
+    """Pools of over 2^32 bytes: tokens at both ends."""
+    page, Hkv, D = 64, 16, 128
+    pages = 2 ** 32 // (page * Hkv * D) + 40
+    k = torch.zeros((pages, page, Hkv, D), dtype=torch.uint8, device="cuda")
+    v = torch.zeros_like(k)
+    ke = torch.full((pages, page // 16, Hkv), 130, dtype=torch.uint8, device="cuda")
+    ve = ke.clone()
+    x = torch.full((2, Hkv, D), 3.5, dtype=torch.bfloat16, device="cuda")          # 448 * 2^-7: the scale's byte is 120
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    f = psd.append_tokens(ctx(), None, x, x, None, q_indptr=i32([0, 1, 2]), kv_len=i32([17, 64]), page_indptr=i32([0, 1, 2]),
+                          page_indices=i32([0, pages - 1]), k_pool=k, v_pool=v, rope=psd.rope_frequencies(32), neox=True,
+                          positions=i32([0, 0]), scales=psd.BlockScales(ke, ve, 16))
+    assert int(f) == 0
+    for pool, e in ((k, ke), (v, ve)):
+        for g, slot, block, scale in ((0, 16, 1, 120), (pages - 1, 63, 3, 130)):   # the second's block has older tokens
+            code = 0x7E if scale == 120 else 5 << 3 | 6                              # 3.5 * 2^-3 = 1.75 * 2^-2
+            assert bool((pool[g, slot] == code).all()) and bool((e[g, block] == scale).all())
+            pool[g, slot], e[g, block] = 0, 130
+        assert not pool[0].any() and not pool[-1].any() and not pool[pages // 2:].any() and bool((e == 130).all())
+
+
 def test_captured_and_replayed():
     s = _make(**RAGGED, seed=13)
     rope, sc = psd.rope_frequencies(64), psd.BlockScales(s["ke"], s["ve"], 16)
