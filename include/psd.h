@@ -758,7 +758,15 @@ psd_status append_tokens_scaled(psd_ctx *ctx, const psd_append_args *args, const
                                 psd_stream_t stream);
 
 /* multi_token_decode over such a cache: k_j = 2^(e_K - 127) code, v_j = 2^(e_V - 127) code.
- * Everything else is as there, the workspace too. */
+ * Scales of a request's hidden places must not be that of NaN, as values there must be finite;
+ * blocks without any of its tokens may have any.  Everything else is as there, the workspace
+ * too, with three kernels: head dims 64 and 128 with up to 32 query rows a KV head (n_b times
+ * the group; page sizes that are multiples of 16) on mma.sync, more rows on tcgen05 under the
+ * conditions there, other shapes on CUDA cores.  On both kinds of tensor-core kernel P meets V as one f16 term
+ * (2^-11) for bf16 outputs and two (2^-22) for f32 outputs, and a weight is kept to 2^-32 of the row's largest times
+ * the largest V scale seen.  The tcgen05 kernel brings the 64 keys of a tile to their largest K scale, and
+ * to their largest V scale, in f16, which is exact for scales down to 2^-15 of it; codes of
+ * smaller scales are rounded to 2^-25 of the largest scale. */
 psd_status multi_token_decode_scaled(psd_ctx *ctx, const psd_multi_token_args *args, const psd_block_scales *scales,
                                      const psd_multi_token_plan *plan, void *o, float *lse, void *workspace,
                                      size_t workspace_bytes, psd_stream_t stream);
@@ -789,7 +797,7 @@ typedef struct {
   const float *scores;      /* device [rows] */
   const uint8_t *finished;  /* device [rows] or NULL */
   int32_t rows, beams;      /* rows a multiple of beams; beams in [1, 64], beams * k <= 4096 */
-  int32_t vocab, k;         /* k in [1, 64] */
+  int32_t vocab, k;         /* vocab up to 2^30, k in [1, 64] */
   int32_t pad_token;
   float *out_scores;        /* device [rows / beams, k] */
   int32_t *out_rows, *out_tokens; /* device [rows / beams, k] */

@@ -36,7 +36,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChunk = 2048;                 // a split's logits are a multiple of this
 constexpr int kKeep = 1024;                  // candidates before they are thinned out
 constexpr int kFew = 256;                    // candidates at the end that are put in order among themselves
-constexpr int kMaxK = 64, kMaxBeams = 64;
+constexpr int kMaxK = 64, kMaxBeams = 64, kMaxVocab = 1 << 30;  // (so that a place behind the last tile is an int)
 constexpr int kMost = 8192;                  // candidates of a request in the second kernel
 
 struct SelectParams {
@@ -470,7 +470,7 @@ static psd_status launch_select(const psd_beam_args *a, void *workspace, const D
   const int splits = std::min(chunks, most_splits(dev.num_sms, a->rows, a->beams, a->k));
   const int each = (chunks + splits - 1) / splits;
   p.splits = (chunks + each - 1) / each;
-  p.chunk = int(std::min<int64_t>(int64_t(each) * kChunk, 0x7ffff800));
+  p.chunk = each * kChunk;
   uint8_t *at = static_cast<uint8_t *>(workspace);
   const size_t pieces = size_t(a->rows) * p.splits;
   p.sums = reinterpret_cast<double *>(at);
@@ -526,9 +526,9 @@ extern "C" psd_status beam_select(psd_ctx *ctx, const psd_beam_args *a, void *wo
   if (!ctx || !a) return fail(PSD_ERR_INVALID_ARG, "beam_select: NULL");
   if (a->beams < 1 || a->k < 1 || a->vocab < 1 || a->rows < 0 || a->rows % a->beams)
     return fail(PSD_ERR_INVALID_ARG, "beam_select: %d rows, %d beams, vocab %d, k %d", a->rows, a->beams, a->vocab, a->k);
-  if (a->beams > kMaxBeams || a->k > kMaxK || a->beams * a->k > 4096)
-    return fail(PSD_ERR_UNSUPPORTED, "beam_select: at most %d beams, k %d, beams * k 4096 (beams %d, k %d)", kMaxBeams, kMaxK,
-                a->beams, a->k);
+  if (a->beams > kMaxBeams || a->k > kMaxK || a->beams * a->k > 4096 || a->vocab > kMaxVocab)
+    return fail(PSD_ERR_UNSUPPORTED, "beam_select: at most %d beams, k %d, beams * k 4096, vocab %d (beams %d, k %d, vocab %d)",
+                kMaxBeams, kMaxK, kMaxVocab, a->beams, a->k, a->vocab);
   if (a->logits_type < PSD_LOGITS_F32 || a->logits_type > PSD_LOGITS_F16)
     return fail(PSD_ERR_INVALID_ARG, "beam_select: logits_type %d", a->logits_type);
   if (a->logits_stride < a->vocab) return fail(PSD_ERR_INVALID_ARG, "beam_select: logits_stride shorter than a row");

@@ -195,6 +195,44 @@ def test_captured_and_replayed_on_another_stream():
         assert all(torch.equal(a, b) for a, b in zip(out, want)) and int(fault) == 0
 
 
+def test_the_longest_rows():
+    """5 rows of 2^30 logits: offsets beyond 2^32 elements, and a row that many CTAs share."""
+    V, low = 1 << 30, -4.0
+    x = torch.full((5, V), low, dtype=torch.bfloat16, device="cuda")
+    at = [0, 1, 2047, 2048, V // 2, V - 2, V - 1]
+    for i, t in enumerate(at):
+        x[:, t] = 5.0 + i
+    out, fault = _run(x, [0.0, -1.0, -2.0, -3.0, -4.0], 5, 7)
+    assert fault == 0
+    lse = np.log((V - 7) * np.exp(low) + np.exp(5.0 + np.arange(7)).sum())
+    best = sorted(((5.0 + i - r - lse, -r, -t) for r in range(5) for i, t in enumerate(at)), reverse=True)
+    got = out[0][0].double().cpu().numpy()
+    for n in range(7):                                                # values of several rows are equal but for the sums' rounding
+        r, t = int(out[1][0, n]), int(out[2][0, n])
+        assert abs(got[n] - best[n][0]) <= 2.0 ** -24 * abs(best[n][0]) + 2.0 ** -21
+        assert abs(5.0 + at.index(t) - r - lse - best[n][0]) < 1e-5
+    assert len({*zip(out[1][0].tolist(), out[2][0].tolist())}) == 7
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with its workspace, are as they are alone."""
+    xs, s = [_logits(16, 50001, kind, seed=40) for kind in ("f32", "bf16")], _scores(16)
+    alone = [_run(x, s, 8, 16)[0] for x in xs]
+    dev = torch.as_tensor(s.astype(np.float32)).cuda()
+    outs = [[torch.zeros_like(t) for t in a] for a in alone]
+    spaces = [psd.beam_workspace(ctx(), 16, 8, 16, "cuda") for _ in xs]
+    faults = [torch.zeros(1, dtype=torch.int32, device="cuda") for _ in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                psd.beam_select(ctx(), xs[i], dev, *outs[i], spaces[i], beams=8, fault=faults[i])
+    torch.cuda.synchronize()
+    for out, a, fault in zip(outs, alone, faults):
+        assert int(fault) == 0 and all(torch.equal(p, q) for p, q in zip(out, a))
+
+
 def test_no_rows():
     out = [torch.zeros((0, 4), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
     psd.beam_select(ctx(), torch.zeros((0, 10), device="cuda"), torch.zeros(0, device="cuda"), *out,

@@ -159,7 +159,7 @@ def test_scale_bytes_of_zero(n):
 
 @pytest.mark.parametrize("n", [1, 30])
 def test_a_scale_of_nan_is_seen(n):
-    """Rows that see a block whose scale is NaN are NaN; where the causal mask hides it, nothing is."""
+    """Rows that see a block whose scale is NaN are NaN."""
     s = Scaled([n], [130], Hq=4, Hkv=1, D=64, seed=17)
     s.ve[int(s.page_indices[2])] = 255
     o, _ = s.run(out_f32=True)
@@ -239,6 +239,72 @@ def test_bad_page_ids_are_reported(n, D):
     assert e.value.fault_bits == 1
     good = s.run()
     assert torch.equal(o[n: n + 1], good[0][n: n + 1]) and torch.equal(lse[n: n + 1], good[1][n: n + 1])
+
+
+@pytest.mark.parametrize("D,out_f32", [(64, True), (128, False)])
+def test_bounded_wait_runs_out_and_is_reported(D, out_f32):
+    """Loads of the tcgen05 kernel are withheld from a unit's second key tile on: the waits for them run out (about 1 ms), the
+    call completes and reports it, and the next call is right."""
+    s = Scaled([40, 70, 9], [1500, 300, 900], D=D, seed=25)
+    ctx().test_withhold_loads(1, 2_000_000)
+    try:
+        with pytest.raises(psd.PsdError) as e:
+            s.run(out_f32=out_f32)
+    finally:
+        ctx().test_withhold_loads(-1)
+    assert e.value.status == 4 and e.value.fault_bits == 2
+    _check(s, out_f32=out_f32)
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+@pytest.mark.parametrize("Hkv", [1, 2, 3])
+@pytest.mark.parametrize("off", [1, 2])
+def test_scales_at_any_address(off, Hkv, n):
+    """Scale arrays are bytes: they need no alignment."""
+    s = Scaled([n, 2], [333, 70], Hq=4 * Hkv, Hkv=Hkv, D=64, page=48, seed=26)
+    views = []
+    for e in (s.ke, s.ve):
+        wide = torch.full((e.numel() + 8,), 255, dtype=torch.uint8, device="cuda")
+        views.append(wide[off: off + e.numel()].view(e.shape))
+        views[-1].copy_(e)
+    s.scales = lambda: psd.BlockScales(*views, 16)
+    _check(s, out_f32=True)
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_two_streams_at_once(n):
+    """Calls that overlap on two streams, each with its workspace, are as they are alone."""
+    cases = [Scaled([n, 1, n], [4000, 300, 900 + i], Hq=8, Hkv=2, D=128, seed=27 + i) for i in range(2)]
+    alone = [s.run(out_f32=True) for s in cases]
+    plans, streams = [s.plan() for s in cases], [torch.cuda.Stream() for _ in cases]
+    args = [s.args() for s in cases]
+    spaces = [psd.multi_token_workspace(ctx(), p, 128, "cuda") for p in plans]
+    outs = [[torch.full_like(t, 5.0) for t in a] for a in alone]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                psd.multi_token_decode(ctx(), args[i], plans[i], *outs[i], spaces[i])
+    torch.cuda.synchronize()
+    for i, stream in enumerate(streams):
+        assert psd.check_device_error(ctx(), spaces[i]) == 0
+        assert all(torch.equal(a, b) for a, b in zip(outs[i], alone[i]))
+
+
+def test_one_workspace_for_call_after_call():
+    """Calls of all three kernels behind each other on one stream use one workspace."""
+    cases = [Scaled([n, 2], [900, 30], Hq=8, Hkv=2, D=D, seed=30 + n) for n, D in ((1, 128), (40, 128), (3, 80), (2, 64))]
+    alone = [s.run() for s in cases]
+    plans, args = [s.plan() for s in cases], [s.args() for s in cases]
+    size = max(psd.multi_token_workspace(ctx(), p, s.D, "cuda").numel() for s, p in zip(cases, plans))
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    outs = [[torch.full_like(t, 5.0) for t in a] for a in alone]
+    for _ in range(5):
+        for i in range(len(cases)):
+            psd.multi_token_decode(ctx(), args[i], plans[i], *outs[i], ws)
+    assert psd.check_device_error(ctx(), ws) == 0
+    for out, a in zip(outs, alone):
+        assert all(torch.equal(x, y) for x, y in zip(out, a))
 
 
 def test_pools_past_32_bits():
