@@ -8,16 +8,16 @@
 // terms are added pairwise, the 16-sums with the error of each addition kept beside it, and threads, splits and
 // rows meet in 64 bits.  What is left is the rounding of the single terms, some 1e-8 of the sum, and does not
 // depend on where a row lies in memory: equal rows tie.
-//   Candidates: each warp keeps the r-th largest of its lanes' largest logits, r = ceil(k / 8); the least of the
-// 8 warps' is a lower bound of the k-th largest so far (8 r >= k logits are no smaller), found without a sort, and
-// rises tile by tile.  What is not below it is kept: some k ln(tiles) + k of a CTA's logits.  Order numbers
-// among those that are not below the last bound (a count of the larger ones) give the exact k.  Warps wait for each
-// other only after the first tile, which makes the bound: with two barriers a tile 240 rows of 131072 took 38 us.
-// Where more is kept than there is room for (logits that rise, many equal ones) the CTA begins again and thins them
-// out tile by tile.
+//   Candidates: each warp takes the r-th largest of its lanes' largest logits, r = ceil(k / 8); the least of the
+// 8 warps' is a lower bound of the k-th largest (8 r >= k logits are no smaller), found without a sort.  The pass keeps
+// each thread's largest of every tile; some 2 k of these are not below the bound, and only their 16 logits are read again.
+// Order numbers (a count of the larger ones) give the exact k.  So the pass is left with 6 instructions a logit; with a
+// bound and a search tile by tile it was 13.  Where more is found than there is room for (many equal logits) the CTA goes
+// over its logits again and thins them out on the way.
 //
-// A row is split over CTAs so that all SMs have work; a second kernel, one CTA a request, joins the
-// splits' sums and takes the k largest of the rows' candidates in 64 bits.
+// Rows are split so that all SMs have equal work: the rows that are read (not finished, not empty) share the CTAs that run
+// at once, to within a split.  A second kernel, one CTA a request, joins the splits' sums and takes the k largest of the
+// rows' candidates in 64 bits.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -34,8 +34,9 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kChunk = 2048;                 // a split's logits are a multiple of this
-constexpr int kKeep = 1024;                  // candidates before they are thinned out
-constexpr int kFew = 256;                    // candidates at the end that are put in order among themselves
+constexpr int kSlots = 16;                   // a thread's maxima that are kept: of a tile each, or of several
+constexpr int kKeep = 1024;                  // candidates there is room for, and threads' tiles that hold some
+constexpr int kFew = 256;                    // candidates that are put in order among themselves
 constexpr int kMaxK = 64, kMaxBeams = 64, kMaxVocab = 1 << 30;  // (so that a place behind the last tile is an int)
 constexpr int kMost = 8192;                  // candidates of a request in the second kernel
 
@@ -44,13 +45,56 @@ struct SelectParams {
   int64_t stride;
   const float *scores;
   const uint8_t *finished;
-  int rows, beams, vocab, k, pad, splits, chunk;
+  int rows, beams, vocab, k, pad;
+  int pieces, most_splits;   // CTAs of the first kernel; of a row at most (1: piece and row are the same number)
   float *out_scores;
   int32_t *out_rows, *out_tokens, *fault;
-  double *sums;              // [rows][splits] in units of 2^ref
-  float *refs;               // [rows][splits]
-  unsigned long long *keys;  // [rows][splits][k] descending, 0: none
+  double *sums;              // [pieces] in units of 2^ref
+  int2 *refs;                // [pieces] R's bits, and the row's number in its request
+  unsigned long long *keys;  // [pieces][k] descending, 0: none
 };
+
+// Rows whose logits are read share the pieces: of L such rows the j-th has those from first(j) to first(j + 1).  (A NaN
+// score is reported by the second kernel.)
+constexpr int kMostRanked = 1024;
+static_assert(kMostRanked / 32 == 32, "a lane a word");
+struct Shares {
+  int rows, pieces;  // L, and the pieces in use
+  __device__ __forceinline__ int first(int j) const { return (j * pieces + rows - 1) / rows; }
+  __device__ __forceinline__ int row_of(int piece) const { return piece * rows / pieces; }
+};
+// All rows' bits, 32 a word; all kThreads threads.
+__device__ __forceinline__ void mark_rows(const SelectParams &p, uint32_t *words) {
+  constexpr int kEach = kMostRanked / kThreads;
+  float score[kEach];
+  uint8_t done[kEach];
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const int i = n * kThreads + int(threadIdx.x);
+    score[n] = i < p.rows ? p.scores[i] : neg_inf();
+    done[n] = i < p.rows && p.finished ? p.finished[i] : uint8_t(0);
+  }
+#pragma unroll
+  for (int n = 0; n < kEach; ++n) {
+    const uint32_t is = __ballot_sync(0xffffffffu, score[n] != neg_inf() && !done[n]);
+    if ((threadIdx.x & 31) == 0) words[(n * kThreads + int(threadIdx.x)) / 32] = is;
+  }
+}
+// The lane's word's rows, and those before; all lanes.
+__device__ __forceinline__ Shares share_rows(const SelectParams &p, const uint32_t *words, int &here, int &before) {
+  here = __popc(words[threadIdx.x & 31]);
+  before = here;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, d);
+    if ((threadIdx.x & 31) >= d) before += y;
+  }
+  Shares s;
+  s.rows = __shfl_sync(0xffffffffu, before, 31);
+  s.pieces = min(p.pieces, s.rows * p.most_splits);
+  before -= here;
+  return s;
+}
 
 // Unsigned numbers that are ordered as floats and doubles are (no NaN; -0 is made 0 before).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -103,30 +147,47 @@ template <typename T> __device__ __forceinline__ void unpack(uint32_t w, float *
 
 // What a CTA takes at a time: 16 logits a thread, the next on their way while a tile is worked on.
 constexpr int kPer = 16, kTile = kThreads * kPer;
+constexpr int kStep = kThreads * 4;          // the same where candidates are thinned out on the way
 
-// blockIdx.x: split, blockIdx.y (and z): row.  VEC: rows are 16-byte aligned; otherwise a warp's loads are
+// A CTA a piece.  VEC: rows are 16-byte aligned; otherwise a warp's loads are
 // neighbours one by one.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectParams p) {
   constexpr int N = 16 / int(sizeof(T));  // logits of a 16-byte load
-  __shared__ unsigned long long kept[kKeep + kTile], few[kFew], chosen[kMaxK];
-  __shared__ volatile float bound[kWarps];
-  __shared__ int n_kept, n_few;
+  __shared__ float tops[kSlots][kThreads];
+  __shared__ unsigned long long kept[kKeep + kStep], few[kFew], chosen[kMaxK];
+  __shared__ uint16_t found[kKeep];         // slot and thread
+  __shared__ float bound[kWarps];
+  __shared__ int n_found, n_kept, n_few;
   __shared__ double warp_sum[kWarps];
   __shared__ float warp_ref[kWarps];
   dependents_may_launch();
-  const int row = int(blockIdx.y + gridDim.y * blockIdx.z), split = blockIdx.x;
-  if (row >= p.rows) return;
-  const float score = p.scores[row];
-  // no continuations, or one: the second kernel sees to it (a NaN goes on, to be reported there)
-  if (score == neg_inf() || (p.finished && p.finished[row])) return;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int begin = split * p.chunk, size = min(p.vocab - begin, p.chunk);  // (below 2^31: the splits cover the row just)
+  const int piece = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int row = piece, begin = 0, size = p.vocab;
+  if (p.most_splits > 1) {
+    __shared__ uint32_t words[kMostRanked / 32];
+    mark_rows(p, words);
+    __syncthreads();
+    int here, before;
+    const Shares shares = share_rows(p, words, here, before);
+    if (piece >= shares.pieces) return;
+    const int j = shares.row_of(piece), first = shares.first(j), splits = shares.first(j + 1) - first;
+    const int word = __ffs(__ballot_sync(0xffffffffu, j >= before && j < before + here)) - 1;
+    const uint32_t is = words[word];
+    const int rank = j - __shfl_sync(0xffffffffu, before, word);
+    row = 32 * word + __ffs(__ballot_sync(0xffffffffu, (is >> lane & 1) && __popc(is & ((1u << lane) - 1u)) == rank)) - 1;
+    const int chunks = (p.vocab + kChunk - 1) / kChunk, at = piece - first;
+    begin = int(int64_t(at) * chunks / splits) * kChunk;
+    size = min(int(int64_t(at + 1) * chunks / splits) * kChunk, p.vocab) - begin;
+  } else if (p.scores[row] == neg_inf() || (p.finished && p.finished[row])) {
+    return;  // no continuations, or one: the second kernel sees to it
+  }
   const T *x_split = static_cast<const T *>(p.logits) + int64_t(row) * p.stride + begin;
   const int r = (p.k + kWarps - 1) / kWarps;
-  if (tid == 0) n_kept = 0;
+  if (tid == 0) n_found = n_kept = 0;
   // Where a thread's c-th logit lies in a tile.
-  auto place = [&](int c) { return VEC ? (c / N) * (kThreads * N) + tid * N + c % N : c * kThreads + tid; };
+  auto place_of = [&](int t, int c) { return VEC ? (c / N) * (kThreads * N) + t * N + c % N : c * kThreads + t; };
+  auto place = [&](int c) { return place_of(tid, c); };
   constexpr int kRaw = VEC ? kPer * int(sizeof(T)) / 4 : kPer;  // words on their way
   uint32_t raw[kRaw];
   const T *x_mine = x_split + place(0);
@@ -188,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
     for (int w = 1; w < kWarps; ++w) low = fminf(low, bound[w]);
     return low;
   };
-  // The k largest of those kept, in order, to the front; all threads.
+  // The k largest of those kept, in order, to the front; all threads, behind a barrier.
   auto thin = [&]() {
     const int n = n_kept;
     const float low = lowest();
@@ -216,87 +277,133 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
     if (tid == 0) n_kept = min(n, p.k);
     __syncthreads();
   };
-  // One pass over the split's logits.  Careful: what is kept is thinned out wherever there could be too much of it.
-  // Otherwise false where there was.
-  auto pass = [&](bool careful) {
-    const int room = careful ? kKeep : kKeep + kTile;
-    bool full = false;  // this thread has found no room, or, careful, put one behind the kKeep-th
-    load(0);
-    for (int tile = 0; tile < size; tile += kTile) {
-      values(tile);
-      if (size - tile > kTile) load(tile + kTile);
-      float top = neg_inf();  // (NaN loses)
+  auto sharpen = [&]() {
+    const uint32_t mine = nth_largest(ordered(best), r);
+    if (lane == 0) bound[warp] = from_ordered(mine);
+  };
+
+  // ---- one pass over the split's logits: the sum, and each thread's largest of every tile, or of `group` tiles
+  const int tiles = (size + kTile - 1) / kTile, group = (tiles + kSlots - 1) / kSlots;
+  int slot = 0, left = group;
+  float slot_top = neg_inf();
+  load(0);
+  for (int tile = 0; tile < size; tile += kTile) {
+    values(tile);
+    if (size - tile > kTile) load(tile + kTile);
+    float top = neg_inf();  // (NaN loses)
 #pragma unroll
-      for (int c = 0; c < kPer; c += 2) top = max3(top, x[c], x[c + 1]);
-      if (top * kL > ref + 16.f) {  // (false while all are -inf)
-        const float to = fminf(ceilf(top * kL), 3e38f);
-        const float down = ref == neg_inf() ? 0.f : ex2(ref - to);
-        sum *= down, rest *= down;
-        ref = to;
+    for (int c = 0; c < kPer; c += 2) top = max3(top, x[c], x[c + 1]);
+    slot_top = fmaxf(slot_top, top);
+    if (--left == 0) {
+      tops[slot++][tid] = slot_top;
+      best = fmaxf(best, slot_top);
+      slot_top = neg_inf();
+      left = group;
+    }
+    if (top * kL > ref + 16.f) {  // (false while all are -inf)
+      const float to = fminf(ceilf(top * kL), 3e38f);
+      const float down = ref == neg_inf() ? 0.f : ex2(ref - to);
+      sum *= down, rest *= down;
+      ref = to;
+    }
+    const float from = ref == neg_inf() ? 0.f : -ref;
+    const float2 from2 = make_float2(from, from), l2 = make_float2(kL, kL), l22 = make_float2(kL2, kL2);
+    float e0;
+    for (;;) {
+      float2 e[kPer / 2];
+#pragma unroll
+      for (int c = 0; c < kPer / 2; ++c) {
+        const float2 y = make_float2(x[2 * c], x[2 * c + 1]);
+        const float2 z = __ffma2_rn(y, l22, __ffma2_rn(y, l2, from2));
+        e[c] = make_float2(ex2(z.x), ex2(z.y));
       }
-      const float from = ref == neg_inf() ? 0.f : -ref;
-      const float2 from2 = make_float2(from, from), l2 = make_float2(kL, kL), l22 = make_float2(kL2, kL2);
-      float e0;
-      for (;;) {
-        float2 e[kPer / 2];
 #pragma unroll
-        for (int c = 0; c < kPer / 2; ++c) {
-          const float2 y = make_float2(x[2 * c], x[2 * c + 1]);
-          const float2 z = __ffma2_rn(y, l22, __ffma2_rn(y, l2, from2));
-          e[c] = make_float2(ex2(z.x), ex2(z.y));
+      for (int d = kPer / 4; d; d >>= 1)
+#pragma unroll
+        for (int c = 0; c < d; ++c) e[c] = __fadd2_rn(e[c], e[c + d]);
+      e0 = e[0].x + e[0].y;
+      if (e0 == e0) break;
+      bool nan = false;  // NaN counts as -inf (a sum that is NaN without one: +inf among the logits)
+#pragma unroll
+      for (int c = 0; c < kPer; ++c) {
+        nan |= x[c] != x[c];
+        x[c] = fmaxf(x[c], neg_inf());
+      }
+      if (!nan) break;
+    }
+    const float s = sum + e0, t = s - sum;
+    rest += (sum - (s - t)) + (e0 - t);
+    sum = s;
+  }
+  if (left != group) {
+    tops[slot++][tid] = slot_top;
+    best = fmaxf(best, slot_top);
+  }
+  sharpen();
+  __syncthreads();
+
+  // ---- the logits that are not below the bound (-inf is no candidate): which threads' tiles have any, then those read anew
+  const float low = fmaxf(lowest(), -3.402823466e38f);
+  if (best >= low)
+    for (int i = 0; i < slot; ++i)
+      if (tops[i][tid] >= low) {
+        const int at = atomicAdd(&n_found, 1);
+        if (at < kKeep) found[at] = uint16_t(i * kThreads + tid);
+      }
+  __syncthreads();
+  bool careful = n_found > kKeep;
+  if (!careful) {
+    constexpr int kLanes = 16, kAtOnce = kThreads / kLanes, kBatch = 4;  // lanes a thread's tile
+    static_assert(kLanes == kPer && kSlots * kThreads <= 65536, "a lane a logit");
+    const int jobs = n_found * group, c = tid % kLanes;
+    for (int job0 = tid / kLanes; job0 < jobs; job0 += kBatch * kAtOnce) {
+      int at[kBatch];
+      float v[kBatch];
+#pragma unroll
+      for (int n = 0; n < kBatch; ++n) {
+        const int job = job0 + n * kAtOnce, f = group == 1 ? job : job / group;
+        at[n] = -1, v[n] = neg_inf();
+        if (job < jobs) {
+          const int which = found[f], tile = (which / kThreads) * group + (job - f * group);
+          at[n] = tile * kTile + place_of(which % kThreads, c);
+          if (at[n] < size) v[n] = logit<T>(x_split[at[n]]);
         }
+      }
 #pragma unroll
-        for (int d = kPer / 4; d; d >>= 1)
-#pragma unroll
-          for (int c = 0; c < d; ++c) e[c] = __fadd2_rn(e[c], e[c + d]);
-        e0 = e[0].x + e[0].y;
-        if (e0 == e0) break;
-        bool nan = false;  // NaN counts as -inf (a sum that is NaN without one: +inf among the logits)
-#pragma unroll
-        for (int c = 0; c < kPer; ++c) {
-          nan |= x[c] != x[c];
-          x[c] = fmaxf(x[c], neg_inf());
+      for (int n = 0; n < kBatch; ++n)
+        if (v[n] >= low) {
+          const int to = atomicAdd(&n_kept, 1);
+          if (to < kKeep) kept[to] = key_of(v[n], uint32_t(begin + at[n]));
         }
-        if (!nan) break;
-      }
-      const float s = sum + e0, t = s - sum;
-      rest += (sum - (s - t)) + (e0 - t);
-      sum = s;
-      const bool first = tile == 0;
-      if (__any_sync(0xffffffffu, first || top > best)) {
-        best = fmaxf(best, top);
-        const uint32_t mine = nth_largest(ordered(best), r);
-        if (lane == 0) bound[warp] = from_ordered(mine);
-      }
-      if (careful) {
-        if (__syncthreads_or(full)) {
-          thin();
-          full = false;
-        }
-      } else if (first) {
-        __syncthreads();
-      }
-      const float low = lowest();  // (what others have put since only makes it sharper)
-      if (top >= low) {
+    }
+    __syncthreads();
+    careful = n_kept > kKeep;
+  }
+  if (careful) {  // logits that rise along the row, many equal ones: tile by tile, the k largest so far
+    __syncthreads();
+    if (tid == 0) n_kept = 0;
+    best = neg_inf();
+    unsigned long long least = 0;  // the k-th largest, once there is one
+    for (int at = 0; at < size; at += kStep) {
+      __syncthreads();
 #pragma unroll
-        for (int c = 0; c < kPer; ++c)
-          if (x[c] >= low && x[c] != neg_inf()) {
-            const int at = atomicAdd(&n_kept, 1);
-            if (at < kKeep + kTile) kept[at] = key_of(x[c], uint32_t(begin + tile + place(c)));
-            full |= at >= room;
-          }
+      for (int c = 0; c < kStep / kThreads; ++c) {
+        const int i = at + c * kThreads + tid;
+        const float y = i < size ? fmaxf(logit<T>(x_split[i]), neg_inf()) : neg_inf();
+        const unsigned long long key = key_of(y, uint32_t(begin + i));
+        best = fmaxf(best, y);
+        if (y != neg_inf() && key > least) kept[atomicAdd(&n_kept, 1)] = key;
+      }
+      sharpen();
+      __syncthreads();
+      if (n_kept > kKeep) {
+        thin();
+        least = kept[p.k - 1];
       }
     }
-    return !__syncthreads_or(full);
-  };
-  for (bool careful = false; !pass(careful) && !careful; careful = true) {
-    if (tid == 0) n_kept = 0;
-    ref = best = neg_inf(), sum = rest = 0.f;
-    __syncthreads();
   }
   thin();
-  const int64_t at = int64_t(row) * p.splits + split;
-  if (tid < p.k) p.keys[at * p.k + tid] = kept[tid];
+  if (tid < p.k) p.keys[int64_t(piece) * p.k + tid] = kept[tid];
   // The threads' sums to the largest reference.
   float most = ref;
 #pragma unroll
@@ -313,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
   __syncthreads();
   if (tid == 0) {
     for (int w = 1; w < kWarps; ++w) all += warp_sum[w];
-    p.sums[at] = all;
-    p.refs[at] = most;
+    p.sums[piece] = all;
+    p.refs[piece] = make_int2(__float_as_int(most), row % p.beams);
   }
 }
 
@@ -323,35 +430,71 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
 __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParams p) {
   extern __shared__ unsigned long long shared[];
   const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per_row = p.splits * p.k, most = p.beams * per_row;
+  const int most = p.beams * (p.most_splits * p.k + 1);
   unsigned long long *value = shared, *key = shared + most;  // candidates: v in order, and the logit and token
   uint8_t *of = reinterpret_cast<uint8_t *>(key + most);     // and the row
   __shared__ double base[kMaxBeams];                         // what a row's logits are added to
   __shared__ float row_ref[kMaxBeams], base_down[kMaxBeams], base_up[kMaxBeams];
   __shared__ uint8_t kind[kMaxBeams];                        // 0: no continuation, 1: pad_token, 2: candidates
   __shared__ float bound[kWarps];
-  __shared__ int n_shared;
-  // A warp takes every eighth candidate, so that all have some of every row: one without any leaves no bound.
-  wait_for_prior_grid();
-  const int64_t from = int64_t(b) * most;
-  const int first = lane * kWarps + warp;
-  const unsigned long long early = first < most ? p.keys[from + first] : 0;  // on its way beside the sums
+  __shared__ int n_shared, first_of[kMaxBeams + 1];          // a row's first piece
+  __shared__ uint32_t words[kMostRanked / 32];
+  const int row0 = b * p.beams;
   float score = 0.f;
   bool done = false;
   if (tid < p.beams) {
-    score = p.scores[b * p.beams + tid];
-    done = p.finished && p.finished[b * p.beams + tid];
+    score = p.scores[row0 + tid];
+    done = p.finished && p.finished[row0 + tid];
   }
   if (tid == 0) n_shared = 0;
+  if (p.most_splits > 1) {
+    mark_rows(p, words);
+    __syncthreads();
+    if (warp < 3) {
+      int here, before;
+      const Shares shares = share_rows(p, words, here, before);
+      const int row = min(row0 + tid, kMostRanked);
+      int rank = __shfl_sync(0xffffffffu, before, row / 32 & 31);  // rows that are read before it
+      rank = row == kMostRanked ? shares.rows : rank + __popc(words[row / 32] & ((1u << (row & 31)) - 1u));
+      if (tid <= p.beams) first_of[tid] = shares.rows ? shares.first(rank) : 0;
+    }
+  } else {
+    if (tid <= p.beams) first_of[tid] = row0 + tid;
+  }
+  __syncthreads();
+  const int piece0 = first_of[0], n_keys = (first_of[p.beams] - piece0) * p.k, n_all = n_keys + p.beams;
+  wait_for_prior_grid();
+  // The i-th candidate's logit and token, 0: none, and its row: the pieces' first, then one for each row that may be finished.
+  const uint32_t by_k = (1u << 20) / uint32_t(p.k) + 1u;      // i / k = i by_k >> 20, i < 2^14 and k <= 64
+  auto fetch = [&](int i, int &w) {
+    w = i - n_keys;
+    if (i >= n_keys) return 0ull;
+    const int piece = int(uint64_t(uint32_t(i)) * by_k >> 20);
+    w = p.most_splits > 1 ? p.refs[piece0 + piece].y : piece;  // (of rows that are not read nothing was written)
+    return p.keys[int64_t(piece0) * p.k + i];
+  };
+  auto candidate = [&](int i, int w, unsigned long long x) {
+    if (i >= n_keys) return kind[w] == 1 ? key_of(0.f, uint32_t(p.pad)) : 0ull;
+    return kind[w] == 2 ? x : 0ull;  // (rows that are not read have left nothing)
+  };
+  // A warp takes every eighth candidate, so that all have some of every row: one without any leaves no bound.  A thread's
+  // first are on their way beside the sums.
+  constexpr int kHeld = 4;
+  const int first = lane * kWarps + warp;
+  unsigned long long held[kHeld];
+  int held_of[kHeld];
+#pragma unroll
+  for (int n = 0; n < kHeld; ++n)
+    if (first + n * kThreads < n_all) held[n] = fetch(first + n * kThreads, held_of[n]);
   for (int w = warp; w < p.beams; w += kWarps) {
-    const int64_t at = int64_t(b * p.beams + w) * p.splits;
+    const int at = first_of[w], splits = first_of[w + 1] - at;
     float refs[2];
     double sums[2];  // at most 64 splits: two a lane
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = lane + 32 * i;
-      refs[i] = s < p.splits ? p.refs[at + s] : neg_inf();
-      sums[i] = s < p.splits ? p.sums[at + s] : 0.0;
+      refs[i] = s < splits ? __int_as_float(p.refs[at + s].x) : neg_inf();
+      sums[i] = s < splits ? p.sums[at + s] : 0.0;
     }
     float ref = fmaxf(refs[0], refs[1]);
 #pragma unroll
@@ -360,7 +503,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
     if (ref != neg_inf()) sum = sums[0] * double(ex2(refs[0] - ref)) + sums[1] * double(ex2(refs[1] - ref));
 #pragma unroll
     for (int d = 16; d; d >>= 1)
-      if (d < p.splits) sum += __shfl_xor_sync(0xffffffffu, sum, d);  // (lanes behind the splits hold 0)
+      if (d < splits) sum += __shfl_xor_sync(0xffffffffu, sum, d);  // (lanes behind the splits hold 0)
     if (lane == 0) base[w] = sum, row_ref[w] = ref;
   }
   __syncthreads();
@@ -385,16 +528,18 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
     kind[tid] = uint8_t(what);
   }
   __syncthreads();
-  // A candidate's logit and token; 0: none.
-  auto candidate = [&](int i, int w) {
-    if (kind[w] == 2) return i == first ? early : p.keys[from + i];
-    return kind[w] == 1 && i == w * per_row ? key_of(0.f, uint32_t(p.pad)) : 0ull;
-  };
   float best = neg_inf();
-  for (int i = first; i < most; i += kThreads) {
-    const int w = i / per_row;
-    const unsigned long long k = candidate(i, w);
-    if (k) best = fmaxf(best, __fadd_rd(from_ordered(uint32_t(k >> 32)), base_down[w]));
+  auto see = [&](int i, int w, unsigned long long x) {
+    x = candidate(i, w, x);
+    if (x) best = fmaxf(best, __fadd_rd(from_ordered(uint32_t(x >> 32)), base_down[w]));
+  };
+#pragma unroll
+  for (int n = 0; n < kHeld; ++n)
+    if (first + n * kThreads < n_all) see(first + n * kThreads, held_of[n], held[n]);
+  for (int i = first + kHeld * kThreads; i < n_all; i += kThreads) {
+    int w;
+    const unsigned long long x = fetch(i, w);
+    see(i, w, x);
   }
   const uint32_t mine = nth_largest(ordered(best), (p.k + kWarps - 1) / kWarps);
   if (lane == 0) bound[warp] = from_ordered(mine);
@@ -402,16 +547,23 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   float low = bound[0];
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) low = fminf(low, bound[w]);
-  for (int i = first; i < most; i += kThreads) {
-    const int w = i / per_row;
-    const unsigned long long k = candidate(i, w);
-    if (k == 0) continue;
+  auto take = [&](int i, int w, unsigned long long k) {
+    k = candidate(i, w, k);
+    if (k == 0) return;
     const float x = from_ordered(uint32_t(k >> 32));
-    if (__fadd_ru(x, base_up[w]) < low) continue;
+    if (__fadd_ru(x, base_up[w]) < low) return;
     const int at = atomicAdd(&n_shared, 1);
     value[at] = ordered(double(x) + base[w]);
     key[at] = k;
     of[at] = uint8_t(w);
+  };
+#pragma unroll
+  for (int n = 0; n < kHeld; ++n)
+    if (first + n * kThreads < n_all) take(first + n * kThreads, held_of[n], held[n]);
+  for (int i = first + kHeld * kThreads; i < n_all; i += kThreads) {
+    int w;
+    const unsigned long long x = fetch(i, w);
+    take(i, w, x);
   }
   __syncthreads();
   const int n = n_shared;
@@ -441,13 +593,15 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   }
 }
 
-// CTAs a row may be split over: those that run at once, four an SM, and what the second kernel's CTA can hold.  (A second
-// wave of few CTAs takes as long as the first.)
-int most_splits(int sms, int rows, int beams, int k) {
-  return int(std::max<int64_t>(1, std::min<int64_t>({4 * int64_t(sms) / rows, kMost / (beams * k), 64})));
+// CTAs of the first kernel: those that run at once, four an SM, or the rows if they are more.  (A second wave of few CTAs
+// takes as long as the first.)
+int pieces_of(int sms, int rows) { return std::max(std::min(4 * sms, kMostRanked), rows); }
+// CTAs a row may be split over: what the second kernel's CTA can hold, and twice what all rows would have.
+int most_splits(int pieces, int rows, int chunks, int beams, int k) {
+  return std::max(1, std::min({2 * ((pieces + rows - 1) / rows), chunks, kMost / (beams * k), 64}));
 }
 
-size_t join_bytes(const SelectParams &p) { return size_t(p.beams) * p.splits * p.k * 17; }
+size_t join_bytes(const SelectParams &p) { return size_t(p.beams) * (p.most_splits * p.k + 1) * 17; }
 
 }  // namespace
 
@@ -467,23 +621,21 @@ static psd_status launch_select(const psd_beam_args *a, void *workspace, const D
   p.out_tokens = a->out_tokens;
   p.fault = a->fault_dev;
   const int chunks = int((int64_t(a->vocab) + kChunk - 1) / kChunk);
-  const int splits = std::min(chunks, most_splits(dev.num_sms, a->rows, a->beams, a->k));
-  const int each = (chunks + splits - 1) / splits;
-  p.splits = (chunks + each - 1) / each;
-  p.chunk = each * kChunk;
+  p.pieces = pieces_of(dev.num_sms, a->rows);
+  p.most_splits = p.pieces == a->rows ? 1 : most_splits(p.pieces, a->rows, chunks, a->beams, a->k);
+  if (p.most_splits == 1) p.pieces = a->rows;
+  p.pieces = int(std::min(int64_t(p.pieces), int64_t(p.most_splits) * a->rows));
   uint8_t *at = static_cast<uint8_t *>(workspace);
-  const size_t pieces = size_t(a->rows) * p.splits;
+  const size_t pieces = size_t(p.pieces);
   p.sums = reinterpret_cast<double *>(at);
   p.keys = reinterpret_cast<unsigned long long *>(at + pieces * 8);
-  p.refs = reinterpret_cast<float *>(at + pieces * 8 * (1 + size_t(a->k)));
+  p.refs = reinterpret_cast<int2 *>(at + pieces * 8 * (1 + size_t(a->k)));
   const size_t size = a->logits_type == PSD_LOGITS_F32 ? 4 : 2;
   const bool vec = aligned16(a->logits) && (a->logits_stride * int64_t(size)) % 16 == 0;
-  const int high = std::min(a->rows, 32768);
-  const dim3 grid(unsigned(p.splits), unsigned(high), unsigned((a->rows + high - 1) / high));
   auto go = [&](auto type) {
     using T = decltype(type);
     auto kern = vec ? select_rows_kernel<T, true> : select_rows_kernel<T, false>;
-    kern<<<grid, kThreads, 0, s>>>(p);
+    kern<<<unsigned(p.pieces), kThreads, 0, s>>>(p);
   };
   if (a->logits_type == PSD_LOGITS_F32) go(float{});
   else if (a->logits_type == PSD_LOGITS_BF16) go(__nv_bfloat16{});
@@ -492,7 +644,7 @@ static psd_status launch_select(const psd_beam_args *a, void *workspace, const D
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "beam_select launch: %s", cudaGetErrorString(e));
   const size_t shared = join_bytes(p);
   if (shared > 40 * 1024) {
-    e = cudaFuncSetAttribute(select_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 17 * kMost);
+    e = cudaFuncSetAttribute(select_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 17 * (kMost + kMaxBeams));
     if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
   }
   cudaLaunchConfig_t cfg = {};
@@ -516,8 +668,7 @@ using namespace psd;
 
 extern "C" size_t psd_beam_workspace_bytes(const psd_ctx *ctx, int32_t rows, int32_t beams, int32_t k) {
   if (!ctx || rows < 0 || beams < 1 || beams > kMaxBeams || k < 1 || k > kMaxK || beams * k > 4096) return 0;
-  // rows * splits is at most 4 an SM, or the rows: more rows never need less
-  return 256 + size_t(std::max(4 * ctx->dev.num_sms, rows)) * (12 + 8 * size_t(k));
+  return 256 + size_t(pieces_of(ctx->dev.num_sms, rows)) * (16 + 8 * size_t(k));
 }
 
 extern "C" psd_status beam_select(psd_ctx *ctx, const psd_beam_args *a, void *workspace, size_t workspace_bytes,

@@ -295,7 +295,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
 // The same by one CTA with the counts in shared memory, for up to kFewChildren children, kFewPages pages and
 // kFewEntries new entries: its barriers and atomics take tens of cycles where the cluster's take hundreds.  It is
 // bound by the latency of what depends on what, one SM's loads and atomics a table entry among it.  A whole call, copies
-// included: 4 children of 40 pages 7 us against 21; 128 of some 150 among 20000 pages 23 us (this kernel 20) against 39.
+// included: 4 children of 40 pages 7 us against 20; 128 of some 150 among 20000 pages 23 us (this kernel 20) against 32.
 constexpr int kFewChildren = 1024, kFewPages = 49152, kFewEntries = (1 << 21) - 2;
 
 __device__ __forceinline__ int block_scan(int v, int &total, int *sums) {  // the sum over the threads before

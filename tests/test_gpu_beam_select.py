@@ -161,6 +161,46 @@ def test_rising_and_falling_logits():
     _check(torch.stack([x, x.flip(0), x * 0.001, x.flip(0) * 0.001]), [-1.0] * 4, 2, 64, twins=True)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("k", [1, 10, 64])
+@pytest.mark.parametrize("pattern", ["half", "steps", "levels", "last"])
+def test_many_logits_at_the_top(pattern, k, kind):
+    """More logits than the candidates' room are no smaller than the bound: they are thinned out on the way."""
+    V, rng = 30011, np.random.default_rng(50)
+    x = rng.standard_normal((2, V))
+    if pattern == "half":                                             # equal ones, scattered
+        x[:, rng.random(V) < 0.5] = 6.0
+    elif pattern == "steps":                                          # rising, each value 1500 times
+        x[:] = np.arange(V) // 1500 * 0.25
+    elif pattern == "levels":                                         # few values in any order
+        x = np.floor(x)
+    else:                                                             # all equal but the last ones
+        x[:], x[:, -5:] = 1.0, 2.0
+    _check(torch.from_numpy(x.astype(np.float32)).to(TYPES[kind]).cuda(), [0.0, -0.5], 2, k)
+
+
+@pytest.mark.parametrize("fill", [0, 127, 255])
+@pytest.mark.parametrize("rows,beams,vocab", [(6, 3, 500), (700, 7, 3000), (12, 4, 9000)])
+def test_rows_that_are_not_read_leave_nothing(rows, beams, vocab, fill):
+    """Whatever the workspace held: rows at their end and empty ones have no part of it."""
+    x, s, done = _logits(rows, vocab, seed=51), _scores(rows), [r % 3 == 1 for r in range(rows)]
+    s[::5] = -np.inf
+    ws = psd.beam_workspace(ctx(), rows, beams, 6, "cuda")
+    ws.fill_(fill)
+    out, fault = _run(x, s, beams, 6, finished=done, workspace=ws)
+    want = BM.select(x.double().cpu().numpy(), np.asarray(s, dtype=np.float32), beams, 6, done, 0)
+    assert fault == 0 and np.array_equal(out[1].cpu().numpy(), want[1]) and np.array_equal(out[2].cpu().numpy(), want[2])
+
+
+@pytest.mark.parametrize("live", [0, 1, 7])
+def test_few_rows_are_read(live):
+    """All but some rows are at their end: those share the CTAs."""
+    rows, x = 64, _logits(64, 40013, seed=52)
+    done = np.ones(rows, dtype=bool)
+    done[np.random.default_rng(53).permutation(rows)[:live]] = False
+    _check(x, _scores(rows), 8, 16, finished=[bool(d) for d in done], pad=3)
+
+
 def test_near_values_across_rows():
     """Two rows whose best values differ by some 1e-6 either way."""
     x = _logits(2, 100003, seed=15, spread=2.0)
