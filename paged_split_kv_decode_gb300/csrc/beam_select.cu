@@ -60,8 +60,8 @@ constexpr int kMostRanked = 1024;
 static_assert(kMostRanked / 32 == 32, "a lane a word");
 struct Shares {
   int rows, pieces;  // L, and the pieces in use
-  __device__ __forceinline__ int first(int j) const { return (j * pieces + rows - 1) / rows; }
-  __device__ __forceinline__ int row_of(int piece) const { return piece * rows / pieces; }
+  __device__ __forceinline__ int first(int j) const { return int(uint32_t(j * pieces + rows - 1) / uint32_t(rows)); }
+  __device__ __forceinline__ int row_of(int piece) const { return int(uint32_t(piece * rows) / uint32_t(pieces)); }
 };
 // All rows' bits, 32 a word; all kThreads threads.
 __device__ __forceinline__ void mark_rows(const SelectParams &p, uint32_t *words) {
@@ -70,12 +70,17 @@ __device__ __forceinline__ void mark_rows(const SelectParams &p, uint32_t *words
   uint8_t done[kEach];
 #pragma unroll
   for (int n = 0; n < kEach; ++n) {
+    if (n * kThreads >= p.rows) break;
     const int i = n * kThreads + int(threadIdx.x);
     score[n] = i < p.rows ? p.scores[i] : neg_inf();
     done[n] = i < p.rows && p.finished ? p.finished[i] : uint8_t(0);
   }
 #pragma unroll
   for (int n = 0; n < kEach; ++n) {
+    if (n * kThreads >= p.rows) {
+      if (threadIdx.x < kWarps) words[n * kWarps + threadIdx.x] = 0;
+      continue;
+    }
     const uint32_t is = __ballot_sync(0xffffffffu, score[n] != neg_inf() && !done[n]);
     if ((threadIdx.x & 31) == 0) words[(n * kThreads + int(threadIdx.x)) / 32] = is;
   }
@@ -177,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
     const int rank = j - __shfl_sync(0xffffffffu, before, word);
     row = 32 * word + __ffs(__ballot_sync(0xffffffffu, (is >> lane & 1) && __popc(is & ((1u << lane) - 1u)) == rank)) - 1;
     const int chunks = (p.vocab + kChunk - 1) / kChunk, at = piece - first;
-    begin = int(int64_t(at) * chunks / splits) * kChunk;
-    size = min(int(int64_t(at + 1) * chunks / splits) * kChunk, p.vocab) - begin;
+    begin = int(uint32_t(at * chunks) / uint32_t(splits)) * kChunk;  // (at < 64, chunks < 2^20)
+    size = min(int(uint32_t((at + 1) * chunks) / uint32_t(splits)) * kChunk, p.vocab) - begin;
   } else if (p.scores[row] == neg_inf() || (p.finished && p.finished[row])) {
     return;  // no continuations, or one: the second kernel sees to it
   }
@@ -308,28 +313,25 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
     }
     const float from = ref == neg_inf() ? 0.f : -ref;
     const float2 from2 = make_float2(from, from), l2 = make_float2(kL, kL), l22 = make_float2(kL2, kL2);
-    float e0;
-    for (;;) {
-      float2 e[kPer / 2];
+    float2 e[kPer / 2];
 #pragma unroll
-      for (int c = 0; c < kPer / 2; ++c) {
-        const float2 y = make_float2(x[2 * c], x[2 * c + 1]);
-        const float2 z = __ffma2_rn(y, l22, __ffma2_rn(y, l2, from2));
-        e[c] = make_float2(ex2(z.x), ex2(z.y));
-      }
+    for (int c = 0; c < kPer / 2; ++c) {
+      const float2 y = make_float2(x[2 * c], x[2 * c + 1]);
+      const float2 z = __ffma2_rn(y, l22, __ffma2_rn(y, l2, from2));
+      e[c] = make_float2(ex2(z.x), ex2(z.y));
+    }
 #pragma unroll
-      for (int d = kPer / 4; d; d >>= 1)
+    for (int d = kPer / 4; d; d >>= 1)
 #pragma unroll
-        for (int c = 0; c < d; ++c) e[c] = __fadd2_rn(e[c], e[c + d]);
-      e0 = e[0].x + e[0].y;
-      if (e0 == e0) break;
-      bool nan = false;  // NaN counts as -inf (a sum that is NaN without one: +inf among the logits)
+      for (int c = 0; c < d; ++c) e[c] = __fadd2_rn(e[c], e[c + d]);
+    float e0 = e[0].x + e[0].y;
+    if (e0 != e0) {  // NaN counts as -inf (a sum that is NaN without one: +inf among the logits)
+      e0 = 0.f;
 #pragma unroll
       for (int c = 0; c < kPer; ++c) {
-        nan |= x[c] != x[c];
-        x[c] = fmaxf(x[c], neg_inf());
+        const float y = fmaxf(x[c], neg_inf());
+        e0 += ex2(fmaf(y, kL2, fmaf(y, kL, from)));
       }
-      if (!nan) break;
     }
     const float s = sum + e0, t = s - sum;
     rest += (sum - (s - t)) + (e0 - t);
