@@ -26,7 +26,8 @@ constexpr int kPoolsALaunch = 128;
 // The workspace: a header, then lists of 32-bit numbers.
 struct Header {
   int32_t moves;                  // entries of the list of moves
-  int32_t pad[15];
+  int32_t accepted;               // 0: the call has been refused
+  int32_t pad[14];
   long long totals[8][kCtas];     // one row for each exchange between the CTAs
   uint32_t faults[8][kCtas];
 };
@@ -273,7 +274,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
   if (faults) {  // the same for all
     if (id == 0) {
       atomicOr(p.fault, int32_t(faults));
-      p.w.head->moves = 0;
+      p.w.head->moves = p.w.head->accepted = 0;
     }
     return;
   }
@@ -289,13 +290,15 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
   if (id == 0) {
     if (p.new_indptr) p.new_indptr[p.N] = pages_wanted;
     p.w.head->moves = p.N;
+    p.w.head->accepted = 1;
   }
 }
 
 // The same by one CTA with the counts in shared memory, for up to kFewChildren children, kFewPages pages and
-// kFewEntries new entries: its barriers and atomics take tens of cycles where the cluster's take hundreds.  It is
-// bound by the latency of what depends on what, one SM's loads and atomics a table entry among it.  A whole call, copies
-// included: 4 children of 40 pages 7 us against 20; 128 of some 150 among 20000 pages 23 us (this kernel 20) against 32.
+// kFewEntries new entries: its barriers and atomics take tens of cycles where the cluster's take hundreds.  Counts and the old
+// table come by asynchronous copies while the children are looked up (with a load at a time the kernel took 20 us where it
+// takes 14, caches cold).  It is bound by the latency of what depends on what, and one SM's atomics a table entry.  A
+// whole call, copies included: 4 children of 40 pages 8 us against 20; 128 of some 150 among 20000 pages 21 us against 32.
 constexpr int kFewChildren = 1024, kFewPages = 49152, kFewEntries = (1 << 21) - 2;
 
 __device__ __forceinline__ int block_scan(int v, int &total, int *sums) {  // the sum over the threads before
@@ -320,32 +323,56 @@ __device__ __forceinline__ int block_scan(int v, int &total, int *sums) {  // th
   return (warp ? before : 0) + up - v;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams p) {
-  extern __shared__ int count[];  // [num_pages], then the rows
-  __shared__ int sums[32];
-  int4 *rows = reinterpret_cast<int4 *>(count + (p.num_pages + 3) / 4 * 4);
+// Shared memory: the counts, padded to kRun, the rows, and the old table's entries where they fit.
+constexpr int kRun = 128;  // pages of a warp's turn, four a lane
+constexpr size_t kFewShared = 227 * 1024 - 1024;
+size_t few_shared(int64_t num_pages, int num_new, int64_t num_indices) {
+  const size_t least = size_t((num_pages + kRun - 1) / kRun * kRun) * 4 + size_t(num_new) * 16;
+  return std::min(kFewShared, least + size_t(num_indices) * 4 + 16);
+}
+static_assert(kFewPages % kRun == 0 && kFewPages * 4 + kFewChildren * 16 <= kFewShared, "counts and rows fit");
+
+__device__ __forceinline__ uint32_t shared_address(const void *at) { return uint32_t(__cvta_generic_to_shared(at)); }
+// n numbers to shared memory, without waiting: 16 bytes at a time where both lie so, all threads.
+__device__ __forceinline__ void bring(int *dst, const int32_t *src, int n) {
+  int i = threadIdx.x;
+  if ((reinterpret_cast<uintptr_t>(src) & 15) == 0 && (shared_address(dst) & 15) == 0) {
+    for (; i < n / 4; i += kThreads)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_address(dst + 4 * i)), "l"(src + 4 * i) : "memory");
+    i = n / 4 * 4 + threadIdx.x;
+  }
+  for (; i < n; i += kThreads)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_address(dst + i)), "l"(src + i) : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams p, int shared_entries) {
+  extern __shared__ __align__(16) int count[];  // [num_pages], then the rows, then the entries
+  __shared__ int sums[32], n_moves;
+  const int padded = int((p.num_pages + kRun - 1) / kRun * kRun);
+  int4 *rows = reinterpret_cast<int4 *>(count + padded);
   dependents_may_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_pages = int(p.num_pages);
   uint32_t faults = 0;
   int total;
-  // The children, with their part-full pages; the counts.
+  // The counts and the old table's entries are on their way while the children are looked up.
+  bring(count, p.ref, n_pages);
+  if (tid == 0) n_moves = 0;
+  for (int g = n_pages + tid; g < padded; g += kThreads) count[g] = 1;
+  int old_end = p.B > 0 ? p.indptr[p.B] : 0, old_begin = p.B > 0 ? p.indptr[0] : 0;
+  if (old_begin < 0 || old_end < old_begin || old_end > p.num_indices) {
+    faults |= PSD_FAULT_RANGE;
+    old_begin = old_end = 0;
+  }
+  // (from the last 16-byte border before them, so that the wide copies fit)
+  int before = int(reinterpret_cast<uintptr_t>(p.indices + old_begin) / 4 & 3);
+  if (before > old_begin) before = 0;
+  const bool staged = old_end - old_begin <= shared_entries - before;
+  int *entries = reinterpret_cast<int *>(rows + p.N);
+  if (staged) bring(entries, p.indices + (old_begin - before), old_end - old_begin + before);
+  const int *entry0 = entries + before - old_begin;
+  auto entry = [&](int e) { return staged && e >= old_begin && e < old_end ? entry0[e] : p.indices[e]; };
   Child c{0, 0, 0, 0, false};
-  int tail = 0;
-  if (tid < p.N) {
-    c = child_of(p, tid, faults);
-    if (c.tail) {
-      tail = p.indices[c.first + c.full];
-      if (tail < 0 || tail >= n_pages) faults |= PSD_FAULT_PAGE_ID, c.tail = false;
-    }
-  }
-  const int64_t old_end = p.B > 0 ? p.indptr[p.B] : 0, old_begin = p.B > 0 ? p.indptr[0] : 0;
-  if (old_begin < 0 || old_end < old_begin || old_end > p.num_indices) faults |= PSD_FAULT_RANGE;
-#pragma unroll 8
-  for (int g = tid; g < n_pages; g += kThreads) {
-    const int r = p.ref[g];
-    if (r < 0) faults |= PSD_FAULT_RANGE;
-    count[g] = r;
-  }
+  if (tid < p.N) c = child_of(p, tid, faults);
   // (of wants that do not fit into the new table the sum only has to stay too large)
   const int start = block_scan(int(min(int64_t(c.want), p.capacity + 1)), total, sums);
   if (total > p.capacity) faults |= PSD_FAULT_RANGE;
@@ -361,24 +388,29 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
   auto give_up = [&]() {
     if (tid == 0) {
       atomicOr(p.fault, int32_t(faults));
-      p.w.head->moves = 0;
+      p.w.head->moves = p.w.head->accepted = 0;
     }
   };
-  if (__syncthreads_or(faults != 0)) {
-    together();
-    give_up();
-    return;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  int tail = 0;
+  if (c.tail) {
+    tail = entry(c.first + c.full);
+    if (tail < 0 || tail >= n_pages) faults |= PSD_FAULT_PAGE_ID, c.tail = false;
   }
   // The old requests let go of their pages.
-#pragma unroll 8
-  for (int64_t e = old_begin + tid; e < old_end; e += kThreads) {
-    const int g = p.indices[e];
+#pragma unroll 4
+  for (uint32_t e = old_begin + tid; e < uint32_t(old_end); e += kThreads) {
+    const int g = staged ? entry0[e] : p.indices[e];
     if (g < 0 || g >= n_pages) faults |= PSD_FAULT_PAGE_ID;
     else if (p.release) atomicSub(count + g, 1);
   }
   __syncthreads();
-  for (int g = tid; g < n_pages; g += kThreads)
-    if (count[g] < 0) faults |= PSD_FAULT_RANGE;  // referred to more often than counted
+  int4 *const count4 = reinterpret_cast<int4 *>(count);
+  for (int k = tid; k < padded / 4; k += kThreads) {
+    const int4 r = count4[k];
+    if ((r.x | r.y | r.z | r.w) < 0) faults |= PSD_FAULT_RANGE;  // below 0, or referred to more often than counted
+  }
   if (__syncthreads_or(faults != 0)) {
     together();
     give_up();
@@ -390,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
   if (claims) atomicMin(count + tail, tid - kFewChildren);
   __syncthreads();
   const bool mine = claims && count[tail] == tid - kFewChildren;
-  const bool kept_tail = c.tail && (!p.room || mine);
+  const bool kept_tail = c.tail && (!p.room || mine), copies = c.tail && !kept_tail;
+  const int move = copies ? atomicAdd(&n_moves, 1) : 0;  // (the order of the moves shows nowhere)
   __syncthreads();
   if (mine) count[tail] = 0;
   const int kept = c.full + kept_tail;
@@ -402,21 +435,22 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
   const int parts = max(1, kThreads / 32 / max(p.N, 1));  // warps a child
   for (int u = warp; u < p.N * parts; u += kThreads / 32) {
     const int4 r = rows[u / parts];
-#pragma unroll 8
+#pragma unroll 4
     for (int j = (u % parts) * 32 + lane; j < r.y; j += 32 * parts) {
-      const int g = p.indices[r.x + j];
+      const int g = entry(r.x + j);
       if (g < 0 || g >= n_pages) faults |= PSD_FAULT_PAGE_ID;  // (behind the old table's end)
       else atomicAdd(count + g, 1);
     }
   }
   __syncthreads();
-  // The free pages, lowest first: a warp has a stretch of them, 32 at a time.
-  const int groups = (n_pages + 31) / 32, each = (groups + 31) / 32;
+  // The free pages, lowest first: a warp has a stretch of them, kRun at a time.
+  const int runs = padded / kRun, each = (runs + 31) / 32, run0 = warp * each, run1 = min(runs, run0 + each);
   int free_pages = 0;
-  for (int k = warp * each; k < min(groups, (warp + 1) * each); ++k) {
-    const int g = 32 * k + lane;
-    free_pages += __popc(__ballot_sync(0xffffffffu, g < n_pages && count[g] == 0));
+  for (int k = run0; k < run1; ++k) {
+    const int4 r = count4[32 * k + lane];
+    free_pages += (r.x == 0) + (r.y == 0) + (r.z == 0) + (r.w == 0);
   }
+  free_pages = __reduce_add_sync(0xffffffffu, free_pages);
   int at = block_scan(lane == 0 ? free_pages : 0, total, sums);
   at = __shfl_sync(0xffffffffu, at, 0);
   if (total < all_blanks) faults |= PSD_FAULT_NO_PAGES;
@@ -425,25 +459,45 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
     give_up();
     return;
   }
-  for (int k = warp * each; k < min(groups, (warp + 1) * each); ++k) {
-    const int g = 32 * k + lane;
-    const bool free = g < n_pages && count[g] == 0;
-    const uint32_t who = __ballot_sync(0xffffffffu, free);
-    const int rank = at + __popc(who & ((1u << lane) - 1u));
-    if (free && rank < all_blanks) p.w.fresh[rank] = g;
-    if (g < n_pages) p.new_ref[g] = free && rank < all_blanks ? 1 : count[g];
-    at += __popc(who);
+  const bool wide = (reinterpret_cast<uintptr_t>(p.new_ref) & 15) == 0;
+  for (int k = run0; k < run1; ++k) {
+    const int4 r = count4[32 * k + lane];
+    const int g = kRun * k + 4 * lane;
+    int of[4] = {r.x, r.y, r.z, r.w};
+    uint32_t who[4];
+    int rank = at, all = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      who[i] = __ballot_sync(0xffffffffu, of[i] == 0);
+      rank += __popc(who[i] & ((1u << lane) - 1u));
+      all += __popc(who[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (of[i] == 0) {
+        if (rank < all_blanks) p.w.fresh[rank] = g + i, of[i] = 1;
+        ++rank;
+      }
+    at += all;
+    if (wide && g + 4 <= n_pages) {
+      *reinterpret_cast<int4 *>(p.new_ref + g) = make_int4(of[0], of[1], of[2], of[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (g + i < n_pages) p.new_ref[g + i] = of[i];
+    }
   }
   __syncthreads();
   if (tid < p.N) {
     p.new_indptr[tid] = start;
     p.new_len[tid] = c.want ? c.len + p.room : 0;
-    p.w.moves[tid] = c.tail && !kept_tail ? make_int2(tail, p.w.fresh[blank]) : make_int2(-1, -1);
+    if (copies) p.w.moves[move] = make_int2(tail, p.w.fresh[blank]);
     if (tid == p.N - 1) p.new_indptr[p.N] = start + c.want;
   }
   if (tid == 0) {
     if (p.N == 0 && p.new_indptr) p.new_indptr[0] = 0;
-    p.w.head->moves = p.N;
+    p.w.head->moves = n_moves;
+    p.w.head->accepted = 1;
   }
 }
 
@@ -477,7 +531,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) com
   if (faults) {
     if (id == 0) {
       atomicOr(p.fault, int32_t(faults));
-      p.w.head->moves = 0;
+      p.w.head->moves = p.w.head->accepted = 0;
     }
     return;
   }
@@ -512,6 +566,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) com
   }
   if (id == 0) {
     *p.num_live = int(n_live);
+    p.w.head->accepted = 1;
     p.w.head->moves = int(total & 0xffffffff);
   }
 }
@@ -521,12 +576,12 @@ struct CopyPools {
   psd_page_pool pool[kPoolsALaunch];
 };
 struct CopyParams {
-  const int32_t *count;       // entries, on the device, or
+  const Header *head;         // how many entries there are, or
   const int32_t *src, *dst;   // lists of a caller's, n long
   const int2 *moves;
   int32_t *fault;
   int64_t num_pages;
-  int n, pools;
+  int n, pools, parts;        // parts of a page of a pool
   // a new table to be written first, if there are children
   int children;
   const int4 *rows;
@@ -534,53 +589,67 @@ struct CopyParams {
   int32_t *new_indices;
 };
 
-// A CTA writes the rows of some children, then takes one page of one pool at a time: 16 bytes a thread and access, four of
-// them on their way.  (The rows here and not in the kernel before: 152 SMs write them beside the copies.)
+// A CTA takes a part of a page of one pool at a time, of 16 KB so that few large pages keep all SMs busy: 16 bytes a thread and
+// access, four of them on their way.  Its next part's place is added up, not divided out (a third of the instructions).  The
+// last CTAs, which may have a part less, write the new table's rows first.  (Here and not in the kernel before: 152 SMs write
+// them beside the copies.)  Bound by DRAM: 14700 pages of 16 KB in 75 us, 0.97 of the copy rate; 22 moves in 32 pools, 23 MB
+// read, in 11 us, where the chain from the list to the last store shows.
+constexpr int kPart = 16384;
 __global__ void __launch_bounds__(256) copy_pages_kernel(const CopyParams p, const __grid_constant__ CopyPools pools) {
+  const int per = p.pools * p.parts, first = per ? int(blockIdx.x) / per : 0;
   wait_for_prior_grid();
-  const int n = p.count ? __ldcg(p.count) : p.n;
-  if (n > 0)  // (0: the call has been refused)
-    for (int i = blockIdx.x; i < p.children; i += gridDim.x) {
+  // (the first move on its way beside the number of them: the list has an entry for every CTA)
+  const int2 first_move = p.moves ? __ldcg(p.moves + first) : make_int2(0, 0);
+  const int n = p.head ? __ldcg(&p.head->moves) : p.n;
+  if (p.children > 0 && __ldcg(&p.head->accepted))
+    for (int i = gridDim.x - 1 - blockIdx.x; i < p.children; i += gridDim.x) {
       const int4 r = __ldcg(p.rows + i);
       const int want = __ldcg(p.new_indptr + i + 1) - r.z;
 #pragma unroll 4
       for (int j = threadIdx.x; j < want; j += 256)
         p.new_indices[r.z + j] = j < r.y ? p.indices[r.x + j] : __ldcg(p.fresh + r.w + j - r.y);
     }
-  for (int64_t u = blockIdx.x; u < int64_t(n) * p.pools; u += gridDim.x) {
-    const int i = int(u / p.pools);
-    const psd_page_pool pool = pools.pool[u - int64_t(i) * p.pools];
-    int64_t from, to;
-    if (p.moves) {
-      const int2 m = __ldcg(p.moves + i);
-      from = m.x, to = m.y;
-      if (from < 0) continue;
-    } else {
-      from = p.src[i], to = p.dst[i];
-      if (from < 0 || from >= p.num_pages || to < 0 || to >= p.num_pages) {
-        if (threadIdx.x == 0) atomicOr(p.fault, PSD_FAULT_PAGE_ID);
-        continue;
+  if (per == 0) return;
+  const int step = int(gridDim.x) / per, step_rest = int(gridDim.x) - step * per;
+  for (int i = first, rest = int(blockIdx.x) - first * per, turn = 0; i < n; ++turn) {
+    const int which = p.parts == 1 ? rest : rest / p.parts, part = rest - which * p.parts;
+    const psd_page_pool pool = pools.pool[which];
+    int2 m = first_move;
+    bool good = true;
+    if (!p.moves) {
+      m = make_int2(p.src[i], p.dst[i]);
+      good = m.x >= 0 && m.x < p.num_pages && m.y >= 0 && m.y < p.num_pages;
+      if (!good && threadIdx.x == 0) atomicOr(p.fault, PSD_FAULT_PAGE_ID);
+    } else if (turn > 0) {
+      m = __ldcg(p.moves + i);
+    }
+    if (good && m.x >= 0 && m.x != m.y) {
+      const bool wide = ((reinterpret_cast<uintptr_t>(pool.base) | uint64_t(pool.page_bytes)) & 15) == 0;
+      const int64_t size = wide ? pool.page_bytes / 16 : pool.page_bytes;  // words, or bytes
+      const int64_t each = p.parts == 1 ? size : max(int64_t(wide ? kPart / 16 : kPart), (size + p.parts - 1) / p.parts);
+      const int64_t begin = part * each;
+      const int left = int(min(size - begin, each));                       // (none, where the pool's pages are smaller)
+      const uint8_t *base = static_cast<const uint8_t *>(pool.base);
+      if (wide) {
+        const uint4 *x = reinterpret_cast<const uint4 *>(base + int64_t(m.x) * pool.page_bytes) + begin + threadIdx.x;
+        uint4 *y = reinterpret_cast<uint4 *>(const_cast<uint8_t *>(base + int64_t(m.y) * pool.page_bytes)) + begin + threadIdx.x;
+        int k = threadIdx.x;
+        for (; k + 768 < left; k += 1024, x += 1024, y += 1024) {
+          uint4 w[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) w[c] = __ldcs(x + 256 * c);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) y[256 * c] = w[c];
+        }
+        for (; k < left; k += 256, x += 256, y += 256) *y = __ldcs(x);
+      } else {
+        const uint8_t *x = base + int64_t(m.x) * pool.page_bytes + begin;
+        uint8_t *y = const_cast<uint8_t *>(base + int64_t(m.y) * pool.page_bytes) + begin;
+        for (int k = threadIdx.x; k < left; k += 256) y[k] = x[k];
       }
     }
-    if (from == to) continue;
-    const uint8_t *a = static_cast<const uint8_t *>(pool.base) + from * pool.page_bytes;
-    uint8_t *b = static_cast<uint8_t *>(pool.base) + to * pool.page_bytes;
-    if (((reinterpret_cast<uintptr_t>(pool.base) | uint64_t(pool.page_bytes)) & 15) == 0) {
-      const int64_t words = pool.page_bytes / 16;
-      const uint4 *x = reinterpret_cast<const uint4 *>(a);
-      uint4 *y = reinterpret_cast<uint4 *>(b);
-      for (int64_t k = threadIdx.x; k < words; k += 4 * 256) {
-        uint4 w[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (k + 256 * c < words) w[c] = __ldcs(x + k + 256 * c);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (k + 256 * c < words) y[k + 256 * c] = w[c];
-      }
-    } else {
-      for (int64_t k = threadIdx.x; k < pool.page_bytes; k += 256) b[k] = a[k];
-    }
+    i += step, rest += step_rest;
+    if (rest >= per) ++i, rest -= per;
   }
 }
 
@@ -591,8 +660,11 @@ psd_status launch_copy(CopyParams p, const psd_page_pool *pools, int num_pools, 
     CopyPools c;
     p.pools = most > 0 ? std::min(kPoolsALaunch, num_pools - k) : 0;
     std::copy(pools + k, pools + k + p.pools, c.pool);
+    int64_t page = 1;
+    for (int i = 0; i < p.pools; ++i) page = std::max(page, c.pool[i].page_bytes);
+    p.parts = int(std::min<int64_t>((page + kPart - 1) / kPart, 1024));
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(std::min<int64_t>(std::max<int64_t>(most * p.pools, p.children), int64_t(dev.num_sms) * 8)));
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(std::max<int64_t>(most * p.pools * p.parts, p.children), int64_t(dev.num_sms) * 8)));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -679,24 +751,23 @@ extern "C" psd_status fork_pages(psd_ctx *ctx, const psd_fork_args *a, void *wor
   p.room = a->room;
   p.release = a->keep_old == 0;
   cudaError_t e = cudaSuccess;
-  const size_t shared = (size_t(a->num_pages) + 3) / 4 * 16 + size_t(a->num_new) * 16;
   if (a->num_new <= kFewChildren && a->num_pages <= kFewPages && a->new_capacity <= kFewEntries) {
     static std::atomic<uint64_t> ready{0};
     const uint64_t bit = ctx->dev.device < 64 ? uint64_t(1) << ctx->dev.device : 0;
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-      e = cudaFuncSetAttribute(fork_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kFewPages * 4 + kFewChildren * 16);
+      e = cudaFuncSetAttribute(fork_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kFewShared));
       if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
       ready.fetch_or(bit, std::memory_order_release);
     }
-    fork_few_kernel<<<1, kThreads, shared, s>>>(p);
+    const size_t shared = few_shared(a->num_pages, a->num_new, a->num_page_indices), least = few_shared(a->num_pages, a->num_new, 0);
+    fork_few_kernel<<<1, kThreads, shared, s>>>(p, int((shared - least + 16) / 4));
   } else {
     fork_kernel<<<kCtas, kThreads, 0, s>>>(p);
   }
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "fork_pages launch: %s", cudaGetErrorString(e));
   CopyParams c = {};
-  c.count = &p.w.head->moves;
+  c.head = p.w.head;
   c.moves = p.w.moves;
   c.fault = a->fault_dev;
   c.num_pages = a->num_pages;
@@ -761,7 +832,7 @@ extern "C" psd_status compact_pages(psd_ctx *ctx, const psd_compact_args *a, voi
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "compact_pages launch: %s", cudaGetErrorString(e));
   CopyParams c = {};
-  c.count = &p.w.head->moves;
+  c.head = p.w.head;
   c.moves = p.w.moves;
   c.fault = a->fault_dev;
   c.num_pages = a->num_pages;

@@ -245,6 +245,43 @@ def test_copies(width):
         assert torch.equal(old, pool)
 
 
+@pytest.mark.parametrize("widths", [(40001, 16, 131072), (16384, 16383, 16400), (2 ** 25 + 16, 7, 2 ** 25 + 1)])
+def test_copies_of_large_pages(widths):
+    """Pages of several parts beside small ones, on and off their alignment."""
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    pools = [torch.randint(0, 256, (6, w), dtype=torch.uint8, device="cuda", generator=gen) for w in widths]
+    before = [p.clone() for p in pools]
+    fault = psd.copy_pages(ctx(), psd.PagePools(pools), i32([5, 1, 3]), i32([0, 2, 3]))
+    assert int(fault) == 0
+    for old, pool in zip(before, pools):
+        old[[0, 2]] = old[[5, 1]]
+        assert torch.equal(old, pool)
+
+
+@pytest.mark.parametrize("off", [0, 1, 2, 3])
+def test_tables_off_their_alignment(off):
+    """Tables and counts that begin anywhere in a larger tensor, and an old table that begins behind other entries."""
+    c = Cache([40, 70, 20, 33], 16, shared=1, extra=30, seed=40)
+    parents, N = [0, 2, 2, 1], 4
+    wide = lambda a: torch.cat([i32([7] * off), i32(a)])[off:]  # noqa: E731
+    lead = 3
+    indptr, indices = [x + lead for x in c.indptr], [0] * lead + list(c.indices)
+    out = dict(new_indptr=wide([0] * (N + 1)), new_indices=wide([0] * 40), new_len=wide([0] * N))
+    new_ref, ws = wide(c.ref), psd.pages_workspace(c.pages, N, "cuda")
+    before = [p.clone() for p in c.pools]
+    fault = psd.fork_pages(ctx(), c.pages, i32(parents), page_indptr=wide(indptr), page_indices=wide(indices),
+                           kv_len=wide(c.kv_len), page_size=16, room=1, ref_count=wide(c.ref), new_ref_count=new_ref,
+                           workspace=ws, **out)
+    rows, lengths, counts, copies = BM.fork(parents, c.indptr, c.indices, c.kv_len, 16, 1, c.ref)
+    flat = [x for r in rows for x in r]
+    assert int(fault) == 0 and out["new_indices"][: len(flat)].tolist() == flat
+    assert new_ref.tolist() == counts and out["new_len"].tolist() == lengths
+    for old, pool in zip(before, c.pools):
+        for a, b in copies:
+            old[b] = old[a]
+        assert torch.equal(old, pool)
+
+
 def test_pools_past_32_bits():
     """5 GB of pages: offsets beyond 2^32 bytes."""
     pool = torch.zeros((40000, 131072), dtype=torch.uint8, device="cuda")
