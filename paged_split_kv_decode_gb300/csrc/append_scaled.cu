@@ -22,12 +22,13 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kLeast = 95;  // 2^-32
-constexpr int kMaxBlock = 64, kMany = 16;
+constexpr int kMaxBlock = 64, kMany = 16, kManyQueries = 16;  // tokens a CTA at most
+constexpr int kBlockCtas = 2, kQueryCtas = 4;  // CTAs an SM
 
 struct ScaledParams {
   AppendParams a;
   uint8_t *k_scales, *v_scales;
-  int block;
+  int block, shift;  // 2^shift tokens
 };
 
 // A token of the CTA.
@@ -38,16 +39,30 @@ struct Token {
   int64_t slot;  // pool row, or -1
 };
 
-// Token t0 + lane of a warp's, for the lanes below `own`: the warp finds the first one's request, and the lanes walk on from
-// there.  (A search for each token, two a warp one after the other, took twice the time of these dependent loads.)
+// The request of token t0 + lane, for the lanes below `own` (uniform): the warp finds the first one's, and one load of 32 bounds
+// behind it tells the others'.
+__device__ __forceinline__ int request_of_lane(const AppendParams &p, int t0, int own) {
+  const int lane = threadIdx.x & 31, b0 = request_of(p.q_indptr, p.B, t0);
+  if (own == 1) return b0;
+  const int bound = b0 + 1 + lane < p.B ? __ldg(p.q_indptr + b0 + 1 + lane) : 0x7fffffff;
+  int b = b0;
+  for (int i = 0; i < own; ++i) {
+    const int behind = __popc(__ballot_sync(0xffffffffu, bound <= t0 + i));
+    if (lane == i) b = b0 + behind;
+  }
+  if (b == b0 + 32)  // (many requests without tokens)
+    while (b + 1 < p.B && __ldg(p.q_indptr + b + 1) <= t0 + lane) ++b;
+  return b;
+}
+// Token t0 + lane of a warp's, for the lanes below `own`.  (A search for each token, two a warp one after the other, took twice
+// the time of these dependent loads.)
 __device__ __forceinline__ Token locate(const ScaledParams &s, int t0, int own, uint32_t &faults) {
   const AppendParams &p = s.a;
   Token x{-1, 0, 0, -1};
   faults = 0;
   const int t = t0 + int(threadIdx.x & 31), all = __ldg(p.q_indptr + p.B);
-  int b = request_of(p.q_indptr, p.B, t0);
+  const int b = request_of_lane(p, t0, own);
   if (t >= t0 + own || t >= p.T || t >= all) return x;  // not the CTA's, or behind the last request
-  while (b + 1 < p.B && __ldg(p.q_indptr + b + 1) <= t) ++b;
   const int begin = __ldg(p.q_indptr + b), end = __ldg(p.q_indptr + b + 1);
   const int at = __ldg(p.kv_len + b) - (end - t);  // index in the request
   const int first = __ldg(p.page_indptr + b), last = __ldg(p.page_indptr + b + 1);
@@ -65,7 +80,7 @@ __device__ __forceinline__ Token locate(const ScaledParams &s, int t0, int own, 
     return x;
   }
   x.slot = int64_t(id) * p.page_size + at % p.page_size;
-  x.older = at % s.block;
+  x.older = at & (s.block - 1);
   // the first of the block: its request's first token, or the block's
   if (t == begin || x.older == 0) x.count = min(s.block - x.older, min(end, p.T) - t);  // (no row behind the last that is there)
   return x;
@@ -114,9 +129,9 @@ __device__ __forceinline__ F8 values8(const uint2 &w) {
   }
   return f;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {  // NaN operands lose, as in fmaxf
+__device__ __forceinline__ float max_abs(float a, float b, float c) {  // of the magnitudes; NaN operands lose, as in fmaxf
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // The least e with top <= 448 2^(e - 127), top >= 0 finite.
@@ -154,109 +169,186 @@ __device__ __forceinline__ void rotate(F8 &a, F8 &b, const float *c, const float
   }
 }
 
-// KIND: all in one launch, K and V alone, or the queries alone, whose CTAs have more room without the others' code.
-enum { kAllParts, kBlocks, kQueries };
-template <int NT, bool NEOX, int KIND>
-__global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_scaled_kernel(const ScaledParams s, const __grid_constant__ Turns turns) {
+// The angles of tokens from .. n - 1 into `cosine` and `sine`, all kThreads threads; `freq`: the turns per position, in shared
+// memory (lanes that read different parameters of a launch wait for each other).
+__device__ __forceinline__ void make_angles(const int *pos, int from, int n, int half, const uint64_t *freq, float magnitude, float *cosine,
+                                            float *sine) {
+  if (half == 0) return;
+  const int step = kThreads / half, rest = kThreads - step * half;
+  int m = int(threadIdx.x) / half, k = int(threadIdx.x) - m * half;
+  for (m += from; m < n; m += step) {
+    const float2 cs = pos[m] >= 0 ? short_turn(freq[k], pos[m], magnitude) : make_float2(0.f, 0.f);
+    const int at = m * half + angle_at(k, half);
+    cosine[at] = cs.x;
+    sine[at] = cs.y;
+    k += rest;
+    if (k >= half) k -= half, ++m;
+  }
+}
+// A thread's place in a token's query heads: a group of pairs, or a run that is not rotated.
+struct Column {
+  int at;       // of the first run of 8 (element in the token's row)
+  int group;    // of pairs; negative: not rotated
+  __device__ __forceinline__ Column(const AppendParams &p, int job, int groups, int per_head, bool neox) {
+    const int h = job / per_head, g = job - h * per_head;
+    group = g < groups ? g : -1;
+    int col = g < groups ? p.rot_col + (neox ? 8 * g : 16 * g) : 8 * (g - groups);
+    if (g >= groups && col >= p.rot_col) col += p.rot;
+    at = h * p.D + col;
+  }
+};
+
+// Queries of `per` tokens a CTA: a thread has the same column of all of them, two tokens on their way.  (With two tokens a CTA
+// every other cycle went into waiting for their places: 26 us for 8118 tokens of 32 heads of 128.)
+template <bool NEOX>
+__global__ void __launch_bounds__(kThreads, kQueryCtas) append_queries_kernel(const ScaledParams s, const __grid_constant__ Turns turns, int per) {
   extern __shared__ __align__(16) float table[];  // cosines [tokens][half], then sines
-  __shared__ Token tokens[NT];
-  __shared__ int pos[NT + kMaxBlock];
-  __shared__ int n_table, n_starts, starts[NT];  // tokens whose angles are needed; tokens that begin their block
+  __shared__ int pos[kManyQueries];
+  __shared__ uint64_t freq[kMaxPairs / 2];
+  const AppendParams &p = s.a;
+  dependents_may_launch();  // K and V
+  const int tid = threadIdx.x, lane = tid & 31;
+  for (int k = tid; k < p.rot / 2; k += kThreads) freq[k] = turns.f[k];
+  const int half = p.rot / 2, groups = half / 8, far = NEOX ? half : 8;
+  const int per_head = groups + (p.D - p.rot) / 8, jobs = p.Hq * per_head;
+  const int t0 = blockIdx.x * per, n = min(per, p.T - t0);
+  uint4 wa[2], wb[2];
+  auto fetch = [&](const Column &c, int i, uint4 &a, uint4 &b) {
+    if (i < n) {
+      const __nv_bfloat16 *at = p.q + (t0 + i) * p.q_stride + c.at;
+      a = load_raw(at);
+      if (c.group >= 0) b = load_raw(at + far);
+    }
+  };
+  Column c(p, min(tid, jobs - 1), groups, per_head, NEOX);
+  if (tid < jobs) {  // on their way before their places are known
+    fetch(c, 0, wa[0], wb[0]);
+    fetch(c, 1, wa[1], wb[1]);
+  }
+  if (tid < 32) {
+    const int t = t0 + lane, all = __ldg(p.q_indptr + p.B), b = request_of_lane(p, t0, n);
+    int at = -1;
+    if (lane < n && t < all) {
+      const int begin = __ldg(p.q_indptr + b), end = __ldg(p.q_indptr + b + 1);
+      at = p.positions ? __ldg(p.positions + t) : __ldg(p.kv_len + b) - (end - t);
+      if (t < begin || t >= end) at = -1;  // (K's CTAs report it)
+    }
+    if (lane < n) pos[lane] = max(at, -1);
+  }
+  __syncthreads();
+  float *cosine = table, *sine = table + n * half;
+  make_angles(pos, 0, n, half, freq, p.magnitude, cosine, sine);
+  __syncthreads();
+  // (q_out may be q: both runs of a group are read before either is written)
+  for (int job = tid; job < jobs; job += kThreads) {
+    if (job != tid) {
+      c = Column(p, job, groups, per_head, NEOX);
+      fetch(c, 0, wa[0], wb[0]);
+      fetch(c, 1, wa[1], wb[1]);
+    }
+    __nv_bfloat16 *to = p.q_out + int64_t(t0) * p.Hq * p.D + c.at;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 2) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = i0 + k;
+        const bool there = i < n && pos[i] >= 0;
+        if (c.group >= 0) {
+          F8 x = unpack(wa[k]), y = unpack(wb[k]);
+          fetch(c, i + 2, wa[k], wb[k]);
+          if (there) {
+            rotate<NEOX>(x, y, cosine + i * half, sine + i * half, c.group, half);
+            store8(to, x);
+            store8(to + far, y);
+          }
+        } else {
+          const uint4 w = wa[k];
+          fetch(c, i + 2, wa[k], wb[k]);
+          if (there) *reinterpret_cast<uint4 *>(to) = w;
+        }
+        to += int64_t(p.Hq) * p.D;
+      }
+    }
+  }
+}
+
+// Tokens t0 .. t0 + own - 1 as K's and V's CTAs take them.
+template <int NT>
+struct Tile {
+  Token tokens[NT];
+  int pos[NT + kMaxBlock];
+  int n_table, n_starts, starts[NT];  // tokens whose angles are needed; tokens that begin their block
+};
+// A warp fills it in; returns the faults.
+template <int NT>
+__device__ __forceinline__ uint32_t fill(const ScaledParams &s, int t0, int own, Tile<NT> &tile) {
+  static_assert(NT <= 32, "a lane a token");
+  const int lane = threadIdx.x & 31;
+  uint32_t faults;
+  const Token x = locate(s, t0, own, faults);
+  if (lane < own) tile.tokens[lane] = x;
+  faults = __reduce_or_sync(0xffffffffu, faults);
+  __syncwarp();
+  // the tokens whose angles are needed: its own, and those of its last block behind them
+  const bool begins = x.slot >= 0 && x.count > 0;
+  const uint32_t who = __ballot_sync(0xffffffffu, begins);
+  const int most = __reduce_max_sync(0xffffffffu, begins ? max(own, lane + x.count) : own);
+  for (int n = lane; n < most; n += 32) {
+    if (n < own) {
+      tile.pos[n] = tile.tokens[n].pos;
+    } else {  // of the request of the last block that starts here
+      int at = -1;
+      if (s.a.positions) {
+        at = __ldg(s.a.positions + t0 + n);
+      } else {
+        const int i = 31 - __clz(who);
+        if (tile.tokens[i].count > n - i) at = tile.tokens[i].pos + (n - i);
+      }
+      tile.pos[n] = max(at, -1);
+    }
+  }
+  if (begins) tile.starts[__popc(who & ((1u << lane) - 1u))] = lane;
+  if (lane == 0) tile.n_table = most, tile.n_starts = __popc(who);
+  return faults;
+}
+// The rows of K or V, as far as the CTA's own tokens go, to the second-level cache.
+__device__ __forceinline__ void prefetch_rows(const AppendParams &p, bool is_v, int t0, int own, int id, int threads) {
+  const int bytes = (is_v ? p.Dv : p.D) * p.Hkv * 2;
+  const int64_t stride = 2 * (is_v ? p.v_stride : p.k_stride);
+  const uint8_t *row = reinterpret_cast<const uint8_t *>(is_v ? p.v : p.k) + t0 * stride;
+  for (int n = min(own, p.T - t0); n > 0; --n, row += stride)
+    for (int at = 128 * id; at < bytes; at += 128 * threads) prefetch_l2(row + at);
+}
+
+// The blocks that begin in a tile: K of head h, or V of it, a warp each.  A lane has two runs of 8 columns of a token, up to
+// kPasses tokens at once.  K's angles are made by all kWarps warps, a barrier behind them, while the first block's rows are on
+// their way: `joined` is that barrier.
+template <int NT, bool NEOX, typename Barrier>
+__device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64_t *freq, const Tile<NT> &tile, int t0, bool is_v, float *table,
+                                             Barrier joined) {
+  constexpr int kPasses = 4;
   const AppendParams &p = s.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int half = p.rot / 2;
   const int groups = half / 8, far = NEOX ? half : 8;  // groups of 8 pairs; their second run of 8 columns is `far` behind
-  // CTAs of K (0) and V (1) in turn, NT tokens each, then those of the queries (2), NQ each.
-  constexpr int NQ = NT < 2 ? NT : 2;
-  const int kv_ctas = KIND == kQueries ? 0 : 2 * ((p.T + NT - 1) / NT), cta = blockIdx.x;
-  if (KIND == kQueries) dependents_may_launch();  // K and V are another launch's
-  const int part = KIND == kQueries || (KIND == kAllParts && cta >= kv_ctas) ? 2 : cta & 1, own = part == 2 ? NQ : NT;
-  const int t0 = part == 2 ? (cta - kv_ctas) * NQ : cta / 2 * NT;
-
-  // Queries: a thread has the same group of pairs, or run that is not rotated, of all tokens, which are on their way before
-  // their places are known.
-  const int rest = (p.D - p.rot) / 8, per_head = groups + rest;
-  uint4 qa[NQ], qb[NQ];
-  int job = tid, q_col = 0;
-  bool q_turned = false;
-  auto enter = [&]() {  // the thread's job: its column in a token's heads
-    const int h = job / per_head, g = job - h * per_head;
-    q_turned = g < groups;
-    int col = q_turned ? p.rot_col + (NEOX ? 8 * g : 16 * g) : 8 * (g - groups);
-    if (!q_turned && col >= p.rot_col) col += p.rot;
-    q_col = h * p.D + col;
-  };
-  auto fetch_q = [&]() {
-#pragma unroll
-    for (int q = 0; q < NQ; ++q)
-      if (t0 + q < p.T) {
-        const __nv_bfloat16 *at = p.q + (t0 + q) * p.q_stride + q_col;
-        qa[q] = load_raw(at);
-        if (q_turned) qb[q] = load_raw(at + far);
-      }
-  };
-  if (part == 2) {
-    if (job < p.Hq * per_head) {
-      enter();
-      fetch_q();
-    }
-  } else {  // the rows of K or V, as far as the CTA's own tokens go, to the second-level cache
-    const int lines = ((part ? p.Dv : p.D) * p.Hkv * 2 + 127) / 128;
-    for (int i = tid; i < NT * lines; i += kThreads)
-      if (t0 + i / lines < p.T)
-        prefetch_l2(reinterpret_cast<const uint8_t *>(part ? p.v + (t0 + i / lines) * p.v_stride : p.k + (t0 + i / lines) * p.k_stride) +
-                    i % lines * 128);
-  }
-  if (warp == 0) {
-    static_assert(NT <= 32, "a lane a token");
-    uint32_t faults;
-    const Token x = locate(s, t0, own, faults);
-    if (lane < own) tokens[lane] = x;
-    faults = __reduce_or_sync(0xffffffffu, faults);
-    if (faults && lane == 0 && part == 0) atomicOr(p.fault, int32_t(faults));
-    __syncwarp();
-    // the tokens whose angles are needed: its own, and those of its last block behind them
-    const bool begins = x.slot >= 0 && x.count > 0;
-    const uint32_t who = __ballot_sync(0xffffffffu, begins);
-    const int most = part == 2 ? own : __reduce_max_sync(0xffffffffu, begins ? max(own, lane + x.count) : own);
-    for (int n = lane; n < most; n += 32) {
-      if (n < own) {
-        pos[n] = tokens[n].pos;
-      } else {  // of the request of the last block that starts here
-        int at = -1;
-        if (p.positions) {
-          at = __ldg(p.positions + t0 + n);
-        } else {
-          const int i = 31 - __clz(who);
-          if (tokens[i].count > n - i) at = tokens[i].pos + (n - i);
-        }
-        pos[n] = max(at, -1);
-      }
-    }
-    if (begins) starts[__popc(who & ((1u << lane) - 1u))] = lane;
-    if (lane == 0) n_table = most, n_starts = __popc(who);
-  }
-  __syncthreads();
-  const int nt = n_table;
+  const int nt = tile.n_table, n_starts = tile.n_starts, W = is_v ? p.Dv : p.D;
+  const int *pos = tile.pos;
   float *cosine = table, *sine = table + nt * half;
-  const int from = part == 2 || n_starts == 0 ? 0 : starts[0];  // (tokens before the first block's begin are another CTA's)
-  for (int i = from * half + tid; part != 1 && (part == 2 || n_starts > 0) && i < nt * half; i += kThreads) {
-    const int n = i / half, k = i - n * half;
-    const float2 cs = pos[n] >= 0 ? short_turn(turns.f[k], pos[n], p.magnitude) : make_float2(0.f, 0.f);
-    cosine[n * half + angle_at(k, half)] = cs.x;
-    sine[n * half + angle_at(k, half)] = cs.y;
-  }
-  __syncthreads();
-
-  // ---- blocks: K of head h, or V of it.  A lane has two runs of 8 columns of a token, up to kPasses tokens at once.
-  constexpr int kPasses = 4;
-  const bool is_v = part == 1;
-  const int W = is_v ? p.Dv : p.D;
-  for (int u = warp; part < 2 && u < n_starts * p.Hkv; u += kWarps) {
-    const int start = u / p.Hkv, h = u - start * p.Hkv, n = starts[start];
-    const Token x = tokens[n];
-    const int lanes = (W + 15) / 16, a_pass = 32 / lanes;  // lanes a token, tokens a pass
-    const int mine = lane / lanes, k = lane - mine * lanes;
+  bool ready = is_v;
+  auto angles = [&]() {
+    if (ready) return;
+    const int from = n_starts == 0 ? nt : tile.starts[0];  // (tokens before the first block's begin are another CTA's)
+    make_angles(pos, from, nt, half, freq, p.magnitude, cosine, sine);
+    joined();
+    ready = true;
+  };
+  const int lanes = (W + 15) / 16, a_pass = 32 / lanes;  // lanes a token, tokens a pass
+  const int mine = lane / lanes, k = lane - mine * lanes;
+  for (int start = 0, h = warp;; h += kWarps) {
+    while (h >= p.Hkv && start < n_starts) h -= p.Hkv, ++start;
+    if (start >= n_starts) break;
+    const int n = tile.starts[start];
+    const Token x = tile.tokens[n];
     const bool turned = !is_v && k < groups;
     // the columns of the two runs (the second may not be there): a group of pairs, or two runs that are not rotated
     int ca = turned ? p.rot_col + (NEOX ? 8 * k : 16 * k) : 16 * k - (is_v ? 0 : p.rot), cb = turned ? ca + far : ca + 8;
@@ -269,14 +361,14 @@ __global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_sca
     const int64_t stride = is_v ? p.v_stride : p.k_stride;
     bool any = false;  // of the tokens is appended
     for (int i = lane; i < x.count; i += 32) any |= pos[n + i] >= 0;
-    if (!__any_sync(0xffffffffu, any)) continue;
-    const int passes = (x.count + a_pass - 1) / a_pass;
+    any = __any_sync(0xffffffffu, any);
+    const int passes = x.count <= kPasses * a_pass ? kPasses : (x.count + a_pass - 1) / a_pass;
     F8 a[kPasses], b[kPasses];
+    uint4 wa[kPasses], wb[kPasses];
     uint32_t valid = 0;  // passes of those at hand that have a token for this lane
     auto fetch = [&](int pass0) {
       valid = 0;
       const __nv_bfloat16 *at = src + (t0 + n + pass0 * a_pass + mine) * stride;
-      uint4 wa[kPasses], wb[kPasses];
 #pragma unroll
       for (int q = 0; q < kPasses; ++q) {
         const int i = (pass0 + q) * a_pass + mine;
@@ -288,6 +380,8 @@ __global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_sca
         }
         at += a_pass * stride;
       }
+    };
+    auto turn = [&](int pass0) {
 #pragma unroll
       for (int q = 0; q < kPasses; ++q) {
         a[q] = unpack(wa[q]), b[q] = unpack(wb[q]);
@@ -295,12 +389,16 @@ __global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_sca
         if (turned && (valid >> q & 1)) rotate<NEOX>(a[q], b[q], cosine + i, sine + i, k, half);
       }
     };
+    fetch(0);
+    angles();
+    if (!any) continue;
+    turn(0);
     float top = 0.f;
     // (NaN loses; infinities are looked for again, and left out, where there are any)
     auto larger = [&](const F8 &f, bool finite) {
       if (!finite) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) top = max3(top, fabsf(f.v[i]), fabsf(f.v[i + 1]));
+        for (int i = 0; i < 8; i += 2) top = max_abs(top, f.v[i], f.v[i + 1]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -311,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_sca
     for (bool finite = false;; finite = true) {
 #pragma unroll 1
       for (int pass0 = 0; pass0 < passes; pass0 += kPasses) {
-        if (!finite || passes > kPasses) fetch(pass0);
+        if (passes > kPasses && (finite || pass0 > 0)) fetch(pass0), turn(pass0);
 #pragma unroll
         for (int q = 0; q < kPasses; ++q) {
           larger(a[q], finite);
@@ -323,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_sca
       top = 0.f;
     }
     const int64_t first = x.slot - x.older;              // the block's first row
-    uint8_t *scale = (is_v ? s.v_scales : s.k_scales) + first / s.block * p.Hkv + h;
+    uint8_t *scale = (is_v ? s.v_scales : s.k_scales) + (first >> s.shift) * p.Hkv + h;
     uint8_t *pool = static_cast<uint8_t *>(is_v ? p.v_pool : p.k_pool) + (first * p.Hkv + h) * W;
     const int64_t pool_stride = int64_t(p.Hkv) * W;
     int e = scale_of(top);
@@ -347,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_sca
     const float by = __uint_as_float(uint32_t(254 - min(e, 253)) << 23);
 #pragma unroll 1
     for (int pass0 = 0; pass0 < passes; pass0 += kPasses) {
-      if (passes > kPasses) fetch(pass0);                // (otherwise they are there)
+      if (passes > kPasses) fetch(pass0), turn(pass0);   // (otherwise they are there)
       uint8_t *at = pool + (x.older + pass0 * a_pass + mine) * pool_stride;
 #pragma unroll
       for (int q = 0; q < kPasses; ++q) {
@@ -359,69 +457,148 @@ __global__ void __launch_bounds__(kThreads, KIND == kQueries ? 5 : 2) append_sca
       }
     }
   }
+  angles();
+}
 
-  // ---- queries.  (q_out may be q: both runs of a group are read before either is written.)
-  if (KIND == kBlocks) wait_for_prior_grid();  // what waits for this launch waits for the queries' too
-  while (KIND != kBlocks && part == 2 && job < p.Hq * per_head) {
-    const int g = job % per_head;
-#pragma unroll
-    for (int q = 0; q < NQ; ++q) {
-      if (pos[q] < 0) continue;
-      __nv_bfloat16 *to = p.q_out + int64_t(t0 + q) * p.Hq * p.D + q_col;
-      if (q_turned) {
-        F8 x = unpack(qa[q]), y = unpack(qb[q]);
-        rotate<NEOX>(x, y, cosine + q * half, sine + q * half, g, half);
-        store8(to, x);
-        store8(to + far, y);
-      } else {
-        *reinterpret_cast<uint4 *>(to) = qa[q];
+// K and V of many tokens: a CTA takes tiles of kMany tokens, of K and of V in turn.  Its warps find the places of one tile each,
+// all at once, and bring the rows to the second-level cache.  (With a CTA a tile, seven warps waited for the eighth's dependent
+// loads: 26 us for 8118 tokens of 8 heads of 128 against @@.)
+template <bool NEOX>
+__global__ void __launch_bounds__(kThreads, kBlockCtas) append_blocks_kernel(const ScaledParams s, const __grid_constant__ Turns turns, int) {
+  extern __shared__ __align__(16) float table[];  // cosines [tokens][half], then sines
+  __shared__ Tile<kMany> tiles[kWarps];
+  __shared__ uint64_t freq[kMaxPairs / 2];
+  const AppendParams &p = s.a;
+  for (int k = threadIdx.x; k < p.rot / 2; k += kThreads) freq[k] = turns.f[k];
+  const int items = 2 * ((p.T - 1) / kMany + 1), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = gridDim.x;
+  int turn = 0;
+  for (int item = blockIdx.x; item < items; item += step, ++turn) {
+    __syncthreads();  // the table and the tile before are free
+    if (turn % kWarps == 0) {
+      const int64_t mine = item + int64_t(warp) * step;
+      if (mine < items) {
+        const bool is_v = (mine + warp) & 1;
+        prefetch_rows(p, is_v, int(mine / 2) * kMany, kMany, lane, 32);
+        const uint32_t faults = fill(s, int(mine / 2) * kMany, kMany, tiles[warp]);
+        if (faults && lane == 0 && !is_v) atomicOr(p.fault, int32_t(faults));
       }
+      __syncthreads();
     }
-    job += kThreads;
-    if (job < p.Hq * per_head) {
-      enter();
+    write_blocks<kMany, NEOX>(s, freq, tiles[turn % kWarps], item / 2 * kMany, (item + turn) & 1, table, [] { __syncthreads(); });
+  }
+  wait_for_prior_grid();  // what waits for this launch waits for the queries' too
+}
+
+// Few tokens: a CTA a token's K, its V and its queries, all in one launch.
+template <bool NEOX>
+__global__ void __launch_bounds__(kThreads, 2) append_few_kernel(const ScaledParams s, const __grid_constant__ Turns turns, int) {
+  extern __shared__ __align__(16) float table[];  // cosines [tokens][half], then sines
+  __shared__ Tile<1> tile;
+  __shared__ uint64_t freq[kMaxPairs / 2];
+  const AppendParams &p = s.a;
+  for (int k = threadIdx.x; k < p.rot / 2; k += kThreads) freq[k] = turns.f[k];
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int half = p.rot / 2, groups = half / 8, far = NEOX ? half : 8;
+  // CTAs of K (0) and V (1) in turn, then those of the queries (2).
+  const int kv_ctas = 2 * p.T, cta = blockIdx.x, part = cta >= kv_ctas ? 2 : cta & 1, t0 = part == 2 ? cta - kv_ctas : cta / 2;
+  // The row is on its way before its place is known.
+  const int per_head = groups + (p.D - p.rot) / 8, jobs = p.Hq * per_head;
+  uint4 qa, qb;
+  Column c(p, min(tid, max(jobs - 1, 0)), groups, per_head, NEOX);
+  auto fetch_q = [&]() {
+    const __nv_bfloat16 *at = p.q + t0 * p.q_stride + c.at;
+    qa = load_raw(at);
+    if (c.group >= 0) qb = load_raw(at + far);
+  };
+  if (part < 2) prefetch_rows(p, part == 1, t0, 1, tid, kThreads);
+  else if (tid < jobs) fetch_q();
+  if (warp == 0) {
+    const uint32_t faults = fill(s, t0, 1, tile);
+    if (faults && tid == 0 && part == 0) atomicOr(p.fault, int32_t(faults));
+  }
+  __syncthreads();
+  if (part < 2) {
+    write_blocks<1, NEOX>(s, freq, tile, t0, part == 1, table, [] { __syncthreads(); });
+    return;
+  }
+  // (q_out may be q: both runs of a group are read before either is written)
+  const int pos = tile.pos[0];
+  if (pos < 0) return;
+  float *cosine = table, *sine = table + half;
+  for (int k = tid; k < half; k += kThreads) {
+    const float2 cs = short_turn(freq[k], pos, p.magnitude);
+    cosine[angle_at(k, half)] = cs.x;
+    sine[angle_at(k, half)] = cs.y;
+  }
+  __syncthreads();
+  for (int job = tid; job < jobs; job += kThreads) {
+    if (job != tid) {
+      c = Column(p, job, groups, per_head, NEOX);
       fetch_q();
+    }
+    __nv_bfloat16 *to = p.q_out + int64_t(t0) * p.Hq * p.D + c.at;
+    if (c.group >= 0) {
+      F8 x = unpack(qa), y = unpack(qb);
+      rotate<NEOX>(x, y, cosine, sine, c.group, half);
+      store8(to, x);
+      store8(to + far, y);
+    } else {
+      *reinterpret_cast<uint4 *>(to) = qa;
     }
   }
 }
 
-template <int NT, bool NEOX, int KIND>
-psd_status launch(const ScaledParams &p, const Turns &turns, const DeviceInfo &dev, cudaStream_t s) {
-  constexpr int NQ = NT < 2 ? NT : 2;
-  const size_t shared = size_t(KIND == kQueries ? NQ : NT + p.block - 1) * size_t(p.a.rot) * 4;
-  const int64_t kv_ctas = 2 * ((int64_t(p.a.T) - 1) / NT + 1), q_ctas = (int64_t(p.a.T) - 1) / NQ + 1;
-  const int64_t ctas = KIND == kQueries ? q_ctas : KIND == kBlocks || p.a.Hq == 0 ? kv_ctas : kv_ctas + q_ctas;
+template <typename Kernel>
+psd_status start(Kernel kern, std::atomic<uint64_t> &ready, int64_t ctas, int threads, size_t shared, size_t most_shared, bool behind,
+                 const ScaledParams &p, const Turns &turns, int per, const DeviceInfo &dev, cudaStream_t s) {
   if (ctas > 0x7fffffffLL) return fail(PSD_ERR_UNSUPPORTED, "append_tokens_scaled: %d tokens", p.a.T);
-  auto kern = append_scaled_kernel<NT, NEOX, KIND>;
-  static std::atomic<uint64_t> ready{0};
   const uint64_t bit = dev.device < 64 ? uint64_t(1) << dev.device : 0;
   cudaError_t e = cudaSuccess;
   if (!(ready.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (NT + kMaxBlock - 1) * kMaxPairs * 4);
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most_shared));
     if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
     ready.fetch_or(bit, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(ctas));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = shared;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = KIND == kBlocks && p.a.Hq > 0 ? 1 : 0;  // K and V start while the queries end, and wait for that at their end
-  e = cudaLaunchKernelEx(&cfg, kern, p, turns);
+  cfg.numAttrs = behind ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, p, turns, per);
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "append_tokens_scaled launch: %s", cudaGetErrorString(e));
   return PSD_OK;
 }
 
+// Tokens a CTA of the queries, so that they fill whole rounds of the CTAs that run at once.
+int tokens_a_cta(int64_t tokens, int64_t at_once) {
+  const int64_t rounds = (tokens + at_once * kManyQueries - 1) / (at_once * kManyQueries);
+  return int((tokens + at_once * rounds - 1) / (at_once * rounds));
+}
+
 template <bool NEOX>
 psd_status launch_all(const ScaledParams &p, const Turns &turns, const DeviceInfo &dev, cudaStream_t s) {
+  const int64_t T = p.a.T;
+  const size_t angles = size_t(p.a.rot) * 4;  // bytes a token
+  static std::atomic<uint64_t> one{0}, queries{0}, blocks{0};
   // One launch while its CTAs fit on the SMs at once.
-  if (p.a.T <= 2 * dev.num_sms) return launch<1, NEOX, kAllParts>(p, turns, dev, s);
-  const psd_status st = p.a.Hq ? launch<kMany, NEOX, kQueries>(p, turns, dev, s) : PSD_OK;
-  return st != PSD_OK ? st : launch<kMany, NEOX, kBlocks>(p, turns, dev, s);
+  if (T <= 2 * dev.num_sms)
+    return start(append_few_kernel<NEOX>, one, (p.a.Hq ? 3 : 2) * T, kThreads, p.block * angles, kMaxBlock * kMaxPairs * 4, false, p, turns,
+                 1, dev, s);
+  if (p.a.Hq) {
+    const int per = tokens_a_cta(T, kQueryCtas * dev.num_sms);
+    const psd_status st = start(append_queries_kernel<NEOX>, queries, (T + per - 1) / per, kThreads, per * angles,
+                                kManyQueries * kMaxPairs * 4, false, p, turns, per, dev, s);
+    if (st != PSD_OK) return st;
+  }
+  // (K and V start while the queries end, and wait for that at their end)
+  const int64_t items = 2 * ((T + kMany - 1) / kMany);
+  return start(append_blocks_kernel<NEOX>, blocks, std::min<int64_t>(items, kBlockCtas * dev.num_sms), kThreads,
+               (kMany + p.block - 1) * angles, (kMany + kMaxBlock - 1) * kMaxPairs * 4, p.a.Hq > 0, p, turns, kMany, dev, s);
 }
 
 }  // namespace
@@ -466,6 +643,7 @@ extern "C" psd_status append_tokens_scaled(psd_ctx *ctx, const psd_append_args *
   p.k_scales = scales->k;
   p.v_scales = scales->v;
   p.block = scales->block;
+  p.shift = scales->block == 16 ? 4 : scales->block == 32 ? 5 : 6;
   const Turns turns = append_turns(a);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return a->neox ? launch_all<true>(p, turns, ctx->dev, s) : launch_all<false>(p, turns, ctx->dev, s);
