@@ -25,11 +25,16 @@
 // it that costs the same.  A request that a stretch's bound cuts leaves normalised pieces, which a second kernel
 // joins in key order.  Nothing is added atomically.  (With a unit's steps dealt out to the eight warps of a CTA and
 // their O joined in shared memory, that joining took more instructions than the steps.)
+//
+// Bound by DRAM in its steady state: 32 single tokens over 512 to 4096 keys (140 MB, 21 us at the copy rate) take 30 us without
+// the join and 34 with it; three over 20000 to 65536 with f32 outputs (27 us) 36 and 41.  The rest is the launch, the ramp
+// to the first step and the slots' ends.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "device.cuh"
 #include "multi_token.h"
@@ -41,8 +46,10 @@ namespace {
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kHalf = 16, kStep = 2 * kHalf;  // keys
 constexpr float kLazy = 8.f, kBias = 7.f;  // log2 units: P's top is 2^7, and grows to 2^15 at most
-constexpr int kSegmentCost = 1;  // of a request beside its steps, in steps
-constexpr int kLeastSteps = 3;   // of a slot
+constexpr int kSegmentCost = 2;  // of a request beside its steps, in steps
+constexpr int kLeastSteps = 1;   // of a slot (3: 4 tokens over 60 to 400 keys took 9.9 us against 7.8)
+constexpr int kMostPieces = 2048; // slots at most
+constexpr int kFewPieces = 16;   // that a warp joins by itself
 
 template <int D, int NT>
 struct Lay {
@@ -71,6 +78,7 @@ struct RowsParams {
   int Hq, Hkv, G, page_size, shift, out_f32;
   float q_scale;
   int B, slots;
+  bool narrow;  // the line's length times the slots fits 32 bits
 };
 // A launch's requests, and what those before each cost: their steps, and kSegmentCost each.
 struct RowsRequests {
@@ -79,9 +87,13 @@ struct RowsRequests {
 };
 
 __host__ __device__ __forceinline__ int steps_of(const psd_token_request &r) { return (r.kv_len - 1) / kStep + 1; }
+// (64-bit divisions take ten times as long.)
+__host__ __device__ __forceinline__ int64_t divide(const RowsParams &p, int64_t a, int64_t b) {
+  return p.narrow ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
 // The request and step at which slot `x` begins.
 __device__ __forceinline__ int2 begin_of(const RowsParams &p, const RowsRequests &req, int x) {
-  const int64_t want = x * req.before[p.B] / p.slots;
+  const int64_t want = divide(p, x * req.before[p.B], p.slots);
   int b = 0;
   for (int n = p.B; n > 1;) {  // the last request with before <= want
     const int mid = n / 2;
@@ -555,29 +567,95 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
   if (bad) raise_fault(p.fault, bad);
 }
 
+// A request's pieces, and the first one's slot.  The slots that have its first step and its last: slot x begins at cost
+// floor(x C / slots), and all costs up to kSegmentCost behind the request's begin at its first step.
+__host__ __device__ __forceinline__ int pieces_of(const RowsParams &p, const RowsRequests &req, int b, int64_t &first) {
+  const int64_t all = req.before[p.B], n = steps_of(req.r[b]);
+  first = divide(p, (req.before[b] + kSegmentCost + 1) * p.slots - 1, all);
+  const int64_t last = divide(p, (req.before[b] + kSegmentCost + n) * p.slots - 1, all);
+  return int((last < p.slots - 1 ? last : int64_t(p.slots) - 1) - first) + 1;
+}
+
+// Joins the pieces of a row, kFewPieces at most, a warp a row (request blockIdx.x, KV head blockIdx.y, four rows a CTA): a lane
+// has D / 32 columns of all pieces, and its own piece's LSE.  (With the kernel below 32 single tokens took 36 us, 34 so.)
+template <int D>
+__global__ void __launch_bounds__(128) rows_join_few_kernel(const RowsParams p, const __grid_constant__ RowsRequests req, int unit_rows) {
+  constexpr int N = D / 32;
+  using Vec = std::conditional_t<N == 4, float4, float2>;
+  const int b = blockIdx.x, kv = blockIdx.y, lane = threadIdx.x & 31, row = blockIdx.z * 4 + (threadIdx.x >> 5);
+  const psd_token_request &r = req.r[b];
+  int64_t first;
+  const int pieces = pieces_of(p, req, b, first), late = begin_of(p, req, int(first)).x < b;
+  wait_for_prior_grid();
+  if (pieces == 1 || row >= r.num_new * p.G) return;
+  // (all pieces' numbers fit 31 bits: step_rows_floats)
+  const int stride = 2 * p.Hkv * unit_rows, at0 = int(first) * stride + kv * unit_rows + row, late_by = late * p.Hkv * unit_rows;
+  auto at = [&](int i) { return at0 + i * stride + (i == 0 ? late_by : 0); };
+  const float lse = lane < pieces ? p.part_lse[at(lane)] : neg_inf();
+  float y[kFewPieces][N];
+#pragma unroll
+  for (int i = 0; i < kFewPieces; ++i)
+    if (i < pieces) *reinterpret_cast<Vec *>(y[i]) = *reinterpret_cast<const Vec *>(p.part_o + at(i) * D + N * lane);
+  float m = lse;
+#pragma unroll
+  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float w = ex2(lse - (m == neg_inf() ? 0.f : m));
+  float sum = w, x[N] = {};
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+  for (int i = 0; i < kFewPieces; ++i) {
+    const float f = __shfl_sync(0xffffffffu, w, i);
+    if (i < pieces)
+#pragma unroll
+      for (int k = 0; k < N; ++k) x[k] = fmaf(f, y[i][k], x[k]);
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int k = 0; k < N; ++k) x[k] *= inv;
+  const int tok = row / p.G;
+  const int64_t out = (int64_t(r.token0) + tok) * p.Hq + kv * p.G + (row - tok * p.G), o = out * D + N * lane;
+  if (p.out_f32) {
+    *reinterpret_cast<Vec *>(static_cast<float *>(p.o) + o) = *reinterpret_cast<const Vec *>(x);
+  } else {
+    __nv_bfloat162 z[N / 2];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) z[k] = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.o) + o;
+    if constexpr (N == 4) *reinterpret_cast<uint2 *>(to) = *reinterpret_cast<const uint2 *>(z);
+    else *reinterpret_cast<uint32_t *>(to) = *reinterpret_cast<const uint32_t *>(z);
+  }
+  if (lane == 0 && p.lse) p.lse[out] = sum == 0.f ? neg_inf() : m + log2f(sum);
+}
+
 // Joins the pieces of a row (request blockIdx.x, KV head blockIdx.y, row blockIdx.z): D / 4 threads a piece take every
 // NG-th of them, in an order that does not change.
 template <int D>
 __global__ void __launch_bounds__(256) rows_join_kernel(const RowsParams p, const __grid_constant__ RowsRequests req, int unit_rows) {
   constexpr int kLanes = D / 4, NG = 256 / kLanes;
   __shared__ float4 part[NG][kLanes];
-  __shared__ float tops[8], sums[NG];
+  constexpr int kAhead = 8;
+  __shared__ float tops[8], sums[8], weight[kMostPieces];
   const int b = blockIdx.x, kv = blockIdx.y, row = blockIdx.z, tid = threadIdx.x;
   const psd_token_request &r = req.r[b];
-  // The slots that have its first step and its last: slot x begins at cost floor(x C / slots), and all costs up to
-  // kSegmentCost behind the request's begin at its first step.
-  const int64_t all = req.before[p.B], n = steps_of(r);
-  const int64_t first = ((req.before[b] + kSegmentCost + 1) * p.slots - 1) / all;
-  const int pieces = int(min(int64_t(p.slots) - 1, ((req.before[b] + kSegmentCost + n) * p.slots - 1) / all) - first) + 1;
-  const int late = begin_of(p, req, int(first)).x < b;  // the first piece is the second of its slot
+  int64_t first;
+  const int pieces = pieces_of(p, req, b, first), late = begin_of(p, req, int(first)).x < b;  // the first piece is the second of its slot
   wait_for_prior_grid();
   if (pieces == 1 || row >= r.num_new * p.G) return;    // whole
-  auto at = [&](int i) { return (((first + i) * 2 + (i == 0 ? late : 0)) * p.Hkv + kv) * unit_rows + row; };
+  // (all pieces' numbers fit 31 bits: step_rows_floats)
+  const int stride = 2 * p.Hkv * unit_rows, at0 = int(first) * stride + kv * unit_rows + row, late_by = late * p.Hkv * unit_rows;
+  auto at = [&](int i) { return at0 + i * stride + (i == 0 ? late_by : 0); };
   const int group = tid / kLanes, col = tid % kLanes * 4;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-  if (group < pieces) y = *reinterpret_cast<const float4 *>(p.part_o + at(group) * D + col);  // on its way beside the LSEs
+  const float *piece = p.part_o + col;
+  float4 y[kAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)  // on their way beside the LSEs
+    if (group + k * NG < pieces) y[k] = *reinterpret_cast<const float4 *>(piece + at(group + k * NG) * D);
   float m = neg_inf();
-  for (int i = tid; i < pieces; i += 256) m = fmaxf(m, p.part_lse[at(i)]);
+  for (int i = tid; i < pieces; i += 256) {
+    weight[i] = p.part_lse[at(i)];
+    m = fmaxf(m, weight[i]);
+  }
 #pragma unroll
   for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
   if (tid % 32 == 0) tops[tid / 32] = m;
@@ -586,22 +664,38 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const RowsParams p, cons
   for (int w = 0; w < 8; ++w) m = fmaxf(m, tops[w]);
   const float from = m == neg_inf() ? 0.f : m;
   float sum = 0.f;
-  for (int i = group; i < pieces; i += NG) {
-    const float w = ex2(p.part_lse[at(i)] - from);
-    if (i != group) y = *reinterpret_cast<const float4 *>(p.part_o + at(i) * D + col);
+  for (int i = tid; i < pieces; i += 256) {
+    const float w = ex2(weight[i] - from);
+    weight[i] = w;
     sum += w;
-    x.x = fmaf(w, y.x, x.x), x.y = fmaf(w, y.y, x.y), x.z = fmaf(w, y.z, x.z), x.w = fmaf(w, y.w, x.w);
+  }
+#pragma unroll
+  for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (tid % 32 == 0) sums[tid / 32] = sum;
+  __syncthreads();
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = group; i0 < pieces; i0 += kAhead * NG) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const int i = i0 + k * NG;
+      if (i >= pieces) break;
+      const float w = weight[i];
+      const float4 z = y[k];
+      if (i + kAhead * NG < pieces) y[k] = *reinterpret_cast<const float4 *>(piece + at(i + kAhead * NG) * D);
+      x.x = fmaf(w, z.x, x.x), x.y = fmaf(w, z.y, x.y), x.z = fmaf(w, z.z, x.z), x.w = fmaf(w, z.w, x.w);
+    }
   }
   part[group][tid % kLanes] = x;
-  if (tid % kLanes == 0) sums[group] = sum;
   __syncthreads();
   if (group) return;
 #pragma unroll
   for (int k = 1; k < NG; ++k) {
     const float4 z = part[k][tid];
     x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
-    sum += sums[k];
   }
+  sum = sums[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) sum += sums[k];
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int tok = row / p.G;
   const int64_t out = (int64_t(r.token0) + tok) * p.Hq + kv * p.G + (row - tok * p.G), o = out * D + col;
@@ -616,7 +710,7 @@ __global__ void __launch_bounds__(256) rows_join_kernel(const RowsParams p, cons
 }
 
 // Slots for the workers of so many CTAs.
-int slots_of(int ctas, int Hkv) { return std::max(1, ctas * kWarps / Hkv); }
+int slots_of(int ctas, int Hkv) { return std::max(1, std::min(ctas * kWarps / Hkv, kMostPieces)); }
 
 template <int D, int NT, int TERMS>
 psd_status run(const StepParams &S, const StepRequests &sreq, float *base, const DeviceInfo &dev, cudaStream_t s) {
@@ -648,6 +742,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, float *base, const
   req.before[0] = 0;
   for (int b = 0; b < S.B; ++b) req.before[b + 1] = req.before[b] + steps_of(req.r[b]) + kSegmentCost;
   p.slots = int(std::max<int64_t>(1, std::min<int64_t>(slots_of(L::kCtasPerSm * dev.num_sms, S.Hkv), req.before[S.B] / kLeastSteps)));
+  p.narrow = (req.before[S.B] + 1) * (int64_t(p.slots) + 1) < int64_t(1) << 32;
   const int64_t ctas = (int64_t(p.slots) * S.Hkv + kWarps - 1) / kWarps;
   p.part_o = base;
   p.part_lse = base + int64_t(p.slots) * 2 * S.Hkv * 8 * NT * D;
@@ -665,17 +760,22 @@ psd_status run(const StepParams &S, const StepRequests &sreq, float *base, const
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode_scaled launch: %s", cudaGetErrorString(e));
   if (p.slots == 1) return PSD_OK;
   cudaLaunchConfig_t cfg = {};
-  int rows = 0;
-  for (int b = 0; b < S.B; ++b) rows = std::max(rows, req.r[b].num_new * S.G);
-  cfg.gridDim = dim3(unsigned(S.B), unsigned(S.Hkv), unsigned(rows));
-  cfg.blockDim = dim3(256);
+  int rows = 0, pieces = 0;
+  int64_t first;
+  for (int b = 0; b < S.B; ++b) {
+    rows = std::max(rows, req.r[b].num_new * S.G);
+    pieces = std::max(pieces, pieces_of(p, req, b, first));
+  }
+  const bool few = pieces <= kFewPieces;
+  cfg.gridDim = dim3(unsigned(S.B), unsigned(S.Hkv), unsigned(few ? (rows + 3) / 4 : rows));
+  cfg.blockDim = dim3(few ? 128 : 256);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, rows_join_kernel<D>, p, req, 8 * NT);
+  e = cudaLaunchKernelEx(&cfg, few ? rows_join_few_kernel<D> : rows_join_kernel<D>, p, req, 8 * NT);
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode_scaled join launch: %s", cudaGetErrorString(e));
   return PSD_OK;
 }
