@@ -11,13 +11,17 @@
 //   Candidates: each warp takes the r-th largest of its lanes' largest logits, r = ceil(k / 8); the least of the
 // 8 warps' is a lower bound of the k-th largest (8 r >= k logits are no smaller), found without a sort.  The pass keeps
 // each thread's largest of every tile; some 2 k of these are not below the bound, and only their 16 logits are read again.
-// Order numbers (a count of the larger ones) give the exact k.  So the pass is left with 6 instructions a logit; with a
-// bound and a search tile by tile it was 13.  Where more is found than there is room for (many equal logits) the CTA goes
+// Order numbers (a count of the larger ones) give the exact k.  So the pass is left with 9 instructions a logit; with a
+// bound and a search tile by tile 240 rows of 131072 bf16 took 34 us against 24.  Where more is found than there is room for (many equal logits) the CTA goes
 // over its logits again and thins them out on the way.
 //
 // Rows are split so that all SMs have equal work: the rows that are read (not finished, not empty) share the CTAs that run
 // at once, to within a split.  A second kernel, one CTA a request, joins the splits' sums and takes the k largest of the
 // rows' candidates in 64 bits.
+//
+// 128 rows of 98305 f32, a fifth of them finished: 18 us (40 MB, 6 us at the copy rate), 13 of them the pass; bound by the fixed part
+// of a CTA (680 instructions a warp, and a chain of dependent steps) and its 16000 logits in equal parts, then by the second
+// kernel's chain.  240 rows of 131072 bf16: 24 us (8 us at the copy rate), bound by instructions.
 #include <cuda_runtime.h>
 
 #include <algorithm>
