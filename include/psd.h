@@ -786,7 +786,8 @@ psd_status multi_token_decode_scaled(psd_ctx *ctx, const psd_multi_token_args *a
  * to the sum), and neither are rows whose score is -inf.  A row with a logit of +inf, a
  * score that is NaN or +inf, or whose sum overflows has none either and sets
  * PSD_FAULT_RANGE.  Where a request has fewer than k continuations the rest are -inf, -1,
- * -1.  rows == 0 is a no-op.
+ * -1.  rows == 0 is a no-op.  out_scores may be scores where k == beams (the next step's
+ * scores in place of this one's); no output may overlap scores otherwise, nor finished.
  * workspace: >= psd_beam_workspace_bytes(ctx, rows, beams, k) bytes, 16-byte aligned; calls
  * that may overlap need their own. */
 typedef enum { PSD_LOGITS_F32 = 0, PSD_LOGITS_BF16 = 1, PSD_LOGITS_F16 = 2 } psd_logits_type;

@@ -56,6 +56,8 @@ struct SelectParams {
   double *sums;              // [pieces] in units of 2^ref
   int2 *refs;                // [pieces] R's bits, and the row's number in its request
   unsigned long long *keys;  // [pieces][k] descending, 0: none
+  uint32_t *marks;           // the rows that are read, for calls that write the scores over those they had
+  bool in_place;
 };
 
 // Rows whose logits are read share the pieces: of L such rows the j-th has those from first(j) to first(j + 1).  (A NaN
@@ -179,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
     __syncthreads();
     int here, before;
     const Shares shares = share_rows(p, words, here, before);
+    if (p.in_place && piece == 0 && tid < kMostRanked / 32) p.marks[tid] = words[tid];
     if (piece >= shares.pieces) return;
     const int j = shares.row_of(piece), first = shares.first(j), splits = shares.first(j + 1) - first;
     const int word = __ffs(__ballot_sync(0xffffffffu, j >= before && j < before + here)) - 1;
@@ -454,7 +457,12 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   }
   if (tid == 0) n_shared = 0;
   if (p.most_splits > 1) {
-    mark_rows(p, words);
+    if (!p.in_place) {
+      mark_rows(p, words);
+    } else {  // (other requests' scores may have been written already)
+      wait_for_prior_grid();
+      if (tid < kMostRanked / 32) words[tid] = p.marks[tid];
+    }
     __syncthreads();
     if (warp < 3) {
       int here, before;
@@ -636,6 +644,8 @@ static psd_status launch_select(const psd_beam_args *a, void *workspace, const D
   p.sums = reinterpret_cast<double *>(at);
   p.keys = reinterpret_cast<unsigned long long *>(at + pieces * 8);
   p.refs = reinterpret_cast<int2 *>(at + pieces * 8 * (1 + size_t(a->k)));
+  p.marks = reinterpret_cast<uint32_t *>(p.refs + pieces);
+  p.in_place = a->out_scores == a->scores;
   const size_t size = a->logits_type == PSD_LOGITS_F32 ? 4 : 2;
   const bool vec = aligned16(a->logits) && (a->logits_stride * int64_t(size)) % 16 == 0;
   auto go = [&](auto type) {
@@ -694,6 +704,14 @@ extern "C" psd_status beam_select(psd_ctx *ctx, const psd_beam_args *a, void *wo
     return fail(PSD_ERR_INVALID_ARG, "beam_select: NULL pointer");
   if (reinterpret_cast<uintptr_t>(a->logits) % (a->logits_type == PSD_LOGITS_F32 ? 4 : 2))
     return fail(PSD_ERR_INVALID_ARG, "beam_select: logits alignment");
+  const int64_t outputs = int64_t(a->rows / a->beams) * a->k;
+  auto over_scores = [&](const void *out) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(out), y = reinterpret_cast<uintptr_t>(a->scores);
+    return x < y + uintptr_t(a->rows) * 4 && y < x + uintptr_t(outputs) * 4;
+  };
+  if (over_scores(a->out_rows) || over_scores(a->out_tokens) ||
+      (over_scores(a->out_scores) && !(a->out_scores == a->scores && a->k == a->beams)))
+    return fail(PSD_ERR_INVALID_ARG, "beam_select: outputs overlap scores (out_scores may be scores where k is beams)");
   if (!workspace || !aligned16(workspace)) return fail(PSD_ERR_INVALID_ARG, "beam_select: workspace must be 16-byte aligned");
   const size_t need = psd_beam_workspace_bytes(ctx, a->rows, a->beams, a->k);
   if (workspace_bytes < need) return fail(PSD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);

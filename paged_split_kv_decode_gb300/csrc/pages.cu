@@ -703,31 +703,30 @@ extern "C" size_t psd_pages_workspace_bytes(int64_t num_pages, int32_t num_new) 
   return lists_of(nullptr, nullptr, num_pages, num_new);
 }
 
-extern "C" psd_status fork_pages(psd_ctx *ctx, const psd_fork_args *a, void *workspace, size_t workspace_bytes,
-                                 psd_stream_t stream) {
+static psd_status fork_table(const char *what, psd_ctx *ctx, const psd_fork_args *a, void *workspace, size_t workspace_bytes, psd_stream_t stream) {
   clear_error();
-  if (!ctx || !a) return fail(PSD_ERR_INVALID_ARG, "fork_pages: NULL");
-  const psd_status st = check_pools("fork_pages", a->pools, a->num_pools, a->num_pages);
+  if (!ctx || !a) return fail(PSD_ERR_INVALID_ARG, "%s: NULL", what);
+  const psd_status st = check_pools(what, a->pools, a->num_pools, a->num_pages);
   if (st != PSD_OK) return st;
   if (a->num_new < 0 || a->batch < 0 || a->num_page_indices < 0 || a->new_capacity < 0 || a->page_size < 1 || a->room < 0)
-    return fail(PSD_ERR_INVALID_ARG, "fork_pages: bad sizes");
+    return fail(PSD_ERR_INVALID_ARG, "%s: bad sizes", what);
   if (a->num_new > (1 << 24) || a->num_page_indices > 0x7fffffffLL || a->new_capacity > 0x7fffffffLL)
-    return fail(PSD_ERR_UNSUPPORTED, "fork_pages: more than 2^24 new requests or 2^31 - 1 table entries");
-  if (!workspace || !aligned16(workspace)) return fail(PSD_ERR_INVALID_ARG, "fork_pages: workspace must be 16-byte aligned");
+    return fail(PSD_ERR_UNSUPPORTED, "%s: more than 2^24 new requests or 2^31 - 1 table entries", what);
+  if (!workspace || !aligned16(workspace)) return fail(PSD_ERR_INVALID_ARG, "%s: workspace must be 16-byte aligned", what);
   const size_t need = psd_pages_workspace_bytes(a->num_pages, a->num_new);
-  if (workspace_bytes < need) return fail(PSD_ERR_WORKSPACE_TOO_SMALL, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (workspace_bytes < need) return fail(PSD_ERR_WORKSPACE_TOO_SMALL, "%s: workspace %zu < %zu bytes", what, workspace_bytes, need);
   if (!a->ref_count || !a->new_ref_count || !a->fault_dev ||
       (a->batch > 0 && (!a->page_indptr || !a->kv_len || (a->num_page_indices > 0 && !a->page_indices))) ||
       (a->num_new > 0 && (!a->parents || !a->new_indptr || !a->new_len || (a->new_capacity > 0 && !a->new_indices))))
-    return fail(PSD_ERR_INVALID_ARG, "fork_pages: NULL pointer");
+    return fail(PSD_ERR_INVALID_ARG, "%s: NULL pointer", what);
   if (overlap(a->page_indices, a->num_page_indices, a->new_indices, a->new_capacity) ||
       overlap(a->page_indptr, int64_t(a->batch) + 1, a->new_indptr, int64_t(a->num_new) + 1) ||
       overlap(a->kv_len, a->batch, a->new_len, a->num_new) || overlap(a->parents, a->num_new, a->new_len, a->num_new) ||
       overlap(a->parents, a->num_new, a->new_indptr, int64_t(a->num_new) + 1) ||
       overlap(a->parents, a->num_new, a->new_indices, a->new_capacity))
-    return fail(PSD_ERR_INVALID_ARG, "fork_pages: the new table overlaps the old one or the parents");
+    return fail(PSD_ERR_INVALID_ARG, "%s: the new table overlaps the old one or the parents", what);
   if (a->ref_count != a->new_ref_count && overlap(a->ref_count, a->num_pages, a->new_ref_count, a->num_pages))
-    return fail(PSD_ERR_INVALID_ARG, "fork_pages: new_ref_count is ref_count, or apart from it");
+    return fail(PSD_ERR_INVALID_ARG, "%s: new_ref_count is ref_count, or apart from it", what);
   DeviceGuard g(ctx->dev.device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   ForkParams p = {};
@@ -780,6 +779,11 @@ extern "C" psd_status fork_pages(psd_ctx *ctx, const psd_fork_args *a, void *wor
   return launch_copy(c, a->pools, a->num_pools, a->room > 0 ? a->num_new : 0, true, ctx->dev, s);
 }
 
+extern "C" psd_status fork_pages(psd_ctx *ctx, const psd_fork_args *a, void *workspace, size_t workspace_bytes,
+                                 psd_stream_t stream) {
+  return fork_table("fork_pages", ctx, a, workspace, workspace_bytes, stream);
+}
+
 extern "C" psd_status free_pages(psd_ctx *ctx, const int32_t *page_indptr, const int32_t *page_indices, int64_t num_page_indices,
                                  int32_t batch, int32_t *ref_count, int64_t num_pages, int32_t *fault_dev, void *workspace,
                                  size_t workspace_bytes, psd_stream_t stream) {
@@ -794,7 +798,7 @@ extern "C" psd_status free_pages(psd_ctx *ctx, const int32_t *page_indptr, const
   a.new_ref_count = ref_count;
   a.num_pages = num_pages;
   a.fault_dev = fault_dev;
-  return fork_pages(ctx, &a, workspace, workspace_bytes, stream);
+  return fork_table("free_pages", ctx, &a, workspace, workspace_bytes, stream);
 }
 
 extern "C" psd_status compact_pages(psd_ctx *ctx, const psd_compact_args *a, void *workspace, size_t workspace_bytes,

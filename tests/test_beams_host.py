@@ -97,7 +97,8 @@ def _beam(L, **kw):
     (dict(rows=9), 1), (dict(rows=-4), 1), (dict(beams=0), 1), (dict(k=0), 1), (dict(vocab=0), 1), (dict(k=65), 2),
     (dict(beams=65, rows=65), 2), (dict(logits_type=3), 1), (dict(logits_type=-1), 1), (dict(logits_stride=99), 1),
     (dict(logits=None), 1), (dict(scores=None), 1), (dict(out_rows=None), 1), (dict(fault_dev=None), 1), (dict(logits=_ptr(1) + 2), 1),
-    (dict(logits=_ptr(1) + 1, logits_type=1), 1), (dict(vocab=(1 << 30) + 1, logits_stride=1 << 31), 2)])
+    (dict(logits=_ptr(1) + 1, logits_type=1), 1), (dict(vocab=(1 << 30) + 1, logits_stride=1 << 31), 2),
+    (dict(out_scores=_ptr(2)), 1), (dict(out_scores=_ptr(2) + 4, beams=8), 1), (dict(out_rows=_ptr(2) + 28), 1), (dict(out_tokens=_ptr(2)), 1)])
 def test_selection_refusals(lib, blank, args, status):
     from paged_split_kv_decode_gb300 import _lib as L
     assert lib.beam_select(blank, C.byref(_beam(L, **args)), _ptr(7), 1 << 40, None) == status

@@ -273,6 +273,21 @@ def test_two_streams_at_once():
         assert int(fault) == 0 and all(torch.equal(p, q) for p, q in zip(out, a))
 
 
+@pytest.mark.parametrize("rows,beams,vocab", [(256, 4, 9000), (1200, 4, 500), (8, 8, 50001)])
+def test_scores_in_place(rows, beams, vocab):
+    """The new scores written over the old ones: all requests are chosen from the old."""
+    x, s, done = _logits(rows, vocab, seed=70), _scores(rows), [bool(r % 5 == 2) for r in range(rows)]
+    s[::7] = -np.inf
+    want, _ = _run(x, s, beams, beams, finished=done)
+    flags, ws = torch.tensor(done, device="cuda"), psd.beam_workspace(ctx(), rows, beams, beams, "cuda")
+    for _ in range(20):
+        scores = torch.as_tensor(s.astype(np.float32)).cuda()
+        out = [scores.view(-1, beams)] + [torch.zeros((rows // beams, beams), dtype=torch.int32, device="cuda") for _ in range(2)]
+        psd.beam_select(ctx(), x, scores, *out, ws, beams=beams, finished=flags)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
 def test_no_rows():
     out = [torch.zeros((0, 4), dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
     psd.beam_select(ctx(), torch.zeros((0, 10), device="cuda"), torch.zeros(0, device="cuda"), *out,
