@@ -150,7 +150,7 @@ enum {
   T_DRAIN = T_XREADY + 2, T_SLOT, T_TAIL
 };
 // Behind the barriers, scales of key tiles: V's four bytes of 16 tiles (from the V loads to its conversion, at most eight
-// tiles), and four pairs of K's and V's of 32 (from the K loads to its conversion and the softmax: at most eight tiles of
+// tiles), and K's four and both largest of 32 (from the K loads to its conversion and the softmax: at most eight tiles of
 // codes, four of f16 and two that a slot may lag behind).
 constexpr uint32_t kVScaleOff = 704, kScaleOff = 768;
 constexpr int kVScaleTiles = 16, kScaleTiles = 32;
@@ -533,9 +533,22 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         const int64_t at = (slot >> p.scales.shift) * p.Hkv + u.kv;
         return uint32_t(__ldg(p.scales.k + at)) | uint32_t(__ldg(p.scales.v + at)) << 8;
       };
+      // K's and V's largest of the lane's tile, as the softmax takes them: 2^(k - 127) in f32, with V's byte as its low bits.
+      [[maybe_unused]] uint32_t tops = 0;
+      [[maybe_unused]] auto find_tops = [&]() {
+        uint32_t k = scales & 255u, v = scales >> 8 & 255u;
+        k = k == 255u ? 0u : k, v = v == 255u ? 0u : v;
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          k = max(k, __shfl_xor_sync(0xffffffffu, k, d));
+          v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
+        }
+        tops = k << 23 | v;
+      };
       if constexpr (SCALED) {
         ids = load_ids(u.j0);
         scales = load_scales(u.j0, ids);
+        find_tops();
       } else {
         id = next_id(), id_next = next_id();
       }
@@ -547,7 +560,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         int id_after = -1;
         if constexpr (SCALED) {
           const int x = (j - u.j0) & 7;
-          if (x == 0 && j > u.j0) ids = ids_after, scales = scales_after;
+          if (x == 0 && j > u.j0) {
+            ids = ids_after, scales = scales_after;
+            find_tops();
+          }
           if (x == 0) ids_after = load_ids(j + 8);
           if (x == 4) scales_after = load_scales(j + 4, ids_after);
           id = __shfl_sync(0xffffffffu, ids, 4 * x + (lane & 3));
@@ -560,11 +576,11 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           break;
         }
         if constexpr (SCALED) {  // (before the arrival: who has seen that has seen these)
-          const uint32_t w = __shfl_sync(0xffffffffu, scales, 4 * ((j - u.j0) & 7) + (lane & 3));
-          if (lane < 4) {
-            if (is_v) sm[L::kOffBar + kVScaleOff + (g & (kVScaleTiles - 1)) * 4 + lane] = uint8_t(w >> 8);
-            else *reinterpret_cast<uint16_t *>(sm + L::kOffBar + kScaleOff + (g & (kScaleTiles - 1)) * 8 + 2 * lane) = uint16_t(w);
-          }
+          const int x = 4 * ((j - u.j0) & 7);
+          const uint32_t w = __shfl_sync(0xffffffffu, scales, x + (lane & 3)), top = __shfl_sync(0xffffffffu, tops, x);
+          uint8_t *at = sm + L::kOffBar + (is_v ? kVScaleOff + (g & (kVScaleTiles - 1)) * 4 : kScaleOff + (g & (kScaleTiles - 1)) * 8);
+          if (lane < 4) at[lane] = uint8_t(is_v ? w >> 8 : w);
+          if (lane == 0 && !is_v) *reinterpret_cast<uint32_t *>(at + 4) = top;
           __syncwarp();
         }
         if (lane == 0) mbar_arrive_expect_tx(bar(kLanded + st), kCopied);
@@ -627,13 +643,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         __half2 by = __floats2half2_rn(1.f, 1.f);
         bool other = false;
         if constexpr (SCALED) {
-          uint32_t e4;  // the four bytes
-          if (v) {
-            e4 = *reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kVScaleOff + (g & (kVScaleTiles - 1)) * 4);
-          } else {
-            const volatile uint32_t *at = reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kScaleOff + (g & (kScaleTiles - 1)) * 8);
-            e4 = __byte_perm(at[0], at[1], 0x6420);
-          }
+          const uint32_t e4 = *reinterpret_cast<const volatile uint32_t *>(  // the four bytes
+              sm + L::kOffBar + (v ? kVScaleOff + (g & (kVScaleTiles - 1)) * 4 : kScaleOff + (g & (kScaleTiles - 1)) * 8));
           const int mine = int(e4 >> (8 * (th >> 5)) & 255u), down = mine - largest_scale(e4);
           other = down != 0;
           by = mine == 255 ? __float2half2_rn(scale_value(255)) : __float2half2_rn(down < -24 ? 0.f : ex2(float(down)));
@@ -954,9 +965,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         if constexpr (SCALED) {
           if (warp_live) {
             const int i = (g + (u.two ? t >> 1 : t)) & (kScaleTiles - 1);
-            const volatile uint32_t *w = reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kScaleOff + i * 8);
-            const uint32_t w0 = w[0], w1 = w[1];
-            const int ve = largest_scale(__byte_perm(w0, w1, 0x7531));
+            const uint32_t w = *reinterpret_cast<const volatile uint32_t *>(sm + L::kOffBar + kScaleOff + i * 8 + 4);
+            const int ve = int(w & 255u);
             if (ve > vref) {
               // S(t) is complete, so PV(t - 2), issued before it, is too
               if (!empty) {
@@ -975,9 +985,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             }
             if (vref == 0) vref = 1;  // (all of them 2^-127, or NaN: what O is multiplied by must not be 0)
             // (a normal number: times a score of -inf, 0 would be NaN)
-            tile_qs = fmaxf(qs * scale_value(uint32_t(largest_scale(__byte_perm(w0, w1, 0x6420)))), 0x1p-126f);
-            down = float(max(ve - vref, -64));
-            up = ex2(-down);
+            tile_qs = fmaxf(qs * __uint_as_float(w & ~255u), 0x1p-126f);
+            const int below = min(vref - ve, 64);
+            down = -float(below);
+            up = __uint_as_float(uint32_t(127 + below) << 23);
           }
         }
         auto give_part = [&](auto which) -> bool {
