@@ -27,7 +27,7 @@
 // their O joined in shared memory, that joining took more instructions than the steps.)
 //
 // Bound by DRAM in its steady state: 32 single tokens over 512 to 4096 keys (140 MB, 21 us at the copy rate) take 30 us without
-// the join and 34 with it; three over 20000 to 65536 with f32 outputs (27 us) 36 and 41.  The rest is the launch, the ramp
+// the join and 34 with it; three over 20000 to 65536 with f32 outputs (27 us) 36 and 42.  The rest is the launch, the ramp
 // to the first step and the slots' ends.
 #include <cuda_runtime.h>
 
@@ -501,9 +501,12 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
         }
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
+      for (int i = 0; i < kWords; ++i) {
+        // The tensor cores' sums cut low bits towards zero.  f32 outputs see that: a step's O starts anew, and is added in f32
+        // (three tokens over 20000 to 65536 keys: 2.5e-7 of the norm and 41.9 us, against 3.2e-7, most of it bias, and 41.2).
+        float now[TERMS > 1 ? NT : 1][2][4] = {};
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) {
+        for (int x = 0; x < 2; ++x) {
           uint32_t f[4], h[4];
           widen(v[x][i][0], f[0], f[1]);
           widen(v[x][i][1], f[2], f[3]);
@@ -513,10 +516,17 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int z = 0; z < TERMS; ++z) {
-              mma(o[nt][2 * i], f, pb[x][nt][z][0], pb[x][nt][z][1]);
-              mma(o[nt][2 * i + 1], h, pb[x][nt][z][0], pb[x][nt][z][1]);
+              mma(TERMS > 1 ? now[TERMS > 1 ? nt : 0][0] : o[nt][2 * i], f, pb[x][nt][z][0], pb[x][nt][z][1]);
+              mma(TERMS > 1 ? now[TERMS > 1 ? nt : 0][1] : o[nt][2 * i + 1], h, pb[x][nt][z][0], pb[x][nt][z][1]);
             }
         }
+        if constexpr (TERMS > 1) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[nt][2 * i + (k >> 2)][k & 3] += now[nt][k >> 2][k & 3];
+        }
+      }
       if (++stage == NS) stage = 0;
     }
 

@@ -164,6 +164,15 @@ def test_many_single_tokens():
     _check(_make([1] * 900, before, Hq=2, Hkv=1, seed=1), psd.rope_frequencies(64))
 
 
+def test_many_requests_without_tokens():
+    """Runs of requests without new tokens, longer than what a warp looks at at once."""
+    new, before = [], []
+    for n, gap in ((130, 40), (1, 33), (2, 70), (90, 31), (1, 32), (1, 0), (1, 100), (120, 64)):
+        new += [n] + [0] * gap
+        before += [7 * n % 50] + [5] * gap
+    _check(_make(new, before, Hq=2, Hkv=1, D=64, seed=61), psd.rope_frequencies(64))
+
+
 def test_keys_and_values_alone():
     s = _make(**RAGGED, seed=2)
     s["q"] = None
