@@ -118,3 +118,68 @@ def test_beams_over_scaled_blocks(D, page, block):
             assert np.all(np.abs(got - x) <= 1.07 * 2.0 ** -4 * np.abs(x) + 2.0 ** -9 * s + 1e-5)
     psd.free_pages(ctx(), table[0], table[1], ref, ws_pages, fault=fault)
     assert not ref.any() and int(fault) == 0
+
+
+@pytest.mark.parametrize("D,n_beams", [(64, 3), (128, 8)])
+def test_a_step_as_one_graph(D, n_beams):
+    """Selection, fork, append and attention captured together: a replay is the step anew, from the logits on."""
+    rng = np.random.default_rng(D)
+    B, W, Hq, Hkv, V, page, L0 = 2, n_beams, 8, 2, 3000, 16, 37
+    N, held, rope = B * W, 3, psd.rope_frequencies(D)
+    i32 = lambda a: torch.from_numpy(np.asarray(a).astype(np.int32)).cuda()  # noqa: E731
+    num_pages = N * held + N + 5
+    rows = [[2 * b, 2 * b + 1, 2 * B + r] for b in range(B) for r in range(b * W, (b + 1) * W)]   # two pages shared, one each
+    start = dict(k=torch.from_numpy(rng.integers(0, 120, (num_pages, page, Hkv, D)).astype(np.uint8)).cuda(),
+                 v=torch.from_numpy(rng.integers(0, 120, (num_pages, page, Hkv, D)).astype(np.uint8)).cuda(),
+                 ke=torch.full((num_pages, 1, Hkv), 118, dtype=torch.uint8, device="cuda"),
+                 ve=torch.full((num_pages, 1, Hkv), 119, dtype=torch.uint8, device="cuda"),
+                 ref=i32(np.bincount(np.array(rows).ravel(), minlength=num_pages)),
+                 scores=torch.from_numpy(rng.standard_normal(N).astype(np.float32)).cuda())
+    now = {k: t.clone() for k, t in start.items()}
+    logits = torch.zeros((N, V), device="cuda")
+    qkv = torch.from_numpy(rng.standard_normal((N, (Hq + 2 * Hkv) * D)).astype(np.float32)).to(torch.bfloat16).cuda()
+    q, k, v = (qkv[:, a * D: b * D].unflatten(1, (b - a, D)) for a, b in ((0, Hq), (Hq, Hq + Hkv), (Hq + Hkv, Hq + 2 * Hkv)))
+    out = [now["scores"].view(B, W)] + [torch.zeros((B, W), dtype=torch.int32, device="cuda") for _ in range(2)]
+    old = (i32(np.arange(N + 1) * held), i32(np.array(rows).ravel()), i32([L0] * N))
+    new = (i32([0] * (N + 1)), i32([0] * (N * held)), i32([0] * N))
+    cache, scales = psd.PagePools([now[x] for x in ("k", "v", "ke", "ve")]), psd.BlockScales(now["ke"], now["ve"], page)
+    ws_pages, ws_beam = psd.pages_workspace(cache, N, "cuda"), psd.beam_workspace(ctx(), N, W, W, "cuda")
+    plan = psd.plan_multi_token(psd.HostTable(np.arange(N + 1) * held, np.arange(N * held), [L0 + 1 - 32] * N, page), np.arange(N + 1), Hq, Hkv)
+    ws = psd.multi_token_workspace(ctx(), plan, D, "cuda")
+    q_rot, o, lse = torch.empty((N, Hq, D), dtype=torch.bfloat16, device="cuda"), torch.empty((N, Hq, D), device="cuda"), torch.empty((N, Hq), device="cuda")
+    q_indptr, fault = i32(np.arange(N + 1)), i32([0])
+
+    def step():
+        psd.beam_select(ctx(), logits, now["scores"], *out, ws_beam, beams=W, fault=fault)
+        psd.fork_pages(ctx(), cache, out[1].view(-1), page_indptr=old[0], page_indices=old[1], kv_len=old[2], page_size=page, room=1,
+                       ref_count=now["ref"], new_indptr=new[0], new_indices=new[1], new_len=new[2], workspace=ws_pages, fault=fault)
+        psd.append_tokens(ctx(), q, k, v, q_rot, q_indptr=q_indptr, kv_len=new[2], page_indptr=new[0], page_indices=new[1],
+                          k_pool=now["k"], v_pool=now["v"], rope=rope, neox=True, scales=scales, fault=fault)
+        psd.multi_token_decode(ctx(), psd.multi_token_args(q_rot, now["k"], now["v"], new[1], sm_scale=D ** -0.5, scales=scales), plan,
+                               o, lse, ws)
+
+    def again(seed):
+        for x, t in start.items():
+            now[x].copy_(t)
+        logits.copy_(torch.from_numpy(np.random.default_rng(seed).standard_normal((N, V)).astype(np.float32)))
+
+    def result():
+        torch.cuda.synchronize()
+        assert int(fault) == 0 and psd.check_device_error(ctx(), ws) == 0
+        return [t.clone() for t in (*out, *new, *now.values(), q_rot, o, lse)]
+
+    want = []
+    for seed in (1, 2, 3):
+        again(seed)
+        step()
+        want.append(result())
+    assert not torch.equal(want[0][1], want[1][1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        step()
+    for seed in (3, 1, 2):
+        again(seed)
+        g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(result(), want[seed - 1]))
