@@ -825,8 +825,9 @@ typedef struct {
  * and new_len[i] = L + room (0 for an empty one):
  *   - the floor(L / P) full pages of its parent, shared;
  *   - the part-full page, if L % P: shared where room == 0 (nothing will be written);
- *     otherwise the lowest child of all that have the page takes it, if no table entry but
- *     those that are let go refers to it, and every other gets a copy in a fresh page;
+ *     otherwise the lowest child of those whose part-full page it is takes it, if nothing else
+ *     refers to it (no table entry but those that are let go, and no child that has it as a
+ *     full page), and every other gets a copy in a fresh page;
  *   - fresh pages for the rest.  (Pages of the parent behind its L tokens are not handed
  *     down.)
  * Fresh pages are the lowest free ids once the old table has let go of its pages

@@ -69,6 +69,9 @@ def fork(parents, indptr, indices, kv_len, page, room, ref, keep_old=False):
         for g in indices[int(indptr[0]): int(indptr[-1])]:
             ref[int(g)] -= 1
     others, taken = list(ref), set()
+    for p in parents:                       # what a child holds as a full page nobody may write to
+        for j in range(int(kv_len[p]) // page if p >= 0 else 0):
+            others[int(indices[int(indptr[p]) + j])] += 1
     rows, lengths, fresh, copies = [], [], [], []
     for i, p in enumerate(parents):
         if p < 0:

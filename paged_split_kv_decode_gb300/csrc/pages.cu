@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <numeric>
 
 #include "context.h"
 #include "device.cuh"
@@ -141,9 +142,8 @@ struct Child {
   int first, full, want, len;  // first: of the parent's row; want < 0: the child is refused
   bool tail;
 };
-__device__ __forceinline__ Child child_of(const ForkParams &p, int i, uint32_t &faults) {
+__device__ __forceinline__ Child child_of(const ForkParams &p, int parent, uint32_t &faults) {
   Child c{0, 0, 0, 0, false};
-  const int parent = p.parents[i];
   if (parent == -1) return c;
   if (parent < 0 || parent >= p.B) {
     faults |= PSD_FAULT_RANGE;
@@ -178,7 +178,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
 
   // The children's wants; the counts to work on.
   long long want = 0;
-  for (int i = i0; i < i1; ++i) want += child_of(p, i, faults).want;
+  for (int i = i0; i < i1; ++i) want += child_of(p, p.parents[i], faults).want;
   const int64_t old_end = p.B > 0 ? p.indptr[p.B] : 0, old_begin = p.B > 0 ? p.indptr[0] : 0;
   if (old_begin < 0 || old_end < old_begin || old_end > p.num_indices) faults |= PSD_FAULT_RANGE;
   for (int64_t g = id; g < p.num_pages; g += kAll) {
@@ -192,7 +192,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
     for (int i = i0; i < i1; ++i) {
       uint32_t none = 0;
       p.w.start[i] = int(at);
-      at += child_of(p, i, none).want;
+      at += child_of(p, p.parents[i], none).want;
     }
   }
   if (total > p.capacity) faults |= PSD_FAULT_RANGE;
@@ -207,48 +207,54 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
     }
   team.scan(0, total, faults);
 
-  // A part-full page that nobody else refers to goes to its first child.
-  if (!faults) {
+  if (!faults)
     for (int64_t g = id; g < p.num_pages; g += kAll)
       if (__ldcg(p.w.count + g) < 0) faults |= PSD_FAULT_RANGE;  // referred to more often than counted
-    if (p.room)
-      for (int i = i0; i < i1; ++i) {
-        const Child c = child_of(p, i, faults);
-        if (!c.tail) continue;
-        const int g = p.indices[c.first + c.full];
-        if (g < 0 || g >= p.num_pages) faults |= PSD_FAULT_PAGE_ID;  // (behind the old table's end)
-        else if (__ldcg(p.w.count + g) == 0) atomicMin(p.w.first + g, i);
-      }
-  }
   team.scan(0, total, faults);
 
-  // Pages handed down are counted, those to be found are numbered.
-  auto keeps = [&](const Child &c, int i) {
-    return c.tail && (!p.room || __ldcg(p.w.first + p.indices[c.first + c.full]) == i);
-  };
+  // Pages handed down whoever else has them are counted.
   const int parts = max(1, kWarps / max(p.N, 1));  // warps a child
-  long long blanks = 0, all_blanks;
-  if (!faults) {
-    for (int i = i0; i < i1; ++i) {
-      const Child c = child_of(p, i, faults);
-      blanks += c.want - c.full - keeps(c, i);
-    }
+  if (!faults)
     for (int u = warp; u < p.N * parts; u += kWarps) {
-      const int i = u / parts;
-      const Child c = child_of(p, i, faults);
-      const int kept = c.full + keeps(c, i);
-      for (int j = (u % parts) * 32 + lane; j < kept; j += 32 * parts) {
+      const Child c = child_of(p, p.parents[u / parts], faults);
+      const int down = c.full + (c.tail && !p.room);
+      for (int j = (u % parts) * 32 + lane; j < down; j += 32 * parts) {
         const int g = p.indices[c.first + j];
-        if (g < 0 || g >= p.num_pages) faults |= PSD_FAULT_PAGE_ID;
+        if (g < 0 || g >= p.num_pages) faults |= PSD_FAULT_PAGE_ID;  // (behind the old table's end)
         else atomicAdd(p.w.count + g, 1);
       }
     }
-  }
+  team.scan(0, total, faults);
+
+  // A part-full page that will be written to, and that nothing else refers to (not as a full page either), goes to its first
+  // child.
+  if (!faults && p.room)
+    for (int i = i0; i < i1; ++i) {
+      const Child c = child_of(p, p.parents[i], faults);
+      if (!c.tail) continue;
+      const int g = p.indices[c.first + c.full];
+      if (g < 0 || g >= p.num_pages) faults |= PSD_FAULT_PAGE_ID;
+      else if (__ldcg(p.w.count + g) == 0) atomicMin(p.w.first + g, i);
+    }
+  team.scan(0, total, faults);
+
+  // Pages to be found are numbered.
+  auto keeps = [&](const Child &c, int i) {
+    return c.tail && (!p.room || __ldcg(p.w.first + p.indices[c.first + c.full]) == i);
+  };
+  long long blanks = 0, all_blanks;
+  if (!faults)
+    for (int i = i0; i < i1; ++i) {
+      const Child c = child_of(p, p.parents[i], faults);
+      const bool kept = keeps(c, i);
+      blanks += c.want - c.full - kept;
+      if (p.room && kept) p.w.count[p.indices[c.first + c.full]] = 1;
+    }
   {
     long long at = team.scan(blanks, all_blanks, faults);
     if (!faults)
       for (int i = i0; i < i1; ++i) {
-        const Child c = child_of(p, i, faults);
+        const Child c = child_of(p, p.parents[i], faults);
         const int kept = c.full + keeps(c, i);
         p.w.rows[i] = make_int4(c.first, kept, p.w.start[i], int(at));
         at += c.want - kept;
@@ -281,7 +287,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
   cluster_sync();
 
   for (int i = i0; i < i1; ++i) {
-    const Child c = child_of(p, i, faults);
+    const Child c = child_of(p, p.parents[i], faults);
     const int4 r = p.w.rows[i];
     p.new_indptr[i] = r.z;
     p.new_len[i] = c.want ? c.len + p.room : 0;
@@ -297,8 +303,9 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
 // The same by one CTA with the counts in shared memory, for up to kFewChildren children, kFewPages pages and
 // kFewEntries new entries: its barriers and atomics take tens of cycles where the cluster's take hundreds.  Counts and the old
 // table come by asynchronous copies while the children are looked up (with a load at a time the kernel took 20 us where it
-// takes 14, caches cold).  It is bound by the latency of what depends on what, and one SM's atomics a table entry.  A
-// whole call, copies included: 4 children of 40 pages 8 us against 20; 128 of some 150 among 20000 pages 21 us against 32.
+// takes 11, caches cold).  It is bound by one SM's atomics, one or two a table entry and 6 to 9 cycles for 32 of them, and by
+// the latency of what depends on what.  A whole call, copies included: 4 children of 40 pages 8 us against 20; 128 of some
+// 150 pages each 19 us against 32.
 constexpr int kFewChildren = 1024, kFewPages = 49152, kFewEntries = (1 << 21) - 2;
 
 __device__ __forceinline__ int block_scan(int v, int &total, int *sums) {  // the sum over the threads before
@@ -327,10 +334,10 @@ __device__ __forceinline__ int block_scan(int v, int &total, int *sums) {  // th
 constexpr int kRun = 128;  // pages of a warp's turn, four a lane
 constexpr size_t kFewShared = 227 * 1024 - 1024;
 size_t few_shared(int64_t num_pages, int num_new, int64_t num_indices) {
-  const size_t least = size_t((num_pages + kRun - 1) / kRun * kRun) * 4 + size_t(num_new) * 16;
+  const size_t least = size_t((num_pages + kRun - 1) / kRun * kRun) * 4 + size_t(num_new + 1) / 2 * 16;
   return std::min(kFewShared, least + size_t(num_indices) * 4 + 16);
 }
-static_assert(kFewPages % kRun == 0 && kFewPages * 4 + kFewChildren * 16 <= kFewShared, "counts and rows fit");
+static_assert(kFewPages % kRun == 0 && kFewPages * 4 + kFewChildren * 8 <= kFewShared, "counts and rows fit");
 
 __device__ __forceinline__ uint32_t shared_address(const void *at) { return uint32_t(__cvta_generic_to_shared(at)); }
 // n numbers to shared memory, without waiting: 16 bytes at a time where both lie so, all threads.
@@ -345,20 +352,22 @@ __device__ __forceinline__ void bring(int *dst, const int32_t *src, int n) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_address(dst + i)), "l"(src + i) : "memory");
 }
 
-__global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams p, int shared_entries) {
+__global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams p, int shared_entries, int spread) {
   extern __shared__ __align__(16) int count[];  // [num_pages], then the rows, then the entries
   __shared__ int sums[32], n_moves;
   const int padded = int((p.num_pages + kRun - 1) / kRun * kRun);
-  int4 *rows = reinterpret_cast<int4 *>(count + padded);
+  int2 *rows = reinterpret_cast<int2 *>(count + padded);
   dependents_may_launch();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_pages = int(p.num_pages);
   uint32_t faults = 0;
   int total;
   // The counts and the old table's entries are on their way while the children are looked up.
+  int old_end = p.B > 0 ? p.indptr[p.B] : 0, old_begin = p.B > 0 ? p.indptr[0] : 0;
+  const int parent = tid < p.N ? p.parents[tid] : -1;
   bring(count, p.ref, n_pages);
   if (tid == 0) n_moves = 0;
   for (int g = n_pages + tid; g < padded; g += kThreads) count[g] = 1;
-  int old_end = p.B > 0 ? p.indptr[p.B] : 0, old_begin = p.B > 0 ? p.indptr[0] : 0;
+  const Child looked_up = child_of(p, parent, faults);
   if (old_begin < 0 || old_end < old_begin || old_end > p.num_indices) {
     faults |= PSD_FAULT_RANGE;
     old_begin = old_end = 0;
@@ -367,12 +376,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
   int before = int(reinterpret_cast<uintptr_t>(p.indices + old_begin) / 4 & 3);
   if (before > old_begin) before = 0;
   const bool staged = old_end - old_begin <= shared_entries - before;
-  int *entries = reinterpret_cast<int *>(rows + p.N);
+  int *entries = reinterpret_cast<int *>(rows + (p.N + 1) / 2 * 2);
   if (staged) bring(entries, p.indices + (old_begin - before), old_end - old_begin + before);
   const int *entry0 = entries + before - old_begin;
   auto entry = [&](int e) { return staged && e >= old_begin && e < old_end ? entry0[e] : p.indices[e]; };
-  Child c{0, 0, 0, 0, false};
-  if (tid < p.N) c = child_of(p, tid, faults);
+  Child c = looked_up;
   // (of wants that do not fit into the new table the sum only has to stay too large)
   const int start = block_scan(int(min(int64_t(c.want), p.capacity + 1)), total, sums);
   if (total > p.capacity) faults |= PSD_FAULT_RANGE;
@@ -398,13 +406,18 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
     tail = entry(c.first + c.full);
     if (tail < 0 || tail >= n_pages) faults |= PSD_FAULT_PAGE_ID, c.tail = false;
   }
+  if (tid < p.N) rows[tid] = make_int2(c.first, c.full + (c.tail && !p.room));  // what is handed down whoever else has it
   // The old requests let go of their pages.
+  auto let_go = [&](const int *at, int n) {
 #pragma unroll 4
-  for (uint32_t e = old_begin + tid; e < uint32_t(old_end); e += kThreads) {
-    const int g = staged ? entry0[e] : p.indices[e];
-    if (g < 0 || g >= n_pages) faults |= PSD_FAULT_PAGE_ID;
-    else if (p.release) atomicSub(count + g, 1);
-  }
+    for (uint32_t e = tid; e < uint32_t(n); e += kThreads) {
+      const int g = at[e];
+      if (uint32_t(g) >= uint32_t(n_pages)) faults |= PSD_FAULT_PAGE_ID;
+      else if (p.release) atomicSub(count + g, 1);
+    }
+  };
+  if (staged) let_go(entries + before, old_end - old_begin);
+  else let_go(p.indices + old_begin, old_end - old_begin);
   __syncthreads();
   int4 *const count4 = reinterpret_cast<int4 *>(count);
   for (int k = tid; k < padded / 4; k += kThreads) {
@@ -416,7 +429,26 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
     give_up();
     return;
   }
-  // A part-full page that nobody else refers to goes to its first child: the least child, below 0, stands in its count.
+  // Pages handed down are counted.
+  const int parts = max(1, kThreads / 32 / max(p.N, 1));  // warps a child
+  // (Children that share pages, neighbours mostly, are not taken at the same time: their atomics would meet.)
+  for (int x = warp; x < p.N * parts; x += kThreads / 32) {
+    const int u = parts == 1 ? x * spread % p.N : x;
+    const int2 r = rows[parts == 1 ? u : u / parts];
+    auto take = [&](const int *at) {  // (in shared memory a third of the instructions)
+#pragma unroll 1
+      for (int j = (parts == 1 ? 0 : u % parts) * 32 + lane; j < r.y; j += 32 * parts) {
+        const int g = at[j];
+        if (uint32_t(g) >= uint32_t(n_pages)) faults |= PSD_FAULT_PAGE_ID;  // (behind the old table's end)
+        else atomicAdd(count + g, 1);
+      }
+    };
+    if (staged && r.x >= old_begin && r.x + r.y <= old_end) take(entries + before + (r.x - old_begin));
+    else take(p.indices + r.x);
+  }
+  __syncthreads();
+  // A part-full page that will be written to, and that nothing else refers to (not as a full page either), goes to its first
+  // child: the least child, below 0, stands in its count.
   const bool claims = c.tail && p.room && count[tail] == 0;
   __syncthreads();
   if (claims) atomicMin(count + tail, tid - kFewChildren);
@@ -425,24 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) fork_few_kernel(const ForkParams 
   const bool kept_tail = c.tail && (!p.room || mine), copies = c.tail && !kept_tail;
   const int move = copies ? atomicAdd(&n_moves, 1) : 0;  // (the order of the moves shows nowhere)
   __syncthreads();
-  if (mine) count[tail] = 0;
+  if (mine) count[tail] = 1;
   const int kept = c.full + kept_tail;
   int all_blanks;
-  const int blank = block_scan(c.want - kept, all_blanks, sums);
-  if (tid < p.N) rows[tid] = p.w.rows[tid] = make_int4(c.first, kept, start, blank);
-  __syncthreads();
-  // Pages handed down are counted.
-  const int parts = max(1, kThreads / 32 / max(p.N, 1));  // warps a child
-  for (int u = warp; u < p.N * parts; u += kThreads / 32) {
-    const int4 r = rows[u / parts];
-#pragma unroll 4
-    for (int j = (u % parts) * 32 + lane; j < r.y; j += 32 * parts) {
-      const int g = entry(r.x + j);
-      if (g < 0 || g >= n_pages) faults |= PSD_FAULT_PAGE_ID;  // (behind the old table's end)
-      else atomicAdd(count + g, 1);
-    }
-  }
-  __syncthreads();
+  const int blank = block_scan(c.want - kept, all_blanks, sums);  // (with barriers: the counts are complete)
+  if (tid < p.N) p.w.rows[tid] = make_int4(c.first, kept, start, blank);
   // The free pages, lowest first: a warp has a stretch of them, kRun at a time.
   const int runs = padded / kRun, each = (runs + 31) / 32, run0 = warp * each, run1 = min(runs, run0 + each);
   int free_pages = 0;
@@ -759,7 +778,9 @@ static psd_status fork_table(const char *what, psd_ctx *ctx, const psd_fork_args
       ready.fetch_or(bit, std::memory_order_release);
     }
     const size_t shared = few_shared(a->num_pages, a->num_new, a->num_page_indices), least = few_shared(a->num_pages, a->num_new, 0);
-    fork_few_kernel<<<1, kThreads, shared, s>>>(p, int((shared - least + 16) / 4));
+    int spread = std::max(1, a->num_new * 3 / 8);
+    while (std::gcd(spread, a->num_new) > 1) ++spread;
+    fork_few_kernel<<<1, kThreads, shared, s>>>(p, int((shared - least + 16) / 4), spread);
   } else {
     fork_kernel<<<kCtas, kThreads, 0, s>>>(p);
   }

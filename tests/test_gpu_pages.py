@@ -105,6 +105,32 @@ def test_pages_behind_the_tokens_are_let_go(extra):
     check_fork(c, [1, 0], 3)
 
 
+@pytest.mark.parametrize("parents", [[0, 1], [1, 0], [1], [1, 1], [1, 2, 0], [2, 1, 1, 0, 2]])
+@pytest.mark.parametrize("room", [0, 1, 20])
+@BOTH
+def test_pages_full_for_one_and_part_full_for_another(room, parents, extra):
+    """Requests that went back (their last tokens dropped) share a page that is full for another: its holder's tokens stay."""
+    check_fork(Cache([32, 20, 25], 16, shared=2, extra=extra, seed=50), parents, room)
+    c = Cache([32, 20, 25], 16, shared=2, extra=extra, seed=51)
+    if 0 in parents and 1 in parents and room:                        # no page of one child is written to by another
+        _, out, _ = run_fork(c, parents, room)
+        table, indptr, lens = out["new_indices"].tolist(), out["new_indptr"].tolist(), out["new_len"].tolist()
+        for i, p in enumerate(parents):
+            write = {table[indptr[i] + t // 16] for t in range(lens[i] - room, lens[i])}
+            for j in range(len(parents)):
+                assert j == i or not write & set(table[indptr[j]: indptr[j + 1]])
+
+
+@pytest.mark.parametrize("keep_old", [False, True])
+@pytest.mark.parametrize("seed", range(4))
+@BOTH
+def test_requests_that_went_back(seed, keep_old, extra):
+    rng = np.random.default_rng(seed)
+    lengths = [int(n) for n in rng.integers(1, 120, 40)]
+    c = Cache(lengths, 16, shared=5, spare_pages=int(rng.integers(2)), extra=extra + 300, seed=60 + seed)
+    check_fork(c, [int(p) for p in rng.integers(-1, 40, 60)], int(rng.integers(0, 30)), keep_old=keep_old)
+
+
 @pytest.mark.parametrize("parents", [[], [-1, -1], [0]])
 @BOTH
 def test_few_and_none(parents, extra):
