@@ -48,6 +48,7 @@ constexpr int kHalf = 16, kStep = 2 * kHalf;  // keys
 constexpr float kLazy = 8.f, kBias = 7.f;  // log2 units: P's top is 2^7, and grows to 2^15 at most
 constexpr int kSegmentCost = 2;  // of a request beside its steps, in steps
 constexpr int kLeastSteps = 1;   // of a slot (3: 4 tokens over 60 to 400 keys took 9.9 us against 7.8)
+constexpr int kJoinSteps = 4;    // what joining takes, in steps
 constexpr int kMostPieces = 2048; // slots at most
 constexpr int kFewPieces = 16;   // that a warp joins by itself
 
@@ -79,6 +80,7 @@ struct RowsParams {
   float q_scale;
   int B, slots;
   bool narrow;  // the line's length times the slots fits 32 bits
+  bool whole;   // slot x has request x
 };
 // A launch's requests, and what those before each cost: their steps, and kSegmentCost each.
 struct RowsRequests {
@@ -93,6 +95,7 @@ __host__ __device__ __forceinline__ int64_t divide(const RowsParams &p, int64_t 
 }
 // The request and step at which slot `x` begins.
 __device__ __forceinline__ int2 begin_of(const RowsParams &p, const RowsRequests &req, int x) {
+  if (p.whole) return make_int2(x, 0);
   const int64_t want = divide(p, x * req.before[p.B], p.slots);
   int b = 0;
   for (int n = p.B; n > 1;) {  // the last request with before <= want
@@ -751,7 +754,14 @@ psd_status run(const StepParams &S, const StepRequests &sreq, float *base, const
   std::memcpy(req.r, sreq.r, sizeof(psd_token_request) * size_t(S.B));
   req.before[0] = 0;
   for (int b = 0; b < S.B; ++b) req.before[b + 1] = req.before[b] + steps_of(req.r[b]) + kSegmentCost;
-  p.slots = int(std::max<int64_t>(1, std::min<int64_t>(slots_of(L::kCtasPerSm * dev.num_sms, S.Hkv), req.before[S.B] / kLeastSteps)));
+  const int most = slots_of(L::kCtasPerSm * dev.num_sms, S.Hkv);
+  p.slots = int(std::max<int64_t>(1, std::min<int64_t>(most, req.before[S.B] / kLeastSteps)));
+  // A slot for each request, and nothing to join, where that takes no longer: 4 requests of 64 keys 4.9 us against 6.4, 50 of
+  // 128 8.4 against 11.7; of 256 keys (8 steps) 9.8 against 7.0, and 12.8 against 13.8.
+  int longest = 0;
+  for (int b = 0; b < S.B; ++b) longest = std::max(longest, steps_of(req.r[b]));
+  p.whole = S.B <= most && longest <= req.before[S.B] / p.slots + kJoinSteps;
+  if (p.whole) p.slots = S.B;
   p.narrow = (req.before[S.B] + 1) * (int64_t(p.slots) + 1) < int64_t(1) << 32;
   const int64_t ctas = (int64_t(p.slots) * S.Hkv + kWarps - 1) / kWarps;
   p.part_o = base;
@@ -768,7 +778,7 @@ psd_status run(const StepParams &S, const StepRequests &sreq, float *base, const
   kern<<<unsigned(ctas), kThreads, L::kSmem, s>>>(p, req);
   e = cudaGetLastError();
   if (e != cudaSuccess) return fail(PSD_ERR_CUDA, "multi_token_decode_scaled launch: %s", cudaGetErrorString(e));
-  if (p.slots == 1) return PSD_OK;
+  if (p.slots == 1 || p.whole) return PSD_OK;
   cudaLaunchConfig_t cfg = {};
   int rows = 0, pieces = 0;
   int64_t first;

@@ -82,6 +82,14 @@ def test_many_requests(out_f32):
     _check(Scaled(new, [int(x) for x in rng.integers(1, 80, 300)], Hq=4, Hkv=2, seed=4), out_f32=out_f32)
 
 
+@pytest.mark.parametrize("B,keys", [(1, 30), (1, 160), (1, 200), (60, 100), (20, 700), (200, 260), (256, 33), (3, 900)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_requests_that_are_cut_or_not(D, B, keys):
+    """Equal and nearly equal requests: short ones and many of them are not cut, long ones are."""
+    rng = np.random.default_rng(B)
+    _check(Scaled([1] * B, [keys - int(x) for x in rng.integers(0, 20, B)], Hq=8, Hkv=2, D=D, seed=B), out_f32=bool(B % 2))
+
+
 def test_prompt_and_single_tokens():
     _check(Scaled([1, 500, 1, 2], [700, 150, 33, 0], Hq=4, Hkv=1, D=128, seed=7))
     _check(Scaled([1, 500, 1, 2], [700, 150, 33, 0], Hq=4, Hkv=1, D=128, seed=7), out_f32=True)
