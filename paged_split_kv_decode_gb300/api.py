@@ -442,7 +442,9 @@ def _ctx_stream(ctx: Context, stream):
 # Grace host; 35 ctypes field stores take 6) and asks a tensor for its device by get_device().
 _APPEND = struct.Struct("@PPPqqqP9iPd5PqPPqiiffP")
 _VERIFY = struct.Struct("@PPqqPPPiiiPPP")
+_DECODE = struct.Struct("@PqPPPqq6i3fPi0P")
 assert _APPEND.size == C.sizeof(L.AppendArgs) and _VERIFY.size == C.sizeof(L.VerifyArgs)
+assert _DECODE.size == C.sizeof(L.MultiTokenArgs)
 
 
 def _refuse(t, name: str, dtype, dev: int):
@@ -631,11 +633,11 @@ def multi_token_args(q, k_pool, v_pool, page_indices_dev, *, sm_scale: float, k_
         raise ValueError("k_pool and v_pool must be alike, [num_pages, page_size, Hkv, D]")
     if tree_mask is not None and (tree_mask.dtype is not torch.int64 or tree_mask.numel() != T):
         raise ValueError("tree_mask must be int64 [T]")
-    a = L.MultiTokenArgs(
-        q.data_ptr(), stride, _flat(k_pool, "k_pool", pool_type, dev), _flat(v_pool, "v_pool", pool_type, dev),
-        _flat(page_indices_dev, "page_indices", torch.int32, dev), page_indices_dev.numel(), pool_shape[0], T, Hq,
-        pool_shape[2], D, pool_shape[1], kv_dtype_code(k_pool), k_scale, v_scale, sm_scale,
-        None if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, dev), 0)
+    fields = (q.data_ptr(), stride, _flat(k_pool, "k_pool", pool_type, dev), _flat(v_pool, "v_pool", pool_type, dev),
+              _flat(page_indices_dev, "page_indices", torch.int32, dev), page_indices_dev.numel(), pool_shape[0], T, Hq,
+              pool_shape[2], D, pool_shape[1], kv_dtype_code(k_pool), k_scale, v_scale, sm_scale,
+              0 if tree_mask is None else _flat(tree_mask, "tree_mask", torch.int64, dev), 0)
+    a = L.MultiTokenArgs.from_buffer_copy(_DECODE.pack(*fields))
     if scales is not None:
         scales.fit(pool_shape, dev)
     a.tensors, a.device, a.scales = (q, k_pool, v_pool, page_indices_dev, tree_mask), dev, scales
