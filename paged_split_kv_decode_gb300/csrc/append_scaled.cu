@@ -172,20 +172,35 @@ __device__ __forceinline__ void rotate(F8 &a, F8 &b, const float *c, const float
 
 // The angles of tokens from .. n - 1 into `cosine` and `sine`, all kThreads threads; `freq`: the turns per position, in shared
 // memory (lanes that read different parameters of a launch wait for each other).
-__device__ __forceinline__ void make_angles(const int *pos, int from, int n, int half, const uint64_t *freq, float magnitude, float *cosine,
-                                            float *sine) {
+struct Deal {  // of (token, pair) to the threads: the first, and the way to the next
+  int m, k, step, rest;
+  __device__ __forceinline__ explicit Deal(int half) : m(0), k(0), step(1), rest(0) {
+    if (half == 0) return;
+    step = kThreads / half, rest = kThreads - step * half;
+    m = int(threadIdx.x) / half, k = int(threadIdx.x) - m * half;
+  }
+};
+__device__ __forceinline__ void make_angles(const Deal &deal, const int *pos, int from, int n, int half, const uint64_t *freq, float magnitude,
+                                            float *cosine, float *sine) {
   if (half == 0) return;
-  const int step = kThreads / half, rest = kThreads - step * half;
-  int m = int(threadIdx.x) / half, k = int(threadIdx.x) - m * half;
-  for (m += from; m < n; m += step) {
+  int k = deal.k;
+  for (int m = deal.m + from; m < n; m += deal.step) {
     const float2 cs = pos[m] >= 0 ? short_turn(freq[k], pos[m], magnitude) : make_float2(0.f, 0.f);
     const int at = m * half + angle_at(k, half);
     cosine[at] = cs.x;
     sine[at] = cs.y;
-    k += rest;
+    k += deal.rest;
     if (k >= half) k -= half, ++m;
   }
 }
+// A warp's lanes among the tokens of a block: D / 16 a token.
+struct Lanes {
+  int a_pass, mine, k;  // tokens a pass; the lane's token of a pass and its place in it
+  __device__ __forceinline__ explicit Lanes(int width) {
+    const int lane = threadIdx.x & 31, lanes = (width + 15) / 16;
+    a_pass = 32 / lanes, mine = lane / lanes, k = lane - mine * lanes;
+  }
+};
 // A thread's place in a token's query heads: a group of pairs, or a run that is not rotated.
 struct Column {
   int at;       // of the first run of 8 (element in the token's row)
@@ -237,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, kQueryCtas) append_queries_kernel(co
   }
   __syncthreads();
   float *cosine = table, *sine = table + n * half;
-  make_angles(pos, 0, n, half, freq, p.magnitude, cosine, sine);
+  make_angles(Deal(half), pos, 0, n, half, freq, p.magnitude, cosine, sine);
   __syncthreads();
   // (q_out may be q: both runs of a group are read before either is written)
   for (int job = tid; job < jobs; job += kThreads) {
@@ -312,21 +327,21 @@ __device__ __forceinline__ uint32_t fill(const ScaledParams &s, int t0, int own,
   if (lane == 0) tile.n_table = most, tile.n_starts = __popc(who);
   return faults;
 }
-// The rows of K or V, as far as the CTA's own tokens go, to the second-level cache.
-__device__ __forceinline__ void prefetch_rows(const AppendParams &p, bool is_v, int t0, int own, int id, int threads) {
-  const int bytes = (is_v ? p.Dv : p.D) * p.Hkv * 2;
+// The rows of K or V, as far as the CTA's own tokens go, to the second-level cache; all threads, 16 a row.
+__device__ __forceinline__ void prefetch_rows(const AppendParams &p, bool is_v, int t0, int own) {
+  const int bytes = (is_v ? p.Dv : p.D) * p.Hkv * 2, n = min(own, p.T - t0);
   const int64_t stride = 2 * (is_v ? p.v_stride : p.k_stride);
-  const uint8_t *row = reinterpret_cast<const uint8_t *>(is_v ? p.v : p.k) + t0 * stride;
-  for (int n = min(own, p.T - t0); n > 0; --n, row += stride)
-    for (int at = 128 * id; at < bytes; at += 128 * threads) prefetch_l2(row + at);
+  for (int row = threadIdx.x / 16; row < n; row += kThreads / 16)
+    for (int at = 128 * (threadIdx.x % 16); at < bytes; at += 128 * 16)
+      prefetch_l2(reinterpret_cast<const uint8_t *>(is_v ? p.v : p.k) + (t0 + row) * stride + at);
 }
 
 // The blocks that begin in a tile: K of head h, or V of it, a warp each.  A lane has two runs of 8 columns of a token, up to
 // kPasses tokens at once.  K's angles are made by all kWarps warps, a barrier behind them, while the first block's rows are on
 // their way: `joined` is that barrier.
 template <int NT, bool NEOX, typename Barrier>
-__device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64_t *freq, const Tile<NT> &tile, int t0, bool is_v, float *table,
-                                             Barrier joined) {
+__device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64_t *freq, const Deal &deal, const Lanes &lanes, const Tile<NT> &tile, int t0,
+                                             bool is_v, float *table, Barrier joined) {
   constexpr int kPasses = 4;
   const AppendParams &p = s.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -339,12 +354,11 @@ __device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64
   auto angles = [&]() {
     if (ready) return;
     const int from = n_starts == 0 ? nt : tile.starts[0];  // (tokens before the first block's begin are another CTA's)
-    make_angles(pos, from, nt, half, freq, p.magnitude, cosine, sine);
+    make_angles(deal, pos, from, nt, half, freq, p.magnitude, cosine, sine);
     joined();
     ready = true;
   };
-  const int lanes = (W + 15) / 16, a_pass = 32 / lanes;  // lanes a token, tokens a pass
-  const int mine = lane / lanes, k = lane - mine * lanes;
+  const int a_pass = lanes.a_pass, mine = lanes.mine, k = lanes.k;
   for (int start = 0, h = warp;; h += kWarps) {
     while (h >= p.Hkv && start < n_starts) h -= p.Hkv, ++start;
     if (start >= n_starts) break;
@@ -474,20 +488,23 @@ __global__ void __launch_bounds__(kThreads, kBlockCtas) append_blocks_kernel(con
   for (int k = threadIdx.x; k < p.rot / 2; k += kThreads) freq[k] = turns.f[k];
   dependents_may_launch();  // the queries
   const int items = 2 * ((p.T - 1) / kMany + 1), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = gridDim.x;
+  const Deal deal(p.rot / 2);
+  const Lanes of_k(p.D), of_v(p.Dv);
   int turn = 0;
   for (int item = blockIdx.x; item < items; item += step, ++turn) {
     __syncthreads();  // the table and the tile before are free
     if (turn % kWarps == 0) {
       const int64_t mine = item + int64_t(warp) * step;
       if (mine < items) {
-        const bool is_v = (mine + warp) & 1;
-        prefetch_rows(p, is_v, int(mine / 2) * kMany, kMany, lane, 32);
         const uint32_t faults = fill(s, int(mine / 2) * kMany, kMany, tiles[warp]);
-        if (faults && lane == 0 && !is_v) atomicOr(p.fault, int32_t(faults));
+        if (faults && lane == 0 && !((mine + warp) & 1)) atomicOr(p.fault, int32_t(faults));
       }
       __syncthreads();
     }
-    write_blocks<kMany, NEOX>(s, freq, tiles[turn % kWarps], item / 2 * kMany, (item + turn) & 1, table, [] { __syncthreads(); });
+    const bool is_v = (item + turn) & 1;
+    // (one tile ahead: with all tiles' rows asked for at the start, the first places took 6 us to be found)
+    if (item + step < items) prefetch_rows(p, (item + step + turn + 1) & 1, (item + step) / 2 * kMany, kMany);
+    write_blocks<kMany, NEOX>(s, freq, deal, is_v ? of_v : of_k, tiles[turn % kWarps], item / 2 * kMany, is_v, table, [] { __syncthreads(); });
   }
 }
 
@@ -512,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_few_kernel(const ScaledPar
     qa = load_raw(at);
     if (c.group >= 0) qb = load_raw(at + far);
   };
-  if (part < 2) prefetch_rows(p, part == 1, t0, 1, tid, kThreads);
+  if (part < 2) prefetch_rows(p, part == 1, t0, 1);
   else if (tid < jobs) fetch_q();
   if (warp == 0) {
     const uint32_t faults = fill(s, t0, 1, tile);
@@ -520,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_few_kernel(const ScaledPar
   }
   __syncthreads();
   if (part < 2) {
-    write_blocks<1, NEOX>(s, freq, tile, t0, part == 1, table, [] { __syncthreads(); });
+    write_blocks<1, NEOX>(s, freq, Deal(half), Lanes(part ? p.Dv : p.D), tile, t0, part == 1, table, [] { __syncthreads(); });
     return;
   }
   // (q_out may be q: both runs of a group are read before either is written)
