@@ -9,7 +9,7 @@
 // every block has one writer, whatever the lengths, without a list of blocks and without atomics on scales.  A warp takes one
 // block of one head's K or V, D / 16 lanes a token, and keeps the rotated values between finding the scale and writing the
 // codes (blocks of 16 tokens up to 128 columns; larger ones are read and rotated twice).
-//   8118 prompt tokens, 32 query heads and 8 of K and V, of 128: 39 us, 0.69 of the copy rate (183 MB): K and V 22, the queries
+//   8118 prompt tokens, 32 query heads and 8 of K and V, of 128: 36 us, 0.75 of the copy rate (183 MB): K and V 19, the queries
 // 20, which is their bytes at the copy rate, a few of them beside each other.  32 single tokens: 5.2 us, all of it latency.
 #include <algorithm>
 #include <atomic>
@@ -476,9 +476,9 @@ __device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64
 }
 
 // K and V of many tokens: a CTA takes tiles of kMany tokens, of K and of V in turn.  Its warps find the places of one tile each,
-// all at once, and bring the rows to the second-level cache.  (With a CTA a tile, seven warps waited for the eighth's dependent
-// loads: 26 us for 8118 tokens of 8 heads of 128 against 22.)  Bound by instructions, 17 a value, at 40 % of the
-// issue slots with 16 warps an SM.
+// all at once; a tile's rows are brought to the second-level cache while the tile before is worked on.  (With a CTA a tile,
+// seven warps waited for the eighth's dependent loads: 26 us for 8118 tokens of 8 heads of 128 against 19.)  Bound by the chain
+// of a tile (rows, angles, largest, scale, codes: 3 us), with 16 warps an SM at 45 % of the issue slots.
 template <bool NEOX>
 __global__ void __launch_bounds__(kThreads, kBlockCtas) append_blocks_kernel(const ScaledParams s, const __grid_constant__ Turns turns, int) {
   extern __shared__ __align__(16) float table[];  // cosines [tokens][half], then sines
@@ -488,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, kBlockCtas) append_blocks_kernel(con
   for (int k = threadIdx.x; k < p.rot / 2; k += kThreads) freq[k] = turns.f[k];
   dependents_may_launch();  // the queries
   const int items = 2 * ((p.T - 1) / kMany + 1), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, step = gridDim.x;
+  if (int(blockIdx.x) < items) prefetch_rows(p, blockIdx.x & 1, int(blockIdx.x) / 2 * kMany, kMany);
   const Deal deal(p.rot / 2);
   const Lanes of_k(p.D), of_v(p.Dv);
   int turn = 0;
