@@ -5,9 +5,9 @@
 // meet.  One pass over the logits finds both.
 //   Sum: in units of 2^R, R an integer near the running maximum of a thread's logits in log2 units: the term is
 // 2^(x log2 e - R), log2 e in two f32 pieces so that what is rounded is the difference, not the product.  16
-// terms are added pairwise, the 16-sums with the error of each addition kept beside it, and threads, splits and
-// rows meet in 64 bits.  What is left is the rounding of the single terms, some 1e-8 of the sum, and does not
-// depend on where a row lies in memory: equal rows tie.
+// terms are added pairwise, the 16-sums with the error of each addition kept beside it; threads and splits meet as such
+// pairs too, rows in 64 bits.  What is left is the rounding of the single terms, some 1e-8 of the sum, and does not
+// depend on where a row lies in memory: equal rows tie (those of a request are split alike).
 //   Candidates: each warp takes the r-th largest of its lanes' largest logits, r = ceil(k / 8); the least of the
 // 8 warps' is a lower bound of the k-th largest (8 r >= k logits are no smaller), found without a sort.  The pass keeps
 // each thread's largest of every tile; some 2 k of these are not below the bound, and only their 16 logits are read again.
@@ -53,21 +53,26 @@ struct SelectParams {
   int pieces, most_splits;   // CTAs of the first kernel; of a row at most (1: piece and row are the same number)
   float *out_scores;
   int32_t *out_rows, *out_tokens, *fault;
-  double *sums;              // [pieces] in units of 2^ref
+  float2 *sums;              // [pieces] in units of 2^ref, two pieces of a number
   int2 *refs;                // [pieces] R's bits, and the row's number in its request
   unsigned long long *keys;  // [pieces][k] descending, 0: none
   uint32_t *marks;           // the rows that are read, for calls that write the scores over those they had
   bool in_place;
 };
 
-// Rows whose logits are read share the pieces: of L such rows the j-th has those from first(j) to first(j + 1).  (A NaN
-// score is reported by the second kernel.)
+// Rows whose logits are read share the pieces: of L such rows the j-th has those from first(j) to first(j + 1), `splits` of
+// them or, the rows of the first requests, one more.  The rows of a request are split alike, so that equal ones have
+// equal sums.  (A NaN score is reported by the second kernel.)
 constexpr int kMostRanked = 1024;
 static_assert(kMostRanked / 32 == 32, "a lane a word");
 struct Shares {
-  int rows, pieces;  // L, and the pieces in use
-  __device__ __forceinline__ int first(int j) const { return int(uint32_t(j * pieces + rows - 1) / uint32_t(rows)); }
-  __device__ __forceinline__ int row_of(int piece) const { return int(uint32_t(piece * rows) / uint32_t(pieces)); }
+  int rows, splits, more;  // L, and how many rows have one more
+  __device__ __forceinline__ int pieces() const { return rows * splits + more; }
+  __device__ __forceinline__ int first(int j) const { return j * splits + min(j, more); }
+  __device__ __forceinline__ int row_of(int piece) const {
+    const int those = more * (splits + 1);
+    return piece < those ? int(uint32_t(piece) / uint32_t(splits + 1)) : more + int(uint32_t(piece - those) / uint32_t(splits));
+  }
 };
 // All rows' bits, 32 a word; all kThreads threads.
 __device__ __forceinline__ void mark_rows(const SelectParams &p, uint32_t *words) {
@@ -91,20 +96,49 @@ __device__ __forceinline__ void mark_rows(const SelectParams &p, uint32_t *words
     if ((threadIdx.x & 31) == 0) words[(n * kThreads + int(threadIdx.x)) / 32] = is;
   }
 }
-// The lane's word's rows, and those before; all lanes.
-__device__ __forceinline__ Shares share_rows(const SelectParams &p, const uint32_t *words, int &here, int &before) {
-  here = __popc(words[threadIdx.x & 31]);
-  before = here;
+// A warp's view of the marks: rows of the lane's word, and before it.
+struct Ranks {
+  const uint32_t *words;
+  int here, before, all;
+  __device__ __forceinline__ explicit Ranks(const uint32_t *w) : words(w) {
+    here = __popc(words[threadIdx.x & 31]);
+    before = here;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, before, d);
-    if ((threadIdx.x & 31) >= d) before += y;
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, before, d);
+      if ((threadIdx.x & 31) >= d) before += y;
+    }
+    all = __shfl_sync(0xffffffffu, before, 31);
+    before -= here;
   }
-  Shares s;
-  s.rows = __shfl_sync(0xffffffffu, before, 31);
-  s.pieces = min(p.pieces, s.rows * p.most_splits);
-  before -= here;
-  return s;
+  __device__ __forceinline__ int row_of(int rank) const {  // the same in all lanes, below `all`
+    const int lane = threadIdx.x & 31;
+    const int word = __ffs(__ballot_sync(0xffffffffu, rank >= before && rank < before + here)) - 1;
+    const uint32_t is = words[word];
+    const int in_word = rank - __shfl_sync(0xffffffffu, before, word);
+    return 32 * word + __ffs(__ballot_sync(0xffffffffu, (is >> lane & 1) && __popc(is & ((1u << lane) - 1u)) == in_word)) - 1;
+  }
+  __device__ __forceinline__ int rank_of(int row) const {  // rows that are read before it; each lane its own, up to kMostRanked
+    const int x = __shfl_sync(0xffffffffu, before, row / 32 & 31);
+    return row >= kMostRanked ? all : x + __popc(words[row / 32] & ((1u << (row & 31)) - 1u));
+  }
+  __device__ __forceinline__ Shares shares(const SelectParams &p) const {
+    Shares s{all, 1, 0};
+    if (all == 0) return s;
+    s.splits = min(int(uint32_t(p.pieces) / uint32_t(all)), p.most_splits);
+    const int spare = s.splits < p.most_splits ? p.pieces - all * s.splits : 0;  // (fewer than the rows)
+    if (spare > 0) {
+      const int row = row_of(spare);
+      s.more = rank_of(row - row % p.beams);
+    }
+    return s;
+  }
+};
+// (s, e) += (t, f), s and e two pieces of a number: f32 with an error of some 2^-47.
+__device__ __forceinline__ void add_pairs(float &s, float &e, float t, float f) {
+  const float sum = s + t, part = sum - s;
+  e = e + f + ((s - (sum - part)) + (t - part));
+  s = sum;
 }
 
 // Unsigned numbers that are ordered as floats and doubles are (no NaN; -0 is made 0 before).
@@ -170,8 +204,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
   __shared__ uint16_t found[kKeep];         // slot and thread
   __shared__ float bound[kWarps];
   __shared__ int n_found, n_kept, n_few;
-  __shared__ double warp_sum[kWarps];
-  __shared__ float warp_ref[kWarps];
+  __shared__ float warp_ref[kWarps], warp_sum[kWarps], warp_rest[kWarps];
   dependents_may_launch();
   const int piece = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int row = piece, begin = 0, size = p.vocab;
@@ -179,15 +212,12 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
     __shared__ uint32_t words[kMostRanked / 32];
     mark_rows(p, words);
     __syncthreads();
-    int here, before;
-    const Shares shares = share_rows(p, words, here, before);
+    const Ranks ranks(words);
+    const Shares shares = ranks.shares(p);
     if (p.in_place && piece == 0 && tid < kMostRanked / 32) p.marks[tid] = words[tid];
-    if (piece >= shares.pieces) return;
+    if (piece >= shares.pieces()) return;
     const int j = shares.row_of(piece), first = shares.first(j), splits = shares.first(j + 1) - first;
-    const int word = __ffs(__ballot_sync(0xffffffffu, j >= before && j < before + here)) - 1;
-    const uint32_t is = words[word];
-    const int rank = j - __shfl_sync(0xffffffffu, before, word);
-    row = 32 * word + __ffs(__ballot_sync(0xffffffffu, (is >> lane & 1) && __popc(is & ((1u << lane) - 1u)) == rank)) - 1;
+    row = ranks.row_of(j);
     const int chunks = (p.vocab + kChunk - 1) / kChunk, at = piece - first;
     begin = int(uint32_t(at * chunks) / uint32_t(splits)) * kChunk;  // (at < 64, chunks < 2^20)
     size = min(int(uint32_t((at + 1) * chunks) / uint32_t(splits)) * kChunk, p.vocab) - begin;
@@ -349,6 +379,17 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
     best = fmaxf(best, slot_top);
   }
   sharpen();
+  {  // the warp's sum, to its lanes' largest reference.  (A factor below 2^-126 is 0: so are its terms beside the largest.  In
+     // 64 bits, which are slow here, this took a fifth of the kernel's time.)
+    float most = ref;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    const float f = ref == neg_inf() ? 0.f : ex2(ref - most);
+    sum *= f, rest *= f;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) add_pairs(sum, rest, __shfl_xor_sync(0xffffffffu, sum, d), __shfl_xor_sync(0xffffffffu, rest, d));
+    if (lane == 0) warp_ref[warp] = most, warp_sum[warp] = sum, warp_rest[warp] = rest;
+  }
   __syncthreads();
 
   // ---- the logits that are not below the bound (-inf is no candidate): which threads' tiles have any, then those read anew
@@ -411,26 +452,34 @@ __global__ void __launch_bounds__(kThreads, 4) select_rows_kernel(const SelectPa
       }
     }
   }
-  thin();
-  if (tid < p.k) p.keys[int64_t(piece) * p.k + tid] = kept[tid];
-  // The threads' sums to the largest reference.
-  float most = ref;
+  unsigned long long *keys = p.keys + int64_t(piece) * p.k;
+  if (careful) {
+    thin();
+    if (tid < p.k) keys[tid] = kept[tid];
+  } else {  // (none is below the bound: all are put in order at once)
+    const int n = n_kept;
+    for (int i = tid; i < n; i += kThreads) {
+      const unsigned long long mine = kept[i];
+      int larger = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) larger += kept[j] > mine;
+      if (larger < p.k) keys[larger] = mine;
+    }
+    for (int i = n + tid; i < p.k; i += kThreads) keys[i] = 0;
+  }
+  if (warp == kWarps - 1) {  // the warps' sums to the largest reference
+    const float own = warp_ref[lane % kWarps];
+    float most = own;
 #pragma unroll
-  for (int d = 16; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
-  if (lane == 0) warp_ref[warp] = most;
-  __syncthreads();
+    for (int d = kWarps / 2; d; d >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+    const float f = own == neg_inf() ? 0.f : ex2(own - most);
+    sum = warp_sum[lane % kWarps] * f, rest = warp_rest[lane % kWarps] * f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) most = fmaxf(most, warp_ref[w]);
-  // (a factor below 2^-126 is 0: so are its terms beside the largest)
-  double all = ref == neg_inf() ? 0.0 : (double(sum) + double(rest)) * double(ex2(ref - most));
-#pragma unroll
-  for (int d = 16; d; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
-  if (lane == 0) warp_sum[warp] = all;
-  __syncthreads();
-  if (tid == 0) {
-    for (int w = 1; w < kWarps; ++w) all += warp_sum[w];
-    p.sums[piece] = all;
-    p.refs[piece] = make_int2(__float_as_int(most), row % p.beams);
+    for (int d = kWarps / 2; d; d >>= 1) add_pairs(sum, rest, __shfl_xor_sync(0xffffffffu, sum, d), __shfl_xor_sync(0xffffffffu, rest, d));
+    if (lane == 0) {
+      p.sums[piece] = make_float2(sum, rest);
+      p.refs[piece] = make_int2(__float_as_int(most), row % p.beams);
+    }
   }
 }
 
@@ -465,12 +514,10 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
     }
     __syncthreads();
     if (warp < 3) {
-      int here, before;
-      const Shares shares = share_rows(p, words, here, before);
-      const int row = min(row0 + tid, kMostRanked);
-      int rank = __shfl_sync(0xffffffffu, before, row / 32 & 31);  // rows that are read before it
-      rank = row == kMostRanked ? shares.rows : rank + __popc(words[row / 32] & ((1u << (row & 31)) - 1u));
-      if (tid <= p.beams) first_of[tid] = shares.rows ? shares.first(rank) : 0;
+      const Ranks ranks(words);
+      const Shares shares = ranks.shares(p);
+      const int rank = ranks.rank_of(min(row0 + tid, kMostRanked));
+      if (tid <= p.beams) first_of[tid] = shares.first(rank);
     }
   } else {
     if (tid <= p.beams) first_of[tid] = row0 + tid;
@@ -503,21 +550,26 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   for (int w = warp; w < p.beams; w += kWarps) {
     const int at = first_of[w], splits = first_of[w + 1] - at;
     float refs[2];
-    double sums[2];  // at most 64 splits: two a lane
+    float2 sums[2];  // at most 64 splits: two a lane
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int s = lane + 32 * i;
       refs[i] = s < splits ? __int_as_float(p.refs[at + s].x) : neg_inf();
-      sums[i] = s < splits ? p.sums[at + s] : 0.0;
+      sums[i] = s < splits ? p.sums[at + s] : make_float2(0.f, 0.f);
     }
     float ref = fmaxf(refs[0], refs[1]);
 #pragma unroll
     for (int d = 16; d; d >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, d));
-    double sum = 0.0;
-    if (ref != neg_inf()) sum = sums[0] * double(ex2(refs[0] - ref)) + sums[1] * double(ex2(refs[1] - ref));
+    float total = 0.f, rest = 0.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float f = refs[i] == neg_inf() ? 0.f : ex2(refs[i] - ref);
+      add_pairs(total, rest, sums[i].x * f, sums[i].y * f);
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1)
-      if (d < splits) sum += __shfl_xor_sync(0xffffffffu, sum, d);  // (lanes behind the splits hold 0)
+      if (d < splits) add_pairs(total, rest, __shfl_xor_sync(0xffffffffu, total, d), __shfl_xor_sync(0xffffffffu, rest, d));
+    const double sum = double(total) + double(rest);  // (lanes behind the splits hold 0)
     if (lane == 0) base[w] = sum, row_ref[w] = ref;
   }
   __syncthreads();
@@ -641,7 +693,7 @@ static psd_status launch_select(const psd_beam_args *a, void *workspace, const D
   p.pieces = int(std::min(int64_t(p.pieces), int64_t(p.most_splits) * a->rows));
   uint8_t *at = static_cast<uint8_t *>(workspace);
   const size_t pieces = size_t(p.pieces);
-  p.sums = reinterpret_cast<double *>(at);
+  p.sums = reinterpret_cast<float2 *>(at);
   p.keys = reinterpret_cast<unsigned long long *>(at + pieces * 8);
   p.refs = reinterpret_cast<int2 *>(at + pieces * 8 * (1 + size_t(a->k)));
   p.marks = reinterpret_cast<uint32_t *>(p.refs + pieces);

@@ -103,6 +103,17 @@ def test_equal_rows_go_to_lower_rows(vocab):
     _check(x, [-2.0, -2.0, -3.0, -2.0, -3.0, -2.0], 6, 30)
 
 
+@pytest.mark.parametrize("rows,beams,vocab,seed", [(128, 8, 98305, 0), (120, 5, 60001, 1), (300, 4, 9000, 2), (7, 7, 30000, 3), (96, 3, 40000, 4)])
+def test_equal_rows_tie_however_rows_are_split(rows, beams, vocab, seed):
+    """Rows of a request alike, some of them at their end: the values of its rows are equal, and lower rows come first."""
+    rng = np.random.default_rng(seed)
+    x = _logits(rows // beams, vocab, seed=seed).repeat_interleave(beams, 0).contiguous()
+    done = [bool(b) for b in rng.random(rows) < 0.2]
+    s = np.repeat(_scores(rows // beams, seed), beams)
+    s[rng.random(rows) < 0.1] = -np.inf
+    _check(x, s, beams, 12, finished=done, pad=1)
+
+
 def test_signed_zeros_are_equal():
     x = torch.full((1, 300), -1.0, device="cuda")
     x[0, 40], x[0, 20], x[0, 30] = 0.0, -0.0, 0.0
