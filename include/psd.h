@@ -779,7 +779,7 @@ psd_status multi_token_decode_scaled(psd_ctx *ctx, const psd_multi_token_args *a
  * order: out_scores f32, out_rows the row r (of all rows: what fork_pages takes as
  * parents), out_tokens t.  Within a row values are ordered by their logits, between rows
  * in 64 bits; equal ones by lower row, then lower token.  The sums of the exponentials
- * are f32 with compensation, good to some 1e-8 of the sum.  Equal rows (the same logits
+ * are f32 with compensation, and their logarithms, good to some 1e-8.  Equal rows (the same logits
  * and scores) have equal values.
  * A row with finished[r] != 0 has one continuation, pad_token with the value scores[r];
  * its logits are not read.  Logits of -inf and NaN are no continuations (and add nothing

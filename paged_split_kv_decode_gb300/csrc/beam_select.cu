@@ -12,16 +12,16 @@
 // 8 warps' is a lower bound of the k-th largest (8 r >= k logits are no smaller), found without a sort.  The pass keeps
 // each thread's largest of every tile; some 2 k of these are not below the bound, and only their 16 logits are read again.
 // Order numbers (a count of the larger ones) give the exact k.  So the pass is left with 9 instructions a logit; with a
-// bound and a search tile by tile 240 rows of 131072 bf16 took 34 us against 24.  Where more is found than there is room for (many equal logits) the CTA goes
+// bound and a search tile by tile 240 rows of 131072 bf16 took 34 us against 23.  Where more is found than there is room for (many equal logits) the CTA goes
 // over its logits again and thins them out on the way.
 //
 // Rows are split so that all SMs have equal work: the rows that are read (not finished, not empty) share the CTAs that run
 // at once, to within a split.  A second kernel, one CTA a request, joins the splits' sums and takes the k largest of the
 // rows' candidates in 64 bits.
 //
-// 128 rows of 98305 f32, a fifth of them finished: 18 us (40 MB, 6 us at the copy rate), 13 of them the pass; bound by the fixed part
-// of a CTA (680 instructions a warp, and a chain of dependent steps) and its 16000 logits in equal parts, then by the second
-// kernel's chain.  240 rows of 131072 bf16: 24 us (8 us at the copy rate), bound by instructions.
+// 128 rows of 98305 f32, a fifth of them finished: 17 us (40 MB, 6 us at the copy rate), 11 of them the first kernel; bound by the
+// chain of a CTA's steps around its 16000 logits (its row, the bound, the search, the order), then by the second kernel's
+// chain.  240 rows of 131072 bf16: 23 us (8 us at the copy rate), bound by instructions.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -134,6 +134,30 @@ struct Ranks {
     return s;
   }
 };
+// log2 of s + e to 1.4e-9, as its integer part and the rest: with r near 1 / m, 9 bits, m = s 2^-n in [1, 2),
+// log2 m = -log2 r + log2(1 + t), t = m r - 1 below 2^-7 exact but for its last bit, and four terms of a series.  (In 64 bits
+// a logarithm is some 40 slow operations that a whole CTA waits for: 0.7 us of 18.)
+struct Logs {
+  float r[128], high[128], low[128];  // r, and -log2 r in two pieces
+  constexpr Logs() : r{}, high{}, low{} {
+    for (int i = 0; i < 128; ++i) {
+      const int k = int(512.0 * 128.0 / (128.0 + i + 0.5) + 0.5);  // r = k / 512
+      const double x = k / 512.0, y = (x - 1) / (x + 1);           // ln x = 2 (y + y^3 / 3 + ..)
+      double sum = 0, power = y;
+      for (int n = 0; n < 40; ++n) sum += power / (2 * n + 1), power *= y * y;
+      const double log2 = -2 * sum * 1.4426950408889634074;
+      r[i] = float(x), high[i] = float(log2), low[i] = float(log2 - double(float(log2)));
+    }
+  }
+};
+__constant__ const Logs kLogs = Logs();
+__device__ __forceinline__ double log2_of(float s, float e, float ref) {  // 2^ref (s + e), s normal
+  const int u = __float_as_int(s), n = (u >> 23) - 127, i = u >> 16 & 127;
+  const float m = __int_as_float((u & 0x7fffff) | 0x3f800000), tail = e * __int_as_float((127 - max(n, -126)) << 23);
+  const float r = kLogs.r[i], t = fmaf(tail, r, fmaf(m, r, -1.f));
+  const float p = t * fmaf(t, fmaf(t, fmaf(t, -0.360673760f, 0.480898347f), -0.721347520f), 1.442695041f);
+  return double(ref) + double(n) + (double(kLogs.high[i]) + double(kLogs.low[i] + p));
+}
 // (s, e) += (t, f), s and e two pieces of a number: f32 with an error of some 2^-47.
 __device__ __forceinline__ void add_pairs(float &s, float &e, float t, float f) {
   const float sum = s + t, part = sum - s;
@@ -492,7 +516,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
   unsigned long long *value = shared, *key = shared + most;  // candidates: v in order, and the logit and token
   uint8_t *of = reinterpret_cast<uint8_t *>(key + most);     // and the row
   __shared__ double base[kMaxBeams];                         // what a row's logits are added to
-  __shared__ float row_ref[kMaxBeams], base_down[kMaxBeams], base_up[kMaxBeams];
+  __shared__ float row_ref[kMaxBeams], row_sum[kMaxBeams], row_rest[kMaxBeams], base_down[kMaxBeams], base_up[kMaxBeams];
   __shared__ uint8_t kind[kMaxBeams];                        // 0: no continuation, 1: pad_token, 2: candidates
   __shared__ float bound[kWarps];
   __shared__ int n_shared, first_of[kMaxBeams + 1];          // a row's first piece
@@ -569,8 +593,7 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
 #pragma unroll
     for (int d = 16; d; d >>= 1)
       if (d < splits) add_pairs(total, rest, __shfl_xor_sync(0xffffffffu, total, d), __shfl_xor_sync(0xffffffffu, rest, d));
-    const double sum = double(total) + double(rest);  // (lanes behind the splits hold 0)
-    if (lane == 0) base[w] = sum, row_ref[w] = ref;
+    if (lane == 0) row_sum[w] = total, row_rest[w] = rest, row_ref[w] = ref;  // (lanes behind the splits hold 0)
   }
   __syncthreads();
   if (tid < p.beams) {  // a lane a row: the logarithms at once
@@ -578,11 +601,10 @@ __global__ void __launch_bounds__(kThreads) select_join_kernel(const SelectParam
     bool bad = isnan(score) || score == -neg_inf();
     double add = double(score);
     if (what == 2 && !bad) {  // (rows that are finished or were never filled have left no sums)
-      const double sum = base[tid];
-      const float ref = row_ref[tid];
-      if (sum == 0.0) what = 0;  // nothing but -inf
-      else if (!(sum < 1e300) || ref > 3e38f) bad = true;
-      else add -= (double(ref) + log2(sum)) * 0.69314718055994530942;
+      const float sum = row_sum[tid], ref = row_ref[tid];
+      if (sum == 0.f) what = 0;  // nothing but -inf
+      else if (!(sum + row_rest[tid] < 1e37f) || ref > 3e38f) bad = true;
+      else add -= log2_of(sum, row_rest[tid], ref) * 0.69314718055994530942;
     }
     if (bad) {
       what = 0;
