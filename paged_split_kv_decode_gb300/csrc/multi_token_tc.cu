@@ -981,6 +981,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                   for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * alpha);
                   tmem_st32(lane_base + D * slot + c, o);
                 }
+                st_wait();  // the maximum may grow in this tile too, and O is then read again
               }
               vref = ve;
             }
