@@ -457,7 +457,7 @@ __device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64
     }
     __syncwarp();
     if (lane == 0) *scale = uint8_t(e);
-    const float by = __uint_as_float(uint32_t(254 - min(e, 253)) << 23);
+    const float by = __uint_as_float(e >= 254 ? 0x00400000u : uint32_t(254 - e) << 23);  // (2^-127 is subnormal)
 #pragma unroll 1
     for (int pass0 = 0; pass0 < passes; pass0 += kPasses) {
       if (passes > kPasses) fetch(pass0), turn(pass0);   // (otherwise they are there)

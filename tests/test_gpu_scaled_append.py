@@ -231,6 +231,15 @@ def test_borders_of_the_scales():
     _check(s, psd.rope_frequencies(64))
 
 
+@pytest.mark.parametrize("shape", [RAGGED, MANY])
+@pytest.mark.parametrize("had", [252, 253, 254])
+def test_the_largest_scales(had, shape):
+    """Blocks that a caller gave scales of 2^125 to 2^127: new codes are in units of these where older tokens are there."""
+    s = _make(**shape, seed=14, spread=2.0 ** 123)
+    s["ke"][:], s["ve"][:] = had, had
+    _check(s, psd.rope_frequencies(64))
+
+
 def test_in_place_queries():
     a = _make(**RAGGED, seed=9, fused=False, pad_rows=0)
     want, _ = _call(a, psd.rope_frequencies(64))
