@@ -959,8 +959,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           fence_proxy_async();
         }
         const bool masked = __any_sync(0xffffffffu, live && clear < base + NK);
-        // Scaled blocks: the tile's score factor, log2 of its V's scale below vref and the inverse.  (The scales were there
-        // before the tile's K was, and so before the S that is complete now.)
+        // Scaled blocks: the tile's score factor, and what its weights meet V times: 2^down, V's scale below vref.  bf16 outputs
+        // have it in the exponent, and `up`, its inverse, back in l.  For f32 outputs the exponent would be rounded too far (a
+        // sum with 64 to 2^-18): P is multiplied, and l has never had it.  (The scales were there before the tile's K was, and
+        // so before the S that is complete now.)
         float tile_qs = qs;
         [[maybe_unused]] float down = 0.f, up = 1.f;
         if constexpr (SCALED) {
@@ -989,8 +991,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             // (a normal number: times a score of -inf, 0 would be NaN)
             tile_qs = fmaxf(qs * __uint_as_float(w & ~255u), 0x1p-126f);
             const int below = min(vref - ve, 64);
-            down = -float(below);
-            up = __uint_as_float(uint32_t(127 + below) << 23);
+            down = TERMS == 1 ? -float(below) : __uint_as_float(uint32_t(127 - below) << 23);
+            if constexpr (TERMS == 1) up = __uint_as_float(uint32_t(127 + below) << 23);
           }
         }
         auto give_part = [&](auto which) -> bool {
@@ -1003,8 +1005,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             [[maybe_unused]] float pf[TERMS > 1 ? 64 : 1];
             float2 sum[2];
             for (;;) {
-              const float nm = m == neg_inf() ? 0.f : -m;
-              const float2 qs2 = make_float2(tile_qs, tile_qs), nm2 = make_float2(nm + down, nm + down);
+              const float nm = (m == neg_inf() ? 0.f : -m) + (TERMS == 1 ? down : 0.f);
+              const float2 qs2 = make_float2(tile_qs, tile_qs), nm2 = make_float2(nm, nm);
               float t4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
               sum[0] = sum[1] = make_float2(0.f, 0.f);
 #pragma unroll
@@ -1031,8 +1033,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                   if constexpr (TERMS == 1) {
                     pk[(c0 + c) / 2] = p_bits<FP8>(a, b);
                   } else {
-                    pf[c0 + c] = a;
-                    pf[c0 + c + 1] = b;
+                    pf[c0 + c] = SCALED ? a * down : a;
+                    pf[c0 + c + 1] = SCALED ? b * down : b;
                   }
                 }
               }
@@ -1046,7 +1048,8 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                 if (!wait_all(T_HALF + slot, ops)) return false;
                 fence_after();
               }
-              const float m_new = grow ? top - L::kBias : m;
+              // (scaled blocks: an integer, so that sums with exponents of scales are exact)
+              const float m_new = grow ? (SCALED ? floorf(top) : top) - L::kBias : m;
               const float alpha = grow ? ex2(m - m_new) : 1.f;
               l *= alpha;
               if (part > 0 || !empty) {
@@ -1078,7 +1081,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
               }
             }
             sum[0] = __fadd2_rn(sum[0], sum[1]);
-            l = SCALED ? fmaf(sum[0].x + sum[0].y, up, l) : l + (sum[0].x + sum[0].y);
+            l = SCALED && TERMS == 1 ? fmaf(sum[0].x + sum[0].y, up, l) : l + (sum[0].x + sum[0].y);
           }
           st_wait();
           fence_before();

@@ -74,6 +74,45 @@ def _same(a, b):
         assert worst <= 2.0 ** -20, worst
 
 
+@pytest.mark.parametrize("jump", [False, True])
+@pytest.mark.parametrize("n,G", [(1, 4), (3, 4), (40, 1), (40, 4)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_values_in_other_units(D, n, G, jump):
+    """The first half of the values in units of 2^-5, with codes in place of that, or of 2^-3 as the second half, which is
+    zeros.  Scores are equal (or grow once, with the units), and their sum with the units' exponent does not fit f32."""
+    rng, L = np.random.default_rng(D + n), 2048
+    k = np.zeros((L, D), dtype=np.uint8)
+    k[:, 0] = 0x38
+    if jump:
+        k[L // 2:, 0] = 0x40                                         # scores of 12.. and 24..
+    v = np.zeros((L, D), dtype=np.uint8)
+    v[: L // 2] = 0x38 + rng.integers(0, 8, (L // 2, D))             # 1 .. 1.875
+    ke = np.full(L // BLOCK, 127)
+    ve = np.full(L // BLOCK, 124)
+    sm = _scale_for(12.5, 12.75, 16, 6)
+    want = Cache(40, n, k, np.where(v > 0, v - 16, 0).astype(np.uint8), ke, ve, G=G, Hkv=4, sm_scale=sm).run(out_f32=True)
+    ve[: len(ve) // 2] = 122
+    got = Cache(40, n, k, v, ke, ve, G=G, Hkv=4, sm_scale=sm).run(out_f32=True)
+    _same(got, want)
+
+
+@pytest.mark.parametrize("n,G", [(1, 4), (3, 4), (40, 1), (40, 4)])
+@pytest.mark.parametrize("e", [95, 130, 160])
+def test_blocks_of_zeros_in_other_units(e, n, G):
+    """Tiles of zeros have any scale: their weights do not change."""
+    rng, L, D = np.random.default_rng(e + n), 2048, 64
+    k = np.zeros((L, D), dtype=np.uint8)
+    k[:, 0] = 0x38
+    v = np.zeros((L, D), dtype=np.uint8)
+    v[:64], v[1024:1088] = _codes(rng, (64, D)), _codes(rng, (64, D))
+    ke, ve = np.full(L // BLOCK, 127), np.full(L // BLOCK, 170)
+    sm = _scale_for(12.5, 12.75, 8, 4)
+    want = Cache(40, n, k, v, ke, ve, G=G, Hkv=4, sm_scale=sm).run(out_f32=True)
+    ve[[j for j in range(len(ve)) if not v[16 * j: 16 * j + 16].any()]] = e
+    got = Cache(40, n, k, v, ke, ve, G=G, Hkv=4, sm_scale=sm).run(out_f32=True)
+    _same(got, want)
+
+
 @pytest.mark.parametrize("out_f32", [False, True])
 @pytest.mark.parametrize("n,G", [(1, 4), (40, 1), (40, 4)])
 @pytest.mark.parametrize("D", [64, 128])
