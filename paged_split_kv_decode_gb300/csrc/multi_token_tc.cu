@@ -42,11 +42,11 @@
 // kind::f8f6f4, against Q in two e4m3 terms, were no faster.)
 // A cache of 8-bit blocks with a scale each (SCALED): the load warps also bring, eight tiles ahead, each tile's four scale
 // bytes into rings in shared memory, and the conversion gives f16 values in units of the tile's largest scale (a warp has one
-// block; blocks 2^15 below the tile's largest are exact, beyond that what f16 loses is 2^-33 of the largest).  What is left is
+// block; blocks 2^15 below the tile's largest are exact, beyond that values are rounded to 2^-25 of the largest).  What is left is
 // a factor a tile: K's on the scores, V's 2^b in the exponent of P, 2^(s - m + b - r) with r the largest b so far (O is
 // rescaled when r grows; b counts as r - 64 at least) and l += 2^(r - b) sum P.  Factors of every 16 keys in the softmax, whose
 // chain bounds the kernel, took 421 us for 2048 tokens over 4096 keys; the largest of a tile found by every softmax thread 229; so, by the load
-// warps, 217 (unscaled fp8 206).
+// warps, 219 (unscaled fp8 206).
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
@@ -639,16 +639,18 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           tk = (D == 128 ? s >> 1 : s) * 8 + (lane & 7);
           chunk = (D == 128 ? (s & 1) * 4 : 0) + (lane >> 3);
         };
-        // Scaled blocks: a warp has the tile's tokens 16 w .. of one block; its scale, to the tile's largest.
+        // Scaled blocks: a warp has the tile's tokens 16 w .. of one block; its scale, to the tile's largest.  Down to 2^-15 of it
+        // codes stay exact (they are multiples of 2^-9, f16's of 2^-24); what is further below is multiplied twice, and rounded
+        // once, by the second product.  Codes end at 448 2^-34, which is nearer to 0 than to 2^-24.
         static_assert(!SCALED || kSteps * 8 / (D == 128 ? 2 : 1) == 16, "a block a warp");
         __half2 by = __floats2half2_rn(1.f, 1.f);
-        bool other = false;
+        int down = 0;
         if constexpr (SCALED) {
           const uint32_t e4 = *reinterpret_cast<const volatile uint32_t *>(  // the four bytes
               sm + L::kOffBar + (v ? kVScaleOff + (g & (kVScaleTiles - 1)) * 4 : kScaleOff + (g & (kScaleTiles - 1)) * 8));
-          const int mine = int(e4 >> (8 * (th >> 5)) & 255u), down = mine - largest_scale(e4);
-          other = down != 0;
-          by = mine == 255 ? __float2half2_rn(scale_value(255)) : __float2half2_rn(down < -24 ? 0.f : ex2(float(down)));
+          const int mine = int(e4 >> (8 * (th >> 5)) & 255u);
+          down = mine - largest_scale(e4);  // (above 0 for NaN's)
+          by = __float2half2_rn(mine == 255 ? scale_value(255) : __uint_as_float(uint32_t(127 + max(down, -15)) << 23));
         }
         uint4 w[kSteps];
 #pragma unroll
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           place(c, tk, chunk);
           uint32_t out[8];
           codes_to_f16(w[c], out);
-          if (SCALED && other) {
+          if (SCALED && down != 0) {
 #pragma unroll
             for (int y = 0; y < 8; ++y) {
               const __half2 x = __hmul2(*reinterpret_cast<const __half2 *>(out + y), by);
@@ -678,6 +680,20 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           uint8_t *row = dst + (tk >> 3) * L::kGroupBytes + (chunk >> 2) * 1024 + (tk & 7) * 128;
           *reinterpret_cast<uint4 *>(row + ((k ^ (tk & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
           *reinterpret_cast<uint4 *>(row + (((k + 1) ^ (tk & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
+        }
+        if (SCALED && down < -15) {  // (in the loop above, whose code all warps fetch, 2048 tokens over 4096 keys took 221 us against 219)
+          const __half2 again = __float2half2_rn(down < -33 ? 0.f : __uint_as_float(uint32_t(127 + 15 + down) << 23));
+#pragma unroll 1
+          for (int c = 0; c < 2 * kSteps; ++c) {
+            int tk, chunk;
+            place(c >> 1, tk, chunk);
+            const int k = (2 * chunk + (c & 1)) & 7;
+            uint4 *at = reinterpret_cast<uint4 *>(dst + (tk >> 3) * L::kGroupBytes + (chunk >> 2) * 1024 + (tk & 7) * 128 + ((k ^ (tk & 7)) << 4));
+            uint4 x = *at;
+            __half2 *y = reinterpret_cast<__half2 *>(&x);
+            y[0] = __hmul2(y[0], again), y[1] = __hmul2(y[1], again), y[2] = __hmul2(y[2], again), y[3] = __hmul2(y[3], again);
+            *at = x;
+          }
         }
         fence_proxy_async();
         __syncwarp();

@@ -134,3 +134,46 @@ def test_scales_and_scores_that_grow_in_one_tile(D, n, G, out_f32):
     o, lse = o.double().cpu().numpy().reshape(40, n, s.Hq, D), lse.double().cpu().numpy().reshape(40, n, s.Hq)
     assert float(np.max(np.abs(o - want[0]) / e_o)) <= 1
     assert float(np.max(np.abs(lse - want[1]) / e_l)) <= 1
+
+
+@pytest.mark.parametrize("gap", [15, 24, 25, 26, 28, 30, 33])
+@pytest.mark.parametrize("out_f32", [False, True])
+@pytest.mark.parametrize("n", [1, 40])
+def test_values_far_below_the_tiles_largest_scale(n, out_f32, gap):
+    """The largest scale of a tile is that of keys without weight: the others' values are rounded to 2^-25 of it, no more."""
+    rng, L, D = np.random.default_rng(gap), 64, 64
+    k, v = np.zeros((L, D), dtype=np.uint8), _codes(rng, (L, D), 0x70, 0x7F)   # 128 to 448
+    k[:16, 0] = 0xFE                                                  # -448: a weight of e^-448
+    ke, ve = np.full(4, 127), np.array([170, 170 - gap, 170 - gap, 170 - gap])
+    s = Cache(2, n, k, v, ke, ve)
+    o, lse = s.run(out_f32=out_f32)
+    want = s.one()
+    e_o, e_l = bounds(want, D, L, out_f32, 2 if out_f32 else 1)
+    # a value's rounding, and that of its weight to 2^-32 of the largest
+    e_o = e_o + 2.0 ** 43 * (2.0 ** -25 + 2.0 ** -32 * 448)
+    o, lse = o.double().cpu().numpy().reshape(2, n, s.Hq, D), lse.double().cpu().numpy().reshape(2, n, s.Hq)
+    assert float(np.max(np.abs(o - want[0]) / e_o)) <= 1
+    assert float(np.max(np.abs(lse - want[1]) / e_l)) <= 1
+
+
+@pytest.mark.parametrize("gap", [15, 24, 25, 26, 28])
+@pytest.mark.parametrize("n", [1, 40])
+def test_keys_far_below_the_tiles_largest_scale(n, gap):
+    """The largest K scale of a tile is that of keys whose scores leave them no weight."""
+    rng, L, D = np.random.default_rng(gap), 64, 64
+    k, v = np.zeros((L, D), dtype=np.uint8), _codes(rng, (L, D))
+    k[:16, 0] = 0xFE
+    k[16::2, 0] = 0x7E                                                # 448 and 0
+    ke, ve = np.array([170, 170 - gap, 170 - gap, 170 - gap]), np.full(4, 127)
+    unit = 2.0 ** gap / 448                                           # a score of 1 for 448 at the small scale
+    s = Cache(2, n, k, v, ke, ve, sm_scale=unit * 2.0 ** -43)
+    o, lse = s.run(out_f32=True)
+    want = s.one()
+    # a key's rounding is 2^-25 of the largest scale, so 2^-25 unit in its score; twice that of sum p |v| in the output
+    score = 2.0 ** -25 * unit
+    top = want[3].copy()
+    rows = (want[0], want[1], want[2], np.minimum(top, 1.0))          # (the scores that have a weight are 1 at most)
+    e_o, e_l = bounds(rows, D, L, True, 2)
+    o, lse = o.double().cpu().numpy().reshape(2, n, s.Hq, D), lse.double().cpu().numpy().reshape(2, n, s.Hq)
+    assert float(np.max(np.abs(o - want[0]) / (e_o + 2 * score * want[2]))) <= 1
+    assert float(np.max(np.abs(lse - want[1]) / (e_l + score * LOG2E))) <= 1
