@@ -783,9 +783,9 @@ psd_status multi_token_decode_scaled(psd_ctx *ctx, const psd_multi_token_args *a
  * and scores) have equal values.
  * A row with finished[r] != 0 has one continuation, pad_token with the value scores[r];
  * its logits are not read.  Logits of -inf and NaN are no continuations (and add nothing
- * to the sum), and neither are rows whose score is -inf.  A row with a logit of +inf, a
- * score that is NaN or +inf, or whose sum overflows has none either and sets
- * PSD_FAULT_RANGE.  Where a request has fewer than k continuations the rest are -inf, -1,
+ * to the sum), and neither are rows whose score is -inf.  Finite logits may be of any size (a
+ * row whose largest is beyond some 5.8e6 either way is read twice).  A row with a logit of +inf, or a
+ * score that is NaN or +inf, has no continuations either and sets PSD_FAULT_RANGE.  Where a request has fewer than k continuations the rest are -inf, -1,
  * -1.  rows == 0 is a no-op.  out_scores may be scores where k == beams (the next step's
  * scores in place of this one's); no output may overlap scores otherwise, nor finished.
  * workspace: >= psd_beam_workspace_bytes(ctx, rows, beams, k) bytes, 16-byte aligned; calls

@@ -53,9 +53,9 @@ def select(logits, scores, beams, k, finished=None, pad=0):
             top = x.max()
             if math.isinf(top):
                 continue
-            low = top + math.log(math.fsum(np.exp(x - top)))
+            share = math.log(math.fsum(np.exp(x - top)))              # (beside a far-off top it would be lost)
             order = np.lexsort((np.arange(len(x)), -x))[:k]
-            found += [(-(s + (x[t] - low)), r, -x[t], int(t)) for t in order if x[t] > -np.inf]
+            found += [(-(s + ((x[t] - top) - share)), r, -x[t], int(t)) for t in order if x[t] > -np.inf]
         for i, (v, r, _, t) in enumerate(sorted(found)[:k]):
             out[0][b, i], out[1][b, i], out[2][b, i] = -v, r, t
     return out

@@ -136,6 +136,50 @@ def test_masked_logits():
     _check(x[:2], [-inf, -inf], 2, 8)
 
 
+MASKS = [-1e8, -1e9, -1e10, -1e20, -1e30, -1e38, -2.5e38, torch.finfo(torch.float32).min]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("mask", MASKS)
+def test_parts_of_a_row_at_a_large_negative_value(mask, kind):
+    """Masks that are finite: the tokens that are left have the values that they have without the others."""
+    x, mask = _logits(8, 30000, kind, 13), max(mask, torch.finfo(TYPES[kind]).min)
+    x[0, :20000] = mask
+    x[1, 5:] = mask
+    x[2, ::2] = mask
+    x[3, :29000] = mask
+    x[4, 4096:] = mask
+    x[5, 100] = mask
+    x[6, :15000], x[6, 15000:] = -float("inf"), torch.where(x[6, 15000:] > 0, mask, x[6, 15000:])
+    _check(x, _scores(8, 13), 4, 5)
+    _check(x, _scores(8, 13), 1, 4, finished=[0, 0, 0, 0, 0, 0, 0, 1])
+    _check(x[:, :4096], _scores(8, 13), 8, 8)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("value", MASKS + [1e7, -1e7, 3e7, 1e10, 1e30, 3e38, torch.finfo(torch.float32).max])
+def test_rows_at_one_value_however_large(value, kind):
+    """Rows that are one value, or nearly so: tokens share the row evenly, wherever it lies."""
+    value = float(torch.tensor(value).clamp(torch.finfo(TYPES[kind]).min, torch.finfo(TYPES[kind]).max).to(TYPES[kind]))
+    for V in (1, 700, 9001):
+        x = torch.full((6, V), value, dtype=TYPES[kind], device="cuda")
+        x[1] = _logits(1, V, kind, 14)[0]
+        if V > 1:
+            x[2, V // 2:] = -float("inf")
+            x[3, ::3] = float("nan")
+            x[4, V - 1] = torch.nextafter(x[4, 0], torch.tensor(0.0, dtype=TYPES[kind], device="cuda"))
+        _check(x, [-1.0, -1.5, -2.0, -2.5, -3.0, -9.0], 3, 8)
+        _check(x, [-1.0, -1.5, -2.0, -2.5, -3.0, -9.0], 2, 64, finished=[0, 1, 0, 0, 0, 0])
+
+
+def test_many_rows_at_a_large_value():
+    """More rows than CTAs run at once (a CTA a row), some of them of the lowest finite value; the others are not disturbed."""
+    x = _logits(700, 3000, seed=16)
+    x[::50] = torch.finfo(torch.float32).min
+    x[1::50] = -1e10
+    _check(x, _scores(700, 16), 7, 10, finished=[r % 9 == 0 for r in range(700)])
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_finished_beams(kind):
     x = _logits(8, 7000, kind, 4)
