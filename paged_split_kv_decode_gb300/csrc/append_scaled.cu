@@ -443,7 +443,7 @@ __device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64
     if (x.older > 0) {
       const int had = *scale;
       if (e > had) {
-        const float down = ex2(float(had - e));          // (0 below 2^-126)
+        const float down = power_of_two(had - e);        // (ties are kept; 0 below 2^-126)
         for (int i = mine; mine < a_pass && i < x.older; i += a_pass) {
           uint2 *at = reinterpret_cast<uint2 *>(pool + i * pool_stride + ca);
           *at = codes8(values8(*at), down);

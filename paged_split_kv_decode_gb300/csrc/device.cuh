@@ -131,6 +131,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 2^n, n <= 127, exactly (ex2 promises a bound on its error and no more); 0 below 2^-126.
+__device__ __forceinline__ float power_of_two(int n) { return n < -126 ? 0.f : __uint_as_float(uint32_t(127 + n) << 23); }
+
 // Two bf16 packed in a 32-bit word -> two floats (exact: a bf16 is the top half
 // of an f32).
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
       if (most > uint32_t(ref)) {  // the same in all lanes
         const uint32_t finite = max(ve[0] == 255 ? 0u : ve[0], ve[1] == 255 ? 0u : ve[1]);
         if (finite > uint32_t(ref)) {
-          const float down = ref == 0 ? 0.f : ex2(float(ref) - float(finite));  // (O holds nothing yet, or is 0)
+          const float down = ref == 0 ? 0.f : power_of_two(ref - int(finite));  // (O holds nothing yet, or is 0)
           ref = int(finite);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)

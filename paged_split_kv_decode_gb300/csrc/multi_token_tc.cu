@@ -989,7 +989,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             if (ve > vref) {
               // S(t) is complete, so PV(t - 2), issued before it, is too
               if (!empty) {
-                const float alpha = ex2(float(vref - ve));
+                const float alpha = power_of_two(vref - ve);
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                   uint32_t o[32];

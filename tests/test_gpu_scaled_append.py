@@ -240,6 +240,26 @@ def test_the_largest_scales(had, shape):
     _check(s, psd.rope_frequencies(64))
 
 
+def test_older_codes_at_any_new_scale():
+    """All 256 codes in a block that a new token scales anew by 2^1 to 2^40: each goes to the nearest code, ties to even."""
+    n = 40
+    s = _make([1] * n, [15] * n, Hq=1, Hkv=1, D=64, seed=15, fused=False, pad_rows=0)
+    codes = torch.arange(256, dtype=torch.uint8, device="cuda").repeat(4)
+    for b in range(n):
+        page = int(s["host"]["page_indices"][b])
+        s["v_pool"][page].view(-1)[:960], s["ve"][page] = codes[:960], 110
+        s["v"][b] = 448.0 * 2.0 ** (110 - 127 + b + 1)
+    was = s["v_pool"].clone()
+    _, fault = _call(s, psd.rope_frequencies(32))
+    assert fault == 0
+    for b in range(n):
+        page = int(s["host"]["page_indices"][b])
+        assert int(s["ve"][page, 0, 0]) == 110 + b + 1
+        want = BM.e4m3_nearest(_values(was[page, :15].cpu().numpy()) * 2.0 ** -(b + 1))
+        assert np.array_equal(_values(s["v_pool"][page, :15].cpu().numpy()), want, equal_nan=True), b
+        assert bool((s["v_pool"][page, 15] == 0x7E).all())
+
+
 def test_in_place_queries():
     a = _make(**RAGGED, seed=9, fused=False, pad_rows=0)
     want, _ = _call(a, psd.rope_frequencies(64))
