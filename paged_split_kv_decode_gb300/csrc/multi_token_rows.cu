@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
       if (most > uint32_t(ref)) {  // the same in all lanes
         const uint32_t finite = max(ve[0] == 255 ? 0u : ve[0], ve[1] == 255 ? 0u : ve[1]);
         if (finite > uint32_t(ref)) {
-          const float down = ref == 0 ? 0.f : power_of_two(ref - int(finite));  // (O holds nothing yet, or is 0)
+          const float down = power_of_two(ref - int(finite));
           ref = int(finite);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -413,8 +413,6 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
             for (int j = 0; j < kMmas; ++j)
 #pragma unroll
               for (int x = 0; x < 4; ++x) o[nt][j][x] *= down;
-        } else if (ref == 0) {
-          ref = 127;  // a scale of NaN: what O will be multiplied by must not be 0
         }
       }
       const bool masked = tail || j0 + kStep > clear;
@@ -536,6 +534,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
     // ------------------------------------------------------------------------ the request's end
     // Lane (g, c) holds columns D / 8 g .. of rows 2 c and 2 c + 1.
     const bool whole = u.s0 == 0 && u.s1 == u.n;
+    const float unit = scale_value(uint32_t(ref));  // (times 1 / l first, its product could be too small for f32)
     const int64_t piece = ((int64_t(slot) * 2 + (u.first ? 0 : 1)) * p.Hkv + kv) * 8 * NT;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -548,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
         if (row >= rows) continue;
         const int tok = row / p.G;
         const int64_t out = (int64_t(r.token0) + tok) * p.Hq + kv * p.G + (row - tok * p.G);
-        const float f = all == 0.f ? 0.f : scale_value(uint32_t(ref)) / all;
+        const float f = all == 0.f ? 0.f : 1.f / all;
         const int64_t dst = (whole ? out : piece + row) * D + (D / 8) * g;
         if (whole && TERMS == 1) {
           __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(p.o) + dst;
@@ -557,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
             uint32_t w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const __nv_bfloat162 x = __floats2bfloat162_rn(o[nt][j + k][i] * f, o[nt][j + k][2 + i] * f);
+              const __nv_bfloat162 x = __floats2bfloat162_rn(o[nt][j + k][i] * f * unit, o[nt][j + k][2 + i] * f * unit);
               w[k] = *reinterpret_cast<const uint32_t *>(&x);
             }
             *reinterpret_cast<uint4 *>(to + 2 * j) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -566,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, Lay<D, NT>::kCtasPerSm)
           float *to = (whole ? static_cast<float *>(p.o) : p.part_o) + dst;
 #pragma unroll
           for (int j = 0; j < kMmas; j += 2)
-            *reinterpret_cast<float4 *>(to + 2 * j) = make_float4(o[nt][j][i] * f, o[nt][j][2 + i] * f, o[nt][j + 1][i] * f, o[nt][j + 1][2 + i] * f);
+            *reinterpret_cast<float4 *>(to + 2 * j) = make_float4(o[nt][j][i] * f * unit, o[nt][j][2 + i] * f * unit,
+                                                                  o[nt][j + 1][i] * f * unit, o[nt][j + 1][2 + i] * f * unit);
         }
         if (g == 0) {
           const float v = all == 0.f ? neg_inf() : m[nt][i] + log2f(all);

@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           k = max(k, __shfl_xor_sync(0xffffffffu, k, d));
           v = max(v, __shfl_xor_sync(0xffffffffu, v, d));
         }
-        tops = k << 23 | v;
+        tops = max(k << 23, 0x00400000u) | v;  // (2^-127 is subnormal)
       };
       if constexpr (SCALED) {
         ids = load_ids(u.j0);
@@ -1194,7 +1194,13 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
         const float w0 = ex2(m - from), w1 = ex2(m1 - from);  // 0 where a slot saw no key
         const float all = l * w0 + l1 * w1, inv = all == 0.f ? 0.f : p.v_scale / all;
         float f0 = l == 0.f ? 0.f : w0 * inv, f1 = l1 == 0.f ? 0.f : w1 * inv;
-        if constexpr (SCALED) f0 *= scale_value(uint32_t(vref)), f1 *= scale_value(uint32_t(vref1));
+        // Scaled blocks: both in the larger unit, which comes last (before, its product could be too small for f32).
+        [[maybe_unused]] float unit = 1.f;
+        if constexpr (SCALED) {
+          const int most = max(vref, vref1);
+          f0 *= power_of_two(vref - most), f1 *= power_of_two(vref1 - most);
+          unit = scale_value(uint32_t(most));
+        }
         const int c_end = joint ? D / 2 * (slot + 1) : D;
 #pragma unroll 1
         for (int c = joint ? D / 2 * slot : 0; c < c_end; c += 32) {
@@ -1214,6 +1220,10 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
             if (live && flushed && l != 0.f) add_flushed(x, sum_row + c * kRows, keep * f0);
             if (live && keep1 != 0.f && l1 != 0.f)
               add_flushed(x, sum_row + (slot ? -kRows * D : kRows * D) + c * kRows, keep1 * f1);
+          }
+          if constexpr (SCALED) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) x[k] *= unit;
           }
           put32(x, c);
         }

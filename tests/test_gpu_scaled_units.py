@@ -177,3 +177,33 @@ def test_keys_far_below_the_tiles_largest_scale(n, gap):
     o, lse = o.double().cpu().numpy().reshape(2, n, s.Hq, D), lse.double().cpu().numpy().reshape(2, n, s.Hq)
     assert float(np.max(np.abs(o - want[0]) / (e_o + 2 * score * want[2]))) <= 1
     assert float(np.max(np.abs(lse - want[1]) / (e_l + score * LOG2E))) <= 1
+
+
+@pytest.mark.parametrize("n", [1, 3, 40])
+def test_scales_from_zero_on(n):
+    """Blocks of byte 0 and 1 (2^-127 and 2^-126): all of them count."""
+    rng, L, D = np.random.default_rng(n), 1800, 64
+    k, v = np.zeros((L, D), dtype=np.uint8), _codes(rng, (L, D), 0x70, 0x7F)
+    ke, j = np.full(-(-L // BLOCK), 127), np.arange(-(-L // BLOCK))
+    for ve in (j // 40, np.array([0, 1, 0, 2])[j // 29], 0 * j):
+        s = Cache(40, n, k, v, ke, ve, Hkv=4)
+        o, _ = s.run(out_f32=True)
+        want = s.one()
+        # (results are far from f32's subnormals, 2^-149; weights are equal)
+        e_o = bounds(want, D, L, True, 2)[0] - 1e-30 + 2.0 ** -32 * 448 * 2.0 ** (int(ve.max()) - 127) + 2.0 ** -149
+        assert float(np.max(np.abs(o.double().cpu().numpy().reshape(40, n, s.Hq, D) - want[0]) / e_o)) <= 1
+
+
+@pytest.mark.parametrize("n", [1, 40])
+def test_keys_of_scale_zero(n):
+    """Byte 0 of K's blocks under queries of 2^124: the scores count."""
+    rng, L, D = np.random.default_rng(n), 64, 64
+    k, v = np.zeros((L, D), dtype=np.uint8), _codes(rng, (L, D))
+    k[::2, 0] = 0x38                                                  # scores of 2^-127 2^124 16 = 2, and 0
+    s = Cache(2, n, k, v, np.zeros(4, dtype=int), np.full(4, 127), sm_scale=16.0, q=2.0 ** 124)
+    o, lse = s.run(out_f32=True)
+    want = s.one()
+    e_o, e_l = bounds(want, D, L, True, 2)
+    o, lse = o.double().cpu().numpy().reshape(2, n, s.Hq, D), lse.double().cpu().numpy().reshape(2, n, s.Hq)
+    assert float(np.max(np.abs(o - want[0]) / e_o)) <= 1
+    assert float(np.max(np.abs(lse - want[1]) / e_l)) <= 1
