@@ -878,7 +878,7 @@ psd_status free_pages(psd_ctx *ctx, const int32_t *page_indptr, const int32_t *p
  * *num_live = n.  page_map (may be NULL): the new id of each old page, -1 for a free one.
  * A table entry that is out of range or names a free page sets PSD_FAULT_PAGE_ID, a
  * negative count PSD_FAULT_RANGE; then nothing else is written.  new_indices may be
- * page_indices, new_ref_count ref_count.
+ * page_indices, new_ref_count ref_count; outputs lie apart otherwise.
  * workspace: >= psd_pages_workspace_bytes(num_pages, 0) bytes. */
 typedef struct {
   const int32_t *page_indices; /* device [num_page_indices] */

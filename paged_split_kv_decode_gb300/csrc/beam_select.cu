@@ -838,12 +838,14 @@ extern "C" psd_status beam_select(psd_ctx *ctx, const psd_beam_args *a, void *wo
   if (reinterpret_cast<uintptr_t>(a->logits) % (a->logits_type == PSD_LOGITS_F32 ? 4 : 2))
     return fail(PSD_ERR_INVALID_ARG, "beam_select: logits alignment");
   const int64_t outputs = int64_t(a->rows / a->beams) * a->k;
-  auto over_scores = [&](const void *out) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(out), y = reinterpret_cast<uintptr_t>(a->scores);
-    return x < y + uintptr_t(a->rows) * 4 && y < x + uintptr_t(outputs) * 4;
+  auto over = [&](const void *out, const void *in, int size) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(out), y = reinterpret_cast<uintptr_t>(in);
+    return in && x < y + uintptr_t(a->rows) * size && y < x + uintptr_t(outputs) * 4;
   };
-  if (over_scores(a->out_rows) || over_scores(a->out_tokens) ||
-      (over_scores(a->out_scores) && !(a->out_scores == a->scores && a->k == a->beams)))
+  if (over(a->out_rows, a->finished, 1) || over(a->out_tokens, a->finished, 1) || over(a->out_scores, a->finished, 1))
+    return fail(PSD_ERR_INVALID_ARG, "beam_select: outputs overlap finished");
+  if (over(a->out_rows, a->scores, 4) || over(a->out_tokens, a->scores, 4) ||
+      (over(a->out_scores, a->scores, 4) && !(a->out_scores == a->scores && a->k == a->beams)))
     return fail(PSD_ERR_INVALID_ARG, "beam_select: outputs overlap scores (out_scores may be scores where k is beams)");
   if (!workspace || !aligned16(workspace)) return fail(PSD_ERR_INVALID_ARG, "beam_select: workspace must be 16-byte aligned");
   const size_t need = psd_beam_workspace_bytes(ctx, a->rows, a->beams, a->k);

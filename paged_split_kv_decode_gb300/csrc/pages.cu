@@ -835,11 +835,17 @@ extern "C" psd_status compact_pages(psd_ctx *ctx, const psd_compact_args *a, voi
   if (!a->ref_count || !a->new_ref_count || !a->num_live || !a->fault_dev ||
       (a->num_page_indices > 0 && (!a->page_indices || !a->new_indices)))
     return fail(PSD_ERR_INVALID_ARG, "compact_pages: NULL pointer");
-  if ((a->ref_count != a->new_ref_count && overlap(a->ref_count, a->num_pages, a->new_ref_count, a->num_pages)) ||
-      (a->page_indices != a->new_indices && overlap(a->page_indices, a->num_page_indices, a->new_indices, a->num_page_indices)) ||
-      overlap(a->page_map, a->num_pages, a->ref_count, a->num_pages) ||
-      overlap(a->page_map, a->num_pages, a->page_indices, a->num_page_indices))
-    return fail(PSD_ERR_INVALID_ARG, "compact_pages: an output is its input, or apart from all of them");
+  const struct {
+    const int32_t *at;
+    int64_t n;
+  } inputs[2] = {{a->page_indices, a->num_page_indices}, {a->ref_count, a->num_pages}},
+    outputs[4] = {{a->new_indices, a->num_page_indices}, {a->new_ref_count, a->num_pages}, {a->page_map, a->num_pages}, {a->num_live, 1}};
+  for (int i = 0; i < 4; ++i) {
+    bool bad = false;
+    for (int j = 0; j < 2; ++j) bad |= !(i == j && outputs[i].at == inputs[j].at) && overlap(outputs[i].at, outputs[i].n, inputs[j].at, inputs[j].n);
+    for (int j = 0; j < i; ++j) bad |= overlap(outputs[i].at, outputs[i].n, outputs[j].at, outputs[j].n);
+    if (bad) return fail(PSD_ERR_INVALID_ARG, "compact_pages: an output is its input, or apart from all others");
+  }
   DeviceGuard g(ctx->dev.device);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CompactParams p = {};

@@ -223,6 +223,27 @@ def test_binding_passes_on_what_it_is_given(monkeypatch):
             sc.fit(shape, dev)
 
 
+@pytest.mark.parametrize("args", [dict(out_rows=_ptr(8) + 4), dict(out_tokens=_ptr(8)), dict(out_scores=_ptr(8) - 60), dict(out_scores=_ptr(2), k=4, finished=_ptr(2) + 31)])
+def test_selection_refuses_outputs_over_flags(lib, blank, args):
+    """Flags that another request's part of the call may still read."""
+    from paged_split_kv_decode_gb300 import _lib as L
+    assert lib.beam_select(blank, C.byref(_beam(L, **{**dict(finished=_ptr(8)), **args})), _ptr(7), 1 << 40, None) == 1
+    assert "overlap finished" in _message(lib)
+
+
+@pytest.mark.parametrize("args", [dict(page_map=_ptr(4)), dict(page_map=_ptr(3)), dict(num_live=_ptr(2) + 40), dict(num_live=_ptr(1)),
+                                  dict(num_live=_ptr(4) + 196), dict(new_indices=_ptr(2)), dict(new_ref_count=_ptr(1)),
+                                  dict(new_ref_count=_ptr(3) + 36), dict(page_map=_ptr(9), num_live=_ptr(9) + 4)])
+def test_compaction_refuses_outputs_over_each_other(lib, blank, args):
+    from paged_split_kv_decode_gb300 import _lib as L
+    good = (L.PagePool * 1)(L.PagePool(_ptr(20), 64))
+    a = L.CompactArgs(_ptr(1), 10, _ptr(2), 50, _ptr(3), _ptr(4), _ptr(5), None, C.cast(good, C.c_void_p), 1, _ptr(6))
+    for k, v in args.items():
+        setattr(a, k, v)
+    assert lib.compact_pages(blank, C.byref(a), _ptr(12), 1 << 40, None) == 1
+    assert "apart" in _message(lib)
+
+
 # ------------------------------------------------------------- pins of the oracle
 def test_oracle_codes_are_torchs():
     x = np.random.default_rng(0).standard_normal(20000) * np.exp(4 * np.random.default_rng(1).standard_normal(20000))
