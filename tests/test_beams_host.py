@@ -307,3 +307,10 @@ def test_oracle_forks_keep_every_count(seed):
                 assert ref[r[j]] == 1                                  # what gets the new tokens is nobody else's
         assert not {b for _, b in copies} & {a for a, _ in copies}
         rows = new
+
+
+@pytest.mark.parametrize("x", [0.0, -1e10, -3.4e38, 3.4e38])
+def test_oracle_rows_of_one_value(x):
+    """Tokens share such a row evenly, wherever it lies."""
+    got = BM.select(np.full((1, 4), x), [-1.0], 1, 4)
+    assert np.allclose(got[0], -1 - math.log(4)) and list(got[2][0]) == [0, 1, 2, 3]
