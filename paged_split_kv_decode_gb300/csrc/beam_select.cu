@@ -517,10 +517,16 @@ template <typename T>
 __device__ __noinline__ float2 sum_far(const T *x, int vocab, float top) {
   __shared__ float2 of_warp[kWarps];
   float s = 0.f, e = 0.f;
-#pragma unroll 8
-  for (int i = threadIdx.x; i < vocab; i += kThreads) {
-    const float d = logit<T>(x[i]) - top;  // (exact where it is not far below 0; NaN is no continuation)
-    add_pairs(s, e, d <= 0.f ? ex2(d * 1.44269502f) : 0.f, 0.f);
+  constexpr int kAtOnce = 16;  // loads on their way
+  for (int i0 = threadIdx.x; i0 < vocab; i0 += kAtOnce * kThreads) {
+    float y[kAtOnce];
+#pragma unroll
+    for (int c = 0; c < kAtOnce; ++c) y[c] = i0 + c * kThreads < vocab ? logit<T>(x[i0 + c * kThreads]) : neg_inf();
+#pragma unroll
+    for (int c = 0; c < kAtOnce; ++c) {
+      const float d = y[c] - top;  // (exact where it is not far below 0; NaN is no continuation)
+      add_pairs(s, e, d <= 0.f ? ex2(d * 1.44269502f) : 0.f, 0.f);
+    }
   }
 #pragma unroll
   for (int d = 16; d; d >>= 1) add_pairs(s, e, __shfl_xor_sync(0xffffffffu, s, d), __shfl_xor_sync(0xffffffffu, e, d));
