@@ -43,10 +43,11 @@
 // A cache of 8-bit blocks with a scale each (SCALED): the load warps also bring, eight tiles ahead, each tile's four scale
 // bytes into rings in shared memory, and the conversion gives f16 values in units of the tile's largest scale (a warp has one
 // block; blocks 2^15 below the tile's largest are exact, beyond that values are rounded to 2^-25 of the largest).  What is left is
-// a factor a tile: K's on the scores, V's 2^b in the exponent of P, 2^(s - m + b - r) with r the largest b so far (O is
-// rescaled when r grows; b counts as r - 64 at least) and l += 2^(r - b) sum P.  Factors of every 16 keys in the softmax, whose
+// a factor a tile: K's on the scores, V's 2^b on P, 2^(s - m) 2^(b - r) with r the largest b so far (O is rescaled when r
+// grows; b counts as r - 64 at least), for bf16 outputs in the exponent, with l += 2^(r - b) sum P.  m is rounded where
+// it grows, so that its sums with exponents of scales are exact.  Factors of every 16 keys in the softmax, whose
 // chain bounds the kernel, took 421 us for 2048 tokens over 4096 keys; the largest of a tile found by every softmax thread 229; so, by the load
-// warps, 219 (unscaled fp8 206).
+// warps, 220 (unscaled fp8 206).  f32 outputs: 240 us for 2048 tokens over 2048 keys, bf16 136.
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
@@ -681,7 +682,7 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
           *reinterpret_cast<uint4 *>(row + ((k ^ (tk & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
           *reinterpret_cast<uint4 *>(row + (((k + 1) ^ (tk & 7)) << 4)) = make_uint4(out[4], out[5], out[6], out[7]);
         }
-        if (SCALED && down < -15) {  // (in the loop above, whose code all warps fetch, 2048 tokens over 4096 keys took 221 us against 219)
+        if (SCALED && down < -15) {  // (in the loop above, whose code all warps fetch, 2048 tokens over 4096 keys took 2 us more)
           const __half2 again = __float2half2_rn(down < -33 ? 0.f : __uint_as_float(uint32_t(127 + 15 + down) << 23));
 #pragma unroll 1
           for (int c = 0; c < 2 * kSteps; ++c) {
@@ -1064,8 +1065,11 @@ __global__ void __launch_bounds__(Lay<D, TERMS, FP8>::kThreads, 1)
                 if (!wait_all(T_HALF + slot, ops)) return false;
                 fence_after();
               }
-              // (scaled blocks: an integer, so that sums with exponents of scales are exact)
-              const float m_new = grow ? (SCALED ? floorf(top) : top) - L::kBias : m;
+              // (scaled blocks: to a multiple of 2^-13, or of 2^-16 for bf16 outputs, so that its sums with scales' exponents,
+              // below 2^10, or with 64, are exact.  The row's largest weight is still 2^kBias to 2^-13, which f16 holds: with
+              // integers bf16 outputs were 9e-4 of the norm off those of exact weights, with these 5e-4.)
+              constexpr float kGrid = 1.5f * (TERMS == 1 ? 128.f : 1024.f);
+              const float m_new = grow ? (SCALED ? (top + kGrid) - kGrid : top) - L::kBias : m;
               const float alpha = grow ? ex2(m - m_new) : 1.f;
               l *= alpha;
               if (part > 0 || !empty) {
