@@ -749,7 +749,8 @@ typedef struct {
  * larger of e' and the e it has; then the older tokens' codes c become the codes nearest
  * to c * 2^(e_old - e), ties to even.  New codes are nearest to x * 2^(127 - e), ties to
  * even; NaN stays NaN, infinities become 448.  Slots of the block behind the request's
- * tokens keep what they hold.
+ * tokens keep what they hold.  Angles are whole multiples of 2^-32 turns (append_tokens keeps 64 bits
+ * of a turn until it rounds to f32): 1.5e-9 rad.
  * Head dims D and Dv are multiples of 8 up to 256 and Dv > 0, rot_dim is a multiple of 16
  * and rot_col of 8, strides are multiples of 8, tensors 16-byte aligned; other shapes are
  * refused as PSD_ERR_UNSUPPORTED.  Where two requests' new tokens meet in one block (a
@@ -778,8 +779,10 @@ psd_status multi_token_decode_scaled(psd_ctx *ctx, const psd_multi_token_args *a
  * x the logits; the k largest over the request's rows and tokens go out in descending
  * order: out_scores f32, out_rows the row r (of all rows: what fork_pages takes as
  * parents), out_tokens t.  Within a row values are ordered by their logits, between rows
- * in 64 bits; equal ones by lower row, then lower token.  The sums of the exponentials
- * are f32 with compensation, and their logarithms, good to some 1e-8.  Equal rows (the same logits
+ * in 64 bits; equal ones by lower row, then lower token.  The exponentials are f32, off by
+ * 2^-20 of themselves at most, their sums f32 with compensation: a row's logarithm is off by 2^-20 at most
+ * (where one token has most of the weight), by some 1e-8 where many terms make the sum, and values of
+ * different rows that lie nearer than that may come in either order.  Equal rows (the same logits
  * and scores) have equal values.
  * A row with finished[r] != 0 has one continuation, pad_token with the value scores[r];
  * its logits are not read.  Logits of -inf and NaN are no continuations (and add nothing

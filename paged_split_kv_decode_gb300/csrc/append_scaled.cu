@@ -478,7 +478,7 @@ __device__ __forceinline__ void write_blocks(const ScaledParams &s, const uint64
 // K and V of many tokens: a CTA takes tiles of kMany tokens, of K and of V in turn.  Its warps find the places of one tile each,
 // all at once; a tile's rows are brought to the second-level cache while the tile before is worked on.  (With a CTA a tile,
 // seven warps waited for the eighth's dependent loads: 26 us for 8118 tokens of 8 heads of 128 against 19.)  Bound by the chain
-// of a tile (rows, angles, largest, scale, codes: 3 us), with 16 warps an SM at 45 % of the issue slots.
+// of a tile (rows, angles, largest, scale, codes: 3 us), with 16 warps an SM at 47 % of the issue slots.
 template <bool NEOX>
 __global__ void __launch_bounds__(kThreads, kBlockCtas) append_blocks_kernel(const ScaledParams s, const __grid_constant__ Turns turns, int) {
   extern __shared__ __align__(16) float table[];  // cosines [tokens][half], then sines

@@ -3,20 +3,23 @@
 // Mathematics.  v(r, t) = score(r) + x(r, t) - log sum exp x(r, s): within a row the order is that of the
 // logits, so a row's k largest logits hold all of it that can be chosen, and its sum enters only when rows
 // meet.  One pass over the logits finds both.
-//   Sum: in units of 2^R, R an integer near the running maximum of a thread's logits in log2 units, -2^23 at least: the term is
-// 2^(x log2 e - R), log2 e in two f32 pieces so that what is rounded is the difference, not the product.  16
-// terms are added pairwise, the 16-sums with the error of each addition kept beside it; threads and splits meet as such
-// pairs too, rows in 64 bits.  What is left is the rounding of the single terms, some 1e-8 of the sum, and does not
-// depend on where a row lies in memory: equal rows tie (those of a request are split alike).  Beyond 2^23 either way R would
+//   Sum: in units of 2^R, R an integer near the running maximum of a thread's logits in log2 units, -2^23 at least: the term
+// is 2^(x log2 e - R), log2 e in two f32 pieces so that what is rounded is the difference, not the product.  16 terms are added
+// pairwise, the 16-sums with the error of each addition kept beside it; threads and splits meet as such pairs too, rows in 64
+// bits.  What is left is the rounding of the single terms: 2^-20 of a term at most (exp2 2 ulp, 2^-22; its argument, up to 16,
+// rounded twice, 2^-21 ln 2 each), so that of the sum where one term is most of it, and some 1e-8 where many are alike.  It does
+// not depend on where a row lies in memory: equal rows tie (those of a request are split alike).  Beyond 2^23 either way R would
 // not be an integer near the maximum any more.  Logits of -2^23 and less, masks mostly, add nothing to a sum with larger ones; a
 // row whose largest lies so far off is summed once more by the second kernel, relative to that logit, and its values are the
 // logits' differences from it.
 //   Candidates: each warp takes the r-th largest of its lanes' largest logits, r = ceil(k / 8); the least of the
 // 8 warps' is a lower bound of the k-th largest (8 r >= k logits are no smaller), found without a sort.  The pass keeps
 // each thread's largest of every tile; some 2 k of these are not below the bound, and only their 16 logits are read again.
-// Order numbers (a count of the larger ones) give the exact k.  So the pass is left with 9 instructions a logit; with a
-// bound and a search tile by tile 240 rows of 131072 bf16 took 34 us against 23.  Where more is found than there is room for (many equal logits) the CTA goes
-// over its logits again and thins them out on the way.
+// Order numbers (a count of the larger ones) give the exact k.  All in all a
+// logit of bf16 takes 13 instructions; with a bound and a search tile by tile 240 rows of 131072 bf16 took 34 us against 23.
+// Where more is found than there is room for (many equal logits) the CTA goes over its logits again and thins them out on the
+// way, which is slow: with half of the logits equal, at the top, 128 rows of 98305 f32 take 430 us against 20, and 421 with nine
+// tenths of each row at a finite mask such as -1e10 (a CTA's share of a row may be masked whole; masks of -inf: 18).
 //
 // Rows are split so that all SMs have equal work: the rows that are read (not finished, not empty) share the CTAs that run
 // at once, to within a split.  A second kernel, one CTA a request, joins the splits' sums and takes the k largest of the
@@ -24,7 +27,9 @@
 //
 // 128 rows of 98305 f32, a fifth of them finished: 17 us (40 MB, 6 us at the copy rate), 11 of them the first kernel; bound by the
 // chain of a CTA's steps around its 16000 logits (its row, the bound, the search, the order), then by the second kernel's
-// chain.  240 rows of 131072 bf16: 23 us (8 us at the copy rate), bound by instructions.
+// chain.  240 rows of 131072 bf16: 23 us (8 us at the copy rate); f16 25 and bf16 26 with no beam finished.  59 % of the issue
+// slots and 32 % of DRAM: its warps wait for the tile ahead (38 % of their time) and for results (18 %) more than for either.  A
+// row that lies far from zero: 24 us more, for the second kernel's pass over 98305 logits.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -46,7 +46,10 @@ StepPlace step_tc_place(int ctas, int D, float *base);
 bool step_tc_supports(const StepParams &p);
 psd_status launch_step_tc(const StepParams &p, const StepRequests &req, const StepPlace &place, const DeviceInfo &dev,
                           cudaStream_t s);
-// Few rows a KV head (new tokens times query heads) over a cache of 8-bit blocks.
+// Few rows a KV head (new tokens times query heads) over a cache of 8-bit blocks.  32 requests over 512 to 4096 keys, 8 KV heads
+// of 128, on mma.sync and on tcgen05: 4 rows 31 and 58 us, 8 rows 32 and 58, 16 rows 41 and 60, 24 rows 52 and 60, 28 rows 87 and
+// 60, 32 rows 85 and 60; f32 outputs: 4 rows 32 and 83, 16 rows 43 and 86, 32 rows 91 and 88.  4 requests over 60 to 400: 16 rows 13
+// and 14, 32 rows 20 and 15.  (So the two meet between 24 and 28 rows, not at 32.)
 constexpr int kFewRows = 32;
 bool step_rows_supports(const StepParams &p);
 size_t step_rows_floats(int sms, int D);  // what it keeps from its base on

@@ -305,7 +305,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) for
 // table come by asynchronous copies while the children are looked up (with a load at a time the kernel took 20 us where it
 // takes 11, caches cold).  It is bound by one SM's atomics, one or two a table entry and 6 to 9 cycles for 32 of them, and by
 // the latency of what depends on what.  A whole call, copies included: 4 children of 40 pages 8 us against 20; 128 of some
-// 150 pages each 19 us against 32.
+// 150 pages each 19 us against 32.  At the border, 128 children of some 145 pages and 4 pools: 49152 pages 25 us, 49153, by the
+// cluster, 37; 200000 pages 67.  Letting go of such a table alone: 8 us of 3100 pages, 15 of 49152, 27 and 58 by the cluster.
 constexpr int kFewChildren = 1024, kFewPages = 49152, kFewEntries = (1 << 21) - 2;
 
 __device__ __forceinline__ int block_scan(int v, int &total, int *sums) {  // the sum over the threads before
@@ -611,8 +612,8 @@ struct CopyParams {
 // A CTA takes a part of a page of one pool at a time, of 16 KB so that few large pages keep all SMs busy: 16 bytes a thread and
 // access, four of them on their way.  Its next part's place is added up, not divided out (a third of the instructions).  The
 // last CTAs, which may have a part less, write the new table's rows first.  (Here and not in the kernel before: 152 SMs write
-// them beside the copies.)  Bound by DRAM: 14700 pages of 16 KB in 75 us, 0.97 of the copy rate; 22 moves in 32 pools, 23 MB
-// read, in 11 us, where the chain from the list to the last store shows.
+// them beside the copies.)  Bound by DRAM: 14700 pages of 16 KB in 75 us, 0.97 of the copy rate; 36 to 45 moves in 32 pools, 18 to 23 MB
+// read, in 12 us, where the chain from the list to the last store shows.
 constexpr int kPart = 16384;
 __global__ void __launch_bounds__(256) copy_pages_kernel(const CopyParams p, const __grid_constant__ CopyPools pools) {
   const int per = p.pools * p.parts, first = per ? int(blockIdx.x) / per : 0;
