@@ -47,7 +47,7 @@
 // grows; b counts as r - 64 at least), for bf16 outputs in the exponent, with l += 2^(r - b) sum P.  m is rounded where
 // it grows, so that its sums with exponents of scales are exact.  Factors of every 16 keys in the softmax, whose
 // chain bounds the kernel, took 421 us for 2048 tokens over 4096 keys; the largest of a tile found by every softmax thread 229; so, by the load
-// warps, 220 (unscaled fp8 206).  f32 outputs: 240 us for 2048 tokens over 2048 keys, bf16 136.
+// warps, 219 (unscaled fp8 206).  f32 outputs: 240 us for 2048 tokens over 2048 keys, bf16 136.
 //
 // Precision.  S and O are f32.  P meets V as TERMS bf16 terms: one for bf16 outputs (P off
 // by at most 2^-8 of itself, as the output is), three for f32 outputs (24 bits).  Three
